@@ -422,6 +422,130 @@ Q4Q_API q4q_status q4q_debug_mul_mat_path(const void* src0, int64_t ne00, int64_
 Q4Q_API q4q_status q4q_debug_mul_mat_path_workspace_size(int64_t ne00, int64_t ne01, int64_t ne11, int path,
                                                  size_t* bytes);
 
+/* ------------------------------------------------ MXFP4 weights ---- */
+
+/* Element types of the calls below. */
+#define Q4Q_TYPE_F32 0
+#define Q4Q_TYPE_F16 1
+#define Q4Q_TYPE_BF16 2
+
+/* How a product encodes its activations (32-element blocks along K, E8M0 scales). */
+#define Q4Q_ACTS_MXFP4 0   /* E2M1: both operands in 4 bits, the fastest      */
+#define Q4Q_ACTS_MXFP8 1   /* E4M3: 3 mantissa bits more for the activations  */
+
+/* An MXFP4 matrix [ne00, ne01] (OCP microscaling format): blocks of 32 consecutive
+ * weights of a row, each an E2M1 code (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives,
+ * sign in bit 3) times the block's E8M0 scale 2^(byte - 127); byte 255 makes the block
+ * NaN.  It is one 256-byte aligned buffer of two planes:
+ *   codes:  ne01 rows of Kp / 2 bytes, Kp = ne00 rounded up to 256, element 2i in the
+ *           low nibble of byte i, zeros past ne00; rounded up to 256 bytes;
+ *   scales: for each 128 rows and each 128 columns, row groups outermost, 512 bytes
+ *           with the scale of row r, block b at (r % 32) * 16 + (r / 32 % 4) * 4 + b % 4;
+ *           zeros past the matrix.
+ * This is the order in which the tensor cores' copies take both, so products move the
+ * bytes as they lie.  q4q_mxfp4_size: the buffer's size, a multiple of 256.
+ * Limits everywhere below: 0 < ne00 < 2^20, ne00 % 32 == 0, 0 <= ne01 < 2^31. */
+Q4Q_API q4q_status q4q_mxfp4_size(int64_t ne00, int64_t ne01, size_t* bytes);
+
+/* MXFP4 encode of nmats matrices: for each 32-element block of each row,
+ *   e = max(floor(log2(amax)) - 2, -127)  (-127 when amax == 0),
+ *   code = E2M1(x * 2^-e) to nearest, ties to the even code, magnitudes above 6 to 6.
+ * A block that holds an infinity or a NaN gets scale byte 255 and codes 0.
+ * src: device, src_type [nmats][nrows][ncols] contiguous, aligned to its type (16-byte
+ * aligned is faster); dst: device, 256-byte aligned, matrix m at m * q4q_mxfp4_size.
+ * Every byte of dst is written.  nrows * ncols * nmats < 2^40. */
+Q4Q_API q4q_status q4q_quantize_mxfp4(const void* src, int src_type, void* dst, int64_t ncols, int64_t nrows,
+                              int64_t nmats, q4q_stream_t stream);
+
+/* Row gather from an MXFP4 matrix, exact in fp32 (ids, dst, limits and out-of-range ids
+ * as q4q_get_rows_q4_0). */
+Q4Q_API q4q_status q4q_get_rows_mxfp4(const void* src0, int64_t ne00, int64_t ne01, const int32_t* ids,
+                              int64_t n_ids, float* dst, q4q_stream_t stream);
+
+/* Bytes of device workspace q4q_mul_mat_mxfp4 needs on the current device: the encoded
+ * activations, the call's control words and two partial output tiles per SM. */
+Q4Q_API q4q_status q4q_mul_mat_mxfp4_workspace_size(int64_t ne00, int64_t ne01, int64_t ne11, int acts, size_t* bytes);
+
+/* mul_mat with MXFP4 weights on the block-scaled tensor cores, for any token count:
+ * each src1 row is encoded as `acts` says (MXFP4 as q4q_quantize_mxfp4 does; MXFP8 with
+ * e = max(floor(log2(amax)) - 8, -127), E4M3 codes to nearest even, magnitudes above 448
+ * to 448), then
+ *   dst[i11*ne01 + i01] = sum_b 2^(ew[i01][b] + ex[i11][b]) * sum_{k in b} w[i01][k] * x[i11][k]
+ * with fp32 accumulation, rounded once to dst_type.  A NaN block of either side makes
+ * the outputs it takes part in NaN.
+ * src0: device, 256-byte aligned MXFP4 matrix; src1: device, src1_type [ne11][ne10],
+ * dst: device, dst_type [ne11][ne01], each aligned to its type; workspace: 256-byte
+ * aligned, q4q_mul_mat_mxfp4_workspace_size bytes.  flags as q4q_mul_mat_ex.  The result
+ * depends on the operands and the device alone (sums split over CTAs are joined in the
+ * order of K).  Limits: 0 <= ne11 < 2^20; an unknown acts or type: Q4Q_ERR_ARG. */
+Q4Q_API q4q_status q4q_mul_mat_mxfp4(const void* src0, int64_t ne00, int64_t ne01, const void* src1, int src1_type,
+                             int64_t ne10, int64_t ne11, int acts, void* dst, int dst_type, void* workspace,
+                             size_t workspace_bytes, unsigned int flags, q4q_stream_t stream);
+
+/* Debug: the failure path of that kernel's bounded waits (see q4q_debug_mul_mat_timeout):
+ * every wait is bounded by limit_ns and the first CTA leaves out its first stage. */
+Q4Q_API q4q_status q4q_debug_mul_mat_mxfp4_timeout(const void* src0, int64_t ne00, int64_t ne01, const float* src1,
+                                           int64_t ne11, int acts, float* dst, void* workspace,
+                                           size_t workspace_bytes, uint64_t limit_ns, q4q_stream_t stream);
+
+/* ------------------------------------------------ experts ---- */
+
+/* Sort the choices of a router by expert.  Slot s = t * top_k + j is choice j of token t,
+ * ids[s] its expert; an id outside [0, n_experts) is a dropped choice.  The sorted rows
+ * are the slots of expert 0, of expert 1, ..., then the dropped ones, each in slot order:
+ *   first[e]: first sorted row of expert e; first[n_experts]: first dropped row;
+ *   slot[r]:  slot of sorted row r;  row[s]: sorted row of slot s (both permutations).
+ * ids [n_tokens][top_k], first [n_experts + 1], slot and row [n_tokens * top_k]: device
+ * int32, 4-byte aligned.  top_k >= 1, 1 <= n_experts <= 1024, else Q4Q_ERR_ARG;
+ * n_tokens * top_k < 2^31.  n_tokens == 0 writes `first` alone.  One launch. */
+Q4Q_API q4q_status q4q_moe_sort(const int32_t* ids, int64_t n_tokens, int top_k, int n_experts, int32_t* first,
+                        int32_t* slot, int32_t* row, q4q_stream_t stream);
+
+/* Tokens to their experts' rows and back, with gradients.  first and row as q4q_moe_sort
+ * wrote them; a slot counts as used if row[s] < first[n_experts]; r = row[t * top_k + j]:
+ *   gather:        dst[r] = used ? src[t] : 0
+ *   gather_back:   d_src[t] = sum_{j used} d_dst[r]
+ *   combine:       dst[t] = sum_{j used} weights[t][j] * rows[r]
+ *   combine_back:  d_rows[r] = used ? weights[t][j] * d_dst[t] : 0,
+ *                  d_weights[t][j] = used ? <d_dst[t], rows[r]> : 0
+ * Unused rows are never read (they may hold anything).  Sums are fp32 in a fixed order,
+ * rounded once to `type`.  Matrices are device, `type`, contiguous with rows of ne0
+ * elements (src, dst, d_dst of [n_tokens], rows, sorted ones of [n_tokens * top_k]),
+ * aligned to their type (rows of 16-byte multiples at 16-byte aligned pointers are
+ * faster); weights and d_weights fp32 [n_tokens][top_k].  Outputs must not overlap
+ * inputs.  0 < ne0 < 2^20; other limits as q4q_moe_sort. */
+Q4Q_API q4q_status q4q_moe_gather(const void* src, int type, int64_t ne0, int64_t n_tokens, int top_k,
+                          const int32_t* first, int n_experts, const int32_t* row, void* dst, q4q_stream_t stream);
+Q4Q_API q4q_status q4q_moe_gather_back(const void* d_dst, int type, int64_t ne0, int64_t n_tokens, int top_k,
+                               const int32_t* first, int n_experts, const int32_t* row, void* d_src,
+                               q4q_stream_t stream);
+Q4Q_API q4q_status q4q_moe_combine(const void* rows, int type, int64_t ne0, int64_t n_tokens, int top_k,
+                           const int32_t* first, int n_experts, const int32_t* row, const float* weights, void* dst,
+                           q4q_stream_t stream);
+Q4Q_API q4q_status q4q_moe_combine_back(const void* d_dst, const void* rows, int type, int64_t ne0, int64_t n_tokens,
+                                int top_k, const int32_t* first, int n_experts, const int32_t* row,
+                                const float* weights, void* d_rows, float* d_weights, q4q_stream_t stream);
+
+/* Bytes of device workspace q4q_mul_mat_id_mxfp4 needs on the current device. */
+Q4Q_API q4q_status q4q_mul_mat_id_mxfp4_workspace_size(int64_t ne00, int64_t ne01, int64_t n_src1, int64_t n_rows,
+                                               int n_experts, int acts, size_t* bytes);
+
+/* The experts' products: sorted row r of expert e (first[e] <= r < first[e + 1]) is
+ *   dst[r] = mul_mat of src0's matrix e and one row of src1,
+ * computed as q4q_mul_mat_mxfp4 computes it; the row of src1 is slot[r] / top_k (src1
+ * holds tokens), or r where slot is NULL (src1 holds sorted rows).  Rows of no expert
+ * (r >= first[n_experts]) are written as zeros.  The experts' row counts stay on the
+ * device: nothing is read back.
+ * src0: n_experts MXFP4 matrices [ne00, ne01], one every q4q_mxfp4_size bytes, 256-byte
+ * aligned; src1: device, src1_type [n_src1][ne10]; first, slot: as q4q_moe_sort wrote
+ * them; dst: device, dst_type [n_rows][ne01]; workspace as the query says, 256-byte
+ * aligned.  n_rows <= n_src1 * top_k with slot, else n_rows <= n_src1; n_rows < 2^24,
+ * n_src1 < 2^20.  flags as q4q_mul_mat_ex (`first` and `slot` may still be in flight). */
+Q4Q_API q4q_status q4q_mul_mat_id_mxfp4(const void* src0, int64_t ne00, int64_t ne01, int n_experts, const void* src1,
+                                int src1_type, int64_t ne10, int64_t n_src1, const int32_t* first,
+                                const int32_t* slot, int64_t n_rows, int top_k, int acts, void* dst, int dst_type,
+                                void* workspace, size_t workspace_bytes, unsigned int flags, q4q_stream_t stream);
+
 /* Synchronizes the device, returns (in *status) the first device-side error
  * recorded since the last call (Q4Q_OK if none) and clears it.  This is where a
  * bounded wait that ran out (Q4Q_ERR_TIMEOUT) or an out-of-range row id of

@@ -27,6 +27,10 @@ __all__ = [
     "q4q_mul_mat_swiglu", "q4q_get_rows_q4_0", "q4q_get_rows_q8_0", "q4q_mul_mat_q8_0_workspace_size",
     "q4q_mul_mat_q8_0", "q4q_debug_block_isums_q8_0", "Q4Q_GROUP_MAX", "q4q_mul_mat_group_workspace_size",
     "q4q_mul_mat_group", "q4q_debug_wait_timeout",
+    "Q4Q_ACTS_MXFP4", "Q4Q_ACTS_MXFP8", "q4q_mxfp4_size", "q4q_quantize_mxfp4", "q4q_get_rows_mxfp4",
+    "q4q_mul_mat_mxfp4_workspace_size", "q4q_mul_mat_mxfp4", "q4q_debug_mul_mat_mxfp4_timeout", "q4q_moe_sort",
+    "q4q_moe_gather", "q4q_moe_gather_back", "q4q_moe_combine", "q4q_moe_combine_back",
+    "q4q_mul_mat_id_mxfp4_workspace_size", "q4q_mul_mat_id_mxfp4",
 ]
 
 QK = 32
@@ -509,3 +513,12 @@ def q4q_mul_mat_chain(links, workspace: Optional[torch.Tensor] = None, stream=No
         workspace = torch.empty(q4q_mul_mat_chain_workspace_size(n), dtype=torch.uint8, device=links[0][0].device)
     _check("q4q_mul_mat_chain", _lib.load().q4q_mul_mat_chain(arr, n, 1, _dev(workspace, "workspace"),
                                                              workspace.numel(), 0, _stream(stream)))
+
+
+# ------------------------------------------------- MXFP4 weights, experts --
+
+from .mxfp4 import (  # noqa: E402
+    Q4Q_ACTS_MXFP4, Q4Q_ACTS_MXFP8, q4q_debug_mul_mat_mxfp4_timeout, q4q_get_rows_mxfp4, q4q_moe_combine,
+    q4q_moe_combine_back, q4q_moe_gather, q4q_moe_gather_back, q4q_moe_sort, q4q_mul_mat_id_mxfp4,
+    q4q_mul_mat_id_mxfp4_workspace_size, q4q_mul_mat_mxfp4, q4q_mul_mat_mxfp4_workspace_size, q4q_mxfp4_size,
+    q4q_quantize_mxfp4)

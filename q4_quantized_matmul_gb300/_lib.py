@@ -18,7 +18,9 @@ _lib = None
 
 P = ctypes.c_void_p
 I64 = ctypes.c_int64
+INT = ctypes.c_int
 STATUS = ctypes.c_int
+SIZE = ctypes.POINTER(ctypes.c_size_t)
 
 _SIGNATURES = {
     "q4q_quantize_q4_0": (STATUS, [P, P, I64, I64, P]),
@@ -53,6 +55,20 @@ _SIGNATURES = {
     "q4q_debug_mma_splits": (STATUS, [I64, I64, I64, ctypes.c_int, ctypes.POINTER(ctypes.c_int)]),
     "q4q_mul_mat_chain_workspace_size": (STATUS, [ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)]),
     "q4q_mul_mat_chain": (STATUS, [P, ctypes.c_int, I64, P, ctypes.c_size_t, ctypes.c_uint, P]),
+    "q4q_mxfp4_size": (STATUS, [I64, I64, SIZE]),
+    "q4q_quantize_mxfp4": (STATUS, [P, INT, P, I64, I64, I64, P]),
+    "q4q_get_rows_mxfp4": (STATUS, [P, I64, I64, P, I64, P, P]),
+    "q4q_mul_mat_mxfp4_workspace_size": (STATUS, [I64, I64, I64, INT, SIZE]),
+    "q4q_mul_mat_mxfp4": (STATUS, [P, I64, I64, P, INT, I64, I64, INT, P, INT, P, ctypes.c_size_t, ctypes.c_uint, P]),
+    "q4q_debug_mul_mat_mxfp4_timeout": (STATUS, [P, I64, I64, P, I64, INT, P, P, ctypes.c_size_t, ctypes.c_uint64, P]),
+    "q4q_moe_sort": (STATUS, [P, I64, INT, INT, P, P, P, P]),
+    "q4q_moe_gather": (STATUS, [P, INT, I64, I64, INT, P, INT, P, P, P]),
+    "q4q_moe_gather_back": (STATUS, [P, INT, I64, I64, INT, P, INT, P, P, P]),
+    "q4q_moe_combine": (STATUS, [P, INT, I64, I64, INT, P, INT, P, P, P, P]),
+    "q4q_moe_combine_back": (STATUS, [P, P, INT, I64, I64, INT, P, INT, P, P, P, P, P]),
+    "q4q_mul_mat_id_mxfp4_workspace_size": (STATUS, [I64, I64, I64, I64, INT, INT, SIZE]),
+    "q4q_mul_mat_id_mxfp4": (STATUS, [P, I64, I64, INT, P, INT, I64, I64, P, P, I64, INT, INT, P, INT, P,
+                                      ctypes.c_size_t, ctypes.c_uint, P]),
     "q4q_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "q4q_version": (ctypes.c_int, []),
 }

@@ -13,6 +13,7 @@
 
 #include "q4q_common.cuh"
 #include "q4q_internal.h"
+#include "q4q_mx_internal.h"
 
 namespace q4q {
 
@@ -292,7 +293,8 @@ extern "C" q4q_status q4q_device_status(q4q_status* status) {
                                   gemv_swiglu_take_device_status(), gemv_w8_take_device_status(),
                                   gemv_group_take_device_status(), gemv_epi_take_device_status(),
                                   rows_take_device_status(), debug_take_device_status(),
-                                  chain_take_device_status(), rmma_take_device_status()};
+                                  chain_take_device_status(), rmma_take_device_status(),
+                                  mxfp4_take_device_status(), mxmm_take_device_status()};
     unsigned int first = 0;
     for (unsigned int w : words)
         if (!first) first = w;

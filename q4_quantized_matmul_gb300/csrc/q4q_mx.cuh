@@ -1,0 +1,168 @@
+// q4q_mx.cuh -- what the MXFP4 kernels share: the element types, the block encoders
+// and the layout of the operand planes.
+//
+// Microscaling (OCP MX 1.0): a block is 32 values along K with one E8M0 scale 2^e.
+//   e = floor(log2(amax)) - emax   (emax = 2 for E2M1, 8 for E4M3), at least -127
+//   element = round_to_nearest_even(x * 2^-e), saturated at 6 (E2M1) or 448 (E4M3)
+// x * 2^-e is exact in fp32 (a power of two; for amax below 2^-125, where e stops at
+// -127, the product still only grows), so the hardware conversions round x itself once.
+// A block of zeros has scale byte 0 and codes 0; one that holds an infinity or a NaN
+// has scale byte 255 (the format's NaN) and codes 0: all of its values are NaN.
+//
+// Planes.  Codes: row-major, rows of Kp elements (Kp = K rounded up to 256, zeros past
+// K), two per byte for E2M1 (low nibble first), one per byte for E4M3.  Scales: for each
+// group of RB <= 128 rows and 128 columns one 512-byte chunk in the order in which
+// tcgen05.cp takes scale factors into tensor memory: the byte of row r, block b is at
+// (r % 32) * 16 + (r / 32) * 4 + b, chunks ordered by row group, then by column.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp4.h>
+#include <cuda_fp8.h>
+
+#include "q4q_common.cuh"
+
+namespace q4q {
+
+constexpr int MX_KP = 256;            // K is padded to this
+constexpr int MX_CHUNK = 512;         // bytes of one scale chunk (up to 128 rows x 128 columns)
+constexpr int MX_MAX_EXPERTS = 1024;
+
+__host__ __device__ __forceinline__ int64_t mx_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
+__host__ __device__ __forceinline__ int64_t mx_code_bytes(int64_t ne00, int64_t ne01) {
+    return mx_up(ne01 * (mx_up(ne00, MX_KP) / 2), 256);
+}
+__host__ __device__ __forceinline__ int64_t mx_scale_bytes(int64_t ne00, int64_t ne01) {
+    return mx_up(ne01, 128) * (mx_up(ne00, MX_KP) / 32);
+}
+
+template <typename T>
+__device__ __forceinline__ float mx_to_f32(T v) { return (float)v; }
+template <typename T>
+__device__ __forceinline__ T mx_from_f32(float v);
+template <>
+__device__ __forceinline__ float mx_from_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __half mx_from_f32<__half>(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 mx_from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// N values of T at `p`, one to three 16-byte loads where `vec` says that p allows them
+// (16-byte aligned); N * sizeof(T) is a multiple of 16.
+template <typename T, int N>
+__device__ __forceinline__ void mx_load(const T* __restrict__ p, bool vec, float (&v)[N]) {
+    constexpr int PER = 16 / (int)sizeof(T);
+    if (vec) {
+#pragma unroll
+        for (int i = 0; i < N / PER; ++i) {
+            const uint4 u = __ldg(reinterpret_cast<const uint4*>(p) + i);
+            const T* t = reinterpret_cast<const T*>(&u);
+#pragma unroll
+            for (int k = 0; k < PER; ++k) v[i * PER + k] = mx_to_f32(t[k]);
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[k] = mx_to_f32(p[k]);
+    }
+}
+
+// Encode 256 consecutive columns of one row: lane l of the (converged) warp holds columns
+// 8l .. 8l+7 in v, four lanes a block.  Writes the codes at `codes` (the segment's first
+// byte; null: none) and the segment's 8 scale bytes, 4 in each of the chunk words
+// `scales` and `scales + 512`.
+template <bool E4M3>
+__device__ __forceinline__ void mx_encode_segment(const float (&v)[8], uint8_t* codes, uint8_t* scales) {
+    const int lane = threadIdx.x & 31;
+    constexpr int EMAX = E4M3 ? 8 : 2;
+    // magnitudes compare as integers; an infinity or NaN has exponent field 255
+    uint32_t mag = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) mag = max(mag, __float_as_uint(v[k]) & 0x7fffffffu);
+    mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 1));
+    mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 2));
+    const int field = (int)(mag >> 23);
+    const bool bad = field == 255;
+    const int sf = bad ? 255 : max(field - EMAX, 0);               // e + 127; 0 also where amax is 0 or subnormal
+    // 2^-e = 2^(127 - sf): 127 - sf is -126 .. 127 for finite blocks
+    const float inv = bad ? 0.0f : __uint_as_float((uint32_t)(254 - sf) << 23);
+    float t[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) t[k] = bad ? 0.0f : __fmul_rn(v[k], inv);
+    if (codes) {
+        if constexpr (E4M3) {
+            uint32_t w[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(t[4 * h], t[4 * h + 1]), __NV_SATFINITE, __NV_E4M3);
+                const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(t[4 * h + 2], t[4 * h + 3]), __NV_SATFINITE, __NV_E4M3);
+                w[h] = lo | (hi << 16);
+            }
+            reinterpret_cast<uint2*>(codes)[lane] = make_uint2(w[0], w[1]);
+        } else {
+            uint32_t w = 0;
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+                w |= (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(t[2 * h], t[2 * h + 1]), __NV_E2M1, cudaRoundNearest) << (8 * h);
+            reinterpret_cast<uint32_t*>(codes)[lane] = w;
+        }
+    }
+    // lanes 0 and 16 collect the scale bytes of their four blocks (lanes l, l+4, l+8, l+12)
+    uint32_t word = (uint32_t)sf;
+    word |= __shfl_down_sync(0xffffffffu, word, 4) << 8;
+    word |= __shfl_down_sync(0xffffffffu, word, 8) << 16;
+    if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(scales + (lane >> 4) * MX_CHUNK) = word;
+}
+
+// Offset of row r's first scale word inside the scale plane, for 128-column chunk kc.
+__device__ __forceinline__ int64_t mx_scale_offset(int64_t r, int rb, int nkc, int kc) {
+    const int in = (int)(r % rb);
+    return (r / rb * nkc + kc) * MX_CHUNK + (in & 31) * 16 + (in >> 5) * 4;
+}
+
+// The experts' segments: rows start[e] .. start[e + 1] - 1 of the sorted order, at row
+// base[e] * bn of the activation operand (every segment starts a new token tile).  Whatever
+// `first` holds, no segment leaves [0, n_rows) and all of them together take at most
+// max_groups token tiles.  All of the block's threads call it (a multiple of 32, at most
+// 1024); `tmp` holds 33 words.
+__device__ __forceinline__ void mx_segments(const int32_t* __restrict__ first, int n_experts, int64_t n_rows, int bn,
+                                            int64_t max_groups, int* start, int* base, int* tmp) {
+    const int per = (n_experts + (int)blockDim.x - 1) / (int)blockDim.x;
+    const int e0 = threadIdx.x * per, e1 = min(e0 + per, n_experts);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    auto at = [&](int e) { return (int)min(max((int64_t)__ldg(first + e), (int64_t)0), n_rows); };
+    int sum = 0;
+    for (int e = e0; e < e1; ++e) sum += (max(at(e + 1) - at(e), 0) + bn - 1) / bn;
+    int inc = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, inc, d);
+        if (lane >= d) inc += o;
+    }
+    if (lane == 31) tmp[warp] = inc;
+    __syncthreads();
+    int before = inc - sum;
+    for (int w = 0; w < warp; ++w) before += tmp[w];
+    for (int e = e0; e < e1; ++e) {
+        start[e] = at(e);
+        base[e] = (int)min((int64_t)before, max_groups);
+        before += (max(at(e + 1) - at(e), 0) + bn - 1) / bn;
+        if (e == n_experts - 1) {
+            start[n_experts] = at(n_experts);
+            base[n_experts] = (int)min((int64_t)before, max_groups);
+        }
+    }
+    __syncthreads();
+}
+
+// The e with base[e] <= g < base[e + 1].
+__device__ __forceinline__ int mx_find(const int* base, int n_experts, int g) {
+    int lo = 0, hi = n_experts;                        // base[lo] <= g < base[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (base[mid] <= g) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+}  // namespace q4q
