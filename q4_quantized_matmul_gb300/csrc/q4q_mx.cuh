@@ -11,9 +11,11 @@
 //
 // Planes.  Codes: row-major, rows of Kp elements (Kp = K rounded up to 256, zeros past
 // K), two per byte for E2M1 (low nibble first), one per byte for E4M3.  Scales: for each
-// group of RB <= 128 rows and 128 columns one 512-byte chunk in the order in which
-// tcgen05.cp takes scale factors into tensor memory: the byte of row r, block b is at
-// (r % 32) * 16 + (r / 32) * 4 + b, chunks ordered by row group, then by column.
+// 128 rows and 128 columns 512 bytes in the order in which tcgen05.cp takes scale factors
+// into tensor memory: the byte of row r, block b is at (r % 32) * 16 + (r / 32 % 4) * 4 + b.
+// A tile of `bn` rows (128 for weights, a token tile's for activations) has for each 128
+// columns one chunk: its 512-byte pieces, or, up to 32 rows, only the 16 bn bytes in use.
+// Chunks are ordered by row tile, then by column, so a tile's K range is one piece.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -25,8 +27,11 @@
 namespace q4q {
 
 constexpr int MX_KP = 256;            // K is padded to this
-constexpr int MX_CHUNK = 512;         // bytes of one scale chunk (up to 128 rows x 128 columns)
+constexpr int MX_CHUNK = 512;         // scale bytes of 128 rows x 128 columns
 constexpr int MX_MAX_EXPERTS = 1024;
+
+// bytes of a row tile's scales for 128 columns
+__host__ __device__ constexpr int mx_chunk_bytes(int bn) { return bn <= 32 ? bn * 16 : bn <= 128 ? MX_CHUNK : bn / 128 * MX_CHUNK; }
 
 __host__ __device__ __forceinline__ int64_t mx_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 __host__ __device__ __forceinline__ int64_t mx_code_bytes(int64_t ne00, int64_t ne01) {
@@ -66,13 +71,30 @@ __device__ __forceinline__ void mx_load(const T* __restrict__ p, bool vec, float
     }
 }
 
-// Encode 256 consecutive columns of one row: lane l of the (converged) warp holds columns
-// 8l .. 8l+7 in v, four lanes a block.  Writes the codes at `codes` (the segment's first
-// byte; null: none) and the segment's 8 scale bytes, 4 in each of the chunk words
-// `scales` and `scales + 512`.
+// 8 values of T as they were loaded, looked at only when they are needed; `live`: not zeros.
+template <typename T>
+struct MxRaw {
+    uint4 bits[sizeof(T) / 2];
+    bool live;
+    __device__ __forceinline__ void load(const T* __restrict__ p, bool vec) {
+        if (vec) {
+#pragma unroll
+            for (int i = 0; i < (int)sizeof(T) / 2; ++i) bits[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) reinterpret_cast<T*>(bits)[k] = p[k];
+        }
+    }
+    __device__ __forceinline__ void values(float (&v)[8]) const {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = live ? mx_to_f32(reinterpret_cast<const T*>(bits)[k]) : 0.0f;
+    }
+};
+
+// Encode 8 values a lane, four neighbouring lanes a block (the whole converged warp calls
+// it): the codes in w (8 bytes for E4M3, 4 for E2M1), the block's scale byte returned.
 template <bool E4M3>
-__device__ __forceinline__ void mx_encode_segment(const float (&v)[8], uint8_t* codes, uint8_t* scales) {
-    const int lane = threadIdx.x & 31;
+__device__ __forceinline__ uint32_t mx_encode8(const float (&v)[8], uint32_t (&w)[2]) {
     constexpr int EMAX = E4M3 ? 8 : 2;
     // magnitudes compare as integers; an infinity or NaN has exponent field 255
     uint32_t mag = 0;
@@ -88,35 +110,53 @@ __device__ __forceinline__ void mx_encode_segment(const float (&v)[8], uint8_t* 
     float t[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) t[k] = bad ? 0.0f : __fmul_rn(v[k], inv);
-    if (codes) {
-        if constexpr (E4M3) {
-            uint32_t w[2];
+    if constexpr (E4M3) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(t[4 * h], t[4 * h + 1]), __NV_SATFINITE, __NV_E4M3);
-                const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(t[4 * h + 2], t[4 * h + 3]), __NV_SATFINITE, __NV_E4M3);
-                w[h] = lo | (hi << 16);
-            }
-            reinterpret_cast<uint2*>(codes)[lane] = make_uint2(w[0], w[1]);
-        } else {
-            uint32_t w = 0;
-#pragma unroll
-            for (int h = 0; h < 4; ++h)
-                w |= (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(t[2 * h], t[2 * h + 1]), __NV_E2M1, cudaRoundNearest) << (8 * h);
-            reinterpret_cast<uint32_t*>(codes)[lane] = w;
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(t[4 * h], t[4 * h + 1]), __NV_SATFINITE, __NV_E4M3);
+            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(t[4 * h + 2], t[4 * h + 3]), __NV_SATFINITE, __NV_E4M3);
+            w[h] = lo | (hi << 16);
         }
+    } else {
+        w[0] = w[1] = 0;
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+            w[0] |= (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(t[2 * h], t[2 * h + 1]), __NV_E2M1, cudaRoundNearest) << (8 * h);
     }
-    // lanes 0 and 16 collect the scale bytes of their four blocks (lanes l, l+4, l+8, l+12)
-    uint32_t word = (uint32_t)sf;
-    word |= __shfl_down_sync(0xffffffffu, word, 4) << 8;
-    word |= __shfl_down_sync(0xffffffffu, word, 8) << 16;
-    if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(scales + (lane >> 4) * MX_CHUNK) = word;
+    return (uint32_t)sf;
 }
 
-// Offset of row r's first scale word inside the scale plane, for 128-column chunk kc.
-__device__ __forceinline__ int64_t mx_scale_offset(int64_t r, int rb, int nkc, int kc) {
-    const int in = (int)(r % rb);
-    return (r / rb * nkc + kc) * MX_CHUNK + (in & 31) * 16 + (in >> 5) * 4;
+// Encode 256 consecutive columns of one row: lane l of the (converged) warp holds columns
+// 8l .. 8l+7 in v.  Writes the codes at `codes` (the segment's first byte; null: none) and
+// the segment's 8 scale bytes, 4 in each of the words at `scales` and, in the next chunk,
+// `scales + chunk`.
+template <bool E4M3>
+__device__ __forceinline__ void mx_encode_segment(const float (&v)[8], uint8_t* codes, uint8_t* scales, int chunk) {
+    const int lane = threadIdx.x & 31;
+    uint32_t w[2];
+    uint32_t word = mx_encode8<E4M3>(v, w);
+    if (codes) {
+        if constexpr (E4M3) reinterpret_cast<uint2*>(codes)[lane] = make_uint2(w[0], w[1]);
+        else reinterpret_cast<uint32_t*>(codes)[lane] = w[0];
+    }
+    // lanes 0 and 16 collect the scale bytes of their four blocks (lanes l, l+4, l+8, l+12)
+    word |= __shfl_down_sync(0xffffffffu, word, 4) << 8;
+    word |= __shfl_down_sync(0xffffffffu, word, 8) << 16;
+    if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(scales + (lane >> 4) * chunk) = word;
+}
+
+// dst[i] = v, rounded to the type
+__device__ __forceinline__ void mx_store(void* dst, int type, int64_t i, float v) {
+    if (type == Q4Q_TYPE_F32) static_cast<float*>(dst)[i] = v;
+    else if (type == Q4Q_TYPE_F16) static_cast<__half*>(dst)[i] = __float2half_rn(v);
+    else static_cast<__nv_bfloat16*>(dst)[i] = __float2bfloat16_rn(v);
+}
+
+// Offset of the scale word of row r for the 128 columns kc, in tiles of bn rows.
+__device__ __forceinline__ int64_t mx_scale_offset(int64_t r, int bn, int nkc, int kc) {
+    const int64_t tile = r / bn;
+    const int in = (int)(r - tile * bn);
+    return (tile * nkc + kc) * mx_chunk_bytes(bn) + (in >> 7) * MX_CHUNK + (in & 31) * 16 + ((in >> 5) & 3) * 4;
 }
 
 // The experts' segments: rows start[e] .. start[e + 1] - 1 of the sorted order, at row

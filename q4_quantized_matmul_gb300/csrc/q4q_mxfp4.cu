@@ -42,7 +42,7 @@ encode_kernel(const T* __restrict__ src, bool vec, uint8_t* __restrict__ dst, in
         // the code plane ends on a 256-byte boundary: after an odd number of segments, one more of zeros
         const bool codes = r < rows || (r == rows && seg == 0 && (rows * segs) % 2 != 0);
         mx_encode_segment<false>(v, codes ? out + (r * segs + seg) * (MX_KP / 2) : nullptr,
-                                 out + code_bytes + mx_scale_offset(r, 128, nkc, 2 * seg));
+                                 out + code_bytes + mx_scale_offset(r, 128, nkc, 2 * seg), MX_CHUNK);
     }
 }
 
@@ -58,7 +58,7 @@ struct ActArgs {
     int64_t max_groups;
     const int32_t* first;      // null: dense
     const int32_t* slot;       // null: row i of src is row i
-    int n_experts, top_k, K, bn, rb;
+    int n_experts, top_k, K, bn;
     bool vec, pdl;
 };
 
@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(THREADS) acts_kernel(const ActArgs a) {
             for (int k = 0; k < 8; ++k) v[k] = 0.0f;
         }
         mx_encode_segment<E4M3>(v, a.codes + (to * segs + seg) * SEG_BYTES,
-                                a.scales + mx_scale_offset(to, a.rb, nkc, 2 * seg));
+                                a.scales + mx_scale_offset(to, a.bn, nkc, 2 * seg), mx_chunk_bytes(a.bn));
     }
 }
 
@@ -163,7 +163,7 @@ unsigned int mxfp4_take_device_status() {
 }
 
 q4q_status mx_encode_acts(const MxActs& m, unsigned int* ctrl, int64_t n_ctrl, uint8_t* codes, uint8_t* scales, int bn,
-                          int rb, int64_t max_groups, bool pdl, cudaStream_t stream, const DeviceInfo& info) {
+                          int64_t max_groups, bool pdl, cudaStream_t stream, const DeviceInfo& info) {
     ActArgs a;
     a.src = m.src;
     a.codes = codes;
@@ -179,7 +179,6 @@ q4q_status mx_encode_acts(const MxActs& m, unsigned int* ctrl, int64_t n_ctrl, u
     a.top_k = m.top_k;
     a.K = (int)m.K;
     a.bn = bn;
-    a.rb = rb;
     a.vec = aligned(m.src, 16);
     a.pdl = pdl;
     const int64_t units = m.n_rows * ((m.K + MX_KP - 1) / MX_KP);

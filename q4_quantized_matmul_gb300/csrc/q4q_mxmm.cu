@@ -4,17 +4,18 @@
 //   dst[n][m] = sum_b 2^(ew[m][b] + ex[n][b]) * sum_{k in block b} w[m][k] * x[n][k]
 //
 // with w in E2M1 and x, encoded on the fly (q4q_mxfp4.cu), in E2M1 (kind::mxf4) or E4M3
-// (kind::mxf8f6f4).  The tensor core takes codes and scales as they lie in memory, so
-// nothing is unpacked by CUDA cores at any token count: one token and two thousand run
-// the same kernel, with the weight rows as the MMA's M = 128 and the tokens as its N.
+// (kind::mxf8f6f4); up to 8 tokens q4q_mxmv.cu has its own kernel.  The tensor core takes codes and scales as they lie in memory, so
+// nothing is unpacked by CUDA cores; the weight rows are the MMA's M = 128 and the tokens
+// its N.
 // All products of two E2M1 values are multiples of 1/4 up to 36 and the accumulator is
 // fp32.
 //
 // Roles (one CTA per SM, 256 threads):
-//   warp 0    : TMA producer.  A stage is 128 bytes of each smem row: 256 K of packed
-//               E2M1, or 128 K of E4M3 with the weights widened by the tensor map to one
-//               byte each (16U4_ALIGN16B: HBM still moves the packed nibbles), plus the
-//               stage's scale chunks.  The ring fills what shared memory there is.
+//   warp 0    : TMA producer.  A stage is one or more atoms of 128 bytes of each smem row
+//               (256 K of packed E2M1, or 128 K of E4M3 with the weights widened by the
+//               tensor map to one byte each, 16U4_ALIGN16B: HBM still moves the packed
+//               nibbles) and their scale chunks, in four copies.  The ring fills what
+//               shared memory there is.
 //   warp 1    : MMA issuer: scale chunks to tensor memory (tcgen05.cp), 4 MMAs a stage.
 //   warps 4-7 : epilogue: accumulator (two of them while 2 BN <= 256 columns) to dst.
 //
@@ -22,7 +23,8 @@
 // part of that line, so that all SMs stream the same amount whatever the shape; a tile cut
 // by a boundary is summed by the CTA that finishes it last, from fp32 partial sums in the
 // workspace in the order of K, so that the result does not depend on which CTA that is.
-// In whole mode the cuts are moved to tile boundaries.
+// In whole mode CTA c takes tiles c, c + CTAs, ...: the CTAs walk K together over
+// neighbouring tiles, so what one reads from HBM the others find in L2.
 //
 // Every mbarrier wait is bounded; one that runs out records Q4Q_ERR_TIMEOUT, raises the
 // call's abort word (zeroed by the activation encoder before every launch) and the CTA
@@ -35,6 +37,7 @@
 
 #include "q4q_internal.h"
 #include "q4q_mx.cuh"
+#include "q4q_mx_tc.cuh"
 #include "q4q_mx_internal.h"
 
 namespace q4q {
@@ -42,99 +45,10 @@ namespace {
 
 __device__ unsigned int g_mxmm_status = 0;
 
-constexpr int BM = 128;
 constexpr int THREADS = 256;
 constexpr int CTRL_ABORT = 0;                 // control words: the abort word, then a counter per tile
 constexpr int CTRL_COUNT = 64;
 constexpr int MIN_SPLIT_STAGES = 4;           // least stages of a CTA's part in split mode
-
-// ------------------------------------------------------------------ PTX ----
-
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, int x, int y, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-        ::"r"(dst), "l"(tmap), "r"(x), "r"(y), "r"(bar) : "memory");
-}
-
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int x, int y, int z, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
-        ::"r"(dst), "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
-}
-
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-__device__ __forceinline__ void tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-}
-
-__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
-}
-
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-                 : "memory");
-}
-
-// 32 rows x 16 bytes of scale factors, repeated in the four lane quadrants: 4 columns
-__device__ __forceinline__ void scales_to_tmem(uint32_t taddr, uint64_t desc) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
-}
-
-// one block-scaled MMA: 64 K of E2M1 x E2M1, or 32 K of E2M1 x E4M3
-template <bool E4M3>
-__device__ __forceinline__ void mma_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
-                                       uint32_t accumulate) {
-    if constexpr (E4M3)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.block32 [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
-            ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate) : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.block32 [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
-            ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate) : "memory");
-}
-
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(taddr));
-}
-
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr));
-}
-
-template <int N>
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N]) {
-    static_assert(N == 8 || N == 32, "column counts of a load");
-    if constexpr (N == 8) tmem_ld8(taddr, r);
-    else tmem_ld32(taddr, r);
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-
-// Shared-memory descriptors: a K-major operand in the 128-byte swizzle (8-row atoms of
-// 1024 bytes), and 32 x 16 bytes of scales without one (8-row groups of 128 bytes).
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t addr) {
-    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
-           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
-__device__ __forceinline__ uint64_t desc_scales(uint32_t addr) {
-    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
-}
 
 // ---------------------------------------------------------------- the work --
 
@@ -159,48 +73,43 @@ struct MxParams {
 
 template <int BN, bool E4M3>
 struct Cfg {
-    static constexpr int RB = BN < 128 ? BN : 128;        // activation rows of one scale chunk
-    static constexpr int NB = BN / RB;                    // scale chunks of a token tile
-    static constexpr int KS = E4M3 ? 128 : 256;           // K of a stage
-    static constexpr int CH = KS / 128;                   // scale chunks along K
-    static constexpr int A_BYTES = BM * 128;
-    static constexpr int A_TX = E4M3 ? A_BYTES / 2 : A_BYTES;   // bytes the copy reads
+    static constexpr int ATOM_K = E4M3 ? 128 : 256;       // K of a 128-byte shared-memory row
+    static constexpr int CH = ATOM_K / 128;               // scale chunks of an atom
+    static constexpr int ATOMS = BN <= 64 ? (E4M3 ? 2 : 1) : 1;   // atoms of a stage
+    static constexpr int NB = BN <= 128 ? 1 : BN / 128;   // 512-byte pieces of a token tile's scale chunk
+    static constexpr int CHUNK = mx_chunk_bytes(BN);
+    static constexpr int A_BYTES = BM * 128;              // of one atom
     static constexpr int B_BYTES = BN * 128;
-    static constexpr int SFA_BYTES = CH * MX_CHUNK;
-    // of a chunk only the first RB rows matter; up to 32 rows they are its first bytes
-    static constexpr int SFB_ROW = RB <= 32 ? RB * 16 : MX_CHUNK;
-    static constexpr int SFB_BYTES = CH * NB * MX_CHUNK;
-    static constexpr int STAGE = (A_BYTES + B_BYTES + SFA_BYTES + SFB_BYTES + 1023) / 1024 * 1024;
-    static constexpr int TX = A_TX + B_BYTES + SFA_BYTES + CH * NB * SFB_ROW;
-    static constexpr int FIXED = 1024 + 1024 + 2 * (MX_MAX_EXPERTS + 1) * 4 + 64;   // alignment, barriers, segments
-    static constexpr int ST_ = (227 * 1024 - FIXED) / STAGE;
+    static constexpr int OFF_B = ATOMS * A_BYTES;
+    static constexpr int OFF_SFA = OFF_B + ATOMS * B_BYTES;
+    static constexpr int OFF_SFB = OFF_SFA + ATOMS * CH * MX_CHUNK;
+    static constexpr int STAGE = (OFF_SFB + ATOMS * CH * CHUNK + 1023) / 1024 * 1024;
+    // bytes that the operand copies of a stage read (the widened weights as they lie in memory)
+    static constexpr int TX = ATOMS * ((E4M3 ? A_BYTES / 2 : A_BYTES) + B_BYTES);
+    static constexpr int SEG_BYTES = 2 * (MX_MAX_EXPERTS + 1) * 4 + 64;
+    static constexpr int ST_ = (227 * 1024 - 2048 - SEG_BYTES) / STAGE;
     static constexpr int ST = ST_ > 12 ? 12 : ST_;
     static constexpr int OFF_BAR = ST * STAGE;
     static constexpr int OFF_SEG = OFF_BAR + 1024;
-    static constexpr int SMEM = OFF_SEG + 2 * (MX_MAX_EXPERTS + 1) * 4 + 64 + 1024;
+    static constexpr int SMEM = OFF_SEG + SEG_BYTES + 1024;          // + alignment slack
     static constexpr int NACC = 2 * BN <= 256 ? 2 : 1;
     static constexpr int SFA_COL = NACC * BN;
-    static constexpr int SFB_COL = SFA_COL + 4 * CH;
-    static constexpr int USED = SFB_COL + 4 * CH * NB;
+    static constexpr int SFB_COL = SFA_COL + 4 * ATOMS * CH;
+    static constexpr int USED = SFB_COL + 4 * ATOMS * CH * NB;
     static constexpr int COLS = USED <= 32 ? 32 : USED <= 64 ? 64 : USED <= 128 ? 128 : USED <= 256 ? 256 : 512;
-    static_assert(USED <= 512 && B_BYTES % 1024 == 0 && SMEM <= 227 * 1024, "fits the SM");
+    static_assert(USED <= 512 && B_BYTES % 1024 == 0 && ST >= 3 && SMEM <= 227 * 1024, "fits the SM");
 };
 
-// A CTA's share of the work line, and its walk over it.
+// A CTA's share of the work and its walk over it.
 struct Walk {
-    int64_t pos, end;      // in stages
+    int64_t pos, end;      // split: stages of the line; whole: tiles, in steps of `parts`
     int64_t total;         // stages in all
-    int parts;             // CTAs that share the line
+    int parts;             // CTAs that share the work
     bool split;
 };
 
-__device__ __forceinline__ int64_t part_begin(const Walk& w, int kst, int64_t c) {
-    if (w.split) return c * w.total / w.parts;
-    return (c * (w.total / kst) / w.parts) * kst;
-}
-
 struct Frag {
-    int mat, m0, k0, k1;
+    int mat, m0, k0, k1;   // matrix, first weight row, K stages
     int x_row;             // first row of the activation operand
     int64_t tile;
     int64_t dst_row;
@@ -211,11 +120,20 @@ struct Frag {
 template <int BN>
 __device__ __forceinline__ bool next_frag(Walk& w, const MxParams& p, const int* start, const int* units, Frag& f) {
     if (w.pos >= w.end) return false;
-    const int64_t t = w.pos / p.kst;
-    f.k0 = (int)(w.pos - t * p.kst);
-    f.k1 = (int)min((int64_t)p.kst, f.k0 + (w.end - w.pos));
-    w.pos += f.k1 - f.k0;
-    f.whole = f.k0 == 0 && f.k1 == p.kst;
+    int64_t t;
+    if (w.split) {
+        t = w.pos / p.kst;
+        f.k0 = (int)(w.pos - t * p.kst);
+        f.k1 = (int)min((int64_t)p.kst, f.k0 + (w.end - w.pos));
+        w.pos += f.k1 - f.k0;
+        f.whole = f.k0 == 0 && f.k1 == p.kst;
+    } else {
+        t = w.pos;
+        w.pos += w.parts;
+        f.k0 = 0;
+        f.k1 = p.kst;
+        f.whole = true;
+    }
     f.tile = t;
     // tiles: by segment, then weight rows, then tokens (the weights of a row tile are read
     // by consecutive tiles)
@@ -231,11 +149,13 @@ __device__ __forceinline__ bool next_frag(Walk& w, const MxParams& p, const int*
         g0 = units[e];
         groups = units[e + 1] - g0;
     }
-    const int64_t in = t - (int64_t)g0 * p.mtiles;
-    const int mt = (int)(in / groups), nt = (int)(in - (int64_t)mt * groups);
-    f.mat = e;
+    const int in = (int)(t - (int64_t)g0 * p.mtiles);
+    const int mt = __shfl_sync(0xffffffffu, in / groups, 0), nt = __shfl_sync(0xffffffffu, in - mt * groups, 0);
+    // (from lane 0, so that the compiler knows them to be the same in the whole warp: it keeps
+    // the descriptors of copies and MMAs in uniform registers only then)
+    f.mat = __shfl_sync(0xffffffffu, e, 0);
     f.m0 = mt * BM;
-    f.x_row = (g0 + nt) * BN;
+    f.x_row = (__shfl_sync(0xffffffffu, g0, 0) + nt) * BN;
     f.dst_row = (p.first ? start[e] : 0) + (int64_t)nt * BN;
     const int64_t left = (p.first ? (int64_t)start[e + 1] : p.n_rows) - f.dst_row;
     f.valid = (int)min(left, (int64_t)BN);
@@ -249,12 +169,6 @@ __device__ __forceinline__ bool epilogue_all(bool ok) {
         "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(all) : "r"((uint32_t)ok) : "memory");
     return all != 0;
-}
-
-__device__ __forceinline__ void store_as(void* dst, int type, int64_t i, float v) {
-    if (type == Q4Q_TYPE_F32) static_cast<float*>(dst)[i] = v;
-    else if (type == Q4Q_TYPE_F16) static_cast<__half*>(dst)[i] = __float2half_rn(v);
-    else static_cast<__nv_bfloat16*>(dst)[i] = __float2bfloat16_rn(v);
 }
 
 template <int BN, bool E4M3>
@@ -274,7 +188,7 @@ mxmm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ 
     int* start = reinterpret_cast<int*>(smem + C::OFF_SEG);
     int* units = start + MX_MAX_EXPERTS + 1;
     const Waiter wt{abort_flag, p.ctrl + CTRL_ABORT, p.limit_ns, &g_mxmm_status};
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < ST; ++s) {
@@ -290,11 +204,11 @@ mxmm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ 
         fence_mbar_init();
     }
     if (warp == 1) tmem_alloc(slot_addr, C::COLS);
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    pdl_trigger();
     // the experts' segments are known before the activations are
     Walk walk;
     if (p.first) {
-        if (p.wait_first) asm volatile("griddepcontrol.wait;" ::: "memory");
+        if (p.wait_first) pdl_wait();
         mx_segments(p.first, p.n_mats, p.n_rows, BN, p.max_groups, start, units, tmp);
     } else if (threadIdx.x == 0) {
         units[0] = 0;
@@ -305,9 +219,10 @@ mxmm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ 
     tc_fence_after();
     uint32_t tmem;
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(slot_addr));
+    tmem = __shfl_sync(0xffffffffu, tmem, 0);
 
     {
-        const int64_t tiles = (int64_t)units[p.first ? p.n_mats : 1] * p.mtiles;
+        const int64_t tiles = (int64_t)__shfl_sync(0xffffffffu, units[p.first ? p.n_mats : 1], 0) * p.mtiles;   // the same in the whole warp
         walk.total = tiles * p.kst;
         // whole tiles where they fill the SMs within a tenth; equal parts of the line elsewhere
         const int64_t rounds = (tiles + gridDim.x - 1) / gridDim.x;
@@ -316,119 +231,129 @@ mxmm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ 
         walk.parts = (int)max((int64_t)1, min((int64_t)gridDim.x, most));
         walk.pos = walk.end = 0;
         if ((int)blockIdx.x < walk.parts) {
-            walk.pos = part_begin(walk, p.kst, blockIdx.x);
-            walk.end = part_begin(walk, p.kst, (int64_t)blockIdx.x + 1);
+            walk.pos = walk.split ? blockIdx.x * walk.total / walk.parts : blockIdx.x;
+            walk.end = walk.split ? (blockIdx.x + 1) * walk.total / walk.parts : tiles;
         }
     }
 
     if (warp == 0) {
         // ---------------- producer
-        if (lane == 0) {
-            // the weights of the first stages do not wait for the activation encoder
-            Walk ahead = walk;
-            Frag f;
-            int pre = 0;
-            auto load_w = [&](const Frag& g, int k, int s) {
-                const uint32_t st = sbase + s * C::STAGE, bar = full + 8 * s;
-                tma_load_3d(st, &tmap_w, k * 128, g.m0, g.mat, bar);
-                bulk_g2s(st + C::A_BYTES + C::B_BYTES,
-                         p.w_scales + g.mat * p.mat_stride + ((int64_t)(g.m0 / BM) * p.nkc + (int64_t)k * C::CH) * MX_CHUNK,
-                         C::SFA_BYTES, bar);
-            };
-            auto load_x = [&](const Frag& g, int k, int s) {
-                const uint32_t st = sbase + s * C::STAGE, bar = full + 8 * s;
-                tma_load_2d(st + C::A_BYTES, &tmap_x, k * 128, g.x_row, bar);
-#pragma unroll
-                for (int b = 0; b < C::NB; ++b)
-#pragma unroll
-                    for (int c = 0; c < C::CH; ++c)
-                        bulk_g2s(st + C::A_BYTES + C::B_BYTES + C::SFA_BYTES + (b * C::CH + c) * MX_CHUNK,
-                                 p.x_scales + ((int64_t)(g.x_row / C::RB + b) * p.nkc + (int64_t)k * C::CH + c) * MX_CHUNK,
-                                 C::SFB_ROW, bar);
-            };
-            const bool skip = p.fault && blockIdx.x == 0;
-            while (pre < ST && next_frag<BN>(ahead, p, start, units, f))
-                for (int k = f.k0; k < f.k1 && pre < ST; ++k, ++pre) {
-                    if (skip && pre == 0) continue;
-                    mbar_arrive_expect_tx(full + 8 * pre, C::TX);
-                    load_w(f, k, pre);
-                }
-            asm volatile("griddepcontrol.wait;" ::: "memory");
-            int i = 0;
-            bool ok = true;
-            while (ok && next_frag<BN>(walk, p, start, units, f))
-                for (int k = f.k0; k < f.k1; ++k, ++i) {
-                    const int s = i % ST;
-                    if (i >= pre) {
-                        if (!wait_or_abort(empty + 8 * s, ((i / ST) + 1) & 1, wt)) {
-                            ok = false;
-                            break;
-                        }
-                        mbar_arrive_expect_tx(full + 8 * s, C::TX);
-                        load_w(f, k, s);
-                    } else if (skip && i == 0) {
-                        continue;
-                    }
-                    load_x(f, k, s);
-                }
-            // every copy lands before the CTA can exit, also after an abort
-            for (int j = max(0, i - ST); j < i; ++j)
-                if (!(skip && j == 0)) mbar_wait_bounded(full + 8 * (j % ST), (j / ST) & 1, p.limit_ns);
-        }
-    } else if (warp == 1) {
-        // ---------------- MMA issuer
-        asm volatile("griddepcontrol.wait;" ::: "memory");
-        if (lane == 0) {
-            // M = 128, N = BN, E8M0 scales, A = E2M1 (code 1 in kind::mxf4, 5 in kind::mxf8f6f4)
-            constexpr uint32_t IDESC = ((uint32_t)(BN >> 3) << 17) | (1u << 23) | ((uint32_t)(BM >> 7) << 27) |
-                                       (E4M3 ? (5u << 7) : (1u << 7) | (1u << 10));
-            const uint32_t sfa = tmem + C::SFA_COL, sfb = tmem + C::SFB_COL;
-            Frag f;
-            int i = 0, n = 0;
-            bool ok = true;
-            while (ok && next_frag<BN>(walk, p, start, units, f)) {
-                const int buf = n % C::NACC;
-                if (n >= C::NACC && !wait_or_abort(acc_empty + 8 * buf, ((n / C::NACC) + 1) & 1, wt)) break;
-                tc_fence_after();
-                const uint32_t d = tmem + buf * BN;
-                for (int k = f.k0; k < f.k1; ++k, ++i) {
-                    const int s = i % ST;
-                    if (!wait_or_abort(full + 8 * s, (i / ST) & 1, wt)) {
+        const bool lead = elect_one();
+        auto load_w = [&](const Frag& g, int k, int s) {
+            const uint32_t st = sbase + s * C::STAGE, bar = full + 8 * s;
+            const int chunks = min(C::ATOMS * C::CH, p.nkc - k * (C::ATOMS * C::CH));
+            mbar_arrive_expect_tx(bar, C::TX + chunks * (MX_CHUNK + C::CHUNK));
+            tma_load_4d(st, &tmap_w, 0, g.m0, k * C::ATOMS, g.mat, bar);
+            bulk_g2s(st + C::OFF_SFA,
+                     p.w_scales + g.mat * p.mat_stride + ((int64_t)(g.m0 / BM) * p.nkc + k * (C::ATOMS * C::CH)) * MX_CHUNK,
+                     chunks * MX_CHUNK, bar);
+        };
+        auto load_x = [&](const Frag& g, int k, int s) {
+            const uint32_t st = sbase + s * C::STAGE, bar = full + 8 * s;
+            const int chunks = min(C::ATOMS * C::CH, p.nkc - k * (C::ATOMS * C::CH));
+            tma_load_3d(st + C::OFF_B, &tmap_x, 0, g.x_row, k * C::ATOMS, bar);
+            bulk_g2s(st + C::OFF_SFB, p.x_scales + ((int64_t)(g.x_row / BN) * p.nkc + k * (C::ATOMS * C::CH)) * C::CHUNK,
+                     chunks * C::CHUNK, bar);
+        };
+        // the weights of the first stages do not wait for the activation encoder
+        const bool skip = p.fault && blockIdx.x == 0;
+        Walk ahead = walk;
+        Frag f;
+        int pre = 0;
+        while (pre < ST && next_frag<BN>(ahead, p, start, units, f))
+            for (int k = f.k0; k < f.k1 && pre < ST; ++k, ++pre)
+                if (lead && !(skip && pre == 0)) load_w(f, k, pre);
+        pdl_wait();
+        int i = 0, s = 0;
+        uint32_t parity = 1;                 // of the wait on the slot's previous use, from its second on
+        bool ok = true;
+        while (ok && next_frag<BN>(walk, p, start, units, f))
+            for (int k = f.k0; k < f.k1; ++k, ++i) {
+                if (i >= pre) {
+                    if (i >= ST && !warp_wait(empty + 8 * s, parity, wt)) {
                         ok = false;
                         break;
                     }
-                    tc_fence_after();
+                    if (lead) load_w(f, k, s);
+                }
+                if (lead && !(skip && i == 0)) load_x(f, k, s);
+                if (++s == ST) {
+                    s = 0;
+                    parity ^= 1;
+                }
+            }
+        // every copy lands before the CTA can exit, also after an abort
+        if (lead)
+            for (int j = max(0, i - ST); j < i; ++j)
+                if (!(skip && j == 0)) mbar_wait_bounded(full + 8 * (j % ST), (j / ST) & 1, p.limit_ns);
+    } else if (warp == 1) {
+        // ---------------- MMA issuer
+        pdl_wait();
+        // M = 128, N = BN, E8M0 scales, A = E2M1 (code 1 in kind::mxf4, 5 in kind::mxf8f6f4)
+        constexpr uint32_t IDESC = ((uint32_t)(BN >> 3) << 17) | (1u << 23) | ((uint32_t)(BM >> 7) << 27) |
+                                   (E4M3 ? (5u << 7) : (1u << 7) | (1u << 10));
+        const bool lead = elect_one();
+        const int atoms = (p.nkc + C::CH - 1) / C::CH;
+        const uint32_t sfa = tmem + C::SFA_COL, sfb = tmem + C::SFB_COL;
+        Frag f;
+        int s = 0, n = 0;
+        uint32_t parity = 0;
+        bool ok = true;
+        while (ok && next_frag<BN>(walk, p, start, units, f)) {
+            const int buf = n % C::NACC;
+            if (n >= C::NACC && !warp_wait(acc_empty + 8 * buf, ((n / C::NACC) + 1) & 1, wt)) break;
+            const uint32_t d = tmem + buf * BN;
+            for (int k = f.k0; k < f.k1; ++k) {
+                if (!warp_wait(full + 8 * s, parity, wt)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                if (lead) {
                     const uint32_t st = sbase + s * C::STAGE;
-                    // tcgen05 operations of one thread run in order: these copies follow the
-                    // MMAs that read the columns' last values, and precede the ones below
+                    const int n_atoms = min(C::ATOMS, atoms - k * C::ATOMS);
 #pragma unroll
-                    for (int c = 0; c < C::CH; ++c) {
-                        scales_to_tmem(sfa + 4 * c, desc_scales(st + C::A_BYTES + C::B_BYTES + c * MX_CHUNK));
+                    for (int q = 0; q < C::ATOMS; ++q) {
+                        if (q > 0 && q >= n_atoms) break;
+                        // tcgen05 operations of one thread run in order: these copies follow the
+                        // MMAs that read the columns' last values, and precede the ones below
 #pragma unroll
-                        for (int b = 0; b < C::NB; ++b)
-                            scales_to_tmem(sfb + (c * C::NB + b) * 4,
-                                           desc_scales(st + C::A_BYTES + C::B_BYTES + C::SFA_BYTES + (b * C::CH + c) * MX_CHUNK));
-                    }
-                    const uint64_t a = desc_sw128(st), b = desc_sw128(st + C::A_BYTES);
+                        for (int c = 0; c < C::CH; ++c) {
+                            const int h = q * C::CH + c;
+                            scales_to_tmem(sfa + 4 * h, desc_scales(st + C::OFF_SFA + h * MX_CHUNK));
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        // an MMA takes 1 (E4M3) or 2 (E2M1) of a chunk's 4 scales per row
-                        const uint32_t c = E4M3 ? 0 : j >> 1, id = E4M3 ? j : (j & 1) * 2;
-                        mma_mx<E4M3>(d, a + (uint64_t)(j * 2), b + (uint64_t)(j * 2), IDESC | (id << 4) | (id << 29),
-                                     sfa + 4 * c, sfb + 4 * C::NB * c, k > f.k0 || j > 0);
+                            for (int b = 0; b < C::NB; ++b)
+                                scales_to_tmem(sfb + (h * C::NB + b) * 4, desc_scales(st + C::OFF_SFB + h * C::CHUNK + b * MX_CHUNK));
+                        }
+                        const uint64_t a = desc_sw128(st + q * C::A_BYTES), b = desc_sw128(st + C::OFF_B + q * C::B_BYTES);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            // an MMA takes 1 (E4M3) or 2 (E2M1) of a chunk's 4 scales per row
+                            const uint32_t h = q * C::CH + (E4M3 ? 0 : j >> 1), id = E4M3 ? j : (j & 1) * 2;
+                            mma_mx<E4M3>(d, a + (uint64_t)(j * 2), b + (uint64_t)(j * 2), IDESC | (id << 4) | (id << 29),
+                                         sfa + 4 * h, sfb + 4 * C::NB * h, q > 0 || j > 0 || k > f.k0);
+                        }
                     }
                     mma_commit(empty + 8 * s);
+                    if (k == f.k1 - 1) mma_commit(acc_full + 8 * buf);
                 }
-                if (ok) mma_commit(acc_full + 8 * buf);
-                ++n;
+                __syncwarp();
+                if (++s == ST) {
+                    s = 0;
+                    parity ^= 1;
+                }
             }
-            // no MMA is in flight when the CTA frees its tensor memory
+            ++n;
+        }
+        // no MMA is in flight when the CTA frees its tensor memory
+        if (lead) {
             mma_commit(drain);
             mbar_wait_bounded(drain, 0, p.limit_ns);
         }
+        __syncwarp();
     } else if (warp >= 4) {
         // ---------------- epilogue
-        asm volatile("griddepcontrol.wait;" ::: "memory");
+        pdl_wait();
         const int quad = warp & 3, row = quad * 32 + lane;
         const uint32_t tq = tmem + ((uint32_t)(quad * 32) << 16);
         constexpr int CW = BN < 32 ? 8 : 32;                // columns of one load
@@ -449,7 +374,7 @@ mxmm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ 
                     if (m < p.M) {
 #pragma unroll
                         for (int c = 0; c < CW; ++c)
-                            if (c0 + c < f.valid) store_as(p.dst, p.dst_type, (f.dst_row + c0 + c) * p.M + m, __uint_as_float(r[c]));
+                            if (c0 + c < f.valid) mx_store(p.dst, p.dst_type, (f.dst_row + c0 + c) * p.M + m, __uint_as_float(r[c]));
                     }
                 }
                 tc_fence_before();
@@ -498,7 +423,7 @@ mxmm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ 
                         if (m < p.M) {
 #pragma unroll
                             for (int c = 0; c < 8; ++c)
-                                if (c0 + c < f.valid) store_as(p.dst, p.dst_type, (f.dst_row + c0 + c) * p.M + m, acc[c]);
+                                if (c0 + c < f.valid) mx_store(p.dst, p.dst_type, (f.dst_row + c0 + c) * p.M + m, acc[c]);
                         }
                     }
                 }
@@ -509,7 +434,7 @@ mxmm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ 
         if (p.first) {
             const int64_t from = (int64_t)max(start[p.n_mats], 0) * p.M, to = p.n_rows * p.M;
             for (int64_t i = from + (int64_t)blockIdx.x * 128 + (threadIdx.x - 128); i < to; i += (int64_t)gridDim.x * 128)
-                store_as(p.dst, p.dst_type, i, 0.0f);
+                mx_store(p.dst, p.dst_type, i, 0.0f);
         }
     }
 
@@ -537,7 +462,7 @@ bool get_encode() {
 
 // A product's shape, tile and workspace.
 struct Plan {
-    int bn, rb;
+    int bn;
     int64_t kp, max_groups, tiles_most, n_counters;
     size_t codes, scales, ctrl, part, total;       // offsets after the codes, and the whole size
 };
@@ -547,15 +472,15 @@ struct Plan {
 int pick_bn(int64_t n_rows, int64_t n_tokens, int n_experts) {
     int64_t expect = n_rows;
     if (n_experts > 0) expect = std::min(n_tokens, 2 * ((n_rows + n_experts - 1) / n_experts));
-    for (int bn : {8, 16, 32, 64, 128})
+    for (int bn : {MXMV_TOKENS, 16, 32, 64, 128})
         if (expect <= bn) return bn;
     return 256;
 }
 
 Plan make_plan(int64_t K, int64_t M, int64_t n_rows, int64_t n_tokens, int n_experts, int acts, int sm_count) {
-    Plan q;
+    Plan q{};
     q.bn = pick_bn(n_rows, n_tokens, n_experts);
-    q.rb = std::min(q.bn, 128);
+    if (q.bn == MXMV_TOKENS) return q;             // q4q_mxmv.cu needs no workspace
     q.kp = mx_up(K, MX_KP);
     const int64_t mtiles = (M + BM - 1) / BM;
     // token tiles of BN rows: each segment starts a new one
@@ -568,10 +493,21 @@ Plan make_plan(int64_t K, int64_t M, int64_t n_rows, int64_t n_tokens, int n_exp
     const int64_t rows = tiles_n * q.bn;
     q.codes = 0;
     q.scales = (size_t)mx_up(rows * (acts == Q4Q_ACTS_MXFP8 ? q.kp : q.kp / 2), 1024);
-    q.ctrl = q.scales + (size_t)(rows / q.rb * (q.kp / 128) * MX_CHUNK);
+    q.ctrl = q.scales + (size_t)mx_up(tiles_n * (q.kp / 128) * mx_chunk_bytes(q.bn), 256);
     q.part = q.ctrl + (size_t)mx_up((CTRL_COUNT + q.n_counters) * 4, 256);
     q.total = q.part + (size_t)sm_count * 2 * BM * q.bn * 4;
     return q;
+}
+
+// atoms of a stage (Cfg::ATOMS)
+int atoms_of(int bn, bool e4m3) {
+    switch (bn) {
+        case 16: return e4m3 ? Cfg<16, true>::ATOMS : Cfg<16, false>::ATOMS;
+        case 32: return e4m3 ? Cfg<32, true>::ATOMS : Cfg<32, false>::ATOMS;
+        case 64: return e4m3 ? Cfg<64, true>::ATOMS : Cfg<64, false>::ATOMS;
+        case 128: return e4m3 ? Cfg<128, true>::ATOMS : Cfg<128, false>::ATOMS;
+        default: return e4m3 ? Cfg<256, true>::ATOMS : Cfg<256, false>::ATOMS;
+    }
 }
 
 template <int BN, bool E4M3>
@@ -602,7 +538,6 @@ q4q_status launch_t(const CUtensorMap& tw, const CUtensorMap& tx, const MxParams
 template <bool E4M3>
 q4q_status launch_bn(int bn, const CUtensorMap& tw, const CUtensorMap& tx, const MxParams& p, int grid, cudaStream_t stream, int device) {
     switch (bn) {
-        case 8: return launch_t<8, E4M3>(tw, tx, p, grid, stream, device);
         case 16: return launch_t<16, E4M3>(tw, tx, p, grid, stream, device);
         case 32: return launch_t<32, E4M3>(tw, tx, p, grid, stream, device);
         case 64: return launch_t<64, E4M3>(tw, tx, p, grid, stream, device);
@@ -616,32 +551,28 @@ q4q_status run(const void* src0, int64_t ne00, int64_t ne01, int n_mats, const M
     DeviceInfo info;
     q4q_status st = current_device_info(&info);
     if (st != Q4Q_OK) return st;
+    if (info.cc_major != 10 || !get_encode()) return Q4Q_ERR_CUDA;
+    if (pick_bn(acts.n_rows, n_tokens, acts.first ? n_mats : 0) == MXMV_TOKENS)
+        return mxmv_run(src0, ne00, ne01, n_mats, acts, dst, dst_type, pdl, stream, info, dbg);
     const Plan q = make_plan(ne00, ne01, acts.n_rows, n_tokens, acts.first ? n_mats : 0, acts.acts, info.sm_count);
     if (workspace_bytes < q.total) return Q4Q_ERR_WORKSPACE;
     if (!workspace) return Q4Q_ERR_NULL;
     if (!aligned(workspace, 256)) return Q4Q_ERR_ALIGN;
-    if (info.cc_major != 10 || !get_encode()) return Q4Q_ERR_CUDA;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const bool e4m3 = acts.acts == Q4Q_ACTS_MXFP8;
     const int64_t code_bytes = mx_code_bytes(ne00, ne01), stride = code_bytes + mx_scale_bytes(ne00, ne01);
 
     CUtensorMap tw, tx;
     const cuuint32_t one[3] = {1, 1, 1};
+    const int64_t atoms = q.kp / (e4m3 ? 128 : 256);
+    const int stage_atoms = atoms_of(q.bn, e4m3);
+    if (!mx_encode_weight_map(&tw, src0, ne00, ne01, n_mats, e4m3, stage_atoms)) return Q4Q_ERR_CUDA;
     {
-        const cuuint64_t dims[3] = {(cuuint64_t)(e4m3 ? q.kp : q.kp / 2), (cuuint64_t)ne01, (cuuint64_t)n_mats};
-        const cuuint64_t strides[2] = {(cuuint64_t)(q.kp / 2), (cuuint64_t)stride};
-        const cuuint32_t box[3] = {128, BM, 1};
-        if (g_encode(&tw, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3,
-                     const_cast<void*>(src0), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-            return Q4Q_ERR_CUDA;
-    }
-    {
-        const int64_t row = e4m3 ? q.kp : q.kp / 2;
-        const cuuint64_t dims[2] = {(cuuint64_t)row, (cuuint64_t)(q.max_groups * q.bn)};
-        const cuuint64_t strides[1] = {(cuuint64_t)row};
-        const cuuint32_t box[2] = {128, (cuuint32_t)q.bn};
-        if (g_encode(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, ws + q.codes, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+        // {128 bytes, tokens, atoms}
+        const cuuint64_t dims[3] = {128, (cuuint64_t)(q.max_groups * q.bn), (cuuint64_t)atoms};
+        const cuuint64_t strides[2] = {(cuuint64_t)(e4m3 ? q.kp : q.kp / 2), 128};
+        const cuuint32_t box[3] = {128, (cuuint32_t)q.bn, (cuuint32_t)stage_atoms};
+        if (g_encode(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, ws + q.codes, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
                      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return Q4Q_ERR_CUDA;
     }
@@ -652,7 +583,7 @@ q4q_status run(const void* src0, int64_t ne00, int64_t ne01, int n_mats, const M
     p.max_groups = q.max_groups;
     p.wait_first = pdl;
     p.mtiles = (int)((ne01 + BM - 1) / BM);
-    const int ks = e4m3 ? 128 : 256;
+    const int ks = (e4m3 ? 128 : 256) * stage_atoms;
     p.kst = (int)((ne00 + ks - 1) / ks);
     p.nkc = (int)(q.kp / 128);
     p.first = acts.first;
@@ -666,7 +597,7 @@ q4q_status run(const void* src0, int64_t ne00, int64_t ne01, int n_mats, const M
     p.n_counters = q.n_counters;
     p.limit_ns = dbg ? dbg->limit_ns : WAIT_LIMIT_NS;
     p.fault = dbg ? dbg->fault : 0;
-    st = mx_encode_acts(acts, p.ctrl, CTRL_COUNT + q.n_counters, ws + q.codes, ws + q.scales, q.bn, q.rb, q.max_groups, pdl, stream, info);
+    st = mx_encode_acts(acts, p.ctrl, CTRL_COUNT + q.n_counters, ws + q.codes, ws + q.scales, q.bn, q.max_groups, pdl, stream, info);
     if (st != Q4Q_OK) return st;
     // no more CTAs than there can be parts of the work
     const int64_t stages = q.tiles_most * p.kst;
@@ -695,6 +626,19 @@ q4q_status mul_mat(const void* src0, int64_t ne00, int64_t ne01, const void* src
 }
 
 }  // namespace
+
+// {128 elements (E4M3: widened to bytes) or bytes, weight rows, atoms along K, matrices}
+bool mx_encode_weight_map(CUtensorMap* map, const void* src0, int64_t ne00, int64_t ne01, int n_mats, bool e4m3, int stage_atoms) {
+    if (!get_encode()) return false;
+    const int64_t kp = mx_up(ne00, MX_KP), stride = mx_code_bytes(ne00, ne01) + mx_scale_bytes(ne00, ne01);
+    const cuuint64_t dims[4] = {128, (cuuint64_t)ne01, (cuuint64_t)(kp / (e4m3 ? 128 : 256)), (cuuint64_t)n_mats};
+    const cuuint64_t strides[3] = {(cuuint64_t)(kp / 2), (cuuint64_t)(e4m3 ? 64 : 128), (cuuint64_t)stride};
+    const cuuint32_t box[4] = {128, BM, (cuuint32_t)stage_atoms, 1};
+    const cuuint32_t one[4] = {1, 1, 1, 1};
+    return g_encode(map, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B : CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(src0),
+                    dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 unsigned int mxmm_take_device_status() {
     unsigned int v = 0, z = 0;

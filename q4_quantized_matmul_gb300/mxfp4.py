@@ -13,7 +13,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from . import _check, _dev, _lib, _stream
+from . import Q4QError, _lib
 
 Q4Q_ACTS_MXFP4 = 0
 Q4Q_ACTS_MXFP8 = 1
@@ -21,56 +21,95 @@ Q4Q_ACTS_MXFP8 = 1
 _TYPE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 
 
+# These calls take a few microseconds on the GPU, so what surrounds them is kept short: the
+# C functions are looked up once, pointers are plain integers, and the device is switched
+# only where the tensors lie on another one than the current.
+
+_current_device = torch.cuda.current_device
+_current_stream = torch._C._cuda_getCurrentRawStream
+
+
+class _Lib:
+    """The loaded library's functions, each looked up at its first use."""
+
+    def __getattr__(self, name):
+        fn = getattr(_lib.load(), name)
+        setattr(self, name, fn)
+        return fn
+
+
+_c = _Lib()
+
+
 def _on_device_of(fn):
-    """Run with the device of the first argument current.  Switches only where it is
-    another one: these calls take a few microseconds, and a switch costs as much."""
+    """Run with the device of the first argument current."""
     @functools.wraps(fn)
     def wrapper(t, *args, **kwargs):
-        if isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() != torch.cuda.current_device():
+        if isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() != _current_device():
             with torch.cuda.device(t.device):
                 return fn(t, *args, **kwargs)
         return fn(t, *args, **kwargs)
     return wrapper
 
 
+def _check(fn: str, status: int):
+    if status:
+        raise Q4QError(fn, status)
+
+
+def _stream(stream, like: torch.Tensor) -> int:
+    """The cudaStream_t of a torch stream or integer; the current stream of `like`'s device for None."""
+    if stream is None:
+        return _current_stream(like.get_device())
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else stream
+
+
 def _type(t: torch.Tensor, name: str) -> int:
-    if not isinstance(t, torch.Tensor) or t.dtype not in _TYPE:
+    type_ = _TYPE.get(t.dtype) if isinstance(t, torch.Tensor) else None
+    if type_ is None:
         raise TypeError("%s must be a float32, float16 or bfloat16 tensor" % name)
-    return _TYPE[t.dtype]
+    return type_
 
 
-def _new(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
+def _ptr(t: torch.Tensor, name: str, dtype: Optional[torch.dtype], count: int) -> int:
+    """The address of a contiguous CUDA tensor of `dtype` (any for None) that holds `count` elements (bytes for None)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % name)
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError("%s must be a %s tensor" % (name, dtype))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    have = t.numel() if dtype is not None else t.numel() * t.element_size()
+    if have < count:
+        raise ValueError("%s holds %d %s, the call reads or writes %d" % (
+            name, have, "elements" if dtype is not None else "bytes", count))
+    return t.data_ptr()
+
+
+def _new(like: torch.Tensor, shape, dtype: torch.dtype, stream) -> torch.Tensor:
     """A tensor of the call's own, whose memory the allocator keeps from other users until `stream` is past the call."""
-    t = torch.empty(shape, dtype=dtype, device=device)
+    t = torch.empty(shape, dtype=dtype, device=like.device)
     if stream is not None:
         t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream))
     return t
 
 
-def _int32(t: torch.Tensor, name: str, count: int):
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32:
-        raise TypeError("%s must be an int32 tensor" % name)
-    return _dev(t, name, 4 * count)
+def _scratch(like: torch.Tensor, size: int, stream) -> Optional[torch.Tensor]:
+    return _new(like, (size,), torch.uint8, stream) if size else None
 
 
-def _f32(t: torch.Tensor, name: str, count: int):
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32:
-        raise TypeError("%s must be a float32 tensor" % name)
-    return _dev(t, name, 4 * count)
-
-
-def _matrix(t: torch.Tensor, name: str, type_: torch.dtype, rows: int, cols: int):
-    """An argument of `type_` that holds rows x cols elements."""
-    if not isinstance(t, torch.Tensor) or t.dtype != type_:
-        raise TypeError("%s must be a %s tensor" % (name, type_))
-    return _dev(t, name, rows * cols * t.element_size())
+def _bytes(workspace: Optional[torch.Tensor]):
+    """Address and size of a workspace."""
+    if workspace is None:
+        return None, 0
+    return _ptr(workspace, "workspace", None, 0), workspace.numel() * workspace.element_size()
 
 
 @functools.lru_cache(maxsize=4096)
 def q4q_mxfp4_size(ne00: int, ne01: int) -> int:
     """Bytes of one MXFP4 matrix."""
     n = ctypes.c_size_t(0)
-    _check("q4q_mxfp4_size", _lib.load().q4q_mxfp4_size(ne00, ne01, ctypes.byref(n)))
+    _check("q4q_mxfp4_size", _c.q4q_mxfp4_size(ne00, ne01, ctypes.byref(n)))
     return int(n.value)
 
 
@@ -83,9 +122,9 @@ def q4q_quantize_mxfp4(src: torch.Tensor, dst: Optional[torch.Tensor] = None, st
     nmats, (nrows, ncols) = (src.shape[0] if src.dim() == 3 else 1), src.shape[-2:]
     size = q4q_mxfp4_size(ncols, nrows)
     if dst is None:
-        dst = _new((nmats, size) if src.dim() == 3 else (size,), torch.uint8, src.device, stream)
-    _check("q4q_quantize_mxfp4", _lib.load().q4q_quantize_mxfp4(
-        _dev(src, "src"), type_, _dev(dst, "dst", nmats * size), ncols, nrows, nmats, _stream(stream)))
+        dst = _new(src, (nmats, size) if src.dim() == 3 else (size,), torch.uint8, stream)
+    _check("q4q_quantize_mxfp4", _c.q4q_quantize_mxfp4(
+        _ptr(src, "src", src.dtype, 0), type_, _ptr(dst, "dst", None, nmats * size), ncols, nrows, nmats, _stream(stream, src)))
     return dst
 
 
@@ -98,12 +137,13 @@ def q4q_get_rows_mxfp4(src0: torch.Tensor, ne00: int, ne01: int, ids: Optional[t
     elif n_ids is None:
         n_ids = ne01
     if dst is None:
-        dst = _new((n_ids, ne00), torch.float32, src0.device, stream)
+        dst = _new(src0, (n_ids, ne00), torch.float32, stream)
     if n_ids == 0:
         return dst
-    _check("q4q_get_rows_mxfp4", _lib.load().q4q_get_rows_mxfp4(
-        _dev(src0, "src0", q4q_mxfp4_size(ne00, ne01)), ne00, ne01, _int32(ids, "ids", n_ids) if ids is not None else None,
-        n_ids, _f32(dst, "dst", n_ids * ne00), _stream(stream)))
+    _check("q4q_get_rows_mxfp4", _c.q4q_get_rows_mxfp4(
+        _ptr(src0, "src0", None, q4q_mxfp4_size(ne00, ne01)), ne00, ne01,
+        _ptr(ids, "ids", torch.int32, n_ids) if ids is not None else None, n_ids,
+        _ptr(dst, "dst", torch.float32, n_ids * ne00), _stream(stream, src0)))
     return dst
 
 
@@ -114,20 +154,20 @@ def _acts(src1: torch.Tensor) -> torch.Tensor:
 def _out(dst: Optional[torch.Tensor], dtype: Optional[torch.dtype], like: torch.Tensor, rows: int, cols: int, stream) -> torch.Tensor:
     if dst is not None:
         return dst
-    return _new((rows, cols), like.dtype if dtype is None else dtype, like.device, stream)
+    return _new(like, (rows, cols), like.dtype if dtype is None else dtype, stream)
 
 
 @functools.lru_cache(maxsize=4096)
 def _dense_workspace(ne00: int, ne01: int, ne11: int, acts: int, device: int) -> int:
     n = ctypes.c_size_t(0)
     _check("q4q_mul_mat_mxfp4_workspace_size",
-           _lib.load().q4q_mul_mat_mxfp4_workspace_size(ne00, ne01, ne11, acts, ctypes.byref(n)))
+           _c.q4q_mul_mat_mxfp4_workspace_size(ne00, ne01, ne11, acts, ctypes.byref(n)))
     return int(n.value)
 
 
 def q4q_mul_mat_mxfp4_workspace_size(ne00: int, ne01: int, ne11: int, acts: int = Q4Q_ACTS_MXFP8) -> int:
     """Bytes of workspace of q4q_mul_mat_mxfp4 on the current device."""
-    return _dense_workspace(ne00, ne01, ne11, int(acts), torch.cuda.current_device())
+    return _dense_workspace(ne00, ne01, ne11, int(acts), _current_device())
 
 
 @_on_device_of
@@ -142,11 +182,10 @@ def q4q_mul_mat_mxfp4(src0: torch.Tensor, ne00: int, ne01: int, src1: torch.Tens
     if ne01 * ne11 == 0:
         return dst
     if workspace is None:
-        workspace = _new(q4q_mul_mat_mxfp4_workspace_size(ne00, ne01, ne11, acts), torch.uint8, x.device, stream)
-    _check("q4q_mul_mat_mxfp4", _lib.load().q4q_mul_mat_mxfp4(
-        _dev(src0, "src0", q4q_mxfp4_size(ne00, ne01)), ne00, ne01, _dev(x, "src1"), type_, ne10, ne11, int(acts),
-        _matrix(dst, "dst", dst.dtype, ne11, ne01), _type(dst, "dst"), _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
-        int(flags), _stream(stream)))
+        workspace = _scratch(x, _dense_workspace(ne00, ne01, ne11, acts, _current_device()), stream)
+    _check("q4q_mul_mat_mxfp4", _c.q4q_mul_mat_mxfp4(
+        _ptr(src0, "src0", None, q4q_mxfp4_size(ne00, ne01)), ne00, ne01, _ptr(x, "src1", src1.dtype, 0), type_, ne10, ne11,
+        acts, _ptr(dst, "dst", dst.dtype, ne11 * ne01), _type(dst, "dst"), *_bytes(workspace), flags, _stream(stream, x)))
     return dst
 
 
@@ -156,11 +195,11 @@ def q4q_debug_mul_mat_mxfp4_timeout(src0: torch.Tensor, ne00: int, ne01: int, sr
     """q4q_mul_mat_mxfp4 with its first CTA's first stage left out and every wait bounded by limit_ns:
     q4q_device_status() then reports Q4Q_ERR_TIMEOUT (6) and the result is incomplete."""
     x = _acts(src1)
-    dst = _new((x.shape[0], ne01), torch.float32, x.device, stream)
-    workspace = _new(q4q_mul_mat_mxfp4_workspace_size(ne00, ne01, x.shape[0], acts), torch.uint8, x.device, stream)
-    _check("q4q_debug_mul_mat_mxfp4_timeout", _lib.load().q4q_debug_mul_mat_mxfp4_timeout(
-        _dev(src0, "src0", q4q_mxfp4_size(ne00, ne01)), ne00, ne01, _f32(x, "src1", x.shape[0] * ne00), x.shape[0], int(acts),
-        _dev(dst, "dst"), _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(), int(limit_ns), _stream(stream)))
+    dst = _new(x, (x.shape[0], ne01), torch.float32, stream)
+    workspace = _new(x, q4q_mul_mat_mxfp4_workspace_size(ne00, ne01, x.shape[0], acts), torch.uint8, stream)
+    _check("q4q_debug_mul_mat_mxfp4_timeout", _c.q4q_debug_mul_mat_mxfp4_timeout(
+        _ptr(src0, "src0", None, q4q_mxfp4_size(ne00, ne01)), ne00, ne01, _ptr(x, "src1", torch.float32, x.shape[0] * ne00),
+        x.shape[0], acts, dst.data_ptr(), workspace.data_ptr(), workspace.numel(), limit_ns, _stream(stream, x)))
     return dst
 
 
@@ -175,19 +214,19 @@ def q4q_moe_sort(ids: torch.Tensor, n_experts: int, first: Optional[torch.Tensor
     n_tokens, top_k = ids.shape
     n = n_tokens * top_k
     if first is None:
-        first = _new(n_experts + 1, torch.int32, ids.device, stream)
+        first = _new(ids, (n_experts + 1,), torch.int32, stream)
     if slot is None:
-        slot = _new(n, torch.int32, ids.device, stream)
+        slot = _new(ids, (n,), torch.int32, stream)
     if row is None:
-        row = _new(n, torch.int32, ids.device, stream)
-    _check("q4q_moe_sort", _lib.load().q4q_moe_sort(
-        _int32(ids, "ids", n), n_tokens, top_k, n_experts, _int32(first, "first", n_experts + 1), _int32(slot, "slot", n),
-        _int32(row, "row", n), _stream(stream)))
+        row = _new(ids, (n,), torch.int32, stream)
+    _check("q4q_moe_sort", _c.q4q_moe_sort(
+        _ptr(ids, "ids", torch.int32, n), n_tokens, top_k, n_experts, _ptr(first, "first", torch.int32, n_experts + 1),
+        _ptr(slot, "slot", torch.int32, n), _ptr(row, "row", torch.int32, n), _stream(stream, ids)))
     return first, slot, row
 
 
 def _row_args(first: torch.Tensor, row: torch.Tensor, n: int):
-    return _int32(first, "first", 1), first.numel() - 1, _int32(row, "row", n)
+    return _ptr(first, "first", torch.int32, 1), first.numel() - 1, _ptr(row, "row", torch.int32, n)
 
 
 @_on_device_of
@@ -197,8 +236,9 @@ def q4q_moe_gather(src: torch.Tensor, first: torch.Tensor, row: torch.Tensor, to
     type_, (n, ne0) = _type(src, "src"), src.shape
     dst = _out(dst, None, src, n * top_k, ne0, stream)
     f, e, r = _row_args(first, row, n * top_k)
-    _check("q4q_moe_gather", _lib.load().q4q_moe_gather(
-        _dev(src, "src"), type_, ne0, n, top_k, f, e, r, _matrix(dst, "dst", src.dtype, n * top_k, ne0), _stream(stream)))
+    _check("q4q_moe_gather", _c.q4q_moe_gather(
+        _ptr(src, "src", src.dtype, 0), type_, ne0, n, top_k, f, e, r, _ptr(dst, "dst", src.dtype, n * top_k * ne0),
+        _stream(stream, src)))
     return dst
 
 
@@ -212,8 +252,9 @@ def q4q_moe_gather_back(d_dst: torch.Tensor, first: torch.Tensor, row: torch.Ten
     n = slots // top_k
     d_src = _out(d_src, None, d_dst, n, ne0, stream)
     f, e, r = _row_args(first, row, slots)
-    _check("q4q_moe_gather_back", _lib.load().q4q_moe_gather_back(
-        _dev(d_dst, "d_dst"), type_, ne0, n, top_k, f, e, r, _matrix(d_src, "d_src", d_dst.dtype, n, ne0), _stream(stream)))
+    _check("q4q_moe_gather_back", _c.q4q_moe_gather_back(
+        _ptr(d_dst, "d_dst", d_dst.dtype, 0), type_, ne0, n, top_k, f, e, r, _ptr(d_src, "d_src", d_dst.dtype, n * ne0),
+        _stream(stream, d_dst)))
     return d_src
 
 
@@ -224,9 +265,9 @@ def q4q_moe_combine(rows: torch.Tensor, first: torch.Tensor, row: torch.Tensor, 
     type_, (n, top_k), ne0 = _type(rows, "rows"), weights.shape, rows.shape[-1]
     dst = _out(dst, None, rows, n, ne0, stream)
     f, e, r = _row_args(first, row, n * top_k)
-    _check("q4q_moe_combine", _lib.load().q4q_moe_combine(
-        _matrix(rows, "rows", rows.dtype, n * top_k, ne0), type_, ne0, n, top_k, f, e, r, _f32(weights, "weights", n * top_k),
-        _matrix(dst, "dst", rows.dtype, n, ne0), _stream(stream)))
+    _check("q4q_moe_combine", _c.q4q_moe_combine(
+        _ptr(rows, "rows", rows.dtype, n * top_k * ne0), type_, ne0, n, top_k, f, e, r,
+        _ptr(weights, "weights", torch.float32, n * top_k), _ptr(dst, "dst", rows.dtype, n * ne0), _stream(stream, rows)))
     return dst
 
 
@@ -238,19 +279,19 @@ def q4q_moe_combine_back(d_dst: torch.Tensor, rows: torch.Tensor, first: torch.T
     type_, (n, top_k), ne0 = _type(d_dst, "d_dst"), weights.shape, rows.shape[-1]
     d_rows = _out(d_rows, None, rows, n * top_k, ne0, stream)
     if d_weights is None:
-        d_weights = _new((n, top_k), torch.float32, rows.device, stream)
+        d_weights = _new(rows, (n, top_k), torch.float32, stream)
     f, e, r = _row_args(first, row, n * top_k)
-    _check("q4q_moe_combine_back", _lib.load().q4q_moe_combine_back(
-        _matrix(d_dst, "d_dst", rows.dtype, n, ne0), _matrix(rows, "rows", rows.dtype, n * top_k, ne0), type_, ne0, n, top_k, f, e, r,
-        _f32(weights, "weights", n * top_k), _matrix(d_rows, "d_rows", rows.dtype, n * top_k, ne0),
-        _f32(d_weights, "d_weights", n * top_k), _stream(stream)))
+    _check("q4q_moe_combine_back", _c.q4q_moe_combine_back(
+        _ptr(d_dst, "d_dst", rows.dtype, n * ne0), _ptr(rows, "rows", rows.dtype, n * top_k * ne0), type_, ne0, n, top_k, f, e, r,
+        _ptr(weights, "weights", torch.float32, n * top_k), _ptr(d_rows, "d_rows", rows.dtype, n * top_k * ne0),
+        _ptr(d_weights, "d_weights", torch.float32, n * top_k), _stream(stream, rows)))
     return d_rows, d_weights
 
 
 @functools.lru_cache(maxsize=4096)
 def _id_workspace(ne00: int, ne01: int, n_src1: int, n_rows: int, n_experts: int, acts: int, device: int) -> int:
     n = ctypes.c_size_t(0)
-    _check("q4q_mul_mat_id_mxfp4_workspace_size", _lib.load().q4q_mul_mat_id_mxfp4_workspace_size(
+    _check("q4q_mul_mat_id_mxfp4_workspace_size", _c.q4q_mul_mat_id_mxfp4_workspace_size(
         ne00, ne01, n_src1, n_rows, n_experts, acts, ctypes.byref(n)))
     return int(n.value)
 
@@ -258,7 +299,7 @@ def _id_workspace(ne00: int, ne01: int, n_src1: int, n_rows: int, n_experts: int
 def q4q_mul_mat_id_mxfp4_workspace_size(ne00: int, ne01: int, n_src1: int, n_rows: int, n_experts: int,
                                         acts: int = Q4Q_ACTS_MXFP8) -> int:
     """Bytes of workspace of q4q_mul_mat_id_mxfp4 on the current device."""
-    return _id_workspace(ne00, ne01, n_src1, n_rows, n_experts, int(acts), torch.cuda.current_device())
+    return _id_workspace(ne00, ne01, n_src1, n_rows, n_experts, int(acts), _current_device())
 
 
 @_on_device_of
@@ -279,11 +320,10 @@ def q4q_mul_mat_id_mxfp4(src0: torch.Tensor, ne00: int, ne01: int, src1: torch.T
     if ne01 * n_rows == 0:
         return dst
     if workspace is None:
-        workspace = _new(q4q_mul_mat_id_mxfp4_workspace_size(ne00, ne01, n_src1, n_rows, n_experts, acts), torch.uint8,
-                         x.device, stream)
-    _check("q4q_mul_mat_id_mxfp4", _lib.load().q4q_mul_mat_id_mxfp4(
-        _dev(src0, "src0", n_experts * q4q_mxfp4_size(ne00, ne01)), ne00, ne01, n_experts, _dev(x, "src1"), type_, ne10, n_src1,
-        _int32(first, "first", n_experts + 1), _int32(slot, "slot", n_rows) if slot is not None else None, n_rows, int(top_k),
-        int(acts), _matrix(dst, "dst", dst.dtype, n_rows, ne01), _type(dst, "dst"), _dev(workspace, "workspace"),
-        workspace.numel() * workspace.element_size(), int(flags), _stream(stream)))
+        workspace = _scratch(x, _id_workspace(ne00, ne01, n_src1, n_rows, n_experts, acts, _current_device()), stream)
+    _check("q4q_mul_mat_id_mxfp4", _c.q4q_mul_mat_id_mxfp4(
+        _ptr(src0, "src0", None, n_experts * q4q_mxfp4_size(ne00, ne01)), ne00, ne01, n_experts, _ptr(x, "src1", src1.dtype, 0),
+        type_, ne10, n_src1, _ptr(first, "first", torch.int32, n_experts + 1),
+        _ptr(slot, "slot", torch.int32, n_rows) if slot is not None else None, n_rows, top_k, acts,
+        _ptr(dst, "dst", dst.dtype, n_rows * ne01), _type(dst, "dst"), *_bytes(workspace), flags, _stream(stream, x)))
     return dst
