@@ -45,10 +45,11 @@ namespace {
 
 __device__ unsigned int g_mxmm_status = 0;
 
-constexpr int THREADS = 256;
+constexpr int EPI_WARPS = 8;
+constexpr int THREADS = 128 + 32 * EPI_WARPS;
 constexpr int CTRL_ABORT = 0;                 // control words: the abort word, then a counter per tile
 constexpr int CTRL_COUNT = 64;
-constexpr int MIN_SPLIT_STAGES = 4;           // least stages of a CTA's part in split mode
+constexpr int MIN_SPLIT_ATOMS = 8;            // least work of a CTA in split mode, in 128-byte atoms
 
 // ---------------------------------------------------------------- the work --
 
@@ -57,6 +58,7 @@ struct MxParams {
     int64_t n_rows;               // rows of dst (tokens, or sorted rows)
     int64_t max_groups;           // token tiles of the activation operand
     bool wait_first;              // `first` may still be being written when the kernel starts
+    bool may_split;               // whether tiles may be cut along K
     int mtiles, kst, nkc;         // weight row tiles, K stages, 128-column scale chunks
     const int32_t* first;         // experts' first rows, or null (dense: one segment)
     const uint8_t* w_scales;      // scale plane of matrix 0
@@ -71,20 +73,23 @@ struct MxParams {
     int fault;                    // test only: CTA 0 leaves out its first stage's copies
 };
 
-template <int BN, bool E4M3>
+// CG: CTAs of a tile.  Two of them take 256 weight rows and share the tokens: each loads its
+// 128 rows and half of the token tile, and the pair's MMA reads both halves.
+template <int BN, bool E4M3, int CG>
 struct Cfg {
     static constexpr int ATOM_K = E4M3 ? 128 : 256;       // K of a 128-byte shared-memory row
     static constexpr int CH = ATOM_K / 128;               // scale chunks of an atom
-    static constexpr int ATOMS = BN <= 64 ? (E4M3 ? 2 : 1) : 1;   // atoms of a stage
+    static constexpr int ATOMS = BN <= 64 ? 2 : 1;        // atoms of a stage
     static constexpr int NB = BN <= 128 ? 1 : BN / 128;   // 512-byte pieces of a token tile's scale chunk
     static constexpr int CHUNK = mx_chunk_bytes(BN);
     static constexpr int A_BYTES = BM * 128;              // of one atom
-    static constexpr int B_BYTES = BN * 128;
+    static constexpr int B_ROWS = BN / CG;                // tokens that a CTA loads
+    static constexpr int B_BYTES = B_ROWS * 128;
     static constexpr int OFF_B = ATOMS * A_BYTES;
     static constexpr int OFF_SFA = OFF_B + ATOMS * B_BYTES;
     static constexpr int OFF_SFB = OFF_SFA + ATOMS * CH * MX_CHUNK;
     static constexpr int STAGE = (OFF_SFB + ATOMS * CH * CHUNK + 1023) / 1024 * 1024;
-    // bytes that the operand copies of a stage read (the widened weights as they lie in memory)
+    // bytes that the operand copies of a CTA's stage read (the widened weights as they lie in memory)
     static constexpr int TX = ATOMS * ((E4M3 ? A_BYTES / 2 : A_BYTES) + B_BYTES);
     static constexpr int SEG_BYTES = 2 * (MX_MAX_EXPERTS + 1) * 4 + 64;
     static constexpr int ST_ = (227 * 1024 - 2048 - SEG_BYTES) / STAGE;
@@ -97,6 +102,9 @@ struct Cfg {
     static constexpr int SFB_COL = SFA_COL + 4 * ATOMS * CH;
     static constexpr int USED = SFB_COL + 4 * ATOMS * CH * NB;
     static constexpr int COLS = USED <= 32 ? 32 : USED <= 64 ? 64 : USED <= 128 ? 128 : USED <= 256 ? 256 : 512;
+    // columns of an epilogue warp; the narrowest tile leaves half of the warps idle
+    static constexpr int CW = BN <= 16 ? BN : BN / 2;
+    static constexpr int EPI = BN <= 16 ? 4 : 8;          // epilogue warps at work
     static_assert(USED <= 512 && B_BYTES % 1024 == 0 && ST >= 3 && SMEM <= 227 * 1024, "fits the SM");
 };
 
@@ -104,7 +112,7 @@ struct Cfg {
 struct Walk {
     int64_t pos, end;      // split: stages of the line; whole: tiles, in steps of `parts`
     int64_t total;         // stages in all
-    int parts;             // CTAs that share the work
+    int parts;             // CTAs (or pairs) that share the work
     bool split;
 };
 
@@ -117,7 +125,7 @@ struct Frag {
     bool whole;
 };
 
-template <int BN>
+template <int BN, int CG>
 __device__ __forceinline__ bool next_frag(Walk& w, const MxParams& p, const int* start, const int* units, Frag& f) {
     if (w.pos >= w.end) return false;
     int64_t t;
@@ -154,7 +162,7 @@ __device__ __forceinline__ bool next_frag(Walk& w, const MxParams& p, const int*
     // (from lane 0, so that the compiler knows them to be the same in the whole warp: it keeps
     // the descriptors of copies and MMAs in uniform registers only then)
     f.mat = __shfl_sync(0xffffffffu, e, 0);
-    f.m0 = mt * BM;
+    f.m0 = mt * (BM * CG);
     f.x_row = (__shfl_sync(0xffffffffu, g0, 0) + nt) * BN;
     f.dst_row = (p.first ? start[e] : 0) + (int64_t)nt * BN;
     const int64_t left = (p.first ? (int64_t)start[e + 1] : p.n_rows) - f.dst_row;
@@ -162,19 +170,29 @@ __device__ __forceinline__ bool next_frag(Walk& w, const MxParams& p, const int*
     return true;
 }
 
-// whether `ok` holds in all four epilogue warps
-__device__ __forceinline__ bool epilogue_all(bool ok) {
+// column c of a tile to dst[at + c * stride]
+template <typename T, int N>
+__device__ __forceinline__ void store_columns(void* dst, int64_t at, int64_t stride, const uint32_t (&r)[N], int valid) {
+    T* p = static_cast<T*>(dst) + at;
+#pragma unroll
+    for (int c = 0; c < N; ++c, p += stride)
+        if (c < valid) *p = mx_from_f32<T>(__uint_as_float(r[c]));
+}
+
+// whether `ok` holds in all of the n epilogue threads
+__device__ __forceinline__ bool epilogue_all(bool ok, int n) {
     uint32_t all;
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(all) : "r"((uint32_t)ok) : "memory");
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(all) : "r"((uint32_t)ok), "r"(n) : "memory");
     return all != 0;
 }
 
-template <int BN, bool E4M3>
+template <int BN, bool E4M3, int CG>
 __global__ void __launch_bounds__(THREADS, 1)
-mxmm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_x, const MxParams p) {
-    using C = Cfg<BN, E4M3>;
+mxmm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_x,
+            const __grid_constant__ CUtensorMap tmap_sw, const __grid_constant__ CUtensorMap tmap_sx, const MxParams p) {
+    using C = Cfg<BN, E4M3, CG>;
     constexpr int ST = C::ST;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -189,6 +207,7 @@ mxmm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ 
     int* units = start + MX_MAX_EXPERTS + 1;
     const Waiter wt{abort_flag, p.ctrl + CTRL_ABORT, p.limit_ns, &g_mxmm_status};
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const int rank = CG == 2 ? (int)(blockIdx.x & 1) : 0;        // in the pair; 0 issues its MMAs
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < ST; ++s) {
@@ -197,13 +216,15 @@ mxmm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ 
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(acc_full + 8 * s, 1);
-            mbar_init(acc_empty + 8 * s, 4);
+            mbar_init(acc_empty + 8 * s, CG * C::EPI);
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
+        prefetch_map(&tmap_w);
+        prefetch_map(&tmap_x);
     }
-    if (warp == 1) tmem_alloc(slot_addr, C::COLS);
+    if (warp == 1) tmem_alloc<CG>(slot_addr, C::COLS);
     pdl_trigger();
     // the experts' segments are known before the activations are
     Walk walk;
@@ -216,6 +237,10 @@ mxmm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ 
     }
     tc_fence_before();
     __syncthreads();
+    if constexpr (CG == 2) {                                     // both CTAs' barriers and tensor memory exist
+        cluster_arrive();
+        cluster_wait();
+    }
     tc_fence_after();
     uint32_t tmem;
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(slot_addr));
@@ -223,16 +248,15 @@ mxmm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ 
 
     {
         const int64_t tiles = (int64_t)__shfl_sync(0xffffffffu, units[p.first ? p.n_mats : 1], 0) * p.mtiles;   // the same in the whole warp
+        const int workers = (int)gridDim.x / CG, me = (int)blockIdx.x / CG;
         walk.total = tiles * p.kst;
-        // whole tiles where they fill the SMs within a tenth; equal parts of the line elsewhere
-        const int64_t rounds = (tiles + gridDim.x - 1) / gridDim.x;
-        walk.split = rounds * gridDim.x * 10 > tiles * 11 && tiles <= p.n_counters;
-        const int64_t most = walk.split ? max(walk.total / MIN_SPLIT_STAGES, (int64_t)1) : tiles;
-        walk.parts = (int)max((int64_t)1, min((int64_t)gridDim.x, most));
+        walk.split = CG == 1 && p.may_split && tiles <= p.n_counters;
+        const int64_t most = walk.split ? max(walk.total * C::ATOMS / MIN_SPLIT_ATOMS, (int64_t)1) : tiles;
+        walk.parts = (int)max((int64_t)1, min((int64_t)workers, most));
         walk.pos = walk.end = 0;
-        if ((int)blockIdx.x < walk.parts) {
-            walk.pos = walk.split ? blockIdx.x * walk.total / walk.parts : blockIdx.x;
-            walk.end = walk.split ? (blockIdx.x + 1) * walk.total / walk.parts : tiles;
+        if (me < walk.parts) {
+            walk.pos = walk.split ? me * walk.total / walk.parts : me;
+            walk.end = walk.split ? (me + 1) * walk.total / walk.parts : tiles;
         }
     }
 
@@ -240,34 +264,50 @@ mxmm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ 
         // ---------------- producer
         const bool lead = elect_one();
         auto load_w = [&](const Frag& g, int k, int s) {
-            const uint32_t st = sbase + s * C::STAGE, bar = full + 8 * s;
-            const int chunks = min(C::ATOMS * C::CH, p.nkc - k * (C::ATOMS * C::CH));
-            mbar_arrive_expect_tx(bar, C::TX + chunks * (MX_CHUNK + C::CHUNK));
-            tma_load_4d(st, &tmap_w, 0, g.m0, k * C::ATOMS, g.mat, bar);
-            bulk_g2s(st + C::OFF_SFA,
-                     p.w_scales + g.mat * p.mat_stride + ((int64_t)(g.m0 / BM) * p.nkc + k * (C::ATOMS * C::CH)) * MX_CHUNK,
-                     chunks * MX_CHUNK, bar);
+            const uint32_t st = sbase + s * C::STAGE;
+            const int kc = k * (C::ATOMS * C::CH), chunks = min(C::ATOMS * C::CH, p.nkc - kc);
+            if constexpr (CG == 1) {
+                const uint32_t bar = full + 8 * s;
+                mbar_arrive_expect_tx(bar, C::TX + chunks * (MX_CHUNK + C::CHUNK));
+                tma_load_4d(st, &tmap_w, 0, g.m0, k * C::ATOMS, g.mat, bar);
+                bulk_g2s(st + C::OFF_SFA, p.w_scales + g.mat * p.mat_stride + ((int64_t)(g.m0 / BM) * p.nkc + kc) * MX_CHUNK,
+                         chunks * MX_CHUNK, bar);
+            } else {
+                // all of the pair's bytes are counted on the first CTA's barrier
+                const uint32_t bar = mapa_shared(full + 8 * s, 0);
+                if (rank == 0) mbar_arrive_expect_tx(full + 8 * s, CG * (C::TX + C::ATOMS * C::CH * (MX_CHUNK + C::CHUNK)));
+                // (a second half past the last row repeats the first; its rows are not stored)
+                const int rows = g.m0 + rank * BM < p.M ? g.m0 + rank * BM : g.m0;
+                tma_load_4d_pair(st, &tmap_w, 0, rows, k * C::ATOMS, g.mat, bar);
+                tma_load_4d_pair(st + C::OFF_SFA, &tmap_sw, 0, kc, rows / BM, g.mat, bar);
+            }
         };
         auto load_x = [&](const Frag& g, int k, int s) {
-            const uint32_t st = sbase + s * C::STAGE, bar = full + 8 * s;
-            const int chunks = min(C::ATOMS * C::CH, p.nkc - k * (C::ATOMS * C::CH));
-            tma_load_3d(st + C::OFF_B, &tmap_x, 0, g.x_row, k * C::ATOMS, bar);
-            bulk_g2s(st + C::OFF_SFB, p.x_scales + ((int64_t)(g.x_row / BN) * p.nkc + k * (C::ATOMS * C::CH)) * C::CHUNK,
-                     chunks * C::CHUNK, bar);
+            const uint32_t st = sbase + s * C::STAGE;
+            const int kc = k * (C::ATOMS * C::CH), chunks = min(C::ATOMS * C::CH, p.nkc - kc);
+            if constexpr (CG == 1) {
+                const uint32_t bar = full + 8 * s;
+                tma_load_3d(st + C::OFF_B, &tmap_x, 0, g.x_row, k * C::ATOMS, bar);
+                bulk_g2s(st + C::OFF_SFB, p.x_scales + ((int64_t)(g.x_row / BN) * p.nkc + kc) * C::CHUNK, chunks * C::CHUNK, bar);
+            } else {
+                const uint32_t bar = mapa_shared(full + 8 * s, 0);
+                tma_load_3d_pair(st + C::OFF_B, &tmap_x, 0, g.x_row + rank * C::B_ROWS, k * C::ATOMS, bar);
+                tma_load_3d_pair(st + C::OFF_SFB, &tmap_sx, 0, kc, g.x_row / BN, bar);
+            }
         };
         // the weights of the first stages do not wait for the activation encoder
         const bool skip = p.fault && blockIdx.x == 0;
         Walk ahead = walk;
         Frag f;
         int pre = 0;
-        while (pre < ST && next_frag<BN>(ahead, p, start, units, f))
+        while (pre < ST && next_frag<BN, CG>(ahead, p, start, units, f))
             for (int k = f.k0; k < f.k1 && pre < ST; ++k, ++pre)
                 if (lead && !(skip && pre == 0)) load_w(f, k, pre);
         pdl_wait();
         int i = 0, s = 0;
         uint32_t parity = 1;                 // of the wait on the slot's previous use, from its second on
         bool ok = true;
-        while (ok && next_frag<BN>(walk, p, start, units, f))
+        while (ok && next_frag<BN, CG>(walk, p, start, units, f))
             for (int k = f.k0; k < f.k1; ++k, ++i) {
                 if (i >= pre) {
                     if (i >= ST && !warp_wait(empty + 8 * s, parity, wt)) {
@@ -282,148 +322,150 @@ mxmm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ 
                     parity ^= 1;
                 }
             }
-        // every copy lands before the CTA can exit, also after an abort
-        if (lead)
+        // every copy lands before the CTA (or the pair) can exit, also after an abort
+        if (lead && rank == 0)
             for (int j = max(0, i - ST); j < i; ++j)
-                if (!(skip && j == 0)) mbar_wait_bounded(full + 8 * (j % ST), (j / ST) & 1, p.limit_ns);
+                if (!(skip && j == 0) && !mbar_wait_bounded(full + 8 * (j % ST), (j / ST) & 1, p.limit_ns)) break;
     } else if (warp == 1) {
         // ---------------- MMA issuer
         pdl_wait();
-        // M = 128, N = BN, E8M0 scales, A = E2M1 (code 1 in kind::mxf4, 5 in kind::mxf8f6f4)
-        constexpr uint32_t IDESC = ((uint32_t)(BN >> 3) << 17) | (1u << 23) | ((uint32_t)(BM >> 7) << 27) |
+        // M = 128 for each CTA, N = BN, E8M0 scales, A = E2M1 (code 1 in kind::mxf4, 5 in kind::mxf8f6f4)
+        constexpr uint32_t IDESC = ((uint32_t)(BN >> 3) << 17) | (1u << 23) | ((uint32_t)(CG * BM >> 7) << 27) |
                                    (E4M3 ? (5u << 7) : (1u << 7) | (1u << 10));
-        const bool lead = elect_one();
-        const int atoms = (p.nkc + C::CH - 1) / C::CH;
-        const uint32_t sfa = tmem + C::SFA_COL, sfb = tmem + C::SFB_COL;
-        Frag f;
-        int s = 0, n = 0;
-        uint32_t parity = 0;
-        bool ok = true;
-        while (ok && next_frag<BN>(walk, p, start, units, f)) {
-            const int buf = n % C::NACC;
-            if (n >= C::NACC && !warp_wait(acc_empty + 8 * buf, ((n / C::NACC) + 1) & 1, wt)) break;
-            const uint32_t d = tmem + buf * BN;
-            for (int k = f.k0; k < f.k1; ++k) {
-                if (!warp_wait(full + 8 * s, parity, wt)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                if (lead) {
-                    const uint32_t st = sbase + s * C::STAGE;
-                    const int n_atoms = min(C::ATOMS, atoms - k * C::ATOMS);
-#pragma unroll
-                    for (int q = 0; q < C::ATOMS; ++q) {
-                        if (q > 0 && q >= n_atoms) break;
-                        // tcgen05 operations of one thread run in order: these copies follow the
-                        // MMAs that read the columns' last values, and precede the ones below
-#pragma unroll
-                        for (int c = 0; c < C::CH; ++c) {
-                            const int h = q * C::CH + c;
-                            scales_to_tmem(sfa + 4 * h, desc_scales(st + C::OFF_SFA + h * MX_CHUNK));
-#pragma unroll
-                            for (int b = 0; b < C::NB; ++b)
-                                scales_to_tmem(sfb + (h * C::NB + b) * 4, desc_scales(st + C::OFF_SFB + h * C::CHUNK + b * MX_CHUNK));
-                        }
-                        const uint64_t a = desc_sw128(st + q * C::A_BYTES), b = desc_sw128(st + C::OFF_B + q * C::B_BYTES);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            // an MMA takes 1 (E4M3) or 2 (E2M1) of a chunk's 4 scales per row
-                            const uint32_t h = q * C::CH + (E4M3 ? 0 : j >> 1), id = E4M3 ? j : (j & 1) * 2;
-                            mma_mx<E4M3>(d, a + (uint64_t)(j * 2), b + (uint64_t)(j * 2), IDESC | (id << 4) | (id << 29),
-                                         sfa + 4 * h, sfb + 4 * C::NB * h, q > 0 || j > 0 || k > f.k0);
-                        }
+        if (rank == 0) {
+            const bool lead = elect_one();
+            const int atoms = (p.nkc + C::CH - 1) / C::CH;
+            const uint32_t sfa = tmem + C::SFA_COL, sfb = tmem + C::SFB_COL;
+            Frag f;
+            int s = 0, n = 0;
+            uint32_t parity = 0;
+            bool ok = true;
+            while (ok && next_frag<BN, CG>(walk, p, start, units, f)) {
+                const int buf = n % C::NACC;
+                if (n >= C::NACC && !warp_wait(acc_empty + 8 * buf, ((n / C::NACC) + 1) & 1, wt)) break;
+                const uint32_t d = tmem + buf * BN;
+                const int k0 = __shfl_sync(0xffffffffu, f.k0, 0), k1 = __shfl_sync(0xffffffffu, f.k1, 0);
+                for (int k = k0; k < k1; ++k) {
+                    if (!warp_wait(full + 8 * s, parity, wt)) {
+                        ok = false;
+                        break;
                     }
-                    mma_commit(empty + 8 * s);
-                    if (k == f.k1 - 1) mma_commit(acc_full + 8 * buf);
+                    tc_fence_after();
+                    if (lead) {
+                        const uint32_t st = sbase + s * C::STAGE;
+                        const int n_atoms = min(C::ATOMS, atoms - k * C::ATOMS);
+#pragma unroll
+                        for (int q = 0; q < C::ATOMS; ++q) {
+                            if (q > 0 && q >= n_atoms) break;
+                            // tcgen05 operations of one thread run in order: these copies follow the
+                            // MMAs that read the columns' last values, and precede the ones below
+#pragma unroll
+                            for (int c = 0; c < C::CH; ++c) {
+                                const int h = q * C::CH + c;
+                                scales_to_tmem<CG>(sfa + 4 * h, desc_scales(st + C::OFF_SFA + h * MX_CHUNK));
+#pragma unroll
+                                for (int b = 0; b < C::NB; ++b)
+                                    scales_to_tmem<CG>(sfb + (h * C::NB + b) * 4, desc_scales(st + C::OFF_SFB + h * C::CHUNK + b * MX_CHUNK));
+                            }
+                            const uint64_t a = desc_sw128(st + q * C::A_BYTES), b = desc_sw128(st + C::OFF_B + q * C::B_BYTES);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                // an MMA takes 1 (E4M3) or 2 (E2M1) of a chunk's 4 scales per row
+                                const uint32_t h = q * C::CH + (E4M3 ? 0 : j >> 1), id = E4M3 ? j : (j & 1) * 2;
+                                mma_mx<E4M3, CG>(d, a + (uint64_t)(j * 2), b + (uint64_t)(j * 2), IDESC | (id << 4) | (id << 29),
+                                                 sfa + 4 * h, sfb + 4 * C::NB * h, q > 0 || j > 0 || k > k0);
+                            }
+                        }
+                        mma_commit<CG>(empty + 8 * s);
+                        if (k == k1 - 1) mma_commit<CG>(acc_full + 8 * buf);
+                    }
+                    __syncwarp();
+                    if (++s == ST) {
+                        s = 0;
+                        parity ^= 1;
+                    }
                 }
-                __syncwarp();
-                if (++s == ST) {
-                    s = 0;
-                    parity ^= 1;
-                }
+                ++n;
             }
-            ++n;
-        }
-        // no MMA is in flight when the CTA frees its tensor memory
-        if (lead) {
-            mma_commit(drain);
-            mbar_wait_bounded(drain, 0, p.limit_ns);
+            // no MMA is in flight when the CTAs free their tensor memory
+            if (lead) {
+                mma_commit<CG>(drain);
+                mbar_wait_bounded(drain, 0, p.limit_ns);
+            }
         }
         __syncwarp();
-    } else if (warp >= 4) {
-        // ---------------- epilogue
+    } else if (warp >= 4 && warp < 4 + C::EPI) {
+        // ---------------- epilogue: two warps to a lane quadrant, half of the columns each
         pdl_wait();
-        const int quad = warp & 3, row = quad * 32 + lane;
-        const uint32_t tq = tmem + ((uint32_t)(quad * 32) << 16);
-        constexpr int CW = BN < 32 ? 8 : 32;                // columns of one load
-        Walk mine = walk;
+        constexpr int CW = C::CW, N_THREADS = 32 * C::EPI;
+        const int quad = warp & 3, row = quad * 32 + lane, col0 = (warp - 4) / 4 * CW;
+        const uint32_t tq = tmem + ((uint32_t)(quad * 32) << 16) + col0;
+        const uint32_t freed = CG == 2 ? mapa_shared(acc_empty, 0) : acc_empty;
+        const Walk mine = walk;
         Frag f;
         int n = 0;
-        while (next_frag<BN>(walk, p, start, units, f)) {
+        while (next_frag<BN, CG>(walk, p, start, units, f)) {
             const int buf = n % C::NACC;
-            // one verdict for all four warps: none of them waits below for one that gave up
-            if (!epilogue_all(warp_wait(acc_full + 8 * buf, (n / C::NACC) & 1, wt))) break;
+            // one verdict for all warps: none of them waits below for one that gave up
+            if (!epilogue_all(warp_wait(acc_full + 8 * buf, (n / C::NACC) & 1, wt), N_THREADS)) break;
             tc_fence_after();
-            const int m = f.m0 + row;
+            const int m = f.m0 + rank * BM + row;
+            // the whole tile into registers, so that the next one's MMAs can start
+            uint32_t r[CW];
+            tmem_ld<CW>(tq + (uint32_t)(buf * BN), r);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (CG == 2) mbar_arrive_cluster(freed + 8 * buf);
+                else mbar_arrive(freed + 8 * buf);
+            }
+            const int valid = f.valid - col0;
+            const int64_t at = (f.dst_row + col0) * p.M + m;
             if (f.whole) {
-#pragma unroll 1
-                for (int c0 = 0; c0 < BN; c0 += CW) {
-                    uint32_t r[CW];
-                    tmem_ld<CW>(tq + (uint32_t)(buf * BN + c0), r);
-                    if (m < p.M) {
-#pragma unroll
-                        for (int c = 0; c < CW; ++c)
-                            if (c0 + c < f.valid) mx_store(p.dst, p.dst_type, (f.dst_row + c0 + c) * p.M + m, __uint_as_float(r[c]));
-                    }
+                if (m < p.M) {
+                    if (p.dst_type == Q4Q_TYPE_F32) store_columns<float, CW>(p.dst, at, p.M, r, valid);
+                    else if (p.dst_type == Q4Q_TYPE_F16) store_columns<__half, CW>(p.dst, at, p.M, r, valid);
+                    else store_columns<__nv_bfloat16, CW>(p.dst, at, p.M, r, valid);
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(acc_empty + 8 * buf);
             } else {
                 // this CTA's partial tile: slot 0 if it starts inside the tile, else slot 1
                 const int64_t me = blockIdx.x;
-                float* out = p.part + (me * 2 + (f.k0 == 0 ? 1 : 0)) * (int64_t)(BM * BN) + row;
-#pragma unroll 1
-                for (int c0 = 0; c0 < BN; c0 += CW) {
-                    uint32_t r[CW];
-                    tmem_ld<CW>(tq + (uint32_t)(buf * BN + c0), r);
+                constexpr int64_t PART = BM * BN;
+                float* out = p.part + (me * 2 + (f.k0 == 0 ? 1 : 0)) * PART + col0 * BM + row;
 #pragma unroll
-                    for (int c = 0; c < CW; ++c)
-                        if (c0 + c < f.valid) __stcg(out + (c0 + c) * BM, __uint_as_float(r[c]));
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(acc_empty + 8 * buf);
+                for (int c = 0; c < CW; ++c)
+                    if (c < valid) __stcg(out + c * BM, __uint_as_float(r[c]));
                 // the CTAs that share the tile: from the owner of its first stage to that of its last
                 const int64_t s0 = f.tile * p.kst, s1 = s0 + p.kst - 1;
                 const int64_t c_first = ((s0 + 1) * mine.parts - 1) / mine.total, c_last = ((s1 + 1) * mine.parts - 1) / mine.total;
                 __threadfence();
-                asm volatile("bar.sync 1, 128;" ::: "memory");
+                asm volatile("bar.sync 1, %0;" ::"r"(N_THREADS) : "memory");
                 if (threadIdx.x == 128) {
                     const unsigned int before = atomicAdd(p.ctrl + CTRL_COUNT + f.tile, 1u);
                     *last_flag = before == (unsigned int)(c_last - c_first);
                 }
-                asm volatile("bar.sync 1, 128;" ::: "memory");
+                asm volatile("bar.sync 1, %0;" ::"r"(N_THREADS) : "memory");
                 const bool last = *last_flag != 0;
-                asm volatile("bar.sync 1, 128;" ::: "memory");
+                asm volatile("bar.sync 1, %0;" ::"r"(N_THREADS) : "memory");
                 if (last) {
+                    // all columns of one CTA's part in flight at a time, the parts in the order of K
                     __threadfence();
-                    for (int c0 = 0; c0 < f.valid; c0 += 8) {
-                        float acc[8];
-                        const float* q = p.part + (c_first * 2 + 1) * (int64_t)(BM * BN) + row + c0 * BM;
+                    constexpr int CC = CW < 32 ? CW : 32;
+#pragma unroll 1
+                    for (int c0 = 0; c0 < CW && c0 < valid; c0 += CC) {
+                        float acc[CC];
+                        for (int64_t o = c_first; o <= c_last; ++o) {
+                            const float* q = p.part + (o * 2 + (o == c_first ? 1 : 0)) * PART + (col0 + c0) * BM + row;
+                            float v[CC];
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) acc[c] = c0 + c < f.valid ? __ldcg(q + c * BM) : 0.0f;
-                        for (int64_t o = c_first + 1; o <= c_last; ++o) {
-                            q = p.part + o * 2 * (int64_t)(BM * BN) + row + c0 * BM;
+                            for (int c = 0; c < CC; ++c) v[c] = c0 + c < valid ? __ldcg(q + c * BM) : 0.0f;
 #pragma unroll
-                            for (int c = 0; c < 8; ++c)
-                                if (c0 + c < f.valid) acc[c] = __fadd_rn(acc[c], __ldcg(q + c * BM));
+                            for (int c = 0; c < CC; ++c) acc[c] = o == c_first ? v[c] : __fadd_rn(acc[c], v[c]);
                         }
                         if (m < p.M) {
 #pragma unroll
-                            for (int c = 0; c < 8; ++c)
-                                if (c0 + c < f.valid) mx_store(p.dst, p.dst_type, (f.dst_row + c0 + c) * p.M + m, acc[c]);
+                            for (int c = 0; c < CC; ++c)
+                                if (c0 + c < valid) mx_store(p.dst, p.dst_type, at + (int64_t)(c0 + c) * p.M, acc[c]);
                         }
                     }
                 }
@@ -432,16 +474,20 @@ mxmm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ 
         }
         // rows of no expert are zeros
         if (p.first) {
-            const int64_t from = (int64_t)max(start[p.n_mats], 0) * p.M, to = p.n_rows * p.M;
-            for (int64_t i = from + (int64_t)blockIdx.x * 128 + (threadIdx.x - 128); i < to; i += (int64_t)gridDim.x * 128)
+            const int64_t from = (int64_t)start[p.n_mats] * p.M, to = p.n_rows * p.M;
+            for (int64_t i = from + (int64_t)blockIdx.x * N_THREADS + (threadIdx.x - 128); i < to; i += (int64_t)gridDim.x * N_THREADS)
                 mx_store(p.dst, p.dst_type, i, 0.0f);
         }
     }
 
     tc_fence_before();
     __syncthreads();
+    if constexpr (CG == 2) {                                     // neither CTA leaves while the other uses its memory
+        cluster_arrive();
+        cluster_wait();
+    }
     tc_fence_after();
-    if (warp == 1) tmem_dealloc(tmem, C::COLS);
+    if (warp == 1) tmem_dealloc<CG>(tmem, C::COLS);
 }
 
 // ------------------------------------------------------------------ host ----
@@ -460,61 +506,82 @@ bool get_encode() {
     return g_encode != nullptr;
 }
 
-// A product's shape, tile and workspace.
+// A product's tile and workspace.
 struct Plan {
-    int bn;
-    int64_t kp, max_groups, tiles_most, n_counters;
+    int bn, cg;
+    bool split;
+    int64_t kp, max_groups, n_counters;
     size_t codes, scales, ctrl, part, total;       // offsets after the codes, and the whole size
 };
 
-// Token tile: the least that holds the tokens a segment is expected to have (all of them,
-// or twice the mean of the experts' shares; a larger share takes several tiles).
-int pick_bn(int64_t n_rows, int64_t n_tokens, int n_experts) {
-    int64_t expect = n_rows;
-    if (n_experts > 0) expect = std::min(n_tokens, 2 * ((n_rows + n_experts - 1) / n_experts));
-    for (int bn : {MXMV_TOKENS, 16, 32, 64, 128})
-        if (expect <= bn) return bn;
-    return 256;
+// Whether few tokens are expected: all of them, or twice the mean of the experts' shares.
+int64_t expected_rows(int64_t n_rows, int64_t n_tokens, int n_experts) {
+    return n_experts > 0 ? std::min(n_tokens, 2 * ((n_rows + n_experts - 1) / n_experts)) : n_rows;
+}
+
+// The tile, and whether tiles are cut along K.  Up to 64 expected rows, the least tile that
+// holds them, cut into equal parts.  Above that, the choice that is expected to take least:
+// SM rounds x K x the cycles of an atom (what its copies take: 2.1 a row of 128 bytes, or its
+// MMAs: 2 a token, 1 for each CTA of a pair) + 3000 a tile, of
+//   one CTA a tile of 128 x 128, cut along K;  a pair a tile of 256 x 128 or 256 x 256.
+void pick_tile(Plan& q, int64_t K, int64_t M, int64_t n_rows, int64_t n_tokens, int n_experts, int acts, int sm_count) {
+    const int64_t expect = expected_rows(n_rows, n_tokens, n_experts);
+    q.cg = 1;
+    q.split = true;
+    for (int bn : {MXMV_TOKENS, 16, 32, 64})
+        if (expect <= bn) {
+            q.bn = bn;
+            return;
+        }
+    const int64_t segments = n_experts > 0 ? std::min<int64_t>(n_experts, n_rows) : 1, mean = (n_rows + segments - 1) / segments;
+    const int64_t atoms = (K + (acts == Q4Q_ACTS_MXFP8 ? 127 : 255)) / (acts == Q4Q_ACTS_MXFP8 ? 128 : 256);
+    double least = 1e300;
+    const struct { int bn, cg; } forms[] = {{64, 1}, {128, 1}, {128, 2}, {256, 2}};
+    for (const auto& f : forms) {
+        const int64_t tiles = segments * ((mean + f.bn - 1) / f.bn) * ((M + BM * f.cg - 1) / (BM * f.cg));
+        const int64_t workers = sm_count / f.cg;
+        const double rounds = f.cg == 1 ? std::max(1.0, (double)tiles / workers) : (double)((tiles + workers - 1) / workers);
+        const double cycles = std::max(2.1 * (BM + f.bn / f.cg), 2.0 * f.bn);
+        // a cut tile is also written to and read from the workspace
+        const double cost = rounds * (atoms * cycles + 3000) + (f.cg == 1 ? 6000 : 0);
+        if (cost < least) {
+            least = cost;
+            q.bn = f.bn;
+            q.cg = f.cg;
+            q.split = f.cg == 1;
+        }
+    }
 }
 
 Plan make_plan(int64_t K, int64_t M, int64_t n_rows, int64_t n_tokens, int n_experts, int acts, int sm_count) {
     Plan q{};
-    q.bn = pick_bn(n_rows, n_tokens, n_experts);
+    pick_tile(q, K, M, n_rows, n_tokens, n_experts, acts, sm_count);
     if (q.bn == MXMV_TOKENS) return q;             // q4q_mxmv.cu needs no workspace
     q.kp = mx_up(K, MX_KP);
-    const int64_t mtiles = (M + BM - 1) / BM;
-    // token tiles of BN rows: each segment starts a new one
-    const int64_t extra = n_experts > 0 ? std::min<int64_t>(n_experts, n_rows) : 0;
-    const int64_t tiles_n = (n_rows + q.bn - 1) / q.bn + extra;
+    // token tiles: each segment starts a new one
+    const int64_t tiles_n = (n_rows + q.bn - 1) / q.bn + (n_experts > 0 ? std::min<int64_t>(n_experts, n_rows) : 0);
     q.max_groups = tiles_n;
-    q.tiles_most = tiles_n * mtiles;
-    // split mode needs a counter for each tile; with more tiles than this whole tiles fill the SMs
-    q.n_counters = std::min<int64_t>(q.tiles_most, 16 * (int64_t)sm_count);
-    const int64_t rows = tiles_n * q.bn;
-    q.codes = 0;
-    q.scales = (size_t)mx_up(rows * (acts == Q4Q_ACTS_MXFP8 ? q.kp : q.kp / 2), 1024);
+    // a counter for each tile that may be cut; with more tiles than this whole ones fill the SMs
+    q.n_counters = q.split ? std::min<int64_t>(tiles_n * ((M + BM - 1) / BM), 64 * (int64_t)sm_count) : 0;
+    q.scales = (size_t)mx_up(tiles_n * q.bn * (acts == Q4Q_ACTS_MXFP8 ? q.kp : q.kp / 2), 1024);
     q.ctrl = q.scales + (size_t)mx_up(tiles_n * (q.kp / 128) * mx_chunk_bytes(q.bn), 256);
     q.part = q.ctrl + (size_t)mx_up((CTRL_COUNT + q.n_counters) * 4, 256);
-    q.total = q.part + (size_t)sm_count * 2 * BM * q.bn * 4;
+    q.total = q.part + (q.split ? (size_t)sm_count * 2 * BM * q.bn * 4 : 0);
     return q;
 }
 
-// atoms of a stage (Cfg::ATOMS)
-int atoms_of(int bn, bool e4m3) {
-    switch (bn) {
-        case 16: return e4m3 ? Cfg<16, true>::ATOMS : Cfg<16, false>::ATOMS;
-        case 32: return e4m3 ? Cfg<32, true>::ATOMS : Cfg<32, false>::ATOMS;
-        case 64: return e4m3 ? Cfg<64, true>::ATOMS : Cfg<64, false>::ATOMS;
-        case 128: return e4m3 ? Cfg<128, true>::ATOMS : Cfg<128, false>::ATOMS;
-        default: return e4m3 ? Cfg<256, true>::ATOMS : Cfg<256, false>::ATOMS;
-    }
-}
+int atoms_of(int bn) { return bn <= 64 ? 2 : 1; }      // of a stage (Cfg::ATOMS)
 
-template <int BN, bool E4M3>
-q4q_status launch_t(const CUtensorMap& tw, const CUtensorMap& tx, const MxParams& p, int grid, cudaStream_t stream, int device) {
-    using C = Cfg<BN, E4M3>;
+struct Maps {
+    CUtensorMap w, x, sw, sx;
+};
+
+template <int BN, bool E4M3, int CG>
+q4q_status launch_t(const Maps& maps, const MxParams& p, int64_t workers, cudaStream_t stream, int device) {
+    using C = Cfg<BN, E4M3, CG>;
+    static_assert(C::ATOMS == (BN <= 64 ? 2 : 1), "the tensor maps' boxes");
     static std::atomic<int> configured[64];
-    auto kern = mxmm_kernel<BN, E4M3>;
+    auto kern = mxmm_kernel<BN, E4M3, CG>;
     if (device < 0 || device >= 64) return Q4Q_ERR_CUDA;
     if (!configured[device].load()) {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
@@ -522,28 +589,46 @@ q4q_status launch_t(const CUtensorMap& tw, const CUtensorMap& tx, const MxParams
         configured[device].store(1);
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
+    cfg.gridDim = dim3((unsigned)(workers * CG));
     cfg.blockDim = dim3(THREADS);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // behind the activation encoder
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kern, tw, tx, p) != cudaSuccess) return (cudaGetLastError(), Q4Q_ERR_CUDA);
+    cfg.numAttrs = CG == 1 ? 1 : 2;
+    if (cudaLaunchKernelEx(&cfg, kern, maps.w, maps.x, maps.sw, maps.sx, p) != cudaSuccess) return (cudaGetLastError(), Q4Q_ERR_CUDA);
     return launch_status();
 }
 
 template <bool E4M3>
-q4q_status launch_bn(int bn, const CUtensorMap& tw, const CUtensorMap& tx, const MxParams& p, int grid, cudaStream_t stream, int device) {
-    switch (bn) {
-        case 16: return launch_t<16, E4M3>(tw, tx, p, grid, stream, device);
-        case 32: return launch_t<32, E4M3>(tw, tx, p, grid, stream, device);
-        case 64: return launch_t<64, E4M3>(tw, tx, p, grid, stream, device);
-        case 128: return launch_t<128, E4M3>(tw, tx, p, grid, stream, device);
-        default: return launch_t<256, E4M3>(tw, tx, p, grid, stream, device);
+q4q_status launch_bn(const Plan& q, const Maps& maps, const MxParams& p, int64_t workers, cudaStream_t stream, int device) {
+    switch (q.bn) {
+        case 16: return launch_t<16, E4M3, 1>(maps, p, workers, stream, device);
+        case 32: return launch_t<32, E4M3, 1>(maps, p, workers, stream, device);
+        case 64: return launch_t<64, E4M3, 1>(maps, p, workers, stream, device);
+        case 128:
+            return q.cg == 1 ? launch_t<128, E4M3, 1>(maps, p, workers, stream, device)
+                             : launch_t<128, E4M3, 2>(maps, p, workers, stream, device);
+        default: return launch_t<256, E4M3, 2>(maps, p, workers, stream, device);
     }
+}
+
+// 32-bit words of scales: {a chunk, 128-column chunks, row tiles, matrices}, boxes of `chunks` chunks
+bool encode_scale_map(CUtensorMap* map, const void* base, int chunk_bytes, int64_t nkc, int64_t tiles, int64_t n_mats,
+                      int64_t mat_stride, int chunks) {
+    const cuuint64_t dims[4] = {(cuuint64_t)(chunk_bytes / 4), (cuuint64_t)nkc, (cuuint64_t)tiles, (cuuint64_t)n_mats};
+    const cuuint64_t strides[3] = {(cuuint64_t)chunk_bytes, (cuuint64_t)(nkc * chunk_bytes), (cuuint64_t)mat_stride};
+    const cuuint32_t box[4] = {(cuuint32_t)(chunk_bytes / 4), (cuuint32_t)chunks, 1, 1};
+    const cuuint32_t one[4] = {1, 1, 1, 1};
+    return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_INT32, mat_stride ? 4 : 3, const_cast<void*>(base), dims, strides, box, one,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 q4q_status run(const void* src0, int64_t ne00, int64_t ne01, int n_mats, const MxActs& acts, int64_t n_tokens, void* dst,
@@ -552,42 +637,46 @@ q4q_status run(const void* src0, int64_t ne00, int64_t ne01, int n_mats, const M
     q4q_status st = current_device_info(&info);
     if (st != Q4Q_OK) return st;
     if (info.cc_major != 10 || !get_encode()) return Q4Q_ERR_CUDA;
-    if (pick_bn(acts.n_rows, n_tokens, acts.first ? n_mats : 0) == MXMV_TOKENS)
-        return mxmv_run(src0, ne00, ne01, n_mats, acts, dst, dst_type, pdl, stream, info, dbg);
     const Plan q = make_plan(ne00, ne01, acts.n_rows, n_tokens, acts.first ? n_mats : 0, acts.acts, info.sm_count);
+    if (q.bn == MXMV_TOKENS) return mxmv_run(src0, ne00, ne01, n_mats, acts, dst, dst_type, pdl, stream, info, dbg);
     if (workspace_bytes < q.total) return Q4Q_ERR_WORKSPACE;
     if (!workspace) return Q4Q_ERR_NULL;
     if (!aligned(workspace, 256)) return Q4Q_ERR_ALIGN;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const bool e4m3 = acts.acts == Q4Q_ACTS_MXFP8;
     const int64_t code_bytes = mx_code_bytes(ne00, ne01), stride = code_bytes + mx_scale_bytes(ne00, ne01);
+    const uint8_t* w_scales = static_cast<const uint8_t*>(src0) + code_bytes;
+    const int stage_atoms = atoms_of(q.bn), ch = e4m3 ? 1 : 2;
+    const int64_t atoms = q.kp / (128 * ch), nkc = q.kp / 128;
 
-    CUtensorMap tw, tx;
-    const cuuint32_t one[3] = {1, 1, 1};
-    const int64_t atoms = q.kp / (e4m3 ? 128 : 256);
-    const int stage_atoms = atoms_of(q.bn, e4m3);
-    if (!mx_encode_weight_map(&tw, src0, ne00, ne01, n_mats, e4m3, stage_atoms)) return Q4Q_ERR_CUDA;
+    Maps maps{};
+    if (!mx_encode_weight_map(&maps.w, src0, ne00, ne01, n_mats, e4m3, stage_atoms)) return Q4Q_ERR_CUDA;
     {
         // {128 bytes, tokens, atoms}
         const cuuint64_t dims[3] = {128, (cuuint64_t)(q.max_groups * q.bn), (cuuint64_t)atoms};
         const cuuint64_t strides[2] = {(cuuint64_t)(e4m3 ? q.kp : q.kp / 2), 128};
-        const cuuint32_t box[3] = {128, (cuuint32_t)q.bn, (cuuint32_t)stage_atoms};
-        if (g_encode(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, ws + q.codes, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+        const cuuint32_t box[3] = {128, (cuuint32_t)(q.bn / q.cg), (cuuint32_t)stage_atoms};
+        const cuuint32_t one[3] = {1, 1, 1};
+        if (g_encode(&maps.x, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, ws + q.codes, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
                      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return Q4Q_ERR_CUDA;
     }
+    if (q.cg == 2 && (!encode_scale_map(&maps.sw, w_scales, MX_CHUNK, nkc, (ne01 + BM - 1) / BM, n_mats, stride, stage_atoms * ch) ||
+                      !encode_scale_map(&maps.sx, ws + q.scales, mx_chunk_bytes(q.bn), nkc, q.max_groups, 1, 0, stage_atoms * ch)))
+        return Q4Q_ERR_CUDA;
     MxParams p;
     p.M = (int)ne01;
     p.n_mats = n_mats;
     p.n_rows = acts.n_rows;
     p.max_groups = q.max_groups;
     p.wait_first = pdl;
-    p.mtiles = (int)((ne01 + BM - 1) / BM);
-    const int ks = (e4m3 ? 128 : 256) * stage_atoms;
+    p.may_split = q.split;
+    p.mtiles = (int)((ne01 + BM * q.cg - 1) / (BM * q.cg));
+    const int ks = 128 * ch * stage_atoms;
     p.kst = (int)((ne00 + ks - 1) / ks);
-    p.nkc = (int)(q.kp / 128);
+    p.nkc = (int)nkc;
     p.first = acts.first;
-    p.w_scales = static_cast<const uint8_t*>(src0) + code_bytes;
+    p.w_scales = w_scales;
     p.mat_stride = stride;
     p.x_scales = ws + q.scales;
     p.dst = dst;
@@ -600,10 +689,10 @@ q4q_status run(const void* src0, int64_t ne00, int64_t ne01, int n_mats, const M
     st = mx_encode_acts(acts, p.ctrl, CTRL_COUNT + q.n_counters, ws + q.codes, ws + q.scales, q.bn, q.max_groups, pdl, stream, info);
     if (st != Q4Q_OK) return st;
     // no more CTAs than there can be parts of the work
-    const int64_t stages = q.tiles_most * p.kst;
-    const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(info.sm_count, stages / MIN_SPLIT_STAGES));
-    return e4m3 ? launch_bn<true>(q.bn, tw, tx, p, grid, stream, info.device)
-                : launch_bn<false>(q.bn, tw, tx, p, grid, stream, info.device);
+    const int64_t tiles = q.max_groups * p.mtiles;
+    const int64_t most = q.split ? tiles * p.kst * stage_atoms / MIN_SPLIT_ATOMS : tiles;
+    const int64_t workers = std::max<int64_t>(1, std::min<int64_t>(info.sm_count / q.cg, most));
+    return e4m3 ? launch_bn<true>(q, maps, p, workers, stream, info.device) : launch_bn<false>(q, maps, p, workers, stream, info.device);
 }
 
 q4q_status check_product(int64_t ne00, int64_t ne01, int src1_type, int64_t ne10, int64_t ne11, int acts, int dst_type, unsigned int flags) {
