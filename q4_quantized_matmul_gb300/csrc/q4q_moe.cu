@@ -34,6 +34,7 @@ namespace {
 constexpr int SORT_THREADS = 1024;
 constexpr int SORT_WARPS = SORT_THREADS / 32;
 constexpr int SORT_MAX_CLUSTER = 8;
+constexpr int KEYS = 4;
 
 // histograms [warps][bins], CTA totals [bins], places [bins], scan scratch
 __host__ __device__ constexpr size_t sort_smem(int warps, int bins) { return ((size_t)(warps + 2) * bins + 40) * 4; }
@@ -60,12 +61,20 @@ sort_kernel(const int32_t* __restrict__ ids, int n, int n_experts, int32_t* __re
         const int id = s < s1 ? __ldg(ids + s) : -1;
         return s < s1 ? ((unsigned)id < (unsigned)n_experts ? id : n_experts) : -1;
     };
-    for (int64_t s = s0; s < s1; s += 32) {
-        const int k = key(s + lane);
+    // a run's first KEYS steps stay in registers for the second walk
+    int keys[KEYS];
+    const int steps = (int)((max(s1 - s0, (int64_t)0) + 31) / 32);
+#pragma unroll
+    for (int i = 0; i < KEYS; ++i) keys[i] = key(s0 + 32 * i + lane);
+    auto count = [&](int k) {
         const uint32_t peers = __match_any_sync(0xffffffffu, k);
         if (k >= 0 && (__ffs(peers) - 1) == lane) mine[k] += __popc(peers);
         __syncwarp();
-    }
+    };
+#pragma unroll
+    for (int i = 0; i < KEYS; ++i)
+        if (i < steps) count(keys[i]);
+    for (int i = KEYS; i < steps; ++i) count(key(s0 + 32 * (int64_t)i + lane));
     __syncthreads();
     for (int e = tid; e < bins; e += blockDim.x) {
         int sum = 0;
@@ -120,19 +129,23 @@ sort_kernel(const int32_t* __restrict__ ids, int n, int n_experts, int32_t* __re
         before += a;
     }
     __syncthreads();
-    for (int64_t s = s0; s < s1; s += 32) {
-        const int k = key(s + lane);
+    auto put = [&](int i, int k) {
+        const int64_t s = s0 + 32 * (int64_t)i + lane;
         const uint32_t peers = __match_any_sync(0xffffffffu, k);
         int at = 0;
         if (k >= 0) at = mine[k] + place[k] + __popc(peers & ((1u << lane) - 1u));
         __syncwarp();
         if (k >= 0) {
             if ((__ffs(peers) - 1) == lane) mine[k] += __popc(peers);
-            slot[at] = (int32_t)(s + lane);
-            row[s + lane] = at;
+            slot[at] = (int32_t)s;
+            row[s] = at;
         }
         __syncwarp();
-    }
+    };
+#pragma unroll
+    for (int i = 0; i < KEYS; ++i)
+        if (i < steps) put(i, keys[i]);
+    for (int i = KEYS; i < steps; ++i) put(i, key(s0 + 32 * (int64_t)i + lane));
     // no CTA leaves while another may still read its totals
     if (ctas > 1) {
         cluster_arrive();
@@ -211,13 +224,25 @@ combine_kernel(const T* __restrict__ rows, const float* __restrict__ w, T* __res
         float acc[V];
 #pragma unroll
         for (int k = 0; k < V; ++k) acc[k] = 0.0f;
-        for (int j = 0; j < g.top_k; ++j) {
-            const int64_t r = __ldg(g.row + t * g.top_k + j);
-            if (r < 0 || r >= kept) continue;
-            const float f = w ? __ldg(w + t * g.top_k + j) : 1.0f;
-            const Vec<T, V> v = ldv<T, V>(rows + r * g.ne0 + c);
+        // four choices' loads in flight (from row 0 where a choice is not used), added in order
+        for (int j0 = 0; j0 < g.top_k; j0 += 4) {
+            int64_t r[4];
+            float f[4];
+            Vec<T, V> v[4];
 #pragma unroll
-            for (int k = 0; k < V; ++k) acc[k] = __fmaf_rn(f, mx_to_f32(v.v[k]), acc[k]);
+            for (int j = 0; j < 4; ++j) {
+                r[j] = j0 + j < g.top_k ? (int64_t)__ldg(g.row + t * g.top_k + j0 + j) : -1;
+                if (r[j] >= kept) r[j] = -1;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                f[j] = w && r[j] >= 0 ? __ldg(w + t * g.top_k + j0 + j) : 1.0f;
+                v[j] = ldv<T, V>(rows + max(r[j], (int64_t)0) * g.ne0 + c);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int k = 0; k < V; ++k) acc[k] = r[j] >= 0 ? __fmaf_rn(f[j], mx_to_f32(v[j].v[k]), acc[k]) : acc[k];
         }
         Vec<T, V> o;
 #pragma unroll
@@ -337,11 +362,11 @@ extern "C" q4q_status q4q_moe_sort(const int32_t* ids, int64_t n_tokens, int top
     if (info.device < 0 || info.device >= 64) return Q4Q_ERR_CUDA;
     cudaStream_t stream = (cudaStream_t)stream_;
     const int64_t n = n_tokens * top_k;
-    // a warp takes at least 32 slots; more CTAs once every warp of one has that
+    // a warp takes at least 32 slots; more CTAs once every warp of one has KEYS times that
     const int64_t want = std::max<int64_t>(1, (n + 31) / 32);
     const int warps = (int)std::min<int64_t>(want, SORT_WARPS);
     int ctas = 1;
-    while (ctas < SORT_MAX_CLUSTER && (int64_t)ctas * SORT_WARPS < want) ctas *= 2;
+    while (ctas < SORT_MAX_CLUSTER && (int64_t)ctas * SORT_WARPS * KEYS < want) ctas *= 2;
     const int64_t per = (n + (int64_t)ctas * warps - 1) / ((int64_t)ctas * warps);
     const int per_warp = (int)mx_up(std::max<int64_t>(per, 1), 32);
     const size_t smem = sort_smem(warps, n_experts + 1);

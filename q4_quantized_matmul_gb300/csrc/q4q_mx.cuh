@@ -20,7 +20,6 @@
 
 #include <cuda_bf16.h>
 #include <cuda_fp4.h>
-#include <cuda_fp8.h>
 
 #include "q4q_common.cuh"
 
@@ -52,26 +51,8 @@ __device__ __forceinline__ __half mx_from_f32<__half>(float v) { return __float2
 template <>
 __device__ __forceinline__ __nv_bfloat16 mx_from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// N values of T at `p`, one to three 16-byte loads where `vec` says that p allows them
-// (16-byte aligned); N * sizeof(T) is a multiple of 16.
-template <typename T, int N>
-__device__ __forceinline__ void mx_load(const T* __restrict__ p, bool vec, float (&v)[N]) {
-    constexpr int PER = 16 / (int)sizeof(T);
-    if (vec) {
-#pragma unroll
-        for (int i = 0; i < N / PER; ++i) {
-            const uint4 u = __ldg(reinterpret_cast<const uint4*>(p) + i);
-            const T* t = reinterpret_cast<const T*>(&u);
-#pragma unroll
-            for (int k = 0; k < PER; ++k) v[i * PER + k] = mx_to_f32(t[k]);
-        }
-    } else {
-#pragma unroll
-        for (int k = 0; k < N; ++k) v[k] = mx_to_f32(p[k]);
-    }
-}
-
-// 8 values of T as they were loaded, looked at only when they are needed; `live`: not zeros.
+// 8 values of T as they were loaded, looked at only when they are needed; `live`: not zeros
+// (the same in the four lanes of a block).
 template <typename T>
 struct MxRaw {
     uint4 bits[sizeof(T) / 2];
@@ -87,62 +68,72 @@ struct MxRaw {
     }
     __device__ __forceinline__ void values(float (&v)[8]) const {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = live ? mx_to_f32(reinterpret_cast<const T*>(bits)[k]) : 0.0f;
+        for (int k = 0; k < 8; ++k) v[k] = mx_to_f32(reinterpret_cast<const T*>(bits)[k]);
     }
 };
+
+// the largest magnitude of three, NaN if one is
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+    float m;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+    return m;
+}
 
 // Encode 8 values a lane, four neighbouring lanes a block (the whole converged warp calls
 // it): the codes in w (8 bytes for E4M3, 4 for E2M1), the block's scale byte returned.
 template <bool E4M3>
-__device__ __forceinline__ uint32_t mx_encode8(const float (&v)[8], uint32_t (&w)[2]) {
+__device__ __forceinline__ uint32_t mx_encode8(const float (&v)[8], bool live, uint32_t (&w)[2]) {
     constexpr int EMAX = E4M3 ? 8 : 2;
-    // magnitudes compare as integers; an infinity or NaN has exponent field 255
-    uint32_t mag = 0;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) mag = max(mag, __float_as_uint(v[k]) & 0x7fffffffu);
-    mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 1));
-    mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 2));
-    const int field = (int)(mag >> 23);
-    const bool bad = field == 255;
-    const int sf = bad ? 255 : max(field - EMAX, 0);               // e + 127; 0 also where amax is 0 or subnormal
+    float m = max3_abs(v[0], v[1], v[2]);
+    m = max3_abs(m, v[3], v[4]);
+    m = max3_abs(m, v[5], v[6]);
+    m = max3_abs(m, v[7], __shfl_xor_sync(0xffffffffu, max3_abs(m, v[7], v[7]), 1));
+    m = max3_abs(m, m, __shfl_xor_sync(0xffffffffu, m, 2));
+    const int field = (int)(__float_as_uint(m) >> 23);             // 255: the block holds an infinity or a NaN
+    const bool use = live && field != 255;
+    int sf = max(field - EMAX, 0);                                 // e + 127; 0 also where amax is 0 or subnormal
     // 2^-e = 2^(127 - sf): 127 - sf is -126 .. 127 for finite blocks
-    const float inv = bad ? 0.0f : __uint_as_float((uint32_t)(254 - sf) << 23);
+    const float inv = __uint_as_float((uint32_t)(254 - sf) << 23);
     float t[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) t[k] = bad ? 0.0f : __fmul_rn(v[k], inv);
+    for (int k = 0; k < 8; ++k) t[k] = __fmul_rn(v[k], inv);
     if constexpr (E4M3) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(t[4 * h], t[4 * h + 1]), __NV_SATFINITE, __NV_E4M3);
-            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(t[4 * h + 2], t[4 * h + 3]), __NV_SATFINITE, __NV_E4M3);
-            w[h] = lo | (hi << 16);
-        }
+        for (int h = 0; h < 2; ++h)
+            asm("{\n\t.reg .b16 a, b;\n\t"
+                "cvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 b, %4, %3;\n\t"
+                "mov.b32 %0, {a, b};\n\t}"
+                : "=r"(w[h]) : "f"(t[4 * h]), "f"(t[4 * h + 1]), "f"(t[4 * h + 2]), "f"(t[4 * h + 3]));
+        w[0] = use ? w[0] : 0u;
+        w[1] = use ? w[1] : 0u;
     } else {
-        w[0] = w[1] = 0;
-#pragma unroll
-        for (int h = 0; h < 4; ++h)
-            w[0] |= (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(t[2 * h], t[2 * h + 1]), __NV_E2M1, cudaRoundNearest) << (8 * h);
+        asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+            "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+            "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+            "mov.b32 %0, {a, b, c, d};\n\t}"
+            : "=r"(w[0]) : "f"(t[0]), "f"(t[1]), "f"(t[2]), "f"(t[3]), "f"(t[4]), "f"(t[5]), "f"(t[6]), "f"(t[7]));
+        w[0] = use ? w[0] : 0u;
+        w[1] = 0u;
     }
+    sf = use ? sf : live ? 255 : 0;
     return (uint32_t)sf;
 }
 
 // Encode 256 consecutive columns of one row: lane l of the (converged) warp holds columns
-// 8l .. 8l+7 in v.  Writes the codes at `codes` (the segment's first byte; null: none) and
-// the segment's 8 scale bytes, 4 in each of the words at `scales` and, in the next chunk,
-// `scales + chunk`.
-template <bool E4M3>
-__device__ __forceinline__ void mx_encode_segment(const float (&v)[8], uint8_t* codes, uint8_t* scales, int chunk) {
-    const int lane = threadIdx.x & 31;
+// 8l .. 8l+7.  Writes the lane's codes at `codes` and, from lanes 0 and 16, the four scale
+// bytes of each half of the segment at `scales`.
+template <bool E4M3, typename T>
+__device__ __forceinline__ void mx_encode_segment(const MxRaw<T>& raw, uint8_t* codes, uint8_t* scales) {
+    float v[8];
+    raw.values(v);
     uint32_t w[2];
-    uint32_t word = mx_encode8<E4M3>(v, w);
-    if (codes) {
-        if constexpr (E4M3) reinterpret_cast<uint2*>(codes)[lane] = make_uint2(w[0], w[1]);
-        else reinterpret_cast<uint32_t*>(codes)[lane] = w[0];
-    }
-    // lanes 0 and 16 collect the scale bytes of their four blocks (lanes l, l+4, l+8, l+12)
+    uint32_t word = mx_encode8<E4M3>(v, raw.live, w);
+    if constexpr (E4M3) *reinterpret_cast<uint2*>(codes) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint32_t*>(codes) = w[0];
+    // the bytes of lanes l, l+4, l+8, l+12
     word |= __shfl_down_sync(0xffffffffu, word, 4) << 8;
     word |= __shfl_down_sync(0xffffffffu, word, 8) << 16;
-    if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(scales + (lane >> 4) * chunk) = word;
+    if ((threadIdx.x & 15) == 0) *reinterpret_cast<uint32_t*>(scales) = word;
 }
 
 // dst[i] = v, rounded to the type
@@ -152,11 +143,12 @@ __device__ __forceinline__ void mx_store(void* dst, int type, int64_t i, float v
     else static_cast<__nv_bfloat16*>(dst)[i] = __float2bfloat16_rn(v);
 }
 
-// Offset of the scale word of row r for the 128 columns kc, in tiles of bn rows.
-__device__ __forceinline__ int64_t mx_scale_offset(int64_t r, int bn, int nkc, int kc) {
-    const int64_t tile = r / bn;
-    const int in = (int)(r - tile * bn);
-    return (tile * nkc + kc) * mx_chunk_bytes(bn) + (in >> 7) * MX_CHUNK + (in & 31) * 16 + ((in >> 5) & 3) * 4;
+// Offset of the scale word of row r for the 128 columns kc, in tiles of 2^bn_log rows whose
+// chunks take `chunk` bytes.
+__device__ __forceinline__ int64_t mx_scale_offset(int64_t r, int bn_log, int chunk, int nkc, int kc) {
+    const int64_t tile = r >> bn_log;
+    const int in = (int)r & ((1 << bn_log) - 1);
+    return (tile * nkc + kc) * chunk + (in >> 7) * MX_CHUNK + (in & 31) * 16 + ((in >> 5) & 3) * 4;
 }
 
 // The experts' segments: rows start[e] .. start[e + 1] - 1 of the sorted order, at row

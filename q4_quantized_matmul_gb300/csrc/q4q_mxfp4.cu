@@ -2,8 +2,10 @@
 // (q4q_get_rows_mxfp4) and the activation encoder of the MXFP4 products.
 //
 // All three are bound by HBM (the encoder reads 4 bytes and writes 0.53 per fp32 value,
-// the gather the reverse).  A warp takes 256 consecutive columns of one row: 8 values a
-// lane in one or two 16-byte loads, four lanes a block, one 128-byte line of codes.
+// the gather the reverse).  A unit is 256 consecutive columns of one row: in the encoders 8
+// values a lane in one or two 16-byte loads, four lanes a block, one 128-byte line of codes;
+// in the gather 4 values a lane twice, so that each of a warp's 16-byte stores is one piece
+// of 512 bytes.  A warp takes UNITS units at a time, their loads in flight together.
 #include <algorithm>
 
 #include "q4q_internal.h"
@@ -17,32 +19,76 @@ __device__ unsigned int g_mxfp4_status = 0;
 
 constexpr int THREADS = 256;
 
-// rows_pad = rows rounded up to 128: the scale bytes past the matrix are written as 0
-template <typename T>
-__global__ void __launch_bounds__(THREADS)
-encode_kernel(const T* __restrict__ src, bool vec, uint8_t* __restrict__ dst, int K, int64_t rows, int64_t rows_pad,
-              int64_t nmats, int64_t mat_stride, int64_t code_bytes) {
-    const int lane = threadIdx.x & 31;
-    const int segs = (K + MX_KP - 1) / MX_KP, nkc = 2 * segs;
-    const int64_t per_mat = rows_pad * segs, total = per_mat * nmats;
-    for (int64_t u = ((int64_t)blockIdx.x * THREADS + threadIdx.x) >> 5; u < total;
-         u += (int64_t)gridDim.x * (THREADS / 32)) {
-        const int64_t mat = u / per_mat, in = u - mat * per_mat;
-        const int64_t r = in / segs;
-        const int seg = (int)(in - r * segs);
-        uint8_t* out = dst + mat * mat_stride;
-        float v[8];
-        const int col = seg * MX_KP + lane * 8;
-        if (r < rows && col < K) {
-            mx_load<T, 8>(src + (mat * rows + r) * K + col, vec, v);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = 0.0f;
+// Position of a warp in a line of units: row u / segs and segment u % segs, advanced without
+// a division.
+struct Unit {
+    int64_t row;
+    int seg;
+    __device__ __forceinline__ Unit(int64_t u, int segs, bool small) {
+        row = small ? (int64_t)((uint32_t)u / (uint32_t)segs) : u / segs;
+        seg = (int)(u - row * segs);
+    }
+    __device__ __forceinline__ void next(int segs) {
+        if (++seg == segs) {
+            seg = 0;
+            ++row;
         }
-        // the code plane ends on a 256-byte boundary: after an odd number of segments, one more of zeros
-        const bool codes = r < rows || (r == rows && seg == 0 && (rows * segs) % 2 != 0);
-        mx_encode_segment<false>(v, codes ? out + (r * segs + seg) * (MX_KP / 2) : nullptr,
-                                 out + code_bytes + mx_scale_offset(r, 128, nkc, 2 * seg), MX_CHUNK);
+    }
+};
+
+// Units of an encoder's warp at a time: as many as keep its raw values in 16 registers, so that
+// four blocks share an SM.
+template <typename T>
+constexpr int at_a_time = sizeof(T) == 4 ? 2 : 4;
+
+// One matrix for each blockIdx.y (and every gridDim.y-th after it).
+template <typename T, int UNITS>
+__global__ void __launch_bounds__(THREADS, 4)
+encode_kernel(const T* __restrict__ src, bool vec, uint8_t* __restrict__ dst, int K, int64_t rows, int64_t nmats,
+              int64_t mat_stride, int64_t code_bytes) {
+    const int lane = threadIdx.x & 31;
+    const int segs = (K + MX_KP - 1) / MX_KP, nkc = 2 * segs, last = K - (segs - 1) * MX_KP;
+    const int64_t total = rows * segs;
+    const bool small = total < (1ll << 31);
+    for (int64_t mat = blockIdx.y; mat < nmats; mat += gridDim.y) {
+        const T* in = src + mat * rows * K;
+        uint8_t* out = dst + mat * mat_stride;
+        uint8_t* scales = out + code_bytes + (lane >> 4) * MX_CHUNK;
+        for (int64_t u0 = (((int64_t)blockIdx.x * THREADS + threadIdx.x) >> 5) * UNITS; u0 < total;
+             u0 += (int64_t)gridDim.x * (THREADS / 32) * UNITS) {
+            const Unit first(u0, segs, small);
+            const int n = (int)min((int64_t)UNITS, total - u0);
+            MxRaw<T> v[UNITS];
+            const T* p = in + first.row * K + first.seg * MX_KP + lane * 8;
+            int seg = first.seg;
+#pragma unroll
+            for (int k = 0; k < UNITS; ++k) {
+                v[k].live = k < n && (seg < segs - 1 || lane * 8 < last);
+                v[k].load(v[k].live ? p : in, vec);
+                if (++seg == segs) {
+                    seg = 0;
+                    p += last;
+                } else {
+                    p += MX_KP;
+                }
+            }
+            uint8_t* codes = out + u0 * (MX_KP / 2) + lane * 4;
+            Unit at = first;
+#pragma unroll
+            for (int k = 0; k < UNITS; ++k) {
+                if (k >= n) break;
+                mx_encode_segment<false>(v[k], codes + k * (MX_KP / 2), scales + mx_scale_offset(at.row, 7, MX_CHUNK, nkc, 2 * at.seg));
+                at.next(segs);
+            }
+        }
+        // what lies past the matrix: the code plane ends on a 256-byte boundary, the scales' last
+        // row group has 128 rows
+        if (blockIdx.x == 0) {
+            if (total % 2 != 0 && threadIdx.x < 32) reinterpret_cast<uint32_t*>(out + total * (MX_KP / 2))[lane] = 0u;
+            const int64_t pad = (mx_up(rows, 128) - rows) * nkc;
+            for (int64_t i = threadIdx.x; i < pad; i += THREADS)
+                *reinterpret_cast<uint32_t*>(out + code_bytes + mx_scale_offset(rows + i / nkc, 7, MX_CHUNK, nkc, (int)(i % nkc))) = 0u;
+        }
     }
 }
 
@@ -58,12 +104,12 @@ struct ActArgs {
     int64_t max_groups;
     const int32_t* first;      // null: dense
     const int32_t* slot;       // null: row i of src is row i
-    int n_experts, top_k, K, bn;
+    int n_experts, top_k, K, bn, bn_log;
     bool vec, pdl;
 };
 
-template <typename T, bool E4M3>
-__global__ void __launch_bounds__(THREADS) acts_kernel(const ActArgs a) {
+template <typename T, bool E4M3, int UNITS>
+__global__ void __launch_bounds__(THREADS, 4) acts_kernel(const ActArgs a) {
     extern __shared__ int seg_smem[];
     __shared__ int tmp[33];
     const int lane = threadIdx.x & 31;
@@ -74,83 +120,152 @@ __global__ void __launch_bounds__(THREADS) acts_kernel(const ActArgs a) {
     int* start = seg_smem;
     int* base = seg_smem + a.n_experts + 1;
     if (a.first) mx_segments(a.first, a.n_experts, a.n_rows, a.bn, a.max_groups, start, base, tmp);
-    const int segs = (a.K + MX_KP - 1) / MX_KP, nkc = 2 * segs;
-    constexpr int SEG_BYTES = E4M3 ? MX_KP : MX_KP / 2;
+    const int segs = (a.K + MX_KP - 1) / MX_KP, nkc = 2 * segs, chunk = mx_chunk_bytes(a.bn), last = a.K - (segs - 1) * MX_KP;
+    constexpr int LANE_BYTES = E4M3 ? 8 : 4;
+    const T* src = static_cast<const T*>(a.src);
+    uint8_t* scales = a.scales + (lane >> 4) * chunk;
     const int64_t total = a.n_rows * segs;
-    for (int64_t u = ((int64_t)blockIdx.x * THREADS + threadIdx.x) >> 5; u < total;
-         u += (int64_t)gridDim.x * (THREADS / 32)) {
-        const int64_t r = total < (1ll << 32) ? (int64_t)((uint32_t)u / (uint32_t)segs) : u / segs;
-        const int seg = (int)(u - r * segs);
-        int64_t from = r, to = r;
-        if (a.first) {
-            // the expert with start[e] <= r < start[e + 1]; empty experts share a start
-            if (r >= start[a.n_experts] || r < start[0]) continue;
-            const int e = mx_find(start, a.n_experts, (int)r);
-            to = (int64_t)base[e] * a.bn + (r - start[e]);
-            if (to >= (int64_t)base[e + 1] * a.bn) continue;
-            if (a.slot) from = (int64_t)__ldg(a.slot + r) / a.top_k;
-        }
-        float v[8];
-        const int col = seg * MX_KP + lane * 8;
-        if (from >= 0 && from < a.n_src && col < a.K) {
-            mx_load<T, 8>(static_cast<const T*>(a.src) + from * a.K + col, a.vec, v);
-        } else {
+    const bool small = total < (1ll << 31);
+    // where row r comes from (null: zeros) and where it goes (negative: nowhere)
+    auto place = [&](int64_t r, const T*& from, int64_t& to) {
+        from = src + r * a.K + lane * 8;
+        to = r;
+        if (!a.first) return;
+        to = -1;
+        // the expert with start[e] <= r < start[e + 1]; empty experts share a start
+        if (r >= start[a.n_experts] || r < start[0]) return;
+        const int e = mx_find(start, a.n_experts, (int)r);
+        const int64_t at = (int64_t)base[e] * a.bn + (r - start[e]);
+        if (at >= (int64_t)base[e + 1] * a.bn) return;
+        to = at;
+        const int64_t row = a.slot ? (int64_t)((uint32_t)__ldg(a.slot + r) / (uint32_t)a.top_k) : r;
+        from = row < a.n_src ? src + row * a.K + lane * 8 : nullptr;
+    };
+    for (int64_t u0 = (((int64_t)blockIdx.x * THREADS + threadIdx.x) >> 5) * UNITS; u0 < total;
+         u0 += (int64_t)gridDim.x * (THREADS / 32) * UNITS) {
+        const Unit first(u0, segs, small);
+        const int n = (int)min((int64_t)UNITS, total - u0);
+        MxRaw<T> v[UNITS];
+        int64_t to[UNITS];
+        const T* from = nullptr;
+        Unit at = first;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = 0.0f;
+        for (int k = 0; k < UNITS; ++k) {
+            to[k] = -1;
+            if (k < n) {
+                if (k == 0 || at.seg == 0) place(at.row, from, to[k]);
+                else to[k] = to[k - 1];
+            }
+            v[k].live = to[k] >= 0 && from && (at.seg < segs - 1 || lane * 8 < last);
+            v[k].load(v[k].live ? from + at.seg * MX_KP : src, a.vec);
+            at.next(segs);
         }
-        mx_encode_segment<E4M3>(v, a.codes + (to * segs + seg) * SEG_BYTES,
-                                a.scales + mx_scale_offset(to, a.bn, nkc, 2 * seg), mx_chunk_bytes(a.bn));
+        at = first;
+#pragma unroll
+        for (int k = 0; k < UNITS; ++k) {
+            if (to[k] >= 0)
+                mx_encode_segment<E4M3>(v[k], a.codes + ((to[k] * segs + at.seg) * 32 + lane) * LANE_BYTES,
+                                        scales + mx_scale_offset(to[k], a.bn_log, chunk, nkc, 2 * at.seg));
+            at.next(segs);
+        }
     }
 }
 
-// Row gather: 8 values a thread, two 16-byte streaming stores.
+template <int UNITS>
 __global__ void __launch_bounds__(THREADS)
 mx_get_rows_kernel(const uint8_t* __restrict__ table, int64_t code_bytes, int64_t nrows, int K,
                    const int32_t* __restrict__ ids, int64_t n, float* __restrict__ dst) {
-    const int per_row = K / 8, segs = (K + MX_KP - 1) / MX_KP, nkc = 2 * segs;
-    const int64_t total = n * per_row;
-    for (int64_t g = blockIdx.x * (int64_t)THREADS + threadIdx.x; g < total; g += (int64_t)gridDim.x * THREADS) {
-        const int64_t i = total < (1ll << 32) ? (int64_t)((uint32_t)g / (uint32_t)per_row) : g / per_row;
-        const int c = (int)(g - i * per_row);
-        const int64_t id = ids ? (int64_t)__ldg(ids + i) : i;
-        float v[8];
-        if (id < 0 || id >= nrows) {
+    const int lane = threadIdx.x & 31;
+    const int segs = (K + MX_KP - 1) / MX_KP, nkc = 2 * segs;
+    const int64_t total = n * segs;
+    const bool small = total < (1ll << 31);
+    for (int64_t u0 = (((int64_t)blockIdx.x * THREADS + threadIdx.x) >> 5) * UNITS; u0 < total;
+         u0 += (int64_t)gridDim.x * (THREADS / 32) * UNITS) {
+        const Unit first(u0, segs, small);
+        uint32_t code[UNITS][2], scale[UNITS][2];
+        bool known[UNITS];
+        Unit at = first;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = 0.0f;
-            if (c == 0) record_error(&g_mxfp4_status, Q4Q_ERR_ARG);
-        } else {
-            const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(table + id * (segs * (MX_KP / 2))) + c);
-            const int b = c >> 2;
-            const uint32_t sf = __ldg(table + code_bytes + mx_scale_offset(id, 128, nkc, b >> 2) + (b & 3));
-            // 2^(sf - 127); sf = 0 is the subnormal 2^-127, 255 the format's NaN
-            const float s = __uint_as_float(sf == 255 ? 0x7fffffffu : sf == 0 ? 0x00400000u : sf << 23);
+        for (int k = 0; k < UNITS; ++k, at.next(segs)) {
+            const bool in = u0 + k < total;
+            int64_t id = in ? (ids ? (int64_t)__ldg(ids + at.row) : at.row) : 0;
+            known[k] = id >= 0 && id < nrows;
+            if (!known[k]) {
+                id = 0;
+                if (lane == 0 && at.seg == 0 && in) record_error(&g_mxfp4_status, Q4Q_ERR_ARG);
+            }
+            // values 4 lane .. 4 lane + 3 of either half; the planes cover the padded columns
+            const uint16_t* c = reinterpret_cast<const uint16_t*>(table + (id * segs + at.seg) * (MX_KP / 2)) + lane;
+            const uint8_t* sc = table + code_bytes + mx_scale_offset(id, 7, MX_CHUNK, nkc, 2 * at.seg) + (lane >> 3);
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                const __half2_raw p = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)((w >> (8 * h)) & 0xffu), __NV_E2M1);
-                v[2 * h] = __fmul_rn(__half2float(__half(__half_raw{p.x})), s);
-                v[2 * h + 1] = __fmul_rn(__half2float(__half(__half_raw{p.y})), s);
+            for (int h = 0; h < 2; ++h) {
+                code[k][h] = nrows > 0 ? __ldg(c + 32 * h) : 0;
+                scale[k][h] = nrows > 0 ? __ldg(sc + h * MX_CHUNK) : 0;
             }
         }
-        float4* o = reinterpret_cast<float4*>(dst + i * (int64_t)K + c * 8);
-        __stcs(o, make_float4(v[0], v[1], v[2], v[3]));
-        __stcs(o + 1, make_float4(v[4], v[5], v[6], v[7]));
+        at = first;
+#pragma unroll
+        for (int k = 0; k < UNITS; ++k, at.next(segs)) {
+            if (u0 + k >= total) break;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int col = at.seg * MX_KP + h * 128 + lane * 4;
+                if (col >= K) continue;
+                // 2^(byte - 127); byte 0 is the subnormal 2^-127, 255 the format's NaN
+                const uint32_t sf = scale[k][h];
+                const float s = __uint_as_float(sf == 255 ? 0x7fffffffu : sf == 0 ? 0x00400000u : sf << 23);
+                float v[4];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const __half2_raw p = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)((code[k][h] >> (8 * j)) & 0xffu), __NV_E2M1);
+                    v[2 * j] = known[k] ? __fmul_rn(__half2float(__half(__half_raw{p.x})), s) : 0.0f;
+                    v[2 * j + 1] = known[k] ? __fmul_rn(__half2float(__half(__half_raw{p.y})), s) : 0.0f;
+                }
+                __stcs(reinterpret_cast<float4*>(dst + at.row * (int64_t)K + col), make_float4(v[0], v[1], v[2], v[3]));
+            }
+        }
     }
 }
 
-template <typename T>
-q4q_status launch_acts_t(const ActArgs& a, bool e4m3, int grid, size_t smem, cudaStream_t stream) {
+// Units a warp takes at a time: several where there are enough for all SMs' warps
+bool many(int64_t units, const DeviceInfo& info) { return units >= (int64_t)info.sm_count * 64 * 2; }
+
+int grid_of(int64_t units, int units_at_a_time, const DeviceInfo& info) {
+    const int64_t warps = (units + units_at_a_time - 1) / units_at_a_time;
+    return (int)std::max<int64_t>(1, std::min<int64_t>((warps + THREADS / 32 - 1) / (THREADS / 32), (int64_t)info.sm_count * 8));
+}
+
+constexpr int AT_A_TIME = 4;      // units of the row gather's warp
+
+template <typename T, bool E4M3>
+q4q_status launch_acts_t(const ActArgs& a, cudaStream_t stream, const DeviceInfo& info) {
+    constexpr int MANY = at_a_time<T>;
+    const int64_t units = a.n_rows * ((a.K + MX_KP - 1) / MX_KP);
+    const bool several = many(units, info);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
+    cfg.gridDim = dim3((unsigned)grid_of(units, several ? MANY : 1, info));
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = a.first ? 2 * (size_t)(a.n_experts + 1) * sizeof(int) : 0;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = a.pdl ? 1 : 0;
-    const cudaError_t e = e4m3 ? cudaLaunchKernelEx(&cfg, acts_kernel<T, true>, a) : cudaLaunchKernelEx(&cfg, acts_kernel<T, false>, a);
+    const cudaError_t e = several ? cudaLaunchKernelEx(&cfg, acts_kernel<T, E4M3, MANY>, a) : cudaLaunchKernelEx(&cfg, acts_kernel<T, E4M3, 1>, a);
     return e == cudaSuccess ? launch_status() : (cudaGetLastError(), Q4Q_ERR_CUDA);
+}
+
+template <typename T>
+void launch_encode(const void* src, uint8_t* out, int64_t ncols, int64_t nrows, int64_t nmats, cudaStream_t stream, const DeviceInfo& info) {
+    constexpr int MANY = at_a_time<T>;
+    const int64_t units = nrows * (mx_up(ncols, MX_KP) / MX_KP);
+    const int64_t codes = mx_code_bytes(ncols, nrows), stride = codes + mx_scale_bytes(ncols, nrows);
+    const T* in = static_cast<const T*>(src);
+    const bool vec = aligned(src, 16), several = many(units * nmats, info);
+    const dim3 grid((unsigned)grid_of(units, several ? MANY : 1, info), (unsigned)std::min<int64_t>(nmats, 65535));
+    if (several) encode_kernel<T, MANY><<<grid, THREADS, 0, stream>>>(in, vec, out, (int)ncols, nrows, nmats, stride, codes);
+    else encode_kernel<T, 1><<<grid, THREADS, 0, stream>>>(in, vec, out, (int)ncols, nrows, nmats, stride, codes);
 }
 
 }  // namespace
@@ -179,15 +294,15 @@ q4q_status mx_encode_acts(const MxActs& m, unsigned int* ctrl, int64_t n_ctrl, u
     a.top_k = m.top_k;
     a.K = (int)m.K;
     a.bn = bn;
+    a.bn_log = 0;
+    while ((1 << a.bn_log) < bn) ++a.bn_log;
     a.vec = aligned(m.src, 16);
     a.pdl = pdl;
-    const int64_t units = m.n_rows * ((m.K + MX_KP - 1) / MX_KP);
-    const int grid = (int)std::max<int64_t>(1, std::min<int64_t>((units + THREADS / 32 - 1) / (THREADS / 32), (int64_t)info.sm_count * 8));
-    const size_t smem = m.first ? 2 * (size_t)(m.n_experts + 1) * sizeof(int) : 0;
+    const bool e4m3 = m.acts == Q4Q_ACTS_MXFP8;
     switch (m.type) {
-        case Q4Q_TYPE_F32: return launch_acts_t<float>(a, m.acts == Q4Q_ACTS_MXFP8, grid, smem, stream);
-        case Q4Q_TYPE_F16: return launch_acts_t<__half>(a, m.acts == Q4Q_ACTS_MXFP8, grid, smem, stream);
-        default: return launch_acts_t<__nv_bfloat16>(a, m.acts == Q4Q_ACTS_MXFP8, grid, smem, stream);
+        case Q4Q_TYPE_F32: return e4m3 ? launch_acts_t<float, true>(a, stream, info) : launch_acts_t<float, false>(a, stream, info);
+        case Q4Q_TYPE_F16: return e4m3 ? launch_acts_t<__half, true>(a, stream, info) : launch_acts_t<__half, false>(a, stream, info);
+        default: return e4m3 ? launch_acts_t<__nv_bfloat16, true>(a, stream, info) : launch_acts_t<__nv_bfloat16, false>(a, stream, info);
     }
 }
 
@@ -215,21 +330,12 @@ extern "C" q4q_status q4q_quantize_mxfp4(const void* src, int src_type, void* ds
     if (!aligned(src, mx_type_bytes(src_type)) || !aligned(dst, 256)) return Q4Q_ERR_ALIGN;
     DeviceInfo info;
     if ((st = current_device_info(&info)) != Q4Q_OK) return st;
-    const int64_t rows_pad = mx_up(nrows, 128), units = rows_pad * (mx_up(ncols, MX_KP) / MX_KP) * nmats;
-    const int64_t codes = mx_code_bytes(ncols, nrows), stride = codes + mx_scale_bytes(ncols, nrows);
-    const int grid = (int)std::min<int64_t>((units + THREADS / 32 - 1) / (THREADS / 32), (int64_t)info.sm_count * 8);
-    const bool vec = aligned(src, 16);
     uint8_t* out = static_cast<uint8_t*>(dst);
     cudaStream_t stream = (cudaStream_t)stream_;
     switch (src_type) {
-        case Q4Q_TYPE_F32:
-            encode_kernel<float><<<grid, THREADS, 0, stream>>>(static_cast<const float*>(src), vec, out, (int)ncols, nrows, rows_pad, nmats, stride, codes);
-            break;
-        case Q4Q_TYPE_F16:
-            encode_kernel<__half><<<grid, THREADS, 0, stream>>>(static_cast<const __half*>(src), vec, out, (int)ncols, nrows, rows_pad, nmats, stride, codes);
-            break;
-        default:
-            encode_kernel<__nv_bfloat16><<<grid, THREADS, 0, stream>>>(static_cast<const __nv_bfloat16*>(src), vec, out, (int)ncols, nrows, rows_pad, nmats, stride, codes);
+        case Q4Q_TYPE_F32: launch_encode<float>(src, out, ncols, nrows, nmats, stream, info); break;
+        case Q4Q_TYPE_F16: launch_encode<__half>(src, out, ncols, nrows, nmats, stream, info); break;
+        default: launch_encode<__nv_bfloat16>(src, out, ncols, nrows, nmats, stream, info);
     }
     return launch_status();
 }
@@ -245,8 +351,11 @@ extern "C" q4q_status q4q_get_rows_mxfp4(const void* src0, int64_t ne00, int64_t
     if (!aligned(src0, 256) || !aligned(dst, 16) || (ids && !aligned(ids, 4))) return Q4Q_ERR_ALIGN;
     DeviceInfo info;
     if ((st = current_device_info(&info)) != Q4Q_OK) return st;
-    const int64_t items = n_ids * (ne00 / 8);
-    const int grid = (int)std::min<int64_t>((items + THREADS - 1) / THREADS, (int64_t)info.sm_count * 16);
-    mx_get_rows_kernel<<<grid, THREADS, 0, (cudaStream_t)stream>>>(static_cast<const uint8_t*>(src0), mx_code_bytes(ne00, ne01), ne01, (int)ne00, ids, n_ids, dst);
+    const int64_t units = n_ids * (mx_up(ne00, MX_KP) / MX_KP), codes = mx_code_bytes(ne00, ne01);
+    const uint8_t* table = static_cast<const uint8_t*>(src0);
+    if (many(units, info))
+        mx_get_rows_kernel<AT_A_TIME><<<grid_of(units, AT_A_TIME, info), THREADS, 0, (cudaStream_t)stream>>>(table, codes, ne01, (int)ne00, ids, n_ids, dst);
+    else
+        mx_get_rows_kernel<1><<<grid_of(units, 1, info), THREADS, 0, (cudaStream_t)stream>>>(table, codes, ne01, (int)ne00, ids, n_ids, dst);
     return launch_status();
 }

@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(THREADS, MAX_PER_SM) mxmv_kernel(const __grid_
                 float x[8];
                 uint32_t w[2];
                 v[h].values(x);
-                const uint32_t byte = mx_encode8<E4M3>(x, w);
+                const uint32_t byte = mx_encode8<E4M3>(x, v[h].live, w);
                 if (mine) {
                     uint8_t* b = smem + ST * C::A_BYTES + s * C::B_BYTES;
                     uint8_t* sf = smem + sfb_off + s * C::SFB_BYTES;
