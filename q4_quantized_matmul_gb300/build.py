@@ -2,7 +2,8 @@
 
 Each .cu file under csrc/ is compiled by nvcc in parallel, then linked into
 q4_quantized_matmul_gb300/_build/libq4q.so.  The CUDA runtime is linked
-statically so the library only needs the driver at run time.
+statically so the library only needs the driver at run time.  csrc/q4q_torch.cpp,
+the Python side of the MXFP4 calls, becomes _build/_q4q_torch.so beside it.
 """
 from __future__ import annotations
 
@@ -11,11 +12,14 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libq4q.so")
+EXT_SRC = os.path.join(CSRC, "q4q_torch.cpp")
+EXT = os.path.join(OUT_DIR, "_q4q_torch.so")
 ROOT = os.path.dirname(HERE)
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -39,11 +43,40 @@ def _deps():
         [os.path.join(ROOT, "include", "q4q.h")]
 
 
+def _newer(target: str, sources) -> bool:
+    return os.path.exists(target) and all(os.path.getmtime(p) <= os.path.getmtime(target) for p in sources)
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
-        return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    return _newer(LIB, _deps()) and _newer(EXT, [EXT_SRC, os.path.join(ROOT, "include", "q4q.h")])
+
+
+def _run(cmd, what: str):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("%s failed:\n%s\n%s" % (what, r.stdout, r.stderr))
+
+
+def _compile_ext() -> str:
+    """q4q_torch.cpp against this interpreter's torch; the object file."""
+    import torch
+    from torch.utils import cpp_extension
+    includes = cpp_extension.include_paths() + [sysconfig.get_paths()["include"],
+                                                os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")]
+    obj = os.path.join(OUT_DIR, "q4q_torch.o")
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+          "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI), "-I" + os.path.join(ROOT, "include"),
+          *[a for i in includes for a in ("-isystem", i)], "-c", EXT_SRC, "-o", obj], "g++ for " + EXT_SRC)
+    return obj
+
+
+def _link_ext(obj: str):
+    from torch.utils import cpp_extension
+    lib = cpp_extension.library_paths()[0]
+    tmp = EXT + ".tmp.%d" % os.getpid()
+    _run(["g++", "-shared", "-o", tmp, obj, "-L" + OUT_DIR, "-lq4q", "-Wl,-rpath,$ORIGIN", "-L" + lib, "-Wl,-rpath," + lib,
+          "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10_cuda", "-lc10"], "link of " + EXT)
+    os.replace(tmp, EXT)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
@@ -64,13 +97,16 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
+        ext = ex.submit(_compile_ext)
         objs = list(ex.map(compile_one, _sources()))
+        ext_obj = ext.result()
     tmp = LIB + ".tmp.%d" % os.getpid()
     cmd = [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("link failed:\n%s\n%s" % (r.stdout, r.stderr))
     os.replace(tmp, LIB)
+    _link_ext(ext_obj)
     return LIB
 
 
