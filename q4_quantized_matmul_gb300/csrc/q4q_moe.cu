@@ -17,7 +17,7 @@
 // The sort is a counting sort in one launch of one cluster of up to 8 CTAs: every warp
 // counts a contiguous run of slots into its own histogram, prefix sums over warps, CTAs
 // (distributed shared memory) and experts turn the counts into places, and the warp walks
-// its run again.  match.any gives equal ids within a warp their order.  The row movers are
+// its run again; votes on the ids' bits give equal ids within a warp their order.  The row movers are
 // bound by HBM and move 16 bytes a thread.
 #include <algorithm>
 #include <atomic>
@@ -36,17 +36,29 @@ constexpr int SORT_WARPS = SORT_THREADS / 32;
 constexpr int SORT_MAX_CLUSTER = 8;
 constexpr int KEYS = 4;
 
-// histograms [warps][bins], CTA totals [bins], places [bins], scan scratch
-__host__ __device__ constexpr size_t sort_smem(int warps, int bins) { return ((size_t)(warps + 2) * bins + 40) * 4; }
+// histograms [warps][bins], CTA totals, cluster totals and places [bins], scan scratch
+__host__ __device__ constexpr size_t sort_smem(int warps, int bins) { return ((size_t)(warps + 3) * bins + 40) * 4; }
+
+// The lanes with this lane's k (its low `bits` bits, k >= 0); one vote a bit, far quicker than
+// match.any with 32 warps of an SM at it.
+__device__ __forceinline__ uint32_t same_key(int k, int bits) {
+    uint32_t peers = __ballot_sync(0xffffffffu, k >= 0);
+    for (int b = 0; b < bits; ++b) {
+        const uint32_t ones = __ballot_sync(0xffffffffu, (k >> b) & 1);
+        peers &= (k >> b) & 1 ? ones : ~ones;
+    }
+    return peers;
+}
 
 __global__ void __launch_bounds__(SORT_THREADS)
 sort_kernel(const int32_t* __restrict__ ids, int n, int n_experts, int32_t* __restrict__ first,
             int32_t* __restrict__ slot, int32_t* __restrict__ row, int per_warp) {
     extern __shared__ int sm[];
-    const int bins = n_experts + 1, warps = blockDim.x >> 5;
+    const int bins = n_experts + 1, warps = blockDim.x >> 5, bits = 32 - __clz(n_experts);
     int* hist = sm;
     int* total = hist + warps * bins;
-    int* place = total + bins;
+    int* sums = total + bins;
+    int* place = sums + bins;
     int* scan = place + bins;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint32_t rank, ctas;
@@ -65,9 +77,9 @@ sort_kernel(const int32_t* __restrict__ ids, int n, int n_experts, int32_t* __re
     int keys[KEYS];
     const int steps = (int)((max(s1 - s0, (int64_t)0) + 31) / 32);
 #pragma unroll
-    for (int i = 0; i < KEYS; ++i) keys[i] = key(s0 + 32 * i + lane);
+    for (int i = 0; i < KEYS; ++i) keys[i] = i < steps ? key(s0 + 32 * i + lane) : -1;
     auto count = [&](int k) {
-        const uint32_t peers = __match_any_sync(0xffffffffu, k);
+        const uint32_t peers = same_key(k, bits);
         if (k >= 0 && (__ffs(peers) - 1) == lane) mine[k] += __popc(peers);
         __syncwarp();
     };
@@ -76,34 +88,54 @@ sort_kernel(const int32_t* __restrict__ ids, int n, int n_experts, int32_t* __re
         if (i < steps) count(keys[i]);
     for (int i = KEYS; i < steps; ++i) count(key(s0 + 32 * (int64_t)i + lane));
     __syncthreads();
-    for (int e = tid; e < bins; e += blockDim.x) {
-        int sum = 0;
-        for (int w = 0; w < warps; ++w) {
-            const int c = hist[w * bins + e];
-            hist[w * bins + e] = sum;
-            sum += c;
+    // what the CTA's warps before each one counted, and all of them: a thread a bin where there
+    // are few warps, else a warp a bin
+    if (warps <= 4) {
+        for (int e = tid; e < bins; e += blockDim.x) {
+            int sum = 0;
+            for (int w = 0; w < warps; ++w) {
+                const int c = hist[w * bins + e];
+                hist[w * bins + e] = sum;
+                sum += c;
+            }
+            total[e] = sum;
         }
-        total[e] = sum;
+    } else for (int e = warp; e < bins; e += warps) {
+        const int c = lane < warps ? hist[lane * bins + e] : 0;
+        int sum = c;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, sum, d);
+            if (lane >= d) sum += o;
+        }
+        if (lane < warps) hist[lane * bins + e] = sum - c;
+        if (lane == 31) total[e] = sum;
     }
     __syncthreads();
     if (ctas > 1) {
         cluster_arrive();
         cluster_wait();
     }
-    // rows of bin e in the CTAs before this one, and in all of them
+    // rows of bin e in the CTAs before this one, and in all of them: the other CTAs' totals in
+    // flight together
     int all = 0, before = 0;
-    const int per = (bins + (int)blockDim.x - 1) / (int)blockDim.x;      // 1 or 2
+    const int per = (bins + (int)blockDim.x - 1) / (int)blockDim.x;
     const int e0 = tid * per, e1 = min(e0 + per, bins);
     for (int e = e0; e < e1; ++e) {
+        int v[SORT_MAX_CLUSTER];
+#pragma unroll
+        for (int c = 0; c < SORT_MAX_CLUSTER; ++c) {
+            v[c] = 0;
+            if (c < (int)ctas) asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v[c]) : "r"(mapa_shared(smem_u32(total + e), c)) : "memory");
+        }
         int b = 0, a = 0;
-        for (uint32_t c = 0; c < ctas; ++c) {
-            int v;
-            if (c == rank) v = total[e];
-            else asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(mapa_shared(smem_u32(total + e), c)) : "memory");
-            if (c < rank) b += v;
-            a += v;
+#pragma unroll
+        for (int c = 0; c < SORT_MAX_CLUSTER; ++c) {
+            if (c < (int)rank) b += v[c];
+            a += v[c];
         }
         place[e] = b;
+        sums[e] = a;
         all += a;
     }
     int inc = all;
@@ -115,23 +147,17 @@ sort_kernel(const int32_t* __restrict__ ids, int n, int n_experts, int32_t* __re
     if (lane == 31) scan[warp] = inc;
     __syncthreads();
     before = inc - all;
-    for (int w = 0; w < warp; ++w) before += scan[w];
+    if (e0 < bins)
+        for (int w = 0; w < warp; ++w) before += scan[w];
     for (int e = e0; e < e1; ++e) {
         if (rank == 0) first[e] = before;
-        int a = 0;
-        for (uint32_t c = 0; c < ctas; ++c) {
-            int v;
-            if (c == rank) v = total[e];
-            else asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(mapa_shared(smem_u32(total + e), c)) : "memory");
-            a += v;
-        }
         place[e] += before;
-        before += a;
+        before += sums[e];
     }
     __syncthreads();
     auto put = [&](int i, int k) {
         const int64_t s = s0 + 32 * (int64_t)i + lane;
-        const uint32_t peers = __match_any_sync(0xffffffffu, k);
+        const uint32_t peers = same_key(k, bits);
         int at = 0;
         if (k >= 0) at = mine[k] + place[k] + __popc(peers & ((1u << lane) - 1u));
         __syncwarp();
@@ -224,25 +250,13 @@ combine_kernel(const T* __restrict__ rows, const float* __restrict__ w, T* __res
         float acc[V];
 #pragma unroll
         for (int k = 0; k < V; ++k) acc[k] = 0.0f;
-        // four choices' loads in flight (from row 0 where a choice is not used), added in order
-        for (int j0 = 0; j0 < g.top_k; j0 += 4) {
-            int64_t r[4];
-            float f[4];
-            Vec<T, V> v[4];
+        for (int j = 0; j < g.top_k; ++j) {
+            const int64_t r = __ldg(g.row + t * g.top_k + j);
+            if (r < 0 || r >= kept) continue;
+            const float f = w ? __ldg(w + t * g.top_k + j) : 1.0f;
+            const Vec<T, V> v = ldv<T, V>(rows + r * g.ne0 + c);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                r[j] = j0 + j < g.top_k ? (int64_t)__ldg(g.row + t * g.top_k + j0 + j) : -1;
-                if (r[j] >= kept) r[j] = -1;
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                f[j] = w && r[j] >= 0 ? __ldg(w + t * g.top_k + j0 + j) : 1.0f;
-                v[j] = ldv<T, V>(rows + max(r[j], (int64_t)0) * g.ne0 + c);
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int k = 0; k < V; ++k) acc[k] = r[j] >= 0 ? __fmaf_rn(f[j], mx_to_f32(v[j].v[k]), acc[k]) : acc[k];
+            for (int k = 0; k < V; ++k) acc[k] = __fmaf_rn(f, mx_to_f32(v.v[k]), acc[k]);
         }
         Vec<T, V> o;
 #pragma unroll

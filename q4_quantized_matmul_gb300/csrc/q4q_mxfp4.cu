@@ -117,57 +117,59 @@ __global__ void __launch_bounds__(THREADS, 4) acts_kernel(const ActArgs a) {
     if (a.pdl) asm volatile("griddepcontrol.wait;" ::: "memory");
     for (int64_t i = (int64_t)blockIdx.x * THREADS + threadIdx.x; i < a.n_ctrl; i += (int64_t)gridDim.x * THREADS)
         a.ctrl[i] = 0u;
-    int* start = seg_smem;
-    int* base = seg_smem + a.n_experts + 1;
-    if (a.first) mx_segments(a.first, a.n_experts, a.n_rows, a.bn, a.max_groups, start, base, tmp);
     const int segs = (a.K + MX_KP - 1) / MX_KP, nkc = 2 * segs, chunk = mx_chunk_bytes(a.bn), last = a.K - (segs - 1) * MX_KP;
     constexpr int LANE_BYTES = E4M3 ? 8 : 4;
     const T* src = static_cast<const T*>(a.src);
     uint8_t* scales = a.scales + (lane >> 4) * chunk;
-    const int64_t total = a.n_rows * segs;
+    const int64_t total = a.n_rows * segs, step = (int64_t)gridDim.x * (THREADS / 32) * UNITS;
     const bool small = total < (1ll << 31);
-    // where row r comes from (null: zeros) and where it goes (negative: nowhere)
-    auto place = [&](int64_t r, const T*& from, int64_t& to) {
-        from = src + r * a.K + lane * 8;
-        to = r;
-        if (!a.first) return;
-        to = -1;
-        // the expert with start[e] <= r < start[e + 1]; empty experts share a start
-        if (r >= start[a.n_experts] || r < start[0]) return;
-        const int e = mx_find(start, a.n_experts, (int)r);
-        const int64_t at = (int64_t)base[e] * a.bn + (r - start[e]);
-        if (at >= (int64_t)base[e + 1] * a.bn) return;
-        to = at;
-        const int64_t row = a.slot ? (int64_t)((uint32_t)__ldg(a.slot + r) / (uint32_t)a.top_k) : r;
-        from = row < a.n_src ? src + row * a.K + lane * 8 : nullptr;
-    };
-    for (int64_t u0 = (((int64_t)blockIdx.x * THREADS + threadIdx.x) >> 5) * UNITS; u0 < total;
-         u0 += (int64_t)gridDim.x * (THREADS / 32) * UNITS) {
-        const Unit first(u0, segs, small);
-        const int n = (int)min((int64_t)UNITS, total - u0);
-        MxRaw<T> v[UNITS];
-        int64_t to[UNITS];
-        const T* from = nullptr;
-        Unit at = first;
+    MxRaw<T> v[UNITS];
+    // the loads of units u0 ..: rows of src, by way of their slots
+    auto load = [&](int64_t u0) {
+        Unit at(u0, segs, small);
+        const T* from = src;
+        bool there = false;
 #pragma unroll
         for (int k = 0; k < UNITS; ++k) {
-            to[k] = -1;
-            if (k < n) {
-                if (k == 0 || at.seg == 0) place(at.row, from, to[k]);
-                else to[k] = to[k - 1];
+            if (u0 + k < total && (k == 0 || at.seg == 0)) {
+                const int64_t row = a.slot ? (int64_t)((uint32_t)__ldg(a.slot + at.row) / (uint32_t)a.top_k) : at.row;
+                there = row < a.n_src;
+                from = src + row * a.K + lane * 8;
             }
-            v[k].live = to[k] >= 0 && from && (at.seg < segs - 1 || lane * 8 < last);
+            v[k].live = u0 + k < total && there && (at.seg < segs - 1 || lane * 8 < last);
             v[k].load(v[k].live ? from + at.seg * MX_KP : src, a.vec);
             at.next(segs);
         }
-        at = first;
+    };
+    int64_t u0 = (((int64_t)blockIdx.x * THREADS + threadIdx.x) >> 5) * UNITS;
+    if (u0 < total) load(u0);
+    // where the rows go is worked out while the first loads are in flight
+    int* start = seg_smem;
+    int* base = seg_smem + a.n_experts + 1;
+    if (a.first) mx_segments(a.first, a.n_experts, a.n_rows, a.bn, a.max_groups, start, base, tmp);
+    // the operand row of sorted row r; negative: none
+    auto place = [&](int64_t r) -> int64_t {
+        if (!a.first) return r;
+        // the expert with start[e] <= r < start[e + 1]; empty experts share a start
+        if (r >= start[a.n_experts] || r < start[0]) return -1;
+        const int e = mx_find(start, a.n_experts, (int)r);
+        const int64_t to = (int64_t)base[e] * a.bn + (r - start[e]);
+        return to < (int64_t)base[e + 1] * a.bn ? to : -1;
+    };
+    while (u0 < total) {
+        Unit at(u0, segs, small);
+        int64_t to = -1;
 #pragma unroll
         for (int k = 0; k < UNITS; ++k) {
-            if (to[k] >= 0)
-                mx_encode_segment<E4M3>(v[k], a.codes + ((to[k] * segs + at.seg) * 32 + lane) * LANE_BYTES,
-                                        scales + mx_scale_offset(to[k], a.bn_log, chunk, nkc, 2 * at.seg));
+            if (u0 + k >= total) break;
+            if (k == 0 || at.seg == 0) to = place(at.row);
+            if (to >= 0)
+                mx_encode_segment<E4M3>(v[k], a.codes + ((to * segs + at.seg) * 32 + lane) * LANE_BYTES,
+                                        scales + mx_scale_offset(to, a.bn_log, chunk, nkc, 2 * at.seg));
             at.next(segs);
         }
+        u0 += step;
+        if (u0 < total) load(u0);
     }
 }
 
@@ -227,8 +229,9 @@ mx_get_rows_kernel(const uint8_t* __restrict__ table, int64_t code_bytes, int64_
     }
 }
 
-// Units a warp takes at a time: several where there are enough for all SMs' warps
-bool many(int64_t units, const DeviceInfo& info) { return units >= (int64_t)info.sm_count * 64 * 2; }
+// Units a warp takes at a time: several where one each would take more than one round of the
+// SMs' 32 resident warps (2068 rows of 1504 routed to 32 experts: 8.5 us with one, see grid_of)
+bool many(int64_t units, const DeviceInfo& info) { return units > (int64_t)info.sm_count * 32; }
 
 int grid_of(int64_t units, int units_at_a_time, const DeviceInfo& info) {
     const int64_t warps = (units + units_at_a_time - 1) / units_at_a_time;
