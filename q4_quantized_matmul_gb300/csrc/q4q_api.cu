@@ -294,8 +294,7 @@ extern "C" q4q_status q4q_device_status(q4q_status* status) {
                                   gemv_group_take_device_status(), gemv_epi_take_device_status(),
                                   rows_take_device_status(), debug_take_device_status(),
                                   chain_take_device_status(), rmma_take_device_status(),
-                                  mxfp4_take_device_status(), mxmm_take_device_status(),
-                                  mxmv_take_device_status()};
+                                  mxfp4_take_device_status(), mxmm_take_device_status()};
     unsigned int first = 0;
     for (unsigned int w : words)
         if (!first) first = w;

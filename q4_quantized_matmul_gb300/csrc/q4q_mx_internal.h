@@ -24,21 +24,13 @@ struct MxActs {
 unsigned int mxfp4_take_device_status();
 unsigned int mxmm_take_device_status();
 
-constexpr int MXMV_TOKENS = 8;       // token tile of the few-token kernel
-
-unsigned int mxmv_take_device_status();
-
-// The few-token kernel (q4q_mxmv.cu): one launch, no workspace.
-q4q_status mxmv_run(const void* src0, int64_t ne00, int64_t ne01, int n_mats, const MxActs& m, void* dst, int dst_type,
-                    bool pdl, cudaStream_t stream, const DeviceInfo& info, const KernelDebug* dbg);
-
 // The tensor map of MXFP4 weights: boxes of 128 rows and stage_atoms atoms of 128 bytes of
 // shared memory a row (q4q_mxmm.cu).
 bool mx_encode_weight_map(CUtensorMap* map, const void* src0, int64_t ne00, int64_t ne01, int n_mats, bool e4m3, int stage_atoms);
 
 // Encode the activations of a product into `codes` and `scales` (token tiles of bn rows, at
-// most max_groups of them) and zero the n_ctrl control words (q4q_mxfp4.cu).
-q4q_status mx_encode_acts(const MxActs& m, unsigned int* ctrl, int64_t n_ctrl, uint8_t* codes, uint8_t* scales, int bn,
+// most max_groups of them) and zero the call's abort word (q4q_mxfp4.cu).
+q4q_status mx_encode_acts(const MxActs& m, unsigned int* abort_word, uint8_t* codes, uint8_t* scales, int bn,
                           int64_t max_groups, bool pdl, cudaStream_t stream, const DeviceInfo& info);
 
 }  // namespace q4q

@@ -93,13 +93,12 @@ encode_kernel(const T* __restrict__ src, bool vec, uint8_t* __restrict__ dst, in
 }
 
 // The activations of a product: row i of the operand is row i of src (dense), or, for an
-// expert's row, the row of its token.  Also zeroes the product's control words.
+// expert's row, the row of its token.  Also zeroes the product's abort word.
 struct ActArgs {
     const void* src;
     uint8_t* codes;
     uint8_t* scales;
-    unsigned int* ctrl;
-    int64_t n_ctrl;
+    unsigned int* abort_word;
     int64_t n_src, n_rows;
     int64_t max_groups;
     const int32_t* first;      // null: dense
@@ -115,8 +114,7 @@ __global__ void __launch_bounds__(THREADS, 4) acts_kernel(const ActArgs a) {
     const int lane = threadIdx.x & 31;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (a.pdl) asm volatile("griddepcontrol.wait;" ::: "memory");
-    for (int64_t i = (int64_t)blockIdx.x * THREADS + threadIdx.x; i < a.n_ctrl; i += (int64_t)gridDim.x * THREADS)
-        a.ctrl[i] = 0u;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.abort_word = 0u;
     const int segs = (a.K + MX_KP - 1) / MX_KP, nkc = 2 * segs, chunk = mx_chunk_bytes(a.bn), last = a.K - (segs - 1) * MX_KP;
     constexpr int LANE_BYTES = E4M3 ? 8 : 4;
     const T* src = static_cast<const T*>(a.src);
@@ -280,14 +278,13 @@ unsigned int mxfp4_take_device_status() {
     return v;
 }
 
-q4q_status mx_encode_acts(const MxActs& m, unsigned int* ctrl, int64_t n_ctrl, uint8_t* codes, uint8_t* scales, int bn,
+q4q_status mx_encode_acts(const MxActs& m, unsigned int* abort_word, uint8_t* codes, uint8_t* scales, int bn,
                           int64_t max_groups, bool pdl, cudaStream_t stream, const DeviceInfo& info) {
     ActArgs a;
     a.src = m.src;
     a.codes = codes;
     a.scales = scales;
-    a.ctrl = ctrl;
-    a.n_ctrl = n_ctrl;
+    a.abort_word = abort_word;
     a.n_src = m.n_src;
     a.n_rows = m.n_rows;
     a.max_groups = max_groups;

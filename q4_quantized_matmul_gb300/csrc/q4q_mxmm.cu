@@ -4,27 +4,35 @@
 //   dst[n][m] = sum_b 2^(ew[m][b] + ex[n][b]) * sum_{k in block b} w[m][k] * x[n][k]
 //
 // with w in E2M1 and x, encoded on the fly (q4q_mxfp4.cu), in E2M1 (kind::mxf4) or E4M3
-// (kind::mxf8f6f4); up to 8 tokens q4q_mxmv.cu has its own kernel.  The tensor core takes codes and scales as they lie in memory, so
-// nothing is unpacked by CUDA cores; the weight rows are the MMA's M = 128 and the tokens
-// its N.
-// All products of two E2M1 values are multiples of 1/4 up to 36 and the accumulator is
-// fp32.
+// (kind::mxf8f6f4).  The tensor core takes codes and scales as they lie in memory, so
+// nothing is unpacked by CUDA cores at any token count; the weight rows are the MMA's M and
+// the tokens its N.  All products of two E2M1 values are multiples of 1/4 up to 36 and the
+// accumulator is fp32.
 //
-// Roles (one CTA per SM, 256 threads):
+// Roles (one CTA per SM, 384 threads):
 //   warp 0    : TMA producer.  A stage is one or more atoms of 128 bytes of each smem row
 //               (256 K of packed E2M1, or 128 K of E4M3 with the weights widened by the
 //               tensor map to one byte each, 16U4_ALIGN16B: HBM still moves the packed
 //               nibbles) and their scale chunks, in four copies.  The ring fills what
-//               shared memory there is.
-//   warp 1    : MMA issuer: scale chunks to tensor memory (tcgen05.cp), 4 MMAs a stage.
-//   warps 4-7 : epilogue: accumulator (two of them while 2 BN <= 256 columns) to dst.
+//               shared memory there is; the weights of the first stages do not wait for
+//               the activation encoder, behind which the kernel is launched with
+//               programmatic dependent launch.
+//   warp 1    : MMA issuer: scale chunks to tensor memory (tcgen05.cp), 4 MMAs an atom.
+//   warps 4-11: epilogue: accumulator (two of them while 2 BN <= 256 columns) through
+//               registers to dst.
 //
-// Work is the line of all (tile, K stage) pairs.  In split mode CTA c takes the c-th equal
-// part of that line, so that all SMs stream the same amount whatever the shape; a tile cut
-// by a boundary is summed by the CTA that finishes it last, from fp32 partial sums in the
-// workspace in the order of K, so that the result does not depend on which CTA that is.
-// In whole mode CTA c takes tiles c, c + CTAs, ...: the CTAs walk K together over
-// neighbouring tiles, so what one reads from HBM the others find in L2.
+// Three ways to spread the tiles, picked by the expected time (pick_tile):
+//   one CTA a tile of 128 rows x 8 to 64 tokens; CTA c takes tiles c, c + CTAs, ..., so that
+//     neighbouring CTAs walk K together and what one reads from HBM others find in L2;
+//   a pair of CTAs a tile of 256 rows x 64 to 256 tokens: each loads its 128 rows and half
+//     of the tokens, the first issues the pair's MMAs (cta_group::2), which halves what the
+//     token side costs in copies;
+//   few tiles: a cluster of 2 to 8 CTAs shares the K of a tile of 8 to 64 tokens and joins
+//     the parts over distributed shared memory in the order of K.
+//
+// What bounds it: a CTA's copies take 1.05 ns a shared-memory row (128 bytes, two cycles),
+// so an atom of 128 + 16 rows 0.165 us and of a pair's 128 + 128 rows 0.28; its MMAs 0.14 us
+// up to 128 tokens, 0.27 with 256.
 //
 // Every mbarrier wait is bounded; one that runs out records Q4Q_ERR_TIMEOUT, raises the
 // call's abort word (zeroed by the activation encoder before every launch) and the CTA
@@ -47,9 +55,8 @@ __device__ unsigned int g_mxmm_status = 0;
 
 constexpr int EPI_WARPS = 8;
 constexpr int THREADS = 128 + 32 * EPI_WARPS;
-constexpr int CTRL_ABORT = 0;                 // control words: the abort word, then a counter per tile
-constexpr int CTRL_COUNT = 64;
-constexpr int MIN_SPLIT_ATOMS = 8;            // least work of a CTA in split mode, in 128-byte atoms
+constexpr int CTRL_BYTES = 256;               // the call's control words: the abort word
+constexpr int MAX_SPLIT = 8;                  // CTAs that share a tile's K: a portable cluster
 
 // ---------------------------------------------------------------- the work --
 
@@ -58,7 +65,7 @@ struct MxParams {
     int64_t n_rows;               // rows of dst (tokens, or sorted rows)
     int64_t max_groups;           // token tiles of the activation operand
     bool wait_first;              // `first` may still be being written when the kernel starts
-    bool may_split;               // whether tiles may be cut along K
+    int split;                    // CTAs that share a tile's K
     int mtiles, kst, nkc;         // weight row tiles, K stages, 128-column scale chunks
     const int32_t* first;         // experts' first rows, or null (dense: one segment)
     const uint8_t* w_scales;      // scale plane of matrix 0
@@ -66,9 +73,7 @@ struct MxParams {
     const uint8_t* x_scales;
     void* dst;
     int dst_type;
-    float* part;                  // two partial tiles per CTA
-    unsigned int* ctrl;
-    int64_t n_counters;
+    unsigned int* abort_word;
     uint64_t limit_ns;
     int fault;                    // test only: CTA 0 leaves out its first stage's copies
 };
@@ -108,41 +113,27 @@ struct Cfg {
     static_assert(USED <= 512 && B_BYTES % 1024 == 0 && ST >= 3 && SMEM <= 227 * 1024, "fits the SM");
 };
 
-// A CTA's share of the work and its walk over it.
+// The tiles of a CTA (or pair): pos, pos + step, ... below end; `part` of `split` parts of
+// their K.
 struct Walk {
-    int64_t pos, end;      // split: stages of the line; whole: tiles, in steps of `parts`
-    int64_t total;         // stages in all
-    int parts;             // CTAs (or pairs) that share the work
-    bool split;
+    int64_t pos, end, step;
+    int part, split;
 };
 
 struct Frag {
     int mat, m0, k0, k1;   // matrix, first weight row, K stages
     int x_row;             // first row of the activation operand
-    int64_t tile;
     int64_t dst_row;
     int valid;             // tokens of the tile
-    bool whole;
 };
 
 template <int BN, int CG>
 __device__ __forceinline__ bool next_frag(Walk& w, const MxParams& p, const int* start, const int* units, Frag& f) {
     if (w.pos >= w.end) return false;
-    int64_t t;
-    if (w.split) {
-        t = w.pos / p.kst;
-        f.k0 = (int)(w.pos - t * p.kst);
-        f.k1 = (int)min((int64_t)p.kst, f.k0 + (w.end - w.pos));
-        w.pos += f.k1 - f.k0;
-        f.whole = f.k0 == 0 && f.k1 == p.kst;
-    } else {
-        t = w.pos;
-        w.pos += w.parts;
-        f.k0 = 0;
-        f.k1 = p.kst;
-        f.whole = true;
-    }
-    f.tile = t;
+    const int64_t t = w.pos;
+    w.pos += w.step;
+    f.k0 = p.kst * w.part / w.split;
+    f.k1 = p.kst * (w.part + 1) / w.split;
     // tiles: by segment, then weight rows, then tokens (the weights of a row tile are read
     // by consecutive tiles)
     int e = 0, g0 = 0, groups = units[1];
@@ -201,11 +192,10 @@ mxmm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ 
     const uint32_t acc_full = empty + 8 * ST, acc_empty = acc_full + 16;
     const uint32_t drain = acc_empty + 16, slot_addr = drain + 8;
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_BAR + 16 * ST + 48);
-    volatile int* last_flag = abort_flag + 1;
     int* tmp = reinterpret_cast<int*>(smem + C::OFF_BAR + 512);
     int* start = reinterpret_cast<int*>(smem + C::OFF_SEG);
     int* units = start + MX_MAX_EXPERTS + 1;
-    const Waiter wt{abort_flag, p.ctrl + CTRL_ABORT, p.limit_ns, &g_mxmm_status};
+    const Waiter wt{abort_flag, p.abort_word, p.limit_ns, &g_mxmm_status};
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int rank = CG == 2 ? (int)(blockIdx.x & 1) : 0;        // in the pair; 0 issues its MMAs
 
@@ -246,19 +236,13 @@ mxmm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ 
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(slot_addr));
     tmem = __shfl_sync(0xffffffffu, tmem, 0);
 
-    {
-        const int64_t tiles = (int64_t)__shfl_sync(0xffffffffu, units[p.first ? p.n_mats : 1], 0) * p.mtiles;   // the same in the whole warp
-        const int workers = (int)gridDim.x / CG, me = (int)blockIdx.x / CG;
-        walk.total = tiles * p.kst;
-        walk.split = CG == 1 && p.may_split && tiles <= p.n_counters;
-        const int64_t most = walk.split ? max(walk.total * C::ATOMS / MIN_SPLIT_ATOMS, (int64_t)1) : tiles;
-        walk.parts = (int)max((int64_t)1, min((int64_t)workers, most));
-        walk.pos = walk.end = 0;
-        if (me < walk.parts) {
-            walk.pos = walk.split ? me * walk.total / walk.parts : me;
-            walk.end = walk.split ? (me + 1) * walk.total / walk.parts : tiles;
-        }
-    }
+    // the same in the whole warp, and known to be (see q4q_mx_tc.cuh's elect_one)
+    walk.end = (int64_t)__shfl_sync(0xffffffffu, units[p.first ? p.n_mats : 1], 0) * p.mtiles;
+    walk.split = p.split;
+    walk.part = p.split > 1 ? (int)(blockIdx.x % (unsigned)p.split) : 0;
+    walk.pos = blockIdx.x / (unsigned)(CG * p.split);
+    walk.step = gridDim.x / (unsigned)(CG * p.split);
+    const Walk all = walk;
 
     if (warp == 0) {
         // ---------------- producer
@@ -401,7 +385,6 @@ mxmm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ 
         const int quad = warp & 3, row = quad * 32 + lane, col0 = (warp - 4) / 4 * CW;
         const uint32_t tq = tmem + ((uint32_t)(quad * 32) << 16) + col0;
         const uint32_t freed = CG == 2 ? mapa_shared(acc_empty, 0) : acc_empty;
-        const Walk mine = walk;
         Frag f;
         int n = 0;
         while (next_frag<BN, CG>(walk, p, start, units, f)) {
@@ -420,55 +403,18 @@ mxmm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ 
                 else mbar_arrive(freed + 8 * buf);
             }
             const int valid = f.valid - col0;
-            const int64_t at = (f.dst_row + col0) * p.M + m;
-            if (f.whole) {
+            if (p.split == 1) {
+                const int64_t at = (f.dst_row + col0) * p.M + m;
                 if (m < p.M) {
                     if (p.dst_type == Q4Q_TYPE_F32) store_columns<float, CW>(p.dst, at, p.M, r, valid);
                     else if (p.dst_type == Q4Q_TYPE_F16) store_columns<__half, CW>(p.dst, at, p.M, r, valid);
                     else store_columns<__nv_bfloat16, CW>(p.dst, at, p.M, r, valid);
                 }
             } else {
-                // this CTA's partial tile: slot 0 if it starts inside the tile, else slot 1
-                const int64_t me = blockIdx.x;
-                constexpr int64_t PART = BM * BN;
-                float* out = p.part + (me * 2 + (f.k0 == 0 ? 1 : 0)) * PART + col0 * BM + row;
+                // every stage has been read: the CTA's part of its one tile, [token][row], takes their place
+                float* part = reinterpret_cast<float*>(smem) + col0 * BM + row;
 #pragma unroll
-                for (int c = 0; c < CW; ++c)
-                    if (c < valid) __stcg(out + c * BM, __uint_as_float(r[c]));
-                // the CTAs that share the tile: from the owner of its first stage to that of its last
-                const int64_t s0 = f.tile * p.kst, s1 = s0 + p.kst - 1;
-                const int64_t c_first = ((s0 + 1) * mine.parts - 1) / mine.total, c_last = ((s1 + 1) * mine.parts - 1) / mine.total;
-                __threadfence();
-                asm volatile("bar.sync 1, %0;" ::"r"(N_THREADS) : "memory");
-                if (threadIdx.x == 128) {
-                    const unsigned int before = atomicAdd(p.ctrl + CTRL_COUNT + f.tile, 1u);
-                    *last_flag = before == (unsigned int)(c_last - c_first);
-                }
-                asm volatile("bar.sync 1, %0;" ::"r"(N_THREADS) : "memory");
-                const bool last = *last_flag != 0;
-                asm volatile("bar.sync 1, %0;" ::"r"(N_THREADS) : "memory");
-                if (last) {
-                    // all columns of one CTA's part in flight at a time, the parts in the order of K
-                    __threadfence();
-                    constexpr int CC = CW < 32 ? CW : 32;
-#pragma unroll 1
-                    for (int c0 = 0; c0 < CW && c0 < valid; c0 += CC) {
-                        float acc[CC];
-                        for (int64_t o = c_first; o <= c_last; ++o) {
-                            const float* q = p.part + (o * 2 + (o == c_first ? 1 : 0)) * PART + (col0 + c0) * BM + row;
-                            float v[CC];
-#pragma unroll
-                            for (int c = 0; c < CC; ++c) v[c] = c0 + c < valid ? __ldcg(q + c * BM) : 0.0f;
-#pragma unroll
-                            for (int c = 0; c < CC; ++c) acc[c] = o == c_first ? v[c] : __fadd_rn(acc[c], v[c]);
-                        }
-                        if (m < p.M) {
-#pragma unroll
-                            for (int c = 0; c < CC; ++c)
-                                if (c0 + c < valid) mx_store(p.dst, p.dst_type, at + (int64_t)(c0 + c) * p.M, acc[c]);
-                        }
-                    }
-                }
+                for (int c = 0; c < CW; ++c) part[c * BM] = __uint_as_float(r[c]);
             }
             ++n;
         }
@@ -481,6 +427,41 @@ mxmm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ 
     }
 
     tc_fence_before();
+    if (CG == 1 && p.split > 1) {
+        // CTA z adds the z-th share of the tile's values, over the CTAs in the order of K
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();
+        Walk w = all;
+        Frag f;
+        if (next_frag<BN, CG>(w, p, start, units, f)) {
+            // four rows of a token a thread; all parts' loads in flight together
+#pragma unroll 2
+            for (int u = all.part * THREADS + (int)threadIdx.x; u < f.valid * (BM / 4); u += p.split * THREADS) {
+                float4 v[MAX_SPLIT];
+#pragma unroll
+                for (int z = 0; z < MAX_SPLIT; ++z)
+                    if (z < p.split)
+                        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                     : "=f"(v[z].x), "=f"(v[z].y), "=f"(v[z].z), "=f"(v[z].w) : "r"(mapa_shared(sbase + 16 * u, z)) : "memory");
+                float sum[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+                for (int z = 1; z < MAX_SPLIT; ++z)
+                    if (z < p.split) {
+                        sum[0] = __fadd_rn(sum[0], v[z].x);
+                        sum[1] = __fadd_rn(sum[1], v[z].y);
+                        sum[2] = __fadd_rn(sum[2], v[z].z);
+                        sum[3] = __fadd_rn(sum[3], v[z].w);
+                    }
+                const int m = f.m0 + u % (BM / 4) * 4;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (m + k < p.M) mx_store(p.dst, p.dst_type, (f.dst_row + u / (BM / 4)) * p.M + m + k, sum[k]);
+            }
+        }
+        cluster_arrive();                                        // no CTA leaves while another may still read its part
+        cluster_wait();
+    }
     __syncthreads();
     if constexpr (CG == 2) {                                     // neither CTA leaves while the other uses its memory
         cluster_arrive();
@@ -508,47 +489,53 @@ bool get_encode() {
 
 // A product's tile and workspace.
 struct Plan {
-    int bn, cg;
-    bool split;
-    int64_t kp, max_groups, n_counters;
-    size_t codes, scales, ctrl, part, total;       // offsets after the codes, and the whole size
+    int bn, cg, split;
+    int64_t kp, max_groups;
+    size_t scales, ctrl, total;          // offsets after the codes, and the whole size
 };
 
-// Whether few tokens are expected: all of them, or twice the mean of the experts' shares.
+// The rows of a segment that a token tile is chosen for: all of them, or twice the mean of the
+// experts' shares (a larger share takes several tiles).
 int64_t expected_rows(int64_t n_rows, int64_t n_tokens, int n_experts) {
     return n_experts > 0 ? std::min(n_tokens, 2 * ((n_rows + n_experts - 1) / n_experts)) : n_rows;
 }
 
-// The tile, and whether tiles are cut along K.  Up to 64 expected rows, the least tile that
-// holds them, cut into equal parts.  Above that, the choice that is expected to take least:
-// SM rounds x K x the cycles of an atom (what its copies take: 2.1 a row of 128 bytes, or its
-// MMAs: 2 a token, 1 for each CTA of a pair) + 3000 a tile, of
-//   one CTA a tile of 128 x 128, cut along K;  a pair a tile of 256 x 128 or 256 x 256.
+// Clusters of `split` CTAs that the device holds at one CTA an SM (152 SMs hold 76, 36, 15 of 2, 4, 8).
+int64_t clusters_held(int split, int sm_count) { return split == 8 ? sm_count / 10 : split == 4 ? (sm_count - 8) / 4 : sm_count / split; }
+
+// The form that is expected to take least.  Times in ns, fitted to 4096 x 1024, 4096 x 4096,
+// 4096 x 14336 and 14336 x 4096 at 8 to 1024 tokens in every form (within a tenth): a form's start
+// and end, its time for an atom of E4M3 and of E2M1 activations, 2400 (64 tokens: 3200) to join a
+// tile's parts, 600 for each further round of tiles, and what HBM needs at 6500 bytes a ns behind
+// a start of 4400.  For example 14336 x 4096, 8 tokens, E4M3: 20.3 us whole, 15.4 and 12.1 in 2 and
+// 4 parts; 4096 x 4096, E2M1: 6.9 whole, 8.8 and 8.1 in 2 and 4; 14336 x 4096, 128 tokens, E4M3:
+// tiles of 64 tokens 23.5 whole, 18.6 in 2 parts, 20.5 by pairs, tiles of 128 by pairs 27.8.
 void pick_tile(Plan& q, int64_t K, int64_t M, int64_t n_rows, int64_t n_tokens, int n_experts, int acts, int sm_count) {
     const int64_t expect = expected_rows(n_rows, n_tokens, n_experts);
-    q.cg = 1;
-    q.split = true;
-    for (int bn : {MXMV_TOKENS, 16, 32, 64})
-        if (expect <= bn) {
-            q.bn = bn;
-            return;
-        }
     const int64_t segments = n_experts > 0 ? std::min<int64_t>(n_experts, n_rows) : 1, mean = (n_rows + segments - 1) / segments;
-    const int64_t atoms = (K + (acts == Q4Q_ACTS_MXFP8 ? 127 : 255)) / (acts == Q4Q_ACTS_MXFP8 ? 128 : 256);
+    const bool e4m3 = acts == Q4Q_ACTS_MXFP8;
+    const int64_t ka = e4m3 ? 128 : 256, atoms = (K + ka - 1) / ka;
+    const double hbm = (double)segments * M * K * 0.53 / 6500 + 4400;
+    static const struct { int bn, cg, start, e4m3, e2m1; } forms[] = {
+        {8, 1, 4700, 145, 150}, {16, 1, 4700, 155, 165}, {32, 1, 4700, 160, 170}, {64, 1, 4900, 162, 185},
+        {64, 2, 6100, 122, 170}, {128, 2, 6400, 187, 220}, {256, 2, 6800, 270, 310}};
     double least = 1e300;
-    const struct { int bn, cg; } forms[] = {{64, 1}, {128, 1}, {128, 2}, {256, 2}};
     for (const auto& f : forms) {
+        if (f.bn < expect && f.bn < 64) continue;              // narrow tiles only where one holds the tokens
+        const double atom = e4m3 ? f.e4m3 : f.e2m1;
         const int64_t tiles = segments * ((mean + f.bn - 1) / f.bn) * ((M + BM * f.cg - 1) / (BM * f.cg));
-        const int64_t workers = sm_count / f.cg;
-        const double rounds = f.cg == 1 ? std::max(1.0, (double)tiles / workers) : (double)((tiles + workers - 1) / workers);
-        const double cycles = std::max(2.1 * (BM + f.bn / f.cg), 2.0 * f.bn);
-        // a cut tile is also written to and read from the workspace
-        const double cost = rounds * (atoms * cycles + 3000) + (f.cg == 1 ? 6000 : 0);
-        if (cost < least) {
-            least = cost;
-            q.bn = f.bn;
-            q.cg = f.cg;
-            q.split = f.cg == 1;
+        const int64_t workers = sm_count / f.cg, rounds = (tiles + workers - 1) / workers;
+        for (int split = 1; split <= (f.cg == 1 ? MAX_SPLIT : 1); split *= 2) {
+            if (split > 1 && (tiles > clusters_held(split, sm_count) || atoms < 2 * split)) break;
+            const double work = split > 1 ? f.start + (f.bn == 64 ? 3200 : 2400) + atom * ((atoms + split - 1) / split)
+                                          : f.start + atom * rounds * atoms + 600 * (rounds - 1);
+            const double cost = std::max(work, hbm) + 0.01 * f.bn;
+            if (cost < least) {
+                least = cost;
+                q.bn = f.bn;
+                q.cg = f.cg;
+                q.split = split;
+            }
         }
     }
 }
@@ -556,17 +543,13 @@ void pick_tile(Plan& q, int64_t K, int64_t M, int64_t n_rows, int64_t n_tokens, 
 Plan make_plan(int64_t K, int64_t M, int64_t n_rows, int64_t n_tokens, int n_experts, int acts, int sm_count) {
     Plan q{};
     pick_tile(q, K, M, n_rows, n_tokens, n_experts, acts, sm_count);
-    if (q.bn == MXMV_TOKENS) return q;             // q4q_mxmv.cu needs no workspace
     q.kp = mx_up(K, MX_KP);
-    // token tiles: each segment starts a new one
-    const int64_t tiles_n = (n_rows + q.bn - 1) / q.bn + (n_experts > 0 ? std::min<int64_t>(n_experts, n_rows) : 0);
-    q.max_groups = tiles_n;
-    // a counter for each tile that may be cut; with more tiles than this whole ones fill the SMs
-    q.n_counters = q.split ? std::min<int64_t>(tiles_n * ((M + BM - 1) / BM), 64 * (int64_t)sm_count) : 0;
-    q.scales = (size_t)mx_up(tiles_n * q.bn * (acts == Q4Q_ACTS_MXFP8 ? q.kp : q.kp / 2), 1024);
-    q.ctrl = q.scales + (size_t)mx_up(tiles_n * (q.kp / 128) * mx_chunk_bytes(q.bn), 256);
-    q.part = q.ctrl + (size_t)mx_up((CTRL_COUNT + q.n_counters) * 4, 256);
-    q.total = q.part + (q.split ? (size_t)sm_count * 2 * BM * q.bn * 4 : 0);
+    // token tiles: each segment starts a new one, and none is without a row
+    q.max_groups = (n_rows + q.bn - 1) / q.bn + (n_experts > 0 ? std::min<int64_t>(n_experts, n_rows) : 0);
+    q.max_groups = std::min(q.max_groups, n_rows);
+    q.scales = (size_t)mx_up(q.max_groups * q.bn * (acts == Q4Q_ACTS_MXFP8 ? q.kp : q.kp / 2), 1024);
+    q.ctrl = q.scales + (size_t)mx_up(q.max_groups * (q.kp / 128) * mx_chunk_bytes(q.bn), 256);
+    q.total = q.ctrl + CTRL_BYTES;
     return q;
 }
 
@@ -578,6 +561,7 @@ struct Maps {
 
 template <int BN, bool E4M3, int CG>
 q4q_status launch_t(const Maps& maps, const MxParams& p, int64_t workers, cudaStream_t stream, int device) {
+    const int cluster = CG * p.split;
     using C = Cfg<BN, E4M3, CG>;
     static_assert(C::ATOMS == (BN <= 64 ? 2 : 1), "the tensor maps' boxes");
     static std::atomic<int> configured[64];
@@ -589,7 +573,7 @@ q4q_status launch_t(const Maps& maps, const MxParams& p, int64_t workers, cudaSt
         configured[device].store(1);
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(workers * CG));
+    cfg.gridDim = dim3((unsigned)(workers * cluster));
     cfg.blockDim = dim3(THREADS);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = stream;
@@ -597,11 +581,11 @@ q4q_status launch_t(const Maps& maps, const MxParams& p, int64_t workers, cudaSt
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // behind the activation encoder
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = CG == 1 ? 1 : 2;
+    cfg.numAttrs = cluster == 1 ? 1 : 2;
     if (cudaLaunchKernelEx(&cfg, kern, maps.w, maps.x, maps.sw, maps.sx, p) != cudaSuccess) return (cudaGetLastError(), Q4Q_ERR_CUDA);
     return launch_status();
 }
@@ -609,12 +593,13 @@ q4q_status launch_t(const Maps& maps, const MxParams& p, int64_t workers, cudaSt
 template <bool E4M3>
 q4q_status launch_bn(const Plan& q, const Maps& maps, const MxParams& p, int64_t workers, cudaStream_t stream, int device) {
     switch (q.bn) {
+        case 8: return launch_t<8, E4M3, 1>(maps, p, workers, stream, device);
         case 16: return launch_t<16, E4M3, 1>(maps, p, workers, stream, device);
         case 32: return launch_t<32, E4M3, 1>(maps, p, workers, stream, device);
-        case 64: return launch_t<64, E4M3, 1>(maps, p, workers, stream, device);
-        case 128:
-            return q.cg == 1 ? launch_t<128, E4M3, 1>(maps, p, workers, stream, device)
-                             : launch_t<128, E4M3, 2>(maps, p, workers, stream, device);
+        case 64:
+            return q.cg == 1 ? launch_t<64, E4M3, 1>(maps, p, workers, stream, device)
+                             : launch_t<64, E4M3, 2>(maps, p, workers, stream, device);
+        case 128: return launch_t<128, E4M3, 2>(maps, p, workers, stream, device);
         default: return launch_t<256, E4M3, 2>(maps, p, workers, stream, device);
     }
 }
@@ -638,7 +623,6 @@ q4q_status run(const void* src0, int64_t ne00, int64_t ne01, int n_mats, const M
     if (st != Q4Q_OK) return st;
     if (info.cc_major != 10 || !get_encode()) return Q4Q_ERR_CUDA;
     const Plan q = make_plan(ne00, ne01, acts.n_rows, n_tokens, acts.first ? n_mats : 0, acts.acts, info.sm_count);
-    if (q.bn == MXMV_TOKENS) return mxmv_run(src0, ne00, ne01, n_mats, acts, dst, dst_type, pdl, stream, info, dbg);
     if (workspace_bytes < q.total) return Q4Q_ERR_WORKSPACE;
     if (!workspace) return Q4Q_ERR_NULL;
     if (!aligned(workspace, 256)) return Q4Q_ERR_ALIGN;
@@ -657,7 +641,7 @@ q4q_status run(const void* src0, int64_t ne00, int64_t ne01, int n_mats, const M
         const cuuint64_t strides[2] = {(cuuint64_t)(e4m3 ? q.kp : q.kp / 2), 128};
         const cuuint32_t box[3] = {128, (cuuint32_t)(q.bn / q.cg), (cuuint32_t)stage_atoms};
         const cuuint32_t one[3] = {1, 1, 1};
-        if (g_encode(&maps.x, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, ws + q.codes, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+        if (g_encode(&maps.x, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, ws, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
                      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return Q4Q_ERR_CUDA;
     }
@@ -670,7 +654,7 @@ q4q_status run(const void* src0, int64_t ne00, int64_t ne01, int n_mats, const M
     p.n_rows = acts.n_rows;
     p.max_groups = q.max_groups;
     p.wait_first = pdl;
-    p.may_split = q.split;
+    p.split = q.split;
     p.mtiles = (int)((ne01 + BM * q.cg - 1) / (BM * q.cg));
     const int ks = 128 * ch * stage_atoms;
     p.kst = (int)((ne00 + ks - 1) / ks);
@@ -681,17 +665,15 @@ q4q_status run(const void* src0, int64_t ne00, int64_t ne01, int n_mats, const M
     p.x_scales = ws + q.scales;
     p.dst = dst;
     p.dst_type = dst_type;
-    p.part = reinterpret_cast<float*>(ws + q.part);
-    p.ctrl = reinterpret_cast<unsigned int*>(ws + q.ctrl);
-    p.n_counters = q.n_counters;
+    p.abort_word = reinterpret_cast<unsigned int*>(ws + q.ctrl);
     p.limit_ns = dbg ? dbg->limit_ns : WAIT_LIMIT_NS;
     p.fault = dbg ? dbg->fault : 0;
-    st = mx_encode_acts(acts, p.ctrl, CTRL_COUNT + q.n_counters, ws + q.codes, ws + q.scales, q.bn, q.max_groups, pdl, stream, info);
+    st = mx_encode_acts(acts, p.abort_word, ws, ws + q.scales, q.bn, q.max_groups, pdl, stream, info);
     if (st != Q4Q_OK) return st;
-    // no more CTAs than there can be parts of the work
+    // CTAs (pairs) that take tiles in turn, or a cluster for each tile that there may be
     const int64_t tiles = q.max_groups * p.mtiles;
-    const int64_t most = q.split ? tiles * p.kst * stage_atoms / MIN_SPLIT_ATOMS : tiles;
-    const int64_t workers = std::max<int64_t>(1, std::min<int64_t>(info.sm_count / q.cg, most));
+    const int64_t workers = q.split > 1 ? tiles : std::min<int64_t>(info.sm_count / q.cg, tiles);
+    if (workers * q.split >= (1ll << 31)) return Q4Q_ERR_SHAPE;
     return e4m3 ? launch_bn<true>(q, maps, p, workers, stream, info.device) : launch_bn<false>(q, maps, p, workers, stream, info.device);
 }
 
