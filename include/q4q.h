@@ -463,7 +463,7 @@ Q4Q_API q4q_status q4q_get_rows_mxfp4(const void* src0, int64_t ne00, int64_t ne
                               int64_t n_ids, float* dst, q4q_stream_t stream);
 
 /* Bytes of device workspace q4q_mul_mat_mxfp4 needs on the current device: the encoded
- * activations, the call's control words and two partial output tiles per SM. */
+ * activations and the call's control words. */
 Q4Q_API q4q_status q4q_mul_mat_mxfp4_workspace_size(int64_t ne00, int64_t ne01, int64_t ne11, int acts, size_t* bytes);
 
 /* mul_mat with MXFP4 weights on the block-scaled tensor cores, for any token count:
@@ -475,9 +475,10 @@ Q4Q_API q4q_status q4q_mul_mat_mxfp4_workspace_size(int64_t ne00, int64_t ne01, 
  * the outputs it takes part in NaN.
  * src0: device, 256-byte aligned MXFP4 matrix; src1: device, src1_type [ne11][ne10],
  * dst: device, dst_type [ne11][ne01], each aligned to its type; workspace: 256-byte
- * aligned, q4q_mul_mat_mxfp4_workspace_size bytes.  flags as q4q_mul_mat_ex.  The result
- * depends on the operands and the device alone (sums split over CTAs are joined in the
- * order of K).  Limits: 0 <= ne11 < 2^20; an unknown acts or type: Q4Q_ERR_ARG. */
+ * aligned, q4q_mul_mat_mxfp4_workspace_size bytes.  flags as q4q_mul_mat_ex (honoured by
+ * the kernel that encodes src1).  The result depends on the operands and the device alone
+ * (sums shared by several CTAs are joined in the order of K).  Limits: 0 <= ne11 < 2^20;
+ * an unknown acts or type: Q4Q_ERR_ARG. */
 Q4Q_API q4q_status q4q_mul_mat_mxfp4(const void* src0, int64_t ne00, int64_t ne01, const void* src1, int src1_type,
                              int64_t ne10, int64_t ne11, int acts, void* dst, int dst_type, void* workspace,
                              size_t workspace_bytes, unsigned int flags, q4q_stream_t stream);

@@ -17,8 +17,13 @@
 // The sort is a counting sort in one launch of one cluster of up to 8 CTAs: every warp
 // counts a contiguous run of slots into its own histogram, prefix sums over warps, CTAs
 // (distributed shared memory) and experts turn the counts into places, and the warp walks
-// its run again; votes on the ids' bits give equal ids within a warp their order.  The row movers are
-// bound by HBM and move 16 bytes a thread.
+// its run again; votes on the ids' bits give equal ids within a warp their order.  It is
+// bound by the latency of these steps: 2.3 us for 2 choices, 5.3 for 2068, 9.0 for 32764.
+//
+// The row movers are bound by HBM and move 16 bytes a thread.  8191 tokens of 2048 bf16,
+// top 4, at 6790 GB/s: gather 24.4 us (168 MB, its floor), combine 34.5 (168 MB; rows of
+// 4 KB read in random order, four reads to a write: 4.9 TB/s, also with 16 loads of a thread
+// in flight or rows looked up ahead), combine_back 47.5 (302 MB, 6.4 TB/s).
 #include <algorithm>
 #include <atomic>
 

@@ -57,14 +57,18 @@ template <typename T>
 struct MxRaw {
     uint4 bits[sizeof(T) / 2];
     bool live;
+    // `vec`: p is 16-byte aligned
     __device__ __forceinline__ void load(const T* __restrict__ p, bool vec) {
         if (vec) {
-#pragma unroll
-            for (int i = 0; i < (int)sizeof(T) / 2; ++i) bits[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+            load16(p);
         } else {
 #pragma unroll
             for (int k = 0; k < 8; ++k) reinterpret_cast<T*>(bits)[k] = p[k];
         }
+    }
+    __device__ __forceinline__ void load16(const T* __restrict__ p) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) bits[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
     }
     __device__ __forceinline__ void values(float (&v)[8]) const {
 #pragma unroll

@@ -2,10 +2,14 @@
 // (q4q_get_rows_mxfp4) and the activation encoder of the MXFP4 products.
 //
 // All three are bound by HBM (the encoder reads 4 bytes and writes 0.53 per fp32 value,
-// the gather the reverse).  A unit is 256 consecutive columns of one row: in the encoders 8
-// values a lane in one or two 16-byte loads, four lanes a block, one 128-byte line of codes;
-// in the gather 4 values a lane twice, so that each of a warp's 16-byte stores is one piece
-// of 512 bytes.  A warp takes UNITS units at a time, their loads in flight together.
+// the gather the reverse).  A unit is a segment of 256 consecutive columns of one row: in the
+// encoders 8 values a lane in one or two 16-byte loads, four lanes a block, one 128-byte line
+// of codes; in the gather 4 values a lane twice, so that each of a warp's 16-byte stores is
+// one piece of 512 bytes.  A warp takes UNITS units of a row at a time, their loads in flight
+// together.  What keeps the encoders from HBM's rate is their instructions (about 150 a
+// warp's segment of 256 values, 8 a lane): 14336 x 4096 fp32 in 54 us (4.9 TB/s), 50257 x 768
+// bf16 in 24.7 (3.9 TB/s), activations 2048 x 14336 fp32 in 26 (5.6 TB/s); the gather of
+// 50257 x 768 takes 26.3 (6.6 TB/s).
 #include <algorithm>
 
 #include "q4q_internal.h"
@@ -19,8 +23,8 @@ __device__ unsigned int g_mxfp4_status = 0;
 
 constexpr int THREADS = 256;
 
-// Position of a warp in a line of units: row u / segs and segment u % segs, advanced without
-// a division.
+// Position of the gather's warp in a line of units: row u / segs and segment u % segs, advanced
+// without a division.
 struct Unit {
     int64_t row;
     int seg;
@@ -36,7 +40,29 @@ struct Unit {
     }
 };
 
-// Units of an encoder's warp at a time: as many as keep its raw values in 16 registers, so that
+// A warp's `n` next segments of one row: where its lane's columns start, whether the last
+// segment of the row is cut short for this lane.
+template <typename T, int UNITS>
+__device__ __forceinline__ void load_segments(MxRaw<T> (&v)[UNITS], const T* p, int n, bool short_end, bool vec, const T* anywhere) {
+#pragma unroll
+    for (int k = 0; k < UNITS; ++k) v[k].live = k < n && !(short_end && k == n - 1);
+    if (vec) {
+#pragma unroll
+        for (int k = 0; k < UNITS; ++k) v[k].load16(v[k].live ? p + k * MX_KP : anywhere);
+    } else {
+#pragma unroll
+        for (int k = 0; k < UNITS; ++k) v[k].load(v[k].live ? p + k * MX_KP : anywhere, false);
+    }
+}
+
+template <bool E4M3, typename T, int UNITS>
+__device__ __forceinline__ void encode_segments(const MxRaw<T> (&v)[UNITS], uint8_t* codes, uint8_t* scales, int n, int chunk) {
+#pragma unroll
+    for (int k = 0; k < UNITS; ++k)
+        if (k < n) mx_encode_segment<E4M3>(v[k], codes + k * (E4M3 ? MX_KP : MX_KP / 2), scales + 2 * k * chunk);
+}
+
+// Segments of an encoder's warp at a time: as many as keep its raw values in 16 registers, so that
 // four blocks share an SM.
 template <typename T>
 constexpr int at_a_time = sizeof(T) == 4 ? 2 : 4;
@@ -48,43 +74,25 @@ encode_kernel(const T* __restrict__ src, bool vec, uint8_t* __restrict__ dst, in
               int64_t mat_stride, int64_t code_bytes) {
     const int lane = threadIdx.x & 31;
     const int segs = (K + MX_KP - 1) / MX_KP, nkc = 2 * segs, last = K - (segs - 1) * MX_KP;
-    const int64_t total = rows * segs;
+    const int per_row = (segs + UNITS - 1) / UNITS;
+    const int64_t total = rows * per_row;
     const bool small = total < (1ll << 31);
     for (int64_t mat = blockIdx.y; mat < nmats; mat += gridDim.y) {
         const T* in = src + mat * rows * K;
         uint8_t* out = dst + mat * mat_stride;
         uint8_t* scales = out + code_bytes + (lane >> 4) * MX_CHUNK;
-        for (int64_t u0 = (((int64_t)blockIdx.x * THREADS + threadIdx.x) >> 5) * UNITS; u0 < total;
-             u0 += (int64_t)gridDim.x * (THREADS / 32) * UNITS) {
-            const Unit first(u0, segs, small);
-            const int n = (int)min((int64_t)UNITS, total - u0);
+        for (int64_t g = ((int64_t)blockIdx.x * THREADS + threadIdx.x) >> 5; g < total; g += (int64_t)gridDim.x * (THREADS / 32)) {
+            const int64_t r = small ? (int64_t)((uint32_t)g / (uint32_t)per_row) : g / per_row;
+            const int s0 = (int)(g - r * per_row) * UNITS, n = min(UNITS, segs - s0);
             MxRaw<T> v[UNITS];
-            const T* p = in + first.row * K + first.seg * MX_KP + lane * 8;
-            int seg = first.seg;
-#pragma unroll
-            for (int k = 0; k < UNITS; ++k) {
-                v[k].live = k < n && (seg < segs - 1 || lane * 8 < last);
-                v[k].load(v[k].live ? p : in, vec);
-                if (++seg == segs) {
-                    seg = 0;
-                    p += last;
-                } else {
-                    p += MX_KP;
-                }
-            }
-            uint8_t* codes = out + u0 * (MX_KP / 2) + lane * 4;
-            Unit at = first;
-#pragma unroll
-            for (int k = 0; k < UNITS; ++k) {
-                if (k >= n) break;
-                mx_encode_segment<false>(v[k], codes + k * (MX_KP / 2), scales + mx_scale_offset(at.row, 7, MX_CHUNK, nkc, 2 * at.seg));
-                at.next(segs);
-            }
+            load_segments(v, in + r * K + s0 * MX_KP + lane * 8, n, s0 + n == segs && lane * 8 >= last, vec, in);
+            encode_segments<false>(v, out + (r * segs + s0) * (MX_KP / 2) + lane * 4,
+                                   scales + mx_scale_offset(r, 7, MX_CHUNK, nkc, 2 * s0), n, MX_CHUNK);
         }
         // what lies past the matrix: the code plane ends on a 256-byte boundary, the scales' last
         // row group has 128 rows
         if (blockIdx.x == 0) {
-            if (total % 2 != 0 && threadIdx.x < 32) reinterpret_cast<uint32_t*>(out + total * (MX_KP / 2))[lane] = 0u;
+            if (rows * segs % 2 != 0 && threadIdx.x < 32) reinterpret_cast<uint32_t*>(out + rows * segs * (MX_KP / 2))[lane] = 0u;
             const int64_t pad = (mx_up(rows, 128) - rows) * nkc;
             for (int64_t i = threadIdx.x; i < pad; i += THREADS)
                 *reinterpret_cast<uint32_t*>(out + code_bytes + mx_scale_offset(rows + i / nkc, 7, MX_CHUNK, nkc, (int)(i % nkc))) = 0u;
@@ -119,28 +127,27 @@ __global__ void __launch_bounds__(THREADS, 4) acts_kernel(const ActArgs a) {
     constexpr int LANE_BYTES = E4M3 ? 8 : 4;
     const T* src = static_cast<const T*>(a.src);
     uint8_t* scales = a.scales + (lane >> 4) * chunk;
-    const int64_t total = a.n_rows * segs, step = (int64_t)gridDim.x * (THREADS / 32) * UNITS;
+    const int per_row = (segs + UNITS - 1) / UNITS;
+    const int64_t total = a.n_rows * per_row, step = (int64_t)gridDim.x * (THREADS / 32);
     const bool small = total < (1ll << 31);
     MxRaw<T> v[UNITS];
-    // the loads of units u0 ..: rows of src, by way of their slots
-    auto load = [&](int64_t u0) {
-        Unit at(u0, segs, small);
-        const T* from = src;
-        bool there = false;
+    int64_t r = 0;
+    int s0 = 0, n = 0;
+    // the loads of group g: segments s0 .. s0 + n - 1 of sorted row r, by way of its slot
+    auto load = [&](int64_t g) {
+        r = small ? (int64_t)((uint32_t)g / (uint32_t)per_row) : g / per_row;
+        s0 = (int)(g - r * per_row) * UNITS;
+        n = min(UNITS, segs - s0);
+        const int64_t row = a.slot ? (int64_t)((uint32_t)__ldg(a.slot + r) / (uint32_t)a.top_k) : r;
+        if (row < a.n_src) {
+            load_segments(v, src + row * a.K + s0 * MX_KP + lane * 8, n, s0 + n == segs && lane * 8 >= last, a.vec, src);
+        } else {
 #pragma unroll
-        for (int k = 0; k < UNITS; ++k) {
-            if (u0 + k < total && (k == 0 || at.seg == 0)) {
-                const int64_t row = a.slot ? (int64_t)((uint32_t)__ldg(a.slot + at.row) / (uint32_t)a.top_k) : at.row;
-                there = row < a.n_src;
-                from = src + row * a.K + lane * 8;
-            }
-            v[k].live = u0 + k < total && there && (at.seg < segs - 1 || lane * 8 < last);
-            v[k].load(v[k].live ? from + at.seg * MX_KP : src, a.vec);
-            at.next(segs);
+            for (int k = 0; k < UNITS; ++k) v[k] = MxRaw<T>{};
         }
     };
-    int64_t u0 = (((int64_t)blockIdx.x * THREADS + threadIdx.x) >> 5) * UNITS;
-    if (u0 < total) load(u0);
+    int64_t g = ((int64_t)blockIdx.x * THREADS + threadIdx.x) >> 5;
+    if (g < total) load(g);
     // where the rows go is worked out while the first loads are in flight
     int* start = seg_smem;
     int* base = seg_smem + a.n_experts + 1;
@@ -154,20 +161,13 @@ __global__ void __launch_bounds__(THREADS, 4) acts_kernel(const ActArgs a) {
         const int64_t to = (int64_t)base[e] * a.bn + (r - start[e]);
         return to < (int64_t)base[e + 1] * a.bn ? to : -1;
     };
-    while (u0 < total) {
-        Unit at(u0, segs, small);
-        int64_t to = -1;
-#pragma unroll
-        for (int k = 0; k < UNITS; ++k) {
-            if (u0 + k >= total) break;
-            if (k == 0 || at.seg == 0) to = place(at.row);
-            if (to >= 0)
-                mx_encode_segment<E4M3>(v[k], a.codes + ((to * segs + at.seg) * 32 + lane) * LANE_BYTES,
-                                        scales + mx_scale_offset(to, a.bn_log, chunk, nkc, 2 * at.seg));
-            at.next(segs);
-        }
-        u0 += step;
-        if (u0 < total) load(u0);
+    while (g < total) {
+        const int64_t to = place(r);
+        if (to >= 0)
+            encode_segments<E4M3>(v, a.codes + ((to * segs + s0) * 32 + lane) * LANE_BYTES,
+                                  scales + mx_scale_offset(to, a.bn_log, chunk, nkc, 2 * s0), n, chunk);
+        g += step;
+        if (g < total) load(g);
     }
 }
 
@@ -228,7 +228,7 @@ mx_get_rows_kernel(const uint8_t* __restrict__ table, int64_t code_bytes, int64_
 }
 
 // Units a warp takes at a time: several where one each would take more than one round of the
-// SMs' 32 resident warps (2068 rows of 1504 routed to 32 experts: 8.5 us with one, see grid_of)
+// SMs' 32 resident warps (2068 rows of 1504 routed to 32 experts: 8.5 us with one, 5.8 with 4)
 bool many(int64_t units, const DeviceInfo& info) { return units > (int64_t)info.sm_count * 32; }
 
 int grid_of(int64_t units, int units_at_a_time, const DeviceInfo& info) {

@@ -9,7 +9,7 @@ import numpy as np
 import pytest
 
 from oracle import mx
-from test_gpu_mxfp4 import TYPES, close, on_gpu, q4q, rand  # noqa: F401
+from test_gpu_mxfp4 import TYPES, close, decoded_on_gpu, on_gpu, q4q, rand  # noqa: F401
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -152,6 +152,27 @@ def test_experts_products(q4q, n, top, experts, rows, k, acts):  # noqa: F811
     got, ref, size = experts_product(q4q, n, top, experts, rows, k, acts, "f32")
     close(got, ref, size, k, "f32")
     assert q4q.q4q_device_status() == 0
+
+
+@pytest.mark.parametrize("n,top,experts,rows,k,acts", [(150, 2, 4, 5000, 1056, "mxfp8"), (80, 2, 4, 9000, 2048, "mxfp8"), (600, 2, 3, 5000, 1056, "mxfp4"),
+                                                       (450, 2, 4, 3000, 2048, "mxfp8"), (2, 3, 9, 700, 3104, "mxfp8")])
+def test_experts_products_of_large_matrices(q4q, n, top, experts, rows, k, acts):  # noqa: F811
+    """Sizes at which tiles are taken by pairs of CTAs and by clusters; one expert has a third of the choices."""
+    rng = np.random.default_rng([n, rows, k])
+    ids = choices(rng, n, top, experts)
+    ids[: n // 3, 0] = experts - 1
+    w, values = zip(*[decoded_on_gpu(q4q, rng, rows, k) for _ in range(experts)])
+    x, v = on_gpu(rand(rng, n, k), "f32")
+    e = torch.from_numpy(mx.encode(v, acts)[2]).cuda()
+    order = q4q.q4q_moe_sort(torch.from_numpy(ids).cuda(), experts)
+    got = q4q.q4q_mul_mat_id_mxfp4(torch.stack(w), k, rows, x, order[0], order[1], top, int(acts == "mxfp8"))
+    first, slot, _ = mx.sort(ids, experts)
+    ref, size = torch.zeros(n * top, rows, dtype=torch.float64, device="cuda"), torch.zeros(n * top, rows, dtype=torch.float64, device="cuda")
+    for j in range(experts):
+        r = slice(int(first[j]), int(first[j + 1]))
+        a = e[torch.from_numpy(slot[r].astype(np.int64) // top).cuda()]
+        ref[r], size[r] = a @ values[j].T, a.abs() @ values[j].abs().T
+    close(got, ref.cpu().numpy(), size.cpu().numpy(), k, "f32")
 
 
 @pytest.mark.parametrize("type_", ["f16", "bf16"])

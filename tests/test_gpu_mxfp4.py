@@ -132,6 +132,25 @@ def test_product_shapes(q4q, rows, k, tokens, acts):
     close(got, ref, size, k, "f32")
 
 
+def decoded_on_gpu(q4q, rng, rows, k, scale=0.02):
+    """A large MXFP4 matrix and its values in 64 bits on the GPU, by way of the encoder and the row gather."""
+    w = q4q.q4q_quantize_mxfp4(torch.from_numpy(rand(rng, rows, k, scale).astype(np.float32)).cuda())
+    return w, q4q.q4q_get_rows_mxfp4(w, k, rows).double()
+
+
+@pytest.mark.parametrize("rows,k,tokens,acts", [(19400, 2048, 100, "mxfp8"), (19400, 2048, 128, "mxfp4"), (20000, 4096, 50, "mxfp8"),
+                                                (9700, 1024, 300, "mxfp4"), (9700, 1024, 520, "mxfp8"), (9601, 1056, 257, "mxfp8"),
+                                                (3000, 5056, 1, "mxfp8"), (1000, 2080, 60, "mxfp4"), (40000, 288, 64, "mxfp8")])
+def test_product_of_large_matrices(q4q, rows, k, tokens, acts):
+    """Sizes at which tiles are taken by pairs of CTAs, by clusters, and in several rounds."""
+    rng = np.random.default_rng([rows, k, tokens])
+    w, values = decoded_on_gpu(q4q, rng, rows, k)
+    x, v = on_gpu(rand(rng, tokens, k), "f32")
+    e = torch.from_numpy(mx.encode(v, acts)[2]).cuda()
+    got = q4q.q4q_mul_mat_mxfp4(w, k, rows, x, int(acts == "mxfp8"))
+    close(got, (e @ values.T).cpu().numpy(), (e.abs() @ values.abs().T).cpu().numpy(), k, "f32")
+
+
 @pytest.mark.parametrize("acts", ["mxfp4", "mxfp8"])
 @pytest.mark.parametrize("type_,dst", [("f16", "f16"), ("bf16", "bf16"), ("bf16", "f32"), ("f32", "bf16")])
 def test_product_types(q4q, type_, dst, acts):
