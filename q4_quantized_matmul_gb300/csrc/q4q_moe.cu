@@ -30,6 +30,7 @@
 #include "q4q_internal.h"
 #include "q4q_mx.cuh"
 #include "q4q_mx_internal.h"
+#include "q4q_mx_tc.cuh"
 
 namespace q4q {
 namespace {
@@ -59,6 +60,8 @@ __global__ void __launch_bounds__(SORT_THREADS)
 sort_kernel(const int32_t* __restrict__ ids, int n, int n_experts, int32_t* __restrict__ first,
             int32_t* __restrict__ slot, int32_t* __restrict__ row, int per_warp) {
     extern __shared__ int sm[];
+    pdl_trigger();                                       // what follows may start up; it waits for this kernel's end
+    pdl_wait();
     const int bins = n_experts + 1, warps = blockDim.x >> 5, bits = 32 - __clz(n_experts);
     int* hist = sm;
     int* total = hist + warps * bins;
@@ -229,6 +232,8 @@ __device__ __forceinline__ int64_t kept_rows(const Rows& g) {
 
 template <typename T, int V>
 __global__ void __launch_bounds__(THREADS) gather_kernel(const T* __restrict__ x, T* __restrict__ out, const Rows g) {
+    pdl_trigger();
+    pdl_wait();
     const int64_t kept = kept_rows(g), slots = g.n_tokens * g.top_k, total = g.n_tokens * g.per_row;
     for (int64_t i = blockIdx.x * (int64_t)THREADS + threadIdx.x; i < total; i += (int64_t)gridDim.x * THREADS) {
         const int64_t t = total < (1ll << 32) ? (int64_t)((uint32_t)i / (uint32_t)g.per_row) : i / g.per_row;
@@ -248,6 +253,8 @@ __global__ void __launch_bounds__(THREADS) gather_kernel(const T* __restrict__ x
 template <typename T, int V>
 __global__ void __launch_bounds__(THREADS)
 combine_kernel(const T* __restrict__ rows, const float* __restrict__ w, T* __restrict__ y, const Rows g) {
+    pdl_trigger();
+    pdl_wait();
     const int64_t kept = kept_rows(g), total = g.n_tokens * g.per_row;
     for (int64_t i = blockIdx.x * (int64_t)THREADS + threadIdx.x; i < total; i += (int64_t)gridDim.x * THREADS) {
         const int64_t t = total < (1ll << 32) ? (int64_t)((uint32_t)i / (uint32_t)g.per_row) : i / g.per_row;
@@ -275,6 +282,8 @@ template <typename T, int V>
 __global__ void __launch_bounds__(THREADS)
 combine_back_kernel(const T* __restrict__ dy, const T* __restrict__ rows, const float* __restrict__ w,
                     T* __restrict__ drows, float* __restrict__ dw, const Rows g) {
+    pdl_trigger();
+    pdl_wait();
     const int64_t kept = kept_rows(g), slots = g.n_tokens * g.top_k;
     const int lane = threadIdx.x & 31;
     for (int64_t s = (blockIdx.x * (int64_t)THREADS + threadIdx.x) >> 5; s < slots; s += (int64_t)gridDim.x * (THREADS / 32)) {
@@ -331,9 +340,21 @@ void launch_mover_v(Mover what, const Buffers& m, Rows g, const DeviceInfo& info
     const int grid = (int)std::max<int64_t>(1, std::min<int64_t>((items + THREADS - 1) / THREADS, (int64_t)info.sm_count * 16));
     const T *a = static_cast<const T*>(m.a), *b = static_cast<const T*>(m.b);
     T* out = static_cast<T*>(m.out);
-    if (what == GATHER) gather_kernel<T, V><<<grid, THREADS, 0, stream>>>(a, out, g);
-    else if (what == COMBINE) combine_kernel<T, V><<<grid, THREADS, 0, stream>>>(a, m.w, out, g);
-    else combine_back_kernel<T, V><<<grid, THREADS, 0, stream>>>(a, b, m.w, out, m.dw, g);
+    // programmatic dependent launch: every kernel here waits for the work before it first thing,
+    // and its own start overlaps that work's end
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(THREADS);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    // a launch that fails is left for launch_status to report
+    if (what == GATHER) (void)cudaLaunchKernelEx(&cfg, gather_kernel<T, V>, a, out, g);
+    else if (what == COMBINE) (void)cudaLaunchKernelEx(&cfg, combine_kernel<T, V>, a, m.w, out, g);
+    else (void)cudaLaunchKernelEx(&cfg, combine_back_kernel<T, V>, a, b, m.w, out, m.dw, g);
 }
 
 template <typename T>
@@ -401,13 +422,15 @@ extern "C" q4q_status q4q_moe_sort(const int32_t* ids, int64_t n_tokens, int top
     cfg.blockDim = dim3((unsigned)warps * 32);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)ctas;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)ctas;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = ctas > 1 ? 2 : 1;
     if (cudaLaunchKernelEx(&cfg, sort_kernel, ids, (int)n, n_experts, first, slot, row, per_warp) != cudaSuccess)
         return (cudaGetLastError(), Q4Q_ERR_CUDA);
     return launch_status();

@@ -15,6 +15,7 @@
 #include "q4q_internal.h"
 #include "q4q_mx.cuh"
 #include "q4q_mx_internal.h"
+#include "q4q_mx_tc.cuh"
 
 namespace q4q {
 namespace {
@@ -120,8 +121,13 @@ __global__ void __launch_bounds__(THREADS, 4) acts_kernel(const ActArgs a) {
     extern __shared__ int seg_smem[];
     __shared__ int tmp[33];
     const int lane = threadIdx.x & 31;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (a.pdl) asm volatile("griddepcontrol.wait;" ::: "memory");
+    // The kernel is always launched with programmatic dependent launch, so that its start
+    // overlaps the end of the work before it.  The product behind it may read weights at once
+    // when it starts: that is after the work before this kernel, unless the caller says that
+    // none of it writes weights (Q4Q_MUL_MAT_PDL).
+    if (a.pdl) pdl_trigger();
+    pdl_wait();
+    if (!a.pdl) pdl_trigger();
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.abort_word = 0u;
     const int segs = (a.K + MX_KP - 1) / MX_KP, nkc = 2 * segs, chunk = mx_chunk_bytes(a.bn), last = a.K - (segs - 1) * MX_KP;
     constexpr int LANE_BYTES = E4M3 ? 8 : 4;
@@ -252,7 +258,7 @@ q4q_status launch_acts_t(const ActArgs& a, cudaStream_t stream, const DeviceInfo
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = a.pdl ? 1 : 0;
+    cfg.numAttrs = 1;
     const cudaError_t e = several ? cudaLaunchKernelEx(&cfg, acts_kernel<T, E4M3, MANY>, a) : cudaLaunchKernelEx(&cfg, acts_kernel<T, E4M3, 1>, a);
     return e == cudaSuccess ? launch_status() : (cudaGetLastError(), Q4Q_ERR_CUDA);
 }
