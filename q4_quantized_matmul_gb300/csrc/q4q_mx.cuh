@@ -51,29 +51,42 @@ __device__ __forceinline__ __half mx_from_f32<__half>(float v) { return __float2
 template <>
 __device__ __forceinline__ __nv_bfloat16 mx_from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// 8 values of T as they were loaded, looked at only when they are needed; `live`: not zeros
-// (the same in the four lanes of a block).
+// What a lane of the encoders holds: 64 bytes as they were loaded, looked at only when they are
+// needed.  That is a block of a 16-bit type, half a block of fp32 (the other half in the next lane).
 template <typename T>
 struct MxRaw {
-    uint4 bits[sizeof(T) / 2];
-    bool live;
-    // `vec`: p is 16-byte aligned
-    __device__ __forceinline__ void load(const T* __restrict__ p, bool vec) {
-        if (vec) {
-            load16(p);
+    static constexpr int LANES = sizeof(T) / 2;            // lanes of a block
+    static constexpr int N = 32 / LANES;                   // values of a lane
+    uint32_t bits[16];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) bits[i] = 0u;
+    }
+    // `align`: of p, 32 or more, 16, or less.  Two 32-byte loads take each sector in one piece.
+    __device__ __forceinline__ void load(const T* __restrict__ p, int align) {
+        if (align >= 32) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t* b = bits + 8 * h;
+                asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                             : "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3]), "=r"(b[4]), "=r"(b[5]), "=r"(b[6]), "=r"(b[7])
+                             : "l"(p + 16 / LANES * h));
+            }
+        } else if (align >= 16) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
+                bits[4 * i] = v.x, bits[4 * i + 1] = v.y, bits[4 * i + 2] = v.z, bits[4 * i + 3] = v.w;
+            }
         } else {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) reinterpret_cast<T*>(bits)[k] = p[k];
+            for (int k = 0; k < N; ++k) reinterpret_cast<T*>(bits)[k] = p[k];
         }
     }
-    __device__ __forceinline__ void load16(const T* __restrict__ p) {
-#pragma unroll
-        for (int i = 0; i < (int)sizeof(T) / 2; ++i) bits[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
-    }
-    __device__ __forceinline__ void values(float (&v)[8]) const {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = mx_to_f32(reinterpret_cast<const T*>(bits)[k]);
-    }
+    // values 2i and 2i + 1
+    __device__ __forceinline__ float2 pair(int i) const;
+    // the largest magnitude, NaN if one is
+    __device__ __forceinline__ float amax() const;
 };
 
 // the largest magnitude of three, NaN if one is
@@ -83,62 +96,106 @@ __device__ __forceinline__ float max3_abs(float a, float b, float c) {
     return m;
 }
 
-// Encode 8 values a lane, four neighbouring lanes a block (the whole converged warp calls
-// it): the codes in w (8 bytes for E4M3, 4 for E2M1), the block's scale byte returned.
-template <bool E4M3>
-__device__ __forceinline__ uint32_t mx_encode8(const float (&v)[8], bool live, uint32_t (&w)[2]) {
-    constexpr int EMAX = E4M3 ? 8 : 2;
-    float m = max3_abs(v[0], v[1], v[2]);
-    m = max3_abs(m, v[3], v[4]);
-    m = max3_abs(m, v[5], v[6]);
-    m = max3_abs(m, v[7], __shfl_xor_sync(0xffffffffu, max3_abs(m, v[7], v[7]), 1));
-    m = max3_abs(m, m, __shfl_xor_sync(0xffffffffu, m, 2));
-    const int field = (int)(__float_as_uint(m) >> 23);             // 255: the block holds an infinity or a NaN
-    const bool use = live && field != 255;
-    int sf = max(field - EMAX, 0);                                 // e + 127; 0 also where amax is 0 or subnormal
-    // 2^-e = 2^(127 - sf): 127 - sf is -126 .. 127 for finite blocks
-    const float inv = __uint_as_float((uint32_t)(254 - sf) << 23);
-    float t[8];
+template <>
+__device__ __forceinline__ float2 MxRaw<float>::pair(int i) const {
+    return make_float2(__uint_as_float(bits[2 * i]), __uint_as_float(bits[2 * i + 1]));
+}
+template <>
+__device__ __forceinline__ float2 MxRaw<__half>::pair(int i) const {
+    return __half22float2(*reinterpret_cast<const __half2*>(bits + i));
+}
+template <>
+__device__ __forceinline__ float2 MxRaw<__nv_bfloat16>::pair(int i) const {
+    return make_float2(__uint_as_float(bits[i] << 16), __uint_as_float(bits[i] & 0xffff0000u));
+}
+template <>
+__device__ __forceinline__ float MxRaw<float>::amax() const {
+    float m = __uint_as_float(bits[0]);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) t[k] = __fmul_rn(v[k], inv);
+    for (int i = 1; i < 15; i += 2) m = max3_abs(m, __uint_as_float(bits[i]), __uint_as_float(bits[i + 1]));
+    return max3_abs(m, __uint_as_float(bits[15]), __shfl_xor_sync(0xffffffffu, max3_abs(m, __uint_as_float(bits[15]), 0.0f), 1));
+}
+// two at a time; the signs of the running maximum mean nothing
+template <>
+__device__ __forceinline__ float MxRaw<__half>::amax() const {
+    uint32_t m = bits[0];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) asm("max.NaN.xorsign.abs.f16x2 %0, %0, %1;" : "+r"(m) : "r"(bits[i]));
+    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&m));
+    return max3_abs(v.x, v.y, 0.0f);
+}
+template <>
+__device__ __forceinline__ float MxRaw<__nv_bfloat16>::amax() const {
+    uint32_t m = bits[0];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) asm("max.NaN.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(bits[i]));
+    return max3_abs(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u), 0.0f);
+}
+
+// Encode a lane's values (the whole converged warp calls it): the codes in w, N / 2 bytes or, for
+// E4M3, N; the block's scale byte returned.
+template <bool E4M3, typename T>
+__device__ __forceinline__ uint32_t mx_encode(const MxRaw<T>& raw, uint32_t (&w)[MxRaw<T>::N / (E4M3 ? 4 : 8)]) {
+    constexpr int EMAX = E4M3 ? 8 : 2, N = MxRaw<T>::N;
+    const int field = (int)(__float_as_uint(raw.amax()) >> 23);    // 255: the block holds an infinity or a NaN
+    const int sf = max(field - EMAX, 0);                           // e + 127; 0 also where amax is 0 or subnormal
+    // 2^-e = 2^(127 - sf): 127 - sf is -126 .. 127 for finite blocks
+    const uint32_t inv = (uint32_t)(254 - sf) << 23;
+    float2 t[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+        const float2 v = raw.pair(i);
+        asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\t"
+            "mul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+            : "=f"(t[i].x), "=f"(t[i].y) : "f"(v.x), "f"(v.y), "f"(__uint_as_float(inv)));
+    }
     if constexpr (E4M3) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < N / 4; ++h)
             asm("{\n\t.reg .b16 a, b;\n\t"
                 "cvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 b, %4, %3;\n\t"
                 "mov.b32 %0, {a, b};\n\t}"
-                : "=r"(w[h]) : "f"(t[4 * h]), "f"(t[4 * h + 1]), "f"(t[4 * h + 2]), "f"(t[4 * h + 3]));
-        w[0] = use ? w[0] : 0u;
-        w[1] = use ? w[1] : 0u;
+                : "=r"(w[h]) : "f"(t[2 * h].x), "f"(t[2 * h].y), "f"(t[2 * h + 1].x), "f"(t[2 * h + 1].y));
     } else {
-        asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-            "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
-            "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
-            "mov.b32 %0, {a, b, c, d};\n\t}"
-            : "=r"(w[0]) : "f"(t[0]), "f"(t[1]), "f"(t[2]), "f"(t[3]), "f"(t[4]), "f"(t[5]), "f"(t[6]), "f"(t[7]));
-        w[0] = use ? w[0] : 0u;
-        w[1] = 0u;
+#pragma unroll
+        for (int h = 0; h < N / 8; ++h)
+            asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+                "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+                "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+                "mov.b32 %0, {a, b, c, d};\n\t}"
+                : "=r"(w[h]) : "f"(t[4 * h].x), "f"(t[4 * h].y), "f"(t[4 * h + 1].x), "f"(t[4 * h + 1].y),
+                  "f"(t[4 * h + 2].x), "f"(t[4 * h + 2].y), "f"(t[4 * h + 3].x), "f"(t[4 * h + 3].y));
     }
-    sf = use ? sf : live ? 255 : 0;
-    return (uint32_t)sf;
+    if (field == 255)
+#pragma unroll
+        for (int h = 0; h < N / (E4M3 ? 4 : 8); ++h) w[h] = 0u;
+    return field == 255 ? 255u : (uint32_t)sf;
 }
 
-// Encode 256 consecutive columns of one row: lane l of the (converged) warp holds columns
-// 8l .. 8l+7.  Writes the lane's codes at `codes` and, from lanes 0 and 16, the four scale
-// bytes of each half of the segment at `scales`.
-template <bool E4M3, typename T>
-__device__ __forceinline__ void mx_encode_segment(const MxRaw<T>& raw, uint8_t* codes, uint8_t* scales) {
-    float v[8];
-    raw.values(v);
-    uint32_t w[2];
-    uint32_t word = mx_encode8<E4M3>(v, raw.live, w);
-    if constexpr (E4M3) *reinterpret_cast<uint2*>(codes) = make_uint2(w[0], w[1]);
-    else *reinterpret_cast<uint32_t*>(codes) = w[0];
-    // the bytes of lanes l, l+4, l+8, l+12
-    word |= __shfl_down_sync(0xffffffffu, word, 4) << 8;
-    word |= __shfl_down_sync(0xffffffffu, word, 8) << 16;
-    if ((threadIdx.x & 15) == 0) *reinterpret_cast<uint32_t*>(scales) = word;
+// 8, 16 or 32 bytes in one store
+template <int WORDS>
+__device__ __forceinline__ void mx_put(uint8_t* p, const uint32_t (&w)[WORDS]) {
+    if constexpr (WORDS == 2) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    else if constexpr (WORDS == 4) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    else
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                     "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
 }
+
+// n / d for 0 <= n < 2^31 and d >= 2 by a multiplication: with 2^(s - 1) < d <= 2^s and
+// m = ceil(2^(31 + s) / d), which is below 2^32, n m / 2^(31 + s) is at least n / d and less than
+// n / 2^(31 + s) <= 1 / d above it, too little to reach the next integer.
+struct MxDivisor {
+    uint32_t d, m, s;
+};
+inline MxDivisor mx_divisor(uint32_t d) {
+    MxDivisor v{d, 0, 0};
+    while ((1u << v.s) < d) ++v.s;
+    v.m = (uint32_t)(((1ull << (31 + v.s)) + d - 1) / d);
+    --v.s;                                                 // of the high half's shift
+    return v;
+}
+__device__ __forceinline__ uint32_t mx_divide(uint32_t n, const MxDivisor& v) { return __umulhi(n, v.m) >> v.s; }
 
 // dst[i] = v, rounded to the type
 __device__ __forceinline__ void mx_store(void* dst, int type, int64_t i, float v) {

@@ -2,14 +2,18 @@
 // (q4q_get_rows_mxfp4) and the activation encoder of the MXFP4 products.
 //
 // All three are bound by HBM (the encoder reads 4 bytes and writes 0.53 per fp32 value,
-// the gather the reverse).  A unit is a segment of 256 consecutive columns of one row: in the
-// encoders 8 values a lane in one or two 16-byte loads, four lanes a block, one 128-byte line
-// of codes; in the gather 4 values a lane twice, so that each of a warp's 16-byte stores is
-// one piece of 512 bytes.  A warp takes UNITS units of a row at a time, their loads in flight
-// together.  What keeps the encoders from HBM's rate is their instructions (about 150 a
-// warp's segment of 256 values, 8 a lane): 14336 x 4096 fp32 in 54 us (4.9 TB/s), 50257 x 768
-// bf16 in 24.7 (3.9 TB/s), activations 2048 x 14336 fp32 in 26 (5.6 TB/s); the gather of
-// 50257 x 768 takes 26.3 (6.6 TB/s).
+// the gather the reverse).
+//
+// In the encoders a lane holds 64 bytes of a row, in two loads of a 32-byte sector each: a
+// whole block of a 16-bit type, half a block of fp32.  Eight values a lane, four lanes a
+// block and two loads that are one piece for the warp, were slower, by their instructions:
+// 117 for each 256 bf16 values of which 50257 x 768 took 24.4 us; a lane's whole block has no
+// shuffles, one scale for 32 values, its maximum two values at a time, and takes 18.3 us
+// (5.4 TB/s).  14336 x 4096 fp32 take 41 us (6.4 TB/s) where they took 43.
+//
+// In the gather a unit is a segment of 256 columns of one row: 4 values a lane twice, so that
+// each of a warp's 16-byte stores is one piece of 512 bytes, a warp's 4 units in flight
+// together: 50257 x 768 in 26.3 us (6.6 TB/s).
 #include <algorithm>
 
 #include "q4q_internal.h"
@@ -23,6 +27,9 @@ namespace {
 __device__ unsigned int g_mxfp4_status = 0;
 
 constexpr int THREADS = 256;
+// Blocks of the encoders on an SM.  The activation encoder, which has its place to find as well,
+// spills with five: 512 x 4096 bf16 take a product 29.2 us with them, 28.2 with four.
+constexpr int ENCODE_BLOCKS = 5, ACTS_BLOCKS = 4;
 
 // Position of the gather's warp in a line of units: row u / segs and segment u % segs, advanced
 // without a division.
@@ -41,59 +48,53 @@ struct Unit {
     }
 };
 
-// A warp's `n` next segments of one row: where its lane's columns start, whether the last
-// segment of the row is cut short for this lane.
-template <typename T, int UNITS>
-__device__ __forceinline__ void load_segments(MxRaw<T> (&v)[UNITS], const T* p, int n, bool short_end, bool vec, const T* anywhere) {
-#pragma unroll
-    for (int k = 0; k < UNITS; ++k) v[k].live = k < n && !(short_end && k == n - 1);
-    if (vec) {
-#pragma unroll
-        for (int k = 0; k < UNITS; ++k) v[k].load16(v[k].live ? p + k * MX_KP : anywhere);
-    } else {
-#pragma unroll
-        for (int k = 0; k < UNITS; ++k) v[k].load(v[k].live ? p + k * MX_KP : anywhere, false);
-    }
-}
-
-template <bool E4M3, typename T, int UNITS>
-__device__ __forceinline__ void encode_segments(const MxRaw<T> (&v)[UNITS], uint8_t* codes, uint8_t* scales, int n, int chunk) {
-#pragma unroll
-    for (int k = 0; k < UNITS; ++k)
-        if (k < n) mx_encode_segment<E4M3>(v[k], codes + k * (E4M3 ? MX_KP : MX_KP / 2), scales + 2 * k * chunk);
-}
-
-// Segments of an encoder's warp at a time: as many as keep its raw values in 16 registers, so that
-// four blocks share an SM.
+// Where a lane's piece of a matrix of padded rows is: the blocks of a matrix in the order of its
+// code plane, LANES lanes a block.
 template <typename T>
-constexpr int at_a_time = sizeof(T) == 4 ? 2 : 4;
+struct Piece {
+    int64_t row;
+    int block;             // of the row
+    int col;               // its first column; K or more: padding
+    __device__ __forceinline__ Piece(int64_t i, const MxDivisor& blocks, bool small) {
+        const int64_t b = i / MxRaw<T>::LANES;
+        row = small ? (int64_t)mx_divide((uint32_t)b, blocks) : b / blocks.d;
+        block = (int)(b - row * blocks.d);
+        col = block * 32 + (int)(i % MxRaw<T>::LANES) * MxRaw<T>::N;
+    }
+    // whether the lane writes the block's scale byte
+    __device__ __forceinline__ bool first() const { return MxRaw<T>::LANES == 1 || col % 32 == 0; }
+};
 
 // One matrix for each blockIdx.y (and every gridDim.y-th after it).
-template <typename T, int UNITS>
-__global__ void __launch_bounds__(THREADS, 4)
-encode_kernel(const T* __restrict__ src, bool vec, uint8_t* __restrict__ dst, int K, int64_t rows, int64_t nmats,
-              int64_t mat_stride, int64_t code_bytes) {
-    const int lane = threadIdx.x & 31;
-    const int segs = (K + MX_KP - 1) / MX_KP, nkc = 2 * segs, last = K - (segs - 1) * MX_KP;
-    const int per_row = (segs + UNITS - 1) / UNITS;
-    const int64_t total = rows * per_row;
-    const bool small = total < (1ll << 31);
+template <typename T>
+__global__ void __launch_bounds__(THREADS, ENCODE_BLOCKS)
+encode_kernel(const T* __restrict__ src, int align, uint8_t* __restrict__ dst, int K, int64_t rows, int64_t nmats,
+              int64_t mat_stride, int64_t code_bytes, const MxDivisor blocks) {
+    constexpr int WORDS = MxRaw<T>::N / 8;
+    const int nkc = blocks.d / 4;
+    const int64_t total = rows * blocks.d * MxRaw<T>::LANES;
+    const bool small = rows * blocks.d < (1ll << 31);
     for (int64_t mat = blockIdx.y; mat < nmats; mat += gridDim.y) {
         const T* in = src + mat * rows * K;
         uint8_t* out = dst + mat * mat_stride;
-        uint8_t* scales = out + code_bytes + (lane >> 4) * MX_CHUNK;
-        for (int64_t g = ((int64_t)blockIdx.x * THREADS + threadIdx.x) >> 5; g < total; g += (int64_t)gridDim.x * (THREADS / 32)) {
-            const int64_t r = small ? (int64_t)((uint32_t)g / (uint32_t)per_row) : g / per_row;
-            const int s0 = (int)(g - r * per_row) * UNITS, n = min(UNITS, segs - s0);
-            MxRaw<T> v[UNITS];
-            load_segments(v, in + r * K + s0 * MX_KP + lane * 8, n, s0 + n == segs && lane * 8 >= last, vec, in);
-            encode_segments<false>(v, out + (r * segs + s0) * (MX_KP / 2) + lane * 4,
-                                   scales + mx_scale_offset(r, 7, MX_CHUNK, nkc, 2 * s0), n, MX_CHUNK);
+        // (rounded up to whole warps)
+        for (int64_t i = blockIdx.x * (int64_t)THREADS + threadIdx.x; (i & ~31ll) < total; i += (int64_t)gridDim.x * THREADS) {
+            const Piece<T> at(i, blocks, small);
+            MxRaw<T> raw;
+            if (i < total && at.col < K) raw.load(in + at.row * K + at.col, align);
+            else raw.clear();
+            uint32_t w[WORDS];
+            const uint32_t sf = mx_encode<false>(raw, w);
+            if (i < total) {
+                mx_put(out + i * (4 * WORDS), w);
+                if (at.first()) out[code_bytes + mx_scale_offset(at.row, 7, MX_CHUNK, nkc, at.block >> 2) + (at.block & 3)] = (uint8_t)sf;
+            }
         }
         // what lies past the matrix: the code plane ends on a 256-byte boundary, the scales' last
         // row group has 128 rows
         if (blockIdx.x == 0) {
-            if (rows * segs % 2 != 0 && threadIdx.x < 32) reinterpret_cast<uint32_t*>(out + rows * segs * (MX_KP / 2))[lane] = 0u;
+            if (rows * (blocks.d / 8) % 2 != 0 && threadIdx.x < 32)
+                reinterpret_cast<uint32_t*>(out + rows * blocks.d * 16)[threadIdx.x] = 0u;
             const int64_t pad = (mx_up(rows, 128) - rows) * nkc;
             for (int64_t i = threadIdx.x; i < pad; i += THREADS)
                 *reinterpret_cast<uint32_t*>(out + code_bytes + mx_scale_offset(rows + i / nkc, 7, MX_CHUNK, nkc, (int)(i % nkc))) = 0u;
@@ -112,15 +113,15 @@ struct ActArgs {
     int64_t max_groups;
     const int32_t* first;      // null: dense
     const int32_t* slot;       // null: row i of src is row i
-    int n_experts, top_k, K, bn, bn_log;
-    bool vec, pdl;
+    int n_experts, top_k, K, bn, bn_log, align;
+    MxDivisor blocks;
+    bool pdl;
 };
 
-template <typename T, bool E4M3, int UNITS>
-__global__ void __launch_bounds__(THREADS, 4) acts_kernel(const ActArgs a) {
+template <typename T, bool E4M3>
+__global__ void __launch_bounds__(THREADS, ACTS_BLOCKS) acts_kernel(const ActArgs a) {
     extern __shared__ int seg_smem[];
     __shared__ int tmp[33];
-    const int lane = threadIdx.x & 31;
     // The kernel is always launched with programmatic dependent launch, so that its start
     // overlaps the end of the work before it.  The product behind it may read weights at once
     // when it starts: that is after the work before this kernel, unless the caller says that
@@ -129,31 +130,21 @@ __global__ void __launch_bounds__(THREADS, 4) acts_kernel(const ActArgs a) {
     pdl_wait();
     if (!a.pdl) pdl_trigger();
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.abort_word = 0u;
-    const int segs = (a.K + MX_KP - 1) / MX_KP, nkc = 2 * segs, chunk = mx_chunk_bytes(a.bn), last = a.K - (segs - 1) * MX_KP;
-    constexpr int LANE_BYTES = E4M3 ? 8 : 4;
+    constexpr int WORDS = MxRaw<T>::N / (E4M3 ? 4 : 8);
     const T* src = static_cast<const T*>(a.src);
-    uint8_t* scales = a.scales + (lane >> 4) * chunk;
-    const int per_row = (segs + UNITS - 1) / UNITS;
-    const int64_t total = a.n_rows * per_row, step = (int64_t)gridDim.x * (THREADS / 32);
-    const bool small = total < (1ll << 31);
-    MxRaw<T> v[UNITS];
-    int64_t r = 0;
-    int s0 = 0, n = 0;
-    // the loads of group g: segments s0 .. s0 + n - 1 of sorted row r, by way of its slot
-    auto load = [&](int64_t g) {
-        r = small ? (int64_t)((uint32_t)g / (uint32_t)per_row) : g / per_row;
-        s0 = (int)(g - r * per_row) * UNITS;
-        n = min(UNITS, segs - s0);
-        const int64_t row = a.slot ? (int64_t)((uint32_t)__ldg(a.slot + r) / (uint32_t)a.top_k) : r;
-        if (row < a.n_src) {
-            load_segments(v, src + row * a.K + s0 * MX_KP + lane * 8, n, s0 + n == segs && lane * 8 >= last, a.vec, src);
-        } else {
-#pragma unroll
-            for (int k = 0; k < UNITS; ++k) v[k] = MxRaw<T>{};
-        }
+    const int nkc = a.blocks.d / 4, chunk = mx_chunk_bytes(a.bn);
+    const int64_t total = a.n_rows * a.blocks.d * MxRaw<T>::LANES, step = (int64_t)gridDim.x * THREADS;
+    const bool small = a.n_rows * a.blocks.d < (1ll << 31);
+    MxRaw<T> raw;
+    // the lane's piece of sorted row `row`, by way of its slot
+    auto load = [&](const Piece<T>& at, bool in) {
+        int64_t from = at.row;
+        if (in && a.slot) from = (uint32_t)__ldg(a.slot + at.row) / (uint32_t)a.top_k;
+        if (in && at.col < a.K && from < a.n_src) raw.load(src + from * a.K + at.col, a.align);
+        else raw.clear();
     };
-    int64_t g = ((int64_t)blockIdx.x * THREADS + threadIdx.x) >> 5;
-    if (g < total) load(g);
+    int64_t i = blockIdx.x * (int64_t)THREADS + threadIdx.x;
+    if ((i & ~31ll) < total) load(Piece<T>(i, a.blocks, small), i < total);
     // where the rows go is worked out while the first loads are in flight
     int* start = seg_smem;
     int* base = seg_smem + a.n_experts + 1;
@@ -167,13 +158,17 @@ __global__ void __launch_bounds__(THREADS, 4) acts_kernel(const ActArgs a) {
         const int64_t to = (int64_t)base[e] * a.bn + (r - start[e]);
         return to < (int64_t)base[e + 1] * a.bn ? to : -1;
     };
-    while (g < total) {
-        const int64_t to = place(r);
-        if (to >= 0)
-            encode_segments<E4M3>(v, a.codes + ((to * segs + s0) * 32 + lane) * LANE_BYTES,
-                                  scales + mx_scale_offset(to, a.bn_log, chunk, nkc, 2 * s0), n, chunk);
-        g += step;
-        if (g < total) load(g);
+    while ((i & ~31ll) < total) {
+        const Piece<T> at(i, a.blocks, small);
+        uint32_t w[WORDS];
+        const uint32_t sf = mx_encode<E4M3>(raw, w);
+        const int64_t to = i < total ? place(at.row) : -1;
+        if (to >= 0) {
+            mx_put(a.codes + ((to * a.blocks.d + at.block) * MxRaw<T>::LANES + i % MxRaw<T>::LANES) * (4 * WORDS), w);
+            if (at.first()) a.scales[mx_scale_offset(to, a.bn_log, chunk, nkc, at.block >> 2) + (at.block & 3)] = (uint8_t)sf;
+        }
+        i += step;
+        if ((i & ~31ll) < total) load(Piece<T>(i, a.blocks, small), i < total);
     }
 }
 
@@ -233,8 +228,8 @@ mx_get_rows_kernel(const uint8_t* __restrict__ table, int64_t code_bytes, int64_
     }
 }
 
-// Units a warp takes at a time: several where one each would take more than one round of the
-// SMs' 32 resident warps (2068 rows of 1504 routed to 32 experts: 8.5 us with one, 5.8 with 4)
+// Units a warp of the gather takes at a time: several where one each would take more than one
+// round of 32 resident warps an SM
 bool many(int64_t units, const DeviceInfo& info) { return units > (int64_t)info.sm_count * 32; }
 
 int grid_of(int64_t units, int units_at_a_time, const DeviceInfo& info) {
@@ -244,13 +239,18 @@ int grid_of(int64_t units, int units_at_a_time, const DeviceInfo& info) {
 
 constexpr int AT_A_TIME = 4;      // units of the row gather's warp
 
+// blocks of an encoder with a lane for each of `lanes` pieces: one piece a lane up to 8 rounds of
+// the SMs' blocks (1 or 2 rounds measured the same within 2%)
+int encoder_grid(int64_t lanes, int blocks, const DeviceInfo& info) {
+    return (int)std::max<int64_t>(1, std::min<int64_t>((lanes + THREADS - 1) / THREADS, (int64_t)info.sm_count * 8 * blocks));
+}
+
+int alignment(const void* p) { return aligned(p, 32) ? 32 : aligned(p, 16) ? 16 : 1; }
+
 template <typename T, bool E4M3>
 q4q_status launch_acts_t(const ActArgs& a, cudaStream_t stream, const DeviceInfo& info) {
-    constexpr int MANY = at_a_time<T>;
-    const int64_t units = a.n_rows * ((a.K + MX_KP - 1) / MX_KP);
-    const bool several = many(units, info);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid_of(units, several ? MANY : 1, info));
+    cfg.gridDim = dim3((unsigned)encoder_grid(a.n_rows * a.blocks.d * MxRaw<T>::LANES, ACTS_BLOCKS, info));
     cfg.blockDim = dim3(THREADS);
     cfg.dynamicSmemBytes = a.first ? 2 * (size_t)(a.n_experts + 1) * sizeof(int) : 0;
     cfg.stream = stream;
@@ -259,20 +259,17 @@ q4q_status launch_acts_t(const ActArgs& a, cudaStream_t stream, const DeviceInfo
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = several ? cudaLaunchKernelEx(&cfg, acts_kernel<T, E4M3, MANY>, a) : cudaLaunchKernelEx(&cfg, acts_kernel<T, E4M3, 1>, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, acts_kernel<T, E4M3>, a);
     return e == cudaSuccess ? launch_status() : (cudaGetLastError(), Q4Q_ERR_CUDA);
 }
 
 template <typename T>
 void launch_encode(const void* src, uint8_t* out, int64_t ncols, int64_t nrows, int64_t nmats, cudaStream_t stream, const DeviceInfo& info) {
-    constexpr int MANY = at_a_time<T>;
-    const int64_t units = nrows * (mx_up(ncols, MX_KP) / MX_KP);
+    const MxDivisor blocks = mx_divisor((uint32_t)(mx_up(ncols, MX_KP) / 32));
     const int64_t codes = mx_code_bytes(ncols, nrows), stride = codes + mx_scale_bytes(ncols, nrows);
-    const T* in = static_cast<const T*>(src);
-    const bool vec = aligned(src, 16), several = many(units * nmats, info);
-    const dim3 grid((unsigned)grid_of(units, several ? MANY : 1, info), (unsigned)std::min<int64_t>(nmats, 65535));
-    if (several) encode_kernel<T, MANY><<<grid, THREADS, 0, stream>>>(in, vec, out, (int)ncols, nrows, nmats, stride, codes);
-    else encode_kernel<T, 1><<<grid, THREADS, 0, stream>>>(in, vec, out, (int)ncols, nrows, nmats, stride, codes);
+    const dim3 grid((unsigned)encoder_grid(nrows * blocks.d * MxRaw<T>::LANES, ENCODE_BLOCKS, info), (unsigned)std::min<int64_t>(nmats, 65535));
+    encode_kernel<T><<<grid, THREADS, 0, stream>>>(static_cast<const T*>(src), alignment(src), out, (int)ncols, nrows, nmats, stride,
+                                                   codes, blocks);
 }
 
 }  // namespace
@@ -302,7 +299,8 @@ q4q_status mx_encode_acts(const MxActs& m, unsigned int* abort_word, uint8_t* co
     a.bn = bn;
     a.bn_log = 0;
     while ((1 << a.bn_log) < bn) ++a.bn_log;
-    a.vec = aligned(m.src, 16);
+    a.align = alignment(m.src);
+    a.blocks = mx_divisor((uint32_t)(mx_up(m.K, MX_KP) / 32));
     a.pdl = pdl;
     const bool e4m3 = m.acts == Q4Q_ACTS_MXFP8;
     switch (m.type) {
