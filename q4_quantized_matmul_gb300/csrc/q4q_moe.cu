@@ -78,7 +78,7 @@ sort_kernel(const int32_t* __restrict__ ids, int n, int n_experts, int32_t* __re
     const int64_t s0 = ((int64_t)rank * warps + warp) * per_warp;
     const int64_t s1 = min((int64_t)n, s0 + per_warp);
     auto key = [&](int64_t s) {
-        const int id = s < s1 ? __ldg(ids + s) : -1;
+        const int id = s < s1 ? mx_ld(ids + s) : -1;
         return s < s1 ? ((unsigned)id < (unsigned)n_experts ? id : n_experts) : -1;
     };
     // a run's first KEYS steps stay in registers for the second walk
@@ -199,12 +199,12 @@ struct Vec {
 template <typename T, int V>
 __device__ __forceinline__ Vec<T, V> ldv(const T* p) {
     if constexpr (V * sizeof(T) == 16) {
-        const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+        const uint4 u = mx_ld(reinterpret_cast<const uint4*>(p));
         return *reinterpret_cast<const Vec<T, V>*>(&u);
     } else {
         Vec<T, V> r;
 #pragma unroll
-        for (int i = 0; i < V; ++i) r.v[i] = p[i];
+        for (int i = 0; i < V; ++i) r.v[i] = mx_ld(p + i);
         return r;
     }
 }
@@ -227,7 +227,7 @@ struct Rows {
 
 // number of rows that belong to an expert, never more than there are
 __device__ __forceinline__ int64_t kept_rows(const Rows& g) {
-    return min((int64_t)__ldg(g.first + g.n_experts), g.n_tokens * g.top_k);
+    return min((int64_t)mx_ld(g.first + g.n_experts), g.n_tokens * g.top_k);
 }
 
 template <typename T, int V>
@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(THREADS) gather_kernel(const T* __restrict__ x
 #pragma unroll
         for (int k = 0; k < V; ++k) zero.v[k] = mx_from_f32<T>(0.0f);
         for (int j = 0; j < g.top_k; ++j) {
-            const int64_t r = __ldg(g.row + t * g.top_k + j);
+            const int64_t r = mx_ld(g.row + t * g.top_k + j);
             if (r >= 0 && r < slots) stv<T, V>(out + r * g.ne0 + c, r < kept ? v : zero);
         }
     }
@@ -263,9 +263,9 @@ combine_kernel(const T* __restrict__ rows, const float* __restrict__ w, T* __res
 #pragma unroll
         for (int k = 0; k < V; ++k) acc[k] = 0.0f;
         for (int j = 0; j < g.top_k; ++j) {
-            const int64_t r = __ldg(g.row + t * g.top_k + j);
+            const int64_t r = mx_ld(g.row + t * g.top_k + j);
             if (r < 0 || r >= kept) continue;
-            const float f = w ? __ldg(w + t * g.top_k + j) : 1.0f;
+            const float f = w ? mx_ld(w + t * g.top_k + j) : 1.0f;
             const Vec<T, V> v = ldv<T, V>(rows + r * g.ne0 + c);
 #pragma unroll
             for (int k = 0; k < V; ++k) acc[k] = __fmaf_rn(f, mx_to_f32(v.v[k]), acc[k]);
@@ -287,10 +287,10 @@ combine_back_kernel(const T* __restrict__ dy, const T* __restrict__ rows, const 
     const int64_t kept = kept_rows(g), slots = g.n_tokens * g.top_k;
     const int lane = threadIdx.x & 31;
     for (int64_t s = (blockIdx.x * (int64_t)THREADS + threadIdx.x) >> 5; s < slots; s += (int64_t)gridDim.x * (THREADS / 32)) {
-        const int64_t t = s / g.top_k, r = __ldg(g.row + s);
+        const int64_t t = s / g.top_k, r = mx_ld(g.row + s);
         if (r < 0 || r >= slots) continue;
         const bool used = r < kept;
-        const float f = used ? __ldg(w + s) : 0.0f;
+        const float f = used ? mx_ld(w + s) : 0.0f;
         float dot = 0.0f;
 #pragma unroll 4
         for (int v = lane; v < g.per_row; v += 32) {

@@ -51,6 +51,24 @@ __device__ __forceinline__ __half mx_from_f32<__half>(float v) { return __float2
 template <>
 __device__ __forceinline__ __nv_bfloat16 mx_from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
+// A load that stays behind the kernel's wait for the work before it.  (A plain load through a
+// const __restrict__ pointer, like __ldg, is of memory that nothing writes while the kernel
+// runs; the compiler may move it up past the wait, to where that does not hold yet.)
+template <typename T>
+__device__ __forceinline__ T mx_ld(const T* p) {
+    T v;
+    if constexpr (sizeof(T) == 16) {
+        uint4& u = reinterpret_cast<uint4&>(v);
+        asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(p));
+    } else if constexpr (sizeof(T) == 4) {
+        asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(reinterpret_cast<uint32_t&>(v)) : "l"(p));
+    } else {
+        static_assert(sizeof(T) == 2, "2, 4 or 16 bytes");
+        asm volatile("ld.global.nc.b16 %0, [%1];" : "=h"(reinterpret_cast<uint16_t&>(v)) : "l"(p));
+    }
+    return v;
+}
+
 // What a lane of the encoders holds: 64 bytes as they were loaded, looked at only when they are
 // needed.  That is a block of a 16-bit type, half a block of fp32 (the other half in the next lane).
 template <typename T>
@@ -63,7 +81,7 @@ struct MxRaw {
         for (int i = 0; i < 16; ++i) bits[i] = 0u;
     }
     // `align`: of p, 32 or more, 16, or less.  Two 32-byte loads take each sector in one piece.
-    __device__ __forceinline__ void load(const T* __restrict__ p, int align) {
+    __device__ __forceinline__ void load(const T* p, int align) {
         if (align >= 32) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -75,12 +93,12 @@ struct MxRaw {
         } else if (align >= 16) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
+                const uint4 v = mx_ld(reinterpret_cast<const uint4*>(p) + i);
                 bits[4 * i] = v.x, bits[4 * i + 1] = v.y, bits[4 * i + 2] = v.z, bits[4 * i + 3] = v.w;
             }
         } else {
 #pragma unroll
-            for (int k = 0; k < N; ++k) reinterpret_cast<T*>(bits)[k] = p[k];
+            for (int k = 0; k < N; ++k) reinterpret_cast<T*>(bits)[k] = mx_ld(p + k);
         }
     }
     // values 2i and 2i + 1
@@ -222,7 +240,7 @@ __device__ __forceinline__ void mx_segments(const int32_t* __restrict__ first, i
     const int per = (n_experts + (int)blockDim.x - 1) / (int)blockDim.x;
     const int e0 = threadIdx.x * per, e1 = min(e0 + per, n_experts);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    auto at = [&](int e) { return (int)min(max((int64_t)__ldg(first + e), (int64_t)0), n_rows); };
+    auto at = [&](int e) { return (int)min(max((int64_t)mx_ld(first + e), (int64_t)0), n_rows); };
     int sum = 0;
     for (int e = e0; e < e1; ++e) sum += (max(at(e + 1) - at(e), 0) + bn - 1) / bn;
     int inc = sum;

@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(THREADS, ACTS_BLOCKS) acts_kernel(const ActArg
     // the lane's piece of sorted row `row`, by way of its slot
     auto load = [&](const Piece<T>& at, bool in) {
         int64_t from = at.row;
-        if (in && a.slot) from = (uint32_t)__ldg(a.slot + at.row) / (uint32_t)a.top_k;
+        if (in && a.slot) from = (uint32_t)mx_ld(a.slot + at.row) / (uint32_t)a.top_k;
         if (in && at.col < a.K && from < a.n_src) raw.load(src + from * a.K + at.col, a.align);
         else raw.clear();
     };

@@ -92,6 +92,36 @@ def test_encoder_takes_unaligned_rows_and_several_matrices(q4q):
         assert np.array_equal(w[m], mx.pack(v.reshape(3, 70, 160)[m])[0])
 
 
+def at_offset(t, offset):
+    """t in memory that starts `offset` elements behind a 256-byte boundary."""
+    buf = torch.empty(t.numel() + offset, dtype=t.dtype, device="cuda")[offset:]
+    return buf.copy_(t.reshape(-1)).view(t.shape)
+
+
+@pytest.mark.parametrize("type_,offset", [("f32", 1), ("f32", 4), ("f32", 8), ("f16", 3), ("f16", 8), ("f16", 16), ("bf16", 1), ("bf16", 8), ("bf16", 16)])
+def test_encoders_of_rows_at_any_offset(q4q, type_, offset):
+    x, v = on_gpu(special_rows() if type_ == "f32" else rand(np.random.default_rng(5), 21, 64), type_)
+    assert np.array_equal(q4q.q4q_quantize_mxfp4(at_offset(x, offset)).cpu().numpy(), mx.pack(v)[0])
+    rng = np.random.default_rng([6, offset])
+    w = torch.from_numpy(mx.pack(rand(rng, 200, 352, 0.02).astype(np.float32))[0]).cuda()
+    x = on_gpu(rand(rng, 11, 352), type_)[0]
+    for acts in (0, 1):
+        assert torch.equal(q4q.q4q_mul_mat_mxfp4(w, 352, 200, at_offset(x, offset), acts), q4q.q4q_mul_mat_mxfp4(w, 352, 200, x, acts))
+
+
+@pytest.mark.parametrize("type_", ["f16", "bf16"])
+def test_encoder_infinities_and_nan_of_16_bit_types(q4q, type_):
+    """Wherever in a block they stand, with either sign."""
+    x = rand(np.random.default_rng(7), 128, 64)
+    for r in range(128):
+        x[r, r % 64] = [np.inf, -np.inf, np.nan][r % 3]
+    x, v = on_gpu(x, type_)
+    packed, values = mx.pack(v)
+    w = q4q.q4q_quantize_mxfp4(x)
+    assert np.array_equal(w.cpu().numpy(), packed)
+    assert np.array_equal(np.isnan(q4q.q4q_get_rows_mxfp4(w, 64, 128).cpu().numpy()), np.isnan(values))
+
+
 def test_row_gather_ids(q4q):
     x, v = on_gpu(rand(np.random.default_rng(4), 300, 288), "bf16")
     values = mx.pack(v)[1].astype(np.float32)
