@@ -27,8 +27,9 @@
 //   a pair of CTAs a tile of 256 rows x 64 to 256 tokens: each loads its 128 rows and half
 //     of the tokens, the first issues the pair's MMAs (cta_group::2), which halves what the
 //     token side costs in copies;
-//   few tiles: a cluster of 2 to 8 CTAs shares the K of a tile of 8 to 64 tokens and joins
-//     the parts over distributed shared memory in the order of K.
+//   few tiles: a cluster of 2 to 8 CTAs shares the K of a tile of 8 to 64 tokens; each sends
+//     its part of a token over distributed shared memory to the CTA that adds the token up, in
+//     the order of K (fetching the parts instead: 4096 x 4096, 1 token, 7.85 us, sent 7.45).
 //
 // What bounds it: a CTA's copies take 1.05 ns a shared-memory row (128 bytes, two cycles),
 // so an atom of 128 + 16 rows 0.165 us and of a pair's 128 + 128 rows 0.28; its MMAs 0.14 us
@@ -243,6 +244,7 @@ mxmm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ 
     walk.pos = blockIdx.x / (unsigned)(CG * p.split);
     walk.step = gridDim.x / (unsigned)(CG * p.split);
     const Walk all = walk;
+    bool pushed = false;
 
     if (warp == 0) {
         // ---------------- producer
@@ -403,7 +405,7 @@ mxmm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ 
                 else mbar_arrive(freed + 8 * buf);
             }
             const int valid = f.valid - col0;
-            if (p.split == 1) {
+            if (CG == 2 || p.split == 1) {
                 const int64_t at = (f.dst_row + col0) * p.M + m;
                 if (m < p.M) {
                     if (p.dst_type == Q4Q_TYPE_F32) store_columns<float, CW>(p.dst, at, p.M, r, valid);
@@ -411,10 +413,19 @@ mxmm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ 
                     else store_columns<__nv_bfloat16, CW>(p.dst, at, p.M, r, valid);
                 }
             } else {
-                // every stage has been read: the CTA's part of its one tile, [token][row], takes their place
-                float* part = reinterpret_cast<float*>(smem) + col0 * BM + row;
+                // The CTA's part of its one tile goes to those that add it up: token t to CTA t % split,
+                // where [part][t / split][row] takes the place of stages, once all CTAs have read theirs.
+                cluster_arrive();
+                cluster_wait();
+                pushed = true;
+                const uint32_t mask = (uint32_t)p.split - 1u, log = 31 - __clz(p.split);
+                const uint32_t part = sbase + 4 * row + ((uint32_t)walk.part * (BN >> log)) * (4 * BM);
 #pragma unroll
-                for (int c = 0; c < CW; ++c) part[c * BM] = __uint_as_float(r[c]);
+                for (int c = 0; c < CW; ++c) {
+                    const uint32_t t = col0 + c;
+                    if (c < valid)
+                        asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(mapa_shared(part + (t >> log) * (4 * BM), t & mask)), "r"(r[c]) : "memory");
+                }
             }
             ++n;
         }
@@ -428,22 +439,24 @@ mxmm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ 
 
     tc_fence_before();
     if (CG == 1 && p.split > 1) {
-        // CTA z adds the z-th share of the tile's values, over the CTAs in the order of K
         __syncwarp();
+        if (!pushed) {
+            cluster_arrive();
+            cluster_wait();
+        }
         cluster_arrive();
         cluster_wait();
         Walk w = all;
         Frag f;
         if (next_frag<BN, CG>(w, p, start, units, f)) {
-            // four rows of a token a thread; all parts' loads in flight together
-#pragma unroll 2
-            for (int u = all.part * THREADS + (int)threadIdx.x; u < f.valid * (BM / 4); u += p.split * THREADS) {
+            // four rows of a token a thread, the parts in the order of K
+            const int log = 31 - __clz(p.split), tokens = (f.valid - all.part + p.split - 1) >> log;
+            for (int u = threadIdx.x; u < tokens * (BM / 4); u += THREADS) {
+                const float4* part = reinterpret_cast<const float4*>(smem) + u;
                 float4 v[MAX_SPLIT];
 #pragma unroll
                 for (int z = 0; z < MAX_SPLIT; ++z)
-                    if (z < p.split)
-                        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                                     : "=f"(v[z].x), "=f"(v[z].y), "=f"(v[z].z), "=f"(v[z].w) : "r"(mapa_shared(sbase + 16 * u, z)) : "memory");
+                    if (z < p.split) v[z] = part[z * (BN >> log) * (BM / 4)];
                 float sum[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
 #pragma unroll
                 for (int z = 1; z < MAX_SPLIT; ++z)
@@ -454,13 +467,12 @@ mxmm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ 
                         sum[3] = __fadd_rn(sum[3], v[z].w);
                     }
                 const int m = f.m0 + u % (BM / 4) * 4;
+                const int64_t token = f.dst_row + (u / (BM / 4) << log) + all.part;
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    if (m + k < p.M) mx_store(p.dst, p.dst_type, (f.dst_row + u / (BM / 4)) * p.M + m + k, sum[k]);
+                    if (m + k < p.M) mx_store(p.dst, p.dst_type, token * p.M + m + k, sum[k]);
             }
         }
-        cluster_arrive();                                        // no CTA leaves while another may still read its part
-        cluster_wait();
     }
     __syncthreads();
     if constexpr (CG == 2) {                                     // neither CTA leaves while the other uses its memory
