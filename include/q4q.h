@@ -451,7 +451,7 @@ Q4Q_API q4q_status q4q_mxfp4_size(int64_t ne00, int64_t ne01, size_t* bytes);
  *   e = max(floor(log2(amax)) - 2, -127)  (-127 when amax == 0),
  *   code = E2M1(x * 2^-e) to nearest, ties to the even code, magnitudes above 6 to 6.
  * A block that holds an infinity or a NaN gets scale byte 255 and codes 0.
- * src: device, src_type [nmats][nrows][ncols] contiguous, aligned to its type (16-byte
+ * src: device, src_type [nmats][nrows][ncols] contiguous, aligned to its type (32-byte
  * aligned is faster); dst: device, 256-byte aligned, matrix m at m * q4q_mxfp4_size.
  * Every byte of dst is written.  nrows * ncols * nmats < 2^40. */
 Q4Q_API q4q_status q4q_quantize_mxfp4(const void* src, int src_type, void* dst, int64_t ncols, int64_t nrows,

@@ -9,7 +9,8 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
@@ -122,15 +123,32 @@ class Place {
     }
     c10::DeviceIndex device() const { return device_; }
     q4q_stream_t stream() const { return reinterpret_cast<q4q_stream_t>(stream_); }
-    // A tensor of the call's own; where the call runs on another stream than the current, the
-    // allocator keeps its memory from other users until that stream is past the call.
+    // A tensor of the call's own.  Where the call runs on another stream than the current, its
+    // memory is that stream's (of the current stream's free memory, work in flight there may still
+    // be reading), and is kept from its next user until the current stream, where the tensor may
+    // be used next, is past that use.
     at::Tensor make(at::IntArrayRef shape, at::ScalarType type) const {
-        at::Tensor t = at::empty(shape, at::TensorOptions().dtype(type).device(at::Device(at::kCUDA, device_)));
-        if (other_ && t.numel() > 0) t.record_stream(c10::cuda::getStreamFromExternal(stream_, device_).unwrap());
+        if (!other_) return empty(shape, type);
+        const c10::cuda::CUDAStream current = c10::cuda::getCurrentCUDAStream(device_);
+        const c10::cuda::CUDAStreamGuard its(c10::cuda::getStreamFromExternal(stream_, device_));
+        at::Tensor t = empty(shape, type);
+        if (t.numel() > 0) t.record_stream(current.unwrap());
         return t;
+    }
+    // Memory of the call's stream for the length of the call: what is freed is used next by work
+    // that is queued behind the call's.
+    c10::DataPtr scratch(size_t n) const {
+        if (!other_) return c10::cuda::CUDACachingAllocator::get()->allocate(n);
+        const c10::cuda::CUDAStreamGuard its(c10::cuda::getStreamFromExternal(stream_, device_));
+        return c10::cuda::CUDACachingAllocator::get()->allocate(n);
     }
 
    private:
+    // what at::empty comes to, without its way through the dispatcher (1.2 us on the host of a GB300,
+    // about as long as a launch)
+    at::Tensor empty(at::IntArrayRef shape, at::ScalarType type) const {
+        return at::Tensor(at::detail::empty_cuda(shape, type, at::Device(at::kCUDA, device_), std::nullopt));
+    }
     c10::DeviceIndex device_ = 0;
     cudaStream_t stream_ = nullptr;
     bool other_ = false;
@@ -212,7 +230,11 @@ PyObject* get_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
-at::Tensor rows_2d(const at::Tensor& x) { return x.dim() == 2 ? x : x.reshape({-1, x.size(-1)}); }
+// the rows of x, which a view holds: a copy would be made on the current stream, not the call's
+at::Tensor rows_2d(const at::Tensor& x) {
+    if (!x.is_contiguous()) raise(PyExc_ValueError, "src1 must be contiguous");
+    return x.dim() == 2 ? x : x.view({-1, x.size(-1)});
+}
 
 at::ScalarType output_type(PyObject* dtype, const at::Tensor& like) {
     if (dtype == Py_None) return like.scalar_type();
@@ -221,16 +243,16 @@ at::ScalarType output_type(PyObject* dtype, const at::Tensor& like) {
 }
 
 // a workspace of `need` bytes, or the one given: its address and size
-void* workspace_of(PyObject* o, size_t need, const Place& at, at::Tensor& hold, size_t& size) {
-    size = 0;
+void* workspace_of(PyObject* o, size_t need, const Place& at, c10::DataPtr& hold, size_t& size) {
+    size = need;
     if (o == Py_None) {
         if (need == 0) return nullptr;
-        hold = at.make({(int64_t)need}, at::kByte);
-    } else {
-        hold = tensor(o, "workspace");
+        hold = at.scratch(need);
+        return hold.get();
     }
-    size = (size_t)(hold.numel() * hold.element_size());
-    return bytes(hold, "workspace", 0, at.device());
+    const at::Tensor& given = tensor(o, "workspace");
+    size = (size_t)(given.numel() * given.element_size());
+    return bytes(given, "workspace", 0, at.device());
 }
 
 // mul_mat_mxfp4(src0, ne00, ne01, src1, acts, dst, dst_dtype, workspace, stream, flags)
@@ -247,7 +269,7 @@ PyObject* mul_mat(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::Tensor dst = given(a[5], "dst", at, {ne11, ne01}, output_type(a[6], x));
         if (ne01 * ne11 == 0) return wrap(dst);
         size_t need_bytes = 0, size = 0;
-        at::Tensor hold;
+        c10::DataPtr hold;
         if (a[7] == Py_None)
             check("q4q_mul_mat_mxfp4_workspace_size", q4q_mul_mat_mxfp4_workspace_size(ne00, ne01, ne11, acts, &need_bytes));
         void* ws = workspace_of(a[7], need_bytes, at, hold, size);
@@ -403,7 +425,7 @@ PyObject* mul_mat_id(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::Tensor dst = given(a[8], "dst", at, {n_rows, ne01}, output_type(a[9], x));
         if (ne01 * n_rows == 0) return wrap(dst);
         size_t need_bytes = 0, size = 0;
-        at::Tensor hold;
+        c10::DataPtr hold;
         if (a[10] == Py_None)
             check("q4q_mul_mat_id_mxfp4_workspace_size", q4q_mul_mat_id_mxfp4_workspace_size(ne00, ne01, n_src1, n_rows, experts, acts, &need_bytes));
         void* ws = workspace_of(a[10], need_bytes, at, hold, size);

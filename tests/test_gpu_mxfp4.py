@@ -255,6 +255,26 @@ def test_product_on_another_stream_and_chained(q4q):
     assert torch.equal(y, z)
 
 
+def test_results_on_another_stream_take_no_memory_of_this_one(q4q):
+    """A tensor freed here may still be read by work in flight here."""
+    rng = np.random.default_rng(14)
+    wd = torch.from_numpy(mx.pack(rand(rng, 5000, 256, 0.05).astype(np.float32))[0]).cuda()
+    x = on_gpu(rand(rng, 1000, 256), "f32")[0]
+    ref = q4q.q4q_mul_mat_mxfp4(wd, 256, 5000, x)
+    old = torch.empty_like(ref)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    at, size = old.data_ptr(), old.numel() * 4
+    del old
+    got = q4q.q4q_mul_mat_mxfp4(wd, 256, 5000, x, stream=side)
+    assert got.data_ptr() + size <= at or at + size <= got.data_ptr()
+    side.synchronize()
+    assert torch.equal(got, ref)
+    with pytest.raises(ValueError):                           # nor a copy made here
+        q4q.q4q_mul_mat_mxfp4(wd, 256, 5000, x.view(2, 500, 256)[:, ::2], stream=side)
+    assert torch.equal(q4q.q4q_mul_mat_mxfp4(wd, 256, 5000, x.view(2, 500, 256)), ref)
+
+
 def test_product_in_a_graph(q4q):
     rng = np.random.default_rng(12)
     packed, w = mx.pack(rand(rng, 500, 1024, 0.05).astype(np.float32))
