@@ -101,7 +101,8 @@ def q4q_debug_mul_mat_mxfp4_timeout(src0: torch.Tensor, ne00: int, ne01: int, sr
 
 def q4q_moe_sort(ids: torch.Tensor, n_experts: int, first: Optional[torch.Tensor] = None, slot: Optional[torch.Tensor] = None,
                  row: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
-    """Sort the choices ids int32 [tokens, top_k] by expert: (first [n_experts + 1], slot, row [tokens * top_k])."""
+    """Sort the choices ids int32 [tokens, top_k] by expert: (first [n_experts + 1], slot, row [tokens * top_k]),
+    in one storage where none of them is given."""
     return _ext.moe_sort(ids, n_experts, first, slot, row, stream)
 
 
