@@ -62,8 +62,12 @@ __device__ __forceinline__ T mx_ld(const T* p) {
         asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(p));
     } else if constexpr (sizeof(T) == 4) {
         asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(reinterpret_cast<uint32_t&>(v)) : "l"(p));
+    } else if constexpr (sizeof(T) == 1) {
+        uint32_t byte;
+        asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(byte) : "l"(p));
+        v = (T)byte;
     } else {
-        static_assert(sizeof(T) == 2, "2, 4 or 16 bytes");
+        static_assert(sizeof(T) == 2, "1, 2, 4 or 16 bytes");
         asm volatile("ld.global.nc.b16 %0, [%1];" : "=h"(reinterpret_cast<uint16_t&>(v)) : "l"(p));
     }
     return v;

@@ -33,7 +33,10 @@
 //
 // What bounds it: a CTA's copies take 1.05 ns a shared-memory row (128 bytes, two cycles),
 // so an atom of 128 + 16 rows 0.165 us and of a pair's 128 + 128 rows 0.28; its MMAs 0.14 us
-// up to 128 tokens, 0.27 with 256.
+// up to 128 tokens, 0.27 with 256.  In the widest tiles the ring's 6 stages (34 KB each, all that
+// shared memory holds) also have no more than 1.6 us to arrive in: two pairs that shared their tokens
+// by multicast, a quarter less from L2, took the same time (2048 tokens 14336 x 4096: 51.0 us, 51.2),
+// as did tiles with fewer tokens than 256 and MMAs and copies of only so many.
 //
 // Every mbarrier wait is bounded; one that runs out records Q4Q_ERR_TIMEOUT, raises the
 // call's abort word (zeroed by the activation encoder before every launch) and the CTA
