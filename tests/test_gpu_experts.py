@@ -212,3 +212,39 @@ def test_the_example_runs(q4q):  # noqa: F811
     blocks that saturate at 448 and the bf16 roundings between the steps add under 0.02."""
     from examples import moe_ffn_mxfp4
     assert moe_ffn_mxfp4.main(tokens=33, hidden=256, ff=512, experts=8, top=2) < 0.132
+
+
+def test_rows_whose_offsets_pass_32_bits(q4q):  # noqa: F811
+    """540,000 sorted rows of 4096: 2.2e9 values.  Halves and doubles of fp16 normals are exact."""
+    n, top, ne0 = 270000, 2, 4096
+    g = torch.Generator(device="cuda").manual_seed(16)
+    x = torch.randint(1, 1000, (n, ne0), generator=g, device="cuda", dtype=torch.int16).half()
+    ids = torch.stack([torch.randint(0, 4, (n,), generator=g, device="cuda"), torch.randint(4, 7, (n,), generator=g, device="cuda")], 1).int()
+    first, slot, row = q4q.q4q_moe_sort(ids, 7)
+    rows = q4q.q4q_moe_gather(x, first, row, top)
+    tail = slot[-1000:].long() // top
+    assert torch.equal(rows[-1000:], x[tail])
+    w = torch.full((n, top), 0.5, device="cuda")
+    assert torch.equal(q4q.q4q_moe_combine(rows, first, row, w), x)
+    assert torch.equal(q4q.q4q_moe_gather_back(rows, first, row, top), x * 2)
+    drows, dw = q4q.q4q_moe_combine_back(x, rows, first, row, w)
+    assert torch.equal(drows[-1000:], x[tail] / 2)
+    square = (x[-1000:].double() ** 2).sum(1)
+    assert ((dw[-1000:].double() - square[:, None]).abs() <= (ne0 + 1) * 2.0 ** -24 * square[:, None]).all()
+
+
+def test_experts_outputs_whose_offsets_pass_32_bits(q4q):  # noqa: F811
+    """40,000 rows of 60,000 outputs: 2.4e9."""
+    n, top, experts, rows, k = 20000, 2, 3, 60000, 32
+    rng = np.random.default_rng(17)
+    w, values = zip(*(decoded_on_gpu(q4q, rng, rows, k, 0.05) for _ in range(experts)))
+    x, v = on_gpu(rand(rng, n, k), "bf16")
+    ids = choices(rng, n, top, experts, drop=0.0)
+    first, slot, _ = q4q.q4q_moe_sort(torch.from_numpy(ids).cuda(), experts)
+    y = q4q.q4q_mul_mat_id_mxfp4(torch.stack(w), k, rows, x, first, slot, top)
+    at = slot[-300:].long() // top                            # of the last expert
+    assert int(first[experts - 1]) <= n * top - 300
+    e = mx.encode(v, "mxfp8")[2][at.cpu().numpy()]
+    m = values[experts - 1].cpu().numpy()
+    close(y[-300:], e @ m.T, np.abs(e) @ np.abs(m).T, k, "bf16")
+    assert q4q.q4q_device_status() == 0

@@ -302,3 +302,24 @@ def test_product_wait_that_runs_out(q4q):
             assert q4q.q4q_device_status() == 6
             a = q4q.q4q_mul_mat_mxfp4(wd, 4096, 300, x, acts)
             assert q4q.q4q_device_status() == 0 and torch.isfinite(a).all()
+
+
+def test_matrix_whose_offsets_pass_32_bits(q4q):
+    """1,100,000 rows of 4096: 9 GB of bf16, 2.2 GB of codes; what stands in its last rows comes out there."""
+    rows, k, last = 1100000, 4096, 200
+    rng = np.random.default_rng(15)
+    x = torch.zeros(rows, k, dtype=torch.bfloat16, device="cuda")
+    tail, v = on_gpu(rand(rng, last, k, 0.02), "bf16")
+    x[-last:] = tail
+    w = q4q.q4q_quantize_mxfp4(x)
+    del x, tail
+    values = mx.pack(v)[1]
+    n = 270000                                                # 4.4 GB of fp32
+    got = q4q.q4q_get_rows_mxfp4(w, k, rows, torch.arange(rows - n, rows, dtype=torch.int32, device="cuda"))
+    assert np.array_equal(got[-last:].cpu().numpy(), values.astype(np.float32)) and not got[:-last].any()
+    del got
+    t, u = on_gpu(rand(rng, 2, k), "f32")
+    e = mx.encode(u, "mxfp8")[2]
+    y = q4q.q4q_mul_mat_mxfp4(w, k, rows, t)
+    close(y[:, -last:], e @ values.T, np.abs(e) @ np.abs(values).T, k, "f32")
+    assert not y[:, :-last].any() and q4q.q4q_device_status() == 0
