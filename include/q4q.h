@@ -475,8 +475,9 @@ Q4Q_API q4q_status q4q_mul_mat_mxfp4_workspace_size(int64_t ne00, int64_t ne01, 
  * the outputs it takes part in NaN.
  * src0: device, 256-byte aligned MXFP4 matrix; src1: device, src1_type [ne11][ne10],
  * dst: device, dst_type [ne11][ne01], each aligned to its type; workspace: 256-byte
- * aligned, q4q_mul_mat_mxfp4_workspace_size bytes.  flags as q4q_mul_mat_ex (honoured by
- * the kernel that encodes src1).  The result depends on the operands and the device alone
+ * aligned, q4q_mul_mat_mxfp4_workspace_size bytes.  Q4Q_MUL_MAT_PDL as for
+ * q4q_mul_mat_ex: src0 may be read before the work queued ahead of the call completes
+ * (src1 and dst never are).  The result depends on the operands and the device alone
  * (sums shared by several CTAs are joined in the order of K).  Limits: 0 <= ne11 < 2^20;
  * an unknown acts or type: Q4Q_ERR_ARG. */
 Q4Q_API q4q_status q4q_mul_mat_mxfp4(const void* src0, int64_t ne00, int64_t ne01, const void* src1, int src1_type,

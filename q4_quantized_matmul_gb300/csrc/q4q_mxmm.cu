@@ -520,10 +520,10 @@ int64_t clusters_held(int split, int sm_count) { return split == 8 ? sm_count / 
 
 // The form that is expected to take least.  Times in ns, fitted to 4096 x 1024, 4096 x 4096,
 // 4096 x 14336 and 14336 x 4096 at 8 to 1024 tokens in every form (within a tenth): a form's start
-// and end, its time for an atom of E4M3 and of E2M1 activations, 2400 (64 tokens: 3200) to join a
+// and end, its time for an atom of E4M3 and of E2M1 activations, 2050 (64 tokens: 2850) to join a
 // tile's parts, 600 for each further round of tiles, and what HBM needs at 6500 bytes a ns behind
 // a start of 4400.  For example 14336 x 4096, 8 tokens, E4M3: 20.3 us whole, 15.4 and 12.1 in 2 and
-// 4 parts; 4096 x 4096, E2M1: 6.9 whole, 8.8 and 8.1 in 2 and 4; 14336 x 4096, 128 tokens, E4M3:
+// 4 parts; 1024 x 4096, 1 token, E2M1: 6.3 whole, 5.6 in 8; 14336 x 4096, 128 tokens, E4M3:
 // tiles of 64 tokens 23.5 whole, 18.6 in 2 parts, 20.5 by pairs, tiles of 128 by pairs 27.8.
 void pick_tile(Plan& q, int64_t K, int64_t M, int64_t n_rows, int64_t n_tokens, int n_experts, int acts, int sm_count) {
     const int64_t expect = expected_rows(n_rows, n_tokens, n_experts);
@@ -542,7 +542,7 @@ void pick_tile(Plan& q, int64_t K, int64_t M, int64_t n_rows, int64_t n_tokens, 
         const int64_t workers = sm_count / f.cg, rounds = (tiles + workers - 1) / workers;
         for (int split = 1; split <= (f.cg == 1 ? MAX_SPLIT : 1); split *= 2) {
             if (split > 1 && (tiles > clusters_held(split, sm_count) || atoms < 2 * split)) break;
-            const double work = split > 1 ? f.start + (f.bn == 64 ? 3200 : 2400) + atom * ((atoms + split - 1) / split)
+            const double work = split > 1 ? f.start + (f.bn == 64 ? 2850 : 2050) + atom * ((atoms + split - 1) / split)
                                           : f.start + atom * rounds * atoms + 600 * (rounds - 1);
             const double cost = std::max(work, hbm) + 0.01 * f.bn;
             if (cost < least) {

@@ -323,3 +323,10 @@ def test_matrix_whose_offsets_pass_32_bits(q4q):
     y = q4q.q4q_mul_mat_mxfp4(w, k, rows, t)
     close(y[:, -last:], e @ values.T, np.abs(e) @ np.abs(values).T, k, "f32")
     assert not y[:, :-last].any() and q4q.q4q_device_status() == 0
+
+
+@pytest.mark.parametrize("acts", ["mxfp4", "mxfp8"])
+@pytest.mark.parametrize("rows,k,tokens", [(100, 4096, 12), (100, 4096, 30), (4500, 4096, 16), (4500, 4096, 25), (800, 20992, 660)])
+def test_product_of_long_rows(q4q, rows, k, tokens, acts):
+    """Sizes at which clusters share the K of tiles of 16 and 32 tokens, and pairs take tiles of 64."""
+    test_product_of_large_matrices(q4q, rows, k, tokens, acts)
