@@ -57,8 +57,8 @@ __device__ __forceinline__ uint32_t same_key(int k, int bits) {
 }
 
 __global__ void __launch_bounds__(SORT_THREADS)
-sort_kernel(const int32_t* __restrict__ ids, int n, int n_experts, int32_t* __restrict__ first,
-            int32_t* __restrict__ slot, int32_t* __restrict__ row, int per_warp) {
+sort_kernel(const int32_t* ids, int n, int n_experts, int32_t* first,
+            int32_t* slot, int32_t* row, int per_warp) {
     extern __shared__ int sm[];
     pdl_trigger();                                       // what follows may start up; it waits for this kernel's end
     pdl_wait();
@@ -231,7 +231,7 @@ __device__ __forceinline__ int64_t kept_rows(const Rows& g) {
 }
 
 template <typename T, int V>
-__global__ void __launch_bounds__(THREADS) gather_kernel(const T* __restrict__ x, T* __restrict__ out, const Rows g) {
+__global__ void __launch_bounds__(THREADS) gather_kernel(const T* x, T* out, const Rows g) {
     pdl_trigger();
     pdl_wait();
     const int64_t kept = kept_rows(g), slots = g.n_tokens * g.top_k, total = g.n_tokens * g.per_row;
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(THREADS) gather_kernel(const T* __restrict__ x
 // y[t] = sum_j w * rows[row]; without weights the gradient of the gather
 template <typename T, int V>
 __global__ void __launch_bounds__(THREADS)
-combine_kernel(const T* __restrict__ rows, const float* __restrict__ w, T* __restrict__ y, const Rows g) {
+combine_kernel(const T* rows, const float* w, T* y, const Rows g) {
     pdl_trigger();
     pdl_wait();
     const int64_t kept = kept_rows(g), total = g.n_tokens * g.per_row;
@@ -280,8 +280,8 @@ combine_kernel(const T* __restrict__ rows, const float* __restrict__ w, T* __res
 // a warp per slot: drows and the dot product for dw
 template <typename T, int V>
 __global__ void __launch_bounds__(THREADS)
-combine_back_kernel(const T* __restrict__ dy, const T* __restrict__ rows, const float* __restrict__ w,
-                    T* __restrict__ drows, float* __restrict__ dw, const Rows g) {
+combine_back_kernel(const T* dy, const T* rows, const float* w,
+                    T* drows, float* dw, const Rows g) {
     pdl_trigger();
     pdl_wait();
     const int64_t kept = kept_rows(g), slots = g.n_tokens * g.top_k;

@@ -51,24 +51,26 @@ __device__ __forceinline__ __half mx_from_f32<__half>(float v) { return __float2
 template <>
 __device__ __forceinline__ __nv_bfloat16 mx_from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// A load that stays behind the kernel's wait for the work before it.  (A plain load through a
-// const __restrict__ pointer, like __ldg, is of memory that nothing writes while the kernel
-// runs; the compiler may move it up past the wait, to where that does not hold yet.)
+// A load of what the work before this kernel may have written, for kernels that start before that
+// work ends and wait for it (griddepcontrol.wait).  It is a plain ld.global: the non-coherent form
+// (ld.global.nc, which is also what __ldg and reads through const __restrict__ pointers become) is
+// for memory that nothing writes while the kernel runs, and may be served by, or moved up to, a time
+// before the wait.  volatile: it stays behind the wait in the program's order.
 template <typename T>
 __device__ __forceinline__ T mx_ld(const T* p) {
     T v;
     if constexpr (sizeof(T) == 16) {
         uint4& u = reinterpret_cast<uint4&>(v);
-        asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(p));
+        asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(p));
     } else if constexpr (sizeof(T) == 4) {
-        asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(reinterpret_cast<uint32_t&>(v)) : "l"(p));
+        asm volatile("ld.global.b32 %0, [%1];" : "=r"(reinterpret_cast<uint32_t&>(v)) : "l"(p));
     } else if constexpr (sizeof(T) == 1) {
         uint32_t byte;
-        asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(byte) : "l"(p));
+        asm volatile("ld.global.u8 %0, [%1];" : "=r"(byte) : "l"(p));
         v = (T)byte;
     } else {
         static_assert(sizeof(T) == 2, "1, 2, 4 or 16 bytes");
-        asm volatile("ld.global.nc.b16 %0, [%1];" : "=h"(reinterpret_cast<uint16_t&>(v)) : "l"(p));
+        asm volatile("ld.global.b16 %0, [%1];" : "=h"(reinterpret_cast<uint16_t&>(v)) : "l"(p));
     }
     return v;
 }
@@ -90,7 +92,7 @@ struct MxRaw {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 uint32_t* b = bits + 8 * h;
-                asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                              : "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3]), "=r"(b[4]), "=r"(b[5]), "=r"(b[6]), "=r"(b[7])
                              : "l"(p + 16 / LANES * h));
             }
@@ -239,7 +241,7 @@ __device__ __forceinline__ int64_t mx_scale_offset(int64_t r, int bn_log, int ch
 // `first` holds, no segment leaves [0, n_rows) and all of them together take at most
 // max_groups token tiles.  All of the block's threads call it (a multiple of 32, at most
 // 1024); `tmp` holds 33 words.
-__device__ __forceinline__ void mx_segments(const int32_t* __restrict__ first, int n_experts, int64_t n_rows, int bn,
+__device__ __forceinline__ void mx_segments(const int32_t* first, int n_experts, int64_t n_rows, int bn,
                                             int64_t max_groups, int* start, int* base, int* tmp) {
     const int per = (n_experts + (int)blockDim.x - 1) / (int)blockDim.x;
     const int e0 = threadIdx.x * per, e1 = min(e0 + per, n_experts);

@@ -68,7 +68,7 @@ struct Piece {
 // One matrix for each blockIdx.y (and every gridDim.y-th after it).
 template <typename T>
 __global__ void __launch_bounds__(THREADS, ENCODE_BLOCKS)
-encode_kernel(const T* __restrict__ src, int align, uint8_t* __restrict__ dst, int K, int64_t rows, int64_t nmats,
+encode_kernel(const T* src, int align, uint8_t* dst, int K, int64_t rows, int64_t nmats,
               int64_t mat_stride, int64_t code_bytes, const MxDivisor blocks) {
     pdl_trigger();
     pdl_wait();
@@ -175,8 +175,8 @@ __global__ void __launch_bounds__(THREADS, ACTS_BLOCKS) acts_kernel(const ActArg
 
 template <int UNITS>
 __global__ void __launch_bounds__(THREADS)
-mx_get_rows_kernel(const uint8_t* __restrict__ table, int64_t code_bytes, int64_t nrows, int K,
-                   const int32_t* __restrict__ ids, int64_t n, float* __restrict__ dst) {
+mx_get_rows_kernel(const uint8_t* table, int64_t code_bytes, int64_t nrows, int K,
+                   const int32_t* ids, int64_t n, float* dst) {
     pdl_trigger();
     pdl_wait();
     const int lane = threadIdx.x & 31;
