@@ -399,7 +399,7 @@ rmma_reduce_kernel(const float* __restrict__ part, float* __restrict__ dst, int 
 // columns (tokens from N up to 8 NG get zeros); and the call's control words zeroed
 // (its abort word).
 __global__ void __launch_bounds__(ACT_THREADS)
-act_to_rmma_kernel(const float* __restrict__ x, __half* __restrict__ bmat, float* __restrict__ ds, int K, int N,
+act_to_rmma_kernel(const float* x, __half* __restrict__ bmat, float* __restrict__ ds, int K, int N,
                    unsigned int* __restrict__ ctrl, int ctrl_words) {
     const int n8 = (N + 7) / 8 * 8;   // token columns of the layout (8 NG)
     pdl_wait();      // launched behind earlier work only with the caller's PDL flag
@@ -416,7 +416,8 @@ act_to_rmma_kernel(const float* __restrict__ x, __half* __restrict__ bmat, float
         float v[8];
         if (real) {
             const float4* src = reinterpret_cast<const float4*>(x + (int64_t)n * K + b * QK + i * 8);
-            const float4 a = __ldg(src), c = __ldg(src + 1);
+            // from L2: x may have been written by the work that this kernel waits for above
+            const float4 a = __ldcg(src), c = __ldcg(src + 1);
             v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
             v[4] = c.x; v[5] = c.y; v[6] = c.z; v[7] = c.w;
         } else {

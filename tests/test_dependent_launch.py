@@ -28,3 +28,16 @@ def test_mxfp4_and_expert_kernels_read_coherently():
     assert {"q4q_mx.cuh", "q4q_mxfp4.cu", "q4q_mxmm.cu", "q4q_moe.cu"} <= set(names)
     for name in names:
         assert NON_COHERENT.findall(code(name)) == [], name
+
+
+def test_projections_read_their_activations_coherently():
+    """Weights and biases are resident by contract and may be read any way; the activations may not."""
+    for name, kernels in (("q4q_gemv.cuh", ("quantize_acts",)), ("q4q_rmma.cu", ("act_to_rmma_kernel", "rmma_reduce_kernel"))):
+        text = code(name)
+        for kernel in kernels:
+            body = text[text.index(" %s(" % kernel if kernel == "quantize_acts" else "\n%s(" % kernel):]
+            body = body[:body.index("\n}\n")]
+            assert ("__ldcg(" in body or "ld_behind_wait(" in body) and "__ldg(" not in body, kernel
+    # whatever else these files read through the read-only path are biases
+    for name in ("q4q_gemv.cuh", "q4q_rmma.cu"):
+        assert all(a.startswith("p.bias") for a in re.findall(r"__ldg\s*\(([^)]*)\)", code(name))), name
