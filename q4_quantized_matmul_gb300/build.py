@@ -3,12 +3,15 @@
 Each .cu file under csrc/ is compiled by nvcc in parallel, then linked into
 q4_quantized_matmul_gb300/_build/libq4q.so.  The CUDA runtime is linked
 statically so the library only needs the driver at run time.  csrc/q4q_torch.cpp,
-the Python side of the MXFP4 calls, becomes _build/_q4q_torch.so beside it.
+the Python side of the MXFP4 calls, becomes _build/_q4q_torch.so beside it where
+there is a torch to compile it against; the library itself needs none, at build
+time or run time (python q4_quantized_matmul_gb300/build.py).
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -47,8 +50,12 @@ def _newer(target: str, sources) -> bool:
     return os.path.exists(target) and all(os.path.getmtime(p) <= os.path.getmtime(target) for p in sources)
 
 
+def _has_torch() -> bool:
+    return importlib.util.find_spec("torch") is not None
+
+
 def up_to_date() -> bool:
-    return _newer(LIB, _deps()) and _newer(EXT, [EXT_SRC, os.path.join(ROOT, "include", "q4q.h")])
+    return _newer(LIB, _deps()) and (not _has_torch() or _newer(EXT, [EXT_SRC, os.path.join(ROOT, "include", "q4q.h")]))
 
 
 def _run(cmd, what: str):
@@ -97,16 +104,19 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
-        ext = ex.submit(_compile_ext)
+        ext = ex.submit(_compile_ext) if _has_torch() else None
         objs = list(ex.map(compile_one, _sources()))
-        ext_obj = ext.result()
     tmp = LIB + ".tmp.%d" % os.getpid()
     cmd = [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("link failed:\n%s\n%s" % (r.stdout, r.stderr))
     os.replace(tmp, LIB)
-    _link_ext(ext_obj)
+    # the library is there, whatever becomes of the Python side
+    if ext is not None:
+        _link_ext(ext.result())
+    elif verbose:
+        print("no torch: %s is not built" % EXT)
     return LIB
 
 
