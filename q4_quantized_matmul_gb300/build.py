@@ -15,6 +15,7 @@ import importlib.util
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -54,8 +55,24 @@ def _has_torch() -> bool:
     return importlib.util.find_spec("torch") is not None
 
 
+def _ext_abi() -> str:
+    """What _q4q_torch.so is compiled for: this interpreter and this torch (its version file, read and not imported)."""
+    with open(os.path.join(os.path.dirname(importlib.util.find_spec("torch").origin), "version.py"), encoding="utf-8") as f:
+        return "%s\n%s\n%s" % (sys.version, sysconfig.get_config_var("EXT_SUFFIX"), f.read())
+
+
+def _ext_up_to_date() -> bool:
+    """Newer than its sources, and made for the interpreter and torch that are here now: it uses torch's C++ interface,
+    which is that of one version."""
+    try:
+        with open(EXT + ".abi", encoding="utf-8") as f:
+            return f.read() == _ext_abi() and _newer(EXT, [EXT_SRC, os.path.join(ROOT, "include", "q4q.h")])
+    except OSError:
+        return False
+
+
 def up_to_date() -> bool:
-    return _newer(LIB, _deps()) and (not _has_torch() or _newer(EXT, [EXT_SRC, os.path.join(ROOT, "include", "q4q.h")]))
+    return _newer(LIB, _deps()) and (not _has_torch() or _ext_up_to_date())
 
 
 def _run(cmd, what: str):
@@ -84,6 +101,8 @@ def _link_ext(obj: str):
     _run(["g++", "-shared", "-o", tmp, obj, "-L" + OUT_DIR, "-lq4q", "-Wl,-rpath,$ORIGIN", "-L" + lib, "-Wl,-rpath," + lib,
           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10_cuda", "-lc10"], "link of " + EXT)
     os.replace(tmp, EXT)
+    with open(EXT + ".abi", "w", encoding="utf-8") as f:
+        f.write(_ext_abi())
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
@@ -121,5 +140,4 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
 
 
 if __name__ == "__main__":
-    import sys
     print(build(force="--force" in sys.argv, verbose=True))

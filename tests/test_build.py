@@ -43,3 +43,23 @@ def test_library_is_there_when_the_python_side_fails(tmp_path):
     r = run(tmp_path, "\nb.EXT_SRC = os.path.join(sys.argv[1], 'absent.cpp')\nb.build()\n")
     assert r.returncode != 0 and "absent.cpp" in r.stderr
     assert os.path.exists(os.path.join(tmp_path, "libq4q.so")) and not os.path.exists(os.path.join(tmp_path, "_q4q_torch.so"))
+
+
+def test_python_side_of_another_torch_is_not_up_to_date(tmp_path):
+    """The extension is compiled against one torch and one interpreter; file times do not tell them apart."""
+    r = run(tmp_path, "\nb.build()\nassert b.up_to_date()\n")
+    assert r.returncode == 0, r.stderr[-2000:]
+    # in a new process, which has torch not loaded yet, a torch of another version comes first
+    r = run(tmp_path, """
+assert b.up_to_date()
+fake = os.path.join(sys.argv[1], "torch")
+os.makedirs(fake)
+text = open(os.path.join(os.path.dirname(importlib.util.find_spec("torch").origin), "version.py")).read()
+open(os.path.join(fake, "__init__.py"), "w").close()
+open(os.path.join(fake, "version.py"), "w").write(text.replace("__version__ = '", "__version__ = '0"))
+sys.path.insert(0, sys.argv[1])
+importlib.invalidate_caches()
+assert os.path.dirname(importlib.util.find_spec("torch").origin) == fake
+assert not b.up_to_date()
+""")
+    assert r.returncode == 0, r.stderr[-2000:]
