@@ -17,7 +17,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from . import Q4QError, _lib
+from . import Q4QError, _dev, _lib
 
 Q4Q_ACTS_MXFP4 = 0
 Q4Q_ACTS_MXFP8 = 1
@@ -85,14 +85,17 @@ def q4q_debug_mul_mat_mxfp4_timeout(src0: torch.Tensor, ne00: int, ne01: int, sr
                                     limit_ns: int) -> torch.Tensor:
     """q4q_mul_mat_mxfp4 on the current stream with its first CTA's first stage left out and every wait bounded
     by limit_ns: q4q_device_status() then reports Q4Q_ERR_TIMEOUT (6) and the result is incomplete."""
+    w = _dev(src0, "src0", q4q_mxfp4_size(ne00, ne01))
     ne11 = src1.shape[0]
     if src1.dtype != torch.float32 or not src1.is_cuda or not src1.is_contiguous() or src1.shape != (ne11, ne00):
         raise TypeError("src1 must be a contiguous float32 CUDA tensor [ne11, ne00]")
+    if src1.device != src0.device:
+        raise ValueError("src1 is on another device")
     with torch.cuda.device(src1.device):
         dst = torch.empty((ne11, ne01), dtype=torch.float32, device=src1.device)
         workspace = torch.empty(q4q_mul_mat_mxfp4_workspace_size(ne00, ne01, ne11, acts), dtype=torch.uint8, device=src1.device)
         _check("q4q_debug_mul_mat_mxfp4_timeout", _lib.load().q4q_debug_mul_mat_mxfp4_timeout(
-            src0.data_ptr(), ne00, ne01, src1.data_ptr(), ne11, int(acts), dst.data_ptr(), workspace.data_ptr(),
+            w, ne00, ne01, src1.data_ptr(), ne11, int(acts), dst.data_ptr(), workspace.data_ptr(),
             workspace.numel(), int(limit_ns), torch.cuda.current_stream().cuda_stream))
     return dst
 

@@ -1,0 +1,18 @@
+"""Arguments, errors and limits of the MXFP4 and expert calls on the GPU."""
+import pytest
+
+from test_gpu_mxfp4 import q4q  # noqa: F401
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+def test_timeout_call_checks_its_weights(q4q):  # noqa: F811
+    """A matrix that is too small is refused before the launch."""
+    x = torch.zeros(1, 64, device="cuda")
+    small = torch.zeros(q4q.q4q_mxfp4_size(64, 200) - 1, dtype=torch.uint8, device="cuda")
+    with pytest.raises(ValueError, match="src0"):
+        q4q.q4q_debug_mul_mat_mxfp4_timeout(small, 64, 200, x, 1, 10 ** 6)
+    with pytest.raises(TypeError, match="src0"):
+        q4q.q4q_debug_mul_mat_mxfp4_timeout(small.cpu(), 64, 200, x, 1, 10 ** 6)
+    assert q4q.q4q_device_status() == 0
