@@ -14,10 +14,11 @@
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <exception>
 #include <optional>
-#include <stdexcept>
 #include <string>
 
 #include "q4q.h"
@@ -182,8 +183,9 @@ PyObject* guarded(F f) {
     try {
         return f();
     } catch (const Raised&) {
-    } catch (const std::exception& e) {
-        PyErr_SetString(PyExc_RuntimeError, e.what());
+    } catch (const std::exception&) {
+        // as torch raises them, torch.OutOfMemoryError among them
+        torch::translate_exception_to_python(std::current_exception());
     }
     return nullptr;
 }

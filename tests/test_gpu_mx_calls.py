@@ -16,3 +16,13 @@ def test_timeout_call_checks_its_weights(q4q):  # noqa: F811
     with pytest.raises(TypeError, match="src0"):
         q4q.q4q_debug_mul_mat_mxfp4_timeout(small.cpu(), 64, 200, x, 1, 10 ** 6)
     assert q4q.q4q_device_status() == 0
+
+
+def test_memory_that_is_not_there_is_torchs_error(q4q):  # noqa: F811
+    """A million rows of half a million values do not fit: the error is the one that a program catches from torch."""
+    tokens, top = 1000, 1000
+    first, slot, row = q4q.q4q_moe_sort(torch.zeros(tokens, top, dtype=torch.int32, device="cuda"), 4)
+    src = torch.zeros(tokens, 1 << 19, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(torch.OutOfMemoryError):
+        q4q.q4q_moe_gather(src, first, row, top)
+    assert q4q.q4q_moe_gather(src[:, :8].contiguous(), first, row, top).shape == (tokens * top, 8)
