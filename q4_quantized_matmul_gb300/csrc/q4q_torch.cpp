@@ -5,7 +5,8 @@
 // for one call's checks and allocations (measured on the host of a GB300: 14 us for a sort,
 // of which the launch is 2.7).  Every function takes its arguments by position, checks what
 // the C ABI cannot see (types, contiguity, sizes), allocates what was not given and calls
-// the entry point of its name on the tensors' device and the given or current stream.
+// the entry point of its name on the tensors' device and the given or current stream.  What
+// sizes an allocation is checked before it, so a call that is refused has taken no memory.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
@@ -26,6 +27,8 @@
 namespace {
 
 PyObject* g_error = nullptr;       // Q4QError(fn, status)
+
+constexpr int MAX_EXPERTS = 1024;  // q4q_moe_sort's limit
 
 // carries a Python exception that is already set
 struct Raised {};
@@ -224,9 +227,11 @@ PyObject* get_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
             ids = static_cast<const int32_t*>(typed(t, "ids", at::kInt, 0, at.device()));
         }
         if (n_ids < 0) raise(PyExc_ValueError, "n_ids is negative");
+        const void* w = n_ids > 0 ? bytes(src0, "src0", (int64_t)matrix_bytes(ne00, ne01), at.device()) : nullptr;
+        if (!ids && n_ids > ne01) check("q4q_get_rows_mxfp4", Q4Q_ERR_SHAPE);
         const at::Tensor dst = given(a[5], "dst", at, {n_ids, ne00}, at::kFloat);
         if (n_ids > 0)
-            check("q4q_get_rows_mxfp4", q4q_get_rows_mxfp4(bytes(src0, "src0", (int64_t)matrix_bytes(ne00, ne01), at.device()), ne00, ne01, ids, n_ids,
+            check("q4q_get_rows_mxfp4", q4q_get_rows_mxfp4(w, ne00, ne01, ids, n_ids,
                                                            static_cast<float*>(typed(dst, "dst", at::kFloat, n_ids * ne00, at.device())), at.stream()));
         return wrap(dst);
     });
@@ -268,17 +273,18 @@ PyObject* mul_mat(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const Place at(src0, "src0", a[8]);
         const at::Tensor x = rows_2d(src1);
         const int64_t ne11 = x.size(0), ne10 = x.size(1);
+        const bool empty = ne01 == 0 || ne11 == 0;
+        const void* w = empty ? nullptr : bytes(src0, "src0", (int64_t)matrix_bytes(ne00, ne01), at.device());
         const at::Tensor dst = given(a[5], "dst", at, {ne11, ne01}, output_type(a[6], x));
-        if (ne01 * ne11 == 0) return wrap(dst);
+        if (empty) return wrap(dst);
         size_t need_bytes = 0, size = 0;
         c10::DataPtr hold;
         if (a[7] == Py_None)
             check("q4q_mul_mat_mxfp4_workspace_size", q4q_mul_mat_mxfp4_workspace_size(ne00, ne01, ne11, acts, &need_bytes));
         void* ws = workspace_of(a[7], need_bytes, at, hold, size);
         check("q4q_mul_mat_mxfp4",
-              q4q_mul_mat_mxfp4(bytes(src0, "src0", (int64_t)matrix_bytes(ne00, ne01), at.device()), ne00, ne01, address(x, "src1", 0, at.device()), type,
-                                ne10, ne11, acts, address(dst, "dst", ne11 * ne01, at.device()), type_of(dst, "dst"), ws, size,
-                                (unsigned int)integer(a[9], "flags"), at.stream()));
+              q4q_mul_mat_mxfp4(w, ne00, ne01, address(x, "src1", 0, at.device()), type, ne10, ne11, acts,
+                                address(dst, "dst", ne11 * ne01, at.device()), type_of(dst, "dst"), ws, size, (unsigned int)integer(a[9], "flags"), at.stream()));
         return wrap(dst);
     });
 }
@@ -307,16 +313,19 @@ PyObject* moe_sort(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int experts = small_integer(a[1], "n_experts");
         const Place at(ids, "ids", a[5]);
         const int64_t tokens = ids.size(0), top_k = ids.size(1), slots = tokens * top_k;
+        // refused here what sizes the results, before they are allocated
+        if (experts < 1 || experts > MAX_EXPERTS || top_k < 1) check("q4q_moe_sort", Q4Q_ERR_ARG);
+        if (slots >= (1ll << 31)) check("q4q_moe_sort", Q4Q_ERR_SHAPE);
         at::Tensor first, slot, row;
         if (a[2] == Py_None && a[3] == Py_None && a[4] == Py_None) {
             // one allocation instead of three: 1.2 us less
-            const int64_t n_first = std::max<int64_t>(experts, 0) + 1;
+            const int64_t n_first = experts + 1;
             const at::Tensor all = at.make({n_first + 2 * slots}, at::kInt);
             first = piece(all, 0, n_first);
             slot = piece(all, n_first, slots);
             row = piece(all, n_first + slots, slots);
         } else {
-            first = given(a[2], "first", at, {std::max<int64_t>(experts, 0) + 1}, at::kInt);
+            first = given(a[2], "first", at, {experts + 1}, at::kInt);
             slot = given(a[3], "slot", at, {slots}, at::kInt);
             row = given(a[4], "row", at, {slots}, at::kInt);
         }
@@ -348,9 +357,10 @@ PyObject* gather(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int type = type_of(src, "src"), top_k = small_integer(a[3], "top_k");
         const Place at(src, "src", a[5]);
         const int64_t ne0 = columns(src, "src"), tokens = src.size(0), slots = tokens * top_k;
+        const int32_t* places_of_slots = places(row, "row", slots, at);
         const at::Tensor dst = given(a[4], "dst", at, {std::max<int64_t>(slots, 0), ne0}, src.scalar_type());
         check("q4q_moe_gather", q4q_moe_gather(address(src, "src", 0, at.device()), type, ne0, tokens, top_k, places(first, "first", 1, at),
-                                               experts_of(first), places(row, "row", slots, at),
+                                               experts_of(first), places_of_slots,
                                                typed(dst, "dst", src.scalar_type(), slots * ne0, at.device()), at.stream()));
         return wrap(dst);
     });
@@ -443,17 +453,19 @@ PyObject* mul_mat_id(PyObject*, PyObject* const* a, Py_ssize_t n) {
             n_rows = t.numel();
             slot = places(t, "slot", 0, at);
         }
+        const bool empty = ne01 == 0 || n_rows == 0;
+        if (!empty && (experts < 1 || experts > MAX_EXPERTS)) check("q4q_mul_mat_id_mxfp4", Q4Q_ERR_ARG);
+        const void* w = empty ? nullptr : bytes(src0, "src0", (int64_t)matrix_bytes(ne00, ne01) * experts, at.device());
         const at::Tensor dst = given(a[8], "dst", at, {n_rows, ne01}, output_type(a[9], x));
-        if (ne01 * n_rows == 0) return wrap(dst);
+        if (empty) return wrap(dst);
         size_t need_bytes = 0, size = 0;
         c10::DataPtr hold;
         if (a[10] == Py_None)
             check("q4q_mul_mat_id_mxfp4_workspace_size", q4q_mul_mat_id_mxfp4_workspace_size(ne00, ne01, n_src1, n_rows, experts, acts, &need_bytes));
         void* ws = workspace_of(a[10], need_bytes, at, hold, size);
         check("q4q_mul_mat_id_mxfp4",
-              q4q_mul_mat_id_mxfp4(bytes(src0, "src0", (int64_t)matrix_bytes(ne00, ne01) * std::max(experts, 0), at.device()), ne00, ne01, experts,
-                                   address(x, "src1", 0, at.device()), type, ne10, n_src1, places(first, "first", (int64_t)experts + 1, at), slot, n_rows,
-                                   top_k, acts, address(dst, "dst", n_rows * ne01, at.device()), type_of(dst, "dst"), ws, size,
+              q4q_mul_mat_id_mxfp4(w, ne00, ne01, experts, address(x, "src1", 0, at.device()), type, ne10, n_src1,
+                                   places(first, "first", (int64_t)experts + 1, at), slot, n_rows, top_k, acts, address(dst, "dst", n_rows * ne01, at.device()), type_of(dst, "dst"), ws, size,
                                    (unsigned int)integer(a[12], "flags"), at.stream()));
         return wrap(dst);
     });

@@ -26,3 +26,23 @@ def test_memory_that_is_not_there_is_torchs_error(q4q):  # noqa: F811
     with pytest.raises(torch.OutOfMemoryError):
         q4q.q4q_moe_gather(src, first, row, top)
     assert q4q.q4q_moe_gather(src[:, :8].contiguous(), first, row, top).shape == (tokens * top, 8)
+
+
+def test_refused_calls_take_no_memory(q4q):  # noqa: F811
+    """A mistyped size is refused before results of that size are allocated (gigabytes, in these calls)."""
+    u8 = torch.zeros(4096, dtype=torch.uint8, device="cuda")
+    x, ids = torch.zeros(3, 64, device="cuda"), torch.zeros(3, 2, dtype=torch.int32, device="cuda")
+    first, slot, row = q4q.q4q_moe_sort(ids, 4)
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.max_memory_allocated()
+    for error, call in (
+            (q4q.Q4QError, lambda: q4q.q4q_moe_sort(ids, 2 ** 30)),
+            (q4q.Q4QError, lambda: q4q.q4q_moe_sort(ids, 0)),
+            (ValueError, lambda: q4q.q4q_moe_gather(x, first, row, 2 ** 20)),
+            (ValueError, lambda: q4q.q4q_get_rows_mxfp4(u8, 64, 2 ** 24)),
+            (ValueError, lambda: q4q.q4q_mul_mat_mxfp4(u8, 64, 2 ** 28, x)),
+            (ValueError, lambda: q4q.q4q_mul_mat_id_mxfp4(u8, 64, 2 ** 28, x, first, slot, 2))):
+        with pytest.raises(error):
+            call()
+    assert torch.cuda.max_memory_allocated() == before
