@@ -542,7 +542,7 @@ Q4Q_API q4q_status q4q_mul_mat_id_mxfp4_workspace_size(int64_t ne00, int64_t ne0
  * aligned; src1: device, src1_type [n_src1][ne10]; first, slot: as q4q_moe_sort wrote
  * them; dst: device, dst_type [n_rows][ne01]; workspace as the query says, 256-byte
  * aligned.  n_rows <= n_src1 * top_k with slot, else n_rows <= n_src1; n_rows < 2^24,
- * n_src1 < 2^20.  flags as q4q_mul_mat_ex (`first` and `slot` may still be in flight). */
+ * n_src1 < 2^20 with slot, else n_src1 < 2^24 (what one call wrote, the next can read).  flags as q4q_mul_mat_ex (`first` and `slot` may still be in flight). */
 Q4Q_API q4q_status q4q_mul_mat_id_mxfp4(const void* src0, int64_t ne00, int64_t ne01, int n_experts, const void* src1,
                                 int src1_type, int64_t ne10, int64_t n_src1, const int32_t* first,
                                 const int32_t* slot, int64_t n_rows, int top_k, int acts, void* dst, int dst_type,

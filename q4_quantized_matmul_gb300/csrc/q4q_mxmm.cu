@@ -769,7 +769,7 @@ extern "C" q4q_status q4q_mul_mat_id_mxfp4_workspace_size(int64_t ne00, int64_t 
     if (!bytes) return Q4Q_ERR_NULL;
     q4q_status st = check_product(ne00, ne01, Q4Q_TYPE_F32, ne00, 0, acts, Q4Q_TYPE_F32, 0);
     if (st != Q4Q_OK) return st;
-    if (n_src1 < 0 || n_src1 >= (1 << 20) || n_rows < 0 || n_rows >= (1 << 24)) return Q4Q_ERR_SHAPE;
+    if (n_src1 < 0 || n_src1 >= (1 << 24) || n_rows < 0 || n_rows >= (1 << 24)) return Q4Q_ERR_SHAPE;
     if (n_experts < 1 || n_experts > MX_MAX_EXPERTS) return Q4Q_ERR_ARG;
     *bytes = 0;
     if (ne01 == 0 || n_rows == 0) return Q4Q_OK;
@@ -786,7 +786,8 @@ extern "C" q4q_status q4q_mul_mat_id_mxfp4(const void* src0, int64_t ne00, int64
                                            q4q_stream_t stream) {
     q4q_status st = check_product(ne00, ne01, src1_type, ne10, 0, acts, dst_type, flags);
     if (st != Q4Q_OK) return st;
-    if (n_src1 < 0 || n_src1 >= (1 << 20) || n_rows < 0 || n_rows >= (1 << 24)) return Q4Q_ERR_SHAPE;
+    // tokens, or, without slots, sorted rows: as many as a call with slots may have made
+    if (n_src1 < 0 || n_src1 >= (slot ? 1 << 20 : 1 << 24) || n_rows < 0 || n_rows >= (1 << 24)) return Q4Q_ERR_SHAPE;
     if (n_experts < 1 || n_experts > MX_MAX_EXPERTS || top_k < 1) return Q4Q_ERR_ARG;
     if (slot ? n_rows > n_src1 * top_k : n_rows > n_src1) return Q4Q_ERR_SHAPE;
     if (ne01 == 0 || n_rows == 0) return Q4Q_OK;

@@ -1,7 +1,9 @@
 """Arguments, errors and limits of the MXFP4 and expert calls on the GPU."""
+import numpy as np
 import pytest
 
-from test_gpu_mxfp4 import q4q  # noqa: F401
+from oracle import mx
+from test_gpu_mxfp4 import close, on_gpu, q4q, rand  # noqa: F401
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -46,3 +48,21 @@ def test_refused_calls_take_no_memory(q4q):  # noqa: F811
         with pytest.raises(error):
             call()
     assert torch.cuda.max_memory_allocated() == before
+
+
+def test_a_million_sorted_rows(q4q):  # noqa: F811
+    """1,100,000 rows that are sorted already, more than there may be tokens; three experts, K = 32."""
+    n, rows, experts = 1100000, 24, 3
+    rng = np.random.default_rng(41)
+    packs = [mx.pack(rand(rng, rows, 32, 0.05).astype(np.float32)) for _ in range(experts)]
+    w = torch.from_numpy(np.stack([p[0] for p in packs])).cuda()
+    x, v = on_gpu(rand(rng, n, 32), "bf16")
+    at = [0, 5, 600001, n - 1000]                              # the last 1000 rows are nobody's
+    first = torch.tensor(at, dtype=torch.int32, device="cuda")
+    got = q4q.q4q_mul_mat_id_mxfp4(w, 32, rows, x, first, dst_dtype=torch.float32)
+    assert not got[at[3]:].any()
+    for e in range(experts):
+        for r in (slice(at[e], min(at[e] + 300, at[e + 1])), slice(max(at[e + 1] - 300, at[e]), at[e + 1])):
+            a = mx.encode(v[r], "mxfp8")[2]
+            close(got[r], a @ packs[e][1].T, np.abs(a) @ np.abs(packs[e][1]).T, 32, "f32")
+    assert q4q.q4q_device_status() == 0
