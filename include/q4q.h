@@ -548,6 +548,13 @@ Q4Q_API q4q_status q4q_mul_mat_id_mxfp4(const void* src0, int64_t ne00, int64_t 
                                 const int32_t* slot, int64_t n_rows, int top_k, int acts, void* dst, int dst_type,
                                 void* workspace, size_t workspace_bytes, unsigned int flags, q4q_stream_t stream);
 
+/* Test support, host only: the form that a product of these sizes takes on a device of
+ * sm_count SMs (2 or more): form[0] tokens of a tile, form[1] CTAs that run a tile's MMAs
+ * together (1 or 2), form[2] CTAs that share a tile's K.  n_experts 0: q4q_mul_mat_mxfp4 of
+ * n_rows tokens; else q4q_mul_mat_id_mxfp4.  n_rows and n_src1 from 1 to 2^24 - 1. */
+Q4Q_API q4q_status q4q_debug_mxfp4_form(int64_t ne00, int64_t ne01, int64_t n_rows, int64_t n_src1, int n_experts, int acts,
+                                int sm_count, int* form);
+
 /* Synchronizes the device, returns (in *status) the first device-side error
  * recorded since the last call (Q4Q_OK if none) and clears it.  This is where a
  * bounded wait that ran out (Q4Q_ERR_TIMEOUT) or an out-of-range row id of

@@ -61,6 +61,7 @@ _SIGNATURES = {
     "q4q_mul_mat_mxfp4_workspace_size": (STATUS, [I64, I64, I64, INT, SIZE]),
     "q4q_mul_mat_mxfp4": (STATUS, [P, I64, I64, P, INT, I64, I64, INT, P, INT, P, ctypes.c_size_t, ctypes.c_uint, P]),
     "q4q_debug_mul_mat_mxfp4_timeout": (STATUS, [P, I64, I64, P, I64, INT, P, P, ctypes.c_size_t, ctypes.c_uint64, P]),
+    "q4q_debug_mxfp4_form": (STATUS, [I64, I64, I64, I64, INT, INT, INT, ctypes.POINTER(ctypes.c_int)]),
     "q4q_moe_sort": (STATUS, [P, I64, INT, INT, P, P, P, P]),
     "q4q_moe_gather": (STATUS, [P, INT, I64, I64, INT, P, INT, P, P, P]),
     "q4q_moe_gather_back": (STATUS, [P, INT, I64, I64, INT, P, INT, P, P, P]),

@@ -799,3 +799,17 @@ extern "C" q4q_status q4q_mul_mat_id_mxfp4(const void* src0, int64_t ne00, int64
     return run(src0, ne00, ne01, n_experts, a, n_src1, dst, dst_type, workspace, workspace_bytes, (flags & Q4Q_MUL_MAT_PDL) != 0,
                (cudaStream_t)stream, nullptr);
 }
+
+extern "C" q4q_status q4q_debug_mxfp4_form(int64_t ne00, int64_t ne01, int64_t n_rows, int64_t n_src1, int n_experts, int acts,
+                                           int sm_count, int* form) {
+    if (!form) return Q4Q_ERR_NULL;
+    q4q_status st = check_product(ne00, ne01, Q4Q_TYPE_F32, ne00, 0, acts, Q4Q_TYPE_F32, 0);
+    if (st != Q4Q_OK) return st;
+    if (ne01 == 0 || n_rows < 1 || n_rows >= (1 << 24) || n_src1 < 1 || n_src1 >= (1 << 24)) return Q4Q_ERR_SHAPE;
+    if (n_experts < 0 || n_experts > MX_MAX_EXPERTS || sm_count < 2) return Q4Q_ERR_ARG;
+    const Plan q = make_plan(ne00, ne01, n_rows, n_src1, n_experts, acts, sm_count);
+    form[0] = q.bn;
+    form[1] = q.cg;
+    form[2] = q.split;
+    return Q4Q_OK;
+}
