@@ -104,3 +104,65 @@ def test_chain_of_products_in_place(q4q, tokens, type_):  # noqa: F811
     torch.cuda.synchronize()
     assert torch.isfinite(ref).all() and float(ref.abs().max()) > 0
     assert torch.equal(got, ref)
+
+
+@pytest.mark.parametrize("n,top,experts,k,rows,type_", SIZES)
+def test_calls_on_another_stream(q4q, n, top, experts, k, rows, type_):  # noqa: F811
+    b = Block(q4q, n, top, experts, k, rows, type_, [n, k, 1])
+    ref = b.waited()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = []
+    for i in range(6):
+        b.step(i, stream=side)
+        with torch.cuda.stream(side):
+            got.append([t.clone() for t in b.outputs])
+    side.synchronize()
+    for i in range(6):
+        same(got[i], ref[i], "turn %d" % i)
+
+
+def new_results(b, i, stream=None):
+    """The same calls with results and workspaces of their own."""
+    q, ids, x, w, s = b.q4q, b.ids[i % 3], b.x[i % 3], b.weights[i % 3], {"stream": stream}
+    packed = q.q4q_quantize_mxfp4(b.w32[i % 2], **s)
+    decoded = q.q4q_get_rows_mxfp4(packed[0], b.k, b.rows, **s)
+    first, slot, row = q.q4q_moe_sort(ids, b.experts, **s)
+    gathered = q.q4q_moe_gather(x, first, row, b.top, **s)
+    h = q.q4q_mul_mat_id_mxfp4(packed, b.k, b.rows, x, first, slot, b.top, **s)
+    y = q.q4q_moe_combine(h, first, row, w, **s)
+    back = q.q4q_moe_gather_back(gathered, first, row, b.top, **s)
+    drows, dw = q.q4q_moe_combine_back(y, h, first, row, w, **s)
+    return first, slot, row, packed, gathered, h, y, back, drows, dw, decoded
+
+
+@pytest.mark.parametrize("n,top,experts,k,rows,type_", SIZES)
+def test_new_results_on_another_stream(q4q, n, top, experts, k, rows, type_):  # noqa: F811
+    b = Block(q4q, n, top, experts, k, rows, type_, [n, k, 2])
+    ref = b.waited()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = [new_results(b, i, side) for i in range(6)]
+    torch.cuda.current_stream().wait_stream(side)
+    for i in range(6):
+        same(got[i], ref[i], "turn %d" % i)
+
+
+@pytest.mark.parametrize("n,top,experts,k,rows,type_", SIZES)
+def test_calls_in_a_graph(q4q, n, top, experts, k, rows, type_):  # noqa: F811
+    """Two turns in one graph, into the block's buffers and into the graph's own memory."""
+    b = Block(q4q, n, top, experts, k, rows, type_, [n, k, 3])
+    ref = b.waited()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        b.step(0)
+        own = new_results(b, 1)
+        b.step(5)
+    for _ in range(3):
+        for t in b.outputs + own:
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        same(b.outputs, ref[5], "buffers")
+        same(own, ref[1], "the graph's memory")
+    assert q4q.q4q_device_status() == 0
