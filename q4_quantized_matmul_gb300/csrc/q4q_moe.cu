@@ -18,12 +18,16 @@
 // counts a contiguous run of slots into its own histogram, prefix sums over warps, CTAs
 // (distributed shared memory) and experts turn the counts into places, and the warp walks
 // its run again; votes on the ids' bits give equal ids within a warp their order.  It is
-// bound by the latency of these steps: 2.3 us for 2 choices, 5.3 for 2068, 9.0 for 32764.
+// bound by the latency of these steps: 2.0 us for 2 choices, 4.8 for 2068, 8.5 for 32764
+// (back to back).
 //
 // The row movers are bound by HBM and move 16 bytes a thread.  8191 tokens of 2048 bf16,
-// top 4, at 6790 GB/s: gather 24.4 us (168 MB, its floor), combine 34.5 (168 MB; rows of
-// 4 KB read in random order, four reads to a write: 4.9 TB/s, also with 16 loads of a thread
-// in flight or rows looked up ahead), combine_back 47.5 (302 MB, 6.4 TB/s).
+// top 4, calls back to back: gather 25.6 us (168 MB, 6.6 TB/s), combine_back 50.2 (302 MB, 6.0),
+// combine and gather_back 30.7 each (168 MB, 5.5).  The order of the rows is not what holds those
+// two back, for combine_back reads them in the same order.  It gives a warp a whole row, several
+// pieces of 512 bytes in flight; combine gives a warp 512 bytes of each of a token's top_k rows,
+// whose loads follow one another.  With that mapping kept, 16 loads of a thread in flight and
+// rows looked up ahead changed nothing.
 #include <algorithm>
 #include <atomic>
 

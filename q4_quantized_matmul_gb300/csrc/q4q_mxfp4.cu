@@ -8,12 +8,13 @@
 // whole block of a 16-bit type, half a block of fp32.  Eight values a lane, four lanes a
 // block and two loads that are one piece for the warp, were slower, by their instructions:
 // 117 for each 256 bf16 values of which 50257 x 768 took 24.4 us; a lane's whole block has no
-// shuffles, one scale for 32 values, its maximum two values at a time, and takes 18.3 us
-// (5.4 TB/s).  14336 x 4096 fp32 take 41 us (6.4 TB/s) where they took 43.
+// shuffles, one scale for 32 values, its maximum two values at a time, and took 18.3.  With its
+// start under the end of the call before it, 50257 x 768 bf16 take 15.7 us (6.2 TB/s) and
+// 14336 x 4096 fp32 38.7 (6.9 TB/s).
 //
 // In the gather a unit is a segment of 256 columns of one row: 4 values a lane twice, so that
 // each of a warp's 16-byte stores is one piece of 512 bytes, a warp's 4 units in flight
-// together: 50257 x 768 in 26.3 us (6.6 TB/s).
+// together: 50257 x 768 in 29.1 us, 14336 x 4096 in 43.7 (6.0 and 6.1 TB/s, back to back).
 #include <algorithm>
 
 #include "q4q_internal.h"

@@ -33,10 +33,14 @@
 //
 // What bounds it: a CTA's copies take 1.05 ns a shared-memory row (128 bytes, two cycles),
 // so an atom of 128 + 16 rows 0.165 us and of a pair's 128 + 128 rows 0.28; its MMAs 0.14 us
-// up to 128 tokens, 0.27 with 256.  In the widest tiles the ring's 6 stages (34 KB each, all that
-// shared memory holds) also have no more than 1.6 us to arrive in: two pairs that shared their tokens
-// by multicast, a quarter less from L2, took the same time (2048 tokens 14336 x 4096: 51.0 us, 51.2),
-// as did tiles with fewer tokens than 256 and MMAs and copies of only so many.
+// up to 128 tokens, 0.27 with 256 (the tensor pipe's active time over the atoms of a launch: 12.8 us
+// for 47 at 512 tokens, 25.2 for 94 at 2048).  So few tokens are bound by copies.  In the widest
+// tiles an atom takes 0.27 to 0.31 us in all: MMAs and copies keep pace, and either bounds a round.
+// That is why two pairs that shared their tokens by multicast, a quarter less from L2, took the same
+// time (2048 tokens 14336 x 4096: 51.0 us, 51.2), as did tiles with fewer tokens than 256 and MMAs
+// and copies of only so many.  The 40 to 56% of such a launch in which the tensor pipe rests are
+// rounds that do not fill the device, the start, and reading a tile out: 256 columns have one
+// accumulator, and the next tile's MMAs wait for it.
 //
 // Every mbarrier wait is bounded; one that runs out records Q4Q_ERR_TIMEOUT, raises the
 // call's abort word (zeroed by the activation encoder before every launch) and the CTA

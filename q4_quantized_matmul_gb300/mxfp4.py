@@ -3,7 +3,9 @@
 Bindings of the same names in include/q4q.h, which states the formats and formulas.
 Matrices are torch CUDA tensors (float32, float16 or bfloat16, contiguous), MXFP4
 matrices uint8 tensors of q4q_mxfp4_size bytes; outputs, workspaces and the stream
-default to new tensors and the current stream of the tensors' device.  The calls
+default to new tensors and the current stream of the tensors' device.  Autograd does not
+see these calls: their results need no gradient, whatever their inputs need.  The gradients
+of gather and combine are calls of their own; the products have none.  The calls
 themselves are csrc/q4q_torch.cpp: checks and allocations in C++, because they would
 take longer than the kernels in Python.
 """
