@@ -555,6 +555,118 @@ Q4Q_API q4q_status q4q_mul_mat_id_mxfp4(const void* src0, int64_t ne00, int64_t 
 Q4Q_API q4q_status q4q_debug_mxfp4_form(int64_t ne00, int64_t ne01, int64_t n_rows, int64_t n_src1, int n_experts, int acts,
                                 int sm_count, int* form);
 
+/* ------------------------------------------------ attention ---- */
+
+/* Pairs that a position turns: (2i, 2i + 1), or (i, i + rot / 2).  Values past rot stay. */
+#define Q4Q_ROPE_PAIRS 0
+#define Q4Q_ROPE_HALVES 1
+
+/* Cosines and sines of the positions 0 .. n_pos - 1, computed in 64 bits and rounded:
+ *   table[p][i] = cos(p base^(-2i / rot)),  table[p][rot / 2 + i] = sin(...),  i < rot / 2.
+ * table: device, 16-byte aligned fp32 [n_pos][rot]; 0 < rot <= 256, rot % 16 == 0; base > 0.
+ * A table of other angles (scaled frequencies) may be made in its place. */
+Q4Q_API q4q_status q4q_rope_table(float* table, int64_t n_pos, int rot, double base, q4q_stream_t stream);
+
+/* Norms of queries and keys for each head and the rotation by their positions, in one launch.
+ * Of a head's row x (head_dim values) of token t, p = pos[t]:
+ *   r = fp32(1 / sqrt(mean(x^2) + eps)) (sums as in 64 bits),  z = (x r) w;  z = x without a weight;
+ *   a' = a c - b s, b' = b c + a s for the pairs (a, b) of z's first rot values, c and s from row p
+ *   of the table; without a table nothing is turned.
+ * Each product, difference and sum is rounded to fp32, results once more to `type`.
+ * q: device, type, [n_tokens][n_q_heads][head_dim], a token's rows q_stride elements from the last
+ * one's (a view of a fused projection), aligned to its type; k likewise; q_dst, k_dst: contiguous,
+ * of the same type (they may be q and k where those are contiguous).  Rows that are multiples of 16
+ * bytes apart at 16-byte aligned pointers are faster.  q_weight, k_weight: fp32 [head_dim], 16-byte
+ * aligned, or NULL.  table: fp32 [n_pos][rot], 16-byte aligned, or NULL; pos: int32 [n_tokens].  A
+ * position outside the table makes the token's rows zeros and records Q4Q_ERR_ARG
+ * (q4q_device_status).  head_dim 64, 96, 128 or 256; rot % 16 == 0, rot <= head_dim; up to 1024
+ * heads of either kind (0: none, its pointers are not looked at); n_tokens < 2^31; strides from
+ * heads * head_dim to 2^31 - 1.  Values are finite and below 2^60. */
+Q4Q_API q4q_status q4q_qk_norm_rope(const void* q, int64_t q_stride, int n_q_heads, const void* k, int64_t k_stride, int n_k_heads,
+                            int type, int64_t head_dim, int64_t n_tokens, const float* q_weight, const float* k_weight, float eps,
+                            const float* table, int64_t n_pos, int rot, int mode, const int32_t* pos, void* q_dst, void* k_dst,
+                            q4q_stream_t stream);
+
+/* Bytes of device workspace q4q_qk_norm_rope_back needs on the current device where a weight is given. */
+Q4Q_API q4q_status q4q_qk_norm_rope_back_workspace_size(int64_t head_dim, size_t* bytes);
+
+/* The gradients of q4q_qk_norm_rope.  With dz the gradient turned back, xh = x r:
+ *   dx = r (dz w - xh mean(dz w xh)),  dw = sum over tokens and heads of dz xh;  dx = dz without a weight.
+ * d_q_dst, d_k_dst (gradients of the results) and d_q, d_k: contiguous, of `type`; the latter may be
+ * the former.  q and k are read only where their weight is given, d_q_weight and d_k_weight fp32
+ * [head_dim] written only there.  A token whose position is outside the table has zero gradients and
+ * adds nothing.  Sums are fp32 in a fixed order.  workspace: 256-byte aligned, NULL without weights. */
+Q4Q_API q4q_status q4q_qk_norm_rope_back(const void* d_q_dst, const void* d_k_dst, const void* q, int64_t q_stride, int n_q_heads,
+                                 const void* k, int64_t k_stride, int n_k_heads, int type, int64_t head_dim, int64_t n_tokens,
+                                 const float* q_weight, const float* k_weight, float eps, const float* table, int64_t n_pos,
+                                 int rot, int mode, const int32_t* pos, void* d_q, void* d_k, float* d_q_weight, float* d_k_weight,
+                                 void* workspace, size_t workspace_bytes, q4q_stream_t stream);
+
+/* The paged cache: keys and values of one layer as Q4_0 values in pages of page_tokens tokens (a
+ * power of two, 16 to 4096).  A page holds for each key-value head, for each 16 tokens, a chunk of
+ * 18 * head_dim bytes (B = head_dim / 32; words little endian, nibble 0 lowest):
+ *   K codes   [16 tokens][4 t][B blocks b] words: nibble n holds dim 32 b + 8 t + n;
+ *   V codes   [2 octets][8 g][4 pairs p][B blocks b] words: the low half for token 2p of the octet,
+ *             the high half for token 2p + 1; nibble n of a half holds dim 32 b + 4 g + n;
+ *   K scales  [16 tokens][B] fp16, then V scales likewise.  A value is (nibble - 8) * its scale.
+ * The cache is one 256-byte aligned buffer of n_pages pages; slot s is token s % page_tokens of page
+ * s / page_tokens.  q4q_kv_page_size: bytes of a page.  head_dim as above, up to 1024 heads, pages of
+ * less than 2^31 bytes, n_pages * page_tokens < 2^31. */
+Q4Q_API q4q_status q4q_kv_page_size(int n_kv_heads, int64_t head_dim, int page_tokens, size_t* bytes);
+
+/* Append: token t's keys, normed where k_weight is given and rotated where table is given (as
+ * q4q_qk_norm_rope computes them in fp32), and its values into slot slots[t], each limited to
+ * +-65504 and encoded as q4q_quantize_q4_0 encodes its blocks of 32 (so at most the scale 8188).
+ * A block that holds an infinity or a NaN gets a NaN as its scale.  A negative slot skips the token
+ * (a padded batch); a slot past the cache, or a position outside the table, skips it and records
+ * Q4Q_ERR_ARG.  Where two tokens of a call have one slot, it holds parts of both.
+ * k, v: device, type, [n_tokens][n_kv_heads][head_dim] at their strides, as q4q_qk_norm_rope's. */
+Q4Q_API q4q_status q4q_kv_append(void* cache, int64_t n_pages, int page_tokens, const void* k, int64_t k_stride, const void* v,
+                         int64_t v_stride, int type, int n_kv_heads, int64_t head_dim, int64_t n_tokens, const int32_t* slots,
+                         const float* k_weight, float eps, const float* table, int64_t n_pos, int rot, int mode, const int32_t* pos,
+                         q4q_stream_t stream);
+
+/* Row gather from the cache: the keys and values of slots[i], exact in fp32, rounded to dst_type;
+ * k_dst, v_dst: device [n_slots][n_kv_heads][head_dim], either may be NULL.  A negative slot gives
+ * zeros; so does a slot past the cache, which records Q4Q_ERR_ARG.  n_slots < 2^31. */
+Q4Q_API q4q_status q4q_kv_get_rows(const void* cache, int64_t n_pages, int page_tokens, int n_kv_heads, int64_t head_dim,
+                           const int32_t* slots, int64_t n_slots, void* k_dst, void* v_dst, int dst_type, q4q_stream_t stream);
+
+/* Bytes of device workspace q4q_kv_attn needs on the current device for up to n_q rows of queries. */
+Q4Q_API q4q_status q4q_kv_attn_workspace_size(int64_t n_q, int n_q_heads, int n_kv_heads, int64_t head_dim, int64_t n_seqs, int type,
+                                      size_t* bytes);
+
+/* Attention over the cache.  Sequence s has the rows first[s] .. first[s + 1] - 1 of q (row s alone
+ * where first is NULL) and L = kv_len[s] cached tokens, token j in slot (j % page_tokens) of page
+ * pages[s][j / page_tokens].  With n rows, row i and query head h (key-value head h / (n_q_heads /
+ * n_kv_heads)):
+ *   dst = sum_j softmax_j(scale <q, K_j>) V_j   over 0 <= j < L,
+ *   causal != 0: only j <= L - n + i (the cache holds the rows' own keys already);
+ *   window > 0:  only j > last - window, last the largest j that the line above allows.
+ * A row that sees no key gets zeros, and -inf in lse (fp32 [n_q][n_q_heads], natural logarithm of the
+ * sum of exp(scale <q, K_j>); NULL: not written).  Rows of q that belong to no sequence are neither
+ * read nor written.  Keys that a row does not see take no part, whatever their bytes hold.  Sums and
+ * statistics are fp32.  16-bit rows in numbers (see q4q_kv_attn_tc) have keys, values and weights
+ * rounded to fp16 for the tensor cores; elsewhere queries and weights are kept as two fp16 and
+ * codes are exact.
+ * q: device, type, [n_q][n_q_heads][head_dim] at q_stride; dst: contiguous, of the same type; cache,
+ * pages int32 [n_seqs][max_pages], kv_len int32 [n_seqs], first int32 [n_seqs + 1]: device.  kv_len
+ * beyond max_pages pages counts as that many, and a page outside the cache as one that no row
+ * sees; both record Q4Q_ERR_ARG.  workspace: 256-byte aligned.  n_q_heads a multiple of n_kv_heads,
+ * up to 1024; n_q < 2^24, n_seqs < 2^20, max_pages * page_tokens < 2^31.  Queries below 2^100.  The result
+ * depends on the operands and the device alone. */
+Q4Q_API q4q_status q4q_kv_attn(const void* q, int64_t q_stride, int type, int64_t n_q, int n_q_heads, int n_kv_heads, int64_t head_dim,
+                       const void* cache, int64_t n_pages, int page_tokens, const int32_t* pages, int64_t max_pages,
+                       const int32_t* kv_len, const int32_t* first, int64_t n_seqs, float scale, int causal, int64_t window, void* dst,
+                       float* lse, void* workspace, size_t workspace_bytes, q4q_stream_t stream);
+
+/* Debug: the failure path of that kernel's bounded waits (see q4q_debug_mul_mat_timeout): every wait
+ * is bounded by limit_ns and the first CTA's first copy is left out. */
+Q4Q_API q4q_status q4q_debug_kv_attn_timeout(const void* q, int64_t q_stride, int type, int64_t n_q, int n_q_heads, int n_kv_heads,
+                                     int64_t head_dim, const void* cache, int64_t n_pages, int page_tokens, const int32_t* pages,
+                                     int64_t max_pages, const int32_t* kv_len, int64_t n_seqs, float scale, void* dst, void* workspace,
+                                     size_t workspace_bytes, uint64_t limit_ns, q4q_stream_t stream);
+
 /* Synchronizes the device, returns (in *status) the first device-side error
  * recorded since the last call (Q4Q_OK if none) and clears it.  This is where a
  * bounded wait that ran out (Q4Q_ERR_TIMEOUT) or an out-of-range row id of

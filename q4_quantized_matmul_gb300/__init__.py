@@ -31,6 +31,9 @@ __all__ = [
     "q4q_mul_mat_mxfp4_workspace_size", "q4q_mul_mat_mxfp4", "q4q_debug_mul_mat_mxfp4_timeout", "q4q_moe_sort",
     "q4q_moe_gather", "q4q_moe_gather_back", "q4q_moe_combine", "q4q_moe_combine_back",
     "q4q_mul_mat_id_mxfp4_workspace_size", "q4q_mul_mat_id_mxfp4",
+    "Q4Q_ROPE_PAIRS", "Q4Q_ROPE_HALVES", "q4q_rope_table", "q4q_qk_norm_rope", "q4q_qk_norm_rope_back_workspace_size",
+    "q4q_qk_norm_rope_back", "q4q_kv_page_size", "q4q_kv_append", "q4q_kv_get_rows", "q4q_kv_attn_workspace_size", "q4q_kv_attn",
+    "q4q_debug_kv_attn_timeout",
 ]
 
 QK = 32
@@ -522,3 +525,10 @@ from .mxfp4 import (  # noqa: E402
     q4q_moe_combine_back, q4q_moe_gather, q4q_moe_gather_back, q4q_moe_sort, q4q_mul_mat_id_mxfp4,
     q4q_mul_mat_id_mxfp4_workspace_size, q4q_mul_mat_mxfp4, q4q_mul_mat_mxfp4_workspace_size, q4q_mxfp4_size,
     q4q_quantize_mxfp4)
+
+# -------------------------------------------------------------- attention --
+
+from .attn import (  # noqa: E402
+    Q4Q_ROPE_HALVES, Q4Q_ROPE_PAIRS, q4q_debug_kv_attn_timeout, q4q_kv_append, q4q_kv_attn, q4q_kv_attn_workspace_size,
+    q4q_kv_get_rows, q4q_kv_page_size, q4q_qk_norm_rope, q4q_qk_norm_rope_back, q4q_qk_norm_rope_back_workspace_size,
+    q4q_rope_table)

@@ -19,6 +19,7 @@ _lib = None
 P = ctypes.c_void_p
 I64 = ctypes.c_int64
 INT = ctypes.c_int
+F32 = ctypes.c_float
 STATUS = ctypes.c_int
 SIZE = ctypes.POINTER(ctypes.c_size_t)
 
@@ -70,6 +71,18 @@ _SIGNATURES = {
     "q4q_mul_mat_id_mxfp4_workspace_size": (STATUS, [I64, I64, I64, I64, INT, INT, SIZE]),
     "q4q_mul_mat_id_mxfp4": (STATUS, [P, I64, I64, INT, P, INT, I64, I64, P, P, I64, INT, INT, P, INT, P,
                                       ctypes.c_size_t, ctypes.c_uint, P]),
+    "q4q_rope_table": (STATUS, [P, I64, INT, ctypes.c_double, P]),
+    "q4q_qk_norm_rope": (STATUS, [P, I64, INT, P, I64, INT, INT, I64, I64, P, P, F32, P, I64, INT, INT, P, P, P, P]),
+    "q4q_qk_norm_rope_back_workspace_size": (STATUS, [I64, SIZE]),
+    "q4q_qk_norm_rope_back": (STATUS, [P, P, P, I64, INT, P, I64, INT, INT, I64, I64, P, P, F32, P, I64, INT, INT, P, P, P, P, P, P,
+                                       ctypes.c_size_t, P]),
+    "q4q_kv_page_size": (STATUS, [INT, I64, INT, SIZE]),
+    "q4q_kv_append": (STATUS, [P, I64, INT, P, I64, P, I64, INT, INT, I64, I64, P, P, F32, P, I64, INT, INT, P, P]),
+    "q4q_kv_get_rows": (STATUS, [P, I64, INT, INT, I64, P, I64, P, P, INT, P]),
+    "q4q_kv_attn_workspace_size": (STATUS, [I64, INT, INT, I64, I64, INT, SIZE]),
+    "q4q_kv_attn": (STATUS, [P, I64, INT, I64, INT, INT, I64, P, I64, INT, P, I64, P, P, I64, F32, INT, I64, P, P, P, ctypes.c_size_t, P]),
+    "q4q_debug_kv_attn_timeout": (STATUS, [P, I64, INT, I64, INT, INT, I64, P, I64, INT, P, I64, P, I64, F32, P, P, ctypes.c_size_t,
+                                           ctypes.c_uint64, P]),
     "q4q_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "q4q_version": (ctypes.c_int, []),
 }

@@ -11,6 +11,7 @@
 //   anything else                                           -> generic two-kernel path
 #include <mutex>
 
+#include "q4q_attn_internal.h"
 #include "q4q_common.cuh"
 #include "q4q_internal.h"
 #include "q4q_mx_internal.h"
@@ -294,7 +295,9 @@ extern "C" q4q_status q4q_device_status(q4q_status* status) {
                                   gemv_group_take_device_status(), gemv_epi_take_device_status(),
                                   rows_take_device_status(), debug_take_device_status(),
                                   chain_take_device_status(), rmma_take_device_status(),
-                                  mxfp4_take_device_status(), mxmm_take_device_status()};
+                                  mxfp4_take_device_status(), mxmm_take_device_status(),
+                                  rope_take_device_status(), kv_take_device_status(),
+                                  attn_take_device_status()};
     unsigned int first = 0;
     for (unsigned int w : words)
         if (!first) first = w;

@@ -1,0 +1,31 @@
+// q4q_attn_internal.h -- host-side declarations shared by the attention translation units.
+#pragma once
+
+#include "q4q_mx_internal.h"
+
+namespace q4q {
+
+unsigned int rope_take_device_status();
+unsigned int kv_take_device_status();
+unsigned int attn_take_device_status();
+
+// The shape rules of a cache (q4q_kv.cu): its page size as a power of two.
+q4q_status kv_check(int64_t n_pages, int page_tokens, int n_kv_heads, int64_t head_dim, int& page_log);
+
+// One call of q4q_kv_attn.
+struct AttnArgs {
+    const void* q;
+    int64_t q_stride;
+    const uint8_t* cache;
+    const int32_t *pages, *kv_len, *first;
+    int64_t n_q, n_pages, max_pages, window;
+    int n_seqs, heads, kv_heads, shared;       // shared: query heads of a key-value head
+    int type, page_log, causal, align;         // align: of every row of q and dst, 16 or 1
+    float scale_log2;                          // scale * log2(e)
+    void* dst;
+    float* lse;
+    uint64_t limit_ns;
+    int fault;                                 // test support: the first CTA leaves out its first copy
+};
+
+}  // namespace q4q

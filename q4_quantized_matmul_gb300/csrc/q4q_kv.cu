@@ -1,0 +1,336 @@
+// q4q_kv.cu -- keys and values into the paged 4-bit cache and out of it.
+//
+// Append: of token t's rows (keys normed and turned as q4q_rope.cu has them, values as they are) each
+// block of 32 becomes Q4_0: d = amax / 8, code = round(x / d) half away from zero, limited to
+// [-8, 7], plus 8 -- the encoder of q4q_common.cuh, fed from registers, so a key's fp32 values never
+// go to memory.  Rows are limited to +-65504 first: the scale is then at most 8188 and every
+// (code - 8) d is finite in fp16, which the attention's tensor-core form decodes to.  A block with an
+// infinity or a NaN gets the scale NaN and codes of 8.
+//
+// A row takes D / 8 lanes as in q4q_rope.cu: a lane's 8 values are one word of key codes or two halves
+// of value codes.  The order of the cache (q4q_attn.cuh) spreads a value row's bytes over its octet's
+// 4 D bytes; a prompt's neighbours fill the gaps while the lines are in L2.
+#include <algorithm>
+
+#include "q4q_attn.cuh"
+#include "q4q_mx_internal.h"
+
+namespace q4q {
+namespace {
+
+__device__ unsigned int g_kv_status = 0;
+
+constexpr int THREADS = 256;
+constexpr int WARPS = THREADS / 32;
+constexpr int IN_FLIGHT = 4;
+
+struct KvArgs {
+    const void *k, *v;
+    uint8_t* cache;
+    const float* w;
+    const float* table;
+    const int32_t *pos, *slots;
+    void *k_dst, *v_dst;
+    int64_t k_stride, v_stride, n_pos, n_tokens, n_slots;     // n_slots: of the cache
+    int heads, dim, rot, halves, align, page_log;
+    float eps;
+    float2 inv_dim;
+    int per, items;
+};
+
+constexpr float KV_MAX = 65504.0f;
+
+// A lane's 8 values of a block of 32 (4 lanes): the word of codes, and in d_bits the block's scale.
+__device__ __forceinline__ uint32_t encode_block(float (&v)[8], uint16_t& d_bits) {
+    float m = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) m = max3_abs(m, v[e], v[e + 1]);                        // NaN if one is
+    m = max3_abs(m, __shfl_xor_sync(0xffffffffu, m, 1), 0.0f);
+    m = max3_abs(m, __shfl_xor_sync(0xffffffffu, m, 2), 0.0f);
+    const bool finite = m <= 3.402823466e38f;
+    if (__any_sync(0xffffffffu, !(m <= KV_MAX))) {
+        if (!(m <= KV_MAX))
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = finite ? fminf(fmaxf(v[e], -KV_MAX), KV_MAX) : 0.0f;
+        if (!(m <= KV_MAX)) m = finite ? KV_MAX : 0.0f;
+    }
+    const float d = scale_q4(m);
+    const uint32_t word = pack_q4_word(v, d);
+    d_bits = finite ? fp16_bits(d) : 0x7fffu;
+    return word;
+}
+
+template <typename T, int LANES>
+__global__ void __launch_bounds__(THREADS) append_kernel(KvArgs a) {
+    constexpr int ROWS = 32 / LANES;
+    pdl_trigger();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, in_row = lane % LANES, at = in_row * 8;
+    const bool used = at < a.dim;
+    const int64_t items = a.n_tokens * a.items;
+    for (int64_t item = blockIdx.x * (int64_t)WARPS + (threadIdx.x >> 5); item < items; item += (int64_t)gridDim.x * WARPS) {
+        const int64_t token = item / a.items;
+        const int first = (int)(item - token * a.items) * a.per;
+        const int slot = mx_ld(a.slots + token);
+        if (slot < 0) continue;
+        int p = 0;
+        if (a.table) p = mx_ld(a.pos + token);
+        if (slot >= a.n_slots || (a.table && (p < 0 || p >= a.n_pos))) {
+            if (lane == 0) record_error(&g_kv_status, Q4Q_ERR_ARG);
+            continue;
+        }
+        Turn turning;
+        turning.turns = false;
+        if (a.table) turn_load(turning, a.table + (int64_t)p * a.rot, a.rot, a.halves, used ? at : a.rot);
+        const bool key_angles = turning.turns;
+        const int64_t page = slot >> a.page_log;
+        const int group = (slot >> 4) & ((1 << (a.page_log - 4)) - 1), i16 = slot & 15;
+        for (int s0 = 0; s0 < a.per; s0 += IN_FLIGHT) {
+            float v[IN_FLIGHT][8];
+            int head[IN_FLIGHT];
+            bool value[IN_FLIGHT], here[IN_FLIGHT];
+#pragma unroll
+            for (int i = 0; i < IN_FLIGHT; ++i) {
+                const int row = (first + s0 + i) * ROWS + lane / LANES;
+                value[i] = row >= a.heads;
+                head[i] = value[i] ? row - a.heads : row;
+                here[i] = row < 2 * a.heads && used && s0 + i < a.per;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[i][e] = 0.0f;
+                if (here[i])
+                    row_load((value[i] ? static_cast<const T*>(a.v) + token * a.v_stride : static_cast<const T*>(a.k) + token * a.k_stride) +
+                                 (int64_t)head[i] * a.dim + at, a.align, v[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < IN_FLIGHT; ++i) {
+                if (!__any_sync(0xffffffffu, here[i])) break;
+                const bool key = here[i] && !value[i];
+                if (__any_sync(0xffffffffu, key)) {
+                    if (a.w) {
+                        const float r = inverse_norm<LANES>(v[i], a.inv_dim, a.eps);
+                        if (key)
+#pragma unroll
+                            for (int e = 0; e < 8; e += 4) {
+                                const uint4 u = mx_ld(reinterpret_cast<const uint4*>(a.w + at + e));
+                                v[i][e] = __fmul_rn(__fmul_rn(v[i][e], r), __uint_as_float(u.x));
+                                v[i][e + 1] = __fmul_rn(__fmul_rn(v[i][e + 1], r), __uint_as_float(u.y));
+                                v[i][e + 2] = __fmul_rn(__fmul_rn(v[i][e + 2], r), __uint_as_float(u.z));
+                                v[i][e + 3] = __fmul_rn(__fmul_rn(v[i][e + 3], r), __uint_as_float(u.w));
+                            }
+                    }
+                    if (a.table) {
+                        turning.turns = key && key_angles;
+                        turn(v[i], turning, a.halves, at, a.rot);
+                    }
+                }
+                uint16_t d;
+                const uint32_t word = encode_block(v[i], d);
+                if (here[i]) {
+                    uint8_t* chunk = a.cache + kv_chunk_offset(page, head[i], group, a.heads, a.page_log, a.dim);
+                    const int b = in_row >> 2, t = in_row & 3;
+                    if (value[i]) {
+                        *reinterpret_cast<uint16_t*>(chunk + kv_v_half(i16, 2 * t, b, a.dim)) = (uint16_t)word;
+                        *reinterpret_cast<uint16_t*>(chunk + kv_v_half(i16, 2 * t + 1, b, a.dim)) = (uint16_t)(word >> 16);
+                    } else {
+                        *reinterpret_cast<uint32_t*>(chunk + kv_k_word(i16, t, b, a.dim)) = word;
+                    }
+                    if (t == 0) *reinterpret_cast<uint16_t*>(chunk + kv_scale(value[i], i16, b, a.dim)) = d;
+                }
+            }
+        }
+    }
+}
+
+template <typename T, int LANES>
+__global__ void __launch_bounds__(THREADS) get_rows_kernel(KvArgs a) {
+    constexpr int ROWS = 32 / LANES;
+    pdl_trigger();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, in_row = lane % LANES, at = in_row * 8;
+    const int b = in_row >> 2, t = in_row & 3;
+    const bool used = at < a.dim;
+    const int64_t items = a.n_tokens * a.items;
+    for (int64_t item = blockIdx.x * (int64_t)WARPS + (threadIdx.x >> 5); item < items; item += (int64_t)gridDim.x * WARPS) {
+        const int64_t token = item / a.items;
+        const int first = (int)(item - token * a.items) * a.per;
+        const int slot = mx_ld(a.slots + token);
+        const bool known = slot >= 0 && slot < a.n_slots;
+        if (slot >= a.n_slots && lane == 0) record_error(&g_kv_status, Q4Q_ERR_ARG);
+        const int64_t page = known ? slot >> a.page_log : 0;
+        const int group = (slot >> 4) & ((1 << (a.page_log - 4)) - 1), i16 = slot & 15;
+        for (int s0 = 0; s0 < a.per; s0 += IN_FLIGHT) {
+            uint32_t word[IN_FLIGHT];
+            uint16_t d[IN_FLIGHT];
+            int head[IN_FLIGHT];
+            bool value[IN_FLIGHT], here[IN_FLIGHT];
+#pragma unroll
+            for (int i = 0; i < IN_FLIGHT; ++i) {
+                const int row = (first + s0 + i) * ROWS + lane / LANES;
+                value[i] = row >= a.heads;
+                head[i] = value[i] ? row - a.heads : row;
+                here[i] = row < 2 * a.heads && used && s0 + i < a.per && (value[i] ? a.v_dst : a.k_dst);
+                word[i] = 0x88888888u;
+                d[i] = 0;
+                if (here[i] && known) {
+                    const uint8_t* chunk = a.cache + kv_chunk_offset(page, head[i], group, a.heads, a.page_log, a.dim);
+                    if (value[i])
+                        word[i] = (uint32_t)mx_ld(reinterpret_cast<const uint16_t*>(chunk + kv_v_half(i16, 2 * t, b, a.dim))) |
+                                  (uint32_t)mx_ld(reinterpret_cast<const uint16_t*>(chunk + kv_v_half(i16, 2 * t + 1, b, a.dim))) << 16;
+                    else
+                        word[i] = mx_ld(reinterpret_cast<const uint32_t*>(chunk + kv_k_word(i16, t, b, a.dim)));
+                    d[i] = mx_ld(reinterpret_cast<const uint16_t*>(chunk + kv_scale(value[i], i16, b, a.dim)));
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < IN_FLIGHT; ++i) {
+                if (!here[i]) continue;
+                float v[8];
+                const float scale = fp16_to_f32(d[i]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = __fmul_rn((float)((int)((word[i] >> (4 * e)) & 15u) - 8), scale);
+                T* to = static_cast<T*>(value[i] ? a.v_dst : a.k_dst) + (token * a.heads + head[i]) * (int64_t)a.dim + at;
+                row_store(to, a.align, v);
+            }
+        }
+    }
+}
+
+// As q4q_rope.cu's: the most row slots an item that leave every SM two blocks' warps of items.
+void plan(KvArgs& a, int lanes, const DeviceInfo& info) {
+    const int slots = (2 * a.heads + 32 / lanes - 1) / (32 / lanes);
+    a.per = 1;
+    while (a.per < 16 && a.per < slots && a.n_tokens * ((slots + 2 * a.per - 1) / (2 * a.per)) >= (int64_t)info.sm_count * 2 * WARPS) a.per *= 2;
+    a.items = (slots + a.per - 1) / a.per;
+}
+
+template <typename K>
+q4q_status launch(K kernel, const KvArgs& a, cudaStream_t stream, const DeviceInfo& info) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)std::max<int64_t>(1, std::min<int64_t>((a.n_tokens * a.items + WARPS - 1) / WARPS, (int64_t)info.sm_count * 8)));
+    cfg.blockDim = dim3(THREADS);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
+    return e == cudaSuccess ? launch_status() : (cudaGetLastError(), Q4Q_ERR_CUDA);
+}
+
+template <typename T, int LANES>
+q4q_status run_t(KvArgs& a, bool append, cudaStream_t stream, const DeviceInfo& info) {
+    plan(a, LANES, info);
+    return append ? launch(append_kernel<T, LANES>, a, stream, info) : launch(get_rows_kernel<T, LANES>, a, stream, info);
+}
+
+template <typename T>
+q4q_status run_lanes(KvArgs& a, bool append, cudaStream_t stream, const DeviceInfo& info) {
+    return a.dim <= 64 ? run_t<T, 8>(a, append, stream, info) : a.dim <= 128 ? run_t<T, 16>(a, append, stream, info) : run_t<T, 32>(a, append, stream, info);
+}
+
+q4q_status run(KvArgs& a, int type, bool append, cudaStream_t stream) {
+    DeviceInfo info;
+    const q4q_status st = current_device_info(&info);
+    if (st != Q4Q_OK) return st;
+    switch (type) {
+        case Q4Q_TYPE_F32: return run_lanes<float>(a, append, stream, info);
+        case Q4Q_TYPE_F16: return run_lanes<__half>(a, append, stream, info);
+        default: return run_lanes<__nv_bfloat16>(a, append, stream, info);
+    }
+}
+
+}  // namespace
+
+unsigned int kv_take_device_status() {
+    unsigned int v = 0, z = 0;
+    if (cudaMemcpyFromSymbol(&v, g_kv_status, sizeof(v)) != cudaSuccess) return Q4Q_ERR_CUDA;
+    if (v) cudaMemcpyToSymbol(g_kv_status, &z, sizeof(z));
+    return v;
+}
+
+q4q_status kv_check(int64_t n_pages, int page_tokens, int n_kv_heads, int64_t head_dim, int& page_log) {
+    if (!kv_dim_ok(head_dim) || !kv_page_ok(page_tokens) || n_kv_heads < 1 || n_kv_heads > 1024 || n_pages < 0) return Q4Q_ERR_SHAPE;
+    if ((int64_t)n_kv_heads * head_dim * page_tokens / 8 * 9 >= (1ll << 31)) return Q4Q_ERR_SHAPE;
+    if (n_pages >= (1ll << 31) / page_tokens) return Q4Q_ERR_SHAPE;
+    page_log = 4;
+    while ((1 << page_log) < page_tokens) ++page_log;
+    return Q4Q_OK;
+}
+
+}  // namespace q4q
+
+using namespace q4q;
+
+extern "C" q4q_status q4q_kv_page_size(int n_kv_heads, int64_t head_dim, int page_tokens, size_t* bytes) {
+    if (!bytes) return Q4Q_ERR_NULL;
+    int page_log;
+    const q4q_status st = kv_check(0, page_tokens, n_kv_heads, head_dim, page_log);
+    if (st != Q4Q_OK) return st;
+    *bytes = (size_t)n_kv_heads * (page_tokens / KV_GROUP) * kv_chunk_bytes((int)head_dim);
+    return Q4Q_OK;
+}
+
+extern "C" q4q_status q4q_kv_append(void* cache, int64_t n_pages, int page_tokens, const void* k, int64_t k_stride, const void* v,
+                                    int64_t v_stride, int type, int n_kv_heads, int64_t head_dim, int64_t n_tokens, const int32_t* slots,
+                                    const float* k_weight, float eps, const float* table, int64_t n_pos, int rot, int mode,
+                                    const int32_t* pos, q4q_stream_t stream) {
+    KvArgs a{};
+    const q4q_status st = kv_check(n_pages, page_tokens, n_kv_heads, head_dim, a.page_log);
+    if (st != Q4Q_OK) return st;
+    const int64_t width = n_kv_heads * head_dim;
+    if (n_tokens < 0 || n_tokens >= (1ll << 31) || n_pos < 0 || n_pos >= (1ll << 31)) return Q4Q_ERR_SHAPE;
+    if (k_stride < width || v_stride < width || k_stride >= (1ll << 31) || v_stride >= (1ll << 31)) return Q4Q_ERR_SHAPE;
+    if (table && (rot <= 0 || rot % 16 || rot > head_dim)) return Q4Q_ERR_SHAPE;
+    if (!mx_type_ok(type) || (mode != Q4Q_ROPE_PAIRS && mode != Q4Q_ROPE_HALVES) || !(eps >= 0.0f)) return Q4Q_ERR_ARG;
+    if (n_tokens == 0) return Q4Q_OK;
+    if (!cache || !k || !v || !slots || (table && !pos)) return Q4Q_ERR_NULL;
+    const size_t size = mx_type_bytes(type);
+    if (!aligned(cache, 256) || !aligned(k, size) || !aligned(v, size) || !aligned(slots, 4) || (k_weight && !aligned(k_weight, 16)) ||
+        (table && (!aligned(table, 16) || !aligned(pos, 4))))
+        return Q4Q_ERR_ALIGN;
+    a.k = k;
+    a.v = v;
+    a.cache = static_cast<uint8_t*>(cache);
+    a.w = k_weight;
+    a.table = table;
+    a.pos = pos;
+    a.slots = slots;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.n_pos = n_pos;
+    a.n_tokens = n_tokens;
+    a.n_slots = n_pages * page_tokens;
+    a.heads = n_kv_heads;
+    a.dim = (int)head_dim;
+    a.rot = table ? rot : 0;
+    a.halves = mode == Q4Q_ROPE_HALVES;
+    a.align = aligned(k, 16) && aligned(v, 16) && k_stride * size % 16 == 0 && v_stride * size % 16 == 0 ? 16 : 1;
+    a.eps = eps;
+    const double inv = 1.0 / (double)head_dim;
+    a.inv_dim = make_float2((float)inv, (float)(inv - (double)(float)inv));
+    return run(a, type, true, (cudaStream_t)stream);
+}
+
+extern "C" q4q_status q4q_kv_get_rows(const void* cache, int64_t n_pages, int page_tokens, int n_kv_heads, int64_t head_dim,
+                                      const int32_t* slots, int64_t n_slots, void* k_dst, void* v_dst, int dst_type, q4q_stream_t stream) {
+    KvArgs a{};
+    const q4q_status st = kv_check(n_pages, page_tokens, n_kv_heads, head_dim, a.page_log);
+    if (st != Q4Q_OK) return st;
+    if (n_slots < 0 || n_slots >= (1ll << 31)) return Q4Q_ERR_SHAPE;
+    if (!mx_type_ok(dst_type)) return Q4Q_ERR_ARG;
+    if (n_slots == 0 || (!k_dst && !v_dst)) return Q4Q_OK;
+    if (!cache || !slots) return Q4Q_ERR_NULL;
+    const size_t size = mx_type_bytes(dst_type);
+    if (!aligned(cache, 256) || !aligned(slots, 4) || !aligned(k_dst, size) || !aligned(v_dst, size)) return Q4Q_ERR_ALIGN;
+    a.cache = static_cast<uint8_t*>(const_cast<void*>(cache));
+    a.slots = slots;
+    a.k_dst = k_dst;
+    a.v_dst = v_dst;
+    a.n_tokens = n_slots;
+    a.n_slots = n_pages * page_tokens;
+    a.heads = n_kv_heads;
+    a.dim = (int)head_dim;
+    a.align = aligned(k_dst, 16) && aligned(v_dst, 16) ? 16 : 1;
+    return run(a, dst_type, false, (cudaStream_t)stream);
+}

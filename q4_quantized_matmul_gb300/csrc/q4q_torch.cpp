@@ -1,4 +1,4 @@
-// q4q_torch.cpp -- the Python side of the MXFP4 and expert calls: torch tensors in, the C ABI
+// q4q_torch.cpp -- the Python side of the MXFP4, expert and attention calls: torch tensors in, the C ABI
 // of include/q4q.h out.
 //
 // These calls take a few microseconds on the GPU, about as long as ctypes and Python need
@@ -18,7 +18,10 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
+#include <cmath>
 #include <exception>
+#include <initializer_list>
 #include <optional>
 #include <string>
 
@@ -471,6 +474,276 @@ PyObject* mul_mat_id(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// -------------------------------------------------------------- attention --
+
+// [tokens, heads, dim] whose heads lie one after another: a view of a projection's rows
+struct Heads {
+    void* at = nullptr;
+    int64_t tokens = 0, heads = 0, dim = 0, stride = 0;
+};
+
+Heads heads_of(const at::Tensor& t, const char* name, c10::DeviceIndex device) {
+    if (!t.is_cuda()) raise(PyExc_TypeError, std::string(name) + " must be a CUDA tensor");
+    if (t.get_device() != device) raise(PyExc_ValueError, std::string(name) + " is on another device");
+    if (t.dim() != 3) raise(PyExc_ValueError, std::string(name) + " must be [tokens, heads, head_dim]");
+    Heads h;
+    h.tokens = t.size(0);
+    h.heads = t.size(1);
+    h.dim = t.size(2);
+    const int64_t row = h.heads * h.dim;
+    h.stride = h.tokens > 1 ? t.stride(0) : row;
+    if ((h.dim > 1 && t.stride(2) != 1) || (h.heads > 1 && t.stride(1) != h.dim) || h.stride < row)
+        raise(PyExc_ValueError, std::string(name) + " must have its heads' values one after another, and its tokens apart");
+    h.at = t.data_ptr();
+    return h;
+}
+
+bool none(PyObject* o) { return o == Py_None; }
+
+void same_type(const at::Tensor& t, const at::Tensor& like, const char* name) {
+    if (t.scalar_type() != like.scalar_type()) raise(PyExc_TypeError, std::string(name) + " must be a " + type_name(like.scalar_type()) + " tensor");
+}
+
+void* ints(PyObject* o, const char* name, int64_t count, const Place& at) { return typed(tensor(o, name), name, at::kInt, count, at.device()); }
+
+// a head's weight, or nothing
+const float* weight_of(PyObject* o, const char* name, int64_t dim, const Place& at) {
+    return none(o) ? nullptr : static_cast<const float*>(typed(tensor(o, name), name, at::kFloat, dim, at.device()));
+}
+
+// the table of cosines and sines [n_pos, rot] and the tokens' positions, or nothing
+struct Angles {
+    const float* table = nullptr;
+    const int32_t* pos = nullptr;
+    int64_t n_pos = 0;
+    int rot = 0;
+};
+
+Angles angles_of(PyObject* table, PyObject* pos, int64_t tokens, const Place& at) {
+    Angles r;
+    if (none(table)) return r;
+    const at::Tensor& t = tensor(table, "table");
+    if (t.dim() != 2) raise(PyExc_ValueError, "table must be [positions, rot]");
+    r.table = static_cast<const float*>(typed(t, "table", at::kFloat, 0, at.device()));
+    r.n_pos = t.size(0);
+    r.rot = (int)std::min<int64_t>(t.size(1), 1 << 20);
+    if (none(pos)) raise(PyExc_ValueError, "a table needs pos");
+    r.pos = static_cast<const int32_t*>(ints(pos, "pos", tokens, at));
+    return r;
+}
+
+float real(PyObject* o, const char* name) {
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) {
+        PyErr_Clear();
+        raise(PyExc_TypeError, std::string(name) + " must be a number");
+    }
+    return (float)v;
+}
+
+void head_dim_ok(const char* fn, int64_t dim) {
+    if (dim != 64 && dim != 96 && dim != 128 && dim != 256) check(fn, Q4Q_ERR_SHAPE);
+}
+
+PyObject* pack(std::initializer_list<PyObject*> items) {
+    PyObject* all = PyTuple_New((Py_ssize_t)items.size());
+    Py_ssize_t i = 0;
+    bool ok = all != nullptr;
+    for (PyObject* o : items) {
+        ok = ok && o;
+        if (all) PyTuple_SET_ITEM(all, i++, o);
+        else Py_XDECREF(o);
+    }
+    if (!ok) Py_CLEAR(all);
+    return all;
+}
+
+PyObject* wrap_or_none(const at::Tensor& t) { return t.defined() ? wrap(t) : Py_NewRef(Py_None); }
+
+// rope_table(n_pos, rot, base, dst, stream)
+PyObject* rope_table(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&] {
+        need(a, n, 5);
+        const int64_t n_pos = integer(a[0], "n_pos");
+        const int rot = small_integer(a[1], "rot");
+        const double base = PyFloat_AsDouble(a[2]);
+        if (base == -1.0 && PyErr_Occurred()) throw Raised{};
+        const at::Tensor& dst = tensor(a[3], "dst");
+        const Place at(dst, "dst", a[4]);
+        if (n_pos < 0 || rot < 0) check("q4q_rope_table", Q4Q_ERR_SHAPE);
+        check("q4q_rope_table", q4q_rope_table(static_cast<float*>(typed(dst, "dst", at::kFloat, n_pos * rot, at.device())), n_pos, rot, base, at.stream()));
+        return wrap(dst);
+    });
+}
+
+// qk_norm_rope(q, k, q_weight, k_weight, eps, table, pos, mode, q_dst, k_dst, stream) -> (q, k)
+PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&] {
+        need(a, n, 11);
+        const at::Tensor& q = tensor(a[0], "q");
+        const int type = type_of(q, "q");
+        const Place at(q, "q", a[10]);
+        const Heads hq = heads_of(q, "q", at.device());
+        Heads hk;
+        if (!none(a[1])) {
+            const at::Tensor& k = tensor(a[1], "k");
+            same_type(k, q, "k");
+            hk = heads_of(k, "k", at.device());
+            if (hk.tokens != hq.tokens || hk.dim != hq.dim) raise(PyExc_ValueError, "k must have the tokens and head_dim of q");
+        }
+        head_dim_ok("q4q_qk_norm_rope", hq.dim);
+        const float* qw = weight_of(a[2], "q_weight", hq.dim, at);
+        const float* kw = weight_of(a[3], "k_weight", hq.dim, at);
+        const Angles w = angles_of(a[5], a[6], hq.tokens, at);
+        const int mode = small_integer(a[7], "mode");
+        const at::Tensor dq = given(a[8], "q_dst", at, {hq.tokens, hq.heads, hq.dim}, q.scalar_type());
+        at::Tensor dk;
+        if (!none(a[1])) dk = given(a[9], "k_dst", at, {hk.tokens, hk.heads, hk.dim}, q.scalar_type());
+        check("q4q_qk_norm_rope",
+              q4q_qk_norm_rope(hq.at, hq.stride, (int)hq.heads, hk.at, hk.stride, (int)hk.heads, type, hq.dim, hq.tokens, qw, kw, real(a[4], "eps"), w.table,
+                               w.n_pos, w.rot, mode, w.pos, typed(dq, "q_dst", q.scalar_type(), hq.tokens * hq.heads * hq.dim, at.device()),
+                               dk.defined() ? typed(dk, "k_dst", q.scalar_type(), hk.tokens * hk.heads * hk.dim, at.device()) : nullptr, at.stream()));
+        return pack({wrap(dq), wrap_or_none(dk)});
+    });
+}
+
+// qk_norm_rope_back(d_q_dst, d_k_dst, q, k, q_weight, k_weight, eps, table, pos, mode, d_q, d_k, d_q_weight, d_k_weight, workspace, stream)
+//   -> (d_q, d_k, d_q_weight, d_k_weight)
+PyObject* qk_norm_rope_back(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&] {
+        need(a, n, 16);
+        const at::Tensor& q = tensor(a[2], "q");
+        const int type = type_of(q, "q");
+        const Place at(q, "q", a[15]);
+        const Heads hq = heads_of(q, "q", at.device());
+        Heads hk;
+        if (!none(a[3])) {
+            const at::Tensor& k = tensor(a[3], "k");
+            same_type(k, q, "k");
+            hk = heads_of(k, "k", at.device());
+            if (hk.tokens != hq.tokens || hk.dim != hq.dim) raise(PyExc_ValueError, "k must have the tokens and head_dim of q");
+        }
+        head_dim_ok("q4q_qk_norm_rope_back", hq.dim);
+        const int64_t nq = hq.tokens * hq.heads * hq.dim, nk = hk.tokens * hk.heads * hk.dim;
+        const void* gq = typed(tensor(a[0], "d_q_dst"), "d_q_dst", q.scalar_type(), nq, at.device());
+        const void* gk = none(a[3]) ? nullptr : typed(tensor(a[1], "d_k_dst"), "d_k_dst", q.scalar_type(), nk, at.device());
+        const float* qw = weight_of(a[4], "q_weight", hq.dim, at);
+        const float* kw = none(a[3]) ? nullptr : weight_of(a[5], "k_weight", hq.dim, at);
+        const Angles w = angles_of(a[7], a[8], hq.tokens, at);
+        const int mode = small_integer(a[9], "mode");
+        const at::Tensor dq = given(a[10], "d_q", at, {hq.tokens, hq.heads, hq.dim}, q.scalar_type());
+        at::Tensor dk, dqw, dkw;
+        if (!none(a[3])) dk = given(a[11], "d_k", at, {hk.tokens, hk.heads, hk.dim}, q.scalar_type());
+        if (qw) dqw = given(a[12], "d_q_weight", at, {hq.dim}, at::kFloat);
+        if (kw) dkw = given(a[13], "d_k_weight", at, {hq.dim}, at::kFloat);
+        size_t need_bytes = 0, size = 0;
+        c10::DataPtr hold;
+        if (none(a[14]) && (qw || kw)) check("q4q_qk_norm_rope_back_workspace_size", q4q_qk_norm_rope_back_workspace_size(hq.dim, &need_bytes));
+        void* ws = workspace_of(a[14], need_bytes, at, hold, size);
+        check("q4q_qk_norm_rope_back",
+              q4q_qk_norm_rope_back(gq, gk, hq.at, hq.stride, (int)hq.heads, hk.at, hk.stride, (int)hk.heads, type, hq.dim, hq.tokens, qw, kw,
+                                    real(a[6], "eps"), w.table, w.n_pos, w.rot, mode, w.pos, typed(dq, "d_q", q.scalar_type(), nq, at.device()),
+                                    dk.defined() ? typed(dk, "d_k", q.scalar_type(), nk, at.device()) : nullptr,
+                                    qw ? static_cast<float*>(typed(dqw, "d_q_weight", at::kFloat, hq.dim, at.device())) : nullptr,
+                                    kw ? static_cast<float*>(typed(dkw, "d_k_weight", at::kFloat, hq.dim, at.device())) : nullptr, ws, size, at.stream()));
+        return pack({wrap(dq), wrap_or_none(dk), wrap_or_none(dqw), wrap_or_none(dkw)});
+    });
+}
+
+// the whole pages that a buffer holds
+int64_t pages_in(const char* fn, const at::Tensor& cache, int heads, int64_t dim, int page_tokens, const Place& at, void** address_of) {
+    size_t page = 0;
+    check(fn, q4q_kv_page_size(heads, dim, page_tokens, &page));
+    *address_of = bytes(cache, "cache", 0, at.device());
+    const int64_t size = cache.numel() * cache.element_size();
+    if (size % (int64_t)page) raise(PyExc_ValueError, "cache must hold whole pages of " + std::to_string(page) + " bytes");
+    return size / (int64_t)page;
+}
+
+// kv_append(cache, page_tokens, k, v, slots, k_weight, eps, table, pos, mode, stream) -> cache
+PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&] {
+        need(a, n, 11);
+        const at::Tensor &cache = tensor(a[0], "cache"), &k = tensor(a[2], "k"), &v = tensor(a[3], "v");
+        const int page_tokens = small_integer(a[1], "page_tokens"), type = type_of(k, "k");
+        const Place at(cache, "cache", a[10]);
+        same_type(v, k, "v");
+        const Heads hk = heads_of(k, "k", at.device()), hv = heads_of(v, "v", at.device());
+        if (hk.tokens != hv.tokens || hk.heads != hv.heads || hk.dim != hv.dim) raise(PyExc_ValueError, "k and v must have the same shape");
+        if (hk.heads > 1024) check("q4q_kv_append", Q4Q_ERR_SHAPE);
+        void* buffer = nullptr;
+        const int64_t n_pages = pages_in("q4q_kv_append", cache, (int)hk.heads, hk.dim, page_tokens, at, &buffer);
+        const Angles w = angles_of(a[7], a[8], hk.tokens, at);
+        check("q4q_kv_append", q4q_kv_append(buffer, n_pages, page_tokens, hk.at, hk.stride, hv.at, hv.stride, type, (int)hk.heads, hk.dim, hk.tokens,
+                                             static_cast<const int32_t*>(ints(a[4], "slots", hk.tokens, at)), weight_of(a[5], "k_weight", hk.dim, at),
+                                             real(a[6], "eps"), w.table, w.n_pos, w.rot, small_integer(a[9], "mode"), w.pos, at.stream()));
+        return wrap(cache);
+    });
+}
+
+// kv_get_rows(cache, page_tokens, n_kv_heads, head_dim, slots, dst_dtype, k_dst, v_dst, stream) -> (k, v)
+PyObject* kv_get_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&] {
+        need(a, n, 9);
+        const at::Tensor &cache = tensor(a[0], "cache"), &slots = tensor(a[4], "slots");
+        const int page_tokens = small_integer(a[1], "page_tokens"), heads = small_integer(a[2], "n_kv_heads");
+        const int64_t dim = integer(a[3], "head_dim"), count = slots.numel();
+        const Place at(cache, "cache", a[8]);
+        void* buffer = nullptr;
+        const int64_t n_pages = pages_in("q4q_kv_get_rows", cache, heads, dim, page_tokens, at, &buffer);
+        const void* ids = ints(a[4], "slots", 0, at);
+        if (!THPDtype_Check(a[5])) raise(PyExc_TypeError, "dst_dtype must be a torch.dtype");
+        at::ScalarType type = reinterpret_cast<THPDtype*>(a[5])->scalar_type;
+        if (type != at::kFloat && type != at::kHalf && type != at::kBFloat16) raise(PyExc_TypeError, "dst_dtype must be float32, float16 or bfloat16");
+        const at::Tensor k = given(a[6], "k_dst", at, {count, heads, dim}, type), v = given(a[7], "v_dst", at, {count, heads, dim}, type);
+        check("q4q_kv_get_rows", q4q_kv_get_rows(buffer, n_pages, page_tokens, heads, dim, static_cast<const int32_t*>(ids), count,
+                                                 typed(k, "k_dst", type, count * heads * dim, at.device()),
+                                                 typed(v, "v_dst", type, count * heads * dim, at.device()), type_of(k, "k_dst"), at.stream()));
+        return pack({wrap(k), wrap(v)});
+    });
+}
+
+// kv_attn(q, cache, page_tokens, n_kv_heads, pages, kv_len, first, scale, causal, window, dst, lse, workspace, stream, limit_ns) -> dst
+PyObject* kv_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&] {
+        need(a, n, 15);
+        const at::Tensor &q = tensor(a[0], "q"), &cache = tensor(a[1], "cache"), &pages = tensor(a[4], "pages"), &len = tensor(a[5], "kv_len");
+        const int type = type_of(q, "q"), page_tokens = small_integer(a[2], "page_tokens"), kv_heads = small_integer(a[3], "n_kv_heads");
+        const Place at(q, "q", a[13]);
+        const Heads h = heads_of(q, "q", at.device());
+        if (h.heads > 1024) check("q4q_kv_attn", Q4Q_ERR_SHAPE);
+        head_dim_ok("q4q_kv_attn", h.dim);
+        void* buffer = nullptr;
+        const int64_t n_pages = pages_in("q4q_kv_attn", cache, kv_heads, h.dim, page_tokens, at, &buffer);
+        if (pages.dim() != 2) raise(PyExc_ValueError, "pages must be [sequences, pages]");
+        const int64_t seqs = pages.size(0), max_pages = pages.size(1);
+        const void* table = ints(a[4], "pages", seqs * max_pages, at);
+        const void* lengths = typed(len, "kv_len", at::kInt, seqs, at.device());
+        const void* first = none(a[6]) ? nullptr : ints(a[6], "first", seqs + 1, at);
+        const float scale = none(a[7]) ? (float)(1.0 / std::sqrt((double)h.dim)) : real(a[7], "scale");
+        const int64_t causal = PyObject_IsTrue(a[8]), window = integer(a[9], "window");
+        if (causal < 0) throw Raised{};
+        const at::Tensor dst = given(a[10], "dst", at, {h.tokens, h.heads, h.dim}, q.scalar_type());
+        void* out = typed(dst, "dst", q.scalar_type(), h.tokens * h.heads * h.dim, at.device());
+        float* lse = none(a[11]) ? nullptr : static_cast<float*>(typed(tensor(a[11], "lse"), "lse", at::kFloat, h.tokens * h.heads, at.device()));
+        if (h.tokens == 0 || seqs == 0) return wrap(dst);
+        size_t need_bytes = 0, size = 0;
+        c10::DataPtr hold;
+        if (none(a[12])) check("q4q_kv_attn_workspace_size", q4q_kv_attn_workspace_size(h.tokens, (int)h.heads, kv_heads, h.dim, seqs, type, &need_bytes));
+        void* ws = workspace_of(a[12], need_bytes, at, hold, size);
+        if (none(a[14]))
+            check("q4q_kv_attn", q4q_kv_attn(h.at, h.stride, type, h.tokens, (int)h.heads, kv_heads, h.dim, buffer, n_pages, page_tokens,
+                                             static_cast<const int32_t*>(table), max_pages, static_cast<const int32_t*>(lengths),
+                                             static_cast<const int32_t*>(first), seqs, scale, (int)causal, window, out, lse, ws, size, at.stream()));
+        else
+            check("q4q_debug_kv_attn_timeout",
+                  q4q_debug_kv_attn_timeout(h.at, h.stride, type, h.tokens, (int)h.heads, kv_heads, h.dim, buffer, n_pages, page_tokens,
+                                            static_cast<const int32_t*>(table), max_pages, static_cast<const int32_t*>(lengths), seqs, scale, out, ws, size,
+                                            (uint64_t)integer(a[14], "limit_ns"), at.stream()));
+        return wrap(dst);
+    });
+}
+
 // set_error(Q4QError): the class of the exceptions for statuses other than Q4Q_OK
 PyObject* set_error(PyObject*, PyObject* cls) {
     Py_XDECREF(g_error);
@@ -489,6 +762,12 @@ PyMethodDef methods[] = {
     Q4Q_FAST("moe_combine", combine),
     Q4Q_FAST("moe_combine_back", combine_back),
     Q4Q_FAST("mul_mat_id_mxfp4", mul_mat_id),
+    Q4Q_FAST("rope_table", rope_table),
+    Q4Q_FAST("qk_norm_rope", qk_norm_rope),
+    Q4Q_FAST("qk_norm_rope_back", qk_norm_rope_back),
+    Q4Q_FAST("kv_append", kv_append),
+    Q4Q_FAST("kv_get_rows", kv_get_rows),
+    Q4Q_FAST("kv_attn", kv_attn),
     {"set_error", set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
