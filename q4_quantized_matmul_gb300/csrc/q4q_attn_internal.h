@@ -28,4 +28,15 @@ struct AttnArgs {
     int fault;                                 // test support: the first CTA leaves out its first copy
 };
 
+// The kernels of each head size (q4q_attn_d*.cu).
+#define Q4Q_ATTN_DIM(D)                                                                                                  \
+    q4q_status attn_run_##D(const AttnArgs& a, bool wide, void* workspace, cudaStream_t stream, const DeviceInfo& info); \
+    size_t attn_workspace_##D(const DeviceInfo& info);                                                                   \
+    unsigned int attn_take_device_status_##D();
+Q4Q_ATTN_DIM(64)
+Q4Q_ATTN_DIM(96)
+Q4Q_ATTN_DIM(128)
+Q4Q_ATTN_DIM(256)
+#undef Q4Q_ATTN_DIM
+
 }  // namespace q4q

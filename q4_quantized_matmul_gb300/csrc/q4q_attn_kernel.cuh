@@ -1,0 +1,860 @@
+// q4q_attn_kernel.cuh -- attention over the paged 4-bit cache on warp-level MMAs: few rows of queries
+// a key-value head, and every case that needs fp32 through and through.  q4q_attn_d*.cu instantiate it.
+//
+// Of query row i and key-value head h, over the keys j that the row sees:
+//   s_j = scale <q_i, K_j>,  o_i = sum_j exp(s_j) V_j / sum_j exp(s_j)
+// in one pass over the cache with the running maximum m and sum l of the softmax (base 2: the scale
+// takes log2 e along).  With K = (code - 8) d by blocks of 32 dims, V likewise:
+//   s_j = sum_b dk_jb (sum_{c in b} q_c (code_jc - 8)),  o = sum_j (p_j dv_jb) (code_jc - 8)
+// so codes are exact integers in m16n8k16 MMAs with fp32 sums; the keys' scales multiply the sums of
+// a block, the values' scales the weights p, and neither is ever rounded.  The codes are the operand of
+// 16 rows (16 keys, then 16 dims), the queries the one of 8 columns:
+//   S^T [16 keys, 8] = K [16 keys, 32 of a block] q^T,   O^T [16 dims, 8] += V^T [16 dims, 16 keys] P^T
+// A lane's sums of S are keys g, g + 8 and columns 2t, 2t + 1; scaled and packed to fp16, an 8 x 8 transposition
+// (movmatrix) makes them the operand of the second product.
+//  - SPLIT: columns 0-3 hold the high, 4-7 the low fp16 half of 4 queries, and of their weights, so that both
+//    count with 22 bits; else 8 queries, exact as fp16 of a power of two times their row, weights rounded
+//    to fp16 (2^-12, less than a bf16 result's rounding by 2^3).
+//  - CENTRED: key codes become code - 8 in fp16 (9 operations for 8 codes).  Else they are taken as they are, a
+//    nibble as a fp16 subnormal, code 2^-24, or 16 times that where it lies in a byte's upper half, whose q was
+//    divided by 16, and -8 sum q is what the sum starts from (5 operations for 8).  The tensor cores align a
+//    subnormal by its nominal exponent, which costs about 7 bits: scores are good to 1e-5.
+//    Value codes are always centred: an offset left in sums over many keys would be far larger than they.
+//  - Weights are exp2(s - m - E + 8) with E the largest exponent of the values' scales so far: p dv is
+//    at most 2^8, and m and E move only when something passes them by 2^6, which a vote over
+//    the warp finds; sums are rescaled only then.
+//
+// Work.  All chunks (16 tokens of a head, 2304 bytes at D = 128) of all pieces -- a sequence, head and tile of
+// rows -- in a row are cut into equal shares, one a CTA, two CTAs an SM, so a ragged batch or one long sequence
+// both fill the GPU.  A producer warp's 32 lanes each find and copy one chunk in 32 (a bulk copy into a ring of
+// 32 slots), the consumer warps take them in turn.  At the end of a piece its consumers' sums are joined in
+// shared memory; what a CTA leaves of a piece to others goes to the workspace as sums with m and l, and
+// a second kernel joins the parts in order.
+#pragma once
+
+#include <algorithm>
+#include <type_traits>
+
+#include "q4q_attn.cuh"
+#include "q4q_attn_internal.h"
+
+namespace q4q {
+namespace {
+
+__device__ unsigned int g_attn_status = 0;
+
+// What a type of queries is computed as.
+enum Kind { KIND_F32, KIND_F16, KIND_BF16 };
+
+template <int B_, int KIND, int NG_>
+struct Cfg {
+    static constexpr int B = B_;                       // blocks of 32 dims
+    static constexpr int NG = NG_;                     // groups of 8 columns
+    static constexpr bool SPLIT = KIND != KIND_BF16;
+    static constexpr bool CENTRED = KIND == KIND_F32;
+    using T = std::conditional_t<KIND == KIND_F32, float, std::conditional_t<KIND == KIND_F16, __half, __nv_bfloat16>>;
+    static constexpr int ROWS = (SPLIT ? 4 : 8) * NG;  // of a tile
+    static constexpr int DIM = 32 * B;
+    static constexpr int CHUNK = kv_chunk_bytes(DIM);
+    // Two CTAs of 8 warps an SM where 128 registers are enough (8 B for the sums of a group of columns, 4 B for its
+    // queries), so that one's end of a piece hides behind the other's chunks.
+    static constexpr int CTAS = B <= 4 && NG == 1 ? 2 : 1;
+    static constexpr int CONSUMERS = B <= 4 && NG == 2 ? 11 : 7;
+    static constexpr int THREADS = (CONSUMERS + 1) * 32;
+    static constexpr int SLOTS = B > 4 && NG == 2 ? 16 : 32;
+    static constexpr int OUT_STRIDE = DIM + 4;         // of a row of a warp's sums: conflict-free
+    static constexpr int BARS = 0;                     // full, then empty
+    static constexpr int META = BARS + 2 * SLOTS * 8;  // of each slot: 1 if its page is not there
+    static constexpr int MISC = META + SLOTS * 4;      // scan and broadcast words
+    static constexpr int STOP = MISC + 248;            // the abort flag
+    static constexpr int STATS = MISC + 256;           // [CONSUMERS][ROWS] reference and sum
+    static constexpr int RING = (STATS + CONSUMERS * ROWS * 8 + 127) / 128 * 128;
+    static constexpr int OUT = RING + SLOTS * CHUNK;
+    static constexpr int BYTES = OUT + CONSUMERS * ROWS * OUT_STRIDE * 4;
+    static_assert(MISC % 8 == 0 && CHUNK % 16 == 0 && OUT % 16 == 0, "alignment of copies and vectors");
+    static_assert(BYTES * CTAS <= (227 - CTAS) * 1024, "shared memory of an SM");
+};
+
+// What a worker left in the workspace: a part of a segment (sequence, head, tile), its chunks from .. to - 1
+// of `of`.
+struct Part {
+    int seq, head, tile;
+    int from, to, of;
+};
+
+// The workspace: parts [2 * workers], then of each ROWS x D sums and their references and sums.
+struct Plan {
+    Part* parts;
+    float* rows;
+    int workers;
+    int least;            // chunks a worker should have at least
+    int whole;            // 1: a piece is never cut
+};
+
+// A sequence's rows and keys.
+struct Seq {
+    int q0, n, len;       // first row, rows, cached tokens
+    int tiles;            // of TILE_ROWS rows (tokens x shared heads)
+    int cost;             // chunks that a tile is counted as
+};
+
+template <int TILE_ROWS>
+__device__ __forceinline__ Seq seq_of(const AttnArgs& a, int s, bool whole) {
+    Seq r;
+    if (a.first) {
+        const int64_t f0 = mx_ld(a.first + s), f1 = mx_ld(a.first + s + 1);
+        r.q0 = (int)min(max(f0, (int64_t)0), a.n_q);
+        r.n = (int)(min(max(f1, (int64_t)r.q0), a.n_q) - r.q0);
+    } else {
+        r.q0 = s;
+        r.n = s < a.n_q ? 1 : 0;
+    }
+    const int64_t most = a.max_pages << a.page_log;
+    const int l = mx_ld(a.kv_len + s);
+    if ((l < 0 || l > most) && threadIdx.x % 32 == 0) record_error(&g_attn_status, Q4Q_ERR_ARG);
+    r.len = (int)min(max((int64_t)l, (int64_t)0), most);
+    r.tiles = (int)(((int64_t)r.n * a.shared + TILE_ROWS - 1) / TILE_ROWS);
+    int64_t keys = r.len;
+    if (a.window > 0) keys = min(keys, a.window + TILE_ROWS + KV_GROUP);  // a tile's rows are at most as many tokens
+    r.cost = whole ? 1 : max(1, (int)((keys + KV_GROUP - 1) / KV_GROUP));
+    return r;
+}
+
+__device__ __forceinline__ int64_t units_of(const AttnArgs& a, const Seq& s) { return (int64_t)s.tiles * a.kv_heads * s.cost; }
+
+// The keys that row `row` (token * shared + head) of a sequence sees: [lo, hi).
+__device__ __forceinline__ void keys_of(const AttnArgs& a, const Seq& s, int row, int& lo, int& hi) {
+    const int64_t last = a.causal ? (int64_t)s.len - s.n + row / a.shared : (int64_t)s.len - 1;
+    hi = (int)max(last + 1, (int64_t)0);
+    lo = a.window > 0 ? (int)max(last + 1 - a.window, (int64_t)0) : 0;
+    if (lo > hi) lo = hi;
+}
+
+// A walk over a worker's units [at, end): pieces, one after another.
+struct Walk {
+    int64_t at, end, base;     // base: the first unit of sequence s
+    int s;
+    Seq seq;
+    int head, tile, from, to;  // the piece
+    int g0, g1;                // its chunks: g0 .. g1 - 1 of the sequence
+    bool valid;
+};
+
+template <int TILE_ROWS>
+__device__ __forceinline__ void next_piece(const AttnArgs& a, Walk& w, bool whole) {
+    w.valid = false;
+    while (w.at < w.end) {
+        const int64_t units = units_of(a, w.seq);
+        if (w.at - w.base >= units) {
+            w.base += units;
+            ++w.s;
+            w.seq = seq_of<TILE_ROWS>(a, w.s, whole);
+            continue;
+        }
+        const uint32_t cost = (uint32_t)w.seq.cost;
+        const int64_t rel = w.at - w.base;
+        const int64_t segment = rel / cost;
+        w.from = (int)(rel - segment * cost);
+        w.to = (int)min((int64_t)cost, w.from + (w.end - w.at));
+        w.head = (int)(segment / w.seq.tiles);
+        w.tile = (int)(segment - (int64_t)w.head * w.seq.tiles);
+        w.at += w.to - w.from;
+        // the tile's chunks, and this piece's of them
+        int lo, hi, unused;
+        keys_of(a, w.seq, w.tile * TILE_ROWS, lo, unused);
+        keys_of(a, w.seq, min(w.tile * TILE_ROWS + TILE_ROWS, w.seq.n * a.shared) - 1, unused, hi);
+        const int c0 = lo / KV_GROUP, c1 = (hi + KV_GROUP - 1) / KV_GROUP;
+        w.g0 = whole ? c0 : min(c0 + w.from, c1);
+        w.g1 = whole ? c1 : min(c0 + w.to, c1);
+        w.valid = true;
+        return;
+    }
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1,
+                                        float c0, float c1, float c2, float c3) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    mma_f16(d, a0, a1, a2, a3, b0, b1, d[0], d[1], d[2], d[3]);
+}
+
+// an 8 x 8 matrix of 16-bit values turned over, two values a lane
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t half2_bits(float x, float y) {
+    const __half2 h = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// what the fp16 pair h leaves of x and y, as fp16
+__device__ __forceinline__ uint32_t rest2(float x, float y, uint32_t h) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    return half2_bits(x - f.x, y - f.y);
+}
+
+template <int WORDS>
+__device__ __forceinline__ void lds(uint32_t addr, uint32_t (&v)[WORDS]) {
+    if constexpr (WORDS % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < WORDS; i += 4)
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[i]), "=r"(v[i + 1]), "=r"(v[i + 2]), "=r"(v[i + 3]) : "r"(addr + i * 4));
+    } else if constexpr (WORDS % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < WORDS; i += 2) asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v[i]), "=r"(v[i + 1]) : "r"(addr + i * 4));
+    } else {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v[i]) : "r"(addr + i * 4));
+    }
+}
+
+// B fp16 scales of a token, two a word
+template <int B>
+__device__ __forceinline__ void lds_scales(uint32_t addr, uint32_t (&v)[(B + 1) / 2]) {
+    if constexpr (B % 2 == 0) {
+        lds<B / 2>(addr, v);
+    } else {
+        uint16_t h[B];
+#pragma unroll
+        for (int i = 0; i < B; ++i) asm volatile("ld.shared.b16 %0, [%1];" : "=h"(h[i]) : "r"(addr + i * 2));
+#pragma unroll
+        for (int i = 0; i < (B + 1) / 2; ++i) v[i] = h[2 * i] | (2 * i + 1 < B ? (uint32_t)h[2 * i + 1] << 16 : 0u);
+    }
+}
+
+template <int W>
+__device__ __forceinline__ float scale_at(const uint32_t (&w)[W], int i) {
+    return fp16_to_f32(i & 1 ? w[i >> 1] >> 16 : w[i >> 1]);
+}
+
+// 2^e as fp32, -126 <= e <= 127
+__device__ __forceinline__ float two_to(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// whether the phase is complete, without the wait that try_wait may take
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
+}
+
+template <typename T>
+__device__ __forceinline__ void store4(const AttnArgs& a, int64_t at, float4 v) {
+    T* p = static_cast<T*>(a.dst) + at;
+    if constexpr (sizeof(T) == 4) {
+        if (a.align >= 16) *reinterpret_cast<float4*>(p) = v;
+        else p[0] = v.x, p[1] = v.y, p[2] = v.z, p[3] = v.w;
+    } else {
+        const T h0 = mx_from_f32<T>(v.x), h1 = mx_from_f32<T>(v.y), h2 = mx_from_f32<T>(v.z), h3 = mx_from_f32<T>(v.w);
+        if (a.align >= 16) {
+            auto bits = [](T lo, T hi) { return (uint32_t)reinterpret_cast<const uint16_t&>(lo) | (uint32_t)reinterpret_cast<const uint16_t&>(hi) << 16; };
+            *reinterpret_cast<uint2*>(p) = make_uint2(bits(h0, h1), bits(h2, h3));
+        } else {
+            p[0] = h0, p[1] = h1, p[2] = h2, p[3] = h3;
+        }
+    }
+}
+
+// The share of a part with reference r in sums whose reference is R (none where r is -inf; a NaN stays)
+__device__ __forceinline__ float share_of(float r, float R) { return r == -INFINITY ? 0.0f : exp2f(r - R); }
+__device__ __forceinline__ float larger(float x, float y) { return x != x || y != y ? NAN : fmaxf(x, y); }
+
+// One worker's units and what it is to write down of them.
+struct Share {
+    int64_t u0, u1, base;
+    int s;
+};
+
+// All units, this worker's share of them, and the sequence that it starts in: every thread takes a
+// run of sequences, the block adds them up.  `words`: WARPS + 2 words of shared memory.
+template <int THREADS, int TILE_ROWS>
+__device__ __forceinline__ Share share_of_worker(const AttnArgs& a, const Plan& plan, int64_t* words) {
+    constexpr int WARPS = THREADS / 32;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (a.n_seqs + THREADS - 1) / THREADS, s0 = min(tid * per, a.n_seqs), s1 = min(s0 + per, a.n_seqs);
+    int64_t sum = 0;
+    for (int s = s0; s < s1; ++s) sum += units_of(a, seq_of<TILE_ROWS>(a, s, plan.whole));
+    int64_t inc = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, inc, d);
+        if (lane >= d) inc += o;
+    }
+    if (lane == 31) words[warp] = inc;
+    __syncthreads();
+    int64_t before = inc - sum, total = 0;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+        if (w < warp) before += words[w];
+        total += words[w];
+    }
+    const int64_t workers = min((int64_t)plan.workers, max((int64_t)1, total / plan.least));
+    Share r;
+    r.u0 = min(total, (total * blockIdx.x + workers - 1) / workers);
+    r.u1 = blockIdx.x >= workers ? r.u0 : min(total, (total * (blockIdx.x + 1) + workers - 1) / workers);
+    if (blockIdx.x >= workers) r.u0 = r.u1 = total;
+    // the thread whose run holds the first unit walks to its sequence
+    if (r.u0 < r.u1 && before <= r.u0 && r.u0 < before + sum) {
+        int s = s0;
+        while (true) {
+            const int64_t n = units_of(a, seq_of<TILE_ROWS>(a, s, plan.whole));
+            if (r.u0 < before + n) break;
+            before += n;
+            ++s;
+        }
+        words[WARPS] = before;
+        words[WARPS + 1] = s;
+    }
+    __syncthreads();
+    r.base = words[WARPS];
+    r.s = (int)words[WARPS + 1];
+    return r;
+}
+
+// The producer warp: its lanes find the next SLOTS chunks, one each, and copy each when its slot is free.
+template <typename C>
+__device__ __forceinline__ void produce(const AttnArgs& a, const Plan& plan, Walk w, uint32_t base, uint8_t* smem) {
+    const int lane = threadIdx.x & 31, in_page = a.page_log - 4;
+    volatile int* stop = reinterpret_cast<volatile int*>(smem + C::STOP);
+    bool skip_copy = a.fault && blockIdx.x == 0 && lane == 0;
+    int used = 0;                                    // chunks of the piece that are handled
+    uint32_t phase = 0;                              // copies made into this lane's slot
+    bool ok = true;
+    next_piece<C::ROWS>(a, w, plan.whole);
+    while (w.valid) {
+        bool mine = false;
+        int s = 0, head = 0, group = 0, filled = 0;
+        while (w.valid && filled < C::SLOTS) {
+            const int n = min(w.g1 - w.g0 - used, C::SLOTS - filled);
+            if (lane >= filled && lane < filled + n) {
+                mine = true;
+                s = w.s;
+                head = w.head;
+                group = w.g0 + used + lane - filled;
+            }
+            filled += n;
+            used += n;
+            if (used == w.g1 - w.g0) {
+                next_piece<C::ROWS>(a, w, plan.whole);
+                used = 0;
+            }
+        }
+        int page = -1;
+        if (mine) page = mx_ld(a.pages + s * a.max_pages + (group >> in_page));
+        const bool there = page >= 0 && page < a.n_pages;
+        if (mine && !there) record_error(&g_attn_status, Q4Q_ERR_ARG);
+        const uint8_t* from = a.cache + kv_chunk_offset(there ? page : 0, head, group & ((1 << in_page) - 1), a.kv_heads, a.page_log, C::DIM);
+        const uint32_t full = base + C::BARS + lane * 8, empty = full + C::SLOTS * 8;
+        bool done = !mine;
+        uint64_t t0 = 0;
+        for (uint32_t n = 1; !__all_sync(0xffffffffu, done); ++n) {
+            if (!done && (phase == 0 || mbar_test(empty, (phase - 1) & 1))) {
+                reinterpret_cast<volatile int*>(smem + C::META)[lane] = !there;
+                if (there) {
+                    mbar_arrive_expect_tx(full, C::CHUNK);
+                    if (!skip_copy) bulk_g2s(base + C::RING + lane * C::CHUNK, from, C::CHUNK, full);
+                } else {
+                    mbar_arrive(full);
+                }
+                skip_copy = false;
+                ++phase;
+                done = true;
+            } else if (!done && (n & 63u) == 0u) {
+                // a consumer gave up, or none has freed this slot in time
+                const uint64_t now = global_timer_ns();
+                if (t0 == 0) t0 = now;
+                if (*stop || now - t0 > a.limit_ns) {
+                    ok = false;
+                    done = true;
+                }
+            }
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+    }
+    if (!ok) *stop = 1;
+    // copies in flight must land before this CTA's shared memory is another's: consumers that gave up leave some
+    if (phase > 0) mbar_wait_bounded(base + C::BARS + lane * 8, (phase - 1) & 1, a.limit_ns);
+    __syncwarp();
+}
+
+template <typename C>
+__global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ Plan plan) {
+    constexpr int B = C::B, NG = C::NG, CONSUMERS = C::CONSUMERS;
+    using T = typename C::T;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const uint32_t base = smem_u32(smem);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    volatile int* stop = reinterpret_cast<volatile int*>(smem + C::STOP);
+    if (tid < 2 * C::SLOTS) mbar_init(base + C::BARS + tid * 8, 1);
+    if (tid == 0) *stop = 0;
+    fence_mbar_init();
+    pdl_trigger();
+    pdl_wait();
+    // what is copied below may have been written by ordinary stores of the work before
+    asm volatile("fence.proxy.async;" ::: "memory");
+    const Share share = share_of_worker<C::THREADS, C::ROWS>(a, plan, reinterpret_cast<int64_t*>(smem + C::MISC));
+    if (tid < 2 && !plan.whole) plan.parts[2 * blockIdx.x + tid].of = -1;
+    if (share.u0 >= share.u1) return;
+    Walk work;
+    work.at = share.u0;
+    work.end = share.u1;
+    work.base = share.base;
+    work.s = share.s;
+    work.seq = seq_of<C::ROWS>(a, work.s, plan.whole);
+    if (warp == CONSUMERS) {
+        produce<C>(a, plan, work, base, smem);
+        return;
+    }
+
+    float2* stats = reinterpret_cast<float2*>(smem + C::STATS);
+    float* out = reinterpret_cast<float*>(smem + C::OUT);
+    uint32_t numbered = 0;                           // chunks of this CTA before the piece's
+    bool dead = false;                               // a wait ran out: the rest is passed over
+    while (true) {
+        next_piece<C::ROWS>(a, work, plan.whole);
+        if (!work.valid) break;
+        const Seq& seq = work.seq;
+        const int rows = seq.n * a.shared, tile0 = work.tile * C::ROWS, chunks = work.g1 - work.g0;
+
+        // The queries' operand.  Lane (g, t) holds column g's dims 32 b + 8 t .. + 7, scaled by a power of two so that the
+        // row's largest is in [2^14, 2^15), in the order of the codes' nibbles: (0, 4), (1, 5), (2, 6), (3, 7).
+        uint32_t qf[NG][B][4];
+        float off[NG][C::CENTRED ? 1 : B][2];
+        float row_scale[NG][2];
+        int lo[NG][2], hi[NG][2];                    // keys that this lane's columns 2t, 2t + 1 see
+#pragma unroll
+        for (int q = 0; q < NG; ++q) {
+            const int row = min(tile0 + (C::SPLIT ? q * 4 + (g & 3) : q * 8 + g), rows - 1);
+            const T* from = static_cast<const T*>(a.q) + (int64_t)(seq.q0 + row / a.shared) * a.q_stride +
+                            (int64_t)(work.head * a.shared + row % a.shared) * C::DIM + 8 * t;
+            float v[B][8];
+            float top = 0.0f;
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                row_load(from + 32 * b, a.align, v[b]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[b][e]));
+            }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 100);
+            const float up = two_to(14 - e);
+            // back from 2^(14 - e), and with codes taken as subnormals from their 2^-24
+            const float mine = a.scale_log2 * two_to(C::CENTRED ? e - 14 : e + 10);
+            row_scale[q][0] = __shfl_sync(0xffffffffu, mine, 8 * t);
+            row_scale[q][1] = __shfl_sync(0xffffffffu, mine, 8 * t + 4);
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[b][k] *= up;
+                if constexpr (!C::CENTRED) {
+                    float sum = 0.0f;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) sum += v[b][k];
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                    sum *= -8.0f * 5.9604644775390625e-8f;                        // 2^-24
+                    const bool high = !C::SPLIT || t < 2;
+                    const float s0 = __shfl_sync(0xffffffffu, sum, 8 * t), s1 = __shfl_sync(0xffffffffu, sum, 8 * t + 4);
+                    off[q][b][0] = high ? s0 : 0.0f;
+                    off[q][b][1] = high ? s1 : 0.0f;
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float less = !C::CENTRED && k % 2 ? 0.0625f : 1.0f;
+                    const float x = v[b][k] * less, y = v[b][k + 4] * less;
+                    const uint32_t h = half2_bits(x, y);
+                    qf[q][b][k] = C::SPLIT && g >= 4 ? rest2(x, y, h) : h;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                keys_of(a, seq, min(tile0 + (C::SPLIT ? q * 4 + ((2 * t + i) & 3) : q * 8 + 2 * t + i), rows - 1), lo[q][i], hi[q][i]);
+        }
+        int lo_all = lo[0][0], hi_all = hi[0][0];    // seen by every row of the tile
+#pragma unroll
+        for (int q = 0; q < NG; ++q) lo_all = max(lo_all, max(lo[q][0], lo[q][1])), hi_all = min(hi_all, min(hi[q][0], hi[q][1]));
+        lo_all = __reduce_max_sync(0xffffffffu, lo_all);
+        hi_all = __reduce_min_sync(0xffffffffu, hi_all);
+
+        float o[NG][B][2][4];
+#pragma unroll
+        for (int q = 0; q < NG; ++q)
+#pragma unroll
+            for (int b = 0; b < B; ++b)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[q][b][i / 4][i % 4] = 0.0f;
+        float m[NG][2], l[NG][2], ref[NG][2];        // of columns 2t, 2t + 1: the maximum referred to; this lane's sum; m + E - 8
+#pragma unroll
+        for (int q = 0; q < NG; ++q) m[q][0] = m[q][1] = ref[q][0] = ref[q][1] = -INFINITY, l[q][0] = l[q][1] = 0.0f;
+        int top_e = -32;                             // E: the values' scales are below 2^E
+
+        const int start = (int)((uint32_t)(warp + CONSUMERS) - numbered % CONSUMERS) % CONSUMERS;
+        for (int i = start; i < chunks && !dead; i += CONSUMERS) {
+            const uint32_t number = numbered + i, slot = number % C::SLOTS, full = base + C::BARS + slot * 8;
+            const uint32_t chunk = base + C::RING + slot * C::CHUNK, parity = (number / C::SLOTS) & 1;
+            const bool ok = mbar_try_wait(full, parity) || mbar_wait_until(full, parity, stop, a.limit_ns);
+            if (!__all_sync(0xffffffffu, ok)) {
+                dead = true;
+                if (lane == 0) {
+                    if (!*stop) record_error(&g_attn_status, DEV_TIMEOUT);
+                    *stop = 1;
+                }
+                break;
+            }
+            if (reinterpret_cast<volatile int*>(smem + C::META)[slot]) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(full + C::SLOTS * 8);
+                continue;
+            }
+            const int key0 = (work.g0 + i) * KV_GROUP;
+            const bool edge = key0 < lo_all || key0 + KV_GROUP > hi_all;
+
+            // scores of keys g, g + 8 and columns 2t, 2t + 1
+            float y[NG][4];
+            uint32_t dv[2][(B + 1) / 2];
+            {
+                uint32_t w[2][B], dk[2][(B + 1) / 2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    lds<B>(chunk + (j * 32 + lane) * 4 * B, w[j]);
+                    lds_scales<B>(chunk + 16 * C::DIM + (j * 8 + g) * 2 * B, dk[j]);
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) lds_scales<B>(chunk + 17 * C::DIM + (j * 8 + g) * 2 * B, dv[j]);
+                uint64_t s[NG][2];
+#pragma unroll
+                for (int q = 0; q < NG; ++q) s[q][0] = s[q][1] = 0;
+#pragma unroll
+                for (int b = 0; b < B; ++b) {
+                    uint32_t c[2][4];                // codes of key g, g + 8: nibbles (0, 4), (1, 5), (2, 6), (3, 7)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        if constexpr (C::CENTRED) {
+                            const uint4 x = nibbles_to_f16x8(w[j][b]);
+                            c[j][0] = x.x, c[j][1] = x.y, c[j][2] = x.z, c[j][3] = x.w;
+                        } else {
+                            const uint32_t w8 = w[j][b] >> 8;
+                            c[j][0] = w[j][b] & 0x000F000Fu, c[j][1] = w[j][b] & 0x00F000F0u, c[j][2] = w8 & 0x000F000Fu, c[j][3] = w8 & 0x00F000F0u;
+                        }
+                    }
+                    const float d0 = scale_at(dk[0], b), d1 = scale_at(dk[1], b);
+#pragma unroll
+                    for (int q = 0; q < NG; ++q) {
+                        float acc[4];
+                        const float o0 = C::CENTRED ? 0.0f : off[q][C::CENTRED ? 0 : b][0], o1 = C::CENTRED ? 0.0f : off[q][C::CENTRED ? 0 : b][1];
+                        mma_f16(acc, c[0][0], c[1][0], c[0][1], c[1][1], qf[q][b][0], qf[q][b][1], o0, o1, o0, o1);
+                        mma_f16(acc, c[0][2], c[1][2], c[0][3], c[1][3], qf[q][b][2], qf[q][b][3]);
+                        s[q][0] = ffma2(pack2(acc[0], acc[1]), pack2(d0, d0), s[q][0]);
+                        s[q][1] = ffma2(pack2(acc[2], acc[3]), pack2(d1, d1), s[q][1]);
+                    }
+                }
+#pragma unroll
+                for (int q = 0; q < NG; ++q) {
+                    unpack2(s[q][0], y[q][0], y[q][1]);
+                    unpack2(s[q][1], y[q][2], y[q][3]);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if constexpr (C::SPLIT) y[q][k] += __shfl_xor_sync(0xffffffffu, y[q][k], 2);
+                        y[q][k] *= row_scale[q][k & 1];
+                    }
+                }
+            }
+            if (edge) {
+                // keys that a row does not see, and the scales of slots that no row does
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int key = key0 + 8 * j + g;
+#pragma unroll
+                    for (int q = 0; q < NG; ++q) {
+                        if (key < lo[q][0] || key >= hi[q][0]) y[q][2 * j] = -INFINITY;
+                        if (key < lo[q][1] || key >= hi[q][1]) y[q][2 * j + 1] = -INFINITY;
+                    }
+                    if (key >= seq.len)
+#pragma unroll
+                        for (int k = 0; k < (B + 1) / 2; ++k) dv[j][k] = 0u;
+                }
+            }
+            uint32_t bits = 0;
+#pragma unroll
+            for (int k = 0; k < (B + 1) / 2; ++k) bits = __vmaxu2(bits, __vmaxu2(dv[0][k], dv[1][k]));
+            bits = max(bits >> 16, bits & 0xFFFFu);
+            bool grows = (int)(bits >> 10) - 14 > top_e;                           // a scale is below 2^(exponent field - 14)
+            float x[NG][4];
+#pragma unroll
+            for (int q = 0; q < NG; ++q)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    x[q][k] = y[q][k] - ref[q][k & 1];
+                    grows |= x[q][k] > (float)(14 - top_e);                        // y > m + 6
+                }
+            if (__any_sync(0xffffffffu, grows)) {
+                // an infinite or NaN scale makes its own dims so, and says nothing about the others'
+                uint32_t finite = 0;
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int k = 0; k < (B + 1) / 2; ++k) {
+                        const uint32_t h0 = dv[j][k] & 0x7FFFu, h1 = (dv[j][k] >> 16) & 0x7FFFu;
+                        finite = max(finite, max(h0 < 0x7C00u ? h0 : 0u, h1 < 0x7C00u ? h1 : 0u));
+                    }
+                const int e = max(top_e, (int)(__reduce_max_sync(0xffffffffu, finite) >> 10) - 14);
+#pragma unroll
+                for (int q = 0; q < NG; ++q)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float n = fmaxf(y[q][c], y[q][2 + c]);
+                        n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, 4));
+                        n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, 8));
+                        n = fmaxf(m[q][c], fmaxf(n, __shfl_xor_sync(0xffffffffu, n, 16)));
+                        const float down = m[q][c] == -INFINITY ? 0.0f : exp2f((m[q][c] - n) + (float)(top_e - e));
+                        m[q][c] = n;
+                        ref[q][c] = n + (float)(e - 8);
+                        l[q][c] *= down;
+#pragma unroll
+                        for (int b = 0; b < B; ++b) o[q][b][0][c] *= down, o[q][b][0][2 + c] *= down, o[q][b][1][c] *= down, o[q][b][1][2 + c] *= down;
+                        x[q][c] = y[q][c] - ref[q][c];
+                        x[q][2 + c] = y[q][2 + c] - ref[q][c];
+                    }
+                top_e = e;
+            }
+#pragma unroll
+            for (int q = 0; q < NG; ++q)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    x[q][k] = ex2(x[q][k]);                                        // from here the weight
+                    if (edge && y[q][k] == -INFINITY) x[q][k] = 0.0f;
+                    l[q][k & 1] += x[q][k];
+                }
+            uint32_t w[2][B];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) lds<B>(chunk + 8 * C::DIM + (j * 32 + lane) * 4 * B, w[j]);
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                const float d0 = scale_at(dv[0], b), d1 = scale_at(dv[1], b);
+                const uint4 c0 = nibbles_to_f16x8(w[0][b]), c1 = nibbles_to_f16x8(w[1][b]);
+#pragma unroll
+                for (int q = 0; q < NG; ++q) {
+                    float p[4] = {x[q][0] * d0, x[q][1] * d0, x[q][2] * d1, x[q][3] * d1};
+                    if (edge)                                                      // a scale may be anything where the weight is none
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (y[q][k] == -INFINITY) p[k] = 0.0f;
+                    uint32_t p0 = half2_bits(p[0], p[1]), p1 = half2_bits(p[2], p[3]);
+                    if constexpr (C::SPLIT) {
+                        const uint32_t r0 = rest2(p[0], p[1], p0), r1 = rest2(p[2], p[3], p1);
+                        p0 = t < 2 ? p0 : r0;
+                        p1 = t < 2 ? p1 : r1;
+                    }
+                    p0 = transposed(p0);
+                    p1 = transposed(p1);
+                    mma_f16(o[q][b][0], c0.x, c0.y, c1.x, c1.y, p0, p1);
+                    mma_f16(o[q][b][1], c0.z, c0.w, c1.z, c1.w, p0, p1);
+                }
+            }
+            __syncwarp();                            // the chunk is read by all lanes before it is written again
+            if (lane == 0) mbar_arrive(full + C::SLOTS * 8);
+        }
+        numbered += (uint32_t)chunks;
+
+        // Join the warps: of column 2t + c this lane's dims 32 b + 4 g .. + 3, its reference and sum.
+        const bool any = start < chunks;
+#pragma unroll
+        for (int q = 0; q < NG; ++q)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float sum = l[q][c];
+                sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+                const int row = C::SPLIT ? q * 4 + 2 * (t & 1) + c : q * 8 + 2 * t + c;
+                if (g == 0 && (!C::SPLIT || t < 2)) stats[warp * C::ROWS + row] = make_float2(any && m[q][c] != -INFINITY ? ref[q][c] : -INFINITY, sum);
+                if (any)
+#pragma unroll
+                    for (int b = 0; b < B; ++b) {
+                        float4 v = make_float4(o[q][b][0][c], o[q][b][0][2 + c], o[q][b][1][c], o[q][b][1][2 + c]);
+                        if constexpr (C::SPLIT) {
+                            v.x += __shfl_xor_sync(0xffffffffu, v.x, 2), v.y += __shfl_xor_sync(0xffffffffu, v.y, 2);
+                            v.z += __shfl_xor_sync(0xffffffffu, v.z, 2), v.w += __shfl_xor_sync(0xffffffffu, v.w, 2);
+                        }
+                        if (!C::SPLIT || t < 2) *reinterpret_cast<float4*>(out + (warp * C::ROWS + row) * C::OUT_STRIDE + 32 * b + 4 * g) = v;
+                    }
+            }
+        asm volatile("bar.sync 1, %0;" ::"n"(CONSUMERS * 32) : "memory");
+        const bool complete = work.from == 0 && work.to == seq.cost;
+        const int part = 2 * blockIdx.x + (work.from == 0 ? 1 : 0);
+        float* part_rows = plan.rows + (int64_t)part * (C::ROWS * (C::DIM + 2));
+        if (!complete && tid == 0) plan.parts[part] = {work.s, work.head, work.tile, work.from, work.to, seq.cost};
+        for (int i = tid; i < C::ROWS * (C::DIM / 4); i += CONSUMERS * 32) {
+            const int r = i / (C::DIM / 4), c = i % (C::DIM / 4) * 4;
+            if (tile0 + r >= rows) break;                                          // r grows with i
+            float2 st[CONSUMERS];
+            float top = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < CONSUMERS; ++w) {
+                st[w] = stats[w * C::ROWS + r];
+                top = larger(top, st[w].x);
+            }
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            float sum = 0.0f;
+#pragma unroll
+            for (int w = 0; w < CONSUMERS; ++w) {
+                if (st[w].x == -INFINITY) continue;                                // nothing was written there
+                const float k = exp2f(st[w].x - top);
+                const float4 x = *reinterpret_cast<const float4*>(out + (w * C::ROWS + r) * C::OUT_STRIDE + c);
+                sum = fmaf(k, st[w].y, sum);
+                v.x = fmaf(k, x.x, v.x), v.y = fmaf(k, x.y, v.y), v.z = fmaf(k, x.z, v.z), v.w = fmaf(k, x.w, v.w);
+            }
+            if (complete) {
+                const float inv = top == -INFINITY ? 0.0f : 1.0f / sum;
+                const int64_t at = (int64_t)(seq.q0 + (tile0 + r) / a.shared) * a.heads + work.head * a.shared + (tile0 + r) % a.shared;
+                store4<T>(a, at * C::DIM + c, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+                if (c == 0 && a.lse) a.lse[at] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+            } else {
+                *reinterpret_cast<float4*>(part_rows + r * C::DIM + c) = v;
+                if (c == 0) *reinterpret_cast<float2*>(part_rows + C::ROWS * C::DIM + 2 * r) = make_float2(top, sum);
+            }
+        }
+        asm volatile("bar.sync 1, %0;" ::"n"(CONSUMERS * 32) : "memory");
+    }
+}
+
+// Joins the parts of the segments that were cut.  A segment's parts are a worker's last one (its
+// start) and the first ones of the workers behind it; block (w, r) joins row r of the one that starts
+// in worker w.
+constexpr int JOIN_WARPS = 4;
+
+template <typename C>
+__global__ void __launch_bounds__(JOIN_WARPS * 32) join_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ Plan plan) {
+    constexpr int VEC = C::DIM / 32;
+    __shared__ float sums[JOIN_WARPS][C::DIM];
+    __shared__ float2 stats[JOIN_WARPS];
+    pdl_wait();
+    const int w = blockIdx.x, r = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const Part* parts = plan.parts;
+    const int of = mx_ld(&parts[2 * w + 1].of), to0 = mx_ld(&parts[2 * w + 1].to);
+    if (of < 0 || to0 >= of) return;                       // no segment starts here, or none that goes on
+    const int s = mx_ld(&parts[2 * w + 1].seq), head = mx_ld(&parts[2 * w + 1].head), tile = mx_ld(&parts[2 * w + 1].tile);
+    const Seq seq = seq_of<C::ROWS>(a, s, plan.whole);
+    const int row = tile * C::ROWS + r;
+    if (row >= seq.n * a.shared) return;
+    // parts until the segment's end
+    int n = 1;
+    while (w + n < plan.workers && mx_ld(&parts[2 * (w + n)].of) >= 0 && mx_ld(&parts[2 * (w + n)].to) < of) ++n;
+    n = min(n + 1, plan.workers - w);
+    float ref = -INFINITY, sum = 0.0f, v[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[i] = 0.0f;
+    // the largest reference first: all of them in flight together
+    for (int p = lane; p < n; p += 32) {
+        const float* rows = plan.rows + (p == 0 ? 2 * w + 1 : 2 * (w + p)) * (int64_t)(C::ROWS * (C::DIM + 2));
+        ref = larger(ref, mx_ld(rows + C::ROWS * C::DIM + 2 * r));
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) ref = larger(ref, __shfl_xor_sync(0xffffffffu, ref, d));
+    for (int p = warp; p < n; p += JOIN_WARPS) {
+        const float* rows = plan.rows + (p == 0 ? 2 * w + 1 : 2 * (w + p)) * (int64_t)(C::ROWS * (C::DIM + 2));
+        const float k = share_of(mx_ld(rows + C::ROWS * C::DIM + 2 * r), ref);
+        sum = fmaf(k, mx_ld(rows + C::ROWS * C::DIM + 2 * r + 1), sum);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[i] = fmaf(k, mx_ld(rows + r * C::DIM + i * 32 + lane), v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) sums[warp][i * 32 + lane] = v[i];
+    if (lane == 0) stats[warp] = make_float2(ref, sum);
+    __syncthreads();
+    sum = 0.0f;
+#pragma unroll
+    for (int x = 0; x < JOIN_WARPS; ++x) sum += stats[x].y;
+    const float inv = ref == -INFINITY ? 0.0f : 1.0f / sum;
+    const int64_t at = (int64_t)(seq.q0 + row / a.shared) * a.heads + head * a.shared + row % a.shared;
+    for (int c = threadIdx.x * 4; c < C::DIM; c += JOIN_WARPS * 128) {
+        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < JOIN_WARPS; ++i) {
+            const float4 y = *reinterpret_cast<const float4*>(&sums[i][c]);
+            x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+        }
+        store4<typename C::T>(a, at * C::DIM + c, make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
+    }
+    if (threadIdx.x == 0 && a.lse) a.lse[at] = ref == -INFINITY ? -INFINITY : (ref + log2f(sum)) * 0.69314718055994531f;
+}
+
+template <typename K, typename... Args>
+q4q_status launch(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    return e == cudaSuccess ? launch_status() : (cudaGetLastError(), Q4Q_ERR_CUDA);
+}
+
+template <typename C>
+q4q_status run(const AttnArgs& a, void* workspace, cudaStream_t stream, const DeviceInfo& info) {
+    const cudaError_t e = cudaFuncSetAttribute(attn_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES);
+    if (e != cudaSuccess) return cudaGetLastError(), Q4Q_ERR_CUDA;
+    Plan plan;
+    plan.workers = info.sm_count * C::CTAS;
+    plan.whole = (a.max_pages << a.page_log) <= KV_GROUP * C::CONSUMERS;
+    plan.least = plan.whole ? 1 : C::CONSUMERS;
+    plan.parts = static_cast<Part*>(workspace);
+    plan.rows = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + mx_up((int64_t)sizeof(Part) * 2 * plan.workers, 256));
+    const q4q_status st = launch(attn_kernel<C>, dim3((unsigned)plan.workers), C::THREADS, C::BYTES, stream, a, plan);
+    if (st != Q4Q_OK || plan.whole) return st;
+    return launch(join_kernel<C>, dim3((unsigned)plan.workers, C::ROWS), JOIN_WARPS * 32, 0, stream, a, plan);
+}
+
+template <typename C>
+size_t workspace_of(const DeviceInfo& info) {
+    const int64_t workers = (int64_t)info.sm_count * C::CTAS;
+    return (size_t)(mx_up((int64_t)sizeof(Part) * 2 * workers, 256) + (int64_t)sizeof(float) * C::ROWS * (C::DIM + 2) * 2 * workers);
+}
+
+// that of the forms with the most rows
+template <int B>
+size_t attn_workspace(const DeviceInfo& info) {
+    return std::max(workspace_of<Cfg<B, KIND_BF16, 1>>(info), workspace_of<Cfg<B, KIND_BF16, 2>>(info));
+}
+
+// `wide`: two groups of columns
+template <int B>
+q4q_status attn_run(const AttnArgs& a, bool wide, void* workspace, cudaStream_t stream, const DeviceInfo& info) {
+    switch (a.type) {
+        case Q4Q_TYPE_F32: return wide ? run<Cfg<B, KIND_F32, 2>>(a, workspace, stream, info) : run<Cfg<B, KIND_F32, 1>>(a, workspace, stream, info);
+        case Q4Q_TYPE_F16: return wide ? run<Cfg<B, KIND_F16, 2>>(a, workspace, stream, info) : run<Cfg<B, KIND_F16, 1>>(a, workspace, stream, info);
+        default: return wide ? run<Cfg<B, KIND_BF16, 2>>(a, workspace, stream, info) : run<Cfg<B, KIND_BF16, 1>>(a, workspace, stream, info);
+    }
+}
+
+unsigned int attn_take_status_word() {
+    unsigned int v = 0, z = 0;
+    if (cudaMemcpyFromSymbol(&v, g_attn_status, sizeof(v)) != cudaSuccess) return Q4Q_ERR_CUDA;
+    if (v) cudaMemcpyToSymbol(g_attn_status, &z, sizeof(z));
+    return v;
+}
+
+}  // namespace
+}  // namespace q4q
