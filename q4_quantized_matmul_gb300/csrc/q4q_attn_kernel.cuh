@@ -24,10 +24,10 @@
 //    at most 2^8, and m and E move only when something passes them by 2^6, which a vote over
 //    the warp finds; sums are rescaled only then.
 //
-// Work.  All chunks (16 tokens of a head, 2304 bytes at D = 128) of all pieces -- a sequence, head and tile of
-// rows -- in a row are cut into equal shares, one a CTA, two CTAs an SM, so a ragged batch or one long sequence
-// both fill the GPU.  A producer warp's 32 lanes each find and copy one chunk in 32 (a bulk copy into a ring of
-// 32 slots), the consumer warps take them in turn.  At the end of a piece its consumers' sums are joined in
+// Work.  All steps (two chunks of 16 tokens of a head, 2304 bytes each at D = 128) of all pieces -- a sequence, head and
+// tile of rows -- in a row are cut into equal shares, one a CTA, two CTAs an SM, so a ragged batch or one long
+// sequence both fill the GPU.  A producer warp's 32 lanes each find and copy one chunk in 32 (a bulk copy into a
+// ring of steps), the consumer warps take the steps in turn.  At the end of a piece its consumers' sums are joined in
 // shared memory; what a CTA leaves of a piece to others goes to the workspace as sums with m and l, and
 // a second kernel joins the parts in order.
 #pragma once
@@ -42,6 +42,10 @@ namespace q4q {
 namespace {
 
 __device__ unsigned int g_attn_status = 0;
+
+constexpr int STEP = 2 * KV_GROUP;        // tokens that a warp takes at a time: two chunks
+
+constexpr float NONE = -1e30f;           // the reference of a row that has seen no key: exp2(-inf - NONE) is 0
 
 // What a type of queries is computed as.
 enum Kind { KIND_F32, KIND_F16, KIND_BF16 };
@@ -59,23 +63,27 @@ struct Cfg {
     // Two CTAs of 8 warps an SM where 128 registers are enough (8 B for the sums of a group of columns, 4 B for its
     // queries), so that one's end of a piece hides behind the other's chunks.
     static constexpr int CTAS = B <= 4 && NG == 1 ? 2 : 1;
-    static constexpr int CONSUMERS = B <= 4 && NG == 2 ? 11 : 7;
+    static constexpr int CONSUMERS = 7;
     static constexpr int THREADS = (CONSUMERS + 1) * 32;
-    static constexpr int SLOTS = B > 4 && NG == 2 ? 16 : 32;
+    // Slots of a step each.  A slot is always the same warp's: one that took another's could run a round ahead of it and
+    // mistake the phase before for its own.
+    static constexpr int PER_WARP = B > 4 && NG == 2 ? 1 : 2;
+    static constexpr int SLOTS = PER_WARP * CONSUMERS;
     static constexpr int OUT_STRIDE = DIM + 4;         // of a row of a warp's sums: conflict-free
     static constexpr int BARS = 0;                     // full, then empty
-    static constexpr int META = BARS + 2 * SLOTS * 8;  // of each slot: 1 if its page is not there
-    static constexpr int MISC = META + SLOTS * 4;      // scan and broadcast words
+    static constexpr int META = BARS + 2 * SLOTS * 8;  // [SLOTS][2]: 1 for a chunk that is not there
+    static constexpr int MISC = META + SLOTS * 8;      // scan and broadcast words
     static constexpr int STOP = MISC + 248;            // the abort flag
     static constexpr int STATS = MISC + 256;           // [CONSUMERS][ROWS] reference and sum
     static constexpr int RING = (STATS + CONSUMERS * ROWS * 8 + 127) / 128 * 128;
-    static constexpr int OUT = RING + SLOTS * CHUNK;
+    static constexpr int OUT = RING + SLOTS * 2 * CHUNK;
     static constexpr int BYTES = OUT + CONSUMERS * ROWS * OUT_STRIDE * 4;
+    static_assert(SLOTS <= 16, "a lane of the producer for each half of a slot");
     static_assert(MISC % 8 == 0 && CHUNK % 16 == 0 && OUT % 16 == 0, "alignment of copies and vectors");
     static_assert(BYTES * CTAS <= (227 - CTAS) * 1024, "shared memory of an SM");
 };
 
-// What a worker left in the workspace: a part of a segment (sequence, head, tile), its chunks from .. to - 1
+// What a worker left in the workspace: a part of a segment (sequence, head, tile), its steps from .. to - 1
 // of `of`.
 struct Part {
     int seq, head, tile;
@@ -87,7 +95,7 @@ struct Plan {
     Part* parts;
     float* rows;
     int workers;
-    int least;            // chunks a worker should have at least
+    int least;            // steps a worker should have at least
     int whole;            // 1: a piece is never cut
 };
 
@@ -95,7 +103,7 @@ struct Plan {
 struct Seq {
     int q0, n, len;       // first row, rows, cached tokens
     int tiles;            // of TILE_ROWS rows (tokens x shared heads)
-    int cost;             // chunks that a tile is counted as
+    int cost;             // steps that a tile is counted as
 };
 
 template <int TILE_ROWS>
@@ -115,8 +123,8 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs& a, int s, bool whole) {
     r.len = (int)min(max((int64_t)l, (int64_t)0), most);
     r.tiles = (int)(((int64_t)r.n * a.shared + TILE_ROWS - 1) / TILE_ROWS);
     int64_t keys = r.len;
-    if (a.window > 0) keys = min(keys, a.window + TILE_ROWS + KV_GROUP);  // a tile's rows are at most as many tokens
-    r.cost = whole ? 1 : max(1, (int)((keys + KV_GROUP - 1) / KV_GROUP));
+    if (a.window > 0) keys = min(keys, a.window + TILE_ROWS + STEP);  // a tile's rows are at most as many tokens
+    r.cost = whole ? 1 : max(1, (int)((keys + STEP - 1) / STEP));
     return r;
 }
 
@@ -136,7 +144,7 @@ struct Walk {
     int s;
     Seq seq;
     int head, tile, from, to;  // the piece
-    int g0, g1;                // its chunks: g0 .. g1 - 1 of the sequence
+    int g0, g1;                // its steps: g0 .. g1 - 1 of the sequence
     bool valid;
 };
 
@@ -159,11 +167,11 @@ __device__ __forceinline__ void next_piece(const AttnArgs& a, Walk& w, bool whol
         w.head = (int)(segment / w.seq.tiles);
         w.tile = (int)(segment - (int64_t)w.head * w.seq.tiles);
         w.at += w.to - w.from;
-        // the tile's chunks, and this piece's of them
+        // the tile's steps, and this piece's of them
         int lo, hi, unused;
         keys_of(a, w.seq, w.tile * TILE_ROWS, lo, unused);
         keys_of(a, w.seq, min(w.tile * TILE_ROWS + TILE_ROWS, w.seq.n * a.shared) - 1, unused, hi);
-        const int c0 = lo / KV_GROUP, c1 = (hi + KV_GROUP - 1) / KV_GROUP;
+        const int c0 = lo / STEP, c1 = (hi + STEP - 1) / STEP;
         w.g0 = whole ? c0 : min(c0 + w.from, c1);
         w.g1 = whole ? c1 : min(c0 + w.to, c1);
         w.valid = true;
@@ -236,7 +244,8 @@ __device__ __forceinline__ void lds_scales(uint32_t addr, uint32_t (&v)[(B + 1) 
 
 template <int W>
 __device__ __forceinline__ float scale_at(const uint32_t (&w)[W], int i) {
-    return fp16_to_f32(i & 1 ? w[i >> 1] >> 16 : w[i >> 1]);
+    const __half2 h = *reinterpret_cast<const __half2*>(&w[i >> 1]);
+    return i & 1 ? __high2float(h) : __low2float(h);
 }
 
 // 2^e as fp32, -126 <= e <= 127
@@ -326,26 +335,31 @@ __device__ __forceinline__ Share share_of_worker(const AttnArgs& a, const Plan& 
     return r;
 }
 
-// The producer warp: its lanes find the next SLOTS chunks, one each, and copy each when its slot is free.
+// The producer warp: its lanes find the chunks of the next SLOTS steps, one each (lane 2 i + h: half h of step i), and
+// copy each when its slot is free.
+constexpr int AHEAD = 7;
+
 template <typename C>
 __device__ __forceinline__ void produce(const AttnArgs& a, const Plan& plan, Walk w, uint32_t base, uint8_t* smem) {
-    const int lane = threadIdx.x & 31, in_page = a.page_log - 4;
+    const int lane = threadIdx.x & 31, in_page = a.page_log - 4, step = lane >> 1;
     volatile int* stop = reinterpret_cast<volatile int*>(smem + C::STOP);
+    const uint32_t full = base + C::BARS + step * 8, empty = full + C::SLOTS * 8;
     bool skip_copy = a.fault && blockIdx.x == 0 && lane == 0;
-    int used = 0;                                    // chunks of the piece that are handled
-    uint32_t phase = 0;                              // copies made into this lane's slot
+    int used = 0;                                    // steps of the piece that are handled
+    uint32_t phase = 0;                              // copies made into this lane's half slot
     bool ok = true;
     next_piece<C::ROWS>(a, w, plan.whole);
     while (w.valid) {
         bool mine = false;
-        int s = 0, head = 0, group = 0, filled = 0;
+        int s = 0, head = 0, group = 0, filled = 0, groups = 0;
         while (w.valid && filled < C::SLOTS) {
             const int n = min(w.g1 - w.g0 - used, C::SLOTS - filled);
-            if (lane >= filled && lane < filled + n) {
+            if (step >= filled && step < filled + n) {
                 mine = true;
                 s = w.s;
                 head = w.head;
-                group = w.g0 + used + lane - filled;
+                group = 2 * (w.g0 + used + step - filled) + (lane & 1);
+                groups = (w.seq.len + KV_GROUP - 1) / KV_GROUP;
             }
             filled += n;
             used += n;
@@ -354,16 +368,26 @@ __device__ __forceinline__ void produce(const AttnArgs& a, const Plan& plan, Wal
                 used = 0;
             }
         }
+        // the second half of a sequence's last step may lie behind its last token
         int page = -1;
-        if (mine) page = mx_ld(a.pages + s * a.max_pages + (group >> in_page));
+        if (mine && group < groups) page = mx_ld(a.pages + s * a.max_pages + (group >> in_page));
         const bool there = page >= 0 && page < a.n_pages;
-        if (mine && !there) record_error(&g_attn_status, Q4Q_ERR_ARG);
+        if (mine && group < groups && !there) record_error(&g_attn_status, Q4Q_ERR_ARG);
         const uint8_t* from = a.cache + kv_chunk_offset(there ? page : 0, head, group & ((1 << in_page) - 1), a.kv_heads, a.page_log, C::DIM);
-        const uint32_t full = base + C::BARS + lane * 8, empty = full + C::SLOTS * 8;
-        bool done = !mine;
-        uint64_t t0 = 0;
-        for (uint32_t n = 1; !__all_sync(0xffffffffu, done); ++n) {
-            if (!done && (phase == 0 || mbar_test(empty, (phase - 1) & 1))) {
+        uint32_t open = __ballot_sync(0xffffffffu, mine);
+        while (open) {
+            // Wait for one of the next slots that are still to be filled, not for each of them: they are freed in about this
+            // order.  (One that is filled already would be waited for in vain, where its step is of a piece behind this one's.)
+            const int next = 31 - __clz(open & (0xffffffffu >> (31 - min(__ffs(open) - 1 + AHEAD, 31))));
+            const uint32_t its = __shfl_sync(0xffffffffu, phase, next), bar = __shfl_sync(0xffffffffu, empty, next);
+            if (its > 0) {
+                const bool free = mbar_try_wait(bar, (its - 1) & 1) || mbar_wait_until(bar, (its - 1) & 1, stop, a.limit_ns);
+                if (!__all_sync(0xffffffffu, free)) {
+                    ok = false;
+                    break;
+                }
+            }
+            if (mine && (phase == 0 || mbar_test(empty, (phase - 1) & 1))) {
                 reinterpret_cast<volatile int*>(smem + C::META)[lane] = !there;
                 if (there) {
                     mbar_arrive_expect_tx(full, C::CHUNK);
@@ -373,35 +397,27 @@ __device__ __forceinline__ void produce(const AttnArgs& a, const Plan& plan, Wal
                 }
                 skip_copy = false;
                 ++phase;
-                done = true;
-            } else if (!done && (n & 63u) == 0u) {
-                // a consumer gave up, or none has freed this slot in time
-                const uint64_t now = global_timer_ns();
-                if (t0 == 0) t0 = now;
-                if (*stop || now - t0 > a.limit_ns) {
-                    ok = false;
-                    done = true;
-                }
+                mine = false;
             }
+            open = __ballot_sync(0xffffffffu, mine);
         }
-        ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
     }
     if (!ok) *stop = 1;
     // copies in flight must land before this CTA's shared memory is another's: consumers that gave up leave some
-    if (phase > 0) mbar_wait_bounded(base + C::BARS + lane * 8, (phase - 1) & 1, a.limit_ns);
+    if (phase > 0) mbar_wait_bounded(full, (phase - 1) & 1, a.limit_ns);
     __syncwarp();
 }
 
 template <typename C>
 __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ Plan plan) {
-    constexpr int B = C::B, NG = C::NG, CONSUMERS = C::CONSUMERS;
+    constexpr int B = C::B, NG = C::NG, CONSUMERS = C::CONSUMERS, W = (B + 1) / 2;
     using T = typename C::T;
     extern __shared__ __align__(128) uint8_t smem[];
     const uint32_t base = smem_u32(smem);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     volatile int* stop = reinterpret_cast<volatile int*>(smem + C::STOP);
-    if (tid < 2 * C::SLOTS) mbar_init(base + C::BARS + tid * 8, 1);
+    if (tid < 2 * C::SLOTS) mbar_init(base + C::BARS + tid * 8, tid < C::SLOTS ? 2 : 1);
     if (tid == 0) *stop = 0;
     fence_mbar_init();
     pdl_trigger();
@@ -424,18 +440,19 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_kernel(const __grid_
 
     float2* stats = reinterpret_cast<float2*>(smem + C::STATS);
     float* out = reinterpret_cast<float*>(smem + C::OUT);
-    uint32_t numbered = 0;                           // chunks of this CTA before the piece's
+    int numbered = 0;                                // steps of this CTA before the piece's
+    int taken = 0;                                   // steps of this warp: the CTA's every CONSUMERS-th
     bool dead = false;                               // a wait ran out: the rest is passed over
     while (true) {
         next_piece<C::ROWS>(a, work, plan.whole);
         if (!work.valid) break;
         const Seq& seq = work.seq;
-        const int rows = seq.n * a.shared, tile0 = work.tile * C::ROWS, chunks = work.g1 - work.g0;
+        const int rows = seq.n * a.shared, tile0 = work.tile * C::ROWS, steps = work.g1 - work.g0;
 
         // The queries' operand.  Lane (g, t) holds column g's dims 32 b + 8 t .. + 7, scaled by a power of two so that the
         // row's largest is in [2^14, 2^15), in the order of the codes' nibbles: (0, 4), (1, 5), (2, 6), (3, 7).
         uint32_t qf[NG][B][4];
-        float off[NG][C::CENTRED ? 1 : B][2];
+        uint32_t off[NG][2];                         // -8 sum q of each block, in two fp16: blocks 2t, 2t + 1 of column g
         float row_scale[NG][2];
         int lo[NG][2], hi[NG][2];                    // keys that this lane's columns 2t, 2t + 1 see
 #pragma unroll
@@ -444,7 +461,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_kernel(const __grid_
             const T* from = static_cast<const T*>(a.q) + (int64_t)(seq.q0 + row / a.shared) * a.q_stride +
                             (int64_t)(work.head * a.shared + row % a.shared) * C::DIM + 8 * t;
             float v[B][8];
-            float top = 0.0f;
+            float top = 0.0f, off_low = 0.0f;
+            off[q][0] = off[q][1] = 0u;
 #pragma unroll
             for (int b = 0; b < B; ++b) {
                 row_load(from + 32 * b, a.align, v[b]);
@@ -469,11 +487,12 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_kernel(const __grid_
                     for (int k = 0; k < 8; ++k) sum += v[b][k];
                     sum += __shfl_xor_sync(0xffffffffu, sum, 1);
                     sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                    sum *= -8.0f * 5.9604644775390625e-8f;                        // 2^-24
-                    const bool high = !C::SPLIT || t < 2;
-                    const float s0 = __shfl_sync(0xffffffffu, sum, 8 * t), s1 = __shfl_sync(0xffffffffu, sum, 8 * t + 4);
-                    off[q][b][0] = high ? s0 : 0.0f;
-                    off[q][b][1] = high ? s1 : 0.0f;
+                    sum *= C::SPLIT && g >= 4 ? 0.0f : -8.0f * 5.9604644775390625e-8f;   // 2^-24
+                    if (b % 2 == 0) off_low = sum;
+                    if ((b % 2 == 1 || b == B - 1) && t == b / 2) {
+                        off[q][0] = half2_bits(off_low, b % 2 ? sum : 0.0f);
+                        off[q][1] = rest2(off_low, b % 2 ? sum : 0.0f, off[q][0]);
+                    }
                 }
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -502,13 +521,13 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_kernel(const __grid_
                 for (int i = 0; i < 8; ++i) o[q][b][i / 4][i % 4] = 0.0f;
         float m[NG][2], l[NG][2], ref[NG][2];        // of columns 2t, 2t + 1: the maximum referred to; this lane's sum; m + E - 8
 #pragma unroll
-        for (int q = 0; q < NG; ++q) m[q][0] = m[q][1] = ref[q][0] = ref[q][1] = -INFINITY, l[q][0] = l[q][1] = 0.0f;
+        for (int q = 0; q < NG; ++q) m[q][0] = m[q][1] = -INFINITY, ref[q][0] = ref[q][1] = NONE, l[q][0] = l[q][1] = 0.0f;
         int top_e = -32;                             // E: the values' scales are below 2^E
 
-        const int start = (int)((uint32_t)(warp + CONSUMERS) - numbered % CONSUMERS) % CONSUMERS;
-        for (int i = start; i < chunks && !dead; i += CONSUMERS) {
-            const uint32_t number = numbered + i, slot = number % C::SLOTS, full = base + C::BARS + slot * 8;
-            const uint32_t chunk = base + C::RING + slot * C::CHUNK, parity = (number / C::SLOTS) & 1;
+        const int start = warp + CONSUMERS * taken - numbered;
+        for (int i = start; i < steps && !dead; i += CONSUMERS, ++taken) {
+            const uint32_t slot = warp + CONSUMERS * (taken % C::PER_WARP), parity = (taken / C::PER_WARP) & 1;
+            const uint32_t full = base + C::BARS + slot * 8, chunk = base + C::RING + slot * 2 * C::CHUNK;
             const bool ok = mbar_try_wait(full, parity) || mbar_wait_until(full, parity, stop, a.limit_ns);
             if (!__all_sync(0xffffffffu, ok)) {
                 dead = true;
@@ -518,29 +537,40 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_kernel(const __grid_
                 }
                 break;
             }
-            if (reinterpret_cast<volatile int*>(smem + C::META)[slot]) {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(full + C::SLOTS * 8);
-                continue;
-            }
-            const int key0 = (work.g0 + i) * KV_GROUP;
-            const bool edge = key0 < lo_all || key0 + KV_GROUP > hi_all;
+            uint32_t gone[2];                        // chunks that are not there
+            lds<2>(base + C::META + slot * 8, gone);
+            const int key0 = (work.g0 + i) * STEP;
+            const bool edge = key0 < lo_all || key0 + STEP > hi_all || (gone[0] | gone[1]);
 
-            // scores of keys g, g + 8 and columns 2t, 2t + 1
-            float y[NG][4];
-            uint32_t dv[2][(B + 1) / 2];
-            {
-                uint32_t w[2][B], dk[2][(B + 1) / 2];
+            // scores of keys g + 8 j and columns 2t, 2t + 1
+            float y[NG][8];
+            uint32_t dv[4][W];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t at = chunk + h * C::CHUNK;
+                uint32_t w[2][B], dk[2][W];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    lds<B>(chunk + (j * 32 + lane) * 4 * B, w[j]);
-                    lds_scales<B>(chunk + 16 * C::DIM + (j * 8 + g) * 2 * B, dk[j]);
+                    lds<B>(at + (j * 32 + lane) * 4 * B, w[j]);
+                    lds_scales<B>(at + 16 * C::DIM + (j * 8 + g) * 2 * B, dk[j]);
+                    lds_scales<B>(at + 17 * C::DIM + (j * 8 + g) * 2 * B, dv[2 * h + j]);
                 }
 #pragma unroll
-                for (int j = 0; j < 2; ++j) lds_scales<B>(chunk + 17 * C::DIM + (j * 8 + g) * 2 * B, dv[j]);
-                uint64_t s[NG][2];
+                for (int q = 0; q < NG; ++q) {
+                    float first[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    if constexpr (!C::CENTRED) {
+                        // sum_b d_b (-8 sum q): 8 blocks deep, the high and the low halves of the sums
+                        uint32_t d[2];
 #pragma unroll
-                for (int q = 0; q < NG; ++q) s[q][0] = s[q][1] = 0;
+                        for (int j = 0; j < 2; ++j) {
+                            d[j] = t & 1 ? dk[j][1 % W] : dk[j][0];
+                            if constexpr (W > 2) d[j] = t & 2 ? (t & 1 ? dk[j][3 % W] : dk[j][2 % W]) : d[j];
+                        }
+                        mma_f16(first, d[0], d[1], d[0], d[1], off[q][0], off[q][1], 0.0f, 0.0f, 0.0f, 0.0f);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) y[q][4 * h + k] = first[k];
+                }
 #pragma unroll
                 for (int b = 0; b < B; ++b) {
                     uint32_t c[2][4];                // codes of key g, g + 8: nibbles (0, 4), (1, 5), (2, 6), (3, 7)
@@ -558,59 +588,64 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_kernel(const __grid_
 #pragma unroll
                     for (int q = 0; q < NG; ++q) {
                         float acc[4];
-                        const float o0 = C::CENTRED ? 0.0f : off[q][C::CENTRED ? 0 : b][0], o1 = C::CENTRED ? 0.0f : off[q][C::CENTRED ? 0 : b][1];
-                        mma_f16(acc, c[0][0], c[1][0], c[0][1], c[1][1], qf[q][b][0], qf[q][b][1], o0, o1, o0, o1);
+                        mma_f16(acc, c[0][0], c[1][0], c[0][1], c[1][1], qf[q][b][0], qf[q][b][1], 0.0f, 0.0f, 0.0f, 0.0f);
                         mma_f16(acc, c[0][2], c[1][2], c[0][3], c[1][3], qf[q][b][2], qf[q][b][3]);
-                        s[q][0] = ffma2(pack2(acc[0], acc[1]), pack2(d0, d0), s[q][0]);
-                        s[q][1] = ffma2(pack2(acc[2], acc[3]), pack2(d1, d1), s[q][1]);
-                    }
-                }
-#pragma unroll
-                for (int q = 0; q < NG; ++q) {
-                    unpack2(s[q][0], y[q][0], y[q][1]);
-                    unpack2(s[q][1], y[q][2], y[q][3]);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        if constexpr (C::SPLIT) y[q][k] += __shfl_xor_sync(0xffffffffu, y[q][k], 2);
-                        y[q][k] *= row_scale[q][k & 1];
+                        float* z = y[q] + 4 * h;
+                        z[0] = fmaf(acc[0], d0, z[0]), z[1] = fmaf(acc[1], d0, z[1]);
+                        z[2] = fmaf(acc[2], d1, z[2]), z[3] = fmaf(acc[3], d1, z[3]);
                     }
                 }
             }
-            if (edge) {
-                // keys that a row does not see, and the scales of slots that no row does
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int key = key0 + 8 * j + g;
-#pragma unroll
-                    for (int q = 0; q < NG; ++q) {
-                        if (key < lo[q][0] || key >= hi[q][0]) y[q][2 * j] = -INFINITY;
-                        if (key < lo[q][1] || key >= hi[q][1]) y[q][2 * j + 1] = -INFINITY;
-                    }
-                    if (key >= seq.len)
-#pragma unroll
-                        for (int k = 0; k < (B + 1) / 2; ++k) dv[j][k] = 0u;
-                }
-            }
-            uint32_t bits = 0;
-#pragma unroll
-            for (int k = 0; k < (B + 1) / 2; ++k) bits = __vmaxu2(bits, __vmaxu2(dv[0][k], dv[1][k]));
-            bits = max(bits >> 16, bits & 0xFFFFu);
-            bool grows = (int)(bits >> 10) - 14 > top_e;                           // a scale is below 2^(exponent field - 14)
-            float x[NG][4];
 #pragma unroll
             for (int q = 0; q < NG; ++q)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    x[q][k] = y[q][k] - ref[q][k & 1];
-                    grows |= x[q][k] > (float)(14 - top_e);                        // y > m + 6
+                for (int k = 0; k < 8; ++k) {
+                    if constexpr (C::SPLIT) y[q][k] += __shfl_xor_sync(0xffffffffu, y[q][k], 2);
+                    y[q][k] *= row_scale[q][k & 1];
                 }
+            bool careful = false;
+            if (edge) {
+                // keys that a row does not see, and the scales of slots that no row does
+                uint32_t odd = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int key = key0 + 8 * j + g;
+                    const bool lost = gone[j / 2];
+#pragma unroll
+                    for (int q = 0; q < NG; ++q) {
+                        if (key < lo[q][0] || key >= hi[q][0] || lost) y[q][2 * j] = -INFINITY;
+                        if (key < lo[q][1] || key >= hi[q][1] || lost) y[q][2 * j + 1] = -INFINITY;
+                    }
+#pragma unroll
+                    for (int k = 0; k < W; ++k) {
+                        if (key >= seq.len || lost) dv[j][k] = 0u;
+                        odd |= __vcmpgtu2(dv[j][k] & 0x7FFF7FFFu, 0x7BFF7BFFu);
+                    }
+                }
+                // a scale that is no number, in a step that not every row sees: weights of 0 have to stay 0
+                careful = __any_sync(0xffffffffu, odd != 0);
+            }
+            uint32_t bits = 0;
+#pragma unroll
+            for (int k = 0; k < W; ++k) bits = __vmaxu2(__vmaxu2(bits, __vmaxu2(dv[0][k], dv[1][k])), __vmaxu2(dv[2][k], dv[3][k]));
+            bits = max(bits >> 16, bits & 0xFFFFu);
+            bool grows = (int)(bits >> 10) - 14 > top_e;                           // a scale is below 2^(exponent field - 14)
+            float x[NG][8], most = -INFINITY;
+#pragma unroll
+            for (int q = 0; q < NG; ++q)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    x[q][k] = y[q][k] - ref[q][k & 1];
+                    most = fmaxf(most, x[q][k]);
+                }
+            grows |= most > (float)(14 - top_e);                                   // a y > m + 6
             if (__any_sync(0xffffffffu, grows)) {
                 // an infinite or NaN scale makes its own dims so, and says nothing about the others'
                 uint32_t finite = 0;
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                for (int j = 0; j < 4; ++j)
 #pragma unroll
-                    for (int k = 0; k < (B + 1) / 2; ++k) {
+                    for (int k = 0; k < W; ++k) {
                         const uint32_t h0 = dv[j][k] & 0x7FFFu, h1 = (dv[j][k] >> 16) & 0x7FFFu;
                         finite = max(finite, max(h0 < 0x7C00u ? h0 : 0u, h1 < 0x7C00u ? h1 : 0u));
                     }
@@ -619,62 +654,69 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_kernel(const __grid_
                 for (int q = 0; q < NG; ++q)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        float n = fmaxf(y[q][c], y[q][2 + c]);
+                        float n = fmaxf(fmaxf(y[q][c], y[q][2 + c]), fmaxf(y[q][4 + c], y[q][6 + c]));
                         n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, 4));
                         n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, 8));
                         n = fmaxf(m[q][c], fmaxf(n, __shfl_xor_sync(0xffffffffu, n, 16)));
                         const float down = m[q][c] == -INFINITY ? 0.0f : exp2f((m[q][c] - n) + (float)(top_e - e));
                         m[q][c] = n;
-                        ref[q][c] = n + (float)(e - 8);
+                        ref[q][c] = n == -INFINITY ? NONE : n + (float)(e - 8);
                         l[q][c] *= down;
 #pragma unroll
                         for (int b = 0; b < B; ++b) o[q][b][0][c] *= down, o[q][b][0][2 + c] *= down, o[q][b][1][c] *= down, o[q][b][1][2 + c] *= down;
-                        x[q][c] = y[q][c] - ref[q][c];
-                        x[q][2 + c] = y[q][2 + c] - ref[q][c];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) x[q][2 * j + c] = y[q][2 * j + c] - ref[q][c];
                     }
                 top_e = e;
             }
 #pragma unroll
             for (int q = 0; q < NG; ++q)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
+                for (int k = 0; k < 8; ++k) {
                     x[q][k] = ex2(x[q][k]);                                        // from here the weight
-                    if (edge && y[q][k] == -INFINITY) x[q][k] = 0.0f;
                     l[q][k & 1] += x[q][k];
                 }
-            uint32_t w[2][B];
+            const auto values = [&](auto of_care) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) lds<B>(chunk + 8 * C::DIM + (j * 32 + lane) * 4 * B, w[j]);
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t w[2][B];
 #pragma unroll
-            for (int b = 0; b < B; ++b) {
-                const float d0 = scale_at(dv[0], b), d1 = scale_at(dv[1], b);
-                const uint4 c0 = nibbles_to_f16x8(w[0][b]), c1 = nibbles_to_f16x8(w[1][b]);
+                    for (int j = 0; j < 2; ++j) lds<B>(chunk + h * C::CHUNK + 8 * C::DIM + (j * 32 + lane) * 4 * B, w[j]);
 #pragma unroll
-                for (int q = 0; q < NG; ++q) {
-                    float p[4] = {x[q][0] * d0, x[q][1] * d0, x[q][2] * d1, x[q][3] * d1};
-                    if (edge)                                                      // a scale may be anything where the weight is none
+                    for (int b = 0; b < B; ++b) {
+                        const float d0 = scale_at(dv[2 * h], b), d1 = scale_at(dv[2 * h + 1], b);
+                        const uint4 c0 = nibbles_to_f16x8(w[0][b]), c1 = nibbles_to_f16x8(w[1][b]);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            if (y[q][k] == -INFINITY) p[k] = 0.0f;
-                    uint32_t p0 = half2_bits(p[0], p[1]), p1 = half2_bits(p[2], p[3]);
-                    if constexpr (C::SPLIT) {
-                        const uint32_t r0 = rest2(p[0], p[1], p0), r1 = rest2(p[2], p[3], p1);
-                        p0 = t < 2 ? p0 : r0;
-                        p1 = t < 2 ? p1 : r1;
+                        for (int q = 0; q < NG; ++q) {
+                            const float* z = x[q] + 4 * h;
+                            float p[4] = {z[0] * d0, z[1] * d0, z[2] * d1, z[3] * d1};
+                            if constexpr (decltype(of_care)::value)
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    if (y[q][4 * h + k] == -INFINITY) p[k] = 0.0f;
+                            uint32_t p0 = half2_bits(p[0], p[1]), p1 = half2_bits(p[2], p[3]);
+                            if constexpr (C::SPLIT) {
+                                const uint32_t r0 = rest2(p[0], p[1], p0), r1 = rest2(p[2], p[3], p1);
+                                p0 = t < 2 ? p0 : r0;
+                                p1 = t < 2 ? p1 : r1;
+                            }
+                            p0 = transposed(p0);
+                            p1 = transposed(p1);
+                            mma_f16(o[q][b][0], c0.x, c0.y, c1.x, c1.y, p0, p1);
+                            mma_f16(o[q][b][1], c0.z, c0.w, c1.z, c1.w, p0, p1);
+                        }
                     }
-                    p0 = transposed(p0);
-                    p1 = transposed(p1);
-                    mma_f16(o[q][b][0], c0.x, c0.y, c1.x, c1.y, p0, p1);
-                    mma_f16(o[q][b][1], c0.z, c0.w, c1.z, c1.w, p0, p1);
                 }
-            }
-            __syncwarp();                            // the chunk is read by all lanes before it is written again
+            };
+            if (careful) values(std::true_type{});
+            else values(std::false_type{});
+            __syncwarp();                            // the step is read by all lanes before it is written again
             if (lane == 0) mbar_arrive(full + C::SLOTS * 8);
         }
-        numbered += (uint32_t)chunks;
+        numbered += steps;
 
         // Join the warps: of column 2t + c this lane's dims 32 b + 4 g .. + 3, its reference and sum.
-        const bool any = start < chunks;
+        const bool any = start < steps;
 #pragma unroll
         for (int q = 0; q < NG; ++q)
 #pragma unroll
@@ -818,7 +860,7 @@ q4q_status run(const AttnArgs& a, void* workspace, cudaStream_t stream, const De
     if (e != cudaSuccess) return cudaGetLastError(), Q4Q_ERR_CUDA;
     Plan plan;
     plan.workers = info.sm_count * C::CTAS;
-    plan.whole = (a.max_pages << a.page_log) <= KV_GROUP * C::CONSUMERS;
+    plan.whole = (a.max_pages << a.page_log) <= STEP * C::CONSUMERS;
     plan.least = plan.whole ? 1 : C::CONSUMERS;
     plan.parts = static_cast<Part*>(workspace);
     plan.rows = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + mx_up((int64_t)sizeof(Part) * 2 * plan.workers, 256));
