@@ -14,6 +14,8 @@
 // codes of values as pairs of consecutive keys, the depth of the second product.
 #pragma once
 
+#include <type_traits>
+
 #include "q4q_mx.cuh"
 #include "q4q_mx_tc.cuh"
 
@@ -40,41 +42,101 @@ __device__ __forceinline__ int kv_scale(bool v, int i, int b, int dim) { return 
 
 // ---------------------------------------------------------- rows of a head --
 
-// A lane holds 8 consecutive values of a row; a row takes LANES lanes (8, 16 or 32, D / 8 of them in
-// use), so a warp holds 32 / LANES rows.
+// A lane holds 8 consecutive values of a row as 4 pairs, which the two-lane fp32 instructions take; a row takes LANES
+// lanes (8, 16 or 32, D / 8 of them in use), so a warp holds 32 / LANES rows.
+struct Row8 {
+    uint64_t p[4];
+    __device__ __forceinline__ void clear() { p[0] = p[1] = p[2] = p[3] = 0; }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) unpack2(p[i], v[2 * i], v[2 * i + 1]);
+    }
+    __device__ __forceinline__ void set(const float (&v)[8]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = pack2(v[2 * i], v[2 * i + 1]);
+    }
+};
+
+// a + b and a - b.  Where a or b is a product the assembler may contract both into one multiply-add (it does, for the two-lane
+// forms, whatever their rounding says): only for sums that take no harm from it.
+__device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) { return ffma2(a, pack2(1.0f, 1.0f), b); }
+__device__ __forceinline__ uint64_t fsub2(uint64_t a, uint64_t b) { return ffma2(b, pack2(-1.0f, -1.0f), a); }
+
+// what a row's 8 values of a lane are loaded as
+template <typename T>
+struct Raw8 {
+    uint4 w[sizeof(T) / 2];
+};
 
 // 8 values at p; `align`: of every row's start, in bytes
 template <typename T>
-__device__ __forceinline__ void row_load(const T* p, int align, float (&v)[8]) {
-    if constexpr (sizeof(T) == 4) {
-        if (align >= 16) {
-            const uint4 a = mx_ld(reinterpret_cast<const uint4*>(p)), b = mx_ld(reinterpret_cast<const uint4*>(p) + 1);
-            v[0] = __uint_as_float(a.x), v[1] = __uint_as_float(a.y), v[2] = __uint_as_float(a.z), v[3] = __uint_as_float(a.w);
-            v[4] = __uint_as_float(b.x), v[5] = __uint_as_float(b.y), v[6] = __uint_as_float(b.z), v[7] = __uint_as_float(b.w);
-            return;
+__device__ __forceinline__ void raw_load(const T* p, int align, Raw8<T>& r) {
+    if (align >= 16) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.w[i] = mx_ld(reinterpret_cast<const uint4*>(p) + i);
+    } else {
+        uint32_t b[4 * (sizeof(T) / 2)];
+#pragma unroll
+        for (int i = 0; i < 4 * (int)sizeof(T) / 2; ++i) {
+            if constexpr (sizeof(T) == 4) b[i] = mx_ld(reinterpret_cast<const uint32_t*>(p) + i);
+            else b[i] = (uint32_t)mx_ld(reinterpret_cast<const uint16_t*>(p) + 2 * i) | (uint32_t)mx_ld(reinterpret_cast<const uint16_t*>(p) + 2 * i + 1) << 16;
         }
-    } else if (align >= 16) {
-        const uint4 a = mx_ld(reinterpret_cast<const uint4*>(p));
-        const T* h = reinterpret_cast<const T*>(&a);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = mx_to_f32(h[e]);
-        return;
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.w[i] = make_uint4(b[4 * i], b[4 * i + 1], b[4 * i + 2], b[4 * i + 3]);
     }
+}
+__device__ __forceinline__ void raw_get(const Raw8<float>& r, Row8& v) {
+    v.p[0] = (uint64_t)r.w[0].y << 32 | r.w[0].x, v.p[1] = (uint64_t)r.w[0].w << 32 | r.w[0].z;
+    v.p[2] = (uint64_t)r.w[1].y << 32 | r.w[1].x, v.p[3] = (uint64_t)r.w[1].w << 32 | r.w[1].z;
+}
+__device__ __forceinline__ void raw_get(const Raw8<__half>& r, Row8& v) {
+    const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = mx_to_f32(mx_ld(p + e));
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        v.p[i] = pack2(f.x, f.y);
+    }
+}
+__device__ __forceinline__ void raw_get(const Raw8<__nv_bfloat16>& r, Row8& v) {
+    const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v.p[i] = pack2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
 }
 
 template <typename T>
-__device__ __forceinline__ void row_store(T* p, int align, const float (&v)[8]) {
-    T h[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) h[e] = mx_from_f32<T>(v[e]);
+__device__ __forceinline__ void row_load(const T* p, int align, float (&v)[8]) {
+    Raw8<T> r;
+    raw_load(p, align, r);
+    Row8 x;
+    raw_get(r, x);
+    x.get(v);
+}
+
+template <typename T>
+__device__ __forceinline__ void row_store(T* p, int align, const Row8& x) {
+    float v[8];
+    x.get(v);
     if (align >= 16) {
+        if constexpr (sizeof(T) == 4) {
+            reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+            reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+            uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(p)[i] = reinterpret_cast<const uint4*>(h)[i];
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (std::is_same_v<T, __half>) {
+                    const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+                    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+                } else {
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+                    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+                }
+            }
+            *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) p[e] = h[e];
+        for (int e = 0; e < 8; ++e) p[e] = mx_from_f32<T>(v[e]);
     }
 }
 
@@ -85,94 +147,136 @@ __device__ __forceinline__ float two_sum(float a, float b, float& lost) {
     return s;
 }
 
-// 1 / sqrt(mean of squares + eps), correctly rounded to fp32 but for about one row in 2^20: what
-// 64-bit arithmetic gives, so that a cached code next to a border does not depend on the order of a
-// sum.  Sums are kept as two fp32 (the products' and sums' roundings are carried on), about 12
-// fp32 operations a value; in fp64, of which this chip does a 64th as many, 8192 tokens' keys would
-// take 90 us.  inv_dim: 1 / D as two fp32.  The estimate y of rsqrtf takes one Newton step,
-// y - y (a y^2 - 1) / 2, whose residual is computed from the exact square of y.
-template <int LANES>
-__device__ __forceinline__ float inverse_norm(const float (&v)[8], float2 inv_dim, float eps) {
-    float hi = 0.0f, lo = 0.0f;
+// 1 / sqrt(mean of squares + eps) of 4 rows, of which a lane holds 8 values each, correctly rounded to fp32 but for
+// about one row in 2^20: what 64-bit arithmetic gives, so that a cached code next to a border does not depend on the
+// order of a sum.  Sums are kept as two fp32 (what the squares' and sums' roundings lose is carried on); fp64, of which
+// this chip does a 64th as many, would take 90 us for 8192 tokens' keys.  The lanes of a row halve the rows among them
+// in the first two steps of the sum, so that each ends with one row's, takes its root and hands it round.  inv_dim:
+// 1 / D as two fp32.  The estimate y of rsqrtf takes one Newton step, y - y (a y^2 - 1) / 2, whose residual
+// is computed from the exact square of y.  EXACT: squares of 16-bit values are exact in fp32.  (A square contracted into its
+// sum changes that sum by at most its own rounding, which the two-sum then carries on.)
+template <int LANES, bool EXACT>
+__device__ __forceinline__ void inverse_norm4(const Row8 (&v)[4], float2 inv_dim, float eps, float (&r)[4]) {
+    const int lane = threadIdx.x & 31;
+    float hi[4], lo[4], lost;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float p = __fmul_rn(v[e], v[e]);
-        float lost;
-        hi = two_sum(hi, p, lost);
-        lo = __fadd_rn(lo, __fadd_rn(__fmaf_rn(v[e], v[e], -p), lost));
+    for (int n = 0; n < 4; ++n) {
+        uint64_t h = 0, l = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint64_t p = fmul2(v[n].p[i], v[n].p[i]);
+            if constexpr (!EXACT) l = fadd2(l, ffma2(v[n].p[i], v[n].p[i], fmul2(p, pack2(-1.0f, -1.0f))));
+            if (i == 0) {
+                h = p;
+            } else {
+                const uint64_t s = fadd2(h, p), bb = fsub2(s, h);
+                l = fadd2(l, fadd2(fsub2(h, fsub2(s, bb)), fsub2(p, bb)));
+                h = s;
+            }
+        }
+        float h0, h1, l0, l1;
+        unpack2(h, h0, h1);
+        unpack2(l, l0, l1);
+        hi[n] = two_sum(h0, h1, lost);
+        lo[n] = __fadd_rn(__fadd_rn(l0, l1), lost);
+    }
+    int d = LANES / 2;
+    bool upper = lane & d;
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+        const float h2 = __shfl_xor_sync(0xffffffffu, upper ? hi[n] : hi[n + 2], d), l2 = __shfl_xor_sync(0xffffffffu, upper ? lo[n] : lo[n + 2], d);
+        hi[n] = two_sum(upper ? hi[n + 2] : hi[n], h2, lost);
+        lo[n] = __fadd_rn(__fadd_rn(upper ? lo[n + 2] : lo[n], l2), lost);
+    }
+    d /= 2;
+    upper = lane & d;
+    float h = upper ? hi[1] : hi[0], l = upper ? lo[1] : lo[0];
+    {
+        const float h2 = __shfl_xor_sync(0xffffffffu, upper ? hi[0] : hi[1], d), l2 = __shfl_xor_sync(0xffffffffu, upper ? lo[0] : lo[1], d);
+        h = two_sum(h, h2, lost);
+        l = __fadd_rn(__fadd_rn(l, l2), lost);
     }
 #pragma unroll
-    for (int d = 1; d < LANES; d <<= 1) {
-        const float h2 = __shfl_xor_sync(0xffffffffu, hi, d), l2 = __shfl_xor_sync(0xffffffffu, lo, d);
-        float lost;
-        hi = two_sum(hi, h2, lost);
-        lo = __fadd_rn(__fadd_rn(lo, l2), lost);
+    for (d /= 2; d > 0; d /= 2) {
+        const float h2 = __shfl_xor_sync(0xffffffffu, h, d), l2 = __shfl_xor_sync(0xffffffffu, l, d);
+        h = two_sum(h, h2, lost);
+        l = __fadd_rn(__fadd_rn(l, l2), lost);
     }
-    float lost;
-    hi = two_sum(hi, lo, lost);
-    lo = lost;
-    const float m = __fmul_rn(hi, inv_dim.x);
-    const float m_lo = __fmaf_rn(hi, inv_dim.y, __fmaf_rn(lo, inv_dim.x, __fmaf_rn(hi, inv_dim.x, -m)));
+    h = two_sum(h, l, lost);
+    l = lost;
+    const float m = __fmul_rn(h, inv_dim.x);
+    const float m_lo = __fmaf_rn(h, inv_dim.y, __fmaf_rn(l, inv_dim.x, __fmaf_rn(h, inv_dim.x, -m)));
     float a = two_sum(m, eps, lost);
     float a_lo = __fadd_rn(lost, m_lo);
     a = two_sum(a, a_lo, lost);
     a_lo = lost;
     const float y = rsqrtf(a), y2 = __fmul_rn(y, y), y2_lo = __fmaf_rn(y, y, -y2);
     const float residual = __fadd_rn(__fmaf_rn(a, y2, -1.0f), __fmaf_rn(a, y2_lo, __fmul_rn(a_lo, y2)));
-    return __fmaf_rn(__fmul_rn(-0.5f, y), residual, y);
+    const float mine = __fmaf_rn(__fmul_rn(-0.5f, y), residual, y);
+#pragma unroll
+    for (int n = 0; n < 4; ++n) r[n] = __shfl_sync(0xffffffffu, mine, (lane & ~(LANES - 1)) | (n & 2 ? LANES / 2 : 0) | (n & 1 ? LANES / 4 : 0));
 }
 
-// cosines and sines of a lane's values: pairs (i, i + rot / 2), or (2i, 2i + 1)
+// Cosines and sines of a lane's values: pairs (i, i + rot / 2), or (2i, 2i + 1).  Of a pair (a, b) the first becomes
+// a c - b s, the second b c + a s: s has its sign here.
 struct Turn {
-    float c[8], s[8];
+    Row8 c, s;
+    int from;           // the lane that holds the partners (pairs of halves)
     bool turns;
 };
 
-// `at`: the lane's first value; row: the position's of a table [.][rot] (rot a multiple of 16)
-__device__ __forceinline__ void turn_load(Turn& w, const float* row, int rot, bool halves, int at) {
+__device__ __forceinline__ uint64_t pair_of(uint32_t x, uint32_t y) { return (uint64_t)y << 32 | x; }
+
+// What does not depend on the position; `at`: the lane's first value, rot a multiple of 16.
+__device__ __forceinline__ void turn_init(Turn& w, int rot, bool halves, int at) {
+    const int lane = threadIdx.x & 31;
     w.turns = at < rot;
-    const int half = rot / 2;
+    w.from = halves && w.turns ? (at >= rot / 2 ? lane - rot / 16 : lane + rot / 16) : lane;
+    w.c.clear();
+    w.s.clear();
+}
+
+// row: the position's of a table [.][rot]; back: the opposite angle
+__device__ __forceinline__ void turn_load(Turn& w, const float* row, int rot, bool halves, int at, bool back) {
     if (!w.turns) return;
+    const int half = rot / 2;
     if (halves) {
         const bool second = at >= half;
-        const int i = second ? at - half : at;
-#pragma unroll
-        for (int e = 0; e < 8; e += 4) {
-            const uint4 c = mx_ld(reinterpret_cast<const uint4*>(row + i + e)), s = mx_ld(reinterpret_cast<const uint4*>(row + half + i + e));
-            w.c[e] = __uint_as_float(c.x), w.c[e + 1] = __uint_as_float(c.y), w.c[e + 2] = __uint_as_float(c.z), w.c[e + 3] = __uint_as_float(c.w);
-            w.s[e] = __uint_as_float(s.x), w.s[e + 1] = __uint_as_float(s.y), w.s[e + 2] = __uint_as_float(s.z), w.s[e + 3] = __uint_as_float(s.w);
-        }
-        // the first of a pair takes a c - b s, the second b c + a s
-        if (!second)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) w.s[e] = -w.s[e];
+        const uint4* c = reinterpret_cast<const uint4*>(row + (second ? at - half : at));
+        const uint4 c0 = mx_ld(c), c1 = mx_ld(c + 1), s0 = mx_ld(c + half / 4), s1 = mx_ld(c + half / 4 + 1);
+        const uint32_t flip = second != back ? 0u : 0x80000000u;
+        w.c.p[0] = pair_of(c0.x, c0.y), w.c.p[1] = pair_of(c0.z, c0.w), w.c.p[2] = pair_of(c1.x, c1.y), w.c.p[3] = pair_of(c1.z, c1.w);
+        w.s.p[0] = pair_of(s0.x ^ flip, s0.y ^ flip), w.s.p[1] = pair_of(s0.z ^ flip, s0.w ^ flip);
+        w.s.p[2] = pair_of(s1.x ^ flip, s1.y ^ flip), w.s.p[3] = pair_of(s1.z ^ flip, s1.w ^ flip);
     } else {
         const uint4 c = mx_ld(reinterpret_cast<const uint4*>(row + at / 2)), s = mx_ld(reinterpret_cast<const uint4*>(row + half + at / 2));
-        const uint32_t cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            w.c[e] = __uint_as_float(cc[e / 2]);
-            w.s[e] = e & 1 ? __uint_as_float(ss[e / 2]) : -__uint_as_float(ss[e / 2]);
-        }
+        const uint32_t first = back ? 0u : 0x80000000u, second = back ? 0x80000000u : 0u;
+        w.c.p[0] = pair_of(c.x, c.x), w.c.p[1] = pair_of(c.y, c.y), w.c.p[2] = pair_of(c.z, c.z), w.c.p[3] = pair_of(c.w, c.w);
+        w.s.p[0] = pair_of(s.x ^ first, s.x ^ second), w.s.p[1] = pair_of(s.y ^ first, s.y ^ second);
+        w.s.p[2] = pair_of(s.z ^ first, s.z ^ second), w.s.p[3] = pair_of(s.w ^ first, s.w ^ second);
     }
 }
 
-// v = v c + partner s, each product and the sum rounded (so that results do not depend on who
-// computes them); `back`: by the opposite angle.  All 32 lanes call it; halves is uniform.
-__device__ __forceinline__ void turn(float (&v)[8], const Turn& w, bool halves, int at, int rot, bool back = false) {
-    float o[8];
+// v = v c + partner s, each product and the sum rounded (so that results do not depend on who computes them).  All 32
+// lanes call it; halves is uniform.
+__device__ __forceinline__ void turn(Row8& v, const Turn& w, bool halves) {
+    Row8 o;
     if (halves) {
-        const int lane = threadIdx.x & 31;
-        const int from = w.turns ? (at >= rot / 2 ? lane - rot / 16 : lane + rot / 16) : lane;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = __shfl_sync(0xffffffffu, v[e], from);
+        for (int i = 0; i < 4; ++i)
+            o.p[i] = pair_of(__shfl_sync(0xffffffffu, (uint32_t)v.p[i], w.from), __shfl_sync(0xffffffffu, (uint32_t)(v.p[i] >> 32), w.from));
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = v[e ^ 1];
+        for (int i = 0; i < 4; ++i) o.p[i] = pair_of((uint32_t)(v.p[i] >> 32), (uint32_t)v.p[i]);
     }
     if (w.turns)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = __fadd_rn(__fmul_rn(v[e], w.c[e]), __fmul_rn(o[e], back ? -w.s[e] : w.s[e]));
+        for (int i = 0; i < 4; ++i) {
+            float x0, x1, y0, y1;
+            unpack2(fmul2(v.p[i], w.c.p[i]), x0, x1);
+            unpack2(fmul2(o.p[i], w.s.p[i]), y0, y1);
+            v.p[i] = pack2(__fadd_rn(x0, y0), __fadd_rn(x1, y1));
+        }
 }
 
 }  // namespace q4q

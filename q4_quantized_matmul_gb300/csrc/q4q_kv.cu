@@ -7,8 +7,7 @@
 // (code - 8) d is finite in fp16, which the attention's tensor-core form decodes to.  A block with an
 // infinity or a NaN gets the scale NaN and codes of 8.
 //
-// A row takes D / 8 lanes as in q4q_rope.cu: a lane's 8 values are one word of key codes or two halves
-// of value codes.  The order of the cache (q4q_attn.cuh) spreads a value row's bytes over its octet's
+// Rows, lanes and warps as in q4q_rope.cu: a lane's 8 values are one word of key codes or two halves of value codes.  The order of the cache (q4q_attn.cuh) spreads a value row's bytes over its octet's
 // 4 D bytes; a prompt's neighbours fill the gaps while the lines are in L2.
 #include <algorithm>
 
@@ -22,7 +21,7 @@ __device__ unsigned int g_kv_status = 0;
 
 constexpr int THREADS = 256;
 constexpr int WARPS = THREADS / 32;
-constexpr int IN_FLIGHT = 4;
+constexpr int SLOTS = 4;           // row slots (of 32 / LANES rows) that a warp takes at a time
 
 struct KvArgs {
     const void *k, *v;
@@ -35,24 +34,27 @@ struct KvArgs {
     int heads, dim, rot, halves, align, page_log;
     float eps;
     float2 inv_dim;
-    int per, items;
+    int per, items;                // times SLOTS row slots that a warp takes of one side (keys or values) of a token; warps a side
+    int tokens_at_once;            // of the grid's warps, 2 * items of them a token
 };
 
 constexpr float KV_MAX = 65504.0f;
 
 // A lane's 8 values of a block of 32 (4 lanes): the word of codes, and in d_bits the block's scale.
-__device__ __forceinline__ uint32_t encode_block(float (&v)[8], uint16_t& d_bits) {
-    float m = 0.0f;
+__device__ __forceinline__ uint32_t encode_block(const Row8& x, uint16_t& d_bits) {
+    float v[8], m = 0.0f;
+    x.get(v);
 #pragma unroll
     for (int e = 0; e < 8; e += 2) m = max3_abs(m, v[e], v[e + 1]);                        // NaN if one is
     m = max3_abs(m, __shfl_xor_sync(0xffffffffu, m, 1), 0.0f);
     m = max3_abs(m, __shfl_xor_sync(0xffffffffu, m, 2), 0.0f);
     const bool finite = m <= 3.402823466e38f;
     if (__any_sync(0xffffffffu, !(m <= KV_MAX))) {
-        if (!(m <= KV_MAX))
+        if (!(m <= KV_MAX)) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] = finite ? fminf(fmaxf(v[e], -KV_MAX), KV_MAX) : 0.0f;
-        if (!(m <= KV_MAX)) m = finite ? KV_MAX : 0.0f;
+            m = finite ? KV_MAX : 0.0f;
+        }
     }
     const float d = scale_q4(m);
     const uint32_t word = pack_q4_word(v, d);
@@ -60,81 +62,100 @@ __device__ __forceinline__ uint32_t encode_block(float (&v)[8], uint16_t& d_bits
     return word;
 }
 
+// A warp's side and heads, the same through all of its tokens (as in q4q_rope.cu).
+struct Place {
+    bool value;
+    int row0;
+    int64_t token;
+};
+
+template <int LANES>
+__device__ __forceinline__ Place place_of(const KvArgs& a) {
+    const int id = blockIdx.x * WARPS + (threadIdx.x >> 5), item = id % (2 * a.items);
+    Place p;
+    p.value = item >= a.items;
+    p.row0 = (p.value ? item - a.items : item) * a.per * SLOTS * (32 / LANES) + (threadIdx.x & 31) / LANES;
+    p.token = id / (2 * a.items);
+    if (p.token >= a.tokens_at_once) p.token = a.n_tokens;           // warps that are left over
+    return p;
+}
+
 template <typename T, int LANES>
-__global__ void __launch_bounds__(THREADS) append_kernel(KvArgs a) {
+__global__ void __launch_bounds__(THREADS, 2) append_kernel(const __grid_constant__ KvArgs a) {
     constexpr int ROWS = 32 / LANES;
     pdl_trigger();
     pdl_wait();
-    const int lane = threadIdx.x & 31, in_row = lane % LANES, at = in_row * 8;
+    const int lane = threadIdx.x & 31, in_row = lane % LANES, at = in_row * 8, b = in_row >> 2, t = in_row & 3;
     const bool used = at < a.dim;
-    const int64_t items = a.n_tokens * a.items;
-    for (int64_t item = blockIdx.x * (int64_t)WARPS + (threadIdx.x >> 5); item < items; item += (int64_t)gridDim.x * WARPS) {
-        const int64_t token = item / a.items;
-        const int first = (int)(item - token * a.items) * a.per;
-        const int slot = mx_ld(a.slots + token);
-        if (slot < 0) continue;
-        int p = 0;
-        if (a.table) p = mx_ld(a.pos + token);
-        if (slot >= a.n_slots || (a.table && (p < 0 || p >= a.n_pos))) {
-            if (lane == 0) record_error(&g_kv_status, Q4Q_ERR_ARG);
-            continue;
-        }
-        Turn turning;
-        turning.turns = false;
-        if (a.table) turn_load(turning, a.table + (int64_t)p * a.rot, a.rot, a.halves, used ? at : a.rot);
-        const bool key_angles = turning.turns;
+    Place p = place_of<LANES>(a);
+    const bool turns = a.table && !p.value, norm = a.w && !p.value;
+    Row8 w;
+    w.clear();
+    if (norm && used) {
+        Raw8<float> r;
+        raw_load(a.w + at, 16, r);
+        raw_get(r, w);
+    }
+    Turn turning;
+    turn_init(turning, a.rot, a.halves, used ? at : a.rot);
+    int slot = -1, pos = 0;
+    if (p.token < a.n_tokens) {
+        slot = mx_ld(a.slots + p.token);
+        if (a.table) pos = mx_ld(a.pos + p.token);
+    }
+    for (; p.token < a.n_tokens; p.token += a.tokens_at_once) {
         const int64_t page = slot >> a.page_log;
         const int group = (slot >> 4) & ((1 << (a.page_log - 4)) - 1), i16 = slot & 15;
-        for (int s0 = 0; s0 < a.per; s0 += IN_FLIGHT) {
-            float v[IN_FLIGHT][8];
-            int head[IN_FLIGHT];
-            bool value[IN_FLIGHT], here[IN_FLIGHT];
+        const bool bad = slot >= a.n_slots || (a.table && (pos < 0 || pos >= a.n_pos));
+        const bool known = slot >= 0 && !bad;
+        if (slot >= 0 && bad && lane == 0) record_error(&g_kv_status, Q4Q_ERR_ARG);
+        const T* x_row = (p.value ? static_cast<const T*>(a.v) + p.token * a.v_stride : static_cast<const T*>(a.k) + p.token * a.k_stride) + at;
+        const float* angles = a.table + (int64_t)pos * a.rot;
+        for (int k = 0; k < a.per; ++k) {
+            const int row = p.row0 + k * SLOTS * ROWS;
+            if (row - lane / LANES >= a.heads) break;
+            Raw8<T> in[SLOTS];
 #pragma unroll
-            for (int i = 0; i < IN_FLIGHT; ++i) {
-                const int row = (first + s0 + i) * ROWS + lane / LANES;
-                value[i] = row >= a.heads;
-                head[i] = value[i] ? row - a.heads : row;
-                here[i] = row < 2 * a.heads && used && s0 + i < a.per;
+            for (int i = 0; i < SLOTS; ++i) {
+                in[i] = Raw8<T>{};
+                if (row + i * ROWS < a.heads && used && known) raw_load(x_row + (int64_t)(row + i * ROWS) * a.dim, a.align, in[i]);
+            }
+            if (k == 0) {
+                // this token's angles, and the next one's place
+                if (known && turns) turn_load(turning, angles, a.rot, a.halves, at, false);
+                const int64_t next = p.token + a.tokens_at_once;
+                if (next < a.n_tokens) {
+                    slot = mx_ld(a.slots + next);
+                    if (a.table) pos = mx_ld(a.pos + next);
+                }
+            }
+            if (!known) continue;
+            Row8 v[SLOTS];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[i][e] = 0.0f;
-                if (here[i])
-                    row_load((value[i] ? static_cast<const T*>(a.v) + token * a.v_stride : static_cast<const T*>(a.k) + token * a.k_stride) +
-                                 (int64_t)head[i] * a.dim + at, a.align, v[i]);
+            for (int i = 0; i < SLOTS; ++i) raw_get(in[i], v[i]);
+            if (norm) {
+                float r[SLOTS];
+                inverse_norm4<LANES, sizeof(T) == 2>(v, a.inv_dim, a.eps, r);
+#pragma unroll
+                for (int i = 0; i < SLOTS; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[i].p[j] = fmul2(fmul2(v[i].p[j], pack2(r[i], r[i])), w.p[j]);
             }
 #pragma unroll
-            for (int i = 0; i < IN_FLIGHT; ++i) {
-                if (!__any_sync(0xffffffffu, here[i])) break;
-                const bool key = here[i] && !value[i];
-                if (__any_sync(0xffffffffu, key)) {
-                    if (a.w) {
-                        const float r = inverse_norm<LANES>(v[i], a.inv_dim, a.eps);
-                        if (key)
-#pragma unroll
-                            for (int e = 0; e < 8; e += 4) {
-                                const uint4 u = mx_ld(reinterpret_cast<const uint4*>(a.w + at + e));
-                                v[i][e] = __fmul_rn(__fmul_rn(v[i][e], r), __uint_as_float(u.x));
-                                v[i][e + 1] = __fmul_rn(__fmul_rn(v[i][e + 1], r), __uint_as_float(u.y));
-                                v[i][e + 2] = __fmul_rn(__fmul_rn(v[i][e + 2], r), __uint_as_float(u.z));
-                                v[i][e + 3] = __fmul_rn(__fmul_rn(v[i][e + 3], r), __uint_as_float(u.w));
-                            }
-                    }
-                    if (a.table) {
-                        turning.turns = key && key_angles;
-                        turn(v[i], turning, a.halves, at, a.rot);
-                    }
-                }
+            for (int i = 0; i < SLOTS; ++i) {
+                if (turns) turn(v[i], turning, a.halves);
                 uint16_t d;
                 const uint32_t word = encode_block(v[i], d);
-                if (here[i]) {
-                    uint8_t* chunk = a.cache + kv_chunk_offset(page, head[i], group, a.heads, a.page_log, a.dim);
-                    const int b = in_row >> 2, t = in_row & 3;
-                    if (value[i]) {
+                const int head = row + i * ROWS;
+                if (head < a.heads && used) {
+                    uint8_t* chunk = a.cache + kv_chunk_offset(page, head, group, a.heads, a.page_log, a.dim);
+                    if (p.value) {
                         *reinterpret_cast<uint16_t*>(chunk + kv_v_half(i16, 2 * t, b, a.dim)) = (uint16_t)word;
                         *reinterpret_cast<uint16_t*>(chunk + kv_v_half(i16, 2 * t + 1, b, a.dim)) = (uint16_t)(word >> 16);
                     } else {
                         *reinterpret_cast<uint32_t*>(chunk + kv_k_word(i16, t, b, a.dim)) = word;
                     }
-                    if (t == 0) *reinterpret_cast<uint16_t*>(chunk + kv_scale(value[i], i16, b, a.dim)) = d;
+                    if (t == 0) *reinterpret_cast<uint16_t*>(chunk + kv_scale(p.value, i16, b, a.dim)) = d;
                 }
             }
         }
@@ -142,71 +163,79 @@ __global__ void __launch_bounds__(THREADS) append_kernel(KvArgs a) {
 }
 
 template <typename T, int LANES>
-__global__ void __launch_bounds__(THREADS) get_rows_kernel(KvArgs a) {
+__global__ void __launch_bounds__(THREADS, 2) get_rows_kernel(const __grid_constant__ KvArgs a) {
     constexpr int ROWS = 32 / LANES;
     pdl_trigger();
     pdl_wait();
-    const int lane = threadIdx.x & 31, in_row = lane % LANES, at = in_row * 8;
-    const int b = in_row >> 2, t = in_row & 3;
+    const int lane = threadIdx.x & 31, in_row = lane % LANES, at = in_row * 8, b = in_row >> 2, t = in_row & 3;
     const bool used = at < a.dim;
-    const int64_t items = a.n_tokens * a.items;
-    for (int64_t item = blockIdx.x * (int64_t)WARPS + (threadIdx.x >> 5); item < items; item += (int64_t)gridDim.x * WARPS) {
-        const int64_t token = item / a.items;
-        const int first = (int)(item - token * a.items) * a.per;
-        const int slot = mx_ld(a.slots + token);
+    Place p = place_of<LANES>(a);
+    void* const dst = p.value ? a.v_dst : a.k_dst;
+    int slot = p.token < a.n_tokens ? mx_ld(a.slots + p.token) : -1;
+    for (; p.token < a.n_tokens; p.token += a.tokens_at_once) {
         const bool known = slot >= 0 && slot < a.n_slots;
         if (slot >= a.n_slots && lane == 0) record_error(&g_kv_status, Q4Q_ERR_ARG);
         const int64_t page = known ? slot >> a.page_log : 0;
         const int group = (slot >> 4) & ((1 << (a.page_log - 4)) - 1), i16 = slot & 15;
-        for (int s0 = 0; s0 < a.per; s0 += IN_FLIGHT) {
-            uint32_t word[IN_FLIGHT];
-            uint16_t d[IN_FLIGHT];
-            int head[IN_FLIGHT];
-            bool value[IN_FLIGHT], here[IN_FLIGHT];
+        const int64_t next = p.token + a.tokens_at_once;
+        if (next < a.n_tokens) slot = mx_ld(a.slots + next);
+        if (!dst) continue;
+        T* to = static_cast<T*>(dst) + p.token * a.heads * (int64_t)a.dim + at;
+        for (int k = 0; k < a.per; ++k) {
+            const int row = p.row0 + k * SLOTS * ROWS;
+            if (row - lane / LANES >= a.heads) break;
+            uint32_t word[SLOTS];
+            uint16_t d[SLOTS];
 #pragma unroll
-            for (int i = 0; i < IN_FLIGHT; ++i) {
-                const int row = (first + s0 + i) * ROWS + lane / LANES;
-                value[i] = row >= a.heads;
-                head[i] = value[i] ? row - a.heads : row;
-                here[i] = row < 2 * a.heads && used && s0 + i < a.per && (value[i] ? a.v_dst : a.k_dst);
+            for (int i = 0; i < SLOTS; ++i) {
+                const int head = row + i * ROWS;
                 word[i] = 0x88888888u;
                 d[i] = 0;
-                if (here[i] && known) {
-                    const uint8_t* chunk = a.cache + kv_chunk_offset(page, head[i], group, a.heads, a.page_log, a.dim);
-                    if (value[i])
+                if (head < a.heads && used && known) {
+                    const uint8_t* chunk = a.cache + kv_chunk_offset(page, head, group, a.heads, a.page_log, a.dim);
+                    if (p.value)
                         word[i] = (uint32_t)mx_ld(reinterpret_cast<const uint16_t*>(chunk + kv_v_half(i16, 2 * t, b, a.dim))) |
                                   (uint32_t)mx_ld(reinterpret_cast<const uint16_t*>(chunk + kv_v_half(i16, 2 * t + 1, b, a.dim))) << 16;
                     else
                         word[i] = mx_ld(reinterpret_cast<const uint32_t*>(chunk + kv_k_word(i16, t, b, a.dim)));
-                    d[i] = mx_ld(reinterpret_cast<const uint16_t*>(chunk + kv_scale(value[i], i16, b, a.dim)));
+                    d[i] = mx_ld(reinterpret_cast<const uint16_t*>(chunk + kv_scale(p.value, i16, b, a.dim)));
                 }
             }
 #pragma unroll
-            for (int i = 0; i < IN_FLIGHT; ++i) {
-                if (!here[i]) continue;
+            for (int i = 0; i < SLOTS; ++i) {
+                if (row + i * ROWS >= a.heads || !used) continue;
                 float v[8];
                 const float scale = fp16_to_f32(d[i]);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[e] = __fmul_rn((float)((int)((word[i] >> (4 * e)) & 15u) - 8), scale);
-                T* to = static_cast<T*>(value[i] ? a.v_dst : a.k_dst) + (token * a.heads + head[i]) * (int64_t)a.dim + at;
-                row_store(to, a.align, v);
+                Row8 x;
+                x.set(v);
+                row_store(to + (int64_t)(row + i * ROWS) * a.dim, a.align, x);
             }
         }
     }
 }
 
-// As q4q_rope.cu's: the most row slots an item that leave every SM two blocks' warps of items.
-void plan(KvArgs& a, int lanes, const DeviceInfo& info) {
-    const int slots = (2 * a.heads + 32 / lanes - 1) / (32 / lanes);
+// As q4q_rope.cu's: as many heads of a token to a warp as leave every SM the warps that it holds.
+int plan(KvArgs& a, int lanes, const DeviceInfo& info) {
+    const int64_t warps = (int64_t)info.sm_count * 2 * WARPS;
+    const int rows = SLOTS * 32 / lanes;
     a.per = 1;
-    while (a.per < 16 && a.per < slots && a.n_tokens * ((slots + 2 * a.per - 1) / (2 * a.per)) >= (int64_t)info.sm_count * 2 * WARPS) a.per *= 2;
-    a.items = (slots + a.per - 1) / a.per;
+    a.items = (a.heads + rows - 1) / rows;
+    while (a.items > 1) {
+        const int fewer = (a.heads + rows * 2 * a.per - 1) / (rows * 2 * a.per);
+        if (a.n_tokens * 2 * fewer < warps) break;
+        a.per *= 2;
+        a.items = fewer;
+    }
+    a.tokens_at_once = (int)std::max<int64_t>(1, std::min<int64_t>(a.n_tokens, warps / (2 * a.items)));
+    return (a.tokens_at_once * 2 * a.items + WARPS - 1) / WARPS;
 }
 
 template <typename K>
-q4q_status launch(K kernel, const KvArgs& a, cudaStream_t stream, const DeviceInfo& info) {
+q4q_status launch(K kernel, const KvArgs& a, int blocks, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)std::max<int64_t>(1, std::min<int64_t>((a.n_tokens * a.items + WARPS - 1) / WARPS, (int64_t)info.sm_count * 8)));
+    cfg.gridDim = dim3((unsigned)blocks);
     cfg.blockDim = dim3(THREADS);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -220,8 +249,8 @@ q4q_status launch(K kernel, const KvArgs& a, cudaStream_t stream, const DeviceIn
 
 template <typename T, int LANES>
 q4q_status run_t(KvArgs& a, bool append, cudaStream_t stream, const DeviceInfo& info) {
-    plan(a, LANES, info);
-    return append ? launch(append_kernel<T, LANES>, a, stream, info) : launch(get_rows_kernel<T, LANES>, a, stream, info);
+    const int blocks = plan(a, LANES, info);
+    return append ? launch(append_kernel<T, LANES>, a, blocks, stream) : launch(get_rows_kernel<T, LANES>, a, blocks, stream);
 }
 
 template <typename T>

@@ -8,11 +8,12 @@
 //   dx = r (dz w - xh mean(dz w xh)), xh = x r;   dw = sum over tokens and heads of dz xh
 // Everything is fp32; r is that of 64-bit sums (inverse_norm), the rest rounds each product and sum.
 //
-// A row takes D / 8 lanes, 8 values each; a warp takes a token's rows one after another, so that the
-// token's cosines, sines and weights are loaded once and several rows are in flight.  Bound by HBM
-// when there are many tokens, by the launch and two loads behind one another when there are few.
-// dw is summed in registers over a warp's rows, then over the block's warps, and the blocks' sums by a
-// second kernel in the order of the blocks: no atomics, results do not vary.
+// A row takes D / 8 lanes, 8 values each.  A warp keeps to one side (queries or keys) and one run of heads through all of
+// its tokens, so weights and places are looked up once, and takes 4 row slots at a time (2 backward), whose loads
+// are in flight together and whose norms share their sums' last steps and root.  Bound by HBM when there are many tokens, by the
+// launch and two loads behind one another when there are few.  dw is summed in registers over a warp's rows, then
+// over the block's warps, and the blocks' sums by a second kernel in the order of the blocks: no atomics, results do
+// not vary.
 #include <algorithm>
 
 #include "q4q_attn.cuh"
@@ -25,8 +26,7 @@ __device__ unsigned int g_rope_status = 0;
 
 constexpr int THREADS = 256;
 constexpr int WARPS = THREADS / 32;
-constexpr int IN_FLIGHT = 4;       // row slots that a warp loads ahead
-constexpr int BACK_IN_FLIGHT = 2;
+constexpr int FORWARD_SLOTS = 4, BACK_SLOTS = 2;   // row slots (of 32 / LANES rows) that a warp takes at a time
 
 struct Side {                      // the queries, or the keys
     const void* x;                 // [tokens][heads][D], rows of a token at `stride` elements
@@ -35,6 +35,8 @@ struct Side {                      // the queries, or the keys
     void* out;                     // [tokens][heads][D]: y, or dx
     int64_t stride;
     int heads;
+    int items;                     // warps that share a token's heads
+    int per;                       // times SLOTS row slots that each of them takes
 };
 
 struct RopeArgs {
@@ -45,183 +47,143 @@ struct RopeArgs {
     int dim, rot, halves, align;
     float eps;
     float2 inv_dim;
-    int per;                       // row slots of a work item (a warp holds 32 / LANES rows in one slot)
-    int items;                     // work items of a token
+    int tokens_at_once;            // of the grid's warps, side[0].items + side[1].items of them a token
     float* partial;                // backward: [blocks][2][D]
 };
 
-// The lane's row in slot `slot` of a token: which side and head; false past the last.
-__device__ __forceinline__ bool row_of(const RopeArgs& a, int row, int& side, int& head) {
-    side = row >= a.side[0].heads;
-    head = side ? row - a.side[0].heads : row;
-    return row < a.side[0].heads + a.side[1].heads;
-}
-
-__device__ __forceinline__ void load_weights(const Side& s, int at, float (&w)[8]) {
-#pragma unroll
-    for (int e = 0; e < 8; e += 4) {
-        const uint4 u = mx_ld(reinterpret_cast<const uint4*>(s.w + at + e));
-        w[e] = __uint_as_float(u.x), w[e + 1] = __uint_as_float(u.y), w[e + 2] = __uint_as_float(u.z), w[e + 3] = __uint_as_float(u.w);
-    }
-}
-
-// the token's angles; false where its position has none (its rows become zeros)
-__device__ __forceinline__ bool angles(const RopeArgs& a, int64_t token, int at, Turn& turning) {
-    turning.turns = false;
-    if (!a.table) return true;
-    const int p = mx_ld(a.pos + token);
-    if (p < 0 || p >= a.n_pos) {
-        if ((threadIdx.x & 31) == 0) record_error(&g_rope_status, Q4Q_ERR_ARG);
-        return false;
-    }
-    turn_load(turning, a.table + (int64_t)p * a.rot, a.rot, a.halves, at);
-    return true;
-}
-
-template <typename T, int LANES>
-__global__ void __launch_bounds__(THREADS) norm_rope_kernel(RopeArgs a) {
-    constexpr int ROWS = 32 / LANES;
-    pdl_trigger();
-    pdl_wait();
-    const int lane = threadIdx.x & 31, at = lane % LANES * 8;
-    const bool used = at < a.dim;
-    const int64_t items = a.n_tokens * a.items;
-    for (int64_t item = blockIdx.x * (int64_t)WARPS + (threadIdx.x >> 5); item < items; item += (int64_t)gridDim.x * WARPS) {
-        const int64_t token = item / a.items;
-        const int first = (int)(item - token * a.items) * a.per;
-        Turn turning;
-        const bool known = angles(a, token, used ? at : a.rot, turning);
-        for (int s0 = 0; s0 < a.per; s0 += IN_FLIGHT) {
-            float v[IN_FLIGHT][8];
-            int side[IN_FLIGHT], head[IN_FLIGHT];
-            bool here[IN_FLIGHT];
-#pragma unroll
-            for (int i = 0; i < IN_FLIGHT; ++i) {
-                here[i] = row_of(a, (first + s0 + i) * ROWS + lane / LANES, side[i], head[i]) && used && s0 + i < a.per;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[i][e] = 0.0f;
-                if (here[i]) {
-                    const Side& s = a.side[side[i]];
-                    row_load(static_cast<const T*>(s.x) + token * s.stride + (int64_t)head[i] * a.dim + at, a.align, v[i]);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < IN_FLIGHT; ++i) {
-                if (!__any_sync(0xffffffffu, here[i])) break;
-                const float* w = a.side[side[i]].w;
-                if (__any_sync(0xffffffffu, here[i] && w)) {
-                    const float r = inverse_norm<LANES>(v[i], a.inv_dim, a.eps);
-                    if (here[i] && w) {
-                        float ww[8];
-                        load_weights(a.side[side[i]], at, ww);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) v[i][e] = __fmul_rn(__fmul_rn(v[i][e], r), ww[e]);
-                    }
-                }
-                if (a.table) turn(v[i], turning, a.halves, at, a.rot);
-                if (here[i]) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) v[i][e] = known ? v[i][e] : 0.0f;
-                    const Side& s = a.side[side[i]];
-                    row_store(static_cast<T*>(s.out) + (token * s.heads + head[i]) * (int64_t)a.dim + at, a.align, v[i]);
-                }
-            }
-        }
-    }
-}
-
-template <int LANES>
-__device__ __forceinline__ float row_sum(float v) {
-#pragma unroll
-    for (int d = 1; d < LANES; d <<= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-    return v;
-}
-
-template <typename T, int LANES>
-__global__ void __launch_bounds__(THREADS) norm_rope_back_kernel(RopeArgs a) {
-    constexpr int ROWS = 32 / LANES;
-    extern __shared__ float sums[];            // [warps][2][D] of the rows of a warp's first LANES lanes
+template <typename T, int LANES, bool BACK>
+__global__ void __launch_bounds__(THREADS, 2) norm_rope_kernel(const __grid_constant__ RopeArgs a) {
+    constexpr int ROWS = 32 / LANES, SLOTS = BACK ? BACK_SLOTS : FORWARD_SLOTS;
+    extern __shared__ float sums[];            // backward: [warps][2][D]
     pdl_trigger();
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, at = lane % LANES * 8;
     const bool used = at < a.dim;
-    float dw[2][8];
+    const int items = a.side[0].items + a.side[1].items, id = blockIdx.x * WARPS + warp;
+    const int item = id % items, which = item >= a.side[0].items;
+    const Side& s = a.side[which];
+    const int row0 = (which ? item - a.side[0].items : item) * s.per * SLOTS * ROWS + lane / LANES;
+    const bool norm = s.w != nullptr;
+    Row8 w, dw;
+    w.clear();
+    dw.clear();
+    if (norm && used) {
+        Raw8<float> r;
+        raw_load(s.w + at, 16, r);
+        raw_get(r, w);
+    }
+    Turn turning;
+    turn_init(turning, a.rot, a.halves, used ? at : a.rot);
+    int64_t token = id / items;
+    if (token >= a.tokens_at_once) token = a.n_tokens;               // warps that are left over
+    int pos = 0;
+    if (a.table && token < a.n_tokens) pos = mx_ld(a.pos + token);
+    for (; token < a.n_tokens; token += a.tokens_at_once) {
+        const T* x_row = static_cast<const T*>(s.x) + token * s.stride + at;
+        const T* g_row = static_cast<const T*>(s.dy) + token * s.heads * (int64_t)a.dim + at;
+        T* out_row = static_cast<T*>(s.out) + token * s.heads * (int64_t)a.dim + at;
+        const bool known = !a.table || (pos >= 0 && pos < a.n_pos);
+        for (int k = 0; k < s.per; ++k) {
+            const int row = row0 + k * SLOTS * ROWS;
+            if (row - lane / LANES >= s.heads) break;
+            Raw8<T> in[SLOTS], grad[BACK ? SLOTS : 1];
+            const bool reads_x = !BACK || norm;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) dw[0][e] = dw[1][e] = 0.0f;
-    const int64_t items = a.n_tokens * a.items;
-    for (int64_t item = blockIdx.x * (int64_t)WARPS + warp; item < items; item += (int64_t)gridDim.x * WARPS) {
-        const int64_t token = item / a.items;
-        const int first = (int)(item - token * a.items) * a.per;
-        Turn turning;
-        const bool known = angles(a, token, used ? at : a.rot, turning);
-        for (int s0 = 0; s0 < a.per; s0 += BACK_IN_FLIGHT) {
-            float g[BACK_IN_FLIGHT][8], x[BACK_IN_FLIGHT][8];
-            int side[BACK_IN_FLIGHT], head[BACK_IN_FLIGHT];
-            bool here[BACK_IN_FLIGHT];
-#pragma unroll
-            for (int i = 0; i < BACK_IN_FLIGHT; ++i) {
-                here[i] = row_of(a, (first + s0 + i) * ROWS + lane / LANES, side[i], head[i]) && used && s0 + i < a.per;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) g[i][e] = x[i][e] = 0.0f;
-                if (here[i] && known) {
-                    const Side& s = a.side[side[i]];
-                    row_load(static_cast<const T*>(s.dy) + (token * s.heads + head[i]) * (int64_t)a.dim + at, a.align, g[i]);
-                    if (s.w) row_load(static_cast<const T*>(s.x) + token * s.stride + (int64_t)head[i] * a.dim + at, a.align, x[i]);
+            for (int i = 0; i < SLOTS; ++i) {
+                const int head = row + i * ROWS;
+                in[i] = Raw8<T>{};
+                if constexpr (BACK) grad[i] = Raw8<T>{};
+                if (head < s.heads && used && known) {
+                    if (reads_x) raw_load(x_row + (int64_t)head * a.dim, a.align, in[i]);
+                    if constexpr (BACK) raw_load(g_row + (int64_t)head * a.dim, a.align, grad[i]);
                 }
             }
+            if (k == 0 && a.table) {
+                // this token's angles, and the next one's position
+                if (known) turn_load(turning, a.table + (int64_t)pos * a.rot, a.rot, a.halves, at, BACK);
+                else if (lane == 0) record_error(&g_rope_status, Q4Q_ERR_ARG);
+                if (token + a.tokens_at_once < a.n_tokens) pos = mx_ld(a.pos + token + a.tokens_at_once);
+            }
+            Row8 v[SLOTS];
 #pragma unroll
-            for (int i = 0; i < BACK_IN_FLIGHT; ++i) {
-                if (!__any_sync(0xffffffffu, here[i])) break;
-                if (a.table) turn(g[i], turning, a.halves, at, a.rot, true);
-                const Side& s = a.side[side[i]];
-                const bool norm = here[i] && s.w;
-                if (__any_sync(0xffffffffu, norm)) {
-                    const float r = inverse_norm<LANES>(x[i], a.inv_dim, a.eps);
-                    float w[8], dot = 0.0f;
+            for (int i = 0; i < SLOTS; ++i) raw_get(in[i], v[i]);
+            if constexpr (!BACK) {
+                if (norm) {
+                    float r[SLOTS];
+                    inverse_norm4<LANES, sizeof(T) == 2>(v, a.inv_dim, a.eps, r);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) w[e] = 0.0f;
-                    if (norm) load_weights(s, at, w);
+                    for (int i = 0; i < SLOTS; ++i)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        x[i][e] *= norm && known ? r : 0.0f;                          // xh
-                        const float part = g[i][e] * x[i][e];
-                        // selected, not indexed: the sums stay in registers
-                        dw[0][e] += side[i] == 0 && norm ? part : 0.0f;
-                        dw[1][e] += side[i] == 1 && norm ? part : 0.0f;
-                        if (norm) g[i][e] *= w[e];
-                        dot = fmaf(g[i][e], x[i][e], dot);
-                    }
-                    dot = row_sum<LANES>(dot);
-                    const float mean = fmaf(dot, a.inv_dim.x, dot * a.inv_dim.y);
-                    if (norm)
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) g[i][e] = r * (g[i][e] - x[i][e] * mean);
+                        for (int j = 0; j < 4; ++j) v[i].p[j] = fmul2(fmul2(v[i].p[j], pack2(r[i], r[i])), w.p[j]);
                 }
-                if (here[i]) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) g[i][e] = known ? g[i][e] : 0.0f;
-                    row_store(static_cast<T*>(s.out) + (token * s.heads + head[i]) * (int64_t)a.dim + at, a.align, g[i]);
+                for (int i = 0; i < SLOTS; ++i) {
+                    if (a.table) turn(v[i], turning, a.halves);
+                    const int head = row + i * ROWS;
+                    if (!known) v[i].clear();
+                    if (head < s.heads && used) row_store(out_row + (int64_t)head * a.dim, a.align, v[i]);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < SLOTS; ++i) {
+                    Row8 g;
+                    raw_get(grad[i], g);
+                    if (a.table) turn(g, turning, a.halves);
+                    if (norm) {
+                        // sums of x^2, and of dz w x, over the row
+                        uint64_t sq = 0, dot = 0;
+                        Row8 dh;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            dh.p[j] = fmul2(g.p[j], w.p[j]);
+                            sq = ffma2(v[i].p[j], v[i].p[j], sq);
+                            dot = ffma2(dh.p[j], v[i].p[j], dot);
+                        }
+                        float s0, s1, d0, d1;
+                        unpack2(sq, s0, s1);
+                        unpack2(dot, d0, d1);
+                        s0 += s1, d0 += d1;
+#pragma unroll
+                        for (int d = 1; d < LANES; d <<= 1) {
+                            s0 += __shfl_xor_sync(0xffffffffu, s0, d);
+                            d0 += __shfl_xor_sync(0xffffffffu, d0, d);
+                        }
+                        const float r = known ? rsqrtf(s0 * a.inv_dim.x + a.eps) : 0.0f;
+                        const float back = -(d0 * a.inv_dim.x) * r * r;               // of x: dx = r (dh - x mean(dh x) r^2)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            dw.p[j] = ffma2(g.p[j], fmul2(v[i].p[j], pack2(r, r)), dw.p[j]);
+                            g.p[j] = fmul2(ffma2(v[i].p[j], pack2(back, back), dh.p[j]), pack2(r, r));
+                        }
+                    }
+                    const int head = row + i * ROWS;
+                    if (!known) g.clear();
+                    if (head < s.heads && used) row_store(out_row + (int64_t)head * a.dim, a.align, g);
                 }
             }
         }
     }
-    if (!a.partial) return;
-    // the warp's rows, then the block's warps
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
+    if constexpr (BACK) {
+        if (!a.partial) return;
+        // the warp's rows, then the block's warps
+        float mine[8];
+        dw.get(mine);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            float v = dw[q][e];
 #pragma unroll
-            for (int d = LANES; d < 32; d <<= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-            if (lane < LANES && used) sums[(warp * 2 + q) * a.dim + at + e] = v;
+            for (int d = LANES; d < 32; d <<= 1) mine[e] += __shfl_xor_sync(0xffffffffu, mine[e], d);
+            if (lane < LANES && used) {
+                sums[(warp * 2 + which) * a.dim + at + e] = mine[e];
+                sums[(warp * 2 + !which) * a.dim + at + e] = 0.0f;
+            }
         }
-    __syncthreads();
-    for (int i = threadIdx.x; i < 2 * a.dim; i += THREADS) {
-        float v = 0.0f;
+        __syncthreads();
+        for (int i = threadIdx.x; i < 2 * a.dim; i += THREADS) {
+            float v = 0.0f;
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w) v += sums[w * 2 * a.dim + i];
-        a.partial[(int64_t)blockIdx.x * 2 * a.dim + i] = v;
+            for (int k = 0; k < WARPS; ++k) v += sums[k * 2 * a.dim + i];
+            a.partial[(int64_t)blockIdx.x * 2 * a.dim + i] = v;
+        }
     }
 }
 
@@ -258,18 +220,34 @@ __global__ void __launch_bounds__(THREADS) rope_table_kernel(float* table, int64
     }
 }
 
-// Row slots of a work item.  A warp that takes several rows of a token loads its angles once, but few
-// tokens should use all SMs: the most (of 1, 2, 4, 8, 16) that leaves each SM two blocks' warps of
-// work items.
-void plan(RopeArgs& a, int lanes, const DeviceInfo& info) {
-    const int rows = a.side[0].heads + a.side[1].heads, slots = (rows + 32 / lanes - 1) / (32 / lanes);
-    a.per = 1;
-    while (a.per < 16 && a.per < slots && a.n_tokens * ((slots + 2 * a.per - 1) / (2 * a.per)) >= (int64_t)info.sm_count * 2 * WARPS) a.per *= 2;
-    a.items = (slots + a.per - 1) / a.per;
-}
+constexpr int BLOCKS_PER_SM = 2;   // that 128 registers a thread leave
 
-int blocks_of(const RopeArgs& a, int per_sm, const DeviceInfo& info) {
-    return (int)std::max<int64_t>(1, std::min<int64_t>((a.n_tokens * a.items + WARPS - 1) / WARPS, (int64_t)info.sm_count * per_sm));
+// The grid, and how many warps share a token's heads.  A warp that takes more heads of a token loads its angles fewer
+// times, but few tokens should use all SMs: as many heads as leave every SM the warps of the blocks it holds.  All of the
+// grid's warps then walk on by the same number of tokens.
+int plan(RopeArgs& a, int lanes, int slots, const DeviceInfo& info) {
+    const int64_t warps = (int64_t)info.sm_count * BLOCKS_PER_SM * WARPS;
+    const int rows = slots * 32 / lanes;
+    int items = 0;
+    for (int per = 1;; per *= 2) {
+        int sum = 0, most = 0;
+        for (Side& s : a.side) {
+            const int n = (s.heads + rows * per - 1) / (rows * per);
+            sum += n;
+            most = std::max(most, n);
+        }
+        // no further where a side is one warp's, or too few warps would be left with work
+        if (per > 1 && (items <= 2 || a.n_tokens * sum < warps)) break;
+        items = sum;
+        for (Side& s : a.side) {
+            s.per = per;
+            s.items = (s.heads + rows * per - 1) / (rows * per);
+        }
+        if (most <= 1) break;
+    }
+    const int64_t at_once = std::max<int64_t>(1, std::min<int64_t>(a.n_tokens, warps / items));
+    a.tokens_at_once = (int)at_once;
+    return (int)((at_once * items + WARPS - 1) / WARPS);
 }
 
 template <typename... Params, typename... Args>
@@ -290,31 +268,31 @@ q4q_status launch(void (*kernel)(Params...), int grid, size_t smem, cudaStream_t
 
 int lanes_of(int64_t dim) { return dim <= 64 ? 8 : dim <= 128 ? 16 : 32; }
 
-// blocks a backward call may run at most: its workspace has one row of sums for each
-constexpr int BACK_BLOCKS_PER_SM = 3;
+// A backward call's workspace has one row of sums for each block; with up to 2048 heads a token may take more warps than
+// the SMs hold.
+int back_blocks(const DeviceInfo& info) { return std::max(info.sm_count * BLOCKS_PER_SM, 2 * 1024 / (BACK_SLOTS * WARPS)) + 1; }
 
 template <typename T, int LANES>
-q4q_status run_t(RopeArgs& a, bool back, cudaStream_t stream, const DeviceInfo& info) {
-    plan(a, LANES, info);
-    if (!back) return launch(norm_rope_kernel<T, LANES>, blocks_of(a, 8, info), 0, stream, a);
-    return launch(norm_rope_back_kernel<T, LANES>, blocks_of(a, BACK_BLOCKS_PER_SM, info),
-                  a.partial ? sizeof(float) * WARPS * 2 * a.dim : 0, stream, a);
+q4q_status run_t(RopeArgs& a, bool back, cudaStream_t stream, const DeviceInfo& info, int& blocks) {
+    blocks = plan(a, LANES, back ? BACK_SLOTS : FORWARD_SLOTS, info);
+    if (!back) return launch(norm_rope_kernel<T, LANES, false>, blocks, 0, stream, a);
+    return launch(norm_rope_kernel<T, LANES, true>, blocks, a.partial ? sizeof(float) * WARPS * 2 * a.dim : 0, stream, a);
 }
 
 template <typename T>
-q4q_status run_lanes(RopeArgs& a, bool back, cudaStream_t stream, const DeviceInfo& info) {
+q4q_status run_lanes(RopeArgs& a, bool back, cudaStream_t stream, const DeviceInfo& info, int& blocks) {
     switch (lanes_of(a.dim)) {
-        case 8: return run_t<T, 8>(a, back, stream, info);
-        case 16: return run_t<T, 16>(a, back, stream, info);
-        default: return run_t<T, 32>(a, back, stream, info);
+        case 8: return run_t<T, 8>(a, back, stream, info, blocks);
+        case 16: return run_t<T, 16>(a, back, stream, info, blocks);
+        default: return run_t<T, 32>(a, back, stream, info, blocks);
     }
 }
 
-q4q_status run(RopeArgs& a, int type, bool back, cudaStream_t stream, const DeviceInfo& info) {
+q4q_status run(RopeArgs& a, int type, bool back, cudaStream_t stream, const DeviceInfo& info, int& blocks) {
     switch (type) {
-        case Q4Q_TYPE_F32: return run_lanes<float>(a, back, stream, info);
-        case Q4Q_TYPE_F16: return run_lanes<__half>(a, back, stream, info);
-        default: return run_lanes<__nv_bfloat16>(a, back, stream, info);
+        case Q4Q_TYPE_F32: return run_lanes<float>(a, back, stream, info, blocks);
+        case Q4Q_TYPE_F16: return run_lanes<__half>(a, back, stream, info, blocks);
+        default: return run_lanes<__nv_bfloat16>(a, back, stream, info, blocks);
     }
 }
 
@@ -388,14 +366,15 @@ extern "C" q4q_status q4q_qk_norm_rope(const void* q, int64_t q_stride, int n_q_
                                        const float* table, int64_t n_pos, int rot, int mode, const int32_t* pos, void* q_dst, void* k_dst,
                                        q4q_stream_t stream) {
     RopeArgs a{};
-    a.side[0] = {q, nullptr, q_weight, q_dst, q_stride, n_q_heads};
-    a.side[1] = {k, nullptr, k_weight, k_dst, k_stride, n_k_heads};
+    a.side[0] = {q, nullptr, q_weight, q_dst, q_stride, n_q_heads, 0, 0};
+    a.side[1] = {k, nullptr, k_weight, k_dst, k_stride, n_k_heads, 0, 0};
     bool empty;
     q4q_status st = check(a, type, head_dim, n_tokens, table, n_pos, rot, mode, pos, eps, false, empty);
     if (st != Q4Q_OK || empty) return st;
     DeviceInfo info;
     if ((st = current_device_info(&info)) != Q4Q_OK) return st;
-    return run(a, type, false, (cudaStream_t)stream, info);
+    int blocks;
+    return run(a, type, false, (cudaStream_t)stream, info, blocks);
 }
 
 extern "C" q4q_status q4q_qk_norm_rope_back_workspace_size(int64_t head_dim, size_t* bytes) {
@@ -404,7 +383,7 @@ extern "C" q4q_status q4q_qk_norm_rope_back_workspace_size(int64_t head_dim, siz
     DeviceInfo info;
     const q4q_status st = current_device_info(&info);
     if (st != Q4Q_OK) return st;
-    *bytes = sizeof(float) * 2 * (size_t)head_dim * BACK_BLOCKS_PER_SM * info.sm_count;
+    *bytes = sizeof(float) * 2 * (size_t)head_dim * back_blocks(info);
     return Q4Q_OK;
 }
 
@@ -414,8 +393,8 @@ extern "C" q4q_status q4q_qk_norm_rope_back(const void* d_q_dst, const void* d_k
                                             const int32_t* pos, void* d_q, void* d_k, float* d_q_weight, float* d_k_weight, void* workspace,
                                             size_t workspace_bytes, q4q_stream_t stream_) {
     RopeArgs a{};
-    a.side[0] = {q, d_q_dst, q_weight, d_q, q_stride, n_q_heads};
-    a.side[1] = {k, d_k_dst, k_weight, d_k, k_stride, n_k_heads};
+    a.side[0] = {q, d_q_dst, q_weight, d_q, q_stride, n_q_heads, 0, 0};
+    a.side[1] = {k, d_k_dst, k_weight, d_k, k_stride, n_k_heads, 0, 0};
     bool empty;
     q4q_status st = check(a, type, head_dim, n_tokens, table, n_pos, rot, mode, pos, eps, true, empty);
     if (st != Q4Q_OK) return st;
@@ -441,7 +420,7 @@ extern "C" q4q_status q4q_qk_norm_rope_back(const void* d_q_dst, const void* d_k
         if (workspace_bytes < need) return Q4Q_ERR_WORKSPACE;
         a.partial = static_cast<float*>(workspace);
     }
-    if ((st = run(a, type, true, stream, info)) != Q4Q_OK || !a.partial) return st;
-    return launch(weight_sum_kernel, (2 * a.dim + WARPS - 1) / WARPS, 0, stream, (const float*)a.partial, blocks_of(a, BACK_BLOCKS_PER_SM, info),
-                  a.dim, dwq, dwk);
+    int blocks;
+    if ((st = run(a, type, true, stream, info, blocks)) != Q4Q_OK || !a.partial) return st;
+    return launch(weight_sum_kernel, (2 * a.dim + WARPS - 1) / WARPS, 0, stream, (const float*)a.partial, blocks, a.dim, dwq, dwk);
 }
