@@ -98,41 +98,47 @@ __global__ void __launch_bounds__(THREADS, 2) append_kernel(const __grid_constan
     }
     Turn turning;
     turn_init(turning, a.rot, a.halves, used ? at : a.rot);
-    int slot = -1, pos = 0;
+    constexpr bool AHEAD = sizeof(T) == 2;                           // the next step's rows are loaded before this one's are used
+    Raw8<T> in[SLOTS];
+    const auto load = [&](int64_t of, int row) {
+        const T* x_row = (p.value ? static_cast<const T*>(a.v) + of * a.v_stride : static_cast<const T*>(a.k) + of * a.k_stride) + at;
+#pragma unroll
+        for (int i = 0; i < SLOTS; ++i) {
+            in[i] = Raw8<T>{};
+            if (row + i * ROWS < a.heads && used) raw_load(x_row + (int64_t)(row + i * ROWS) * a.dim, a.align, in[i]);
+        }
+    };
+    int next_slot = -1, next_pos = 0;
     if (p.token < a.n_tokens) {
-        slot = mx_ld(a.slots + p.token);
-        if (a.table) pos = mx_ld(a.pos + p.token);
+        next_slot = mx_ld(a.slots + p.token);
+        if (a.table) next_pos = mx_ld(a.pos + p.token);
+        if (AHEAD) load(p.token, p.row0);
     }
     for (; p.token < a.n_tokens; p.token += a.tokens_at_once) {
-        const int64_t page = slot >> a.page_log;
+        const int slot = next_slot, pos = next_pos;
+        const int64_t page = slot >> a.page_log, next = p.token + a.tokens_at_once;
         const int group = (slot >> 4) & ((1 << (a.page_log - 4)) - 1), i16 = slot & 15;
         const bool bad = slot >= a.n_slots || (a.table && (pos < 0 || pos >= a.n_pos));
         const bool known = slot >= 0 && !bad;
         if (slot >= 0 && bad && lane == 0) record_error(&g_kv_status, Q4Q_ERR_ARG);
-        const T* x_row = (p.value ? static_cast<const T*>(a.v) + p.token * a.v_stride : static_cast<const T*>(a.k) + p.token * a.k_stride) + at;
-        const float* angles = a.table + (int64_t)pos * a.rot;
+        if (known && turns) turn_load(turning, a.table + (int64_t)pos * a.rot, a.rot, a.halves, at, false);
+        if (next < a.n_tokens) {
+            next_slot = mx_ld(a.slots + next);
+            if (a.table) next_pos = mx_ld(a.pos + next);
+        }
         for (int k = 0; k < a.per; ++k) {
             const int row = p.row0 + k * SLOTS * ROWS;
             if (row - lane / LANES >= a.heads) break;
-            Raw8<T> in[SLOTS];
-#pragma unroll
-            for (int i = 0; i < SLOTS; ++i) {
-                in[i] = Raw8<T>{};
-                if (row + i * ROWS < a.heads && used && known) raw_load(x_row + (int64_t)(row + i * ROWS) * a.dim, a.align, in[i]);
-            }
-            if (k == 0) {
-                // this token's angles, and the next one's place
-                if (known && turns) turn_load(turning, angles, a.rot, a.halves, at, false);
-                const int64_t next = p.token + a.tokens_at_once;
-                if (next < a.n_tokens) {
-                    slot = mx_ld(a.slots + next);
-                    if (a.table) pos = mx_ld(a.pos + next);
-                }
-            }
-            if (!known) continue;
+            if (!AHEAD && known) load(p.token, row);
             Row8 v[SLOTS];
 #pragma unroll
             for (int i = 0; i < SLOTS; ++i) raw_get(in[i], v[i]);
+            if (AHEAD) {
+                const bool more = k + 1 < a.per && row - lane / LANES + SLOTS * ROWS < a.heads;
+                if (more) load(p.token, row + SLOTS * ROWS);
+                else if (next < a.n_tokens) load(next, p.row0);
+            }
+            if (!known) continue;
             if (norm) {
                 float r[SLOTS];
                 inverse_norm4<LANES, sizeof(T) == 2>(v, a.inv_dim, a.eps, r);

@@ -76,37 +76,53 @@ __global__ void __launch_bounds__(THREADS, 2) norm_rope_kernel(const __grid_cons
     turn_init(turning, a.rot, a.halves, used ? at : a.rot);
     int64_t token = id / items;
     if (token >= a.tokens_at_once) token = a.n_tokens;               // warps that are left over
-    int pos = 0;
-    if (a.table && token < a.n_tokens) pos = mx_ld(a.pos + token);
+    constexpr bool AHEAD = sizeof(T) == 2;                           // the next step's rows are loaded before this one's are used
+    const bool reads_x = !BACK || norm;
+    Raw8<T> in[SLOTS], grad[BACK ? SLOTS : 1];
+    const auto load = [&](int64_t of, int row) {
+        const T* x_row = static_cast<const T*>(s.x) + of * s.stride + at;
+        const T* g_row = static_cast<const T*>(s.dy) + of * s.heads * (int64_t)a.dim + at;
+#pragma unroll
+        for (int i = 0; i < SLOTS; ++i) {
+            const int head = row + i * ROWS;
+            in[i] = Raw8<T>{};
+            if constexpr (BACK) grad[i] = Raw8<T>{};
+            if (head < s.heads && used) {
+                if (reads_x) raw_load(x_row + (int64_t)head * a.dim, a.align, in[i]);
+                if constexpr (BACK) raw_load(g_row + (int64_t)head * a.dim, a.align, grad[i]);
+            }
+        }
+    };
+    int pos = 0, pos_next = 0;
+    if (token < a.n_tokens) {
+        if (a.table) pos_next = mx_ld(a.pos + token);
+        if (AHEAD) load(token, row0);
+    }
     for (; token < a.n_tokens; token += a.tokens_at_once) {
-        const T* x_row = static_cast<const T*>(s.x) + token * s.stride + at;
-        const T* g_row = static_cast<const T*>(s.dy) + token * s.heads * (int64_t)a.dim + at;
         T* out_row = static_cast<T*>(s.out) + token * s.heads * (int64_t)a.dim + at;
+        const int64_t next = token + a.tokens_at_once;
+        pos = pos_next;
         const bool known = !a.table || (pos >= 0 && pos < a.n_pos);
+        if (a.table) {
+            if (known) turn_load(turning, a.table + (int64_t)pos * a.rot, a.rot, a.halves, at, BACK);
+            else if (lane == 0) record_error(&g_rope_status, Q4Q_ERR_ARG);
+            if (next < a.n_tokens) pos_next = mx_ld(a.pos + next);
+        }
         for (int k = 0; k < s.per; ++k) {
             const int row = row0 + k * SLOTS * ROWS;
             if (row - lane / LANES >= s.heads) break;
-            Raw8<T> in[SLOTS], grad[BACK ? SLOTS : 1];
-            const bool reads_x = !BACK || norm;
+            if (!AHEAD) load(token, row);
+            Row8 v[SLOTS], g[BACK ? SLOTS : 1];
 #pragma unroll
             for (int i = 0; i < SLOTS; ++i) {
-                const int head = row + i * ROWS;
-                in[i] = Raw8<T>{};
-                if constexpr (BACK) grad[i] = Raw8<T>{};
-                if (head < s.heads && used && known) {
-                    if (reads_x) raw_load(x_row + (int64_t)head * a.dim, a.align, in[i]);
-                    if constexpr (BACK) raw_load(g_row + (int64_t)head * a.dim, a.align, grad[i]);
-                }
+                raw_get(in[i], v[i]);
+                if constexpr (BACK) raw_get(grad[i], g[i]);
             }
-            if (k == 0 && a.table) {
-                // this token's angles, and the next one's position
-                if (known) turn_load(turning, a.table + (int64_t)pos * a.rot, a.rot, a.halves, at, BACK);
-                else if (lane == 0) record_error(&g_rope_status, Q4Q_ERR_ARG);
-                if (token + a.tokens_at_once < a.n_tokens) pos = mx_ld(a.pos + token + a.tokens_at_once);
+            if (AHEAD) {
+                const bool more = k + 1 < s.per && row - lane / LANES + SLOTS * ROWS < s.heads;
+                if (more) load(token, row + SLOTS * ROWS);
+                else if (next < a.n_tokens) load(next, row0);
             }
-            Row8 v[SLOTS];
-#pragma unroll
-            for (int i = 0; i < SLOTS; ++i) raw_get(in[i], v[i]);
             if constexpr (!BACK) {
                 if (norm) {
                     float r[SLOTS];
@@ -126,16 +142,15 @@ __global__ void __launch_bounds__(THREADS, 2) norm_rope_kernel(const __grid_cons
             } else {
 #pragma unroll
                 for (int i = 0; i < SLOTS; ++i) {
-                    Row8 g;
-                    raw_get(grad[i], g);
-                    if (a.table) turn(g, turning, a.halves);
+                    if (a.table) turn(g[i], turning, a.halves);
+                    if (!known) g[i].clear();
                     if (norm) {
                         // sums of x^2, and of dz w x, over the row
                         uint64_t sq = 0, dot = 0;
                         Row8 dh;
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            dh.p[j] = fmul2(g.p[j], w.p[j]);
+                            dh.p[j] = fmul2(g[i].p[j], w.p[j]);
                             sq = ffma2(v[i].p[j], v[i].p[j], sq);
                             dot = ffma2(dh.p[j], v[i].p[j], dot);
                         }
@@ -148,17 +163,17 @@ __global__ void __launch_bounds__(THREADS, 2) norm_rope_kernel(const __grid_cons
                             s0 += __shfl_xor_sync(0xffffffffu, s0, d);
                             d0 += __shfl_xor_sync(0xffffffffu, d0, d);
                         }
-                        const float r = known ? rsqrtf(s0 * a.inv_dim.x + a.eps) : 0.0f;
+                        // 0 where this lane holds no row: eps may be 0
+                        const float r = known && row + i * ROWS < s.heads ? rsqrtf(s0 * a.inv_dim.x + a.eps) : 0.0f;
                         const float back = -(d0 * a.inv_dim.x) * r * r;               // of x: dx = r (dh - x mean(dh x) r^2)
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            dw.p[j] = ffma2(g.p[j], fmul2(v[i].p[j], pack2(r, r)), dw.p[j]);
-                            g.p[j] = fmul2(ffma2(v[i].p[j], pack2(back, back), dh.p[j]), pack2(r, r));
+                            dw.p[j] = ffma2(g[i].p[j], fmul2(v[i].p[j], pack2(r, r)), dw.p[j]);
+                            g[i].p[j] = fmul2(ffma2(v[i].p[j], pack2(back, back), dh.p[j]), pack2(r, r));
                         }
                     }
                     const int head = row + i * ROWS;
-                    if (!known) g.clear();
-                    if (head < s.heads && used) row_store(out_row + (int64_t)head * a.dim, a.align, g);
+                    if (head < s.heads && used) row_store(out_row + (int64_t)head * a.dim, a.align, g[i]);
                 }
             }
         }
@@ -228,22 +243,18 @@ constexpr int BLOCKS_PER_SM = 2;   // that 128 registers a thread leave
 int plan(RopeArgs& a, int lanes, int slots, const DeviceInfo& info) {
     const int64_t warps = (int64_t)info.sm_count * BLOCKS_PER_SM * WARPS;
     const int rows = slots * 32 / lanes;
+    const int heads = a.side[0].heads + a.side[1].heads;
     int items = 0;
     for (int per = 1;; per *= 2) {
-        int sum = 0, most = 0;
-        for (Side& s : a.side) {
-            const int n = (s.heads + rows * per - 1) / (rows * per);
-            sum += n;
-            most = std::max(most, n);
-        }
-        // no further where a side is one warp's, or too few warps would be left with work
-        if (per > 1 && (items <= 2 || a.n_tokens * sum < warps)) break;
+        int sum = 0;
+        for (const Side& s : a.side) sum += (s.heads + rows * per - 1) / (rows * per);
+        // no further where too few warps would be left with work, or where warps would have less to do than others
+        if (per > 1 && (sum == items || a.n_tokens * sum < warps || (int64_t)sum * per * rows * 8 > heads * 9)) break;
         items = sum;
         for (Side& s : a.side) {
             s.per = per;
             s.items = (s.heads + rows * per - 1) / (rows * per);
         }
-        if (most <= 1) break;
     }
     const int64_t at_once = std::max<int64_t>(1, std::min<int64_t>(a.n_tokens, warps / items));
     a.tokens_at_once = (int)at_once;
