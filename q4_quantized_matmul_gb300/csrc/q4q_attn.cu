@@ -8,7 +8,14 @@
 namespace q4q {
 namespace {
 
-size_t workspace_bytes(int64_t head_dim, const DeviceInfo& info) {
+// The tcgen05 kernel takes bf16 rows where a sequence has enough of them for a key-value head, on average, to fill its
+// tiles of 128.
+bool on_tensor_cores(int type, int64_t head_dim, int64_t n_q, int shared, int64_t n_seqs) {
+    return type == Q4Q_TYPE_BF16 && head_dim <= 128 && n_q * shared >= n_seqs * 128;
+}
+
+size_t workspace_bytes(int type, int64_t head_dim, int64_t n_q, int shared, int64_t n_seqs, const DeviceInfo& info) {
+    if (on_tensor_cores(type, head_dim, n_q, shared, n_seqs)) return attn_tc_workspace(head_dim, info);
     switch (head_dim) {
         case 64: return attn_workspace_64(info);
         case 96: return attn_workspace_96(info);
@@ -37,7 +44,7 @@ q4q_status check(AttnArgs& a, const void* q, int64_t q_stride, int type, int64_t
         !aligned(first, 4) || !aligned(lse, 4))
         return Q4Q_ERR_ALIGN;
     if ((st = current_device_info(&info)) != Q4Q_OK) return st;
-    if (workspace_bytes_given < workspace_bytes(head_dim, info)) return Q4Q_ERR_WORKSPACE;
+    if (workspace_bytes_given < workspace_bytes(type, head_dim, n_q, n_q_heads / n_kv_heads, n_seqs, info)) return Q4Q_ERR_WORKSPACE;
     a.q = q;
     a.q_stride = q_stride;
     a.cache = static_cast<const uint8_t*>(cache);
@@ -68,6 +75,7 @@ q4q_status check(AttnArgs& a, const void* q, int64_t q_stride, int type, int64_t
 bool wide(const AttnArgs& a) { return a.n_q * a.shared > (int64_t)a.n_seqs * (a.type == Q4Q_TYPE_BF16 ? 8 : 4); }
 
 q4q_status dispatch(const AttnArgs& a, int64_t head_dim, void* workspace, cudaStream_t stream, const DeviceInfo& info) {
+    if (on_tensor_cores(a.type, head_dim, a.n_q, a.shared, a.n_seqs)) return attn_tc_run(a, head_dim, workspace, stream, info);
     switch (head_dim) {
         case 64: return attn_run_64(a, wide(a), workspace, stream, info);
         case 96: return attn_run_96(a, wide(a), workspace, stream, info);
@@ -80,7 +88,8 @@ q4q_status dispatch(const AttnArgs& a, int64_t head_dim, void* workspace, cudaSt
 
 unsigned int attn_take_device_status() {
     unsigned int first = 0;
-    for (unsigned int w : {attn_take_device_status_64(), attn_take_device_status_96(), attn_take_device_status_128(), attn_take_device_status_256()})
+    for (unsigned int w : {attn_take_device_status_64(), attn_take_device_status_96(), attn_take_device_status_128(), attn_take_device_status_256(),
+                           attn_tc_take_device_status()})
         if (!first) first = w;
     return first;
 }
@@ -96,7 +105,7 @@ extern "C" q4q_status q4q_kv_attn_workspace_size(int64_t n_q, int n_q_heads, int
     DeviceInfo info;
     const q4q_status st = current_device_info(&info);
     if (st != Q4Q_OK) return st;
-    *bytes = workspace_bytes(head_dim, info);
+    *bytes = workspace_bytes(type, head_dim, n_q, n_q_heads / n_kv_heads, n_seqs, info);
     return Q4Q_OK;
 }
 

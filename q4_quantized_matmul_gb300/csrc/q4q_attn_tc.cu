@@ -1,0 +1,758 @@
+// q4q_attn_tc.cu -- attention over the paged 4-bit cache on the tcgen05 tensor cores: prompts and chunks of
+// them, bf16, heads of 64, 96 and 128 values.
+//
+// The mathematics is that of q4q_attn_kernel.cuh; here many rows of queries share a key, so keys and values are
+// decoded once, to (code - 8) d in fp16 (one rounding, 2^-12 at most; d is at most 8188, so all are finite), and
+// both products are 128 x 128 MMAs of fp16 with fp32 sums in tensor memory.  Queries become fp16 of a power of
+// two times their row (exact but for values below 2^-24 of the row's largest), weights are rounded to fp16:
+// all three are 2^3 below the bf16 result's own rounding.  m moves only when a row's maximum passes it by 2^8.
+//
+// A CTA takes 256 rows (tokens x shared heads of a key-value head) as two tiles of 128 rows against steps of 128 keys:
+//   warps 0-3, 4-7   softmax of a tile, a thread a row: S from tensor memory twice (maximum, then weights), P over S,
+//                    the sums' rescaling, the result; at the start of a piece the tile's queries
+//   warps 8-11       decode chunks to the MMAs' operands: K [keys][dims], V^T [dims][keys], 128-byte swizzle, two stages
+//                    each.  K's lanes hold 8 dims of a key, a 16-byte unit (dims of a unit in the nibbles' order
+//                    0 4 1 5 2 6 3 7, queries alike); V's words hold two keys of 4 dims, which is what a lane of
+//                    stmatrix holds of an 8 x 8 matrix [dim][key], so rows of V^T are dims 4 g + n at place 8 n + g of
+//                    their block, and results are put back in order from registers
+//   warp 12          MMAs: S_i = Q_i K^T, O_i += P_i V, the two tiles in turn, so that one's softmax runs beside the
+//                    other's MMAs
+//   warp 13          copies: a lane finds and copies every SLOTS-th chunk into a ring
+// Steps of all pieces (sequence, head, 256 rows) in a row are cut into equal shares, one a CTA and SM; parts of a
+// piece are joined by a second kernel in order.
+#include "q4q_attn_kernel.cuh"
+
+namespace q4q {
+namespace {
+
+constexpr int TC_TILE = 128;             // rows of a tile and keys of a step
+constexpr int TC_ROWS = 2 * TC_TILE;     // rows of a piece
+constexpr int TC_CHUNKS = TC_TILE / KV_GROUP;
+constexpr int TC_DECODERS = 4;
+constexpr int TC_THREADS = (8 + TC_DECODERS + 2) * 32;
+constexpr int TC_INFOS = 4;              // steps whose notes are kept: decoders are at most 2 ahead of the softmax
+
+template <int B_>
+struct Tc {
+    static constexpr int B = B_, DIM = 32 * B, CHUNK = kv_chunk_bytes(DIM);
+    static constexpr int ATOMS = (B + 1) / 2;                      // of 64 dims
+    static constexpr int Q_BYTES = ATOMS * TC_TILE * 128, V_BYTES = 2 * DIM * 128;
+    static constexpr int STAGES = 2;
+    static constexpr int SLOTS = B <= 3 ? 16 : 12;                 // of a chunk each; a slot is always the same decoder's
+    // barriers
+    enum { RAW_FULL = 0, RAW_EMPTY = SLOTS, K_FULL = 2 * SLOTS, K_EMPTY = K_FULL + STAGES, V_FULL = K_EMPTY + STAGES, V_EMPTY = V_FULL + STAGES,
+           Q_FULL = V_EMPTY + STAGES, S_FULL = Q_FULL + 2, P_FULL = S_FULL + 2, O_DONE = P_FULL + 2, DRAIN = O_DONE + 2, BARS };
+    static constexpr int META = BARS * 8;                          // [SLOTS]: 1 for a chunk that is not there
+    static constexpr int STOP = META + SLOTS * 4, TMEM = STOP + 4;
+    static constexpr int WORDS = (TMEM + 4 + 7) / 8 * 8;           // scan and broadcast words
+    static constexpr int INFO = 704;                               // [TC_INFOS][8] bytes: bit 0 gone, bit 1 odd
+    static constexpr int ODD = 1024;                               // [TC_INFOS][128] bytes: bit b, the key's scale of V's block b is no number
+    static constexpr int Q = 2048;
+    static constexpr int K = Q + 2 * Q_BYTES, V = K + STAGES * Q_BYTES, RING = V + STAGES * V_BYTES;
+    static constexpr int BYTES = RING + SLOTS * CHUNK + 1024;       // the tiles start on 1024 bytes
+    static_assert(WORDS + (TC_THREADS / 32 + 6) * 8 <= INFO && INFO + TC_INFOS * 8 <= 1024, "small things before the tiles");
+    static_assert(K % 1024 == 0 && V % 1024 == 0 && RING % 128 == 0 && BYTES <= 227 * 1024, "shared memory");
+    static_assert(SLOTS % TC_DECODERS == 0 && SLOTS <= 32, "slots");
+};
+
+// ------------------------------------------------------------ the steps --
+
+// The steps of a tile pair: c0 the first, and how many it is counted as (at least one, so that a piece that sees no key
+// is written too).
+__device__ __forceinline__ int tc_cost(const AttnArgs& a, const Seq& s, int tile, int& c0, int& c1) {
+    int lo, hi, unused;
+    keys_of(a, s, tile * TC_ROWS, lo, unused);
+    keys_of(a, s, min(tile * TC_ROWS + TC_ROWS, s.n * a.shared) - 1, unused, hi);
+    c0 = lo / TC_TILE;
+    c1 = (hi + TC_TILE - 1) / TC_TILE;
+    return max(1, c1 - c0);
+}
+
+__device__ __forceinline__ int64_t tc_head_cost(const AttnArgs& a, const Seq& s) {
+    int64_t sum = 0;
+    int c0, c1;
+    for (int t = 0; t < s.tiles; ++t) sum += tc_cost(a, s, t, c0, c1);
+    return sum;
+}
+
+// A walk over a worker's steps: pieces, one after another.
+struct TcWalk {
+    int64_t left;              // steps behind the piece
+    int s, head, tile, from;   // where they start
+    Seq seq;
+    // the piece: steps g0 .. g1 - 1 of the sequence, `first` .. `last` - 1 of the `of` that its tile is counted as
+    int p_s, p_head, p_tile, first, last, of, g0, g1;
+    Seq p_seq;
+    bool valid;
+};
+
+__device__ __forceinline__ void tc_next(const AttnArgs& a, TcWalk& w) {
+    w.valid = false;
+    while (w.left > 0) {
+        if (w.tile >= w.seq.tiles || w.head >= a.kv_heads) {
+            w.from = 0;
+            w.tile = 0;
+            if (w.seq.tiles == 0 || ++w.head >= a.kv_heads) {
+                w.head = 0;
+                w.seq = seq_of<TC_ROWS>(a, ++w.s, false);
+            }
+            continue;
+        }
+        int c0, c1;
+        const int cost = tc_cost(a, w.seq, w.tile, c0, c1);
+        w.p_s = w.s;
+        w.p_head = w.head;
+        w.p_tile = w.tile;
+        w.p_seq = w.seq;
+        w.first = w.from;
+        w.last = (int)min((int64_t)cost, w.from + w.left);
+        w.of = cost;
+        w.g0 = min(c0 + w.first, c1);
+        w.g1 = min(c0 + w.last, c1);
+        w.left -= w.last - w.first;
+        if (w.last == cost) {
+            w.from = 0;
+            ++w.tile;
+        } else {
+            w.from = w.last;
+        }
+        w.valid = true;
+        return;
+    }
+}
+
+// This worker's share of all steps: its walk.  words: TC_THREADS / 32 + 6 words of shared memory.
+__device__ __forceinline__ TcWalk tc_share(const AttnArgs& a, const Plan& plan, int64_t* words) {
+    constexpr int WARPS = TC_THREADS / 32;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (a.n_seqs + TC_THREADS - 1) / TC_THREADS, s0 = min(tid * per, a.n_seqs), s1 = min(s0 + per, a.n_seqs);
+    int64_t sum = 0;
+    for (int s = s0; s < s1; ++s) sum += a.kv_heads * tc_head_cost(a, seq_of<TC_ROWS>(a, s, false));
+    int64_t inc = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, inc, d);
+        if (lane >= d) inc += o;
+    }
+    if (lane == 31) words[warp] = inc;
+    __syncthreads();
+    int64_t before = inc - sum, total = 0;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+        if (w < warp) before += words[w];
+        total += words[w];
+    }
+    const int64_t workers = min((int64_t)plan.workers, max((int64_t)1, total / plan.least));
+    const bool works = blockIdx.x < workers;
+    const int64_t u0 = works ? (total * blockIdx.x + workers - 1) / workers : total;
+    const int64_t u1 = works ? (total * (blockIdx.x + 1) + workers - 1) / workers : total;
+    if (u0 < u1 && before <= u0 && u0 < before + sum) {
+        int s = s0;
+        int64_t head_cost;
+        while (true) {
+            head_cost = tc_head_cost(a, seq_of<TC_ROWS>(a, s, false));
+            if (u0 < before + head_cost * a.kv_heads) break;
+            before += head_cost * a.kv_heads;
+            ++s;
+        }
+        const Seq seq = seq_of<TC_ROWS>(a, s, false);
+        int64_t rel = u0 - before;
+        const int64_t head = rel / head_cost;
+        rel -= head * head_cost;
+        int tile = 0, c0, c1;
+        for (; tile + 1 < seq.tiles; ++tile) {
+            const int cost = tc_cost(a, seq, tile, c0, c1);
+            if (rel < cost) break;
+            rel -= cost;
+        }
+        words[WARPS] = s;
+        words[WARPS + 1] = head;
+        words[WARPS + 2] = tile;
+        words[WARPS + 3] = rel;
+    }
+    __syncthreads();
+    TcWalk w;
+    w.left = u1 - u0;
+    w.valid = false;
+    if (w.left <= 0) return w;
+    w.s = (int)words[WARPS];
+    w.head = (int)words[WARPS + 1];
+    w.tile = (int)words[WARPS + 2];
+    w.from = (int)words[WARPS + 3];
+    w.seq = seq_of<TC_ROWS>(a, w.s, false);
+    return w;
+}
+
+// What every role's waits look at.
+struct TcWaits {
+    uint32_t bars;
+    volatile int* stop;
+    uint64_t limit_ns;
+    // false: the wait ran out, here or elsewhere in the CTA (the whole warp calls it)
+    __device__ __forceinline__ bool operator()(int bar, uint32_t parity) const {
+        const uint32_t at = bars + bar * 8;
+        const bool ok = mbar_try_wait(at, parity) || mbar_wait_until(at, parity, stop, limit_ns);
+        if (__all_sync(0xffffffffu, ok)) return true;
+        if (!*stop && (threadIdx.x & 31) == 0) record_error(&g_attn_status, DEV_TIMEOUT);
+        __syncwarp();
+        *stop = 1;
+        return false;
+    }
+    __device__ __forceinline__ void arrive(int bar) const { mbar_arrive(bars + bar * 8); }
+};
+
+// ------------------------------------------------------------- the roles --
+
+// Copies: lane i finds and copies every SLOTS-th chunk, when its slot is free.
+template <typename C>
+__device__ __forceinline__ void tc_copy(const AttnArgs& a, TcWalk w, const TcWaits& wait, uint32_t base, uint8_t* smem) {
+    const int lane = threadIdx.x & 31, in_page = a.page_log - 4;
+    const uint32_t full = wait.bars + (C::RAW_FULL + lane) * 8;
+    uint32_t phase = 0;
+    int used = 0;                                    // chunks of the piece that are handled
+    bool ok = true;
+    tc_next(a, w);
+    while (w.valid && ok) {
+        bool mine = false;
+        int s = 0, head = 0, group = 0, filled = 0, groups = 0;
+        while (w.valid && filled < C::SLOTS) {
+            const int all = (w.g1 - w.g0) * TC_CHUNKS, n = min(all - used, C::SLOTS - filled);
+            if (lane >= filled && lane < filled + n) {
+                mine = true;
+                s = w.p_s;
+                head = w.p_head;
+                group = w.g0 * TC_CHUNKS + used + lane - filled;
+                groups = (w.p_seq.len + KV_GROUP - 1) / KV_GROUP;
+            }
+            filled += n;
+            used += n;
+            if (used == all) {
+                tc_next(a, w);
+                used = 0;
+            }
+        }
+        int page = -1;
+        if (mine && group < groups) page = mx_ld(a.pages + s * a.max_pages + (group >> in_page));
+        const bool there = page >= 0 && page < a.n_pages;
+        if (mine && group < groups && !there) record_error(&g_attn_status, Q4Q_ERR_ARG);
+        const uint8_t* from = a.cache + kv_chunk_offset(there ? page : 0, head, group & ((1 << in_page) - 1), a.kv_heads, a.page_log, C::DIM);
+        uint32_t open = __ballot_sync(0xffffffffu, mine);
+        while (open) {
+            // the first slot that is still to be filled; others that are free by then go along
+            const int next = __ffs(open) - 1;
+            const uint32_t its = __shfl_sync(0xffffffffu, phase, next);
+            if (its > 0 && !wait(C::RAW_EMPTY + next, (its - 1) & 1)) {
+                ok = false;
+                break;
+            }
+            if (mine && (phase == 0 || mbar_test(wait.bars + (C::RAW_EMPTY + lane) * 8, (phase - 1) & 1))) {
+                reinterpret_cast<volatile int*>(smem + C::META)[lane] = !there;
+                if (there) {
+                    mbar_arrive_expect_tx(full, C::CHUNK);
+                    bulk_g2s(base + C::RING + lane * C::CHUNK, from, C::CHUNK, full);
+                } else {
+                    mbar_arrive(full);
+                }
+                ++phase;
+                mine = false;
+            }
+            open = __ballot_sync(0xffffffffu, mine);
+        }
+    }
+    // copies in flight must land before this CTA's shared memory is another's
+    if (phase > 0) mbar_wait_bounded(full, (phase - 1) & 1, a.limit_ns);
+    __syncwarp();
+}
+
+__device__ __forceinline__ uint32_t half2_mul(uint32_t a, uint32_t b) {
+    const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ void stmatrix4(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// Decoders: warp d takes chunks d and d + 4 of a step; their keys first, so that the step's scores can start.
+template <typename C>
+__device__ __forceinline__ void tc_decode(const AttnArgs& a, TcWalk w, const TcWaits& wait, uint32_t base, uint8_t* smem) {
+    constexpr int B = C::B, W = (B + 1) / 2, PER = C::SLOTS / TC_DECODERS;
+    const int lane = threadIdx.x & 31, d = (threadIdx.x >> 5) - 8;
+    uint32_t steps = 0, taken = 0;                   // steps of this CTA; chunks of this warp
+    while (true) {
+        tc_next(a, w);
+        if (!w.valid) return;
+        for (int g = w.g0; g < w.g1; ++g, ++steps) {
+            const uint32_t stage = steps % C::STAGES, round = steps / C::STAGES;
+            uint32_t chunk[2];
+            bool gone[2];
+            if (round > 0 && !wait(C::K_EMPTY + stage, (round - 1) & 1)) return;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t slot = d + TC_DECODERS * ((taken + h) % PER);
+                if (!wait(C::RAW_FULL + slot, ((taken + h) / PER) & 1)) return;
+                chunk[h] = base + C::RING + slot * C::CHUNK;
+                gone[h] = reinterpret_cast<volatile int*>(smem + C::META)[slot];
+                const int c = d + TC_DECODERS * h, key0 = g * TC_TILE + c * KV_GROUP;   // of the chunk
+                // value scales that are no number, of keys that are there
+                bool odd = false;
+                if (lane < 16 && !gone[h] && key0 + lane < w.p_seq.len) {
+                    uint32_t v[W];
+                    lds_scales<B>(chunk[h] + 17 * C::DIM + lane * 2 * B, v);
+#pragma unroll
+                    for (int k = 0; k < W; ++k) odd |= __vcmpgtu2(v[k] & 0x7FFF7FFFu, 0x7BFF7BFFu) != 0;
+                }
+                odd = __any_sync(0xffffffffu, odd);
+                if (odd && lane < 16) {
+                    uint32_t v[W], which = 0;
+                    lds_scales<B>(chunk[h] + 17 * C::DIM + lane * 2 * B, v);
+#pragma unroll
+                    for (int b = 0; b < B; ++b) which |= ((v[b / 2] >> (b % 2 * 16)) & 0x7FFFu) > 0x7BFFu && key0 + lane < w.p_seq.len ? 1u << b : 0u;
+                    smem[C::ODD + (steps % TC_INFOS) * TC_TILE + c * KV_GROUP + lane] = (uint8_t)which;
+                }
+                if (lane == 0) smem[C::INFO + (steps % TC_INFOS) * TC_CHUNKS + c] = (uint8_t)((gone[h] ? 1 : 0) | (odd ? 2 : 0));
+                // K: lanes of a quarter-warp take 8 dims of keys i and i + 4, whose 16-byte units then differ
+                const uint32_t to = base + C::K + stage * C::Q_BYTES;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int i = 8 * j + (lane >> 3) + ((lane >> 2) & 1) * 4, t = lane & 3, key = c * KV_GROUP + i;
+                    uint32_t x[B], sc[W];
+                    lds<B>(chunk[h] + (i * 4 + t) * 4 * B, x);
+                    lds_scales<B>(chunk[h] + 16 * C::DIM + i * 2 * B, sc);
+#pragma unroll
+                    for (int b = 0; b < B; ++b) {
+                        const uint32_t s2 = __byte_perm(sc[b / 2], 0, b % 2 ? 0x3232 : 0x1010);
+                        const uint4 v = nibbles_to_f16x8(x[b]);
+                        const int unit = (b % 2) * 4 + t;
+                        sts128(to + (b / 2) * TC_TILE * 128 + key * 128 + ((unit ^ (key & 7)) << 4), half2_mul(v.x, s2), half2_mul(v.y, s2),
+                               half2_mul(v.z, s2), half2_mul(v.w, s2));
+                    }
+                }
+            }
+            fence_async();
+            __syncwarp();
+            if (lane == 0) wait.arrive(C::K_FULL + stage);
+            if (round > 0 && !wait(C::V_EMPTY + stage, (round - 1) & 1)) return;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t slot = d + TC_DECODERS * ((taken + h) % PER);
+                const int c = d + TC_DECODERS * h, p = lane & 3;
+                // V^T: lane (g, p) has keys 2p, 2p + 1 of dims 4 g + n of each block; matrices of 8 dims x 8 keys, row g of
+                // matrix n at place 32 b + 8 n + g.  The address that this lane gives is that of row lane % 8 of matrix lane / 8.
+                const uint32_t row = (lane >> 3) * 8 + (lane & 7);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int octet = 2 * c + j, key = g * TC_TILE + octet * 8 + 2 * p;
+                    uint32_t x[B], s0[W], s1[W];
+                    lds<B>(chunk[h] + 8 * C::DIM + (j * 32 + lane) * 4 * B, x);
+                    lds_scales<B>(chunk[h] + 17 * C::DIM + (8 * j + 2 * p) * 2 * B, s0);
+                    lds_scales<B>(chunk[h] + 17 * C::DIM + (8 * j + 2 * p + 1) * 2 * B, s1);
+                    const uint32_t keep = gone[h] ? 0u : (key < w.p_seq.len ? 0x0000FFFFu : 0u) | (key + 1 < w.p_seq.len ? 0xFFFF0000u : 0u);
+                    const uint32_t to = base + C::V + stage * C::V_BYTES + (octet >> 3) * C::DIM * 128 + row * 128 + (((octet & 7) ^ (row & 7)) << 4);
+#pragma unroll
+                    for (int b = 0; b < B; ++b) {
+                        uint32_t s2 = __byte_perm(s0[b / 2], s1[b / 2], b % 2 ? 0x7632 : 0x5410) & keep;
+                        // what is no number becomes 0 here, and the softmax marks the rows that see it
+                        const uint32_t no = __vcmpgtu2(s2 & 0x7FFF7FFFu, 0x7BFF7BFFu);
+                        s2 &= ~no;
+                        const uint4 v = nibbles_to_f16x8(x[b]);
+                        stmatrix4(to + b * 32 * 128, half2_mul(v.x, s2), half2_mul(v.y, s2), half2_mul(v.z, s2), half2_mul(v.w, s2));
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) wait.arrive(C::RAW_EMPTY + slot);
+            }
+            taken += 2;
+            fence_async();
+            __syncwarp();
+            if (lane == 0) wait.arrive(C::V_FULL + stage);
+        }
+    }
+}
+
+// A = P [128 rows x 16 keys] from tensor memory, or queries from shared memory; B from shared memory, K-major.
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+// fp32 sums, fp16 operands, both K-major, N columns
+__host__ __device__ constexpr uint32_t tc_idesc(int n) { return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(TC_TILE >> 4) << 24); }
+
+// tensor memory: S and P of tile i at 128 i, O at 256 + 128 i
+template <typename C>
+__device__ __forceinline__ void tc_issue(const AttnArgs& a, TcWalk w, const TcWaits& wait, uint32_t base, uint32_t tmem) {
+    const bool one = elect_one();
+    uint32_t steps = 0, pieces = 0, drained = 0;
+    bool ok = true;
+    const auto commit = [&](int bar) {
+        if (one) mma_commit(wait.bars + bar * 8);
+    };
+    const auto scores = [&](int i, uint32_t stage) {
+        const uint64_t q = desc_sw128(base + C::Q + i * C::Q_BYTES), k = desc_sw128(base + C::K + stage * C::Q_BYTES);
+        if (one)
+#pragma unroll
+            for (int x = 0; x < 2 * C::B; ++x) {
+                const uint64_t at = ((x / 4) * TC_TILE * 128 + (x % 4) * 32) >> 4;
+                tc_mma_ss(tmem + i * TC_TILE, q + at, k + at, tc_idesc(TC_TILE), x > 0);
+            }
+        __syncwarp();
+    };
+    const auto values = [&](int i, uint32_t stage, bool more) {
+        const uint64_t v = desc_sw128(base + C::V + stage * C::V_BYTES);
+        if (one)
+#pragma unroll
+            for (int x = 0; x < TC_TILE / 16; ++x)
+                tc_mma_ts(tmem + 2 * TC_TILE + i * TC_TILE, tmem + i * TC_TILE + x * 8, v + (((x / 4) * C::DIM * 128 + (x % 4) * 32) >> 4),
+                          tc_idesc(C::DIM), more || x > 0);
+        __syncwarp();
+    };
+    while (ok) {
+        tc_next(a, w);
+        if (!w.valid) break;
+        const int n = w.g1 - w.g0;
+        if (n <= 0) continue;
+        // the first step's scores
+        ok = wait(C::K_FULL + steps % C::STAGES, (steps / C::STAGES) & 1);
+#pragma unroll
+        for (int i = 0; i < 2 && ok; ++i) {
+            ok = wait(C::Q_FULL + i, pieces & 1);
+            if (!ok) break;
+            tc_fence_after();
+            scores(i, steps % C::STAGES);
+            commit(C::S_FULL + i);
+        }
+        if (!ok) break;
+        commit(C::K_EMPTY + steps % C::STAGES);
+        for (int j = 0; j < n && ok; ++j) {
+            const uint32_t at = steps + j, stage = at % C::STAGES, parity = (at / C::STAGES) & 1, next = (at + 1) % C::STAGES;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                ok = ok && wait(C::P_FULL + i, at & 1) && (i > 0 || wait(C::V_FULL + stage, parity));
+                if (!ok) break;
+                tc_fence_after();
+                values(i, stage, j > 0);
+                if (j + 1 == n) {
+                    commit(C::O_DONE + i);
+                } else {
+                    // behind the product that reads P: MMAs run in the order they were issued in
+                    if (i == 0) ok = wait(C::K_FULL + next, ((at + 1) / C::STAGES) & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    scores(i, next);
+                    commit(C::S_FULL + i);
+                }
+            }
+            if (!ok) break;
+            commit(C::V_EMPTY + stage);
+            if (j + 1 < n) commit(C::K_EMPTY + next);
+        }
+        steps += n;
+        ++pieces;
+    }
+    // nothing is in flight when tensor and shared memory are given back
+    commit(C::DRAIN);
+    mbar_wait_bounded(wait.bars + C::DRAIN * 8, drained & 1, a.limit_ns);
+    __syncwarp();
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+        ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+          "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]) : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// The softmax of tile i, a thread a row: queries, weights, and at a piece's end the results.
+template <typename C>
+__device__ __forceinline__ void tc_softmax(const AttnArgs& a, const Plan& plan, TcWalk w, const TcWaits& wait, uint32_t base, uint8_t* smem, uint32_t tmem) {
+    constexpr int B = C::B;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, i = warp >> 2, r = tid & 127;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;                       // this warp's 32 lanes of tensor memory
+    const uint32_t s_at = tmem + lanes + i * TC_TILE, o_at = tmem + lanes + 2 * TC_TILE + i * TC_TILE;
+    uint32_t steps = 0, pieces = 0;
+    while (true) {
+        tc_next(a, w);
+        if (!w.valid) return;
+        const Seq& seq = w.p_seq;
+        const int rows = seq.n * a.shared, at_row = w.p_tile * TC_ROWS + i * TC_TILE + r, row = min(at_row, rows - 1), n = w.g1 - w.g0;
+        const int64_t at = (int64_t)(seq.q0 + row / a.shared), head = w.p_head * a.shared + row % a.shared;
+        int lo, hi;
+        keys_of(a, seq, row, lo, hi);
+        const int lo_all = __reduce_max_sync(0xffffffffu, lo), hi_all = __reduce_min_sync(0xffffffffu, hi);
+        float scale = 0.0f, ref = NONE, l = 0.0f;
+        uint32_t poison = 0;                                                  // blocks in which the row sees a value that is no number
+        if (n > 0) {
+            // the row as fp16 of a power of two times it, its largest in [1, 2); the scale's sign goes along
+            const __nv_bfloat16* from = static_cast<const __nv_bfloat16*>(a.q) + at * a.q_stride + head * C::DIM;
+            float top = 0.0f;
+            Raw8<__nv_bfloat16> raw[4 * B];
+#pragma unroll
+            for (int u = 0; u < 4 * B; ++u) {
+                raw_load(from + 8 * u, a.align, raw[u]);
+                const uint32_t x[4] = {raw[u].w[0].x, raw[u].w[0].y, raw[u].w[0].z, raw[u].w[0].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) top = fmaxf(top, fmaxf(fabsf(__uint_as_float(x[k] << 16)), fabsf(__uint_as_float(x[k] & 0xffff0000u))));
+            }
+            const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 100);
+            const float up = a.scale_log2 < 0.0f ? -two_to(-e) : two_to(-e);
+            scale = fabsf(a.scale_log2) * two_to(e);
+#pragma unroll
+            for (int u = 0; u < 4 * B; ++u) {
+                Row8 x;
+                float v[8];
+                raw_get(raw[u], x);
+                x.get(v);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] *= up;
+                sts128(base + C::Q + i * C::Q_BYTES + (u / 8) * TC_TILE * 128 + r * 128 + (((u & 7) ^ (r & 7)) << 4), half2_bits(v[0], v[4]),
+                       half2_bits(v[1], v[5]), half2_bits(v[2], v[6]), half2_bits(v[3], v[7]));
+            }
+            fence_async();
+            __syncwarp();
+            if (lane == 0) wait.arrive(C::Q_FULL + i);
+        }
+        for (int j = 0; j < n; ++j, ++steps) {
+            if (!wait(C::S_FULL + i, steps & 1)) return;
+            tc_fence_after();
+            const int key0 = (w.g0 + j) * TC_TILE;
+            const uint64_t info = *reinterpret_cast<volatile uint64_t*>(smem + C::INFO + (steps % TC_INFOS) * TC_CHUNKS);
+            const bool edge = key0 < lo_all || key0 + TC_TILE > hi_all || info != 0;
+            // keys of this step that the row sees: from .. to - 1, but for chunks that are not there
+            const int from = max(lo - key0, 0), to = min(hi - key0, TC_TILE);
+            float most = -INFINITY;
+            if (edge) {
+#pragma unroll 1
+                for (int c = 0; c < TC_TILE; c += 16) {
+                    uint32_t x[16];
+                    tmem_ld<16>(s_at + c, x);
+                    if (!((info >> (c / 2)) & 1))
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) most = c + k >= from && c + k < to ? fmaxf(most, __uint_as_float(x[k])) : most;
+                }
+                for (int c = 0; c < TC_CHUNKS; ++c)
+                    if ((info >> (8 * c + 1)) & 1)
+                        for (int k = 0; k < KV_GROUP; ++k)
+                            if (c * KV_GROUP + k >= from && c * KV_GROUP + k < to)
+                                poison |= *reinterpret_cast<volatile uint8_t*>(smem + C::ODD + (steps % TC_INFOS) * TC_TILE + c * KV_GROUP + k);
+            } else {
+#pragma unroll
+                for (int c = 0; c < TC_TILE; c += 32) {
+                    uint32_t x[32];
+                    tmem_ld<32>(s_at + c, x);
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2) most = fmaxf(most, fmaxf(__uint_as_float(x[k]), __uint_as_float(x[k + 1])));
+                }
+            }
+            const float y = most == -INFINITY ? -INFINITY : most * scale;
+            if (__any_sync(0xffffffffu, y > ref + 8.0f)) {
+                const float to_ref = y > ref + 8.0f ? y : ref, down = exp2f(ref - to_ref);
+                ref = to_ref;
+                l *= down;
+                // this step's scores are there, so the products issued before them are done with the sums
+                if (j > 0) {
+#pragma unroll 1
+                    for (int c = 0; c < C::DIM; c += 16) {
+                        uint32_t x[16];
+                        tmem_ld<16>(o_at + c, x);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * down);
+                        tmem_st16(o_at + c, x);
+                    }
+                }
+            }
+            uint64_t sum = 0;
+            const uint64_t scale2 = pack2(scale, scale), ref2 = pack2(-ref, -ref);
+#pragma unroll 1
+            for (int c = 0; c < TC_TILE; c += 32) {
+                uint32_t x[32], p[16];
+                tmem_ld<32>(s_at + c, x);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    float z0, z1;
+                    unpack2(ffma2(pair_of(x[2 * k], x[2 * k + 1]), scale2, ref2), z0, z1);
+                    z0 = ex2(z0);
+                    z1 = ex2(z1);
+                    if (edge) {
+                        const int key = c + 2 * k;
+                        const bool gone = (info >> (key / 16 * 8)) & 1;
+                        if (key < from || key >= to || gone) z0 = 0.0f;
+                        if (key + 1 < from || key + 1 >= to || gone) z1 = 0.0f;
+                    }
+                    sum = ffma2(sum, pack2(1.0f, 1.0f), pack2(z0, z1));
+                    p[k] = half2_bits(z0, z1);
+                }
+                tmem_st16(s_at + c / 2, p);                                   // over scores that have been read
+            }
+            float l0, l1;
+            unpack2(sum, l0, l1);
+            l += l0 + l1;
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) wait.arrive(C::P_FULL + i);
+        }
+        // the results
+        if (n > 0) {
+            if (!wait(C::O_DONE + i, pieces & 1)) return;
+            tc_fence_after();
+            ++pieces;
+        }
+        const bool complete = w.first == 0 && w.last == w.of, there = at_row < rows;
+        const int part = 2 * blockIdx.x + (w.first == 0 ? 1 : 0);
+        float* part_row = plan.rows + (int64_t)part * (TC_ROWS * (C::DIM + 2)) + (i * TC_TILE + r) * C::DIM;
+        if (!complete && tid == 0) plan.parts[part] = {w.p_s, w.p_head, w.p_tile, w.first, w.last, w.of};
+        const bool none = ref == NONE;
+        const float inv = complete ? (none ? 0.0f : 1.0f / l) : 1.0f;
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.dst) + (at * a.heads + head) * C::DIM;
+#pragma unroll 1
+        for (int b = 0; b < B; ++b) {
+            uint32_t x[32];
+            if (n > 0) tmem_ld<32>(o_at + 32 * b, x);
+            float v[32];
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+                // place 8 n + g of the block is dim 4 g + n
+                const float o = n > 0 && !none ? __uint_as_float(x[k]) * inv : 0.0f;
+                v[4 * (k % 8) + k / 8] = (poison >> b) & 1 ? NAN : o;
+            }
+            if (there && complete) {
+#pragma unroll
+                for (int k = 0; k < 32; k += 8) {
+                    Row8 y;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) y.p[q] = pack2(v[k + 2 * q], v[k + 2 * q + 1]);
+                    row_store(out + 32 * b + k, a.align, y);
+                }
+            } else if (there) {
+#pragma unroll
+                for (int k = 0; k < 32; k += 4) *reinterpret_cast<float4*>(part_row + 32 * b + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+            }
+            __syncwarp();
+        }
+        if (there && !complete)
+            *reinterpret_cast<float2*>(plan.rows + (int64_t)part * (TC_ROWS * (C::DIM + 2)) + TC_ROWS * C::DIM + 2 * (i * TC_TILE + r)) =
+                make_float2(none ? -INFINITY : ref, l);
+        else if (there && a.lse)
+            a.lse[at * a.heads + head] = none ? -INFINITY : (ref + log2f(l)) * 0.69314718055994531f;
+        __syncwarp();
+    }
+}
+
+template <typename C>
+__global__ void __launch_bounds__(TC_THREADS, 1) attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ Plan plan) {
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;     // of the swizzled tiles
+    uint8_t* const smem = smem_raw + (base - smem_u32(smem_raw));
+    const int tid = threadIdx.x, warp = tid >> 5;
+    const TcWaits wait{base, reinterpret_cast<volatile int*>(smem + C::STOP), a.limit_ns};
+    if (tid < C::BARS)
+        mbar_init(base + tid * 8, (tid >= C::K_FULL && tid < C::K_EMPTY) || (tid >= C::V_FULL && tid < C::V_EMPTY) ? TC_DECODERS
+                                  : (tid >= C::Q_FULL && tid < C::S_FULL) || (tid >= C::P_FULL && tid < C::O_DONE) ? 4 : 1);
+    if (tid == 0) *wait.stop = 0;
+    fence_mbar_init();
+    if (warp == 12) tmem_alloc(base + C::TMEM, 512);
+    pdl_trigger();
+    pdl_wait();
+    // what is copied below may have been written by ordinary stores of the work before
+    asm volatile("fence.proxy.async;" ::: "memory");
+    tc_fence_before();
+    const TcWalk walk = tc_share(a, plan, reinterpret_cast<int64_t*>(smem + C::WORDS));     // with barriers of the block
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + C::TMEM);
+    if (tid < 2) plan.parts[2 * blockIdx.x + tid].of = -1;
+    __syncthreads();
+    if (walk.left > 0) {
+        if (warp < 8) tc_softmax<C>(a, plan, walk, wait, base, smem, tmem);
+        else if (warp < 12) tc_decode<C>(a, walk, wait, base, smem);
+        else if (warp == 12) tc_issue<C>(a, walk, wait, base, tmem);
+        else tc_copy<C>(a, walk, wait, base, smem);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 12) tmem_dealloc(tmem, 512);
+}
+
+// Joins the parts of the pieces that were cut: block (w, y) rows 8 y .. of the one that starts in worker w, a warp a row.
+constexpr int TC_JOIN_WARPS = 8;
+
+template <typename C>
+__global__ void __launch_bounds__(TC_JOIN_WARPS * 32) join_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ Plan plan) {
+    constexpr int VEC = C::DIM / 32;
+    pdl_wait();
+    const int w = blockIdx.x, r = blockIdx.y * TC_JOIN_WARPS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const Part* parts = plan.parts;
+    const int of = mx_ld(&parts[2 * w + 1].of), to0 = mx_ld(&parts[2 * w + 1].to);
+    if (of < 0 || to0 >= of) return;                       // no piece starts here, or none that goes on
+    const Seq seq = seq_of<TC_ROWS>(a, mx_ld(&parts[2 * w + 1].seq), false);
+    const int row = mx_ld(&parts[2 * w + 1].tile) * TC_ROWS + r;
+    if (row >= seq.n * a.shared) return;
+    int n = 1;
+    while (w + n < plan.workers && mx_ld(&parts[2 * (w + n)].of) >= 0 && mx_ld(&parts[2 * (w + n)].to) < of) ++n;
+    n = min(n + 1, plan.workers - w);
+    const auto rows_of = [&](int p) { return plan.rows + (p == 0 ? 2 * w + 1 : 2 * (w + p)) * (int64_t)(TC_ROWS * (C::DIM + 2)); };
+    float ref = -INFINITY;
+    for (int p = lane; p < n; p += 32) ref = larger(ref, mx_ld(rows_of(p) + TC_ROWS * C::DIM + 2 * r));
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) ref = larger(ref, __shfl_xor_sync(0xffffffffu, ref, d));
+    float sum = 0.0f, v[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[i] = 0.0f;
+    for (int p = 0; p < n; ++p) {
+        const float* rows = rows_of(p);
+        const float k = share_of(mx_ld(rows + TC_ROWS * C::DIM + 2 * r), ref);
+        sum = fmaf(k, mx_ld(rows + TC_ROWS * C::DIM + 2 * r + 1), sum);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[i] = fmaf(k, mx_ld(rows + r * C::DIM + i * 32 + lane), v[i]);
+    }
+    const float inv = ref == -INFINITY ? 0.0f : 1.0f / sum;
+    const int64_t at = (int64_t)(seq.q0 + row / a.shared) * a.heads + mx_ld(&parts[2 * w + 1].head) * a.shared + row % a.shared;
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.dst) + at * C::DIM;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) out[i * 32 + lane] = __float2bfloat16_rn(v[i] * inv);
+    if (lane == 0 && a.lse) a.lse[at] = ref == -INFINITY ? -INFINITY : (ref + log2f(sum)) * 0.69314718055994531f;
+}
+
+template <int B>
+q4q_status tc_run(const AttnArgs& a, void* workspace, cudaStream_t stream, const DeviceInfo& info) {
+    using C = Tc<B>;
+    const cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES);
+    if (e != cudaSuccess) return cudaGetLastError(), Q4Q_ERR_CUDA;
+    Plan plan;
+    plan.workers = info.sm_count;
+    plan.whole = 0;
+    plan.least = 4;
+    plan.parts = static_cast<Part*>(workspace);
+    plan.rows = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + mx_up((int64_t)sizeof(Part) * 2 * plan.workers, 256));
+    const q4q_status st = launch(attn_tc_kernel<C>, dim3((unsigned)plan.workers), TC_THREADS, C::BYTES, stream, a, plan);
+    if (st != Q4Q_OK) return st;
+    return launch(join_tc_kernel<C>, dim3((unsigned)plan.workers, TC_ROWS / TC_JOIN_WARPS), TC_JOIN_WARPS * 32, 0, stream, a, plan);
+}
+
+}  // namespace
+
+size_t attn_tc_workspace(int64_t head_dim, const DeviceInfo& info) {
+    return (size_t)(mx_up((int64_t)sizeof(Part) * 2 * info.sm_count, 256) + (int64_t)sizeof(float) * TC_ROWS * (head_dim + 2) * 2 * info.sm_count);
+}
+
+q4q_status attn_tc_run(const AttnArgs& a, int64_t head_dim, void* workspace, cudaStream_t stream, const DeviceInfo& info) {
+    switch (head_dim) {
+        case 64: return tc_run<2>(a, workspace, stream, info);
+        case 96: return tc_run<3>(a, workspace, stream, info);
+        default: return tc_run<4>(a, workspace, stream, info);
+    }
+}
+
+unsigned int attn_tc_take_device_status() { return attn_take_status_word(); }
+
+}  // namespace q4q
