@@ -11,13 +11,13 @@
 //   warps 0-3, 4-7   softmax of a tile, a thread a row: S from tensor memory twice (maximum, then weights), P over S,
 //                    the sums' rescaling, the result; at the start of a piece the tile's queries
 //   warps 8-11       decode chunks to the MMAs' operands: K [keys][dims], V^T [dims][keys], 128-byte swizzle, two stages
-//                    each.  K's lanes hold 8 dims of a key, a 16-byte unit (dims of a unit in the nibbles' order
-//                    0 4 1 5 2 6 3 7, queries alike); V's words hold two keys of 4 dims, which is what a lane of
-//                    stmatrix holds of an 8 x 8 matrix [dim][key], so rows of V^T are dims 4 g + n at place 8 n + g of
-//                    their block, and results are put back in order from registers
+//                    each.  Codes and scales come straight from the cache into registers, a step ahead.  A lane of K holds 8
+//                    dims of a key, a 16-byte unit (dims of a unit in the nibbles' order 0 4 1 5 2 6 3 7, queries alike); V's
+//                    words hold two keys of 4 dims, which is what a lane of stmatrix holds of an 8 x 8 matrix [dim][key], so
+//                    rows of V^T are dims 4 g + n at place 8 n + g of their block, and results are put back in order from
+//                    registers
 //   warp 12          MMAs: S_i = Q_i K^T, O_i += P_i V, the two tiles in turn, so that one's softmax runs beside the
 //                    other's MMAs
-//   warp 13          copies: a lane finds and copies every SLOTS-th chunk into a ring
 // Steps of all pieces (sequence, head, 256 rows) in a row are cut into equal shares, one a CTA and SM; parts of a
 // piece are joined by a second kernel in order.
 #include "q4q_attn_kernel.cuh"
@@ -29,30 +29,27 @@ constexpr int TC_TILE = 128;             // rows of a tile and keys of a step
 constexpr int TC_ROWS = 2 * TC_TILE;     // rows of a piece
 constexpr int TC_CHUNKS = TC_TILE / KV_GROUP;
 constexpr int TC_DECODERS = 4;
-constexpr int TC_THREADS = (8 + TC_DECODERS + 2) * 32;
+constexpr int TC_THREADS = (8 + TC_DECODERS + 1) * 32;
 constexpr int TC_INFOS = 4;              // steps whose notes are kept: decoders are at most 2 ahead of the softmax
 
 template <int B_>
 struct Tc {
-    static constexpr int B = B_, DIM = 32 * B, CHUNK = kv_chunk_bytes(DIM);
+    static constexpr int B = B_, DIM = 32 * B;
     static constexpr int ATOMS = (B + 1) / 2;                      // of 64 dims
     static constexpr int Q_BYTES = ATOMS * TC_TILE * 128, V_BYTES = 2 * DIM * 128;
     static constexpr int STAGES = 2;
-    static constexpr int SLOTS = B <= 3 ? 16 : 12;                 // of a chunk each; a slot is always the same decoder's
     // barriers
-    enum { RAW_FULL = 0, RAW_EMPTY = SLOTS, K_FULL = 2 * SLOTS, K_EMPTY = K_FULL + STAGES, V_FULL = K_EMPTY + STAGES, V_EMPTY = V_FULL + STAGES,
-           Q_FULL = V_EMPTY + STAGES, S_FULL = Q_FULL + 2, P_FULL = S_FULL + 2, O_DONE = P_FULL + 2, DRAIN = O_DONE + 2, BARS };
-    static constexpr int META = BARS * 8;                          // [SLOTS]: 1 for a chunk that is not there
-    static constexpr int STOP = META + SLOTS * 4, TMEM = STOP + 4;
+    enum { K_FULL = 0, K_EMPTY = K_FULL + STAGES, V_FULL = K_EMPTY + STAGES, V_EMPTY = V_FULL + STAGES, Q_FULL = V_EMPTY + STAGES, S_FULL = Q_FULL + 2,
+           P_FULL = S_FULL + 2, O_DONE = P_FULL + 2, DRAIN = O_DONE + 2, BARS };
+    static constexpr int STOP = BARS * 8, TMEM = STOP + 4;
     static constexpr int WORDS = (TMEM + 4 + 7) / 8 * 8;           // scan and broadcast words
-    static constexpr int INFO = 704;                               // [TC_INFOS][8] bytes: bit 0 gone, bit 1 odd
-    static constexpr int ODD = 1024;                               // [TC_INFOS][128] bytes: bit b, the key's scale of V's block b is no number
+    static constexpr int GONE = 512, ODD = GONE + TC_INFOS * 8;    // [TC_INFOS][8] bytes: chunks that are not there; with scales that are no number
+    static constexpr int WHICH = 1024;                             // [TC_INFOS][128] bytes: bit b, the key's scale of V's block b is no number
     static constexpr int Q = 2048;
-    static constexpr int K = Q + 2 * Q_BYTES, V = K + STAGES * Q_BYTES, RING = V + STAGES * V_BYTES;
-    static constexpr int BYTES = RING + SLOTS * CHUNK + 1024;       // the tiles start on 1024 bytes
-    static_assert(WORDS + (TC_THREADS / 32 + 6) * 8 <= INFO && INFO + TC_INFOS * 8 <= 1024, "small things before the tiles");
-    static_assert(K % 1024 == 0 && V % 1024 == 0 && RING % 128 == 0 && BYTES <= 227 * 1024, "shared memory");
-    static_assert(SLOTS % TC_DECODERS == 0 && SLOTS <= 32, "slots");
+    static constexpr int K = Q + 2 * Q_BYTES, V = K + STAGES * Q_BYTES;
+    static constexpr int BYTES = V + STAGES * V_BYTES + 1024;      // the tiles start on 1024 bytes
+    static_assert(WORDS + (TC_THREADS / 32 + 6) * 8 <= GONE && ODD + TC_INFOS * 8 <= WHICH, "small things before the tiles");
+    static_assert(K % 1024 == 0 && V % 1024 == 0 && BYTES <= 227 * 1024, "shared memory");
 };
 
 // ------------------------------------------------------------ the steps --
@@ -203,67 +200,6 @@ struct TcWaits {
 
 // ------------------------------------------------------------- the roles --
 
-// Copies: lane i finds and copies every SLOTS-th chunk, when its slot is free.
-template <typename C>
-__device__ __forceinline__ void tc_copy(const AttnArgs& a, TcWalk w, const TcWaits& wait, uint32_t base, uint8_t* smem) {
-    const int lane = threadIdx.x & 31, in_page = a.page_log - 4;
-    const uint32_t full = wait.bars + (C::RAW_FULL + lane) * 8;
-    uint32_t phase = 0;
-    int used = 0;                                    // chunks of the piece that are handled
-    bool ok = true;
-    tc_next(a, w);
-    while (w.valid && ok) {
-        bool mine = false;
-        int s = 0, head = 0, group = 0, filled = 0, groups = 0;
-        while (w.valid && filled < C::SLOTS) {
-            const int all = (w.g1 - w.g0) * TC_CHUNKS, n = min(all - used, C::SLOTS - filled);
-            if (lane >= filled && lane < filled + n) {
-                mine = true;
-                s = w.p_s;
-                head = w.p_head;
-                group = w.g0 * TC_CHUNKS + used + lane - filled;
-                groups = (w.p_seq.len + KV_GROUP - 1) / KV_GROUP;
-            }
-            filled += n;
-            used += n;
-            if (used == all) {
-                tc_next(a, w);
-                used = 0;
-            }
-        }
-        int page = -1;
-        if (mine && group < groups) page = mx_ld(a.pages + s * a.max_pages + (group >> in_page));
-        const bool there = page >= 0 && page < a.n_pages;
-        if (mine && group < groups && !there) record_error(&g_attn_status, Q4Q_ERR_ARG);
-        const uint8_t* from = a.cache + kv_chunk_offset(there ? page : 0, head, group & ((1 << in_page) - 1), a.kv_heads, a.page_log, C::DIM);
-        uint32_t open = __ballot_sync(0xffffffffu, mine);
-        while (open) {
-            // the first slot that is still to be filled; others that are free by then go along
-            const int next = __ffs(open) - 1;
-            const uint32_t its = __shfl_sync(0xffffffffu, phase, next);
-            if (its > 0 && !wait(C::RAW_EMPTY + next, (its - 1) & 1)) {
-                ok = false;
-                break;
-            }
-            if (mine && (phase == 0 || mbar_test(wait.bars + (C::RAW_EMPTY + lane) * 8, (phase - 1) & 1))) {
-                reinterpret_cast<volatile int*>(smem + C::META)[lane] = !there;
-                if (there) {
-                    mbar_arrive_expect_tx(full, C::CHUNK);
-                    bulk_g2s(base + C::RING + lane * C::CHUNK, from, C::CHUNK, full);
-                } else {
-                    mbar_arrive(full);
-                }
-                ++phase;
-                mine = false;
-            }
-            open = __ballot_sync(0xffffffffu, mine);
-        }
-    }
-    // copies in flight must land before this CTA's shared memory is another's
-    if (phase > 0) mbar_wait_bounded(full, (phase - 1) & 1, a.limit_ns);
-    __syncwarp();
-}
-
 __device__ __forceinline__ uint32_t half2_mul(uint32_t a, uint32_t b) {
     const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
     return *reinterpret_cast<const uint32_t*>(&r);
@@ -276,100 +212,192 @@ __device__ __forceinline__ void stmatrix4(uint32_t addr, uint32_t x, uint32_t y,
 }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+// WORDS words of the cache
+template <int WORDS>
+__device__ __forceinline__ void ldg(const uint8_t* p, uint32_t (&v)[WORDS]) {
+    if constexpr (WORDS % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < WORDS / 4; ++i) {
+            const uint4 x = mx_ld(reinterpret_cast<const uint4*>(p) + i);
+            v[4 * i] = x.x, v[4 * i + 1] = x.y, v[4 * i + 2] = x.z, v[4 * i + 3] = x.w;
+        }
+    } else if constexpr (WORDS == 2) {
+        asm volatile("ld.global.v2.b32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "l"(p));
+    } else {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) v[i] = mx_ld(reinterpret_cast<const uint32_t*>(p) + i);
+    }
+}
+
+// B scales of a token, two a word
+template <int B>
+__device__ __forceinline__ void ldg_scales(const uint8_t* p, uint32_t (&v)[(B + 1) / 2]) {
+    if constexpr (B % 2 == 0) {
+        ldg<B / 2>(p, v);
+    } else {
+        uint32_t h[B + 1];
+#pragma unroll
+        for (int i = 0; i < B; ++i) h[i] = mx_ld(reinterpret_cast<const uint16_t*>(p) + i);
+        h[B] = 0;
+#pragma unroll
+        for (int i = 0; i < (B + 1) / 2; ++i) v[i] = h[2 * i] | h[2 * i + 1] << 16;
+    }
+}
+
 // Decoders: warp d takes chunks d and d + 4 of a step; their keys first, so that the step's scores can start.
 template <typename C>
 __device__ __forceinline__ void tc_decode(const AttnArgs& a, TcWalk w, const TcWaits& wait, uint32_t base, uint8_t* smem) {
-    constexpr int B = C::B, W = (B + 1) / 2, PER = C::SLOTS / TC_DECODERS;
-    const int lane = threadIdx.x & 31, d = (threadIdx.x >> 5) - 8;
-    uint32_t steps = 0, taken = 0;                   // steps of this CTA; chunks of this warp
-    while (true) {
-        tc_next(a, w);
-        if (!w.valid) return;
-        for (int g = w.g0; g < w.g1; ++g, ++steps) {
-            const uint32_t stage = steps % C::STAGES, round = steps / C::STAGES;
-            uint32_t chunk[2];
-            bool gone[2];
-            if (round > 0 && !wait(C::K_EMPTY + stage, (round - 1) & 1)) return;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint32_t slot = d + TC_DECODERS * ((taken + h) % PER);
-                if (!wait(C::RAW_FULL + slot, ((taken + h) / PER) & 1)) return;
-                chunk[h] = base + C::RING + slot * C::CHUNK;
-                gone[h] = reinterpret_cast<volatile int*>(smem + C::META)[slot];
-                const int c = d + TC_DECODERS * h, key0 = g * TC_TILE + c * KV_GROUP;   // of the chunk
-                // value scales that are no number, of keys that are there
-                bool odd = false;
-                if (lane < 16 && !gone[h] && key0 + lane < w.p_seq.len) {
-                    uint32_t v[W];
-                    lds_scales<B>(chunk[h] + 17 * C::DIM + lane * 2 * B, v);
-#pragma unroll
-                    for (int k = 0; k < W; ++k) odd |= __vcmpgtu2(v[k] & 0x7FFF7FFFu, 0x7BFF7BFFu) != 0;
-                }
-                odd = __any_sync(0xffffffffu, odd);
-                if (odd && lane < 16) {
-                    uint32_t v[W], which = 0;
-                    lds_scales<B>(chunk[h] + 17 * C::DIM + lane * 2 * B, v);
-#pragma unroll
-                    for (int b = 0; b < B; ++b) which |= ((v[b / 2] >> (b % 2 * 16)) & 0x7FFFu) > 0x7BFFu && key0 + lane < w.p_seq.len ? 1u << b : 0u;
-                    smem[C::ODD + (steps % TC_INFOS) * TC_TILE + c * KV_GROUP + lane] = (uint8_t)which;
-                }
-                if (lane == 0) smem[C::INFO + (steps % TC_INFOS) * TC_CHUNKS + c] = (uint8_t)((gone[h] ? 1 : 0) | (odd ? 2 : 0));
-                // K: lanes of a quarter-warp take 8 dims of keys i and i + 4, whose 16-byte units then differ
-                const uint32_t to = base + C::K + stage * C::Q_BYTES;
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int i = 8 * j + (lane >> 3) + ((lane >> 2) & 1) * 4, t = lane & 3, key = c * KV_GROUP + i;
-                    uint32_t x[B], sc[W];
-                    lds<B>(chunk[h] + (i * 4 + t) * 4 * B, x);
-                    lds_scales<B>(chunk[h] + 16 * C::DIM + i * 2 * B, sc);
-#pragma unroll
-                    for (int b = 0; b < B; ++b) {
-                        const uint32_t s2 = __byte_perm(sc[b / 2], 0, b % 2 ? 0x3232 : 0x1010);
-                        const uint4 v = nibbles_to_f16x8(x[b]);
-                        const int unit = (b % 2) * 4 + t;
-                        sts128(to + (b / 2) * TC_TILE * 128 + key * 128 + ((unit ^ (key & 7)) << 4), half2_mul(v.x, s2), half2_mul(v.y, s2),
-                               half2_mul(v.z, s2), half2_mul(v.w, s2));
-                    }
-                }
-            }
-            fence_async();
-            __syncwarp();
-            if (lane == 0) wait.arrive(C::K_FULL + stage);
-            if (round > 0 && !wait(C::V_EMPTY + stage, (round - 1) & 1)) return;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint32_t slot = d + TC_DECODERS * ((taken + h) % PER);
-                const int c = d + TC_DECODERS * h, p = lane & 3;
-                // V^T: lane (g, p) has keys 2p, 2p + 1 of dims 4 g + n of each block; matrices of 8 dims x 8 keys, row g of
-                // matrix n at place 32 b + 8 n + g.  The address that this lane gives is that of row lane % 8 of matrix lane / 8.
-                const uint32_t row = (lane >> 3) * 8 + (lane & 7);
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int octet = 2 * c + j, key = g * TC_TILE + octet * 8 + 2 * p;
-                    uint32_t x[B], s0[W], s1[W];
-                    lds<B>(chunk[h] + 8 * C::DIM + (j * 32 + lane) * 4 * B, x);
-                    lds_scales<B>(chunk[h] + 17 * C::DIM + (8 * j + 2 * p) * 2 * B, s0);
-                    lds_scales<B>(chunk[h] + 17 * C::DIM + (8 * j + 2 * p + 1) * 2 * B, s1);
-                    const uint32_t keep = gone[h] ? 0u : (key < w.p_seq.len ? 0x0000FFFFu : 0u) | (key + 1 < w.p_seq.len ? 0xFFFF0000u : 0u);
-                    const uint32_t to = base + C::V + stage * C::V_BYTES + (octet >> 3) * C::DIM * 128 + row * 128 + (((octet & 7) ^ (row & 7)) << 4);
-#pragma unroll
-                    for (int b = 0; b < B; ++b) {
-                        uint32_t s2 = __byte_perm(s0[b / 2], s1[b / 2], b % 2 ? 0x7632 : 0x5410) & keep;
-                        // what is no number becomes 0 here, and the softmax marks the rows that see it
-                        const uint32_t no = __vcmpgtu2(s2 & 0x7FFF7FFFu, 0x7BFF7BFFu);
-                        s2 &= ~no;
-                        const uint4 v = nibbles_to_f16x8(x[b]);
-                        stmatrix4(to + b * 32 * 128, half2_mul(v.x, s2), half2_mul(v.y, s2), half2_mul(v.z, s2), half2_mul(v.w, s2));
-                    }
-                }
-                __syncwarp();
-                if (lane == 0) wait.arrive(C::RAW_EMPTY + slot);
-            }
-            taken += 2;
-            fence_async();
-            __syncwarp();
-            if (lane == 0) wait.arrive(C::V_FULL + stage);
+    constexpr int B = C::B, W = (B + 1) / 2;
+    const int lane = threadIdx.x & 31, d = (threadIdx.x >> 5) - 8, in_page = a.page_log - 4;
+    // K: lanes of a quarter-warp take 8 dims of keys i and i + 4 of an octet, whose 16-byte units then differ; V: two keys of
+    // 4 dims of each block
+    const int i = (lane >> 3) + ((lane >> 2) & 1) * 4, t = lane & 3;
+    // The walk is two steps ahead of the decoding: `next` is the step whose chunks' pages are being looked up, `here` the one
+    // whose codes are on their way.
+    struct Step {
+        int g, len, head;
+        int page[2];                                 // as looked up, not looked at before the codes are loaded
+        bool any;
+    } next, here;
+    next.any = false;
+    int g = 0;
+    tc_next(a, w);
+    if (w.valid) g = w.g0;
+    const auto find = [&]() {
+        while (w.valid && g >= w.g1) {
+            tc_next(a, w);
+            if (w.valid) g = w.g0;
         }
+        next.any = w.valid;
+        if (!w.valid) return;
+        next.g = g;
+        next.len = w.p_seq.len;
+        next.head = w.p_head;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int group = g * TC_CHUNKS + d + TC_DECODERS * h;
+            next.page[h] = -1;
+            if (group * KV_GROUP < next.len)
+                next.page[h] = mx_ld(a.pages + w.p_s * a.max_pages + (group >> in_page));
+        }
+        ++g;
+    };
+    const auto there = [&](const Step& s, int h) { return s.page[h] >= 0 && s.page[h] < a.n_pages; };
+    const auto chunk_of = [&](const Step& s, int h) {
+        const int group = s.g * TC_CHUNKS + d + TC_DECODERS * h;
+        return a.cache + kv_chunk_offset(s.page[h], s.head, group & ((1 << in_page) - 1), a.kv_heads, a.page_log, C::DIM);
+    };
+    uint32_t kx[2][2][B], ks[2][2][W], vx[2][2][B], vs[2][2][2][W];
+    const auto load_k = [&](const Step& s) {
+        if (!s.any) return;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (!there(s, h)) continue;
+            const uint8_t* chunk = chunk_of(s, h);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                ldg<B>(chunk + ((8 * j + i) * 4 + t) * 4 * B, kx[h][j]);
+                ldg_scales<B>(chunk + 16 * C::DIM + (8 * j + i) * 2 * B, ks[h][j]);
+            }
+        }
+    };
+    const auto load_v = [&](const Step& s) {
+        if (!s.any) return;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (!there(s, h)) continue;
+            const uint8_t* chunk = chunk_of(s, h);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                ldg<B>(chunk + 8 * C::DIM + (j * 32 + lane) * 4 * B, vx[h][j]);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) ldg_scales<B>(chunk + 17 * C::DIM + (8 * j + 2 * t + k) * 2 * B, vs[h][j][k]);
+            }
+        }
+    };
+#pragma unroll
+    for (int x = 0; x < 4 * B; ++x) kx[x / (2 * B)][x / B % 2][x % B] = vx[x / (2 * B)][x / B % 2][x % B] = 0u;
+    find();
+    here = next;
+    load_k(here);
+    load_v(here);
+    find();
+    for (uint32_t steps = 0; here.any; ++steps) {
+        const uint32_t stage = steps % C::STAGES, round = steps / C::STAGES, note = steps % TC_INFOS;
+        const Step now = here;
+        here = next;
+        if (round > 0 && !wait(C::K_EMPTY + stage, (round - 1) & 1)) return;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int c = d + TC_DECODERS * h;
+            if (lane == 0) {
+                const bool gone = !there(now, h);
+                smem[C::GONE + note * TC_CHUNKS + c] = gone;
+                if (gone && now.g * TC_TILE + c * KV_GROUP < now.len) record_error(&g_attn_status, Q4Q_ERR_ARG);
+            }
+            const uint32_t to = base + C::K + stage * C::Q_BYTES;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int key = c * KV_GROUP + 8 * j + i;
+#pragma unroll
+                for (int b = 0; b < B; ++b) {
+                    const uint32_t s2 = __byte_perm(ks[h][j][b / 2], 0, b % 2 ? 0x3232 : 0x1010);
+                    const uint4 v = nibbles_to_f16x8(kx[h][j][b]);
+                    const int unit = (b % 2) * 4 + t;
+                    sts128(to + (b / 2) * TC_TILE * 128 + key * 128 + ((unit ^ (key & 7)) << 4), half2_mul(v.x, s2), half2_mul(v.y, s2),
+                           half2_mul(v.z, s2), half2_mul(v.w, s2));
+                }
+            }
+        }
+        fence_async();
+        __syncwarp();
+        if (lane == 0) wait.arrive(C::K_FULL + stage);
+        load_k(here);
+        if (round > 0 && !wait(C::V_EMPTY + stage, (round - 1) & 1)) return;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int c = d + TC_DECODERS * h;
+            bool odd = false;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                // matrices of 8 dims x 8 keys, row g of matrix n at place 32 b + 8 n + g; the address that this lane gives is that
+                // of row lane % 8 of matrix lane / 8
+                const int octet = 2 * c + j, key = now.g * TC_TILE + octet * 8 + 2 * t;
+                const uint32_t keep = !there(now, h) ? 0u : (key < now.len ? 0x0000FFFFu : 0u) | (key + 1 < now.len ? 0xFFFF0000u : 0u);
+                const uint32_t to = base + C::V + stage * C::V_BYTES + (octet >> 3) * C::DIM * 128 + lane * 128 + (((octet & 7) ^ (lane & 7)) << 4);
+#pragma unroll
+                for (int b = 0; b < B; ++b) {
+                    uint32_t s2 = __byte_perm(vs[h][j][0][b / 2], vs[h][j][1][b / 2], b % 2 ? 0x7632 : 0x5410) & keep;
+                    // what is no number becomes 0 here, and the softmax marks the rows that see it
+                    const uint32_t no = __vcmpgtu2(s2 & 0x7FFF7FFFu, 0x7BFF7BFFu);
+                    odd |= no != 0;
+                    s2 &= ~no;
+                    const uint4 v = nibbles_to_f16x8(vx[h][j][b]);
+                    stmatrix4(to + b * 32 * 128, half2_mul(v.x, s2), half2_mul(v.y, s2), half2_mul(v.z, s2), half2_mul(v.w, s2));
+                }
+            }
+            odd = __any_sync(0xffffffffu, odd);
+            if (lane == 0) smem[C::ODD + note * TC_CHUNKS + c] = odd;
+            if (odd && lane < 8) {
+                // lanes 0-3 know keys 2t, 2t + 1 of the first octet, and 4-7 write those of the second
+                const int j = lane >> 2;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    uint32_t which = 0;
+#pragma unroll
+                    for (int b = 0; b < B; ++b) {
+                        const uint32_t word = j ? vs[h][1][k][b / 2] : vs[h][0][k][b / 2];
+                        which |= ((word >> (b % 2 * 16)) & 0x7FFFu) > 0x7BFFu ? 1u << b : 0u;
+                    }
+                    smem[C::WHICH + note * TC_TILE + c * KV_GROUP + 8 * j + 2 * t + k] = (uint8_t)which;
+                }
+            }
+        }
+        load_v(here);
+        fence_async();
+        __syncwarp();
+        if (lane == 0) wait.arrive(C::V_FULL + stage);
+        find();
     }
 }
 
@@ -472,6 +500,15 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// Loads issued so far are done; that the registers go through it keeps their uses behind it.
+__device__ __forceinline__ void tmem_ld_done(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]),
+                   "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]),
+                   "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]),
+                   "+r"(r[31])::"memory");
+}
+
 // The softmax of tile i, a thread a row: queries, weights, and at a piece's end the results.
 template <typename C>
 __device__ __forceinline__ void tc_softmax(const AttnArgs& a, const Plan& plan, TcWalk w, const TcWaits& wait, uint32_t base, uint8_t* smem, uint32_t tmem) {
@@ -491,6 +528,14 @@ __device__ __forceinline__ void tc_softmax(const AttnArgs& a, const Plan& plan, 
         const int lo_all = __reduce_max_sync(0xffffffffu, lo), hi_all = __reduce_min_sync(0xffffffffu, hi);
         float scale = 0.0f, ref = NONE, l = 0.0f;
         uint32_t poison = 0;                                                  // blocks in which the row sees a value that is no number
+        // Blocks of values that are no number, of keys of a step that this row sees.  The step's values are decoded by the time of
+        // the next step's scores, or of the result.
+        const auto marks = [&](uint32_t step, int key0) {
+            const uint64_t odd = *reinterpret_cast<volatile uint64_t*>(smem + C::ODD + (step % TC_INFOS) * TC_CHUNKS);
+            if (!odd) return;
+            for (int k = max(lo - key0, 0); k < min(hi - key0, TC_TILE); ++k)
+                if ((odd >> (k / 16 * 8)) & 1) poison |= *reinterpret_cast<volatile uint8_t*>(smem + C::WHICH + (step % TC_INFOS) * TC_TILE + k);
+        };
         if (n > 0) {
             // the row as fp16 of a power of two times it, its largest in [1, 2); the scale's sign goes along
             const __nv_bfloat16* from = static_cast<const __nv_bfloat16*>(a.q) + at * a.q_stride + head * C::DIM;
@@ -525,34 +570,39 @@ __device__ __forceinline__ void tc_softmax(const AttnArgs& a, const Plan& plan, 
             if (!wait(C::S_FULL + i, steps & 1)) return;
             tc_fence_after();
             const int key0 = (w.g0 + j) * TC_TILE;
-            const uint64_t info = *reinterpret_cast<volatile uint64_t*>(smem + C::INFO + (steps % TC_INFOS) * TC_CHUNKS);
-            const bool edge = key0 < lo_all || key0 + TC_TILE > hi_all || info != 0;
+            const uint64_t gone = *reinterpret_cast<volatile uint64_t*>(smem + C::GONE + (steps % TC_INFOS) * TC_CHUNKS);
+            const bool edge = key0 < lo_all || key0 + TC_TILE > hi_all || gone != 0;
+            if (j > 0) marks(steps - 1, key0 - TC_TILE);
             // keys of this step that the row sees: from .. to - 1, but for chunks that are not there
             const int from = max(lo - key0, 0), to = min(hi - key0, TC_TILE);
-            float most = -INFINITY;
-            if (edge) {
-#pragma unroll 1
-                for (int c = 0; c < TC_TILE; c += 16) {
-                    uint32_t x[16];
-                    tmem_ld<16>(s_at + c, x);
-                    if (!((info >> (c / 2)) & 1))
+            // The row's maximum, the last columns first: the first ones are still in registers when the weights begin with them.
+            uint32_t x[2][32];
+            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            const auto maximum = [&](auto of_edge) {
+                tmem_ld32(s_at + 96, x[1]);
+                tmem_ld_done(x[1]);
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) most = c + k >= from && c + k < to ? fmaxf(most, __uint_as_float(x[k])) : most;
+                for (int q = 3; q >= 0; --q) {
+                    uint32_t(&v)[32] = x[q & 1];
+                    if (q > 0) tmem_ld32(s_at + 32 * (q - 1), x[(q - 1) & 1]);
+                    if constexpr (decltype(of_edge)::value) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) {
+                            const int key = 32 * q + k;
+                            if (key >= from && key < to && !((gone >> (key / 16 * 8)) & 1)) top[k & 3] = fmaxf(top[k & 3], __uint_as_float(v[k]));
+                        }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 8)
+#pragma unroll
+                            for (int n = 0; n < 4; ++n) top[n] = fmaxf(top[n], fmaxf(__uint_as_float(v[k + 2 * n]), __uint_as_float(v[k + 2 * n + 1])));
+                    }
+                    if (q > 0) tmem_ld_done(x[(q - 1) & 1]);
                 }
-                for (int c = 0; c < TC_CHUNKS; ++c)
-                    if ((info >> (8 * c + 1)) & 1)
-                        for (int k = 0; k < KV_GROUP; ++k)
-                            if (c * KV_GROUP + k >= from && c * KV_GROUP + k < to)
-                                poison |= *reinterpret_cast<volatile uint8_t*>(smem + C::ODD + (steps % TC_INFOS) * TC_TILE + c * KV_GROUP + k);
-            } else {
-#pragma unroll
-                for (int c = 0; c < TC_TILE; c += 32) {
-                    uint32_t x[32];
-                    tmem_ld<32>(s_at + c, x);
-#pragma unroll
-                    for (int k = 0; k < 32; k += 2) most = fmaxf(most, fmaxf(__uint_as_float(x[k]), __uint_as_float(x[k + 1])));
-                }
-            }
+            };
+            if (edge) maximum(std::true_type{});
+            else maximum(std::false_type{});
+            const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
             const float y = most == -INFINITY ? -INFINITY : most * scale;
             if (__any_sync(0xffffffffu, y > ref + 8.0f)) {
                 const float to_ref = y > ref + 8.0f ? y : ref, down = exp2f(ref - to_ref);
@@ -562,39 +612,45 @@ __device__ __forceinline__ void tc_softmax(const AttnArgs& a, const Plan& plan, 
                 if (j > 0) {
 #pragma unroll 1
                     for (int c = 0; c < C::DIM; c += 16) {
-                        uint32_t x[16];
-                        tmem_ld<16>(o_at + c, x);
+                        uint32_t old[16];
+                        tmem_ld<16>(o_at + c, old);
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * down);
-                        tmem_st16(o_at + c, x);
+                        for (int k = 0; k < 16; ++k) old[k] = __float_as_uint(__uint_as_float(old[k]) * down);
+                        tmem_st16(o_at + c, old);
                     }
                 }
             }
-            uint64_t sum = 0;
+            uint64_t sum[2] = {0, 0};
             const uint64_t scale2 = pack2(scale, scale), ref2 = pack2(-ref, -ref);
-#pragma unroll 1
-            for (int c = 0; c < TC_TILE; c += 32) {
-                uint32_t x[32], p[16];
-                tmem_ld<32>(s_at + c, x);
+            const auto weights = [&](auto of_edge) {
 #pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    float z0, z1;
-                    unpack2(ffma2(pair_of(x[2 * k], x[2 * k + 1]), scale2, ref2), z0, z1);
-                    z0 = ex2(z0);
-                    z1 = ex2(z1);
-                    if (edge) {
-                        const int key = c + 2 * k;
-                        const bool gone = (info >> (key / 16 * 8)) & 1;
-                        if (key < from || key >= to || gone) z0 = 0.0f;
-                        if (key + 1 < from || key + 1 >= to || gone) z1 = 0.0f;
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t(&v)[32] = x[q & 1];
+                    if (q < 3) tmem_ld32(s_at + 32 * (q + 1), x[(q + 1) & 1]);
+                    uint32_t p[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        float z0, z1;
+                        unpack2(ffma2(pair_of(v[2 * k], v[2 * k + 1]), scale2, ref2), z0, z1);
+                        z0 = ex2(z0);
+                        z1 = ex2(z1);
+                        if constexpr (decltype(of_edge)::value) {
+                            const int key = 32 * q + 2 * k;
+                            const bool lost = (gone >> (key / 16 * 8)) & 1;
+                            if (key < from || key >= to || lost) z0 = 0.0f;
+                            if (key + 1 < from || key + 1 >= to || lost) z1 = 0.0f;
+                        }
+                        sum[k & 1] = fadd2(sum[k & 1], pack2(z0, z1));
+                        p[k] = half2_bits(z0, z1);
                     }
-                    sum = ffma2(sum, pack2(1.0f, 1.0f), pack2(z0, z1));
-                    p[k] = half2_bits(z0, z1);
+                    if (q < 3) tmem_ld_done(x[(q + 1) & 1]);
+                    tmem_st16(s_at + 16 * q, p);                              // over scores that have been read
                 }
-                tmem_st16(s_at + c / 2, p);                                   // over scores that have been read
-            }
+            };
+            if (edge) weights(std::true_type{});
+            else weights(std::false_type{});
             float l0, l1;
-            unpack2(sum, l0, l1);
+            unpack2(fadd2(sum[0], sum[1]), l0, l1);
             l += l0 + l1;
             tmem_st_wait();
             tc_fence_before();
@@ -606,6 +662,7 @@ __device__ __forceinline__ void tc_softmax(const AttnArgs& a, const Plan& plan, 
             if (!wait(C::O_DONE + i, pieces & 1)) return;
             tc_fence_after();
             ++pieces;
+            marks(steps - 1, (w.g1 - 1) * TC_TILE);
         }
         const bool complete = w.first == 0 && w.last == w.of, there = at_row < rows;
         const int part = 2 * blockIdx.x + (w.first == 0 ? 1 : 0);
@@ -663,8 +720,6 @@ __global__ void __launch_bounds__(TC_THREADS, 1) attn_tc_kernel(const __grid_con
     if (warp == 12) tmem_alloc(base + C::TMEM, 512);
     pdl_trigger();
     pdl_wait();
-    // what is copied below may have been written by ordinary stores of the work before
-    asm volatile("fence.proxy.async;" ::: "memory");
     tc_fence_before();
     const TcWalk walk = tc_share(a, plan, reinterpret_cast<int64_t*>(smem + C::WORDS));     // with barriers of the block
     tc_fence_after();
@@ -674,8 +729,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) attn_tc_kernel(const __grid_con
     if (walk.left > 0) {
         if (warp < 8) tc_softmax<C>(a, plan, walk, wait, base, smem, tmem);
         else if (warp < 12) tc_decode<C>(a, walk, wait, base, smem);
-        else if (warp == 12) tc_issue<C>(a, walk, wait, base, tmem);
-        else tc_copy<C>(a, walk, wait, base, smem);
+        else tc_issue<C>(a, walk, wait, base, tmem);
     }
     tc_fence_before();
     __syncthreads();
