@@ -10,13 +10,13 @@
 // A CTA takes 256 rows (tokens x shared heads of a key-value head) as two tiles of 128 rows against steps of 128 keys:
 //   warps 0-3, 4-7   softmax of a tile, a thread a row: S from tensor memory twice (maximum, then weights), P over S,
 //                    the sums' rescaling, the result; at the start of a piece the tile's queries
-//   warps 8-11       decode chunks to the MMAs' operands: K [keys][dims], V^T [dims][keys], 128-byte swizzle, two stages
+//   warps 8-15       decode chunks to the MMAs' operands: K [keys][dims], V^T [dims][keys], 128-byte swizzle, two stages
 //                    each.  Codes and scales come straight from the cache into registers, a step ahead.  A lane of K holds 8
 //                    dims of a key, a 16-byte unit (dims of a unit in the nibbles' order 0 4 1 5 2 6 3 7, queries alike); V's
 //                    words hold two keys of 4 dims, which is what a lane of stmatrix holds of an 8 x 8 matrix [dim][key], so
 //                    rows of V^T are dims 4 g + n at place 8 n + g of their block, and results are put back in order from
 //                    registers
-//   warp 12          MMAs: S_i = Q_i K^T, O_i += P_i V, the two tiles in turn, so that one's softmax runs beside the
+//   warp 16          MMAs: S_i = Q_i K^T, O_i += P_i V, the two tiles in turn, so that one's softmax runs beside the
 //                    other's MMAs
 // Steps of all pieces (sequence, head, 256 rows) in a row are cut into equal shares, one a CTA and SM; parts of a
 // piece are joined by a second kernel in order.
@@ -28,8 +28,12 @@ namespace {
 constexpr int TC_TILE = 128;             // rows of a tile and keys of a step
 constexpr int TC_ROWS = 2 * TC_TILE;     // rows of a piece
 constexpr int TC_CHUNKS = TC_TILE / KV_GROUP;
-constexpr int TC_DECODERS = 4;
-constexpr int TC_THREADS = (8 + TC_DECODERS + 1) * 32;
+constexpr int TC_DECODERS = TC_CHUNKS;   // warps, one for each chunk of a step
+constexpr int TC_ISSUER = 8 + TC_DECODERS;
+constexpr int TC_THREADS = (TC_ISSUER + 4) * 32;
+// Registers a thread: at launch, and as the warpgroups share them out, in all the same number.
+constexpr int TC_REGS = 96, TC_SOFTMAX_REGS = 136, TC_DECODE_REGS = 80, TC_OTHER_REGS = 48;
+static_assert(256 * TC_SOFTMAX_REGS + 256 * TC_DECODE_REGS + 128 * TC_OTHER_REGS <= TC_THREADS * TC_REGS, "registers of the launch");
 constexpr int TC_INFOS = 4;              // steps whose notes are kept: decoders are at most 2 ahead of the softmax
 
 template <int B_>
@@ -244,7 +248,7 @@ __device__ __forceinline__ void ldg_scales(const uint8_t* p, uint32_t (&v)[(B + 
     }
 }
 
-// Decoders: warp d takes chunks d and d + 4 of a step; their keys first, so that the step's scores can start.
+// Decoders: warp d takes chunk d of a step; its keys first, so that the step's scores can start.
 template <typename C>
 __device__ __forceinline__ void tc_decode(const AttnArgs& a, TcWalk w, const TcWaits& wait, uint32_t base, uint8_t* smem) {
     constexpr int B = C::B, W = (B + 1) / 2;
@@ -256,7 +260,8 @@ __device__ __forceinline__ void tc_decode(const AttnArgs& a, TcWalk w, const TcW
     // whose codes are on their way.
     struct Step {
         int g, len, head;
-        int page[2];                                 // as looked up, not looked at before the codes are loaded
+        int page;                                    // as looked up, not looked at before the codes are loaded
+        const uint8_t* chunk;                        // null: not there
         bool any;
     } next, here;
     next.any = false;
@@ -273,50 +278,35 @@ __device__ __forceinline__ void tc_decode(const AttnArgs& a, TcWalk w, const TcW
         next.g = g;
         next.len = w.p_seq.len;
         next.head = w.p_head;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int group = g * TC_CHUNKS + d + TC_DECODERS * h;
-            next.page[h] = -1;
-            if (group * KV_GROUP < next.len)
-                next.page[h] = mx_ld(a.pages + w.p_s * a.max_pages + (group >> in_page));
-        }
+        next.page = -1;
+        const int group = g * TC_CHUNKS + d;
+        if (group * KV_GROUP < next.len) next.page = mx_ld(a.pages + w.p_s * a.max_pages + (group >> in_page));
         ++g;
     };
-    const auto there = [&](const Step& s, int h) { return s.page[h] >= 0 && s.page[h] < a.n_pages; };
-    const auto chunk_of = [&](const Step& s, int h) {
-        const int group = s.g * TC_CHUNKS + d + TC_DECODERS * h;
-        return a.cache + kv_chunk_offset(s.page[h], s.head, group & ((1 << in_page) - 1), a.kv_heads, a.page_log, C::DIM);
-    };
-    uint32_t kx[2][2][B], ks[2][2][W], vx[2][2][B], vs[2][2][2][W];
-    const auto load_k = [&](const Step& s) {
-        if (!s.any) return;
+    uint32_t kx[2][B], ks[2][W], vx[2][B], vs[2][2][W];
+    const auto load_k = [&](Step& s) {
+        s.chunk = nullptr;
+        if (!s.any || s.page < 0 || s.page >= a.n_pages) return;
+        s.chunk = a.cache + kv_chunk_offset(s.page, s.head, (s.g * TC_CHUNKS + d) & ((1 << in_page) - 1), a.kv_heads, a.page_log, C::DIM);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if (!there(s, h)) continue;
-            const uint8_t* chunk = chunk_of(s, h);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                ldg<B>(chunk + ((8 * j + i) * 4 + t) * 4 * B, kx[h][j]);
-                ldg_scales<B>(chunk + 16 * C::DIM + (8 * j + i) * 2 * B, ks[h][j]);
-            }
+        for (int j = 0; j < 2; ++j) {
+            ldg<B>(s.chunk + ((8 * j + i) * 4 + t) * 4 * B, kx[j]);
+            ldg_scales<B>(s.chunk + 16 * C::DIM + (8 * j + i) * 2 * B, ks[j]);
         }
     };
     const auto load_v = [&](const Step& s) {
-        if (!s.any) return;
+        if (!s.chunk) return;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if (!there(s, h)) continue;
-            const uint8_t* chunk = chunk_of(s, h);
+        for (int j = 0; j < 2; ++j) {
+            ldg<B>(s.chunk + 8 * C::DIM + (j * 32 + lane) * 4 * B, vx[j]);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                ldg<B>(chunk + 8 * C::DIM + (j * 32 + lane) * 4 * B, vx[h][j]);
-#pragma unroll
-                for (int k = 0; k < 2; ++k) ldg_scales<B>(chunk + 17 * C::DIM + (8 * j + 2 * t + k) * 2 * B, vs[h][j][k]);
-            }
+            for (int k = 0; k < 2; ++k) ldg_scales<B>(s.chunk + 17 * C::DIM + (8 * j + 2 * t + k) * 2 * B, vs[j][k]);
         }
     };
 #pragma unroll
-    for (int x = 0; x < 4 * B; ++x) kx[x / (2 * B)][x / B % 2][x % B] = vx[x / (2 * B)][x / B % 2][x % B] = 0u;
+    for (int x = 0; x < 2 * B; ++x) kx[x / B][x % B] = vx[x / B][x % B] = 0u;
+#pragma unroll
+    for (int x = 0; x < 2 * W; ++x) ks[x / W][x % W] = vs[x / W][0][x % W] = vs[x / W][1][x % W] = 0u;
     find();
     here = next;
     load_k(here);
@@ -324,74 +314,69 @@ __device__ __forceinline__ void tc_decode(const AttnArgs& a, TcWalk w, const TcW
     find();
     for (uint32_t steps = 0; here.any; ++steps) {
         const uint32_t stage = steps % C::STAGES, round = steps / C::STAGES, note = steps % TC_INFOS;
-        const Step now = here;
+        const int key0 = here.g * TC_TILE + d * KV_GROUP, left = here.len - key0;     // of the chunk; its tokens
+        const bool gone = !here.chunk;
         here = next;
+        if (lane == 0) {
+            smem[C::GONE + note * TC_CHUNKS + d] = gone;
+            if (gone && left > 0) record_error(&g_attn_status, Q4Q_ERR_ARG);
+        }
         if (round > 0 && !wait(C::K_EMPTY + stage, (round - 1) & 1)) return;
+        {
+            const uint32_t to = base + C::K + stage * C::Q_BYTES + (d * KV_GROUP + i) * 128;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int c = d + TC_DECODERS * h;
-            if (lane == 0) {
-                const bool gone = !there(now, h);
-                smem[C::GONE + note * TC_CHUNKS + c] = gone;
-                if (gone && now.g * TC_TILE + c * KV_GROUP < now.len) record_error(&g_attn_status, Q4Q_ERR_ARG);
-            }
-            const uint32_t to = base + C::K + stage * C::Q_BYTES;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int key = c * KV_GROUP + 8 * j + i;
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int b = 0; b < B; ++b) {
-                    const uint32_t s2 = __byte_perm(ks[h][j][b / 2], 0, b % 2 ? 0x3232 : 0x1010);
-                    const uint4 v = nibbles_to_f16x8(kx[h][j][b]);
-                    const int unit = (b % 2) * 4 + t;
-                    sts128(to + (b / 2) * TC_TILE * 128 + key * 128 + ((unit ^ (key & 7)) << 4), half2_mul(v.x, s2), half2_mul(v.y, s2),
+                    const uint32_t s2 = __byte_perm(ks[j][b / 2], 0, b % 2 ? 0x3232 : 0x1010);
+                    const uint4 v = nibbles_to_f16x8(kx[j][b]);
+                    sts128(to + (b / 2) * TC_TILE * 128 + j * 1024 + ((((b % 2) * 4 + t) ^ i) << 4), half2_mul(v.x, s2), half2_mul(v.y, s2),
                            half2_mul(v.z, s2), half2_mul(v.w, s2));
                 }
-            }
         }
         fence_async();
         __syncwarp();
         if (lane == 0) wait.arrive(C::K_FULL + stage);
         load_k(here);
+        // Scales of keys that are not there become 0, and so do those that are no number: the softmax marks the rows that see
+        // those.
+        if (gone || left < KV_GROUP)
+#pragma unroll
+            for (int x = 0; x < 4 * W; ++x)
+                if (gone || x / (2 * W) * 8 + 2 * t + x / W % 2 >= left) vs[x / (2 * W)][x / W % 2][x % W] = 0u;
+        uint32_t no = 0;
+#pragma unroll
+        for (int x = 0; x < 4 * W; ++x) no |= __vcmpgtu2(vs[x / (2 * W)][x / W % 2][x % W] & 0x7FFF7FFFu, 0x7BFF7BFFu);
+        const bool odd = __any_sync(0xffffffffu, no != 0);
+        if (lane == 0) smem[C::ODD + note * TC_CHUNKS + d] = odd;
+        if (odd) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const int j = x / 2, k = x % 2;
+                uint32_t which = 0;
+#pragma unroll
+                for (int q = 0; q < W; ++q) {
+                    const uint32_t bad = __vcmpgtu2(vs[j][k][q] & 0x7FFF7FFFu, 0x7BFF7BFFu);
+                    which |= (bad & 1u ? 1u << (2 * q) : 0u) | (bad >> 16 ? 2u << (2 * q) : 0u);
+                    vs[j][k][q] &= ~bad;
+                }
+                if (lane < 4) smem[C::WHICH + note * TC_TILE + d * KV_GROUP + 8 * j + 2 * t + k] = (uint8_t)which;
+            }
+        }
         if (round > 0 && !wait(C::V_EMPTY + stage, (round - 1) & 1)) return;
+        {
+            // matrices of 8 dims x 8 keys, row g of matrix n at place 32 b + 8 n + g; the address that this lane gives is that of
+            // row lane % 8 of matrix lane / 8
+            const uint32_t to = base + C::V + stage * C::V_BYTES + (d >> 2) * C::DIM * 128 + lane * 128;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int c = d + TC_DECODERS * h;
-            bool odd = false;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                // matrices of 8 dims x 8 keys, row g of matrix n at place 32 b + 8 n + g; the address that this lane gives is that
-                // of row lane % 8 of matrix lane / 8
-                const int octet = 2 * c + j, key = now.g * TC_TILE + octet * 8 + 2 * t;
-                const uint32_t keep = !there(now, h) ? 0u : (key < now.len ? 0x0000FFFFu : 0u) | (key + 1 < now.len ? 0xFFFF0000u : 0u);
-                const uint32_t to = base + C::V + stage * C::V_BYTES + (octet >> 3) * C::DIM * 128 + lane * 128 + (((octet & 7) ^ (lane & 7)) << 4);
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int b = 0; b < B; ++b) {
-                    uint32_t s2 = __byte_perm(vs[h][j][0][b / 2], vs[h][j][1][b / 2], b % 2 ? 0x7632 : 0x5410) & keep;
-                    // what is no number becomes 0 here, and the softmax marks the rows that see it
-                    const uint32_t no = __vcmpgtu2(s2 & 0x7FFF7FFFu, 0x7BFF7BFFu);
-                    odd |= no != 0;
-                    s2 &= ~no;
-                    const uint4 v = nibbles_to_f16x8(vx[h][j][b]);
-                    stmatrix4(to + b * 32 * 128, half2_mul(v.x, s2), half2_mul(v.y, s2), half2_mul(v.z, s2), half2_mul(v.w, s2));
+                    const uint32_t s2 = __byte_perm(vs[j][0][b / 2], vs[j][1][b / 2], b % 2 ? 0x7632 : 0x5410);
+                    const uint4 v = nibbles_to_f16x8(vx[j][b]);
+                    stmatrix4(to + b * 32 * 128 + ((((2 * d + j) & 7) ^ (lane & 7)) << 4), half2_mul(v.x, s2), half2_mul(v.y, s2), half2_mul(v.z, s2),
+                              half2_mul(v.w, s2));
                 }
-            }
-            odd = __any_sync(0xffffffffu, odd);
-            if (lane == 0) smem[C::ODD + note * TC_CHUNKS + c] = odd;
-            if (odd && lane < 8) {
-                // lanes 0-3 know keys 2t, 2t + 1 of the first octet, and 4-7 write those of the second
-                const int j = lane >> 2;
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    uint32_t which = 0;
-#pragma unroll
-                    for (int b = 0; b < B; ++b) {
-                        const uint32_t word = j ? vs[h][1][k][b / 2] : vs[h][0][k][b / 2];
-                        which |= ((word >> (b % 2 * 16)) & 0x7FFFu) > 0x7BFFu ? 1u << b : 0u;
-                    }
-                    smem[C::WHICH + note * TC_TILE + c * KV_GROUP + 8 * j + 2 * t + k] = (uint8_t)which;
-                }
-            }
         }
         load_v(here);
         fence_async();
@@ -717,7 +702,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) attn_tc_kernel(const __grid_con
                                   : (tid >= C::Q_FULL && tid < C::S_FULL) || (tid >= C::P_FULL && tid < C::O_DONE) ? 4 : 1);
     if (tid == 0) *wait.stop = 0;
     fence_mbar_init();
-    if (warp == 12) tmem_alloc(base + C::TMEM, 512);
+    if (warp == TC_ISSUER) tmem_alloc(base + C::TMEM, 512);
     pdl_trigger();
     pdl_wait();
     tc_fence_before();
@@ -726,15 +711,20 @@ __global__ void __launch_bounds__(TC_THREADS, 1) attn_tc_kernel(const __grid_con
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + C::TMEM);
     if (tid < 2) plan.parts[2 * blockIdx.x + tid].of = -1;
     __syncthreads();
-    if (walk.left > 0) {
-        if (warp < 8) tc_softmax<C>(a, plan, walk, wait, base, smem, tmem);
-        else if (warp < 12) tc_decode<C>(a, walk, wait, base, smem);
-        else tc_issue<C>(a, walk, wait, base, tmem);
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(TC_SOFTMAX_REGS));
+        if (walk.left > 0) tc_softmax<C>(a, plan, walk, wait, base, smem, tmem);
+    } else if (warp < TC_ISSUER) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(TC_DECODE_REGS));
+        if (walk.left > 0) tc_decode<C>(a, walk, wait, base, smem);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(TC_OTHER_REGS));
+        if (warp == TC_ISSUER && walk.left > 0) tc_issue<C>(a, walk, wait, base, tmem);
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 12) tmem_dealloc(tmem, 512);
+    if (warp == TC_ISSUER) tmem_dealloc(tmem, 512);
 }
 
 // Joins the parts of the pieces that were cut: block (w, y) rows 8 y .. of the one that starts in worker w, a warp a row.
