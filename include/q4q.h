@@ -653,7 +653,7 @@ Q4Q_API q4q_status q4q_kv_attn_workspace_size(int64_t n_q, int n_q_heads, int n_
  * pages int32 [n_seqs][max_pages], kv_len int32 [n_seqs], first int32 [n_seqs + 1]: device.  kv_len
  * beyond max_pages pages counts as that many, and a page outside the cache as one that no row
  * sees; both record Q4Q_ERR_ARG.  workspace: 256-byte aligned.  n_q_heads a multiple of n_kv_heads,
- * up to 1024; n_q < 2^24, n_seqs < 2^20, max_pages * page_tokens < 2^31.  Queries below 2^100.  The result
+ * up to 1024; n_q < 2^24, n_q * n_q_heads / n_kv_heads < 2^31, n_seqs < 2^20, max_pages * page_tokens < 2^31.  Queries below 2^100.  The result
  * depends on the operands and the device alone. */
 Q4Q_API q4q_status q4q_kv_attn(const void* q, int64_t q_stride, int type, int64_t n_q, int n_q_heads, int n_kv_heads, int64_t head_dim,
                        const void* cache, int64_t n_pages, int page_tokens, const int32_t* pages, int64_t max_pages,

@@ -35,6 +35,7 @@ q4q_status check(AttnArgs& a, const void* q, int64_t q_stride, int type, int64_t
         return Q4Q_ERR_SHAPE;
     if (q_stride < n_q_heads * head_dim || q_stride >= (1ll << 31)) return Q4Q_ERR_SHAPE;
     if (!first && n_seqs > n_q) return Q4Q_ERR_SHAPE;
+    if (n_q * (n_q_heads / n_kv_heads) >= (1ll << 31)) return Q4Q_ERR_SHAPE;
     if (!mx_type_ok(type) || !(scale == scale)) return Q4Q_ERR_ARG;
     empty = n_q == 0 || n_seqs == 0;
     if (empty) return Q4Q_OK;
@@ -59,6 +60,11 @@ q4q_status check(AttnArgs& a, const void* q, int64_t q_stride, int type, int64_t
     a.heads = n_q_heads;
     a.kv_heads = n_kv_heads;
     a.shared = n_q_heads / n_kv_heads;
+    if (a.shared > 1) {
+        const MxDivisor d = mx_divisor((uint32_t)a.shared);
+        a.shared_m = d.m;
+        a.shared_s = d.s;
+    }
     a.type = type;
     a.causal = causal != 0;
     a.align = aligned(q, 16) && aligned(dst, 16) && q_stride * size % 16 == 0 ? 16 : 1;

@@ -130,9 +130,12 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs& a, int s, bool whole) {
 
 __device__ __forceinline__ int64_t units_of(const AttnArgs& a, const Seq& s) { return (int64_t)s.tiles * a.kv_heads * s.cost; }
 
+// row / shared
+__device__ __forceinline__ int divided(int row, const AttnArgs& a) { return a.shared == 1 ? row : (int)(__umulhi((uint32_t)row, a.shared_m) >> a.shared_s); }
+
 // The keys that row `row` (token * shared + head) of a sequence sees: [lo, hi).
 __device__ __forceinline__ void keys_of(const AttnArgs& a, const Seq& s, int row, int& lo, int& hi) {
-    const int64_t last = a.causal ? (int64_t)s.len - s.n + row / a.shared : (int64_t)s.len - 1;
+    const int64_t last = a.causal ? (int64_t)s.len - s.n + divided(row, a) : (int64_t)s.len - 1;
     hi = (int)max(last + 1, (int64_t)0);
     lo = a.window > 0 ? (int)max(last + 1 - a.window, (int64_t)0) : 0;
     if (lo > hi) lo = hi;

@@ -9,7 +9,7 @@
 //
 // A CTA takes 256 rows (tokens x shared heads of a key-value head) as two tiles of 128 rows against steps of 128 keys:
 //   warps 0-3, 4-7   softmax of a tile, a thread a row: S from tensor memory twice (maximum, then weights), P over S,
-//                    the sums' rescaling, the result; at the start of a piece the tile's queries
+//                    the sums' rescaling, the result
 //   warps 8-15       decode chunks to the MMAs' operands: K [keys][dims], V^T [dims][keys], 128-byte swizzle, two stages
 //                    each.  Codes and scales come straight from the cache into registers, a step ahead.  A lane of K holds 8
 //                    dims of a key, a 16-byte unit (dims of a unit in the nibbles' order 0 4 1 5 2 6 3 7, queries alike); V's
@@ -18,6 +18,7 @@
 //                    registers
 //   warp 16          MMAs: S_i = Q_i K^T, O_i += P_i V, the two tiles in turn, so that one's softmax runs beside the
 //                    other's MMAs
+//   warps 17-19      the next piece's queries
 // Steps of all pieces (sequence, head, 256 rows) in a row are cut into equal shares, one a CTA and SM; parts of a
 // piece are joined by a second kernel in order.
 #include "q4q_attn_kernel.cuh"
@@ -30,10 +31,12 @@ constexpr int TC_ROWS = 2 * TC_TILE;     // rows of a piece
 constexpr int TC_CHUNKS = TC_TILE / KV_GROUP;
 constexpr int TC_DECODERS = TC_CHUNKS;   // warps, one for each chunk of a step
 constexpr int TC_ISSUER = 8 + TC_DECODERS;
-constexpr int TC_THREADS = (TC_ISSUER + 4) * 32;
+constexpr int TC_LOADERS = 3;
+constexpr int TC_THREADS = (TC_ISSUER + 1 + TC_LOADERS) * 32;
 // Registers a thread: at launch, and as the warpgroups share them out, in all the same number.
 constexpr int TC_REGS = 96, TC_SOFTMAX_REGS = 136, TC_DECODE_REGS = 80, TC_OTHER_REGS = 48;
 static_assert(256 * TC_SOFTMAX_REGS + 256 * TC_DECODE_REGS + 128 * TC_OTHER_REGS <= TC_THREADS * TC_REGS, "registers of the launch");
+constexpr int TC_SNAP = 3;               // steps that a share may be longer or shorter, so that it ends with a piece
 constexpr int TC_INFOS = 4;              // steps whose notes are kept: decoders are at most 2 ahead of the softmax
 
 template <int B_>
@@ -43,16 +46,17 @@ struct Tc {
     static constexpr int Q_BYTES = ATOMS * TC_TILE * 128, V_BYTES = 2 * DIM * 128;
     static constexpr int STAGES = 2;
     // barriers
-    enum { K_FULL = 0, K_EMPTY = K_FULL + STAGES, V_FULL = K_EMPTY + STAGES, V_EMPTY = V_FULL + STAGES, Q_FULL = V_EMPTY + STAGES, S_FULL = Q_FULL + 2,
+    enum { K_FULL = 0, K_EMPTY = K_FULL + STAGES, V_FULL = K_EMPTY + STAGES, V_EMPTY = V_FULL + STAGES, Q_FIRST = V_EMPTY + STAGES, Q_FULL, Q_FREE, S_FULL,
            P_FULL = S_FULL + 2, O_DONE = P_FULL + 2, DRAIN = O_DONE + 2, BARS };
     static constexpr int STOP = BARS * 8, TMEM = STOP + 4;
     static constexpr int WORDS = (TMEM + 4 + 7) / 8 * 8;           // scan and broadcast words
     static constexpr int GONE = 512, ODD = GONE + TC_INFOS * 8;    // [TC_INFOS][8] bytes: chunks that are not there; with scales that are no number
     static constexpr int WHICH = 1024;                             // [TC_INFOS][128] bytes: bit b, the key's scale of V's block b is no number
-    static constexpr int Q = 2048;
+    static constexpr int SCALE = 1536;                             // [2][256] fp32: what a row's scores are multiplied by, of a piece and the next
+    static constexpr int Q = 4096;
     static constexpr int K = Q + 2 * Q_BYTES, V = K + STAGES * Q_BYTES;
     static constexpr int BYTES = V + STAGES * V_BYTES + 1024;      // the tiles start on 1024 bytes
-    static_assert(WORDS + (TC_THREADS / 32 + 6) * 8 <= GONE && ODD + TC_INFOS * 8 <= WHICH, "small things before the tiles");
+    static_assert(WORDS + (TC_THREADS / 32 + 7) * 8 <= GONE && ODD + TC_INFOS * 8 <= WHICH, "small things before the tiles");
     static_assert(K % 1024 == 0 && V % 1024 == 0 && BYTES <= 227 * 1024, "shared memory");
 };
 
@@ -101,6 +105,11 @@ __device__ __forceinline__ void tc_next(const AttnArgs& a, TcWalk& w) {
         }
         int c0, c1;
         const int cost = tc_cost(a, w.seq, w.tile, c0, c1);
+        if (w.from >= cost) {                        // a share that starts with the next piece
+            w.from = 0;
+            ++w.tile;
+            continue;
+        }
         w.p_s = w.s;
         w.p_head = w.head;
         w.p_tile = w.tile;
@@ -122,7 +131,7 @@ __device__ __forceinline__ void tc_next(const AttnArgs& a, TcWalk& w) {
     }
 }
 
-// This worker's share of all steps: its walk.  words: TC_THREADS / 32 + 6 words of shared memory.
+// This worker's share of all steps: its walk.  words: TC_THREADS / 32 + 7 words of shared memory.
 __device__ __forceinline__ TcWalk tc_share(const AttnArgs& a, const Plan& plan, int64_t* words) {
     constexpr int WARPS = TC_THREADS / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -145,41 +154,51 @@ __device__ __forceinline__ TcWalk tc_share(const AttnArgs& a, const Plan& plan, 
     }
     const int64_t workers = min((int64_t)plan.workers, max((int64_t)1, total / plan.least));
     const bool works = blockIdx.x < workers;
-    const int64_t u0 = works ? (total * blockIdx.x + workers - 1) / workers : total;
-    const int64_t u1 = works ? (total * (blockIdx.x + 1) + workers - 1) / workers : total;
-    if (u0 < u1 && before <= u0 && u0 < before + sum) {
-        int s = s0;
-        int64_t head_cost;
-        while (true) {
-            head_cost = tc_head_cost(a, seq_of<TC_ROWS>(a, s, false));
-            if (u0 < before + head_cost * a.kv_heads) break;
-            before += head_cost * a.kv_heads;
-            ++s;
+    // A share ends with a piece where one ends near: what is cut has to be joined.
+    const int64_t snap = min(total / workers / 6, (int64_t)TC_SNAP);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int64_t u = works ? (total * (blockIdx.x + k) + workers - 1) / workers : total;
+        if (u >= total && tid == 0) words[WARPS + 1 + k] = total;
+        if (u < total && before <= u && u < before + sum) {
+            int s = s0;
+            int64_t head_cost, base = before;
+            while (true) {
+                head_cost = tc_head_cost(a, seq_of<TC_ROWS>(a, s, false));
+                if (u < base + head_cost * a.kv_heads) break;
+                base += head_cost * a.kv_heads;
+                ++s;
+            }
+            const Seq seq = seq_of<TC_ROWS>(a, s, false);
+            int64_t rel = u - base;
+            const int64_t head = rel / head_cost;
+            rel -= head * head_cost;
+            int tile = 0, c0, c1, cost;
+            for (;; ++tile) {
+                cost = tc_cost(a, seq, tile, c0, c1);
+                if (rel < cost || tile + 1 >= seq.tiles) break;
+                rel -= cost;
+            }
+            // to the piece's end, which the walk finds by itself, or to its start
+            const int64_t move = cost - rel <= snap ? cost - rel : rel <= snap ? -rel : 0;
+            words[WARPS + 1 + k] = u + move;
+            if (k == 0) {
+                words[WARPS + 3] = s;
+                words[WARPS + 4] = head;
+                words[WARPS + 5] = tile;
+                words[WARPS + 6] = rel + move;
+            }
         }
-        const Seq seq = seq_of<TC_ROWS>(a, s, false);
-        int64_t rel = u0 - before;
-        const int64_t head = rel / head_cost;
-        rel -= head * head_cost;
-        int tile = 0, c0, c1;
-        for (; tile + 1 < seq.tiles; ++tile) {
-            const int cost = tc_cost(a, seq, tile, c0, c1);
-            if (rel < cost) break;
-            rel -= cost;
-        }
-        words[WARPS] = s;
-        words[WARPS + 1] = head;
-        words[WARPS + 2] = tile;
-        words[WARPS + 3] = rel;
     }
     __syncthreads();
     TcWalk w;
-    w.left = u1 - u0;
+    w.left = words[WARPS + 2] - words[WARPS + 1];
     w.valid = false;
     if (w.left <= 0) return w;
-    w.s = (int)words[WARPS];
-    w.head = (int)words[WARPS + 1];
-    w.tile = (int)words[WARPS + 2];
-    w.from = (int)words[WARPS + 3];
+    w.s = (int)words[WARPS + 3];
+    w.head = (int)words[WARPS + 4];
+    w.tile = (int)words[WARPS + 5];
+    w.from = (int)words[WARPS + 6];
     w.seq = seq_of<TC_ROWS>(a, w.s, false);
     return w;
 }
@@ -434,17 +453,16 @@ __device__ __forceinline__ void tc_issue(const AttnArgs& a, TcWalk w, const TcWa
         const int n = w.g1 - w.g0;
         if (n <= 0) continue;
         // the first step's scores
-        ok = wait(C::K_FULL + steps % C::STAGES, (steps / C::STAGES) & 1);
+        ok = (pieces == 0 ? wait(C::Q_FIRST, 0) : wait(C::Q_FULL, (pieces - 1) & 1)) && wait(C::K_FULL + steps % C::STAGES, (steps / C::STAGES) & 1);
+        if (!ok) break;
+        tc_fence_after();
 #pragma unroll
-        for (int i = 0; i < 2 && ok; ++i) {
-            ok = wait(C::Q_FULL + i, pieces & 1);
-            if (!ok) break;
-            tc_fence_after();
+        for (int i = 0; i < 2; ++i) {
             scores(i, steps % C::STAGES);
             commit(C::S_FULL + i);
         }
-        if (!ok) break;
         commit(C::K_EMPTY + steps % C::STAGES);
+        if (n == 1) commit(C::Q_FREE);
         for (int j = 0; j < n && ok; ++j) {
             const uint32_t at = steps + j, stage = at % C::STAGES, parity = (at / C::STAGES) & 1, next = (at + 1) % C::STAGES;
 #pragma unroll
@@ -467,6 +485,7 @@ __device__ __forceinline__ void tc_issue(const AttnArgs& a, TcWalk w, const TcWa
             if (!ok) break;
             commit(C::V_EMPTY + stage);
             if (j + 1 < n) commit(C::K_EMPTY + next);
+            if (j + 2 == n) commit(C::Q_FREE);
         }
         steps += n;
         ++pieces;
@@ -493,6 +512,9 @@ __device__ __forceinline__ void tmem_ld_done(uint32_t (&r)[32]) {
                    "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]),
                    "+r"(r[31])::"memory");
 }
+
+template <typename C>
+__device__ __forceinline__ void tc_rows(const AttnArgs& a, const TcWalk& w, int warp, int warps, uint32_t parity, uint32_t base, uint8_t* smem);
 
 // The softmax of tile i, a thread a row: queries, weights, and at a piece's end the results.
 template <typename C>
@@ -521,46 +543,32 @@ __device__ __forceinline__ void tc_softmax(const AttnArgs& a, const Plan& plan, 
             for (int k = max(lo - key0, 0); k < min(hi - key0, TC_TILE); ++k)
                 if ((odd >> (k / 16 * 8)) & 1) poison |= *reinterpret_cast<volatile uint8_t*>(smem + C::WHICH + (step % TC_INFOS) * TC_TILE + k);
         };
-        if (n > 0) {
-            // the row as fp16 of a power of two times it, its largest in [1, 2); the scale's sign goes along
-            const __nv_bfloat16* from = static_cast<const __nv_bfloat16*>(a.q) + at * a.q_stride + head * C::DIM;
-            float top = 0.0f;
-            Raw8<__nv_bfloat16> raw[4 * B];
-#pragma unroll
-            for (int u = 0; u < 4 * B; ++u) {
-                raw_load(from + 8 * u, a.align, raw[u]);
-                const uint32_t x[4] = {raw[u].w[0].x, raw[u].w[0].y, raw[u].w[0].z, raw[u].w[0].w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) top = fmaxf(top, fmaxf(fabsf(__uint_as_float(x[k] << 16)), fabsf(__uint_as_float(x[k] & 0xffff0000u))));
-            }
-            const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 100);
-            const float up = a.scale_log2 < 0.0f ? -two_to(-e) : two_to(-e);
-            scale = fabsf(a.scale_log2) * two_to(e);
-#pragma unroll
-            for (int u = 0; u < 4 * B; ++u) {
-                Row8 x;
-                float v[8];
-                raw_get(raw[u], x);
-                x.get(v);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) v[k] *= up;
-                sts128(base + C::Q + i * C::Q_BYTES + (u / 8) * TC_TILE * 128 + r * 128 + (((u & 7) ^ (r & 7)) << 4), half2_bits(v[0], v[4]),
-                       half2_bits(v[1], v[5]), half2_bits(v[2], v[6]), half2_bits(v[3], v[7]));
-            }
-            fence_async();
-            __syncwarp();
-            if (lane == 0) wait.arrive(C::Q_FULL + i);
+        if (n > 0 && pieces == 0) {
+            tc_rows<C>(a, w, warp, 8, 0, base, smem);
+            if (lane == 0) wait.arrive(C::Q_FIRST);
         }
         for (int j = 0; j < n; ++j, ++steps) {
             if (!wait(C::S_FULL + i, steps & 1)) return;
             tc_fence_after();
+            if (j == 0) scale = *reinterpret_cast<volatile float*>(smem + C::SCALE + ((pieces & 1) * TC_ROWS + i * TC_TILE + r) * 4);
             const int key0 = (w.g0 + j) * TC_TILE;
             const uint64_t gone = *reinterpret_cast<volatile uint64_t*>(smem + C::GONE + (steps % TC_INFOS) * TC_CHUNKS);
             const bool edge = key0 < lo_all || key0 + TC_TILE > hi_all || gone != 0;
             if (j > 0) marks(steps - 1, key0 - TC_TILE);
             // keys of this step that the row sees: from .. to - 1, but for chunks that are not there
             const int from = max(lo - key0, 0), to = min(hi - key0, TC_TILE);
+            uint32_t seen[4];                        // bit k % 32 of seen[k / 32]: the row sees key k of the step
+            if (edge)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int f = min(max(from - 32 * q, 0), 32), t = min(max(to - 32 * q, 0), 32);
+                    seen[q] = t > f ? (0xffffffffu >> (32 - (t - f))) << f : 0u;
+                    if ((gone >> (16 * q)) & 1) seen[q] &= 0xffff0000u;
+                    if ((gone >> (16 * q + 8)) & 1) seen[q] &= 0x0000ffffu;
+                }
             // The row's maximum, the last columns first: the first ones are still in registers when the weights begin with them.
+            // (Reading halves of the columns once, with a maximum for each, came out slower: 621 us against 539 for 8 x 512 rows
+            // over 8192 keys.)
             uint32_t x[2][32];
             float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
             const auto maximum = [&](auto of_edge) {
@@ -572,10 +580,7 @@ __device__ __forceinline__ void tc_softmax(const AttnArgs& a, const Plan& plan, 
                     if (q > 0) tmem_ld32(s_at + 32 * (q - 1), x[(q - 1) & 1]);
                     if constexpr (decltype(of_edge)::value) {
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) {
-                            const int key = 32 * q + k;
-                            if (key >= from && key < to && !((gone >> (key / 16 * 8)) & 1)) top[k & 3] = fmaxf(top[k & 3], __uint_as_float(v[k]));
-                        }
+                        for (int k = 0; k < 32; ++k) top[k & 3] = (seen[q] >> k) & 1 ? fmaxf(top[k & 3], __uint_as_float(v[k])) : top[k & 3];
                     } else {
 #pragma unroll
                         for (int k = 0; k < 32; k += 8)
@@ -620,10 +625,8 @@ __device__ __forceinline__ void tc_softmax(const AttnArgs& a, const Plan& plan, 
                         z0 = ex2(z0);
                         z1 = ex2(z1);
                         if constexpr (decltype(of_edge)::value) {
-                            const int key = 32 * q + 2 * k;
-                            const bool lost = (gone >> (key / 16 * 8)) & 1;
-                            if (key < from || key >= to || lost) z0 = 0.0f;
-                            if (key + 1 < from || key + 1 >= to || lost) z1 = 0.0f;
+                            z0 = (seen[q] >> (2 * k)) & 1 ? z0 : 0.0f;
+                            z1 = (seen[q] >> (2 * k + 1)) & 1 ? z1 : 0.0f;
                         }
                         sum[k & 1] = fadd2(sum[k & 1], pack2(z0, z1));
                         p[k] = half2_bits(z0, z1);
@@ -690,6 +693,67 @@ __device__ __forceinline__ void tc_softmax(const AttnArgs& a, const Plan& plan, 
     }
 }
 
+// A piece's queries: rows as fp16 of a power of two times them, the largest in [1, 2), the sign of the softmax's scale with
+// them; and what their scores are multiplied by, into buffer `parity`.  Warp `warp` of `warps` takes its share.
+template <typename C>
+__device__ __forceinline__ void tc_rows(const AttnArgs& a, const TcWalk& w, int warp, int warps, uint32_t parity, uint32_t base, uint8_t* smem) {
+    constexpr int LANES = C::B <= 2 ? 8 : 16, ROWS = 32 / LANES, AT_ONCE = 4;
+    const int lane = threadIdx.x & 31, u = lane % LANES, rows = w.p_seq.n * a.shared;
+    const bool used = u < 4 * C::B;
+    const __nv_bfloat16* const q = static_cast<const __nv_bfloat16*>(a.q) + w.p_seq.q0 * a.q_stride + (int64_t)w.p_head * a.shared * C::DIM + 8 * u;
+    const float scale = fabsf(a.scale_log2), sign = a.scale_log2 < 0.0f ? -1.0f : 1.0f;
+    for (int r0 = warp * ROWS * AT_ONCE; r0 < TC_ROWS; r0 += warps * ROWS * AT_ONCE) {
+        Raw8<__nv_bfloat16> raw[AT_ONCE];
+#pragma unroll
+        for (int k = 0; k < AT_ONCE; ++k) {
+            const int row = min(w.p_tile * TC_ROWS + r0 + k * ROWS + lane / LANES, rows - 1), token = divided(row, a);
+            raw[k].w[0] = make_uint4(0, 0, 0, 0);
+            if (used) raw_load(q + token * a.q_stride + (row - token * a.shared) * C::DIM, a.align, raw[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < AT_ONCE; ++k) {
+            const int r = r0 + k * ROWS + lane / LANES;
+            Row8 x;
+            float v[8], top = 0.0f;
+            raw_get(raw[k], x);
+            x.get(v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[e]));
+#pragma unroll
+            for (int d = 1; d < LANES; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 100);
+            const float up = sign * two_to(-e);
+#pragma unroll
+            for (int n = 0; n < 8; ++n) v[n] *= up;
+            if (used)
+                sts128(base + C::Q + (r / TC_TILE) * C::Q_BYTES + (u / 8) * TC_TILE * 128 + (r % TC_TILE) * 128 + (((u & 7) ^ (r & 7)) << 4),
+                       half2_bits(v[0], v[4]), half2_bits(v[1], v[5]), half2_bits(v[2], v[6]), half2_bits(v[3], v[7]));
+            if (u == 0) *reinterpret_cast<float*>(smem + C::SCALE + (parity * TC_ROWS + r) * 4) = scale * two_to(e);
+        }
+    }
+    fence_async();
+    __syncwarp();
+}
+
+// The loaders: the next piece's queries, as soon as the last scores of this one are done.  The first piece's are the softmax
+// warps', who have nothing else to do yet.
+template <typename C>
+__device__ __forceinline__ void tc_queries(const AttnArgs& a, TcWalk w, const TcWaits& wait, uint32_t base, uint8_t* smem) {
+    const int warp = (threadIdx.x >> 5) - TC_ISSUER - 1;
+    uint32_t pieces = 0;
+    while (true) {
+        tc_next(a, w);
+        if (!w.valid) return;
+        if (w.g1 <= w.g0) continue;
+        if (pieces > 0) {
+            if (!wait(C::Q_FREE, (pieces - 1) & 1)) return;
+            tc_rows<C>(a, w, warp, TC_LOADERS, pieces & 1, base, smem);
+            if ((threadIdx.x & 31) == 0) wait.arrive(C::Q_FULL);
+        }
+        ++pieces;
+    }
+}
+
 template <typename C>
 __global__ void __launch_bounds__(TC_THREADS, 1) attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ Plan plan) {
     extern __shared__ __align__(128) uint8_t smem_raw[];
@@ -699,7 +763,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) attn_tc_kernel(const __grid_con
     const TcWaits wait{base, reinterpret_cast<volatile int*>(smem + C::STOP), a.limit_ns};
     if (tid < C::BARS)
         mbar_init(base + tid * 8, (tid >= C::K_FULL && tid < C::K_EMPTY) || (tid >= C::V_FULL && tid < C::V_EMPTY) ? TC_DECODERS
-                                  : (tid >= C::Q_FULL && tid < C::S_FULL) || (tid >= C::P_FULL && tid < C::O_DONE) ? 4 : 1);
+                                  : tid == C::Q_FIRST ? 8 : tid == C::Q_FULL ? TC_LOADERS : tid >= C::P_FULL && tid < C::O_DONE ? 4 : 1);
     if (tid == 0) *wait.stop = 0;
     fence_mbar_init();
     if (warp == TC_ISSUER) tmem_alloc(base + C::TMEM, 512);
@@ -719,7 +783,10 @@ __global__ void __launch_bounds__(TC_THREADS, 1) attn_tc_kernel(const __grid_con
         if (walk.left > 0) tc_decode<C>(a, walk, wait, base, smem);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(TC_OTHER_REGS));
-        if (warp == TC_ISSUER && walk.left > 0) tc_issue<C>(a, walk, wait, base, tmem);
+        if (walk.left > 0) {
+            if (warp == TC_ISSUER) tc_issue<C>(a, walk, wait, base, tmem);
+            else tc_queries<C>(a, walk, wait, base, smem);
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -727,44 +794,47 @@ __global__ void __launch_bounds__(TC_THREADS, 1) attn_tc_kernel(const __grid_con
     if (warp == TC_ISSUER) tmem_dealloc(tmem, 512);
 }
 
-// Joins the parts of the pieces that were cut: block (w, y) rows 8 y .. of the one that starts in worker w, a warp a row.
-constexpr int TC_JOIN_WARPS = 8;
+// Joins the parts of the pieces that were cut: block (w, y) 32 rows of the one that starts in worker w, a warp 4 of them.
+constexpr int TC_JOIN_WARPS = 8, TC_JOIN_ROWS = 32;
 
 template <typename C>
 __global__ void __launch_bounds__(TC_JOIN_WARPS * 32) join_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ Plan plan) {
     constexpr int VEC = C::DIM / 32;
     pdl_wait();
-    const int w = blockIdx.x, r = blockIdx.y * TC_JOIN_WARPS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int w = blockIdx.x, lane = threadIdx.x & 31;
     const Part* parts = plan.parts;
     const int of = mx_ld(&parts[2 * w + 1].of), to0 = mx_ld(&parts[2 * w + 1].to);
     if (of < 0 || to0 >= of) return;                       // no piece starts here, or none that goes on
     const Seq seq = seq_of<TC_ROWS>(a, mx_ld(&parts[2 * w + 1].seq), false);
-    const int row = mx_ld(&parts[2 * w + 1].tile) * TC_ROWS + r;
-    if (row >= seq.n * a.shared) return;
+    const int tile = mx_ld(&parts[2 * w + 1].tile), head = mx_ld(&parts[2 * w + 1].head);
     int n = 1;
     while (w + n < plan.workers && mx_ld(&parts[2 * (w + n)].of) >= 0 && mx_ld(&parts[2 * (w + n)].to) < of) ++n;
     n = min(n + 1, plan.workers - w);
     const auto rows_of = [&](int p) { return plan.rows + (p == 0 ? 2 * w + 1 : 2 * (w + p)) * (int64_t)(TC_ROWS * (C::DIM + 2)); };
-    float ref = -INFINITY;
-    for (int p = lane; p < n; p += 32) ref = larger(ref, mx_ld(rows_of(p) + TC_ROWS * C::DIM + 2 * r));
+    for (int k = threadIdx.x >> 5; k < TC_JOIN_ROWS; k += TC_JOIN_WARPS) {
+        const int r = blockIdx.y * TC_JOIN_ROWS + k, row = tile * TC_ROWS + r;
+        if (row >= seq.n * a.shared) return;
+        float ref = -INFINITY;
+        for (int p = lane; p < n; p += 32) ref = larger(ref, mx_ld(rows_of(p) + TC_ROWS * C::DIM + 2 * r));
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) ref = larger(ref, __shfl_xor_sync(0xffffffffu, ref, d));
-    float sum = 0.0f, v[VEC];
+        for (int d = 16; d > 0; d >>= 1) ref = larger(ref, __shfl_xor_sync(0xffffffffu, ref, d));
+        float sum = 0.0f, v[VEC];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) v[i] = 0.0f;
-    for (int p = 0; p < n; ++p) {
-        const float* rows = rows_of(p);
-        const float k = share_of(mx_ld(rows + TC_ROWS * C::DIM + 2 * r), ref);
-        sum = fmaf(k, mx_ld(rows + TC_ROWS * C::DIM + 2 * r + 1), sum);
+        for (int i = 0; i < VEC; ++i) v[i] = 0.0f;
+        for (int p = 0; p < n; ++p) {
+            const float* rows = rows_of(p);
+            const float s = share_of(mx_ld(rows + TC_ROWS * C::DIM + 2 * r), ref);
+            sum = fmaf(s, mx_ld(rows + TC_ROWS * C::DIM + 2 * r + 1), sum);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) v[i] = fmaf(k, mx_ld(rows + r * C::DIM + i * 32 + lane), v[i]);
+            for (int i = 0; i < VEC; ++i) v[i] = fmaf(s, mx_ld(rows + r * C::DIM + i * 32 + lane), v[i]);
+        }
+        const float inv = ref == -INFINITY ? 0.0f : 1.0f / sum;
+        const int64_t at = (int64_t)(seq.q0 + row / a.shared) * a.heads + head * a.shared + row % a.shared;
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.dst) + at * C::DIM;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) out[i * 32 + lane] = __float2bfloat16_rn(v[i] * inv);
+        if (lane == 0 && a.lse) a.lse[at] = ref == -INFINITY ? -INFINITY : (ref + log2f(sum)) * 0.69314718055994531f;
     }
-    const float inv = ref == -INFINITY ? 0.0f : 1.0f / sum;
-    const int64_t at = (int64_t)(seq.q0 + row / a.shared) * a.heads + mx_ld(&parts[2 * w + 1].head) * a.shared + row % a.shared;
-    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.dst) + at * C::DIM;
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) out[i * 32 + lane] = __float2bfloat16_rn(v[i] * inv);
-    if (lane == 0 && a.lse) a.lse[at] = ref == -INFINITY ? -INFINITY : (ref + log2f(sum)) * 0.69314718055994531f;
 }
 
 template <int B>
@@ -780,7 +850,7 @@ q4q_status tc_run(const AttnArgs& a, void* workspace, cudaStream_t stream, const
     plan.rows = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + mx_up((int64_t)sizeof(Part) * 2 * plan.workers, 256));
     const q4q_status st = launch(attn_tc_kernel<C>, dim3((unsigned)plan.workers), TC_THREADS, C::BYTES, stream, a, plan);
     if (st != Q4Q_OK) return st;
-    return launch(join_tc_kernel<C>, dim3((unsigned)plan.workers, TC_ROWS / TC_JOIN_WARPS), TC_JOIN_WARPS * 32, 0, stream, a, plan);
+    return launch(join_tc_kernel<C>, dim3((unsigned)plan.workers, TC_ROWS / TC_JOIN_ROWS), TC_JOIN_WARPS * 32, 0, stream, a, plan);
 }
 
 }  // namespace
