@@ -34,7 +34,7 @@ constexpr int TC_ISSUER = 8 + TC_DECODERS;
 constexpr int TC_LOADERS = 3;
 constexpr int TC_THREADS = (TC_ISSUER + 1 + TC_LOADERS) * 32;
 // Registers a thread: at launch, and as the warpgroups share them out, in all the same number.
-constexpr int TC_REGS = 96, TC_SOFTMAX_REGS = 136, TC_DECODE_REGS = 80, TC_OTHER_REGS = 48;
+constexpr int TC_REGS = 96, TC_SOFTMAX_REGS = 128, TC_DECODE_REGS = 80, TC_OTHER_REGS = 64;
 static_assert(256 * TC_SOFTMAX_REGS + 256 * TC_DECODE_REGS + 128 * TC_OTHER_REGS <= TC_THREADS * TC_REGS, "registers of the launch");
 constexpr int TC_SNAP = 3;               // steps that a share may be longer or shorter, so that it ends with a piece
 constexpr int TC_INFOS = 4;              // steps whose notes are kept: decoders are at most 2 ahead of the softmax
@@ -73,11 +73,45 @@ __device__ __forceinline__ int tc_cost(const AttnArgs& a, const Seq& s, int tile
     return max(1, c1 - c0);
 }
 
-__device__ __forceinline__ int64_t tc_head_cost(const AttnArgs& a, const Seq& s) {
+// Steps of all tiles of a head.  team 1: this thread alone; 32: the lanes of the warp together.
+__device__ __forceinline__ int64_t tc_head_cost(const AttnArgs& a, const Seq& s, int team) {
     int64_t sum = 0;
     int c0, c1;
-    for (int t = 0; t < s.tiles; ++t) sum += tc_cost(a, s, t, c0, c1);
+    for (int t = (threadIdx.x & 31) % team; t < s.tiles; t += team) sum += tc_cost(a, s, t, c0, c1);
+    if (team > 1)
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
     return sum;
+}
+
+// The tile that step `rel` of a head lies in, its steps; rel from its start.
+__device__ __forceinline__ int tc_tile_of(const AttnArgs& a, const Seq& s, int64_t& rel, int& cost, int team) {
+    int c0, c1;
+    if (team == 1) {
+        for (int tile = 0;; ++tile) {
+            cost = tc_cost(a, s, tile, c0, c1);
+            if (rel < cost || tile + 1 >= s.tiles) return tile;
+            rel -= cost;
+        }
+    }
+    const int lane = threadIdx.x & 31;
+    for (int t0 = 0;; t0 += 32) {
+        const int mine = t0 + lane < s.tiles ? tc_cost(a, s, t0 + lane, c0, c1) : 0;
+        int inc = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, inc, d);
+            if (lane >= d) inc += o;
+        }
+        const uint32_t behind = __ballot_sync(0xffffffffu, inc > rel);
+        if (behind || t0 + 32 >= s.tiles) {
+            const int at = behind ? __ffs(behind) - 1 : min(31, s.tiles - 1 - t0);
+            cost = __shfl_sync(0xffffffffu, mine, at);
+            rel -= __shfl_sync(0xffffffffu, inc, at) - cost;
+            return t0 + at;
+        }
+        rel -= __shfl_sync(0xffffffffu, inc, 31);
+    }
 }
 
 // A walk over a worker's steps: pieces, one after another.
@@ -131,19 +165,22 @@ __device__ __forceinline__ void tc_next(const AttnArgs& a, TcWalk& w) {
     }
 }
 
-// This worker's share of all steps: its walk.  words: TC_THREADS / 32 + 7 words of shared memory.
+// This worker's share of all steps: its walk.  Few sequences: each warp takes a run of them, its lanes their tiles; many: each
+// thread a run.  words: TC_THREADS / 32 + 7 words of shared memory.
 __device__ __forceinline__ TcWalk tc_share(const AttnArgs& a, const Plan& plan, int64_t* words) {
     constexpr int WARPS = TC_THREADS / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (a.n_seqs + TC_THREADS - 1) / TC_THREADS, s0 = min(tid * per, a.n_seqs), s1 = min(s0 + per, a.n_seqs);
+    const int team = a.n_seqs <= 8 * WARPS ? 32 : 1, runs = TC_THREADS / team, run = tid / team;
+    const int per = (a.n_seqs + runs - 1) / runs, s0 = min(run * per, a.n_seqs), s1 = min(s0 + per, a.n_seqs);
     int64_t sum = 0;
-    for (int s = s0; s < s1; ++s) sum += a.kv_heads * tc_head_cost(a, seq_of<TC_ROWS>(a, s, false));
+    for (int s = s0; s < s1; ++s) sum += a.kv_heads * tc_head_cost(a, seq_of<TC_ROWS>(a, s, false), team);
     int64_t inc = sum;
+    if (team == 1)
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int64_t o = __shfl_up_sync(0xffffffffu, inc, d);
-        if (lane >= d) inc += o;
-    }
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t o = __shfl_up_sync(0xffffffffu, inc, d);
+            if (lane >= d) inc += o;
+        }
     if (lane == 31) words[warp] = inc;
     __syncthreads();
     int64_t before = inc - sum, total = 0;
@@ -161,10 +198,10 @@ __device__ __forceinline__ TcWalk tc_share(const AttnArgs& a, const Plan& plan, 
         const int64_t u = works ? (total * (blockIdx.x + k) + workers - 1) / workers : total;
         if (u >= total && tid == 0) words[WARPS + 1 + k] = total;
         if (u < total && before <= u && u < before + sum) {
-            int s = s0;
+            int s = s0, cost;
             int64_t head_cost, base = before;
             while (true) {
-                head_cost = tc_head_cost(a, seq_of<TC_ROWS>(a, s, false));
+                head_cost = tc_head_cost(a, seq_of<TC_ROWS>(a, s, false), team);
                 if (u < base + head_cost * a.kv_heads) break;
                 base += head_cost * a.kv_heads;
                 ++s;
@@ -173,12 +210,7 @@ __device__ __forceinline__ TcWalk tc_share(const AttnArgs& a, const Plan& plan, 
             int64_t rel = u - base;
             const int64_t head = rel / head_cost;
             rel -= head * head_cost;
-            int tile = 0, c0, c1, cost;
-            for (;; ++tile) {
-                cost = tc_cost(a, seq, tile, c0, c1);
-                if (rel < cost || tile + 1 >= seq.tiles) break;
-                rel -= cost;
-            }
+            const int tile = tc_tile_of(a, seq, rel, cost, team);
             // to the piece's end, which the walk finds by itself, or to its start
             const int64_t move = cost - rel <= snap ? cost - rel : rel <= snap ? -rel : 0;
             words[WARPS + 1 + k] = u + move;
@@ -513,8 +545,8 @@ __device__ __forceinline__ void tmem_ld_done(uint32_t (&r)[32]) {
                    "+r"(r[31])::"memory");
 }
 
-template <typename C>
-__device__ __forceinline__ void tc_rows(const AttnArgs& a, const TcWalk& w, int warp, int warps, uint32_t parity, uint32_t base, uint8_t* smem);
+template <typename C, typename F>
+__device__ __forceinline__ void tc_rows(const AttnArgs& a, const TcWalk& w, int warp, int warps, uint32_t parity, uint32_t base, uint8_t* smem, F ready);
 
 // The softmax of tile i, a thread a row: queries, weights, and at a piece's end the results.
 template <typename C>
@@ -544,7 +576,7 @@ __device__ __forceinline__ void tc_softmax(const AttnArgs& a, const Plan& plan, 
                 if ((odd >> (k / 16 * 8)) & 1) poison |= *reinterpret_cast<volatile uint8_t*>(smem + C::WHICH + (step % TC_INFOS) * TC_TILE + k);
         };
         if (n > 0 && pieces == 0) {
-            tc_rows<C>(a, w, warp, 8, 0, base, smem);
+            tc_rows<C>(a, w, warp, 8, 0, base, smem, [] {});
             if (lane == 0) wait.arrive(C::Q_FIRST);
         }
         for (int j = 0; j < n; ++j, ++steps) {
@@ -694,22 +726,31 @@ __device__ __forceinline__ void tc_softmax(const AttnArgs& a, const Plan& plan, 
 }
 
 // A piece's queries: rows as fp16 of a power of two times them, the largest in [1, 2), the sign of the softmax's scale with
-// them; and what their scores are multiplied by, into buffer `parity`.  Warp `warp` of `warps` takes its share.
-template <typename C>
-__device__ __forceinline__ void tc_rows(const AttnArgs& a, const TcWalk& w, int warp, int warps, uint32_t parity, uint32_t base, uint8_t* smem) {
+// them; and what their scores are multiplied by, into buffer `parity`.  Warp `warp` of `warps` takes its share; ready() is called before
+// anything is stored.
+template <typename C, typename F>
+__device__ __forceinline__ void tc_rows(const AttnArgs& a, const TcWalk& w, int warp, int warps, uint32_t parity, uint32_t base, uint8_t* smem, F ready) {
     constexpr int LANES = C::B <= 2 ? 8 : 16, ROWS = 32 / LANES, AT_ONCE = 4;
     const int lane = threadIdx.x & 31, u = lane % LANES, rows = w.p_seq.n * a.shared;
     const bool used = u < 4 * C::B;
     const __nv_bfloat16* const q = static_cast<const __nv_bfloat16*>(a.q) + w.p_seq.q0 * a.q_stride + (int64_t)w.p_head * a.shared * C::DIM + 8 * u;
     const float scale = fabsf(a.scale_log2), sign = a.scale_log2 < 0.0f ? -1.0f : 1.0f;
-    for (int r0 = warp * ROWS * AT_ONCE; r0 < TC_ROWS; r0 += warps * ROWS * AT_ONCE) {
-        Raw8<__nv_bfloat16> raw[AT_ONCE];
+    Raw8<__nv_bfloat16> next[AT_ONCE];
+    const auto load = [&](int r0) {
 #pragma unroll
         for (int k = 0; k < AT_ONCE; ++k) {
             const int row = min(w.p_tile * TC_ROWS + r0 + k * ROWS + lane / LANES, rows - 1), token = divided(row, a);
-            raw[k].w[0] = make_uint4(0, 0, 0, 0);
-            if (used) raw_load(q + token * a.q_stride + (row - token * a.shared) * C::DIM, a.align, raw[k]);
+            next[k].w[0] = make_uint4(0, 0, 0, 0);
+            if (used) raw_load(q + token * a.q_stride + (row - token * a.shared) * C::DIM, a.align, next[k]);
         }
+    };
+    if (warp * ROWS * AT_ONCE < TC_ROWS) load(warp * ROWS * AT_ONCE);
+    ready();
+    for (int r0 = warp * ROWS * AT_ONCE; r0 < TC_ROWS; r0 += warps * ROWS * AT_ONCE) {
+        Raw8<__nv_bfloat16> raw[AT_ONCE];
+#pragma unroll
+        for (int k = 0; k < AT_ONCE; ++k) raw[k] = next[k];
+        if (r0 + warps * ROWS * AT_ONCE < TC_ROWS) load(r0 + warps * ROWS * AT_ONCE);
 #pragma unroll
         for (int k = 0; k < AT_ONCE; ++k) {
             const int r = r0 + k * ROWS + lane / LANES;
@@ -746,8 +787,9 @@ __device__ __forceinline__ void tc_queries(const AttnArgs& a, TcWalk w, const Tc
         if (!w.valid) return;
         if (w.g1 <= w.g0) continue;
         if (pieces > 0) {
-            if (!wait(C::Q_FREE, (pieces - 1) & 1)) return;
-            tc_rows<C>(a, w, warp, TC_LOADERS, pieces & 1, base, smem);
+            bool ok = true;
+            tc_rows<C>(a, w, warp, TC_LOADERS, pieces & 1, base, smem, [&] { ok = wait(C::Q_FREE, (pieces - 1) & 1); });
+            if (!ok) return;
             if ((threadIdx.x & 31) == 0) wait.arrive(C::Q_FULL);
         }
         ++pieces;
@@ -794,47 +836,65 @@ __global__ void __launch_bounds__(TC_THREADS, 1) attn_tc_kernel(const __grid_con
     if (warp == TC_ISSUER) tmem_dealloc(tmem, 512);
 }
 
-// Joins the parts of the pieces that were cut: block (w, y) 32 rows of the one that starts in worker w, a warp 4 of them.
-constexpr int TC_JOIN_WARPS = 8, TC_JOIN_ROWS = 32;
+// Joins the parts of the pieces that were cut: block (w, y) 8 rows of the one that starts in worker w, a warp a row, 4 parts in
+// flight at a time.
+constexpr int TC_JOIN_WARPS = 8;
 
 template <typename C>
 __global__ void __launch_bounds__(TC_JOIN_WARPS * 32) join_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ Plan plan) {
-    constexpr int VEC = C::DIM / 32;
+    constexpr int VEC = C::DIM / 32, AT_ONCE = 4;
     pdl_wait();
-    const int w = blockIdx.x, lane = threadIdx.x & 31;
+    const int w = blockIdx.x, lane = threadIdx.x & 31, r = blockIdx.y * TC_JOIN_WARPS + (threadIdx.x >> 5);
     const Part* parts = plan.parts;
     const int of = mx_ld(&parts[2 * w + 1].of), to0 = mx_ld(&parts[2 * w + 1].to);
     if (of < 0 || to0 >= of) return;                       // no piece starts here, or none that goes on
-    const Seq seq = seq_of<TC_ROWS>(a, mx_ld(&parts[2 * w + 1].seq), false);
-    const int tile = mx_ld(&parts[2 * w + 1].tile), head = mx_ld(&parts[2 * w + 1].head);
+    const int s = mx_ld(&parts[2 * w + 1].seq), tile = mx_ld(&parts[2 * w + 1].tile), head = mx_ld(&parts[2 * w + 1].head);
+    // the workers behind: whose first part ends the piece
     int n = 1;
-    while (w + n < plan.workers && mx_ld(&parts[2 * (w + n)].of) >= 0 && mx_ld(&parts[2 * (w + n)].to) < of) ++n;
-    n = min(n + 1, plan.workers - w);
-    const auto rows_of = [&](int p) { return plan.rows + (p == 0 ? 2 * w + 1 : 2 * (w + p)) * (int64_t)(TC_ROWS * (C::DIM + 2)); };
-    for (int k = threadIdx.x >> 5; k < TC_JOIN_ROWS; k += TC_JOIN_WARPS) {
-        const int r = blockIdx.y * TC_JOIN_ROWS + k, row = tile * TC_ROWS + r;
-        if (row >= seq.n * a.shared) return;
-        float ref = -INFINITY;
-        for (int p = lane; p < n; p += 32) ref = larger(ref, mx_ld(rows_of(p) + TC_ROWS * C::DIM + 2 * r));
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) ref = larger(ref, __shfl_xor_sync(0xffffffffu, ref, d));
-        float sum = 0.0f, v[VEC];
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) v[i] = 0.0f;
-        for (int p = 0; p < n; ++p) {
-            const float* rows = rows_of(p);
-            const float s = share_of(mx_ld(rows + TC_ROWS * C::DIM + 2 * r), ref);
-            sum = fmaf(s, mx_ld(rows + TC_ROWS * C::DIM + 2 * r + 1), sum);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) v[i] = fmaf(s, mx_ld(rows + r * C::DIM + i * 32 + lane), v[i]);
-        }
-        const float inv = ref == -INFINITY ? 0.0f : 1.0f / sum;
-        const int64_t at = (int64_t)(seq.q0 + row / a.shared) * a.heads + head * a.shared + row % a.shared;
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.dst) + at * C::DIM;
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) out[i * 32 + lane] = __float2bfloat16_rn(v[i] * inv);
-        if (lane == 0 && a.lse) a.lse[at] = ref == -INFINITY ? -INFINITY : (ref + log2f(sum)) * 0.69314718055994531f;
+    for (bool more = true; more; n += 32) {
+        const int v = w + n + lane;
+        const bool goes_on = v < plan.workers && mx_ld(&parts[2 * v].of) >= 0 && mx_ld(&parts[2 * v].to) < of;
+        const uint32_t ends = __ballot_sync(0xffffffffu, !goes_on);
+        more = !ends;
+        if (ends) n += __ffs(ends) - 32;
     }
+    n = min(n, plan.workers - w);
+    const Seq seq = seq_of<TC_ROWS>(a, s, false);
+    const int row = tile * TC_ROWS + r;
+    if (row >= seq.n * a.shared) return;
+    const auto rows_of = [&](int p) { return plan.rows + (p == 0 ? 2 * w + 1 : 2 * (w + p)) * (int64_t)(TC_ROWS * (C::DIM + 2)); };
+    float ref = -INFINITY;
+    for (int p = lane; p < n; p += 32) ref = larger(ref, mx_ld(rows_of(p) + TC_ROWS * C::DIM + 2 * r));
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) ref = larger(ref, __shfl_xor_sync(0xffffffffu, ref, d));
+    float sum = 0.0f, v[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[i] = 0.0f;
+    for (int p0 = 0; p0 < n; p0 += AT_ONCE) {
+        float k[AT_ONCE], l[AT_ONCE], x[AT_ONCE][VEC];
+#pragma unroll
+        for (int q = 0; q < AT_ONCE; ++q) {
+            const float* rows = rows_of(min(p0 + q, n - 1));
+            k[q] = mx_ld(rows + TC_ROWS * C::DIM + 2 * r);
+            l[q] = mx_ld(rows + TC_ROWS * C::DIM + 2 * r + 1);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) x[q][i] = mx_ld(rows + r * C::DIM + i * 32 + lane);
+        }
+#pragma unroll
+        for (int q = 0; q < AT_ONCE; ++q) {
+            if (p0 + q >= n) break;
+            const float share = share_of(k[q], ref);
+            sum = fmaf(share, l[q], sum);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) v[i] = fmaf(share, x[q][i], v[i]);
+        }
+    }
+    const float inv = ref == -INFINITY ? 0.0f : 1.0f / sum;
+    const int64_t at = (int64_t)(seq.q0 + row / a.shared) * a.heads + head * a.shared + row % a.shared;
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.dst) + at * C::DIM;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) out[i * 32 + lane] = __float2bfloat16_rn(v[i] * inv);
+    if (lane == 0 && a.lse) a.lse[at] = ref == -INFINITY ? -INFINITY : (ref + log2f(sum)) * 0.69314718055994531f;
 }
 
 template <int B>
@@ -850,7 +910,7 @@ q4q_status tc_run(const AttnArgs& a, void* workspace, cudaStream_t stream, const
     plan.rows = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + mx_up((int64_t)sizeof(Part) * 2 * plan.workers, 256));
     const q4q_status st = launch(attn_tc_kernel<C>, dim3((unsigned)plan.workers), TC_THREADS, C::BYTES, stream, a, plan);
     if (st != Q4Q_OK) return st;
-    return launch(join_tc_kernel<C>, dim3((unsigned)plan.workers, TC_ROWS / TC_JOIN_ROWS), TC_JOIN_WARPS * 32, 0, stream, a, plan);
+    return launch(join_tc_kernel<C>, dim3((unsigned)plan.workers, TC_ROWS / TC_JOIN_WARPS), TC_JOIN_WARPS * 32, 0, stream, a, plan);
 }
 
 }  // namespace
