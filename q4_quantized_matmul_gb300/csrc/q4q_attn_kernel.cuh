@@ -783,50 +783,67 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_kernel(const __grid_
 // Joins the parts of the segments that were cut.  A segment's parts are a worker's last one (its
 // start) and the first ones of the workers behind it; block (w, r) joins row r of the one that starts
 // in worker w.
-constexpr int JOIN_WARPS = 4;
+constexpr int JOIN_WARPS = 8, JOIN_AT_ONCE = 4;   // a warp takes every 8th part, 4 of them in flight
 
 template <typename C>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) join_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ Plan plan) {
     constexpr int VEC = C::DIM / 32;
     __shared__ float sums[JOIN_WARPS][C::DIM];
-    __shared__ float2 stats[JOIN_WARPS];
+    __shared__ float shares[JOIN_WARPS];
     pdl_wait();
     const int w = blockIdx.x, r = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const Part* parts = plan.parts;
     const int of = mx_ld(&parts[2 * w + 1].of), to0 = mx_ld(&parts[2 * w + 1].to);
     if (of < 0 || to0 >= of) return;                       // no segment starts here, or none that goes on
     const int s = mx_ld(&parts[2 * w + 1].seq), head = mx_ld(&parts[2 * w + 1].head), tile = mx_ld(&parts[2 * w + 1].tile);
+    // the workers behind: whose first part ends the segment
+    int n = 1;
+    for (bool more = true; more; n += 32) {
+        const int v = w + n + lane;
+        const bool goes_on = v < plan.workers && mx_ld(&parts[2 * v].of) >= 0 && mx_ld(&parts[2 * v].to) < of;
+        const uint32_t ends = __ballot_sync(0xffffffffu, !goes_on);
+        more = !ends;
+        if (ends) n += __ffs(ends) - 32;
+    }
+    n = min(n, plan.workers - w);
     const Seq seq = seq_of<C::ROWS>(a, s, plan.whole);
     const int row = tile * C::ROWS + r;
     if (row >= seq.n * a.shared) return;
-    // parts until the segment's end
-    int n = 1;
-    while (w + n < plan.workers && mx_ld(&parts[2 * (w + n)].of) >= 0 && mx_ld(&parts[2 * (w + n)].to) < of) ++n;
-    n = min(n + 1, plan.workers - w);
-    float ref = -INFINITY, sum = 0.0f, v[VEC];
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) v[i] = 0.0f;
+    const auto rows_of = [&](int p) { return plan.rows + (p == 0 ? 2 * w + 1 : 2 * (w + p)) * (int64_t)(C::ROWS * (C::DIM + 2)); };
     // the largest reference first: all of them in flight together
-    for (int p = lane; p < n; p += 32) {
-        const float* rows = plan.rows + (p == 0 ? 2 * w + 1 : 2 * (w + p)) * (int64_t)(C::ROWS * (C::DIM + 2));
-        ref = larger(ref, mx_ld(rows + C::ROWS * C::DIM + 2 * r));
-    }
+    float ref = -INFINITY;
+    for (int p = lane; p < n; p += 32) ref = larger(ref, mx_ld(rows_of(p) + C::ROWS * C::DIM + 2 * r));
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) ref = larger(ref, __shfl_xor_sync(0xffffffffu, ref, d));
-    for (int p = warp; p < n; p += JOIN_WARPS) {
-        const float* rows = plan.rows + (p == 0 ? 2 * w + 1 : 2 * (w + p)) * (int64_t)(C::ROWS * (C::DIM + 2));
-        const float k = share_of(mx_ld(rows + C::ROWS * C::DIM + 2 * r), ref);
-        sum = fmaf(k, mx_ld(rows + C::ROWS * C::DIM + 2 * r + 1), sum);
+    float sum = 0.0f, v[VEC];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) v[i] = fmaf(k, mx_ld(rows + r * C::DIM + i * 32 + lane), v[i]);
+    for (int i = 0; i < VEC; ++i) v[i] = 0.0f;
+    for (int p0 = warp; p0 < n; p0 += JOIN_WARPS * JOIN_AT_ONCE) {
+        float k[JOIN_AT_ONCE], l[JOIN_AT_ONCE], x[JOIN_AT_ONCE][VEC];
+#pragma unroll
+        for (int q = 0; q < JOIN_AT_ONCE; ++q) {
+            const float* rows = rows_of(min(p0 + q * JOIN_WARPS, n - 1));
+            k[q] = mx_ld(rows + C::ROWS * C::DIM + 2 * r);
+            l[q] = mx_ld(rows + C::ROWS * C::DIM + 2 * r + 1);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) x[q][i] = mx_ld(rows + r * C::DIM + i * 32 + lane);
+        }
+#pragma unroll
+        for (int q = 0; q < JOIN_AT_ONCE; ++q) {
+            if (p0 + q * JOIN_WARPS >= n) break;
+            const float share = share_of(k[q], ref);
+            sum = fmaf(share, l[q], sum);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) v[i] = fmaf(share, x[q][i], v[i]);
+        }
     }
 #pragma unroll
     for (int i = 0; i < VEC; ++i) sums[warp][i * 32 + lane] = v[i];
-    if (lane == 0) stats[warp] = make_float2(ref, sum);
+    if (lane == 0) shares[warp] = sum;
     __syncthreads();
     sum = 0.0f;
 #pragma unroll
-    for (int x = 0; x < JOIN_WARPS; ++x) sum += stats[x].y;
+    for (int x = 0; x < JOIN_WARPS; ++x) sum += shares[x];
     const float inv = ref == -INFINITY ? 0.0f : 1.0f / sum;
     const int64_t at = (int64_t)(seq.q0 + row / a.shared) * a.heads + head * a.shared + row % a.shared;
     for (int c = threadIdx.x * 4; c < C::DIM; c += JOIN_WARPS * 128) {
