@@ -40,12 +40,20 @@ struct KvArgs {
 
 constexpr float KV_MAX = 65504.0f;
 
-// The word of a lane's 8 codes (element e at bit 4 e), all 32 lanes together: what pack_q4_word of q4q_common.cuh gives, by the
-// same argument (t = x rcp(d) rounds as the IEEE quotient does, but within 5e-5 of a half-integer), in two-lane instructions:
-// 45 of them instead of 150.  t is stopped at 7 before it is rounded; adding 1.5 2^23 + 8 rounds and leaves code + 8 in the low
-// bits, and the constant above them leaves with one subtraction from the sum of all 8, each at its place.
-__device__ __forceinline__ uint32_t code_word(const float (&v)[8], float d) {
-    const float inv = recip_approx(d);
+// The word of a lane's 8 codes (element e at bit 4 e), all 32 lanes together: what pack_q4_word of q4q_common.cuh gives, in
+// two-lane instructions, about 45 of them.  t = x rcp(d) is stopped at 7 and rounded by adding 1.5 2^23 + 8, which leaves
+// code + 8 in the low bits; the constant above them leaves with one subtraction from the sum of all 8, each at its place.
+//
+// `raw`: the values are of a 16-bit type (or +-65504).  Their quotients hit half-integers often, and 8 bf16 rows out of 10 would
+// take the divisions below.  But x and amax have 11-bit mantissas, so a quotient that is no half-integer h is at least h / 2^15 away
+// from one: with the reciprocal made 2^-20 larger (its error and the product's are 2^-22), ties, and they alone, come out
+// just beyond it, where rounding to nearest takes them away from zero, as the code is defined.  (8192 tokens of 8 heads of
+// 128, keys and values: 31 us with the divisions, 16 without.)
+// Otherwise, as there: t rounds as the IEEE quotient does, but within 5e-5 of a half-integer, where that is computed.
+__device__ __forceinline__ uint32_t code_word(const float (&v)[8], float d, bool raw) {
+    float inv = recip_approx(d);
+    const bool sure = raw && __all_sync(0xffffffffu, inv < 1e38f);           // d = 0 and subnormal d take the other way
+    if (sure) inv = fmaf(inv, 9.5367431640625e-7f, inv);
     constexpr float MAGIC = 12582920.0f;                   // 0x4B400008
     uint32_t w = 0;
     float far = 0.0f;
@@ -63,7 +71,7 @@ __device__ __forceinline__ uint32_t code_word(const float (&v)[8], float d) {
         w = (w * 16 + __float_as_uint(r1)) * 16 + __float_as_uint(r0);
     }
     w -= 0x4B400000u * 0x11111111u;
-    const bool near = !(far <= NEAR_LIMIT);
+    const bool near = !sure && !(far <= NEAR_LIMIT);
     if (__any_sync(0xffffffffu, near)) {
         if (near) {
             w = 0;
@@ -75,7 +83,7 @@ __device__ __forceinline__ uint32_t code_word(const float (&v)[8], float d) {
 }
 
 // A lane's 8 values of a block of 32 (4 lanes): the word of codes, and in d_bits the block's scale.
-__device__ __forceinline__ uint32_t encode_block(const Row8& x, uint16_t& d_bits) {
+__device__ __forceinline__ uint32_t encode_block(const Row8& x, bool raw, uint16_t& d_bits) {
     float v[8], m = 0.0f;
     x.get(v);
 #pragma unroll
@@ -91,7 +99,7 @@ __device__ __forceinline__ uint32_t encode_block(const Row8& x, uint16_t& d_bits
         }
     }
     const float d = scale_q4(m);
-    const uint32_t word = code_word(v, d);
+    const uint32_t word = code_word(v, d, raw);
     d_bits = finite ? fp16_bits(d) : 0x7fffu;
     return word;
 }
@@ -185,7 +193,7 @@ __global__ void __launch_bounds__(THREADS, 2) append_kernel(const __grid_constan
             for (int i = 0; i < SLOTS; ++i) {
                 if (turns) turn(v[i], turning, a.halves);
                 uint16_t d;
-                const uint32_t word = encode_block(v[i], d);
+                const uint32_t word = encode_block(v[i], sizeof(T) == 2 && !norm && !turns, d);
                 const int head = row + i * ROWS;
                 if (head < a.heads && used) {
                     uint8_t* chunk = a.cache + kv_chunk_offset(page, head, group, a.heads, a.page_log, a.dim);
