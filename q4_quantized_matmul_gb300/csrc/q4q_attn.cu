@@ -1,5 +1,6 @@
 // q4q_attn.cu -- host side of the attention over the paged 4-bit cache: argument checks and the choice
 // of the kernel (q4q_attn_kernel.cuh).
+#include <algorithm>
 #include <initializer_list>
 
 #include "q4q_attn.cuh"
@@ -8,18 +9,23 @@
 namespace q4q {
 namespace {
 
-// The tcgen05 kernel takes bf16 rows where a sequence has enough of them for a key-value head, on average, to fill its
-// tiles of 128.
-bool on_tensor_cores(int type, int64_t head_dim, int64_t n_q, int shared, int64_t n_seqs) {
-    return type == Q4Q_TYPE_BF16 && head_dim <= 128 && n_q * shared >= n_seqs * 128;
+// The tcgen05 kernel may take bf16 rows where a sequence has 64 of them or more for a key-value head, on average, and does where
+// its longer start pays: from 1024 keys on (the table's pages bound them), or from 256 rows, a CTA's tiles.  us, warp-level
+// MMAs / tcgen05, heads 32/8 of 128: 16 x 64 rows over 2048 keys 84 / 64, 128 rows over 8192 39 / 33, 64 rows over 8192 28 / 32, 256
+// rows over 8192 63 / 36; 8 x 400 rows over 100 keys 70 / 52, 2 x 128 rows over 300 22 / 36.
+bool may_use_tensor_cores(int type, int64_t head_dim, int64_t n_q, int shared, int64_t n_seqs) {
+    return type == Q4Q_TYPE_BF16 && head_dim <= 128 && n_q * shared >= n_seqs * 64;
+}
+bool on_tensor_cores(const AttnArgs& a, int64_t head_dim) {
+    return may_use_tensor_cores(a.type, head_dim, a.n_q, a.shared, a.n_seqs) && ((a.max_pages << a.page_log) >= 1024 || a.n_q * a.shared >= a.n_seqs * 256ll);
 }
 
 size_t workspace_bytes(int type, int64_t head_dim, int64_t n_q, int shared, int64_t n_seqs, const DeviceInfo& info) {
-    if (on_tensor_cores(type, head_dim, n_q, shared, n_seqs)) return attn_tc_workspace(head_dim, info);
+    const size_t most = may_use_tensor_cores(type, head_dim, n_q, shared, n_seqs) ? attn_tc_workspace(head_dim, info) : 0;
     switch (head_dim) {
-        case 64: return attn_workspace_64(info);
-        case 96: return attn_workspace_96(info);
-        case 128: return attn_workspace_128(info);
+        case 64: return std::max(most, attn_workspace_64(info));
+        case 96: return std::max(most, attn_workspace_96(info));
+        case 128: return std::max(most, attn_workspace_128(info));
         default: return attn_workspace_256(info);
     }
 }
@@ -67,7 +73,7 @@ q4q_status check(AttnArgs& a, const void* q, int64_t q_stride, int type, int64_t
     }
     a.type = type;
     a.causal = causal != 0;
-    a.align = aligned(q, 16) && aligned(dst, 16) && q_stride * size % 16 == 0 ? 16 : 1;
+    a.align = aligned(q, 32) && aligned(dst, 32) && q_stride * size % 32 == 0 ? 32 : aligned(q, 16) && aligned(dst, 16) && q_stride * size % 16 == 0 ? 16 : 1;
     a.scale_log2 = (float)((double)scale * 1.4426950408889634);
     a.dst = dst;
     a.lse = lse;
@@ -81,7 +87,7 @@ q4q_status check(AttnArgs& a, const void* q, int64_t q_stride, int type, int64_t
 bool wide(const AttnArgs& a) { return a.n_q * a.shared > (int64_t)a.n_seqs * (a.type == Q4Q_TYPE_BF16 ? 8 : 4); }
 
 q4q_status dispatch(const AttnArgs& a, int64_t head_dim, void* workspace, cudaStream_t stream, const DeviceInfo& info) {
-    if (on_tensor_cores(a.type, head_dim, a.n_q, a.shared, a.n_seqs)) return attn_tc_run(a, head_dim, workspace, stream, info);
+    if (on_tensor_cores(a, head_dim)) return attn_tc_run(a, head_dim, workspace, stream, info);
     switch (head_dim) {
         case 64: return attn_run_64(a, wide(a), workspace, stream, info);
         case 96: return attn_run_96(a, wide(a), workspace, stream, info);

@@ -21,7 +21,7 @@ struct AttnArgs {
     int64_t n_q, n_pages, max_pages, window;
     int n_seqs, heads, kv_heads, shared;       // shared: query heads of a key-value head
     uint32_t shared_m, shared_s;               // division by it (MxDivisor), from 2 on
-    int type, page_log, causal, align;         // align: of every row of q and dst, 16 or 1
+    int type, page_log, causal, align;         // align: of every row of q and dst, 32, 16 or 1
     float scale_log2;                          // scale * log2(e)
     void* dst;
     float* lse;

@@ -212,7 +212,7 @@ __device__ __forceinline__ TcWalk tc_share(const AttnArgs& a, const Plan& plan, 
             rel -= head * head_cost;
             const int tile = tc_tile_of(a, seq, rel, cost, team);
             // to the piece's end, which the walk finds by itself, or to its start
-            const int64_t move = cost - rel <= snap ? cost - rel : rel <= snap ? -rel : 0;
+            const int64_t move = rel == 0 ? 0 : cost - rel <= snap ? cost - rel : rel <= snap ? -rel : 0;
             words[WARPS + 1 + k] = u + move;
             if (k == 0) {
                 words[WARPS + 3] = s;
@@ -702,17 +702,34 @@ __device__ __forceinline__ void tc_softmax(const AttnArgs& a, const Plan& plan, 
                 const float o = n > 0 && !none ? __uint_as_float(x[k]) * inv : 0.0f;
                 v[4 * (k % 8) + k / 8] = (poison >> b) & 1 ? NAN : o;
             }
+            // whole sectors: a thread writes a row of its own
             if (there && complete) {
 #pragma unroll
-                for (int k = 0; k < 32; k += 8) {
-                    Row8 y;
+                for (int k = 0; k < 32; k += 16) {
+                    uint32_t h[8];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) y.p[q] = pack2(v[k + 2 * q], v[k + 2 * q + 1]);
-                    row_store(out + 32 * b + k, a.align, y);
+                    for (int q = 0; q < 8; ++q) {
+                        const __nv_bfloat162 y = __floats2bfloat162_rn(v[k + 2 * q], v[k + 2 * q + 1]);
+                        h[q] = *reinterpret_cast<const uint32_t*>(&y);
+                    }
+                    if (a.align >= 32) {
+                        mx_put<8>(reinterpret_cast<uint8_t*>(out + 32 * b + k), h);
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            reinterpret_cast<uint16_t*>(out + 32 * b + k)[2 * q] = (uint16_t)h[q];
+                            reinterpret_cast<uint16_t*>(out + 32 * b + k)[2 * q + 1] = (uint16_t)(h[q] >> 16);
+                        }
+                    }
                 }
             } else if (there) {
 #pragma unroll
-                for (int k = 0; k < 32; k += 4) *reinterpret_cast<float4*>(part_row + 32 * b + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+                for (int k = 0; k < 32; k += 8) {
+                    uint32_t h[8];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) h[q] = __float_as_uint(v[k + q]);
+                    mx_put<8>(reinterpret_cast<uint8_t*>(part_row + 32 * b + k), h);
+                }
             }
             __syncwarp();
         }

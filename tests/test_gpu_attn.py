@@ -80,7 +80,15 @@ class Case:
 
 
 def on_tensor_cores(case):
-    return case.type == "bf16" and case.dim <= 128 and case.q.shape[0] * (case.heads // case.kv_heads) >= 128 * len(case.len)
+    rows = case.q.shape[0] * (case.heads // case.kv_heads) / len(case.len)
+    return case.type == "bf16" and case.dim <= 128 and rows >= 64 and (case.pages.shape[1] * case.page >= 1024 or rows >= 256)
+
+
+def widened(case):
+    """The same, with a page table of 1024 tokens or more: few rows of prompts then take the tcgen05 kernel too."""
+    more = max(0, -(-1024 // case.page) - case.pages.shape[1])
+    case.pages = np.pad(case.pages, ((0, 0), (0, more)), constant_values=-1)
+    return case
 
 
 def bounds(case, size, span, o):
@@ -143,7 +151,7 @@ def test_ragged_rows_and_windows(q4q, type, lengths, rows, window):
 @pytest.mark.parametrize("window", [0, 100])
 def test_prompts(q4q, dim, heads, kv_heads, lengths, rows, window):
     """bf16 rows enough for the tcgen05 tiles: ragged last tiles of rows and keys, pieces cut between CTAs."""
-    case = Case([dim, heads, window], lengths, rows, heads, kv_heads, dim, 16 if dim == 96 else 64, "bf16")
+    case = widened(Case([dim, heads, window], lengths, rows, heads, kv_heads, dim, 16 if dim == 96 else 64, "bf16"))
     assert on_tensor_cores(case)
     got, lse = case.run(q4q, lse=True, window=window)
     check(case, got, lse, window=window)
@@ -151,9 +159,41 @@ def test_prompts(q4q, dim, heads, kv_heads, lengths, rows, window):
     assert torch.equal(got, case.run(q4q, window=window))
 
 
+@pytest.mark.parametrize("lengths,rows", [([2048, 1126], [2048, 1126]), ([5000, 300, 2100], [1500, 300, 2100]), ([700] * 24, [333] * 24)])
+@pytest.mark.parametrize("window", [0, 500])
+def test_prompts_of_many_pieces(q4q, lengths, rows, window):
+    """Every CTA has several pieces, some of a step, and shares that end with a piece near by: against the kernel of fp32 rows, which the
+    other tests hold to the reference.  The bound is the derivation's with the largest of each factor: 8 d <= amax (1 + 2^-10)."""
+    heads, kv_heads, dim, page = 32, 8, 64, 64
+    rng = np.random.default_rng(len(lengths))
+    g = torch.Generator(device="cuda").manual_seed(7)
+    need = [-(-n // page) for n in lengths]
+    order = torch.from_numpy(rng.permutation(sum(need)).astype(np.int32)).cuda()
+    pages = torch.full((len(need), max(need)), -1, dtype=torch.int32, device="cuda")
+    cache = torch.full((sum(need), q4q.q4q_kv_page_size(kv_heads, dim, page)), 0xFF, dtype=torch.uint8, device="cuda")
+    at, amax = 0, [0.0, 0.0]
+    for s, n in enumerate(lengths):
+        pages[s, : need[s]] = order[at: at + need[s]]
+        at += need[s]
+        k, v = (torch.randn(n, kv_heads, dim, generator=g, device="cuda") for _ in range(2))
+        j = torch.arange(n, device="cuda")
+        q4q.q4q_kv_append(cache, page, k, v, (pages[s].long()[j // page] * page + j % page).int())
+        amax = [max(amax[0], float(k.abs().max())), max(amax[1], float(v.abs().max()))]
+    first = torch.tensor([0] + rows, device="cuda").cumsum(0).int()
+    q = (0.5 * torch.randn(sum(rows), heads, dim, generator=g, device="cuda")).bfloat16()
+    args = (cache, page, kv_heads, pages, torch.tensor(lengths, dtype=torch.int32, device="cuda"))
+    want = q4q.q4q_kv_attn(q.float(), *args, first=first, window=window)
+    got = q4q.q4q_kv_attn(q, *args, first=first, window=window, dst=torch.full_like(q, float("nan")))
+    e = dim ** -0.5 * float(q.float().abs().sum(-1).max()) * amax[0] * (2.0 ** -11 + 2.0 ** -18)
+    assert ((got.float() - want).abs() <= (2 * e + 2.0 ** -9) * amax[1] + want.abs() * 2.0 ** -8).all()
+    # and closely where it counts: rounding errors are as good as independent, so far smaller over a whole head
+    assert float((got.float() - want).norm() / want.norm()) < 2.0 ** -8
+    assert q4q.q4q_device_status() == 0
+
+
 def test_prompts_where_rows_see_nothing(q4q):
     """More rows than tokens, sequences without tokens or rows, every row sees every key, negative and zero scales."""
-    case = Case(31, [100, 0, 64], [200, 180, 0], 4, 2, 64, 16, "bf16")
+    case = widened(Case(31, [100, 0, 64], [200, 180, 0], 4, 2, 64, 16, "bf16"))
     for kw in ({}, {"causal": False}, {"window": 5}, {"scale": -0.3}, {"scale": 0.0}):
         got, lse = case.run(q4q, lse=True, **kw)
         check(case, got, lse, **kw)
@@ -161,7 +201,7 @@ def test_prompts_where_rows_see_nothing(q4q):
 
 
 def test_prompts_with_pages_that_are_not_there(q4q):
-    case = Case(32, [400, 300], [100, 120], 4, 2, 128, 16, "bf16")
+    case = widened(Case(32, [400, 300], [100, 120], 4, 2, 128, 16, "bf16"))
     case.pages[0, [0, 3, 24]] = -1
     case.pages[1, 7:18] = 10 ** 6
     got, lse = case.run(q4q, lse=True)
@@ -170,7 +210,7 @@ def test_prompts_with_pages_that_are_not_there(q4q):
 
 
 def test_prompts_rows_behind_and_strides(q4q):
-    case = Case(33, [160, 70], [150, 60], 4, 2, 64, 16, "bf16")
+    case = widened(Case(33, [160, 70], [150, 60], 4, 2, 64, 16, "bf16"))
     n = case.q.shape[0]
     wide = torch.full((n + 4, 8, 64), float("nan"), dtype=torch.bfloat16, device="cuda")
     wide[:n, :4] = case.q.cuda()
@@ -259,7 +299,7 @@ def test_nan_in_keys_that_a_row_does_not_see(q4q, rows, type):
     """A NaN or infinite scale of a later token, of a token before the window: rows that do not see it are
     what they are without it; rows that do are not finite in the block's dims (values) or everywhere (keys)."""
     n, window = 200, 30
-    case = Case(10, [n], [rows], 4, 2, 64, 16, type)
+    case = widened(Case(10, [n], [rows], 4, 2, 64, 16, type))
     clean = case.run(q4q, window=window).cpu()
     o, _, size, span = case.want(window=window)
     tol = torch.from_numpy(2 * bounds(case, size, span, o)[0])
@@ -267,7 +307,7 @@ def test_nan_in_keys_that_a_row_does_not_see(q4q, rows, type):
     for token, of_v in ((n - 1, True), (n - 1, False), (n - rows - window - 5, True), (n - rows - window - 5, False)):
         if token < 0:
             continue
-        case2 = Case(10, [n], [rows], 4, 2, 64, 16, type)
+        case2 = widened(Case(10, [n], [rows], 4, 2, 64, 16, type))
         slot = int(case2.pages[0][token // 16]) * 16 + token % 16
         where = ref.chunk_of(slot, 1, 2, 64, 16) + at_s(slot % 16, of_v)[1]
         case2.cache[where: where + 2] = np.array([np.inf if token % 2 else np.nan], np.float16).view(np.uint8)
