@@ -609,7 +609,7 @@ Q4Q_API q4q_status q4q_qk_norm_rope_back(const void* d_q_dst, const void* d_k_ds
  *   V codes   [2 octets][8 g][4 pairs p][B blocks b] words: the low half for token 2p of the octet,
  *             the high half for token 2p + 1; nibble n of a half holds dim 32 b + 4 g + n;
  *   K scales  [16 tokens][B] fp16, then V scales likewise.  A value is (nibble - 8) * its scale.
- * The cache is one 256-byte aligned buffer of n_pages pages; slot s is token s % page_tokens of page
+ * The cache is one 16-byte aligned buffer of n_pages pages; slot s is token s % page_tokens of page
  * s / page_tokens.  q4q_kv_page_size: bytes of a page.  head_dim as above, up to 1024 heads, pages of
  * less than 2^31 bytes, n_pages * page_tokens < 2^31. */
 Q4Q_API q4q_status q4q_kv_page_size(int n_kv_heads, int64_t head_dim, int page_tokens, size_t* bytes);
@@ -632,7 +632,8 @@ Q4Q_API q4q_status q4q_kv_append(void* cache, int64_t n_pages, int page_tokens, 
 Q4Q_API q4q_status q4q_kv_get_rows(const void* cache, int64_t n_pages, int page_tokens, int n_kv_heads, int64_t head_dim,
                            const int32_t* slots, int64_t n_slots, void* k_dst, void* v_dst, int dst_type, q4q_stream_t stream);
 
-/* Bytes of device workspace q4q_kv_attn needs on the current device for up to n_q rows of queries. */
+/* Bytes of device workspace q4q_kv_attn needs on the current device for n_seqs sequences with up to
+ * n_q rows of queries (the same rows as fewer sequences may need more). */
 Q4Q_API q4q_status q4q_kv_attn_workspace_size(int64_t n_q, int n_q_heads, int n_kv_heads, int64_t head_dim, int64_t n_seqs, int type,
                                       size_t* bytes);
 
@@ -645,27 +646,34 @@ Q4Q_API q4q_status q4q_kv_attn_workspace_size(int64_t n_q, int n_q_heads, int n_
  *   window > 0:  only j > last - window, last the largest j that the line above allows.
  * A row that sees no key gets zeros, and -inf in lse (fp32 [n_q][n_q_heads], natural logarithm of the
  * sum of exp(scale <q, K_j>); NULL: not written).  Rows of q that belong to no sequence are neither
- * read nor written.  Keys that a row does not see take no part, whatever their bytes hold.  Sums and
- * statistics are fp32.  16-bit rows in numbers (see q4q_kv_attn_tc) have keys, values and weights
- * rounded to fp16 for the tensor cores; elsewhere queries and weights are kept as two fp16 and
- * codes are exact.
- * q: device, type, [n_q][n_q_heads][head_dim] at q_stride; dst: contiguous, of the same type; cache,
- * pages int32 [n_seqs][max_pages], kv_len int32 [n_seqs], first int32 [n_seqs + 1]: device.  kv_len
- * beyond max_pages pages counts as that many, and a page outside the cache as one that no row
- * sees; both record Q4Q_ERR_ARG.  workspace: 256-byte aligned.  n_q_heads a multiple of n_kv_heads,
- * up to 1024; n_q < 2^24, n_q * n_q_heads / n_kv_heads < 2^31, n_seqs < 2^20, max_pages * page_tokens < 2^31.  Queries below 2^100.  The result
- * depends on the operands and the device alone. */
+ * read nor written.  Keys that a row does not see take no part, whatever their bytes hold.
+ * Sums and statistics are fp32, scales are applied in fp32 and codes are exact.  fp32 and fp16
+ * queries and their weights count with 22 bits; weights of bf16 queries are rounded to fp16.  bf16
+ * prompts of 64 rows a key-value head and more, heads up to 128, may run on the tcgen05 tensor
+ * cores, where keys and values are rounded to fp16 as well (scales above 8188, which q4q_kv_append
+ * does not write, would pass its range).  A NaN in a row's query, or in scales of keys that it sees,
+ * gives NaN.
+ * q: device, type, [n_q][n_q_heads][head_dim] at q_stride; dst: contiguous, of the same type, not
+ * overlapping q; cache, pages int32 [n_seqs][max_pages], kv_len int32 [n_seqs], first int32
+ * [n_seqs + 1], ascending: device.  kv_len beyond max_pages pages counts as that many, and a page
+ * outside the cache as one that no row sees; both record Q4Q_ERR_ARG.  workspace: 256-byte aligned,
+ * of one call at a time.  n_q_heads a multiple of n_kv_heads, up to 1024; n_q < 2^24, n_q *
+ * n_q_heads / n_kv_heads < 2^30, n_seqs < 2^20, max_pages * page_tokens < 2^30.  Queries below
+ * 2^100.  The result depends on the operands and the device alone. */
 Q4Q_API q4q_status q4q_kv_attn(const void* q, int64_t q_stride, int type, int64_t n_q, int n_q_heads, int n_kv_heads, int64_t head_dim,
                        const void* cache, int64_t n_pages, int page_tokens, const int32_t* pages, int64_t max_pages,
                        const int32_t* kv_len, const int32_t* first, int64_t n_seqs, float scale, int causal, int64_t window, void* dst,
                        float* lse, void* workspace, size_t workspace_bytes, q4q_stream_t stream);
 
-/* Debug: the failure path of that kernel's bounded waits (see q4q_debug_mul_mat_timeout): every wait
- * is bounded by limit_ns and the first CTA's first copy is left out. */
+/* Debug: the failure path of the bounded waits of either kernel (see q4q_debug_mul_mat_timeout): every
+ * wait is bounded by limit_ns and the first CTA leaves out its first hand-off.  path 0: warp-level
+ * MMAs, one row a sequence (first NULL) or ragged ones; path 1: tcgen05, bf16 and heads up to 128 (else
+ * Q4Q_ERR_SHAPE), with q4q_kv_attn_workspace_size's bytes for 64 n_seqs rows or more. */
 Q4Q_API q4q_status q4q_debug_kv_attn_timeout(const void* q, int64_t q_stride, int type, int64_t n_q, int n_q_heads, int n_kv_heads,
                                      int64_t head_dim, const void* cache, int64_t n_pages, int page_tokens, const int32_t* pages,
-                                     int64_t max_pages, const int32_t* kv_len, int64_t n_seqs, float scale, void* dst, void* workspace,
-                                     size_t workspace_bytes, uint64_t limit_ns, q4q_stream_t stream);
+                                     int64_t max_pages, const int32_t* kv_len, const int32_t* first, int64_t n_seqs, float scale,
+                                     void* dst, void* workspace, size_t workspace_bytes, int path, uint64_t limit_ns,
+                                     q4q_stream_t stream);
 
 /* Synchronizes the device, returns (in *status) the first device-side error
  * recorded since the last call (Q4Q_OK if none) and clears it.  This is where a

@@ -81,7 +81,7 @@ _SIGNATURES = {
     "q4q_kv_get_rows": (STATUS, [P, I64, INT, INT, I64, P, I64, P, P, INT, P]),
     "q4q_kv_attn_workspace_size": (STATUS, [I64, INT, INT, I64, I64, INT, SIZE]),
     "q4q_kv_attn": (STATUS, [P, I64, INT, I64, INT, INT, I64, P, I64, INT, P, I64, P, P, I64, F32, INT, I64, P, P, P, ctypes.c_size_t, P]),
-    "q4q_debug_kv_attn_timeout": (STATUS, [P, I64, INT, I64, INT, INT, I64, P, I64, INT, P, I64, P, I64, F32, P, P, ctypes.c_size_t,
+    "q4q_debug_kv_attn_timeout": (STATUS, [P, I64, INT, I64, INT, INT, I64, P, I64, INT, P, I64, P, P, I64, F32, P, P, ctypes.c_size_t, INT,
                                            ctypes.c_uint64, P]),
     "q4q_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "q4q_version": (ctypes.c_int, []),

@@ -98,11 +98,11 @@ def q4q_kv_attn(q: torch.Tensor, cache: torch.Tensor, page_tokens: int, n_kv_hea
     pages int32 [sequences, pages of one]: the pages of each sequence's tokens; kv_len int32 [sequences]: its cached
     tokens, those of the rows among them; first int32 [sequences + 1]: its rows of q (None: one row each).  scale:
     1 / sqrt(head_dim) by default.  lse: fp32 [rows, query heads], filled where given."""
-    return _ext.kv_attn(q, cache, page_tokens, n_kv_heads, pages, kv_len, first, scale, causal, window, dst, lse, workspace, stream, None)
+    return _ext.kv_attn(q, cache, page_tokens, n_kv_heads, pages, kv_len, first, scale, causal, window, dst, lse, workspace, stream, None, None)
 
 
 def q4q_debug_kv_attn_timeout(q: torch.Tensor, cache: torch.Tensor, page_tokens: int, n_kv_heads: int, pages: torch.Tensor,
-                              kv_len: torch.Tensor, limit_ns: int) -> torch.Tensor:
-    """q4q_kv_attn, one row a sequence, with its first CTA's first copy left out and every wait bounded by limit_ns:
-    q4q_device_status() then reports Q4Q_ERR_TIMEOUT (6) and the result is incomplete."""
-    return _ext.kv_attn(q, cache, page_tokens, n_kv_heads, pages, kv_len, None, None, True, 0, None, None, None, None, limit_ns)
+                              kv_len: torch.Tensor, limit_ns: int, first: Optional[torch.Tensor] = None, path: int = 0) -> torch.Tensor:
+    """q4q_kv_attn on one kernel (path 0: warp-level MMAs, 1: tcgen05, bf16 prompts), its first CTA's first hand-off left out
+    and every wait bounded by limit_ns: q4q_device_status() then reports Q4Q_ERR_TIMEOUT (6) and the result is incomplete."""
+    return _ext.kv_attn(q, cache, page_tokens, n_kv_heads, pages, kv_len, first, None, True, 0, None, None, None, None, path, limit_ns)

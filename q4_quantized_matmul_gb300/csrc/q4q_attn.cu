@@ -37,17 +37,17 @@ q4q_status check(AttnArgs& a, const void* q, int64_t q_stride, int type, int64_t
     q4q_status st = kv_check(n_pages, page_tokens, n_kv_heads, head_dim, a.page_log);
     if (st != Q4Q_OK) return st;
     if (n_q_heads < 1 || n_q_heads > 1024 || n_q_heads % n_kv_heads || n_q < 0 || n_q >= (1 << 24) || n_seqs < 0 || n_seqs >= (1 << 20) ||
-        max_pages < 0 || max_pages >= (1ll << 31) / page_tokens || window < 0)
+        max_pages < 0 || max_pages >= (1ll << 30) / page_tokens || window < 0)
         return Q4Q_ERR_SHAPE;
     if (q_stride < n_q_heads * head_dim || q_stride >= (1ll << 31)) return Q4Q_ERR_SHAPE;
     if (!first && n_seqs > n_q) return Q4Q_ERR_SHAPE;
-    if (n_q * (n_q_heads / n_kv_heads) >= (1ll << 31)) return Q4Q_ERR_SHAPE;
+    if (n_q * (n_q_heads / n_kv_heads) >= (1ll << 30)) return Q4Q_ERR_SHAPE;
     if (!mx_type_ok(type) || !(scale == scale)) return Q4Q_ERR_ARG;
     empty = n_q == 0 || n_seqs == 0;
     if (empty) return Q4Q_OK;
     if (!q || !dst || !kv_len || !workspace || (max_pages > 0 && !pages) || (n_pages > 0 && !cache)) return Q4Q_ERR_NULL;
     const size_t size = mx_type_bytes(type);
-    if (!aligned(q, size) || !aligned(dst, size) || !aligned(cache, 256) || !aligned(workspace, 256) || !aligned(pages, 4) || !aligned(kv_len, 4) ||
+    if (!aligned(q, size) || !aligned(dst, size) || !aligned(cache, 16) || !aligned(workspace, 256) || !aligned(pages, 4) || !aligned(kv_len, 4) ||
         !aligned(first, 4) || !aligned(lse, 4))
         return Q4Q_ERR_ALIGN;
     if ((st = current_device_info(&info)) != Q4Q_OK) return st;
@@ -61,7 +61,7 @@ q4q_status check(AttnArgs& a, const void* q, int64_t q_stride, int type, int64_t
     a.n_q = n_q;
     a.n_pages = n_pages;
     a.max_pages = max_pages;
-    a.window = window;
+    a.window = std::min<int64_t>(window, 1ll << 31);      // which is past every key
     a.n_seqs = (int)n_seqs;
     a.heads = n_q_heads;
     a.kv_heads = n_kv_heads;
@@ -87,7 +87,6 @@ q4q_status check(AttnArgs& a, const void* q, int64_t q_stride, int type, int64_t
 bool wide(const AttnArgs& a) { return a.n_q * a.shared > (int64_t)a.n_seqs * (a.type == Q4Q_TYPE_BF16 ? 8 : 4); }
 
 q4q_status dispatch(const AttnArgs& a, int64_t head_dim, void* workspace, cudaStream_t stream, const DeviceInfo& info) {
-    if (on_tensor_cores(a, head_dim)) return attn_tc_run(a, head_dim, workspace, stream, info);
     switch (head_dim) {
         case 64: return attn_run_64(a, wide(a), workspace, stream, info);
         case 96: return attn_run_96(a, wide(a), workspace, stream, info);
@@ -112,7 +111,9 @@ using namespace q4q;
 
 extern "C" q4q_status q4q_kv_attn_workspace_size(int64_t n_q, int n_q_heads, int n_kv_heads, int64_t head_dim, int64_t n_seqs, int type, size_t* bytes) {
     if (!bytes) return Q4Q_ERR_NULL;
-    if (!kv_dim_ok(head_dim) || n_kv_heads < 1 || n_q_heads < 1 || n_q_heads % n_kv_heads || n_q < 0 || n_seqs < 0) return Q4Q_ERR_SHAPE;
+    if (!kv_dim_ok(head_dim) || n_kv_heads < 1 || n_q_heads < 1 || n_q_heads % n_kv_heads || n_q_heads > 1024 || n_q < 0 || n_q >= (1 << 24) || n_seqs < 0 ||
+        n_seqs >= (1 << 20))
+        return Q4Q_ERR_SHAPE;
     if (!mx_type_ok(type)) return Q4Q_ERR_ARG;
     DeviceInfo info;
     const q4q_status st = current_device_info(&info);
@@ -131,21 +132,26 @@ extern "C" q4q_status q4q_kv_attn(const void* q, int64_t q_stride, int type, int
     const q4q_status st = check(a, q, q_stride, type, n_q, n_q_heads, n_kv_heads, head_dim, cache, n_pages, page_tokens, pages, max_pages, kv_len,
                                 first, n_seqs, scale, causal, window, dst, lse, workspace, workspace_bytes, empty, info);
     if (st != Q4Q_OK || empty) return st;
+    if (on_tensor_cores(a, head_dim)) return attn_tc_run(a, head_dim, workspace, (cudaStream_t)stream, info);
     return dispatch(a, head_dim, workspace, (cudaStream_t)stream, info);
 }
 
 extern "C" q4q_status q4q_debug_kv_attn_timeout(const void* q, int64_t q_stride, int type, int64_t n_q, int n_q_heads, int n_kv_heads,
                                                 int64_t head_dim, const void* cache, int64_t n_pages, int page_tokens, const int32_t* pages,
-                                                int64_t max_pages, const int32_t* kv_len, int64_t n_seqs, float scale, void* dst,
-                                                void* workspace, size_t workspace_bytes, uint64_t limit_ns, q4q_stream_t stream) {
-    if (limit_ns < 1 || limit_ns > WAIT_LIMIT_NS) return Q4Q_ERR_ARG;
+                                                int64_t max_pages, const int32_t* kv_len, const int32_t* first, int64_t n_seqs, float scale,
+                                                void* dst, void* workspace, size_t workspace_bytes_given, int path, uint64_t limit_ns,
+                                                q4q_stream_t stream) {
+    if (limit_ns < 1 || limit_ns > WAIT_LIMIT_NS || path < 0 || path > 1) return Q4Q_ERR_ARG;
     AttnArgs a{};
     DeviceInfo info;
     bool empty;
     const q4q_status st = check(a, q, q_stride, type, n_q, n_q_heads, n_kv_heads, head_dim, cache, n_pages, page_tokens, pages, max_pages, kv_len,
-                                nullptr, n_seqs, scale, 1, 0, dst, nullptr, workspace, workspace_bytes, empty, info);
+                                first, n_seqs, scale, 1, 0, dst, nullptr, workspace, workspace_bytes_given, empty, info);
     if (st != Q4Q_OK || empty) return st;
     a.limit_ns = limit_ns;
     a.fault = 1;
-    return dispatch(a, head_dim, workspace, (cudaStream_t)stream, info);
+    if (path == 0) return dispatch(a, head_dim, workspace, (cudaStream_t)stream, info);
+    if (type != Q4Q_TYPE_BF16 || head_dim > 128) return Q4Q_ERR_SHAPE;
+    if (workspace_bytes_given < attn_tc_workspace(head_dim, info)) return Q4Q_ERR_WORKSPACE;
+    return attn_tc_run(a, head_dim, workspace, (cudaStream_t)stream, info);
 }

@@ -26,7 +26,7 @@ struct AttnArgs {
     void* dst;
     float* lse;
     uint64_t limit_ns;
-    int fault;                                 // test support: the first CTA leaves out its first copy
+    int fault;                                 // test support: the first CTA leaves out its first hand-off
 };
 
 // The kernels of each head size (q4q_attn_d*.cu).

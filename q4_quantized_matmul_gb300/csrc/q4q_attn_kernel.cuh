@@ -729,7 +729,9 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_kernel(const __grid_
                 sum += __shfl_xor_sync(0xffffffffu, sum, 8);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 16);
                 const int row = C::SPLIT ? q * 4 + 2 * (t & 1) + c : q * 8 + 2 * t + c;
-                if (g == 0 && (!C::SPLIT || t < 2)) stats[warp * C::ROWS + row] = make_float2(any && m[q][c] != -INFINITY ? ref[q][c] : -INFINITY, sum);
+                // scores that are all NaN leave no maximum, but a NaN in the sum
+                if (g == 0 && (!C::SPLIT || t < 2))
+                    stats[warp * C::ROWS + row] = make_float2(any && (m[q][c] != -INFINITY || sum != 0.0f) ? ref[q][c] : -INFINITY, sum);
                 if (any)
 #pragma unroll
                     for (int b = 0; b < B; ++b) {

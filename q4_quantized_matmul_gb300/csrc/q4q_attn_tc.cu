@@ -387,7 +387,7 @@ __device__ __forceinline__ void tc_decode(const AttnArgs& a, TcWalk w, const TcW
         }
         fence_async();
         __syncwarp();
-        if (lane == 0) wait.arrive(C::K_FULL + stage);
+        if (lane == 0 && !(a.fault && blockIdx.x == 0 && d == 0 && steps == 0)) wait.arrive(C::K_FULL + stage);
         load_k(here);
         // Scales of keys that are not there become 0, and so do those that are no number: the softmax marks the rows that see
         // those.
@@ -455,7 +455,7 @@ __host__ __device__ constexpr uint32_t tc_idesc(int n) { return (1u << 4) | ((ui
 template <typename C>
 __device__ __forceinline__ void tc_issue(const AttnArgs& a, TcWalk w, const TcWaits& wait, uint32_t base, uint32_t tmem) {
     const bool one = elect_one();
-    uint32_t steps = 0, pieces = 0, drained = 0;
+    uint32_t steps = 0, pieces = 0;
     bool ok = true;
     const auto commit = [&](int bar) {
         if (one) mma_commit(wait.bars + bar * 8);
@@ -524,7 +524,7 @@ __device__ __forceinline__ void tc_issue(const AttnArgs& a, TcWalk w, const TcWa
     }
     // nothing is in flight when tensor and shared memory are given back
     commit(C::DRAIN);
-    mbar_wait_bounded(wait.bars + C::DRAIN * 8, drained & 1, a.limit_ns);
+    mbar_wait_bounded(wait.bars + C::DRAIN * 8, 0, a.limit_ns);
     __syncwarp();
 }
 
@@ -688,7 +688,7 @@ __device__ __forceinline__ void tc_softmax(const AttnArgs& a, const Plan& plan, 
         const int part = 2 * blockIdx.x + (w.first == 0 ? 1 : 0);
         float* part_row = plan.rows + (int64_t)part * (TC_ROWS * (C::DIM + 2)) + (i * TC_TILE + r) * C::DIM;
         if (!complete && tid == 0) plan.parts[part] = {w.p_s, w.p_head, w.p_tile, w.first, w.last, w.of};
-        const bool none = ref == NONE;
+        const bool none = ref == NONE && l == 0.0f;                           // scores that are all NaN leave a NaN in l
         const float inv = complete ? (none ? 0.0f : 1.0f / l) : 1.0f;
         __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.dst) + (at * a.heads + head) * C::DIM;
 #pragma unroll 1

@@ -371,7 +371,7 @@ extern "C" q4q_status q4q_kv_append(void* cache, int64_t n_pages, int page_token
     if (n_tokens == 0) return Q4Q_OK;
     if (!cache || !k || !v || !slots || (table && !pos)) return Q4Q_ERR_NULL;
     const size_t size = mx_type_bytes(type);
-    if (!aligned(cache, 256) || !aligned(k, size) || !aligned(v, size) || !aligned(slots, 4) || (k_weight && !aligned(k_weight, 16)) ||
+    if (!aligned(cache, 16) || !aligned(k, size) || !aligned(v, size) || !aligned(slots, 4) || (k_weight && !aligned(k_weight, 16)) ||
         (table && (!aligned(table, 16) || !aligned(pos, 4))))
         return Q4Q_ERR_ALIGN;
     a.k = k;
@@ -407,7 +407,7 @@ extern "C" q4q_status q4q_kv_get_rows(const void* cache, int64_t n_pages, int pa
     if (n_slots == 0 || (!k_dst && !v_dst)) return Q4Q_OK;
     if (!cache || !slots) return Q4Q_ERR_NULL;
     const size_t size = mx_type_bytes(dst_type);
-    if (!aligned(cache, 256) || !aligned(slots, 4) || !aligned(k_dst, size) || !aligned(v_dst, size)) return Q4Q_ERR_ALIGN;
+    if (!aligned(cache, 16) || !aligned(slots, 4) || !aligned(k_dst, size) || !aligned(v_dst, size)) return Q4Q_ERR_ALIGN;
     a.cache = static_cast<uint8_t*>(const_cast<void*>(cache));
     a.slots = slots;
     a.k_dst = k_dst;

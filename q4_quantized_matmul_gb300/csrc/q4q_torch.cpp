@@ -703,10 +703,11 @@ PyObject* kv_get_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
-// kv_attn(q, cache, page_tokens, n_kv_heads, pages, kv_len, first, scale, causal, window, dst, lse, workspace, stream, limit_ns) -> dst
+// kv_attn(q, cache, page_tokens, n_kv_heads, pages, kv_len, first, scale, causal, window, dst, lse, workspace, stream, path, limit_ns) -> dst;
+// with a path the debug call
 PyObject* kv_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded([&] {
-        need(a, n, 15);
+        need(a, n, 16);
         const at::Tensor &q = tensor(a[0], "q"), &cache = tensor(a[1], "cache"), &pages = tensor(a[4], "pages"), &len = tensor(a[5], "kv_len");
         const int type = type_of(q, "q"), page_tokens = small_integer(a[2], "page_tokens"), kv_heads = small_integer(a[3], "n_kv_heads");
         const Place at(q, "q", a[13]);
@@ -738,8 +739,9 @@ PyObject* kv_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
         else
             check("q4q_debug_kv_attn_timeout",
                   q4q_debug_kv_attn_timeout(h.at, h.stride, type, h.tokens, (int)h.heads, kv_heads, h.dim, buffer, n_pages, page_tokens,
-                                            static_cast<const int32_t*>(table), max_pages, static_cast<const int32_t*>(lengths), seqs, scale, out, ws, size,
-                                            (uint64_t)integer(a[14], "limit_ns"), at.stream()));
+                                            static_cast<const int32_t*>(table), max_pages, static_cast<const int32_t*>(lengths),
+                                            static_cast<const int32_t*>(first), seqs, scale, out, ws, size, small_integer(a[14], "path"),
+                                            (uint64_t)integer(a[15], "limit_ns"), at.stream()));
         return wrap(dst);
     });
 }

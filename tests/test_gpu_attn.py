@@ -426,6 +426,24 @@ def test_timeout_path(q4q):
     q4q.q4q_debug_kv_attn_timeout(*case.args(), 2_000_000)
     assert q4q.q4q_device_status() == 6 and q4q.q4q_device_status() == 0
     check(case, case.run(q4q))
+    case = widened(Case(17, [500], [150], 8, 2, 64, 16, "bf16"))
+    first = torch.from_numpy(case.first).cuda()
+    q4q.q4q_debug_kv_attn_timeout(*case.args(), 2_000_000, first=first, path=1)
+    assert q4q.q4q_device_status() == 6 and q4q.q4q_device_status() == 0
+    check(case, case.run(q4q))
+    with pytest.raises(q4q.Q4QError):
+        q4q.q4q_debug_kv_attn_timeout(*Case(17, [500], [150], 8, 2, 64, 16).args(), 2_000_000, first=first, path=1)
+
+
+@pytest.mark.parametrize("dim", [64, 96, 128, 256])
+@pytest.mark.parametrize("type", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("rows", [1, 2, 9])
+def test_every_kernel_of_warp_level_mmas(q4q, dim, type, rows):
+    """Each head size, type and number of column groups, with more chunks than a CTA takes."""
+    case = Case([dim, rows], [300, 40, 17], [rows, 1, rows], 6, 2, dim, 32, type)
+    assert not on_tensor_cores(case)
+    got, lse = case.run(q4q, lse=True)
+    check(case, got, lse)
 
 
 def test_streams_graphs_and_workspaces(q4q):
@@ -438,8 +456,9 @@ def test_streams_graphs_and_workspaces(q4q):
     dst = torch.empty_like(q)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
-    assert torch.equal(q4q.q4q_kv_attn(q, cache, page, kv, pages, length, first=first, stream=side, workspace=ws).cpu(), want.cpu())
-    torch.cuda.synchronize()
+    got = q4q.q4q_kv_attn(q, cache, page, kv, pages, length, first=first, stream=side, workspace=ws)
+    torch.cuda.synchronize()                             # nothing else orders the comparison behind the other stream
+    assert torch.equal(got, want)
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         q4q.q4q_kv_attn(q, cache, page, kv, pages, length, first=first, dst=dst, workspace=ws)
@@ -453,6 +472,159 @@ def test_streams_graphs_and_workspaces(q4q):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(dst, want2)
+
+
+def test_streams_and_graphs_of_prompts(q4q):
+    case, other = (widened(Case(s, [300, 150], [200, 150], 4, 2, 64, 16, "bf16")) for s in (41, 42))
+    want, want2 = case.run(q4q), other.run(q4q)
+    q, cache, page, kv, pages, length = case.args()
+    first = torch.from_numpy(case.first).cuda()
+    ws = torch.full((q4q.q4q_kv_attn_workspace_size(350, 4, 2, 64, 2, torch.bfloat16),), 0xFF, dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = q4q.q4q_kv_attn(q, cache, page, kv, pages, length, first=first, stream=side, workspace=ws)
+    torch.cuda.synchronize()                             # nothing else orders the comparison behind the other stream
+    assert torch.equal(got, want)
+    dst, graph = torch.empty_like(q), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(2):
+            q4q.q4q_kv_attn(q, cache, page, kv, pages, length, first=first, dst=dst, workspace=ws)
+    q2, cache2, _, _, pages2, _ = other.args()
+    for _ in range(2):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(dst, want)
+    q.copy_(q2), cache.copy_(cache2), pages.copy_(pages2), ws.fill_(0x7F)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(dst, want2)
+    # two calls at once, on streams and workspaces of their own
+    outs = []
+    for s in (torch.cuda.Stream(), torch.cuda.Stream()):
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            outs.append([q4q.q4q_kv_attn(q, cache, page, kv, pages, length, first=first) for _ in range(4)])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want2) for out in outs for o in out)
+
+
+def test_prompts_of_many_sequences(q4q):
+    """More sequences than warps share their tiles between."""
+    rng = np.random.default_rng(43)
+    lengths = [int(x) for x in rng.integers(0, 60, 230)]
+    lengths[100] = 700
+    rows = [min(int(x), n) if n else 2 for x, n in zip(rng.integers(0, 50, 230), lengths)]
+    rows[100] = 600
+    case = widened(Case(43, lengths, rows, 4, 1, 64, 16, "bf16"))
+    assert on_tensor_cores(case)
+    got, lse = case.run(q4q, lse=True)
+    check(case, got, lse)
+    assert q4q.q4q_device_status() == 0
+
+
+@pytest.mark.parametrize("rows,type", [(1, "f32"), (3, "f16"), (9, "bf16"), (80, "bf16")])
+def test_rows_of_nan_and_keys_of_nan(q4q, rows, type):
+    """A row whose query is NaN is NaN, and the others are right; so is every row where all keys are NaN."""
+    case, case2 = (widened(Case([44, rows], [200, 90], [rows, rows], 4, 2, 64, 16, type)) for _ in range(2))
+    want = case.run(q4q)
+    case.q[0, 1, 3] = float("nan")
+    got, lse = case.run(q4q, lse=True)
+    assert torch.isnan(got[0, 1]).all() and torch.isnan(lse[0, 1])
+    # a tile's rows move their references together, so the others may round differently
+    o, true_lse, size, span = case2.want()
+    tol, tol_lse = bounds(case2, size, span, o)
+    keep = np.ones(got.shape[:2], bool)
+    keep[0, 1] = False
+    assert np.all((np.abs(got.double().cpu().numpy() - o) <= tol)[keep])
+    assert np.all((np.abs(lse.double().cpu().numpy() - true_lse) <= tol_lse + 2.0 ** -22 * np.abs(true_lse))[keep])
+    case = widened(Case([44, rows], [200, 90], [rows, rows], 4, 2, 64, 16, type))
+    k = np.full((200, 2, 64), np.nan, np.float32)
+    k[:, 1] = 1.0
+    j = np.arange(200)
+    ref.put(case.cache, 16, case.pages[0][j // 16] * 16 + j % 16, k, np.ones_like(k))
+    got, lse = case.run(q4q, lse=True)
+    assert torch.isnan(got[:rows, :2]).all() and torch.isnan(lse[:rows, :2]).all()
+    assert torch.isfinite(got[:rows, 2:]).all() and torch.equal(got[rows:], want[rows:])
+
+
+@pytest.mark.parametrize("rows,type", [(3, "f32"), (80, "bf16")])
+def test_windows_past_every_key(q4q, rows, type):
+    case = widened(Case(45, [300], [rows], 4, 2, 64, 16, type))
+    want = case.run(q4q)
+    for window in (300, 2 ** 31, 2 ** 63 - 1):
+        assert torch.equal(case.run(q4q, window=window), want)
+
+
+def test_steps_with_projections(q4q):
+    """As a model runs them: fused projection, norm and rotation, append, attention, output projection; prompts of two sequences, then
+    single tokens in a graph whose positions, slots and lengths move on.  Every step against the references, from its own inputs."""
+    import oracle
+    rng = np.random.default_rng(46)
+    heads, kv, dim, page, width, eps = 6, 2, 64, 16, 384, 1e-5
+    rows = (heads + 2 * kv) * dim
+    w_in = oracle.quantize_q4_0(rng.standard_normal((rows, width)).astype(np.float32) / 20)
+    w_out = oracle.quantize_q4_0(rng.standard_normal((width, heads * dim)).astype(np.float32) / 20)
+    wq, wk = ((1 + rng.standard_normal(dim) / 8).astype(np.float32) for _ in range(2))
+    g_in, g_out, g_wq, g_wk = (torch.from_numpy(x).cuda() for x in (w_in, w_out, wq, wk))
+    table = q4q.q4q_rope_table(64, 32)
+    lengths = np.array([21, 5])
+    pages = np.array([[4, 0, 6], [2, 5, 1]], np.int32)
+    mirror = np.zeros(8 * ref.page_size(kv, dim, page), np.uint8)
+    cache = torch.zeros(mirror.size, dtype=torch.uint8, device="cuda")
+    g_pages = torch.from_numpy(pages).cuda()
+
+    def block(x, pos, slots, kv_len, first):
+        qkv = q4q.q4q_mul_mat(g_in, width, rows, x).view(-1, heads + 2 * kv, dim)
+        q, _ = q4q.q4q_qk_norm_rope(qkv[:, :heads], None, g_wq, None, eps, table, pos)
+        q4q.q4q_kv_append(cache, page, qkv[:, heads: heads + kv], qkv[:, heads + kv:], slots, g_wk, eps, table, pos)
+        o = q4q.q4q_kv_attn(q, cache, page, kv, g_pages, kv_len, first=first)
+        return qkv, q, o, q4q.q4q_mul_mat(g_out, heads * dim, width, o.view(-1, heads * dim))
+
+    def verify(x, pos, slots, kv_len, first, got):
+        qkv, q, o, y = (t.cpu().numpy() for t in got)
+        want, size = oracle.mul_mat(w_in, width, rows, x)
+        assert np.all(np.abs(qkv.reshape(-1, rows) - want) <= 1e-5 * size)
+        t = table.cpu().numpy()
+        assert np.array_equal(q, ref.norm_rope(qkv[:, :heads], wq, eps, t, pos, True).astype(np.float32))
+        k = ref.norm_rope(qkv[:, heads: heads + kv], wk, eps, t, pos, True).astype(np.float32)
+        ref.put(mirror, page, slots, k, qkv[:, heads + kv:])
+        assert np.array_equal(cache.cpu().numpy(), mirror)
+        want, _, size, span = ref.attend(q, mirror, page, kv, pages, kv_len, first, dim ** -0.5)
+        u = 2.0 ** -22
+        e = span * (2 + 2 * (dim // 32 + 4)) * u
+        assert np.all(np.abs(o - want) <= size * (2 * e + span * u + (12 + 160 + 2) * u)[..., None] + np.abs(want) * 2.0 ** -24)
+        want, size = oracle.mul_mat(w_out, heads * dim, width, o.reshape(-1, heads * dim))
+        assert np.all(np.abs(y - want) <= 1e-5 * size)
+
+    def inputs(rows_of, base):
+        pos = np.concatenate([np.arange(b, b + n) for b, n in zip(base, rows_of)]).astype(np.int32)
+        seq = np.repeat(np.arange(2), rows_of)
+        x = rng.standard_normal((pos.size, width)).astype(np.float32)
+        return x, pos, (pages[seq, pos // page] * page + pos % page).astype(np.int32), (base + rows_of).astype(np.int32), \
+            np.concatenate([[0], np.cumsum(rows_of)]).astype(np.int32)
+
+    step = inputs(lengths, np.zeros(2, np.int64))
+    verify(*step, block(*(torch.from_numpy(a).cuda() for a in step)))
+    one = np.ones(2, np.int64)
+    held = [torch.from_numpy(a).cuda() for a in inputs(one, lengths)]
+    saved = cache.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        block(*held)
+    torch.cuda.synchronize()
+    cache.copy_(saved)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = block(*held)
+    for n in range(4):
+        step = inputs(one, lengths + n)
+        for t, a in zip(held, step):
+            t.copy_(torch.from_numpy(a))
+        graph.replay()
+        torch.cuda.synchronize()
+        verify(*step, got)
+    assert q4q.q4q_device_status() == 0
 
 
 def test_refusals(q4q):
