@@ -9,6 +9,8 @@
 namespace q4q {
 namespace {
 
+constexpr int64_t STEP_TOKENS = 2 * KV_GROUP;      // of the warp-level kernel
+
 // The tcgen05 kernel may take bf16 rows where a sequence has 64 of them or more for a key-value head, on average, and does where
 // its longer start pays: from 1024 keys on (the table's pages bound them), or from 256 rows, a CTA's tiles.  us, warp-level
 // MMAs / tcgen05, heads 32/8 of 128: 16 x 64 rows over 2048 keys 84 / 64, 128 rows over 8192 39 / 33, 64 rows over 8192 28 / 32, 256
@@ -83,15 +85,24 @@ q4q_status check(AttnArgs& a, const void* q, int64_t q_stride, int type, int64_t
 }
 
 // Two groups of columns where a key-value head has more rows than one group holds (8, or 4 that are split in two
-// fp16), by the average of the rows a sequence: a chunk is then unpacked once for twice the rows.
-bool wide(const AttnArgs& a) { return a.n_q * a.shared > (int64_t)a.n_seqs * (a.type == Q4Q_TYPE_BF16 ? 8 : 4); }
+// fp16), by the average of the rows a sequence: a chunk is then unpacked once for twice the rows, by half as many CTAs an
+// SM.  With few steps (by the table's keys, 24 for each of the 2 CTAs an SM that one group has) the single groups' shorter end of
+// a piece counts more.  us, one group / two, 8 key-value heads of 128, rows a head: fp32, 8 rows over 1023 keys 13.9 / 16.7, 4095
+// 16.3 / 18.3, 16383 20.7 / 18.6, 64 rows over 1023 19.4 / 20.4, 8191 51 / 42; 64 sequences of up to 8192 keys, bf16 12 rows 182 / 176,
+// 4 rows (one group by the rule) 96 / 161, fp32 8 rows 214 / 192, fp16 8 rows 190 / 196.
+bool wide(const AttnArgs& a, const DeviceInfo& info) {
+    const int64_t one = a.type == Q4Q_TYPE_BF16 ? 8 : 4, rows = a.n_q * a.shared;
+    const double steps = (double)((rows + one - 1) / one) * a.kv_heads * (double)(((a.max_pages << a.page_log) + STEP_TOKENS - 1) / STEP_TOKENS);
+    return rows > a.n_seqs * one && steps >= 24.0 * 2 * info.sm_count;
+}
 
 q4q_status dispatch(const AttnArgs& a, int64_t head_dim, void* workspace, cudaStream_t stream, const DeviceInfo& info) {
+    const bool two = wide(a, info);
     switch (head_dim) {
-        case 64: return attn_run_64(a, wide(a), workspace, stream, info);
-        case 96: return attn_run_96(a, wide(a), workspace, stream, info);
-        case 128: return attn_run_128(a, wide(a), workspace, stream, info);
-        default: return attn_run_256(a, wide(a), workspace, stream, info);
+        case 64: return attn_run_64(a, two, workspace, stream, info);
+        case 96: return attn_run_96(a, two, workspace, stream, info);
+        case 128: return attn_run_128(a, two, workspace, stream, info);
+        default: return attn_run_256(a, two, workspace, stream, info);
     }
 }
 

@@ -21,6 +21,11 @@
 //   warps 17-19      the next piece's queries
 // Steps of all pieces (sequence, head, 256 rows) in a row are cut into equal shares, one a CTA and SM; parts of a
 // piece are joined by a second kernel in order.
+//
+// Measured in a graph (heads 32/8 of 128): 512 rows behind 7680 keys 96 us (692 TFLOP/s), 8 such sequences 540 us (985
+// TFLOP/s), two prompts of 2048 with a window of 1024 130 us.  Bound by the softmax: a row's 128 scores are read,
+// exponentiated and written back in one thread, and the two tiles' chains fill about half of the tensor cores' time; a piece's
+// start and end cost about 10 us each time, the shares 4.4 us.
 #include "q4q_attn_kernel.cuh"
 
 namespace q4q {

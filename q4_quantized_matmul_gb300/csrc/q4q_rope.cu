@@ -14,6 +14,9 @@
 // launch and two loads behind one another when there are few.  dw is summed in registers over a warp's rows, then
 // over the block's warps, and the blocks' sums by a second kernel in the order of the blocks: no atomics, results do
 // not vary.
+//
+// Measured in a graph (32 + 8 heads of 128): one token 3.5 us; 8191 bf16 tokens forward 49.6 us (168 MB, 3.4 TB/s: bytes in
+// flight; three blocks an SM with fewer registers were slower, 57.7), backward with both weights 78 us (252 MB, 3.2 TB/s).
 #include <algorithm>
 
 #include "q4q_attn.cuh"

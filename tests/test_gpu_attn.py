@@ -547,6 +547,18 @@ def test_rows_of_nan_and_keys_of_nan(q4q, rows, type):
     assert torch.isfinite(got[:rows, 2:]).all() and torch.equal(got[rows:], want[rows:])
 
 
+@pytest.mark.parametrize("type", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("dim", [64, 96, 128, 256])
+def test_two_groups_of_columns(q4q, type, dim):
+    """More rows than a group holds and steps enough for two groups: by the tables' keys, most of which are not used."""
+    case = Case([dim, 47], [700, 90, 33, 5], [9, 12, 10, 5], 4, 2, dim, 16, type)
+    case.pages = np.pad(case.pages, ((0, 0), (0, 65536 // 16 - case.pages.shape[1])), constant_values=-1)
+    assert not on_tensor_cores(case)
+    got, lse = case.run(q4q, lse=True)
+    check(case, got, lse)
+    assert torch.equal(got, case.run(q4q)) and q4q.q4q_device_status() == 0
+
+
 @pytest.mark.parametrize("rows,type", [(3, "f32"), (80, "bf16")])
 def test_windows_past_every_key(q4q, rows, type):
     case = widened(Case(45, [300], [rows], 4, 2, 64, 16, type))
