@@ -654,7 +654,7 @@ Q4Q_API q4q_status q4q_kv_attn_workspace_size(int64_t n_q, int n_q_heads, int n_
  * does not write, would pass its range).  A NaN in a row's query, or in scales of keys that it sees,
  * gives NaN.
  * q: device, type, [n_q][n_q_heads][head_dim] at q_stride; dst: contiguous, of the same type, not
- * overlapping q; cache, pages int32 [n_seqs][max_pages], kv_len int32 [n_seqs], first int32
+ * overlapping q (Q4Q_ERR_ARG); cache, pages int32 [n_seqs][max_pages], kv_len int32 [n_seqs], first int32
  * [n_seqs + 1], ascending: device.  kv_len beyond max_pages pages counts as that many, and a page
  * outside the cache as one that no row sees; both record Q4Q_ERR_ARG.  workspace: 256-byte aligned,
  * of one call at a time.  n_q_heads a multiple of n_kv_heads, up to 1024; n_q < 2^24, n_q *

@@ -97,7 +97,8 @@ def q4q_kv_attn(q: torch.Tensor, cache: torch.Tensor, page_tokens: int, n_kv_hea
 
     pages int32 [sequences, pages of one]: the pages of each sequence's tokens; kv_len int32 [sequences]: its cached
     tokens, those of the rows among them; first int32 [sequences + 1]: its rows of q (None: one row each).  scale:
-    1 / sqrt(head_dim) by default.  lse: fp32 [rows, query heads], filled where given."""
+    1 / sqrt(head_dim) by default.  lse: fp32 [rows, query heads], filled where given.  Rows of no sequence are left as
+    they are, in a new dst undefined; dst must not overlap q."""
     return _ext.kv_attn(q, cache, page_tokens, n_kv_heads, pages, kv_len, first, scale, causal, window, dst, lse, workspace, stream, None, None)
 
 

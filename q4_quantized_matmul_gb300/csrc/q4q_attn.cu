@@ -52,6 +52,9 @@ q4q_status check(AttnArgs& a, const void* q, int64_t q_stride, int type, int64_t
     if (!aligned(q, size) || !aligned(dst, size) || !aligned(cache, 16) || !aligned(workspace, 256) || !aligned(pages, 4) || !aligned(kv_len, 4) ||
         !aligned(first, 4) || !aligned(lse, 4))
         return Q4Q_ERR_ALIGN;
+    // other CTAs read a row's queries after its result is written
+    const uintptr_t q0 = (uintptr_t)q, d0 = (uintptr_t)dst;
+    if (q0 < d0 + (uintptr_t)(n_q * n_q_heads * head_dim) * size && d0 < q0 + (uintptr_t)((n_q - 1) * q_stride + n_q_heads * head_dim) * size) return Q4Q_ERR_ARG;
     if ((st = current_device_info(&info)) != Q4Q_OK) return st;
     if (workspace_bytes_given < workspace_bytes(type, head_dim, n_q, n_q_heads / n_kv_heads, n_seqs, info)) return Q4Q_ERR_WORKSPACE;
     a.q = q;

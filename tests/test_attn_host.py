@@ -61,14 +61,15 @@ def test_append_and_rows_refuse(lib):
 
 def test_attention_refuses(lib):
     def call(q=AT, stride=256, type=0, n_q=3, heads=4, kv=2, dim=64, cache=AT, pages=4, page=16, table=AT, most=2, len=AT, first=AT, seqs=2, scale=0.1,
-             causal=1, window=0, dst=AT, lse=None, ws=AT, size=0):
+             causal=1, window=0, dst=P(0x100000), lse=None, ws=AT, size=0):
         return lib.q4q_kv_attn(q, stride, type, n_q, heads, kv, dim, cache, pages, page, table, most, len, first, seqs, scale, causal, window, dst, lse, ws,
                                size, None)
     for want, kw in ((SHAPE, dict(dim=72)), (SHAPE, dict(heads=5)), (SHAPE, dict(heads=0)), (SHAPE, dict(stride=255)), (SHAPE, dict(n_q=1 << 24)),
                      (SHAPE, dict(n_q=-1)), (SHAPE, dict(seqs=1 << 20)), (SHAPE, dict(most=1 << 26)), (SHAPE, dict(window=-1)), (SHAPE, dict(page=17)),
                      (SHAPE, dict(first=None, seqs=4)), (SHAPE, dict(n_q=1 << 23, heads=512, kv=2, stride=512 * 64)), (ARG, dict(type=5)),
                      (ARG, dict(scale=float("nan"))), (NULL, dict(q=None)), (NULL, dict(dst=None)), (NULL, dict(len=None)), (NULL, dict(table=None)),
-                     (NULL, dict(ws=None)), (NULL, dict(cache=None)), (ALIGN, dict(ws=P(0x1010))), (ALIGN, dict(cache=P(0x1004))), (ALIGN, dict(lse=ODD)),
+                     (NULL, dict(ws=None)), (NULL, dict(cache=None)), (ALIGN, dict(ws=P(0x1010))), (ALIGN, dict(cache=P(0x1004))), (ALIGN, dict(lse=ODD)), (ARG, dict(dst=AT)),
+                     (ARG, dict(q=P(0x1000), dst=P(0x1000 + 4 * (2 * 256 + 256) - 4))), (ARG, dict(q=P(0x9000), dst=P(0x9000 - 4 * 3 * 256 + 4))),
                      (0, dict(n_q=0)), (0, dict(seqs=0))):
         assert call(**kw) == want, kw
     n = ctypes.c_size_t(0)
