@@ -649,8 +649,8 @@ Q4Q_API q4q_status q4q_kv_attn_workspace_size(int64_t n_q, int n_q_heads, int n_
  * read nor written.  Keys that a row does not see take no part, whatever their bytes hold.
  * Sums and statistics are fp32, scales are applied in fp32 and codes are exact.  fp32 and fp16
  * queries and their weights count with 22 bits; weights of bf16 queries are rounded to fp16.  bf16
- * prompts of 64 rows a key-value head and more, heads up to 128, may run on the tcgen05 tensor
- * cores, where keys and values are rounded to fp16 as well (scales above 8188, which q4q_kv_append
+ * and fp16 prompts of 64 rows a key-value head and more, heads up to 128, may run on the tcgen05
+ * tensor cores, where values and weights, and for bf16 keys, are rounded to fp16 (scales above 8188, which q4q_kv_append
  * does not write, would pass its range).  A NaN in a row's query, or in scales of keys that it sees,
  * gives NaN.
  * q: device, type, [n_q][n_q_heads][head_dim] at q_stride; dst: contiguous, of the same type, not
@@ -667,7 +667,7 @@ Q4Q_API q4q_status q4q_kv_attn(const void* q, int64_t q_stride, int type, int64_
 
 /* Debug: the failure path of the bounded waits of either kernel (see q4q_debug_mul_mat_timeout): every
  * wait is bounded by limit_ns and the first CTA leaves out its first hand-off.  path 0: warp-level
- * MMAs, one row a sequence (first NULL) or ragged ones; path 1: tcgen05, bf16 and heads up to 128 (else
+ * MMAs, one row a sequence (first NULL) or ragged ones; path 1: tcgen05, 16-bit types and heads up to 128 (else
  * Q4Q_ERR_SHAPE), with q4q_kv_attn_workspace_size's bytes for 64 n_seqs rows or more. */
 Q4Q_API q4q_status q4q_debug_kv_attn_timeout(const void* q, int64_t q_stride, int type, int64_t n_q, int n_q_heads, int n_kv_heads,
                                      int64_t head_dim, const void* cache, int64_t n_pages, int page_tokens, const int32_t* pages,

@@ -104,6 +104,6 @@ def q4q_kv_attn(q: torch.Tensor, cache: torch.Tensor, page_tokens: int, n_kv_hea
 
 def q4q_debug_kv_attn_timeout(q: torch.Tensor, cache: torch.Tensor, page_tokens: int, n_kv_heads: int, pages: torch.Tensor,
                               kv_len: torch.Tensor, limit_ns: int, first: Optional[torch.Tensor] = None, path: int = 0) -> torch.Tensor:
-    """q4q_kv_attn on one kernel (path 0: warp-level MMAs, 1: tcgen05, bf16 prompts), its first CTA's first hand-off left out
+    """q4q_kv_attn on one kernel (path 0: warp-level MMAs, 1: tcgen05, 16-bit types), its first CTA's first hand-off left out
     and every wait bounded by limit_ns: q4q_device_status() then reports Q4Q_ERR_TIMEOUT (6) and the result is incomplete."""
     return _ext.kv_attn(q, cache, page_tokens, n_kv_heads, pages, kv_len, first, None, True, 0, None, None, None, None, path, limit_ns)

@@ -11,15 +11,17 @@ namespace {
 
 constexpr int64_t STEP_TOKENS = 2 * KV_GROUP;      // of the warp-level kernel
 
-// The tcgen05 kernel may take bf16 rows where a sequence has 64 of them or more for a key-value head, on average, and does where
-// its longer start pays: from 1024 keys on (the table's pages bound them), or from 256 rows, a CTA's tiles.  us, warp-level
-// MMAs / tcgen05, heads 32/8 of 128: 16 x 64 rows over 2048 keys 84 / 64, 128 rows over 8192 39 / 33, 64 rows over 8192 28 / 32, 256
-// rows over 8192 63 / 36; 8 x 400 rows over 100 keys 70 / 52, 2 x 128 rows over 300 22 / 36.
+// The tcgen05 kernel may take bf16 and fp16 rows where a sequence has 64 of them or more for a key-value head, on average, and
+// does where its longer start pays: from 256 rows, a CTA's tiles, or from 6 2^20 pairs of a row of queries and a key of the tables,
+// which bound the keys.  us, warp-level MMAs / tcgen05, 8 key-value heads of 128, rows a head: bf16, 64 rows over 8192 keys (4.2 M pairs)
+// 28 / 32, 128 over 8192 39 / 33, 256 over 8192 63 / 36, 16 x 64 over 2048 84 / 64, 2 x 128 over 300 22 / 36, 8 x 400 over 100 70 / 52;
+// fp16, 64 over 1023 18.9 / 26.4, 128 over 8191 69 / 34, 2048 over 8192 891 / 103; 7 x 64 of 12 heads over 1021 35.9 / 35.9.
 bool may_use_tensor_cores(int type, int64_t head_dim, int64_t n_q, int shared, int64_t n_seqs) {
-    return type == Q4Q_TYPE_BF16 && head_dim <= 128 && n_q * shared >= n_seqs * 64;
+    return type != Q4Q_TYPE_F32 && head_dim <= 128 && n_q * shared >= n_seqs * 64;
 }
 bool on_tensor_cores(const AttnArgs& a, int64_t head_dim) {
-    return may_use_tensor_cores(a.type, head_dim, a.n_q, a.shared, a.n_seqs) && ((a.max_pages << a.page_log) >= 1024 || a.n_q * a.shared >= a.n_seqs * 256ll);
+    return may_use_tensor_cores(a.type, head_dim, a.n_q, a.shared, a.n_seqs) &&
+           (a.n_q * a.shared >= a.n_seqs * 256ll || (double)a.n_q * a.heads * (double)(a.max_pages << a.page_log) >= 6.0 * (1 << 20));
 }
 
 size_t workspace_bytes(int type, int64_t head_dim, int64_t n_q, int shared, int64_t n_seqs, const DeviceInfo& info) {
@@ -165,7 +167,7 @@ extern "C" q4q_status q4q_debug_kv_attn_timeout(const void* q, int64_t q_stride,
     a.limit_ns = limit_ns;
     a.fault = 1;
     if (path == 0) return dispatch(a, head_dim, workspace, (cudaStream_t)stream, info);
-    if (type != Q4Q_TYPE_BF16 || head_dim > 128) return Q4Q_ERR_SHAPE;
+    if (type == Q4Q_TYPE_F32 || head_dim > 128) return Q4Q_ERR_SHAPE;
     if (workspace_bytes_given < attn_tc_workspace(head_dim, info)) return Q4Q_ERR_WORKSPACE;
     return attn_tc_run(a, head_dim, workspace, (cudaStream_t)stream, info);
 }

@@ -40,7 +40,7 @@ Q4Q_ATTN_DIM(128)
 Q4Q_ATTN_DIM(256)
 #undef Q4Q_ATTN_DIM
 
-// Prompts on the tcgen05 tensor cores (q4q_attn_tc.cu): bf16, heads of 64, 96 and 128 values.
+// Prompts on the tcgen05 tensor cores (q4q_attn_tc.cu): bf16 and fp16, heads of 64, 96 and 128 values.
 q4q_status attn_tc_run(const AttnArgs& a, int64_t head_dim, void* workspace, cudaStream_t stream, const DeviceInfo& info);
 size_t attn_tc_workspace(int64_t head_dim, const DeviceInfo& info);
 unsigned int attn_tc_take_device_status();

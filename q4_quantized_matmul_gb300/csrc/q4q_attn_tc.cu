@@ -1,11 +1,12 @@
 // q4q_attn_tc.cu -- attention over the paged 4-bit cache on the tcgen05 tensor cores: prompts and chunks of
-// them, bf16, heads of 64, 96 and 128 values.
+// them, bf16 and fp16, heads of 64, 96 and 128 values.
 //
 // The mathematics is that of q4q_attn_kernel.cuh; here many rows of queries share a key, so keys and values are
 // decoded once, to (code - 8) d in fp16 (one rounding, 2^-12 at most; d is at most 8188, so all are finite), and
-// both products are 128 x 128 MMAs of fp16 with fp32 sums in tensor memory.  Queries become fp16 of a power of
+// both products are 128 x 128 MMAs of fp16 with fp32 sums in tensor memory.  (For fp16 queries keys are two operands, exact:
+// rounded, they left results of 128 rows over 4096 keys 9.4e-4 from 64 bits, now 2.8e-4; the results' own rounding is 2.1e-4.)  Queries become fp16 of a power of
 // two times their row (exact but for values below 2^-24 of the row's largest), weights are rounded to fp16:
-// all three are 2^3 below the bf16 result's own rounding.  m moves only when a row's maximum passes it by 2^8.
+// values and weights are 2^3 below a bf16 result's own rounding, and as large as an fp16 result's.  m moves only when a row's maximum passes it by 2^8.
 //
 // A CTA takes 256 rows (tokens x shared heads of a key-value head) as two tiles of 128 rows against steps of 128 keys:
 //   warps 0-3, 4-7   softmax of a tile, a thread a row: S from tensor memory twice (maximum, then weights), P over S,
@@ -23,7 +24,7 @@
 // piece are joined by a second kernel in order.
 //
 // Measured in a graph (heads 32/8 of 128): 512 rows behind 7680 keys 96 us (692 TFLOP/s), 8 such sequences 540 us (985
-// TFLOP/s), two prompts of 2048 with a window of 1024 130 us.  Bound by the softmax: a row's 128 scores are read,
+// TFLOP/s), two prompts of 2048 with a window of 1024 130 us; fp16, with a second product of keys, 103 and 137 us.  Bound by the softmax: a row's 128 scores are read,
 // exponentiated and written back in one thread, and the two tiles' chains fill about half of the tensor cores' time; a piece's
 // start and end cost about 10 us each time, the shares 4.4 us.
 #include "q4q_attn_kernel.cuh"
@@ -44,12 +45,16 @@ static_assert(256 * TC_SOFTMAX_REGS + 256 * TC_DECODE_REGS + 128 * TC_OTHER_REGS
 constexpr int TC_SNAP = 3;               // steps that a share may be longer or shorter, so that it ends with a piece
 constexpr int TC_INFOS = 4;              // steps whose notes are kept: decoders are at most 2 ahead of the softmax
 
-template <int B_>
+template <int B_, typename T_>
 struct Tc {
+    using T = T_;                                                  // of queries and results
     static constexpr int B = B_, DIM = 32 * B;
     static constexpr int ATOMS = (B + 1) / 2;                      // of 64 dims
     static constexpr int Q_BYTES = ATOMS * TC_TILE * 128, V_BYTES = 2 * DIM * 128;
     static constexpr int STAGES = 2;
+    // fp16: keys as two operands that add up to them exactly, (code - 8) times the scale's upper 7 bits and its other 4; where two
+    // stages of both do not fit (heads of 96 and 128), one
+    static constexpr int HALVES = std::is_same_v<T, __half> ? 2 : 1, K_STAGES = HALVES == 1 || B <= 2 ? 2 : 1, K_BYTES = HALVES * Q_BYTES;
     // barriers
     enum { K_FULL = 0, K_EMPTY = K_FULL + STAGES, V_FULL = K_EMPTY + STAGES, V_EMPTY = V_FULL + STAGES, Q_FIRST = V_EMPTY + STAGES, Q_FULL, Q_FREE, S_FULL,
            P_FULL = S_FULL + 2, O_DONE = P_FULL + 2, DRAIN = O_DONE + 2, BARS };
@@ -59,7 +64,7 @@ struct Tc {
     static constexpr int WHICH = 1024;                             // [TC_INFOS][128] bytes: bit b, the key's scale of V's block b is no number
     static constexpr int SCALE = 1536;                             // [2][256] fp32: what a row's scores are multiplied by, of a piece and the next
     static constexpr int Q = 4096;
-    static constexpr int K = Q + 2 * Q_BYTES, V = K + STAGES * Q_BYTES;
+    static constexpr int K = Q + 2 * Q_BYTES, V = K + K_STAGES * K_BYTES;
     static constexpr int BYTES = V + STAGES * V_BYTES + 1024;      // the tiles start on 1024 bytes
     static_assert(WORDS + (TC_THREADS / 32 + 7) * 8 <= GONE && ODD + TC_INFOS * 8 <= WHICH, "small things before the tiles");
     static_assert(K % 1024 == 0 && V % 1024 == 0 && BYTES <= 227 * 1024, "shared memory");
@@ -370,6 +375,7 @@ __device__ __forceinline__ void tc_decode(const AttnArgs& a, TcWalk w, const TcW
     find();
     for (uint32_t steps = 0; here.any; ++steps) {
         const uint32_t stage = steps % C::STAGES, round = steps / C::STAGES, note = steps % TC_INFOS;
+        const uint32_t k_stage = steps % C::K_STAGES, k_round = steps / C::K_STAGES;
         const int key0 = here.g * TC_TILE + d * KV_GROUP, left = here.len - key0;     // of the chunk; its tokens
         const bool gone = !here.chunk;
         here = next;
@@ -377,22 +383,28 @@ __device__ __forceinline__ void tc_decode(const AttnArgs& a, TcWalk w, const TcW
             smem[C::GONE + note * TC_CHUNKS + d] = gone;
             if (gone && left > 0) record_error(&g_attn_status, Q4Q_ERR_ARG);
         }
-        if (round > 0 && !wait(C::K_EMPTY + stage, (round - 1) & 1)) return;
+        if (k_round > 0 && !wait(C::K_EMPTY + k_stage, (k_round - 1) & 1)) return;
         {
-            const uint32_t to = base + C::K + stage * C::Q_BYTES + (d * KV_GROUP + i) * 128;
+            const uint32_t to = base + C::K + k_stage * C::K_BYTES + (d * KV_GROUP + i) * 128;
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int b = 0; b < B; ++b) {
                     const uint32_t s2 = __byte_perm(ks[j][b / 2], 0, b % 2 ? 0x3232 : 0x1010);
                     const uint4 v = nibbles_to_f16x8(kx[j][b]);
-                    sts128(to + (b / 2) * TC_TILE * 128 + j * 1024 + ((((b % 2) * 4 + t) ^ i) << 4), half2_mul(v.x, s2), half2_mul(v.y, s2),
-                           half2_mul(v.z, s2), half2_mul(v.w, s2));
+                    const uint32_t at = to + (b / 2) * TC_TILE * 128 + j * 1024 + ((((b % 2) * 4 + t) ^ i) << 4);
+                    const uint32_t high = C::HALVES == 2 ? s2 & 0xFFF0FFF0u : s2;
+                    sts128(at, half2_mul(v.x, high), half2_mul(v.y, high), half2_mul(v.z, high), half2_mul(v.w, high));
+                    if constexpr (C::HALVES == 2) {
+                        const __half2 rest = __hsub2(*reinterpret_cast<const __half2*>(&s2), *reinterpret_cast<const __half2*>(&high));
+                        const uint32_t low = *reinterpret_cast<const uint32_t*>(&rest);
+                        sts128(at + C::Q_BYTES, half2_mul(v.x, low), half2_mul(v.y, low), half2_mul(v.z, low), half2_mul(v.w, low));
+                    }
                 }
         }
         fence_async();
         __syncwarp();
-        if (lane == 0 && !(a.fault && blockIdx.x == 0 && d == 0 && steps == 0)) wait.arrive(C::K_FULL + stage);
+        if (lane == 0 && !(a.fault && blockIdx.x == 0 && d == 0 && steps == 0)) wait.arrive(C::K_FULL + k_stage);
         load_k(here);
         // Scales of keys that are not there become 0, and so do those that are no number: the softmax marks the rows that see
         // those.
@@ -466,12 +478,12 @@ __device__ __forceinline__ void tc_issue(const AttnArgs& a, TcWalk w, const TcWa
         if (one) mma_commit(wait.bars + bar * 8);
     };
     const auto scores = [&](int i, uint32_t stage) {
-        const uint64_t q = desc_sw128(base + C::Q + i * C::Q_BYTES), k = desc_sw128(base + C::K + stage * C::Q_BYTES);
+        const uint64_t q = desc_sw128(base + C::Q + i * C::Q_BYTES), k = desc_sw128(base + C::K + stage * C::K_BYTES);
         if (one)
 #pragma unroll
-            for (int x = 0; x < 2 * C::B; ++x) {
-                const uint64_t at = ((x / 4) * TC_TILE * 128 + (x % 4) * 32) >> 4;
-                tc_mma_ss(tmem + i * TC_TILE, q + at, k + at, tc_idesc(TC_TILE), x > 0);
+            for (int x = 0; x < 2 * C::B * C::HALVES; ++x) {
+                const uint64_t at = ((x % (2 * C::B) / 4) * TC_TILE * 128 + (x % (2 * C::B) % 4) * 32) >> 4;
+                tc_mma_ss(tmem + i * TC_TILE, q + at, k + at + (x / (2 * C::B)) * (C::Q_BYTES >> 4), tc_idesc(TC_TILE), x > 0);
             }
         __syncwarp();
     };
@@ -490,18 +502,19 @@ __device__ __forceinline__ void tc_issue(const AttnArgs& a, TcWalk w, const TcWa
         const int n = w.g1 - w.g0;
         if (n <= 0) continue;
         // the first step's scores
-        ok = (pieces == 0 ? wait(C::Q_FIRST, 0) : wait(C::Q_FULL, (pieces - 1) & 1)) && wait(C::K_FULL + steps % C::STAGES, (steps / C::STAGES) & 1);
+        ok = (pieces == 0 ? wait(C::Q_FIRST, 0) : wait(C::Q_FULL, (pieces - 1) & 1)) &&
+             wait(C::K_FULL + steps % C::K_STAGES, (steps / C::K_STAGES) & 1);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            scores(i, steps % C::STAGES);
+            scores(i, steps % C::K_STAGES);
             commit(C::S_FULL + i);
         }
-        commit(C::K_EMPTY + steps % C::STAGES);
+        commit(C::K_EMPTY + steps % C::K_STAGES);
         if (n == 1) commit(C::Q_FREE);
         for (int j = 0; j < n && ok; ++j) {
-            const uint32_t at = steps + j, stage = at % C::STAGES, parity = (at / C::STAGES) & 1, next = (at + 1) % C::STAGES;
+            const uint32_t at = steps + j, stage = at % C::STAGES, parity = (at / C::STAGES) & 1, next = (at + 1) % C::K_STAGES;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 ok = ok && wait(C::P_FULL + i, at & 1) && (i > 0 || wait(C::V_FULL + stage, parity));
@@ -512,7 +525,7 @@ __device__ __forceinline__ void tc_issue(const AttnArgs& a, TcWalk w, const TcWa
                     commit(C::O_DONE + i);
                 } else {
                     // behind the product that reads P: MMAs run in the order they were issued in
-                    if (i == 0) ok = wait(C::K_FULL + next, ((at + 1) / C::STAGES) & 1);
+                    if (i == 0) ok = wait(C::K_FULL + next, ((at + 1) / C::K_STAGES) & 1);
                     if (!ok) break;
                     tc_fence_after();
                     scores(i, next);
@@ -552,6 +565,18 @@ __device__ __forceinline__ void tmem_ld_done(uint32_t (&r)[32]) {
 
 template <typename C, typename F>
 __device__ __forceinline__ void tc_rows(const AttnArgs& a, const TcWalk& w, int warp, int warps, uint32_t parity, uint32_t base, uint8_t* smem, F ready);
+
+// Two results in 16 bits each.  fp16: weights rounded up on their own may lift a mean of values of 65504 past its range.
+__device__ __forceinline__ float tc_limited(float x) { return x > 65504.0f ? 65504.0f : x < -65504.0f ? -65504.0f : x; }
+template <typename T>
+__device__ __forceinline__ uint32_t tc_bits(float x, float y) {
+    if constexpr (std::is_same_v<T, __half>) {
+        return half2_bits(tc_limited(x), tc_limited(y));
+    } else {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    }
+}
 
 // The softmax of tile i, a thread a row: queries, weights, and at a piece's end the results.
 template <typename C>
@@ -695,7 +720,7 @@ __device__ __forceinline__ void tc_softmax(const AttnArgs& a, const Plan& plan, 
         if (!complete && tid == 0) plan.parts[part] = {w.p_s, w.p_head, w.p_tile, w.first, w.last, w.of};
         const bool none = ref == NONE && l == 0.0f;                           // scores that are all NaN leave a NaN in l
         const float inv = complete ? (none ? 0.0f : 1.0f / l) : 1.0f;
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.dst) + (at * a.heads + head) * C::DIM;
+        typename C::T* out = static_cast<typename C::T*>(a.dst) + (at * a.heads + head) * C::DIM;
 #pragma unroll 1
         for (int b = 0; b < B; ++b) {
             uint32_t x[32];
@@ -713,10 +738,7 @@ __device__ __forceinline__ void tc_softmax(const AttnArgs& a, const Plan& plan, 
                 for (int k = 0; k < 32; k += 16) {
                     uint32_t h[8];
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        const __nv_bfloat162 y = __floats2bfloat162_rn(v[k + 2 * q], v[k + 2 * q + 1]);
-                        h[q] = *reinterpret_cast<const uint32_t*>(&y);
-                    }
+                    for (int q = 0; q < 8; ++q) h[q] = tc_bits<typename C::T>(v[k + 2 * q], v[k + 2 * q + 1]);
                     if (a.align >= 32) {
                         mx_put<8>(reinterpret_cast<uint8_t*>(out + 32 * b + k), h);
                     } else {
@@ -755,9 +777,9 @@ __device__ __forceinline__ void tc_rows(const AttnArgs& a, const TcWalk& w, int 
     constexpr int LANES = C::B <= 2 ? 8 : 16, ROWS = 32 / LANES, AT_ONCE = 4;
     const int lane = threadIdx.x & 31, u = lane % LANES, rows = w.p_seq.n * a.shared;
     const bool used = u < 4 * C::B;
-    const __nv_bfloat16* const q = static_cast<const __nv_bfloat16*>(a.q) + w.p_seq.q0 * a.q_stride + (int64_t)w.p_head * a.shared * C::DIM + 8 * u;
+    const typename C::T* const q = static_cast<const typename C::T*>(a.q) + w.p_seq.q0 * a.q_stride + (int64_t)w.p_head * a.shared * C::DIM + 8 * u;
     const float scale = fabsf(a.scale_log2), sign = a.scale_log2 < 0.0f ? -1.0f : 1.0f;
-    Raw8<__nv_bfloat16> next[AT_ONCE];
+    Raw8<typename C::T> next[AT_ONCE];
     const auto load = [&](int r0) {
 #pragma unroll
         for (int k = 0; k < AT_ONCE; ++k) {
@@ -769,7 +791,7 @@ __device__ __forceinline__ void tc_rows(const AttnArgs& a, const TcWalk& w, int 
     if (warp * ROWS * AT_ONCE < TC_ROWS) load(warp * ROWS * AT_ONCE);
     ready();
     for (int r0 = warp * ROWS * AT_ONCE; r0 < TC_ROWS; r0 += warps * ROWS * AT_ONCE) {
-        Raw8<__nv_bfloat16> raw[AT_ONCE];
+        Raw8<typename C::T> raw[AT_ONCE];
 #pragma unroll
         for (int k = 0; k < AT_ONCE; ++k) raw[k] = next[k];
         if (r0 + warps * ROWS * AT_ONCE < TC_ROWS) load(r0 + warps * ROWS * AT_ONCE);
@@ -913,15 +935,14 @@ __global__ void __launch_bounds__(TC_JOIN_WARPS * 32) join_tc_kernel(const __gri
     }
     const float inv = ref == -INFINITY ? 0.0f : 1.0f / sum;
     const int64_t at = (int64_t)(seq.q0 + row / a.shared) * a.heads + head * a.shared + row % a.shared;
-    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.dst) + at * C::DIM;
+    uint16_t* out = static_cast<uint16_t*>(a.dst) + at * C::DIM;
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) out[i * 32 + lane] = __float2bfloat16_rn(v[i] * inv);
+    for (int i = 0; i < VEC; ++i) out[i * 32 + lane] = (uint16_t)tc_bits<typename C::T>(v[i] * inv, 0.0f);
     if (lane == 0 && a.lse) a.lse[at] = ref == -INFINITY ? -INFINITY : (ref + log2f(sum)) * 0.69314718055994531f;
 }
 
-template <int B>
+template <typename C>
 q4q_status tc_run(const AttnArgs& a, void* workspace, cudaStream_t stream, const DeviceInfo& info) {
-    using C = Tc<B>;
     const cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES);
     if (e != cudaSuccess) return cudaGetLastError(), Q4Q_ERR_CUDA;
     Plan plan;
@@ -935,6 +956,15 @@ q4q_status tc_run(const AttnArgs& a, void* workspace, cudaStream_t stream, const
     return launch(join_tc_kernel<C>, dim3((unsigned)plan.workers, TC_ROWS / TC_JOIN_WARPS), TC_JOIN_WARPS * 32, 0, stream, a, plan);
 }
 
+template <typename T>
+q4q_status tc_run_type(const AttnArgs& a, int64_t head_dim, void* workspace, cudaStream_t stream, const DeviceInfo& info) {
+    switch (head_dim) {
+        case 64: return tc_run<Tc<2, T>>(a, workspace, stream, info);
+        case 96: return tc_run<Tc<3, T>>(a, workspace, stream, info);
+        default: return tc_run<Tc<4, T>>(a, workspace, stream, info);
+    }
+}
+
 }  // namespace
 
 size_t attn_tc_workspace(int64_t head_dim, const DeviceInfo& info) {
@@ -942,11 +972,8 @@ size_t attn_tc_workspace(int64_t head_dim, const DeviceInfo& info) {
 }
 
 q4q_status attn_tc_run(const AttnArgs& a, int64_t head_dim, void* workspace, cudaStream_t stream, const DeviceInfo& info) {
-    switch (head_dim) {
-        case 64: return tc_run<2>(a, workspace, stream, info);
-        case 96: return tc_run<3>(a, workspace, stream, info);
-        default: return tc_run<4>(a, workspace, stream, info);
-    }
+    return a.type == Q4Q_TYPE_F16 ? tc_run_type<__half>(a, head_dim, workspace, stream, info)
+                                  : tc_run_type<__nv_bfloat16>(a, head_dim, workspace, stream, info);
 }
 
 unsigned int attn_tc_take_device_status() { return attn_take_status_word(); }

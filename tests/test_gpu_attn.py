@@ -14,8 +14,10 @@ within 2^-22 of themselves; codes and scales are exact.
 Rounded to the output's type: half a step more.  lse: e + a few u of its size.  Of bf16 queries the weights are one fp16
 each, every product p_j dv_j within half a step, 2^-11, of itself: sum p_j dv_j 2^-11 |code - 8| <= size 2^-11 more.
 
-Prompts of bf16 (tcgen05): keys and values are rounded to fp16, half a step, 2^-11: scores are off by span 2^-11 and D / 16
-MMAs' 2^-22, values by 2^-11 size; weights, fp16 as well, 2^-11 size more.
+Prompts of bf16 and fp16 (tcgen05): keys and values are rounded to fp16, half a step, 2^-11: scores are off by span 2^-11 and D / 16
+MMAs' 2^-22, values by 2^-11 size; weights, fp16 as well, 2^-11 size more.  Of fp16 queries keys are two exact operands, so scores
+are off by 2 D / 16 MMAs' 2^-22 and a few roundings (queries by 2^-25 of their row's largest: 2^-22 span where their mean
+is an eighth of it or more, as here).
 """
 import numpy as np
 import pytest
@@ -81,12 +83,12 @@ class Case:
 
 def on_tensor_cores(case):
     rows = case.q.shape[0] * (case.heads // case.kv_heads) / len(case.len)
-    return case.type == "bf16" and case.dim <= 128 and rows >= 64 and (case.pages.shape[1] * case.page >= 1024 or rows >= 256)
+    return case.type != "f32" and case.dim <= 128 and rows >= 64 and (rows >= 256 or case.q.shape[0] * case.heads * case.pages.shape[1] * case.page >= 6 << 20)
 
 
 def widened(case):
-    """The same, with a page table of 1024 tokens or more: few rows of prompts then take the tcgen05 kernel too."""
-    more = max(0, -(-1024 // case.page) - case.pages.shape[1])
+    """The same, with a longer page table: few rows of prompts then take the tcgen05 kernel too."""
+    more = max(0, -(-(6 << 20) // (case.q.shape[0] * case.heads * case.page)) - case.pages.shape[1])
     case.pages = np.pad(case.pages, ((0, 0), (0, more)), constant_values=-1)
     return case
 
@@ -95,9 +97,9 @@ def bounds(case, size, span, o):
     """(of the outputs, of lse) by the derivations above."""
     u = 2.0 ** -22
     if on_tensor_cores(case):
-        e = span * (2.0 ** -11 + case.dim // 16 * u)
+        e = span * ((2.0 ** -11 + case.dim // 16 * u) if case.type == "bf16" else (case.dim // 8 + 4) * u)
         tol = size * (2 * e + span * u + 2.0 ** -10 + (12 + int(case.len.max()) / 16 + 160) * u)[..., None]
-        return tol + np.abs(o) * 2.0 ** -8 + 2.0 ** -25, 2 * e + 200 * u
+        return tol + np.abs(o) * torch.finfo(TYPES[case.type]).eps / 2 + 2.0 ** -25, 2 * e + 200 * u
     e = span * (2 + 2 * (case.dim // 32 + 4)) * u
     steps = 12 + int(case.len.max()) / 16 + 160
     tol = size * (2 * e + span * u + steps * u + (2.0 ** -11 if case.type == "bf16" else 0.0))[..., None]
@@ -149,9 +151,10 @@ def test_ragged_rows_and_windows(q4q, type, lengths, rows, window):
 @pytest.mark.parametrize("heads,kv_heads,lengths,rows", [(4, 1, [40], [32]), (2, 1, [300], [150]), (1, 1, [129], [128]), (8, 2, [700], [65]),
                                                          (6, 2, [200, 1, 513], [190, 1, 300]), (3, 3, [1000, 10], [260, 10])])
 @pytest.mark.parametrize("window", [0, 100])
-def test_prompts(q4q, dim, heads, kv_heads, lengths, rows, window):
-    """bf16 rows enough for the tcgen05 tiles: ragged last tiles of rows and keys, pieces cut between CTAs."""
-    case = widened(Case([dim, heads, window], lengths, rows, heads, kv_heads, dim, 16 if dim == 96 else 64, "bf16"))
+@pytest.mark.parametrize("type", ["f16", "bf16"])
+def test_prompts(q4q, dim, heads, kv_heads, lengths, rows, window, type):
+    """16-bit rows enough for the tcgen05 tiles: ragged last tiles of rows and keys, pieces cut between CTAs."""
+    case = widened(Case([dim, heads, window], lengths, rows, heads, kv_heads, dim, 16 if dim == 96 else 64, type))
     assert on_tensor_cores(case)
     got, lse = case.run(q4q, lse=True, window=window)
     check(case, got, lse, window=window)
@@ -161,7 +164,8 @@ def test_prompts(q4q, dim, heads, kv_heads, lengths, rows, window):
 
 @pytest.mark.parametrize("lengths,rows", [([2048, 1126], [2048, 1126]), ([5000, 300, 2100], [1500, 300, 2100]), ([700] * 24, [333] * 24)])
 @pytest.mark.parametrize("window", [0, 500])
-def test_prompts_of_many_pieces(q4q, lengths, rows, window):
+@pytest.mark.parametrize("type", ["f16", "bf16"])
+def test_prompts_of_many_pieces(q4q, lengths, rows, window, type):
     """Every CTA has several pieces, some of a step, and shares that end with a piece near by: against the kernel of fp32 rows, which the
     other tests hold to the reference.  The bound is the derivation's with the largest of each factor: 8 d <= amax (1 + 2^-10)."""
     heads, kv_heads, dim, page = 32, 8, 64, 64
@@ -180,7 +184,7 @@ def test_prompts_of_many_pieces(q4q, lengths, rows, window):
         q4q.q4q_kv_append(cache, page, k, v, (pages[s].long()[j // page] * page + j % page).int())
         amax = [max(amax[0], float(k.abs().max())), max(amax[1], float(v.abs().max()))]
     first = torch.tensor([0] + rows, device="cuda").cumsum(0).int()
-    q = (0.5 * torch.randn(sum(rows), heads, dim, generator=g, device="cuda")).bfloat16()
+    q = (0.5 * torch.randn(sum(rows), heads, dim, generator=g, device="cuda")).to(TYPES[type])
     args = (cache, page, kv_heads, pages, torch.tensor(lengths, dtype=torch.int32, device="cuda"))
     want = q4q.q4q_kv_attn(q.float(), *args, first=first, window=window)
     got = q4q.q4q_kv_attn(q, *args, first=first, window=window, dst=torch.full_like(q, float("nan")))
@@ -189,6 +193,19 @@ def test_prompts_of_many_pieces(q4q, lengths, rows, window):
     # and closely where it counts: rounding errors are as good as independent, so far smaller over a whole head
     assert float((got.float() - want).norm() / want.norm()) < 2.0 ** -8
     assert q4q.q4q_device_status() == 0
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_prompts_of_the_largest_values(q4q, sign):
+    """All values fp16's largest: their means stay within its range."""
+    case = widened(Case(34, [400], [150], 4, 2, 64, 16, "f16"))
+    j = np.arange(400)
+    k = np.random.default_rng(34).standard_normal((400, 2, 64)).astype(np.float32)
+    ref.put(case.cache, 16, case.pages[0][j // 16] * 16 + j % 16, k, np.full_like(k, -65504.0 * sign))
+    assert on_tensor_cores(case)
+    got = case.run(q4q)
+    assert torch.isfinite(got).all()
+    check(case, got)
 
 
 def test_prompts_where_rows_see_nothing(q4q):
@@ -522,7 +539,7 @@ def test_prompts_of_many_sequences(q4q):
     assert q4q.q4q_device_status() == 0
 
 
-@pytest.mark.parametrize("rows,type", [(1, "f32"), (3, "f16"), (9, "bf16"), (80, "bf16")])
+@pytest.mark.parametrize("rows,type", [(1, "f32"), (3, "f16"), (9, "bf16"), (80, "bf16"), (80, "f16")])
 def test_rows_of_nan_and_keys_of_nan(q4q, rows, type):
     """A row whose query is NaN is NaN, and the others are right; so is every row where all keys are NaN."""
     case, case2 = (widened(Case([44, rows], [200, 90], [rows, rows], 4, 2, 64, 16, type)) for _ in range(2))
