@@ -6,7 +6,10 @@
 // both products are 128 x 128 MMAs of fp16 with fp32 sums in tensor memory.  (For fp16 queries keys are two operands, exact:
 // rounded, they left results of 128 rows over 4096 keys 9.4e-4 from 64 bits, now 2.8e-4; the results' own rounding is 2.1e-4.)  Queries become fp16 of a power of
 // two times their row (exact but for values below 2^-24 of the row's largest), weights are rounded to fp16:
-// values and weights are 2^3 below a bf16 result's own rounding, and as large as an fp16 result's.  m moves only when a row's maximum passes it by 2^8.
+// values and weights are 2^3 below a bf16 result's own rounding, and as large as an fp16 result's.  The weight of the maximum that a row
+// refers to is 2^7, and the reference moves only when a maximum passes it by 2^8, so the largest weight is between 2^7 and fp16's
+// range, and weights down to 2^-21 of it are normal numbers, others multiples of 2^-31 of it.  (With a weight of 1 those of 2^-14 were the last:
+// where a first key without a value outweighs 499 others by 2^20, bf16 results of the others were 1.7e-2 from 64 bits.)
 //
 // A CTA takes 256 rows (tokens x shared heads of a key-value head) as two tiles of 128 rows against steps of 128 keys:
 //   warps 0-3, 4-7   softmax of a tile, a thread a row: S from tensor memory twice (maximum, then weights), P over S,
@@ -43,6 +46,7 @@ constexpr int TC_THREADS = (TC_ISSUER + 1 + TC_LOADERS) * 32;
 constexpr int TC_REGS = 96, TC_SOFTMAX_REGS = 128, TC_DECODE_REGS = 80, TC_OTHER_REGS = 64;
 static_assert(256 * TC_SOFTMAX_REGS + 256 * TC_DECODE_REGS + 128 * TC_OTHER_REGS <= TC_THREADS * TC_REGS, "registers of the launch");
 constexpr int TC_SNAP = 3;               // steps that a share may be longer or shorter, so that it ends with a piece
+constexpr float TC_TOP = 7.0f, TC_LAG = 8.0f;   // log2 of the weight of the maximum referred to; how far a maximum may pass it
 constexpr int TC_INFOS = 4;              // steps whose notes are kept: decoders are at most 2 ahead of the softmax
 
 template <int B_, typename T_>
@@ -595,7 +599,7 @@ __device__ __forceinline__ void tc_softmax(const AttnArgs& a, const Plan& plan, 
         int lo, hi;
         keys_of(a, seq, row, lo, hi);
         const int lo_all = __reduce_max_sync(0xffffffffu, lo), hi_all = __reduce_min_sync(0xffffffffu, hi);
-        float scale = 0.0f, ref = NONE, l = 0.0f;
+        float scale = 0.0f, ref = NONE, l = 0.0f;                            // weights are exp2(score - ref)
         uint32_t poison = 0;                                                  // blocks in which the row sees a value that is no number
         // Blocks of values that are no number, of keys of a step that this row sees.  The step's values are decoded by the time of
         // the next step's scores, or of the result.
@@ -656,8 +660,8 @@ __device__ __forceinline__ void tc_softmax(const AttnArgs& a, const Plan& plan, 
             else maximum(std::false_type{});
             const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
             const float y = most == -INFINITY ? -INFINITY : most * scale;
-            if (__any_sync(0xffffffffu, y > ref + 8.0f)) {
-                const float to_ref = y > ref + 8.0f ? y : ref, down = exp2f(ref - to_ref);
+            if (__any_sync(0xffffffffu, y > ref + (TC_TOP + TC_LAG))) {
+                const float to_ref = y > ref + (TC_TOP + TC_LAG) ? y - TC_TOP : ref, down = exp2f(ref - to_ref);
                 ref = to_ref;
                 l *= down;
                 // this step's scores are there, so the products issued before them are done with the sums

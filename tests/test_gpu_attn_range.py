@@ -1,0 +1,75 @@
+"""Attention over the cache where weights or values of a row's keys lie far apart, against oracle/attn.py (64 bits).
+
+The bounds are those of test_gpu_attn.  Where outputs are means of many values of either sign, a bound by the sum of their sizes is loose; there the
+2-norm of a whole head's error is held to its result's.  Rounding errors of weights, values and results are independent, each
+within half a step, h = 2^-11 of fp16 or 2^-8 of bf16, uniform in it, so of root mean square h / sqrt(3) at most; the sum of
+three of them (weights, values, result) is below sqrt(3) max(h) / sqrt(3): the limit is 2 h of the results' type.
+"""
+import numpy as np
+import pytest
+
+from oracle import attn as ref
+from test_gpu_attn import Case, TYPES, check, on_tensor_cores, q4q, widened  # noqa: F401
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+def put(case, s, k, v):
+    j = np.arange(len(k))
+    ref.put(case.cache, case.page, case.pages[s][j // case.page] * case.page + j % case.page, k.astype(np.float32), v.astype(np.float32))
+
+
+def with_sink(seed, n, rows, heads, kv_heads, dim, type, nats):
+    """The first key weighs exp(nats) times as much as the others do at a score of zero, and its value is zero."""
+    case = Case(seed, [n], [rows], heads, kv_heads, dim, 16, type)
+    rng = np.random.default_rng(seed)
+    k, v = rng.standard_normal((n, kv_heads, dim)) / 4, rng.standard_normal((n, kv_heads, dim))
+    k[:, :, 32:64] = 0
+    k[0], v[0] = 0, 0
+    # -1 in block 1 of each query: a key of -c there, which is a code of its own, scores 32 c / sqrt(D)
+    k[0, :, 32:64] = -np.float16(nats * dim ** 0.5 / 32)
+    put(case, 0, k, v)
+    case.q[:, :, 32:64] = -1
+    return case
+
+
+def norm_error(got, want):
+    """Of each head: the error's 2-norm over the result's."""
+    e = got.double().cpu().numpy() - want
+    return np.sqrt((e * e).sum((0, 2)) / (want * want).sum((0, 2)))
+
+
+@pytest.mark.parametrize("dim", [64, 96, 128])
+@pytest.mark.parametrize("type", ["f16", "bf16"])
+def test_prompts_whose_first_key_outweighs_the_rest(q4q, dim, type):
+    """By 2^20: weights of the rest are still normal numbers in fp16."""
+    case = widened(with_sink(dim, 500, 200, 4, 2, dim, type, 20 * np.log(2)))
+    assert on_tensor_cores(case)
+    got, lse = case.run(q4q, lse=True)
+    check(case, got, lse)
+    # the first row sees 301 keys
+    assert norm_error(got, case.want()[0]).max() <= torch.finfo(TYPES[type]).eps
+    assert q4q.q4q_device_status() == 0
+
+
+@pytest.mark.parametrize("type", ["f16", "bf16"])
+def test_prompts_whose_first_key_outweighs_4096_others(q4q, type):
+    """By 2^26, each of the others' values 1: their share of 2^-14 is the result.  As many sequences, all of the same tokens, as leave
+    most pieces whole."""
+    n, seqs, rows, heads, dim, page = 4097, 38, 64, 4, 64, 64
+    pages = torch.arange(-(-n // page), dtype=torch.int32, device="cuda").repeat(seqs, 1)
+    cache = torch.zeros((pages.shape[1], q4q.q4q_kv_page_size(heads, dim, page)), dtype=torch.uint8, device="cuda")
+    k, v = torch.zeros(n, heads, dim, device="cuda"), -torch.ones(n, heads, dim, device="cuda")
+    c = float(np.float16(26 * np.log(2) / 4))                  # scores 32 c / 8
+    k[0, :, 32:], v[0] = -c, 0
+    q4q.q4q_kv_append(cache, page, k, v, torch.arange(n, dtype=torch.int32, device="cuda"))
+    q = torch.zeros(seqs * rows, heads, dim, dtype=TYPES[type], device="cuda")
+    q[..., 32:] = -1
+    lse = torch.empty(seqs * rows, heads, device="cuda")
+    got = q4q.q4q_kv_attn(q, cache, page, heads, pages, torch.full((seqs,), n, dtype=torch.int32, device="cuda"),
+                          first=torch.arange(0, seqs * rows + 1, rows, dtype=torch.int32, device="cuda"), causal=False, lse=lse)
+    share = 4096 / (4096 + np.exp(4 * c))
+    # weights of 2^-26 of the first key's are within 2^-32 of it, 2^-6 of themselves
+    assert float((got.double() + share).abs().max()) <= share * (2.0 ** -6 + torch.finfo(TYPES[type]).eps)
+    assert float((lse.double() - (4 * c + np.log1p(4096 * np.exp(-4 * c)))).abs().max()) <= 1e-4
