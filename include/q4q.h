@@ -647,12 +647,12 @@ Q4Q_API q4q_status q4q_kv_attn_workspace_size(int64_t n_q, int n_q_heads, int n_
  * A row that sees no key gets zeros, and -inf in lse (fp32 [n_q][n_q_heads], natural logarithm of the
  * sum of exp(scale <q, K_j>); NULL: not written).  Rows of q that belong to no sequence are neither
  * read nor written.  Keys that a row does not see take no part, whatever their bytes hold.
- * Sums and statistics are fp32, scales are applied in fp32 and codes are exact.  fp32 and fp16
+ * Sums and statistics are fp32, codes and scales of keys count exactly.  fp32 and fp16
  * queries and their weights count with 22 bits; weights of bf16 queries are rounded to fp16.  bf16
  * and fp16 prompts of 64 rows a key-value head and more, heads up to 128, may run on the tcgen05
- * tensor cores, where values and weights, and for bf16 keys, are rounded to fp16 (scales above 8188, which q4q_kv_append
- * does not write, would pass its range).  A NaN in a row's query, or in scales of keys that it sees,
- * gives NaN.
+ * tensor cores, where values and weights are rounded to fp16 (weights below 2^-21 of the largest that a row refers
+ * to: to multiples of 2^-31 of it; scales above 8188, which q4q_kv_append does not write, would pass its range).
+ * A NaN in a row's query, or in scales of keys that it sees, gives NaN.
  * q: device, type, [n_q][n_q_heads][head_dim] at q_stride; dst: contiguous, of the same type, not
  * overlapping q (Q4Q_ERR_ARG); cache, pages int32 [n_seqs][max_pages], kv_len int32 [n_seqs], first int32
  * [n_seqs + 1], ascending: device.  kv_len beyond max_pages pages counts as that many, and a page

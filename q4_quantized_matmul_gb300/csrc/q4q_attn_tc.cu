@@ -2,9 +2,11 @@
 // them, bf16 and fp16, heads of 64, 96 and 128 values.
 //
 // The mathematics is that of q4q_attn_kernel.cuh; here many rows of queries share a key, so keys and values are
-// decoded once, to (code - 8) d in fp16 (one rounding, 2^-12 at most; d is at most 8188, so all are finite), and
-// both products are 128 x 128 MMAs of fp16 with fp32 sums in tensor memory.  (For fp16 queries keys are two operands, exact:
-// rounded, they left results of 128 rows over 4096 keys 9.4e-4 from 64 bits, now 2.8e-4; the results' own rounding is 2.1e-4.)  Queries become fp16 of a power of
+// decoded once, and both products are 128 x 128 MMAs of fp16 with fp32 sums in tensor memory.  Keys are two operands that add up to (code - 8) d
+// exactly: as one, rounded to fp16 (2^-12), they moved the weights by that much of a score: bf16 rows whose scores spread over 6 nats were
+// 1.91e-3 from 64 bits (512 rows over 8192 keys), now 1.66e-3, of which
+// their results' own rounding is 1.64e-3.  The second product costs 96.6 -> 103 us there, 540 -> 587 for 8 such sequences.  Values are
+// (code - 8) d in fp16 (one rounding, 2^-12 at most; d is at most 8188, so all are finite).  Queries become fp16 of a power of
 // two times their row (exact but for values below 2^-24 of the row's largest), weights are rounded to fp16:
 // values and weights are 2^3 below a bf16 result's own rounding, and as large as an fp16 result's.  The weight of the maximum that a row
 // refers to is 2^7, and the reference moves only when a maximum passes it by 2^8, so the largest weight is between 2^7 and fp16's
@@ -26,8 +28,8 @@
 // Steps of all pieces (sequence, head, 256 rows) in a row are cut into equal shares, one a CTA and SM; parts of a
 // piece are joined by a second kernel in order.
 //
-// Measured in a graph (heads 32/8 of 128): 512 rows behind 7680 keys 96 us (692 TFLOP/s), 8 such sequences 540 us (985
-// TFLOP/s), two prompts of 2048 with a window of 1024 130 us; fp16, with a second product of keys, 103 and 137 us.  Bound by the softmax: a row's 128 scores are read,
+// Measured in a graph (heads 32/8 of 128): bf16, 512 rows behind 7680 keys 103 us (647 TFLOP/s), 8 such sequences 587 us (907
+// TFLOP/s), two prompts of 2048 with a window of 1024 135 us; fp16 104 and 137 us.  Bound by the softmax: a row's 128 scores are read,
 // exponentiated and written back in one thread, and the two tiles' chains fill about half of the tensor cores' time; a piece's
 // start and end cost about 10 us each time, the shares 4.4 us.
 #include "q4q_attn_kernel.cuh"
@@ -56,9 +58,9 @@ struct Tc {
     static constexpr int ATOMS = (B + 1) / 2;                      // of 64 dims
     static constexpr int Q_BYTES = ATOMS * TC_TILE * 128, V_BYTES = 2 * DIM * 128;
     static constexpr int STAGES = 2;
-    // fp16: keys as two operands that add up to them exactly, (code - 8) times the scale's upper 7 bits and its other 4; where two
-    // stages of both do not fit (heads of 96 and 128), one
-    static constexpr int HALVES = std::is_same_v<T, __half> ? 2 : 1, K_STAGES = HALVES == 1 || B <= 2 ? 2 : 1, K_BYTES = HALVES * Q_BYTES;
+    // Keys as two operands, (code - 8) times the scale's upper 7 bits and its other 4; where two stages of both do not fit
+    // (heads of 96 and 128), one.
+    static constexpr int K_STAGES = B <= 2 ? 2 : 1, K_BYTES = 2 * Q_BYTES;
     // barriers
     enum { K_FULL = 0, K_EMPTY = K_FULL + STAGES, V_FULL = K_EMPTY + STAGES, V_EMPTY = V_FULL + STAGES, Q_FIRST = V_EMPTY + STAGES, Q_FULL, Q_FREE, S_FULL,
            P_FULL = S_FULL + 2, O_DONE = P_FULL + 2, DRAIN = O_DONE + 2, BARS };
@@ -397,13 +399,11 @@ __device__ __forceinline__ void tc_decode(const AttnArgs& a, TcWalk w, const TcW
                     const uint32_t s2 = __byte_perm(ks[j][b / 2], 0, b % 2 ? 0x3232 : 0x1010);
                     const uint4 v = nibbles_to_f16x8(kx[j][b]);
                     const uint32_t at = to + (b / 2) * TC_TILE * 128 + j * 1024 + ((((b % 2) * 4 + t) ^ i) << 4);
-                    const uint32_t high = C::HALVES == 2 ? s2 & 0xFFF0FFF0u : s2;
+                    const uint32_t high = s2 & 0xFFF0FFF0u;
                     sts128(at, half2_mul(v.x, high), half2_mul(v.y, high), half2_mul(v.z, high), half2_mul(v.w, high));
-                    if constexpr (C::HALVES == 2) {
-                        const __half2 rest = __hsub2(*reinterpret_cast<const __half2*>(&s2), *reinterpret_cast<const __half2*>(&high));
-                        const uint32_t low = *reinterpret_cast<const uint32_t*>(&rest);
-                        sts128(at + C::Q_BYTES, half2_mul(v.x, low), half2_mul(v.y, low), half2_mul(v.z, low), half2_mul(v.w, low));
-                    }
+                    const __half2 rest = __hsub2(*reinterpret_cast<const __half2*>(&s2), *reinterpret_cast<const __half2*>(&high));
+                    const uint32_t low = *reinterpret_cast<const uint32_t*>(&rest);
+                    sts128(at + C::Q_BYTES, half2_mul(v.x, low), half2_mul(v.y, low), half2_mul(v.z, low), half2_mul(v.w, low));
                 }
         }
         fence_async();
@@ -485,7 +485,7 @@ __device__ __forceinline__ void tc_issue(const AttnArgs& a, TcWalk w, const TcWa
         const uint64_t q = desc_sw128(base + C::Q + i * C::Q_BYTES), k = desc_sw128(base + C::K + stage * C::K_BYTES);
         if (one)
 #pragma unroll
-            for (int x = 0; x < 2 * C::B * C::HALVES; ++x) {
+            for (int x = 0; x < 4 * C::B; ++x) {
                 const uint64_t at = ((x % (2 * C::B) / 4) * TC_TILE * 128 + (x % (2 * C::B) % 4) * 32) >> 4;
                 tc_mma_ss(tmem + i * TC_TILE, q + at, k + at + (x / (2 * C::B)) * (C::Q_BYTES >> 4), tc_idesc(TC_TILE), x > 0);
             }

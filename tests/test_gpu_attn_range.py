@@ -3,7 +3,9 @@
 The bounds are those of test_gpu_attn.  Where outputs are means of many values of either sign, a bound by the sum of their sizes is loose; there the
 2-norm of a whole head's error is held to its result's.  Rounding errors of weights, values and results are independent, each
 within half a step, h = 2^-11 of fp16 or 2^-8 of bf16, uniform in it, so of root mean square h / sqrt(3) at most; the sum of
-three of them (weights, values, result) is below sqrt(3) max(h) / sqrt(3): the limit is 2 h of the results' type.
+three of them (weights, values, result) is below sqrt(3) max(h) / sqrt(3): the limit is 2 h of the results' type.  lse is as
+good as the scores, which are sums in fp32 of exact products: D / 8 + 4 roundings or cuts, 2^-22 of what has been summed, which stays near
+the largest score.
 """
 import numpy as np
 import pytest
@@ -73,3 +75,19 @@ def test_prompts_whose_first_key_outweighs_4096_others(q4q, type):
     # weights of 2^-26 of the first key's are within 2^-32 of it, 2^-6 of themselves
     assert float((got.double() + share).abs().max()) <= share * (2.0 ** -6 + torch.finfo(TYPES[type]).eps)
     assert float((lse.double() - (4 * c + np.log1p(4096 * np.exp(-4 * c)))).abs().max()) <= 1e-4
+
+
+@pytest.mark.parametrize("dim", [64, 96, 128])
+@pytest.mark.parametrize("type", ["f16", "bf16"])
+def test_prompts_of_scores_that_spread(q4q, dim, type):
+    """Scores of 20 nats' spread: their weights count as exactly as they do."""
+    case = widened(Case(dim, [400], [200], 4, 2, dim, 16, type))
+    rng = np.random.default_rng(dim)
+    put(case, 0, 4.5 * rng.standard_normal((400, 2, dim)), rng.standard_normal((400, 2, dim)))
+    case.q = 4.5 * case.q
+    assert on_tensor_cores(case)
+    got, lse = case.run(q4q, lse=True)
+    o, want = case.want()[:2]
+    e = lse.double().cpu().numpy() - want
+    assert np.sqrt((e * e).mean()) <= (dim // 8 + 4) * 2.0 ** -22 * np.abs(want).max() + 2.0 ** -18
+    assert norm_error(got, o).max() <= torch.finfo(TYPES[type]).eps
