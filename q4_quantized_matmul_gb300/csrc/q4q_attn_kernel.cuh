@@ -20,9 +20,14 @@
 //    divided by 16, and -8 sum q is what the sum starts from (5 operations for 8).  The tensor cores align a
 //    subnormal by its nominal exponent, which costs about 7 bits: scores are good to 1e-5.
 //    Value codes are always centred: an offset left in sums over many keys would be far larger than they.
-//  - Weights are exp2(s - m - E + 8) with E the largest exponent of the values' scales so far: p dv is
-//    at most 2^8, and m and E move only when something passes them by 2^6, which a vote over
-//    the warp finds; sums are rescaled only then.
+//  - Weights are p = exp2(s - r).  r is a row's: it makes the largest product p dv so far 2^7 to 2^15, which is what goes into
+//    the second MMA.  A block of 32 dims whose products are below 2^2 there has a unit of its own, a power of two u that p dv u is taken
+//    with, so that a product counts to 2^-27 of the largest of its row and block, whatever values other blocks or rows have, or keys without
+//    weight.  (One exponent for a warp, of the largest scale of any key, left scales 2^10 below that 2.4e-3 from 64 bits.)
+//    Every step a lane compares its largest score and scale with 2^15, and a vote over the warp finds where one is past it; only then
+//    r and u move and sums are rescaled: by the largest score where the step's scales are near each other, else by the products
+//    themselves.  r is a score less a whole number: that key's weight is a power of two, its product exact.  (64 bf16 tokens over 8192
+//    keys at most: 96 us with the one exponent, 98 so; 101 with the products looked at each time, 109 with units read in every step.)
 //
 // Work.  All steps (two chunks of 16 tokens of a head, 2304 bytes each at D = 128) of all pieces -- a sequence, head and
 // tile of rows -- in a row are cut into equal shares, one a CTA, two CTAs an SM, so a ragged batch or one long
@@ -31,8 +36,8 @@
 // shared memory; what a CTA leaves of a piece to others goes to the workspace as sums with m and l, and
 // a second kernel joins the parts in order.
 //
-// Measured in a graph (heads 32/8 of 128): one fp32 token over 1023 keys 13.3 us (launches, shares, a piece's end and the
-// join); over 131072 keys, fp16, 47 us (151 MB, 3.2 TB/s); 64 bf16 tokens over 8192 keys at most 96 us (337 MB, 3.5 TB/s).
+// Measured in a graph (heads 32/8 of 128): one fp32 token over 1023 keys 13.9 us (launches, shares, a piece's end and the
+// join); over 131072 keys, fp16, 47 us (151 MB, 3.2 TB/s); 64 bf16 tokens over 8192 keys at most 98 us (337 MB, 3.4 TB/s).
 // Bound by issue: some 300 instructions a chunk of 16 keys and warp, the ALU pipe about half busy with the codes.
 #pragma once
 
@@ -79,7 +84,8 @@ struct Cfg {
     static constexpr int MISC = META + SLOTS * 8;      // scan and broadcast words
     static constexpr int STOP = MISC + 248;            // the abort flag
     static constexpr int STATS = MISC + 256;           // [CONSUMERS][ROWS] reference and sum
-    static constexpr int RING = (STATS + CONSUMERS * ROWS * 8 + 127) / 128 * 128;
+    static constexpr int UNITS = STATS + CONSUMERS * ROWS * 8;   // [CONSUMERS][2][NG][B][4 t] two fp32, of columns 2t, 2t + 1: units, what sums are multiplied by
+    static constexpr int RING = (UNITS + CONSUMERS * NG * B * 64 + 127) / 128 * 128;
     static constexpr int OUT = RING + SLOTS * 2 * CHUNK;
     static constexpr int BYTES = OUT + CONSUMERS * ROWS * OUT_STRIDE * 4;
     static_assert(SLOTS <= 16, "a lane of the producer for each half of a slot");
@@ -257,6 +263,28 @@ __device__ __forceinline__ float scale_at(const uint32_t (&w)[W], int i) {
 
 // 2^e as fp32, -126 <= e <= 127
 __device__ __forceinline__ float two_to(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+// of a normal number above 0
+__device__ __forceinline__ int exponent_of(float x) { return (int)(__float_as_uint(x) >> 23) - 127; }
+
+// Products with a row's reference and a block's unit are at most UNIT_MOST; where they move they make the largest at least
+// 2^UNIT_BITS.  Weights are at most 2^WEIGHT_BITS (of rows whose values are all 0, or next to it).
+constexpr int UNIT_BITS = 7, WEIGHT_BITS = 90;
+constexpr float UNIT_MOST = 32768.0f, UNIT_LEAST = 4.0f;
+__device__ __forceinline__ void pair_load(uint32_t addr, float& x, float& y) {
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(x), "=f"(y) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ float word_load(uint32_t addr) {
+    float x;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(addr) : "memory");
+    return x;
+}
+__device__ __forceinline__ void word_store(uint32_t addr, float x) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(x) : "memory"); }
+
+// the larger of the magnitudes of two fp16 pairs (a NaN gives way)
+__device__ __forceinline__ uint32_t largest2(uint32_t a, uint32_t b) {
+    const __half2 m = __hmax2(__habs2(*reinterpret_cast<const __half2*>(&a)), __habs2(*reinterpret_cast<const __half2*>(&b)));
+    return *reinterpret_cast<const uint32_t*>(&m);
+}
 
 // whether the phase is complete, without the wait that try_wait may take
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
@@ -445,6 +473,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_kernel(const __grid_
         return;
     }
 
+    const uint32_t units = base + C::UNITS + warp * NG * B * 64 + t * 8, downs = units + NG * B * 32;     // + (q * B + b) * 32
     float2* stats = reinterpret_cast<float2*>(smem + C::STATS);
     float* out = reinterpret_cast<float*>(smem + C::OUT);
     int numbered = 0;                                // steps of this CTA before the piece's
@@ -526,10 +555,10 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_kernel(const __grid_
             for (int b = 0; b < B; ++b)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) o[q][b][i / 4][i % 4] = 0.0f;
-        float m[NG][2], l[NG][2], ref[NG][2];        // of columns 2t, 2t + 1: the maximum referred to; this lane's sum; m + E - 8
+        float ref[NG][2], l[NG][2];                  // of columns 2t, 2t + 1; l: this lane's sum
 #pragma unroll
-        for (int q = 0; q < NG; ++q) m[q][0] = m[q][1] = -INFINITY, ref[q][0] = ref[q][1] = NONE, l[q][0] = l[q][1] = 0.0f;
-        int top_e = -32;                             // E: the values' scales are below 2^E
+        for (int q = 0; q < NG; ++q) ref[q][0] = ref[q][1] = NONE, l[q][0] = l[q][1] = 0.0f;
+        bool mixed = false;                          // some block of some row has a unit of its own
 
         const int start = warp + CONSUMERS * taken - numbered;
         for (int i = start; i < steps && !dead; i += CONSUMERS, ++taken) {
@@ -632,49 +661,150 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_kernel(const __grid_
                 // a scale that is no number, in a step that not every row sees: weights of 0 have to stay 0
                 careful = __any_sync(0xffffffffu, odd != 0);
             }
-            uint32_t bits = 0;
+            float x[NG][8], top[NG][2];
 #pragma unroll
-            for (int k = 0; k < W; ++k) bits = __vmaxu2(__vmaxu2(bits, __vmaxu2(dv[0][k], dv[1][k])), __vmaxu2(dv[2][k], dv[3][k]));
+            for (int q = 0; q < NG; ++q) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) x[q][k] = y[q][k] - ref[q][k & 1];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) top[q][c] = fmaxf(fmaxf(x[q][c], x[q][2 + c]), fmaxf(x[q][4 + c], x[q][6 + c]));
+            }
+            float most = top[0][0];
+#pragma unroll
+            for (int q = 0; q < NG; ++q) most = fmaxf(most, fmaxf(top[q][0], top[q][1]));
+            uint32_t dm[W];                                                        // each block's largest scale of this lane's keys
+#pragma unroll
+            for (int k = 0; k < W; ++k) dm[k] = largest2(largest2(dv[0][k], dv[1][k]), largest2(dv[2][k], dv[3][k]));
+            uint32_t bits = dm[0];
+#pragma unroll
+            for (int k = 1; k < W; ++k) bits = __vmaxu2(bits, dm[k]);
             bits = max(bits >> 16, bits & 0xFFFFu);
-            bool grows = (int)(bits >> 10) - 14 > top_e;                           // a scale is below 2^(exponent field - 14)
-            float x[NG][8], most = -INFINITY;
-#pragma unroll
-            for (int q = 0; q < NG; ++q)
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    x[q][k] = y[q][k] - ref[q][k & 1];
-                    most = fmaxf(most, x[q][k]);
-                }
-            grows |= most > (float)(14 - top_e);                                   // a y > m + 6
-            if (__any_sync(0xffffffffu, grows)) {
-                // an infinite or NaN scale makes its own dims so, and says nothing about the others'
-                uint32_t finite = 0;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int k = 0; k < W; ++k) {
-                        const uint32_t h0 = dv[j][k] & 0x7FFFu, h1 = (dv[j][k] >> 16) & 0x7FFFu;
-                        finite = max(finite, max(h0 < 0x7C00u ? h0 : 0u, h1 < 0x7C00u ? h1 : 0u));
-                    }
-                const int e = max(top_e, (int)(__reduce_max_sync(0xffffffffu, finite) >> 10) - 14);
+            bool past = most > (float)min(29 - (int)(bits >> 10), WEIGHT_BITS);    // a scale is below 2^(exponent field - 14)
+            if (mixed) {
 #pragma unroll
                 for (int q = 0; q < NG; ++q)
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        float n = fmaxf(fmaxf(y[q][c], y[q][2 + c]), fmaxf(y[q][4 + c], y[q][6 + c]));
-                        n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, 4));
-                        n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, 8));
-                        n = fmaxf(m[q][c], fmaxf(n, __shfl_xor_sync(0xffffffffu, n, 16)));
-                        const float down = m[q][c] == -INFINITY ? 0.0f : exp2f((m[q][c] - n) + (float)(top_e - e));
-                        m[q][c] = n;
-                        ref[q][c] = n == -INFINITY ? NONE : n + (float)(e - 8);
-                        l[q][c] *= down;
+                    for (int b = 0; b < B; ++b) {
+                        float u[2];
+                        pair_load(units + (q * B + b) * 32, u[0], u[1]);
 #pragma unroll
-                        for (int b = 0; b < B; ++b) o[q][b][0][c] *= down, o[q][b][0][2 + c] *= down, o[q][b][1][c] *= down, o[q][b][1][2 + c] *= down;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) x[q][2 * j + c] = y[q][2 * j + c] - ref[q][c];
+                        for (int c = 0; c < 2; ++c) past |= ex2(top[q][c]) * scale_at(dm, b) * u[c] > UNIT_MOST;
                     }
-                top_e = e;
+            }
+            if (__any_sync(0xffffffffu, past)) {
+                // Where no scale of the step's keys is further than 2^5 below the largest, the key of a row's largest score has products of 2^2
+                // to 2^8 in every block once r is that score less 8 and more the largest scale's exponent.
+                uint32_t low = 0x7BFF7BFFu, high = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const bool there = key0 + 8 * j + g < seq.len && !gone[j / 2];
+#pragma unroll
+                    for (int k = 0; k < W; ++k) {
+                        const uint32_t d = dv[j][k] & 0x7FFF7FFFu;
+                        high = __vmaxu2(high, d);
+                        if (there) low = __vminu2(low, B % 2 && k == W - 1 ? d | 0x7BFF0000u : d);
+                    }
+                }
+                low = __reduce_min_sync(0xffffffffu, min(low >> 16, low & 0xFFFFu)) >> 10;
+                high = __reduce_max_sync(0xffffffffu, max(high >> 16, high & 0xFFFFu)) >> 10;
+                if (!mixed && high < 31 && low > 0 && low + 5 >= high) {
+                    const int e = (int)high - 14;                                  // scales are below 2^e
+#pragma unroll
+                    for (int q = 0; q < NG; ++q)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            float n = fmaxf(fmaxf(y[q][c], y[q][2 + c]), fmaxf(y[q][4 + c], y[q][6 + c]));
+#pragma unroll
+                            for (int d = 4; d < 32; d <<= 1) n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, d));
+                            const float old = ref[q][c], now = n - old > (float)(UNIT_BITS + 8 - e) ? n - (float)(UNIT_BITS + 1 - e) : old;
+                            const float down = ex2(old - now);
+                            l[q][c] *= down;
+                            ref[q][c] = now;
+#pragma unroll
+                            for (int b = 0; b < B; ++b) o[q][b][0][c] *= down, o[q][b][0][2 + c] *= down, o[q][b][1][c] *= down, o[q][b][1][2 + c] *= down;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) x[q][2 * j + c] = y[q][2 * j + c] - now;
+                        }
+                } else {
+                    // The products themselves, of column c and block b the largest of the warp's keys: lanes g = 2 (b % 4) + c share them out.
+                    // An infinite or NaN scale makes its own dims so, and says nothing about the others'.
+                    bool own = false;
+#pragma unroll
+                    for (int q = 0; q < NG; ++q) {
+                        constexpr int SETS = (B + 3) / 4;                              // of 4 blocks
+                        float n[2], w[8], v[SETS][8];
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            n[c] = fmaxf(fmaxf(y[q][c], y[q][2 + c]), fmaxf(y[q][4 + c], y[q][6 + c]));
+#pragma unroll
+                            for (int d = 4; d < 32; d <<= 1) n[c] = fmaxf(n[c], __shfl_xor_sync(0xffffffffu, n[c], d));
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) w[2 * j + c] = ex2(y[q][2 * j + c] - (n[c] == -INFINITY ? 0.0f : n[c]));
+                        }
+                        float all = 0.0f;                                              // the row's largest product, over 2^n
+#pragma unroll
+                        for (int k = 0; k < SETS; ++k) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                v[k][i] = 0.0f;
+                                if (4 * k + i / 2 < B)
+#pragma unroll
+                                    for (int j = 0; j < 4; ++j) {
+                                        const float d = fabsf(scale_at(dv[j], 4 * k + i / 2));
+                                        if (d <= 65504.0f) v[k][i] = fmaxf(v[k][i], w[2 * j + i % 2] * d);
+                                    }
+                            }
+#pragma unroll
+                            for (int d = 4; d > 0; d >>= 1)
+#pragma unroll
+                                for (int i = 0; i < d; ++i) {
+                                    const float other = __shfl_xor_sync(0xffffffffu, g & d ? v[k][i] : v[k][i + d], 4 * d);
+                                    v[k][i] = fmaxf(g & d ? v[k][i + d] : v[k][i], other);
+                                }
+                            all = fmaxf(all, v[k][0]);
+                        }
+                        all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, 8));
+                        all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, 16));
+                        // of this lane's column
+                        const float most_y = g & 1 ? n[1] : n[0], old = g & 1 ? ref[q][1] : ref[q][0];
+                        const bool none = old == NONE;                                 // no sums yet
+                        float now = old;
+                        if (most_y > -INFINITY && (none || most_y - old > (float)WEIGHT_BITS || all * ex2(most_y - old) > UNIT_MOST))
+                            now = most_y - (float)min(UNIT_BITS - exponent_of(all), WEIGHT_BITS);
+                        const float by = none ? 0.0f : now - old, whole = floorf(by), scale = ex2(most_y - now);
+#pragma unroll
+                        for (int k = 0; k < SETS; ++k) {
+                            const int b = 4 * k + (g >> 1);
+                            if (b < B) {
+                                const uint32_t at = (q * B + b) * 32 + (g & 1) * 4;
+                                // As it was, if it can: the block's sums keep their bits.  At most WEIGHT_BITS more than the row's.
+                                const int was = none || !mixed ? 0 : exponent_of(word_load(units + at)), kept = none ? WEIGHT_BITS : min(was + (int)fminf(whole, 1000.0f), WEIGHT_BITS);
+                                const float product = v[k][0] * scale;
+                                const int unit = now == NONE || product >= UNIT_LEAST ? 0 : product * two_to(kept) > UNIT_MOST ? UNIT_BITS - exponent_of(product) : kept;
+                                word_store(units + at, two_to(unit));
+                                word_store(downs + at, none ? 1.0f : ex2(whole - by) * two_to(max(unit - was - (int)fminf(whole, 1000.0f), -126)));
+                                own |= unit != 0;
+                            }
+                        }
+                        const float now2[2] = {__shfl_sync(0xffffffffu, now, t), __shfl_sync(0xffffffffu, now, 4 + t)};
+                        __syncwarp();
+#pragma unroll
+                        for (int b = 0; b < B; ++b) {
+                            float down[2];
+                            pair_load(downs + (q * B + b) * 32, down[0], down[1]);
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) o[q][b][0][c] *= down[c], o[q][b][0][2 + c] *= down[c], o[q][b][1][c] *= down[c], o[q][b][1][2 + c] *= down[c];
+                        }
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            l[q][c] *= ex2(ref[q][c] - now2[c]);
+                            ref[q][c] = now2[c];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) x[q][2 * j + c] = y[q][2 * j + c] - now2[c];
+                        }
+                    }
+                    mixed = __any_sync(0xffffffffu, own);
+                }
             }
 #pragma unroll
             for (int q = 0; q < NG; ++q)
@@ -683,7 +813,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_kernel(const __grid_
                     x[q][k] = ex2(x[q][k]);                                        // from here the weight
                     l[q][k & 1] += x[q][k];
                 }
-            const auto values = [&](auto of_care) {
+            const auto values = [&](auto of_care) {                               // of_care: units, and scales that are no numbers
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     uint32_t w[2][B];
@@ -697,10 +827,15 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_kernel(const __grid_
                         for (int q = 0; q < NG; ++q) {
                             const float* z = x[q] + 4 * h;
                             float p[4] = {z[0] * d0, z[1] * d0, z[2] * d1, z[3] * d1};
-                            if constexpr (decltype(of_care)::value)
+                            if constexpr (decltype(of_care)::value) {
+                                float u[2];
+                                if (mixed) pair_load(units + (q * B + b) * 32, u[0], u[1]);
 #pragma unroll
-                                for (int k = 0; k < 4; ++k)
+                                for (int k = 0; k < 4; ++k) {
+                                    if (mixed) p[k] *= u[k & 1];
                                     if (y[q][4 * h + k] == -INFINITY) p[k] = 0.0f;
+                                }
+                            }
                             uint32_t p0 = half2_bits(p[0], p[1]), p1 = half2_bits(p[2], p[3]);
                             if constexpr (C::SPLIT) {
                                 const uint32_t r0 = rest2(p[0], p[1], p0), r1 = rest2(p[2], p[3], p1);
@@ -715,7 +850,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_kernel(const __grid_
                     }
                 }
             };
-            if (careful) values(std::true_type{});
+            if (careful || mixed) values(std::true_type{});
             else values(std::false_type{});
             __syncwarp();                            // the step is read by all lanes before it is written again
             if (lane == 0) mbar_arrive(full + C::SLOTS * 8);
@@ -735,11 +870,12 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_kernel(const __grid_
                 const int row = C::SPLIT ? q * 4 + 2 * (t & 1) + c : q * 8 + 2 * t + c;
                 // scores that are all NaN leave no maximum, but a NaN in the sum
                 if (g == 0 && (!C::SPLIT || t < 2))
-                    stats[warp * C::ROWS + row] = make_float2(any && (m[q][c] != -INFINITY || sum != 0.0f) ? ref[q][c] : -INFINITY, sum);
+                    stats[warp * C::ROWS + row] = make_float2(any && (ref[q][c] != NONE || sum != 0.0f) ? ref[q][c] : -INFINITY, sum);
                 if (any)
 #pragma unroll
                     for (int b = 0; b < B; ++b) {
-                        float4 v = make_float4(o[q][b][0][c], o[q][b][0][2 + c], o[q][b][1][c], o[q][b][1][2 + c]);
+                        const float u = mixed ? two_to(-exponent_of(word_load(units + (q * B + b) * 32 + c * 4))) : 1.0f;
+                        float4 v = make_float4(o[q][b][0][c] * u, o[q][b][0][2 + c] * u, o[q][b][1][c] * u, o[q][b][1][2 + c] * u);
                         if constexpr (C::SPLIT) {
                             v.x += __shfl_xor_sync(0xffffffffu, v.x, 2), v.y += __shfl_xor_sync(0xffffffffu, v.y, 2);
                             v.z += __shfl_xor_sync(0xffffffffu, v.z, 2), v.w += __shfl_xor_sync(0xffffffffu, v.w, 2);

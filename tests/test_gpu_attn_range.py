@@ -91,3 +91,100 @@ def test_prompts_of_scores_that_spread(q4q, dim, type):
     e = lse.double().cpu().numpy() - want
     assert np.sqrt((e * e).mean()) <= (dim // 8 + 4) * 2.0 ** -22 * np.abs(want).max() + 2.0 ** -18
     assert norm_error(got, o).max() <= torch.finfo(TYPES[type]).eps
+
+
+# ---------------------------------------------- few rows (warp-level MMAs) --
+
+def few(seed, n, rows, dim, type, outlier, exponent, toward):
+    """Values of about 2^exponent, but for one key of +-65504; block 1 of the queries is -1 times `toward` [heads], of the keys zero
+    but for the outlier's: it scores 70 nats below the others' zero where toward is 1, above where it is -1."""
+    case = Case(seed, [n], [rows], 4, 2, dim, 16, type)
+    rng = np.random.default_rng(seed)
+    k, v = rng.standard_normal((n, 2, dim)), rng.standard_normal((n, 2, dim)) * 2.0 ** exponent
+    k[:, :, 32:64] = 0
+    k[outlier, :, 32:64] = 80 * dim ** 0.5 / 32
+    v[outlier] = 65504 * np.sign(v[outlier])
+    put(case, 0, k, v)
+    case.q[:, :, 32:64] = -torch.tensor(toward, dtype=case.q.dtype)[:, None]
+    return case
+
+
+@pytest.mark.parametrize("dim", [64, 96, 128, 256])
+@pytest.mark.parametrize("type", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("exponent", [-2, -6, -10, -16])
+def test_a_large_value_without_weight(q4q, dim, type, exponent):
+    """Every row sees the key, none gives it weight; the other values count as exactly as without it."""
+    for rows in (1, 3, 9):
+        case = few([dim, exponent + 20, rows], 300, rows, dim, type, 77, exponent, [1, 1, 1, 1])
+        got, lse = case.run(q4q, lse=True)
+        check(case, got, lse)
+    assert q4q.q4q_device_status() == 0
+
+
+@pytest.mark.parametrize("type", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("outlier,window", [(299, 0), (298, 50), (299 - 2 - 50, 50), (299 - 2 - 49, 50)])
+def test_a_large_value_that_some_rows_do_not_see(q4q, type, outlier, window):
+    for toward in ([1, 1, 1, 1], [-1, -1, -1, -1], [0, 0, 0, 0]):
+        case = few([outlier, window], 300, 3, 64, type, outlier, -10, toward)
+        got, lse = case.run(q4q, lse=True, window=window)
+        check(case, got, lse, window=window)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("type", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("rows", [2, 9])
+def test_a_large_value_that_one_head_gives_all_weight(q4q, dim, type, rows):
+    """Heads of one tile, of which the first has no weight for anything else and the second none for that key."""
+    case = few([dim, rows], 300, rows, dim, type, 150, -12, [-1, 1, 1, -1])
+    got, lse = case.run(q4q, lse=True)
+    check(case, got, lse)
+
+
+@pytest.mark.parametrize("dim", [64, 96, 128, 256])
+@pytest.mark.parametrize("type", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("wide", [False, True])
+def test_blocks_of_values_of_different_sizes(q4q, dim, type, wide):
+    """From 2^-14 to 2^12 in the blocks of a head, rising and falling along the keys as well; with one and with two groups of columns."""
+    case = Case([dim, 5], [700, 90], [12, 9] if wide else [2, 1], 4, 2, dim, 16, type)
+    if wide:
+        case.pages = np.pad(case.pages, ((0, 0), (0, 65536 // 16 - case.pages.shape[1])), constant_values=-1)
+    rng = np.random.default_rng(dim)
+    for s, n in enumerate((700, 90)):
+        e = np.linspace(-14, 9, dim // 32).repeat(32) * (1 if s else -1) + 3 * np.sin(np.arange(n) / 20)[:, None, None]
+        put(case, s, rng.standard_normal((n, 2, dim)), rng.standard_normal((n, 2, dim)) * 2.0 ** e)
+    assert not on_tensor_cores(case)
+    got, lse = case.run(q4q, lse=True)
+    check(case, got, lse)
+    assert torch.equal(got, case.run(q4q)) and q4q.q4q_device_status() == 0
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("type", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("nats", [12, 60])
+@pytest.mark.parametrize("at", [0, 400])
+def test_a_key_without_value_that_outweighs_the_rest(q4q, dim, type, nats, at):
+    """First or in the middle; by exp(60) the rest is what is left of the result all the same."""
+    case = with_sink([dim, nats], 700, 3, 4, 2, dim, type, nats)
+    if at:
+        k, v = (x[:, :, :] for x in ref.get(case.cache, 16, 2, dim, case.pages[0][np.arange(700) // 16] * 16 + np.arange(700) % 16)[:2])
+        order = np.arange(700)
+        order[[0, at]] = order[[at, 0]]
+        put(case, 0, k[order], v[order])
+    got, lse = case.run(q4q, lse=True)
+    check(case, got, lse)
+
+
+@pytest.mark.parametrize("type", ["f32", "f16", "bf16"])
+def test_negative_scales(q4q, type):
+    """A cache that another program wrote may hold them: codes turned over (8 stays, 0 has no counterpart) are the same values."""
+    case = Case(71, [300, 50], [2, 3], 4, 2, 64, 16, type)
+    slots = np.concatenate([case.pages[0][np.arange(300) // 16] * 16 + np.arange(300) % 16, case.pages[1][np.arange(50) // 16] * 16 + np.arange(50) % 16])
+    at_k, at_v, at_s = ref.places(64)
+    for n, slot in enumerate(slots):
+        for h in range(2):
+            base = ref.chunk_of(int(slot), h, 2, 64, 16)
+            for of_v in (False, True):
+                where = base + at_s(int(slot) % 16, of_v) + 1
+                case.cache[where] ^= np.where((np.arange(2) + n) % 3 == 0, 0x80, 0).astype(np.uint8)
+    got, lse = case.run(q4q, lse=True)
+    check(case, got, lse)
