@@ -7,7 +7,7 @@
 // 1.91e-3 from 64 bits (512 rows over 8192 keys), now 1.66e-3, of which
 // their results' own rounding is 1.64e-3.  The second product costs 96.6 -> 103 us there, 540 -> 587 for 8 such sequences.  Values are
 // (code - 8) d in fp16 (one rounding, 2^-12 at most; d is at most 8188, so all are finite).  Queries become fp16 of a power of
-// two times their row (exact but for values below 2^-24 of the row's largest), weights are rounded to fp16:
+// two times their row, its largest in [2^14, 2^15) (exact down to 2^-28 of that: below, multiples of 2^-39 of it), weights are rounded to fp16:
 // values and weights are 2^3 below a bf16 result's own rounding, and as large as an fp16 result's.  The weight of the maximum that a row
 // refers to is 2^7, and the reference moves only when a maximum passes it by 2^8, so the largest weight is between 2^7 and fp16's
 // range, and weights down to 2^-21 of it are normal numbers, others multiples of 2^-31 of it.  (With a weight of 1 those of 2^-14 were the last:
@@ -773,7 +773,7 @@ __device__ __forceinline__ void tc_softmax(const AttnArgs& a, const Plan& plan, 
     }
 }
 
-// A piece's queries: rows as fp16 of a power of two times them, the largest in [1, 2), the sign of the softmax's scale with
+// A piece's queries: rows as fp16 of a power of two times them, the largest in [2^14, 2^15), the sign of the softmax's scale with
 // them; and what their scores are multiplied by, into buffer `parity`.  Warp `warp` of `warps` takes its share; ready() is called before
 // anything is stored.
 template <typename C, typename F>
@@ -811,13 +811,13 @@ __device__ __forceinline__ void tc_rows(const AttnArgs& a, const TcWalk& w, int 
 #pragma unroll
             for (int d = 1; d < LANES; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
             const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 100);
-            const float up = sign * two_to(-e);
+            const float up = sign * two_to(14 - e);
 #pragma unroll
             for (int n = 0; n < 8; ++n) v[n] *= up;
             if (used)
                 sts128(base + C::Q + (r / TC_TILE) * C::Q_BYTES + (u / 8) * TC_TILE * 128 + (r % TC_TILE) * 128 + (((u & 7) ^ (r & 7)) << 4),
                        half2_bits(v[0], v[4]), half2_bits(v[1], v[5]), half2_bits(v[2], v[6]), half2_bits(v[3], v[7]));
-            if (u == 0) *reinterpret_cast<float*>(smem + C::SCALE + (parity * TC_ROWS + r) * 4) = scale * two_to(e);
+            if (u == 0) *reinterpret_cast<float*>(smem + C::SCALE + (parity * TC_ROWS + r) * 4) = scale * two_to(e - 14);
         }
     }
     fence_async();

@@ -188,3 +188,22 @@ def test_negative_scales(q4q, type):
                 case.cache[where] ^= np.where((np.arange(2) + n) % 3 == 0, 0x80, 0).astype(np.uint8)
     got, lse = case.run(q4q, lse=True)
     check(case, got, lse)
+
+
+@pytest.mark.parametrize("dim", [64, 96, 128])
+@pytest.mark.parametrize("type", ["f16", "bf16"])
+def test_prompts_of_queries_with_one_large_value(q4q, dim, type):
+    """2^18 times as large as the others, in a dim where keys are zero: the others count with all of their bits."""
+    case = widened(Case([dim, 9], [400], [200], 4, 2, dim, 16, type))
+    rng = np.random.default_rng(dim)
+    k, v = 4096 * rng.standard_normal((400, 2, dim)), rng.standard_normal((400, 2, dim))
+    k[:, :, :32] = 0
+    put(case, 0, k, v)
+    case.q = (case.q.float() * 2.0 ** -12).to(TYPES[type])
+    case.q[:, :, 5] = 64
+    assert on_tensor_cores(case)
+    got, lse = case.run(q4q, lse=True)
+    o, want = case.want()[:2]
+    e = lse.double().cpu().numpy() - want
+    assert np.sqrt((e * e).mean()) <= (dim // 8 + 4) * 2.0 ** -22 * np.abs(want).max() + 2.0 ** -18
+    assert norm_error(got, o).max() <= torch.finfo(TYPES[type]).eps
