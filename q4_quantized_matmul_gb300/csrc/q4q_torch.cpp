@@ -525,6 +525,8 @@ Angles angles_of(PyObject* table, PyObject* pos, int64_t tokens, const Place& at
     const at::Tensor& t = tensor(table, "table");
     if (t.dim() != 2) raise(PyExc_ValueError, "table must be [positions, rot]");
     r.table = static_cast<const float*>(typed(t, "table", at::kFloat, 0, at.device()));
+    // its address is null, which would say that there is no table
+    if (t.numel() == 0 && tokens > 0) raise(PyExc_ValueError, "table must hold positions");
     r.n_pos = t.size(0);
     r.rot = (int)std::min<int64_t>(t.size(1), 1 << 20);
     if (none(pos)) raise(PyExc_ValueError, "a table needs pos");
