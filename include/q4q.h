@@ -632,8 +632,8 @@ Q4Q_API q4q_status q4q_kv_append(void* cache, int64_t n_pages, int page_tokens, 
 Q4Q_API q4q_status q4q_kv_get_rows(const void* cache, int64_t n_pages, int page_tokens, int n_kv_heads, int64_t head_dim,
                            const int32_t* slots, int64_t n_slots, void* k_dst, void* v_dst, int dst_type, q4q_stream_t stream);
 
-/* Bytes of device workspace q4q_kv_attn needs on the current device for n_seqs sequences with up to
- * n_q rows of queries (the same rows as fewer sequences may need more). */
+/* Bytes of device workspace that serve every q4q_kv_attn on the current device with these heads and type, up to
+ * n_q rows of queries and up to n_seqs sequences. */
 Q4Q_API q4q_status q4q_kv_attn_workspace_size(int64_t n_q, int n_q_heads, int n_kv_heads, int64_t head_dim, int64_t n_seqs, int type,
                                       size_t* bytes);
 

@@ -81,7 +81,7 @@ def q4q_kv_get_rows(cache: torch.Tensor, page_tokens: int, n_kv_heads: int, head
 
 def q4q_kv_attn_workspace_size(n_q: int, n_q_heads: int, n_kv_heads: int, head_dim: int, n_seqs: int,
                                dtype: torch.dtype = torch.float32) -> int:
-    """Bytes of workspace of q4q_kv_attn on the current device for up to n_q rows of queries of dtype in n_seqs sequences."""
+    """Bytes of workspace that serve every q4q_kv_attn on the current device with up to n_q rows of queries of dtype in up to n_seqs sequences."""
     n = ctypes.c_size_t(0)
     kind = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}[dtype]
     _check("q4q_kv_attn_workspace_size", _lib.load().q4q_kv_attn_workspace_size(n_q, n_q_heads, n_kv_heads, head_dim, n_seqs, kind,

@@ -134,7 +134,8 @@ extern "C" q4q_status q4q_kv_attn_workspace_size(int64_t n_q, int n_q_heads, int
     DeviceInfo info;
     const q4q_status st = current_device_info(&info);
     if (st != Q4Q_OK) return st;
-    *bytes = workspace_bytes(type, head_dim, n_q, n_q_heads / n_kv_heads, n_seqs, info);
+    // what the same rows need as one sequence: fewer sequences may take the form with the larger workspace
+    *bytes = workspace_bytes(type, head_dim, n_q, n_q_heads / n_kv_heads, std::min<int64_t>(n_seqs, 1), info);
     return Q4Q_OK;
 }
 
