@@ -569,7 +569,8 @@ Q4Q_API q4q_status q4q_rope_table(float* table, int64_t n_pos, int rot, double b
 
 /* Norms of queries and keys for each head and the rotation by their positions, in one launch.
  * Of a head's row x (head_dim values) of token t, p = pos[t]:
- *   r = fp32(1 / sqrt(mean(x^2) + eps)) (sums as in 64 bits),  z = (x r) w;  z = x without a weight;
+ *   r = fp32(1 / sqrt(mean(x^2) + eps)) (sums as in 64 bits; one row in 2^20, next to the middle of
+ *       two fp32, may get the other one),  z = (x r) w;  z = x without a weight;
  *   a' = a c - b s, b' = b c + a s for the pairs (a, b) of z's first rot values, c and s from row p
  *   of the table; without a table nothing is turned.
  * Each product, difference and sum is rounded to fp32, results once more to `type`.
@@ -581,7 +582,8 @@ Q4Q_API q4q_status q4q_rope_table(float* table, int64_t n_pos, int rot, double b
  * position outside the table makes the token's rows zeros and records Q4Q_ERR_ARG
  * (q4q_device_status).  head_dim 64, 96, 128 or 256; rot % 16 == 0, rot <= head_dim; up to 1024
  * heads of either kind (0: none, its pointers are not looked at); n_tokens < 2^31; strides from
- * heads * head_dim to 2^31 - 1.  Values are finite and below 2^60. */
+ * heads * head_dim to 2^31 - 1.  Values are finite and below 2^60; mean(x^2) + eps is 2^-90 or more
+ * where a weight is given (squares are fp32). */
 Q4Q_API q4q_status q4q_qk_norm_rope(const void* q, int64_t q_stride, int n_q_heads, const void* k, int64_t k_stride, int n_k_heads,
                             int type, int64_t head_dim, int64_t n_tokens, const float* q_weight, const float* k_weight, float eps,
                             const float* table, int64_t n_pos, int rot, int mode, const int32_t* pos, void* q_dst, void* k_dst,

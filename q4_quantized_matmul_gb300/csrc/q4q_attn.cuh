@@ -153,7 +153,8 @@ __device__ __forceinline__ float two_sum(float a, float b, float& lost) {
 // this chip does a 64th as many, would take 90 us for 8192 tokens' keys.  The lanes of a row halve the rows among them
 // in the first two steps of the sum, so that each ends with one row's, takes its root and hands it round.  inv_dim:
 // 1 / D as two fp32.  The estimate y of rsqrtf takes one Newton step, y - y (a y^2 - 1) / 2, whose residual
-// is computed from the exact square of y.  EXACT: squares of 16-bit values are exact in fp32.  (A square contracted into its
+// is computed from the exact product a y, which is in range wherever a is (y^2 as two fp32 is not: of means past 2^112 its lower part was
+// subnormal, and up to 2% of rows one rounding off).  EXACT: squares of 16-bit values are exact in fp32.  (A square contracted into its
 // sum changes that sum by at most its own rounding, which the two-sum then carries on.)
 template <int LANES, bool EXACT>
 __device__ __forceinline__ void inverse_norm4(const Row8 (&v)[4], float2 inv_dim, float eps, float (&r)[4]) {
@@ -210,8 +211,8 @@ __device__ __forceinline__ void inverse_norm4(const Row8 (&v)[4], float2 inv_dim
     float a_lo = __fadd_rn(lost, m_lo);
     a = two_sum(a, a_lo, lost);
     a_lo = lost;
-    const float y = rsqrtf(a), y2 = __fmul_rn(y, y), y2_lo = __fmaf_rn(y, y, -y2);
-    const float residual = __fadd_rn(__fmaf_rn(a, y2, -1.0f), __fmaf_rn(a, y2_lo, __fmul_rn(a_lo, y2)));
+    const float y = rsqrtf(a), ay = __fmul_rn(a, y), ay_lo = __fmaf_rn(a, y, -ay);
+    const float residual = __fadd_rn(__fmaf_rn(ay, y, -1.0f), __fmaf_rn(ay_lo, y, __fmul_rn(__fmul_rn(a_lo, y), y)));
     const float mine = __fmaf_rn(__fmul_rn(-0.5f, y), residual, y);
 #pragma unroll
     for (int n = 0; n < 4; ++n) r[n] = __shfl_sync(0xffffffffu, mine, (lane & ~(LANES - 1)) | (n & 2 ? LANES / 2 : 0) | (n & 1 ? LANES / 4 : 0));
