@@ -207,3 +207,40 @@ def test_prompts_of_queries_with_one_large_value(q4q, dim, type):
     e = lse.double().cpu().numpy() - want
     assert np.sqrt((e * e).mean()) <= (dim // 8 + 4) * 2.0 ** -22 * np.abs(want).max() + 2.0 ** -18
     assert norm_error(got, o).max() <= torch.finfo(TYPES[type]).eps
+
+
+@pytest.mark.parametrize("dim", [64, 96, 256])
+@pytest.mark.parametrize("type", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("rising", [True, False])
+@pytest.mark.parametrize("values", [0, 1, -1])
+def test_scores_that_rise_or_fall_along_the_keys(q4q, dim, type, rising, values):
+    """By 200 nats: every step finds a new maximum, or none does; values of one size, of falling or of rising size, blocks of different ones."""
+    case = Case([dim, rising, values + 1], [700], [3], 4, 2, dim, 16, type)
+    rng = np.random.default_rng(dim)
+    n = np.arange(700)[:, None, None]
+    k, v = rng.standard_normal((700, 2, dim)) / 8, rng.standard_normal((700, 2, dim))
+    # queries of -1 in block 1: key n scores 200 n / 700 nats (or 699 - n of them) beside the rest
+    k[:, :, 32:64] = -(n if rising else 699 - n) * 200 / 700 * dim ** 0.5 / 32
+    v *= 2.0 ** (values * 12 * (n - 350) / 350) * 2.0 ** np.linspace(-6, 6, dim // 32).repeat(32)
+    put(case, 0, k, v)
+    case.q[:, :, 32:64] = -1
+    got, lse = case.run(q4q, lse=True)
+    check(case, got, lse)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("rows,type", [(1, "f32"), (5, "f16"), (9, "bf16"), (200, "bf16")])
+def test_values_that_are_all_zero(q4q, dim, rows, type):
+    """Of all keys, of all but the last, of a block: zeros, and lse as ever."""
+    for kind in ("all", "but one", "block"):
+        case = widened(Case([dim, rows], [300], [rows], 4, 2, dim, 16, type)) if rows > 99 else Case([dim, rows], [300], [rows], 4, 2, dim, 16, type)
+        rng = np.random.default_rng(dim)
+        k, v = (rng.standard_normal((300, 2, dim)) for _ in range(2))
+        if kind == "block":
+            v[:, :, 32:64] = 0
+        else:
+            v[: 299 if kind == "but one" else 300] = 0
+        put(case, 0, k, v)
+        got, lse = case.run(q4q, lse=True)
+        check(case, got, lse)
+        assert kind == "but one" or not got[..., 32:64].any()
