@@ -14,8 +14,11 @@ constexpr int64_t STEP_TOKENS = 2 * KV_GROUP;      // of the warp-level kernel
 // The tcgen05 kernel may take bf16 and fp16 rows where a sequence has 64 of them or more for a key-value head, on average, and
 // does where its longer start pays: from 256 rows, a CTA's tiles, or from 6 2^20 pairs of a row of queries and a key of the tables,
 // which bound the keys.  us, warp-level MMAs / tcgen05, 8 key-value heads of 128, rows a head: bf16, 64 rows over 8192 keys (4.2 M pairs)
-// 28 / 32, 128 over 8192 39 / 33, 256 over 8192 63 / 36, 16 x 64 over 2048 84 / 64, 2 x 128 over 300 22 / 36, 8 x 400 over 100 70 / 52;
-// fp16, 64 over 1023 18.9 / 26.4, 128 over 8191 69 / 34, 2048 over 8192 891 / 103; 7 x 64 of 12 heads over 1021 35.9 / 35.9.
+// 28 / 33, 128 over 8192 40 / 34, 256 over 8192 64 / 37, 16 x 64 over 2048 82 / 64, 2 x 128 over 300 21 / 37, 8 x 400 over 100 73 / 53;
+// fp16, 64 over 1023 19.6 / 27.5, 128 over 8192 71 / 35, 2048 over 8192 920 / 101.
+// One kernel takes the whole call, by what the host knows.  A batch of unlike sequences is slower than its parts in calls of their own: a
+// prompt of 2048 bf16 tokens beside 63 single ones over 8192 keys 827 us (tcgen05), apart 275 + 139; one of 512 beside them 593
+// (warp-level), apart 100 + 138.  A page table wider than the sequences counts as if they were that long.
 bool may_use_tensor_cores(int type, int64_t head_dim, int64_t n_q, int shared, int64_t n_seqs) {
     return type != Q4Q_TYPE_F32 && head_dim <= 128 && n_q * shared >= n_seqs * 64;
 }
@@ -92,9 +95,10 @@ q4q_status check(AttnArgs& a, const void* q, int64_t q_stride, int type, int64_t
 // Two groups of columns where a key-value head has more rows than one group holds (8, or 4 that are split in two
 // fp16), by the average of the rows a sequence: a chunk is then unpacked once for twice the rows, by half as many CTAs an
 // SM.  With few steps (by the table's keys, 24 for each of the 2 CTAs an SM that one group has) the single groups' shorter end of
-// a piece counts more.  us, one group / two, 8 key-value heads of 128, rows a head: fp32, 8 rows over 1023 keys 13.9 / 16.7, 4095
-// 16.3 / 18.3, 16383 20.7 / 18.6, 64 rows over 1023 19.4 / 20.4, 8191 51 / 42; 64 sequences of up to 8192 keys, bf16 12 rows 182 / 176,
-// 4 rows (one group by the rule) 96 / 161, fp32 8 rows 214 / 192, fp16 8 rows 190 / 196.
+// a piece counts more.  us, one group / two, 8 key-value heads of 128, rows a head: fp32, 8 rows over 1023 keys 14.7 / 18.1, 4095
+// 17.0 / 19.5, 16383 20.7 / 19.2, 64 rows over 1023 20.0 / 21.7, 8191 51 / 45; 64 sequences of up to 8192 keys, bf16 4 rows
+// (one group by the rule) 98 / 163.  A batch whose sequences have 4 or 8 rows, between 4 and 8 on average, would be better off with one
+// (fp32, 142 / 199): the host sees the average alone.
 bool wide(const AttnArgs& a, const DeviceInfo& info) {
     const int64_t one = a.type == Q4Q_TYPE_BF16 ? 8 : 4, rows = a.n_q * a.shared;
     const double steps = (double)((rows + one - 1) / one) * a.kv_heads * (double)(((a.max_pages << a.page_log) + STEP_TOKENS - 1) / STEP_TOKENS);

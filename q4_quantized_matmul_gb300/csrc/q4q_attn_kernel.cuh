@@ -38,7 +38,9 @@
 //
 // Measured in a graph (heads 32/8 of 128): one fp32 token over 1023 keys 13.9 us (launches, shares, a piece's end and the
 // join); over 131072 keys, fp16, 47 us (151 MB, 3.2 TB/s); 64 bf16 tokens over 8192 keys at most 98 us (337 MB, 3.4 TB/s).
-// Bound by issue: some 300 instructions a chunk of 16 keys and warp, the ALU pipe about half busy with the codes.
+// Some 300 instructions a chunk of 16 keys and warp, issued in 55% of the cycles, the ALU pipe busy in half of them, HBM at half its rate:
+// no unit is full, four warps a scheduler leave the rest to latency.  (32 to 72 bytes of spills in one group's forms at D = 128, 450 to 650 in two
+// groups' at D = 256.)
 #pragma once
 
 #include <algorithm>
@@ -69,8 +71,8 @@ struct Cfg {
     static constexpr int ROWS = (SPLIT ? 4 : 8) * NG;  // of a tile
     static constexpr int DIM = 32 * B;
     static constexpr int CHUNK = kv_chunk_bytes(DIM);
-    // Two CTAs of 8 warps an SM where 128 registers are enough (8 B for the sums of a group of columns, 4 B for its
-    // queries), so that one's end of a piece hides behind the other's chunks.
+    // Two CTAs of 8 warps an SM where 128 registers are nearly enough (8 B for the sums of a group of columns, 4 B for its
+    // queries; B = 4 spills up to 72 bytes), so that one's end of a piece hides behind the other's chunks.
     static constexpr int CTAS = B <= 4 && NG == 1 ? 2 : 1;
     static constexpr int CONSUMERS = 7;
     static constexpr int THREADS = (CONSUMERS + 1) * 32;

@@ -28,10 +28,10 @@
 // Steps of all pieces (sequence, head, 256 rows) in a row are cut into equal shares, one a CTA and SM; parts of a
 // piece are joined by a second kernel in order.
 //
-// Measured in a graph (heads 32/8 of 128): bf16, 512 rows behind 7680 keys 103 us (647 TFLOP/s), 8 such sequences 587 us (907
-// TFLOP/s), two prompts of 2048 with a window of 1024 135 us; fp16 104 and 137 us.  Bound by the softmax: a row's 128 scores are read,
-// exponentiated and written back in one thread, and the two tiles' chains fill about half of the tensor cores' time; a piece's
-// start and end cost about 10 us each time, the shares 4.4 us.
+// Measured in a graph (heads 32/8 of 128): bf16, 512 rows behind 7680 keys 103 us (647 TFLOP/s), 8 such sequences 580 us (918
+// TFLOP/s), two prompts of 2048 with a window of 1024 135 us; fp16 103 and 137 us.  A row's 128 scores are read twice, exponentiated
+// and written back by one thread, and only the other tile's MMAs run beside that; the forms spill (276 to 288 bytes of stores, 396 to 404
+// of loads); a piece's start and end cost about 10 us each time, the shares 4.4 us.
 #include "q4q_attn_kernel.cuh"
 
 namespace q4q {

@@ -10,9 +10,10 @@
 // Rows, lanes and warps as in q4q_rope.cu: a lane's 8 values are one word of key codes or two halves of value codes.  The
 // order of the cache (q4q_attn.cuh) spreads a value row's bytes over its octet's 4 D bytes; a prompt's neighbours fill the
 // gaps while the lines are in L2.  Measured in a graph, keys and values of 8 heads of 128: one fp32 token 3.1 us (launch and
-// two loads in a row), 8192 bf16 tokens with norm and rotation 29.6 us, without 19.8 us; 43 MB are moved, so 1.4 and
-// 2.2 TB/s: bound by the encoder's instructions, about 45 for 8 codes and as many again for norm and rotation.  The row
-// gather of 8192 slots: 13.7 us (3.1 TB/s).
+// two loads in a row), 8192 bf16 tokens with norm and rotation 29.3 us, without 19.8 us; 43 MB are moved, so 1.5 and
+// 2.2 TB/s.  Half of the warps keep to keys, half to values, so with norm and rotation the values' are done well before the
+// keys'; the encoder's 45 instructions for 8 codes are a fraction of either time at full issue.  The row
+// gather of 8192 slots: 13.7 us (3.1 TB/s), on append's grid: 16 of the 32 warps an SM that its 56 registers would let in.
 #include <algorithm>
 
 #include "q4q_attn.cuh"

@@ -10,13 +10,15 @@
 //
 // A row takes D / 8 lanes, 8 values each.  A warp keeps to one side (queries or keys) and one run of heads through all of
 // its tokens, so weights and places are looked up once, and takes 4 row slots at a time (2 backward), whose loads
-// are in flight together and whose norms share their sums' last steps and root.  Bound by HBM when there are many tokens, by the
-// launch and two loads behind one another when there are few.  dw is summed in registers over a warp's rows, then
+// are in flight together and whose norms share their sums' last steps and root.  Few tokens are bound by the
+// launch and two loads behind one another.  dw is summed in registers over a warp's rows, then
 // over the block's warps, and the blocks' sums by a second kernel in the order of the blocks: no atomics, results do
 // not vary.
 //
-// Measured in a graph (32 + 8 heads of 128): one token 3.5 us; 8191 bf16 tokens forward 49.6 us (168 MB, 3.4 TB/s: bytes in
-// flight; three blocks an SM with fewer registers were slower, 57.7), backward with both weights 78 us (252 MB, 3.2 TB/s).
+// Measured in a graph (32 + 8 heads of 128): one token 3.5 us; 8191 bf16 tokens forward 49.2 us (168 MB, 3.4 TB/s), backward with both
+// weights 77 us (252 MB, 3.3 TB/s).  What that is made of: neither norm nor rotation, a copy, 29 us (5.8 TB/s), the norm alone 32, the rotation
+// alone 43: a token's angles are loaded when it is its turn, and each value's partner is fetched from another lane.  Backward 38, 51, 54.
+// fp32: 67, 73, 75, both 83.  (Three blocks an SM with fewer registers were slower, 57.7.)
 #include <algorithm>
 
 #include "q4q_attn.cuh"
