@@ -492,7 +492,8 @@ Heads heads_of(const at::Tensor& t, const char* name, c10::DeviceIndex device) {
     h.dim = t.size(2);
     const int64_t row = h.heads * h.dim;
     h.stride = h.tokens > 1 ? t.stride(0) : row;
-    if ((h.dim > 1 && t.stride(2) != 1) || (h.heads > 1 && t.stride(1) != h.dim) || h.stride < row)
+    if (t.numel() == 0) h.stride = row;          // strides of an empty tensor say nothing
+    else if ((h.dim > 1 && t.stride(2) != 1) || (h.heads > 1 && t.stride(1) != h.dim) || h.stride < row)
         raise(PyExc_ValueError, std::string(name) + " must have its heads' values one after another, and its tokens apart");
     h.at = t.data_ptr();
     return h;

@@ -146,3 +146,40 @@ def test_a_prompt_beside_single_tokens(q4q, type, prompt):
         check(c, got, lse)
         close(c, got, lse)
     assert q4q.q4q_device_status() == 0
+
+
+@pytest.mark.parametrize("type", ["f32", "bf16"])
+@pytest.mark.parametrize("heads,kv_heads,lengths,rows", [(1024, 1, [100, 3], [1, 2]), (1024, 1024, [40], [1]), (768, 3, [70, 30], [2, 1])])
+def test_the_most_heads(q4q, type, heads, kv_heads, lengths, rows):
+    case = Case([heads, kv_heads], lengths, rows, heads, kv_heads, 64, 16, type)
+    for c in (case, widened(case) if type != "f32" else case):
+        got, lse = c.run(q4q, lse=True)
+        check(c, got, lse)
+    assert q4q.q4q_device_status() == 0
+
+
+@pytest.mark.parametrize("type", ["f32", "f16", "bf16"])
+def test_the_largest_pages(q4q, type):
+    case = Case(4096, [5000, 4096, 1], [1, 3, 1], 4, 2, 64, 4096, type)
+    got, lse = case.run(q4q, lse=True)
+    check(case, got, lse)
+    case = Case(4097, [4500], [150], 4, 2, 64, 4096, type)
+    got, lse = case.run(q4q, lse=True)
+    check(case, got, lse)
+    assert q4q.q4q_device_status() == 0
+
+
+@pytest.mark.parametrize("type", ["f32", "bf16"])
+@pytest.mark.parametrize("rows", [1, 100])
+def test_sequences_that_share_pages(q4q, type, rows):
+    """The same prefix in every sequence's table, one page twice in one table: as many copies of it give."""
+    case = Case([3, rows], [64], [rows], 4, 2, 64, 16, type)
+    q, cache, page, kv, pages, length = case.args()
+    table = pages.repeat(3, 1)
+    table[2, 3] = table[2, 1]
+    first = torch.arange(0, 3 * rows + 1, rows, dtype=torch.int32, device="cuda")
+    got = q4q.q4q_kv_attn(q.repeat(3, 1, 1), cache, page, kv, table, length.repeat(3), first=first)
+    again = Case([3, rows], [64], [rows], 4, 2, 64, 16, type)
+    again.pages = table.cpu().numpy()
+    again.len, again.first, again.q = np.full(3, 64, np.int32), first.cpu().numpy(), case.q.repeat(3, 1, 1)
+    check(again, got)
