@@ -652,7 +652,7 @@ Q4Q_API q4q_status q4q_kv_attn_workspace_size(int64_t n_q, int n_q_heads, int n_
  * Sums and statistics are fp32, codes and scales of keys count exactly.  fp32 and fp16
  * queries count with 22 bits, and so do products of their weights and values' scales, or to 2^-27 of the largest that the
  * row has in the same 32 dims; of bf16 queries these products are rounded to fp16 (11 bits).  bf16
- * and fp16 prompts of 64 rows a key-value head and more, heads up to 128, may run on the tcgen05
+ * and fp16 prompts of 64 rows a key-value head and more, heads up to 128, tables of up to 2^24 keys, may run on the tcgen05
  * tensor cores, where values and weights are rounded to fp16 (weights below 2^-21 of the largest that a row refers
  * to: to multiples of 2^-31 of it; scales above 8188, which q4q_kv_append does not write, would pass its range).
  * A NaN in a row's query, or in scales of keys that it sees, gives NaN.

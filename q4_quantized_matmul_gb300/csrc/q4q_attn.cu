@@ -22,8 +22,10 @@ constexpr int64_t STEP_TOKENS = 2 * KV_GROUP;      // of the warp-level kernel
 bool may_use_tensor_cores(int type, int64_t head_dim, int64_t n_q, int shared, int64_t n_seqs) {
     return type != Q4Q_TYPE_F32 && head_dim <= 128 && n_q * shared >= n_seqs * 64;
 }
+// Not with tables of more than 2^24 keys: its loaders wait through a piece, 2.4 us for 128 keys, and a wait is bounded by a second.
+constexpr int64_t TC_MOST_KEYS = 1ll << 24;
 bool on_tensor_cores(const AttnArgs& a, int64_t head_dim) {
-    return may_use_tensor_cores(a.type, head_dim, a.n_q, a.shared, a.n_seqs) &&
+    return may_use_tensor_cores(a.type, head_dim, a.n_q, a.shared, a.n_seqs) && (a.max_pages << a.page_log) <= TC_MOST_KEYS &&
            (a.n_q * a.shared >= a.n_seqs * 256ll || (double)a.n_q * a.heads * (double)(a.max_pages << a.page_log) >= 6.0 * (1 << 20));
 }
 

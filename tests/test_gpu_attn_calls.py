@@ -183,3 +183,14 @@ def test_sequences_that_share_pages(q4q, type, rows):
     again.pages = table.cpu().numpy()
     again.len, again.first, again.q = np.full(3, 64, np.int32), first.cpu().numpy(), case.q.repeat(3, 1, 1)
     check(again, got)
+
+
+@pytest.mark.parametrize("pages", [2 ** 12, 2 ** 12 + 1])
+def test_tables_of_2_to_the_24_keys(q4q, pages):
+    """The most that prompts take tcgen05 with, and one page more: a wait of its loaders lasts as long as a piece."""
+    case = Case([24, pages], [4500, 300], [150, 90], 4, 2, 64, 4096, "bf16")
+    case.pages = np.pad(case.pages, ((0, 0), (0, pages - case.pages.shape[1])), constant_values=-1)
+    got, lse = case.run(q4q, lse=True)
+    check(case, got, lse)
+    close(case, got, lse)
+    assert q4q.q4q_device_status() == 0
