@@ -662,7 +662,7 @@ Q4Q_API q4q_status q4q_kv_attn_workspace_size(int64_t n_q, int n_q_heads, int n_
  * outside the cache as one that no row sees; both record Q4Q_ERR_ARG.  workspace: 256-byte aligned,
  * of one call at a time.  n_q_heads a multiple of n_kv_heads, up to 1024; n_q < 2^24, n_q *
  * n_q_heads / n_kv_heads < 2^30, n_seqs < 2^20, max_pages * page_tokens < 2^30.  Queries below
- * 2^100.  The result depends on the operands and the device alone. */
+ * 2^100, scores scale <q, K_j> below 2^22 in size (fp32 does not tell weights of larger ones apart).  The result depends on the operands and the device alone. */
 Q4Q_API q4q_status q4q_kv_attn(const void* q, int64_t q_stride, int type, int64_t n_q, int n_q_heads, int n_kv_heads, int64_t head_dim,
                        const void* cache, int64_t n_pages, int page_tokens, const int32_t* pages, int64_t max_pages,
                        const int32_t* kv_len, const int32_t* first, int64_t n_seqs, float scale, int causal, int64_t window, void* dst,

@@ -33,10 +33,10 @@
 // tile of rows -- in a row are cut into equal shares, one a CTA, two CTAs an SM, so a ragged batch or one long
 // sequence both fill the GPU.  A producer warp's 32 lanes each find and copy one chunk in 32 (a bulk copy into a
 // ring of steps), the consumer warps take the steps in turn.  At the end of a piece its consumers' sums are joined in
-// shared memory; what a CTA leaves of a piece to others goes to the workspace as sums with m and l, and
+// shared memory; what a CTA leaves of a piece to others goes to the workspace as sums with r and l, and
 // a second kernel joins the parts in order.
 //
-// Measured in a graph (heads 32/8 of 128): one fp32 token over 1023 keys 13.9 us (launches, shares, a piece's end and the
+// Measured in a graph (heads 32/8 of 128): one fp32 token over 1023 keys 14.0 us (launches, shares, a piece's end and the
 // join); over 131072 keys, fp16, 47 us (151 MB, 3.2 TB/s); 64 bf16 tokens over 8192 keys at most 98 us (337 MB, 3.4 TB/s).
 // Some 300 instructions a chunk of 16 keys and warp, issued in 55% of the cycles, the ALU pipe busy in half of them, HBM at half its rate:
 // no unit is full, four warps a scheduler leave the rest to latency.  (32 to 72 bytes of spills in one group's forms at D = 128, 450 to 650 in two

@@ -244,3 +244,29 @@ def test_values_that_are_all_zero(q4q, dim, rows, type):
         got, lse = case.run(q4q, lse=True)
         check(case, got, lse)
         assert kind == "but one" or not got[..., 32:64].any()
+
+
+@pytest.mark.parametrize("rows,type", [(2, "f32"), (3, "f16"), (9, "bf16"), (150, "f16"), (150, "bf16")])
+@pytest.mark.parametrize("most", [1e5, -1e6, 4e6])
+def test_scores_of_up_to_2_to_the_22(q4q, rows, type, most):
+    """Of either sign; the best key takes all where it leads by more than the scores can be off by."""
+    case = Case([rows, 22], [300], [rows], 4, 2, 128, 16, type)
+    if rows > 99:
+        case = widened(case)
+    scale = float(np.float32(most / np.abs(case.want(scale=np.sign(most))[1]).max()))
+    got, lse = case.run(q4q, lse=True, scale=scale)
+    got, lse = got.double().cpu().numpy(), lse.double().cpu().numpy()
+    assert np.isfinite(got).all() and np.isfinite(lse).all()
+    o, want, size, span = case.want(scale=scale)
+    assert np.abs(want).max() < 2 ** 22
+    e = span * 2 * (128 // 8 + 4) * 2.0 ** -22
+    assert np.all(np.abs(lse - want) <= e + 2.0 ** -22 * np.abs(want) + 1)
+    k = ref.get(case.cache, 16, 2, 128, case.pages[0][np.arange(300) // 16] * 16 + np.arange(300) % 16)[0]
+    clear = 0
+    for i in range(rows):
+        for h in range(4):
+            s = np.sort(scale * (k[: 300 - rows + 1 + i, h // 2] @ case.q[i, h].double().numpy()))
+            if s[-1] - s[-2] > 30 + 2 * e[i, h]:
+                clear += 1
+                assert np.all(np.abs(got[i, h] - o[i, h]) <= size[i, h] * 2.0 ** -10 + np.abs(o[i, h]) * torch.finfo(TYPES[type]).eps / 2)
+    assert clear > 0
